@@ -377,6 +377,124 @@ int moe_expert_ffn_int4_prefill(const qmv_moe_int4 *m, const uint16_t *x_bf16, i
                                 const int32_t *ids, const float *w, int k, float *out, void *ws,
                                 size_t ws_bytes, qmv_stream_t stream);
 
+/* ---------------------------------------------------------------- attention
+ *
+ * The attention half of a decode or speculative-decoding step next to the
+ * expert half above: rotary positions and the append to a paged key/value
+ * cache, attention of a tree of drafted tokens (or one token) over it, and
+ * eviction from it by accumulated attention weight. */
+
+typedef enum { QMV_F32 = 0, QMV_BF16 = 1, QMV_F16 = 2 } qmv_dtype;
+
+/* A paged cache of one layer. Token `slot` of sequence b is row slot % page of
+ * page table[b][slot / page]; a page holds, per head, `page` rows of D values
+ * in a row. dtype is QMV_BF16 or QMV_F16; D is 64 or 128; page is 16, 32, 64,
+ * 128 or 256; pages * Hkv * page < 2^31. k and v are 16-byte aligned. The
+ * running attention weights, where they are kept, are a float array
+ * [pages][Hkv][page] of the caller. The descriptor is a HOST struct. */
+typedef struct {
+    void *k; /* [pages][Hkv][page][D] */
+    void *v; /* [pages][Hkv][page][D] */
+    int32_t pages, Hkv, page, D, dtype;
+} qmv_attn_cache;
+
+/* Shared by the calls below:
+ *   table   [B][max_pages] int32 page ids; max_pages * page <= 2^30;
+ *           B * Hkv <= 65535.
+ *   ctx     [B] int32: the tokens of each sequence already in the cache.
+ *   cu      [B + 1] int32: the first new token of each sequence, cu[B] = N;
+ *           sequence b's new tokens cu[b] .. cu[b + 1] - 1 have slots
+ *           ctx[b], ctx[b] + 1, ...
+ *   status  [1] int32 or NULL, OR-ed (not cleared) with
+ *             1  a page id outside [0, pages): its tokens are left out;
+ *             2  a sequence whose lengths are negative, do not fit its row of
+ *                the table, or exceed N or max_draft: it is left out (its
+ *                output rows are not written);
+ *             4  a bounded wait on a copy ran out: outputs are not valid.
+ *   B == 0 or N == 0 enqueues nothing. Errors: QMV_EINVAL (null pointer, bad
+ *   count or dtype), QMV_ESHAPE (D, page, or a size past its limit),
+ *   QMV_EALIGN, QMV_EWORKSPACE, QMV_ECUDA. */
+
+/* Rotary positions of N new tokens and their append to the cache. Token n's
+ * query and key heads are turned by the angles pos[n] * inv_freq[i], i < rot/2:
+ *     (a, b) -> mscale * (a cos - b sin, b cos + a sin)
+ * on elements (i, i + rot/2) of a head, or (2i, 2i + 1) when interleaved != 0;
+ * elements rot .. D - 1 pass unchanged. Queries go to q_out, keys and values
+ * to the tokens' slots. Angles are formed in 64 bits (exact for any int32
+ * position), the rest in fp32, rounded once to the cache's type. Scaled
+ * positions for long contexts are a matter of inv_freq and mscale.
+ *   q [N] rows of Hq * D, k and v [N] rows of Hkv * D, q_stride, k_stride and
+ *     v_stride elements apart (so they may be parts of one projection's rows);
+ *     in_dtype QMV_F32 or the cache's. Rows on 16-byte boundaries and rot a
+ *     multiple of 16 take the vector path; any other alignment is correct.
+ *   pos [N] int32; inv_freq [rot/2] double, 8-byte aligned; 2 <= rot <= D, even
+ *   q_out [N][Hq][D] in the cache's type, 16-byte aligned (written)
+ *   acc   running attention weights, or NULL: set to 0 for the new tokens
+ *   Hq a multiple of Hkv, at most 1024; N <= 2^22. */
+int attn_rope_append(const qmv_attn_cache *c, const void *q, int64_t q_stride, const void *k,
+                     int64_t k_stride, const void *v, int64_t v_stride, int in_dtype, int Hq,
+                     const int32_t *pos, const double *inv_freq, int rot, int interleaved,
+                     float mscale, const int32_t *table, int max_pages, const int32_t *ctx,
+                     const int32_t *cu, int B, int N, void *q_out, float *acc, int32_t *status,
+                     qmv_stream_t stream);
+
+/* Workspace of attn_tree, in bytes (0 for unsupported sizes). weights != 0:
+ * with acc_out. */
+size_t attn_tree_workspace_bytes(const qmv_attn_cache *c, int Hq, int B, int N, int max_draft,
+                                 int max_pages, int weights);
+
+/* Attention of each sequence's drafted tokens over its cache, drafts included
+ * (their keys and values are in their slots: attn_rope_append). Head hq reads
+ * key/value head hq / (Hq / Hkv). Token n = cu[b] + t sees every slot below
+ * ctx[b], and draft d of its own sequence when bit d % 32 of
+ * mask[n][d / 32] is set (mask NULL: when d <= t, a chain; a single token is a
+ * tree of one node):
+ *     x_j = scale * q[n][hq] . k_j      over the slots j that it sees
+ *     lse[n][hq] = log sum_j exp(x_j),  o[n][hq] = sum_j exp(x_j - lse) v_j
+ *     acc_out[slot j] = decay * acc_in[slot j] + sum over the tokens of the
+ *                       sequence and the query heads of the key/value head of
+ *                       exp(x_j - lse)                     (where asked for)
+ * A row that sees no key, or only keys of score -inf, gets o = 0 and
+ * lse = -inf and adds no weight. What it does not see never reaches a row:
+ * not stale slots after the end, nor infinities or NaNs in masked drafts.
+ * Results do not depend on the order in which thread blocks finish.
+ *   q [N] rows of Hq * D in the cache's type, 16-byte aligned, q_stride
+ *     elements apart (a multiple of 8)
+ *   max_draft  an upper bound of the drafts of a sequence, 1 .. 256
+ *   mask  [N][mask_words] uint32, mask_words * 32 >= max_draft, or NULL
+ *   o     [N][Hq][D] in o_dtype (QMV_F32 or the cache's), 16-byte aligned
+ *   lse   [N][Hq] fp32
+ *   acc_in, acc_out  [pages][Hkv][page] fp32: acc_out NULL: no weights; acc_in
+ *     NULL: counts as zeros; both may be the same array. Slots that no
+ *     sequence of the call holds are not touched.
+ *   ws  at least attn_tree_workspace_bytes(...) bytes, 256-byte aligned, not
+ *     shared with a concurrent call. */
+int attn_tree(const qmv_attn_cache *c, const void *q, int64_t q_stride, int Hq,
+              const int32_t *table, int max_pages, const int32_t *ctx, const int32_t *cu, int B,
+              int N, int max_draft, const uint32_t *mask, int mask_words, float scale, void *o,
+              int o_dtype, float *lse, const float *acc_in, float *acc_out, float decay,
+              int32_t *status, void *ws, size_t ws_bytes, qmv_stream_t stream);
+
+/* Eviction by accumulated attention weight. Each key/value head of a sequence
+ * of lens[b] tokens keeps min(lens[b], budget) of them: all when they fit,
+ * else the first `sink`, the last `recent` and, of those between, the
+ * budget - sink - recent with the largest acc (equal sums: the lower slot; a
+ * NaN sum counts as the lowest). The kept tokens stay in order and are copied,
+ * with their sums, to slots 0, 1, ... of the pages of dst_table (pages that
+ * hold no token of `table`; dst may be src's pool or another of the same Hkv,
+ * D and dtype). Rotations stay those of the tokens' own positions.
+ *   acc [src pages][Hkv][page] fp32, dst_acc [dst pages][Hkv][dst page] fp32
+ *   dst_table [B][dst_max_pages] int32, with room for the kept tokens
+ *   keep [B][Hkv][budget] int32: the kept slots, ascending, then -1 (written)
+ *   new_lens [B] int32: min(lens[b], budget) (written)
+ *   budget >= 1; sink, recent >= 0, sink + recent <= budget.
+ * A sequence whose length does not fit the table keeps nothing (status 2). */
+int attn_evict(const qmv_attn_cache *src, const float *acc, const int32_t *table, int max_pages,
+               const int32_t *lens, int B, int budget, int sink, int recent,
+               const qmv_attn_cache *dst, float *dst_acc, const int32_t *dst_table,
+               int dst_max_pages, int32_t *keep, int32_t *new_lens, int32_t *status,
+               qmv_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

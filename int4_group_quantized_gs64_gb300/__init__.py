@@ -10,7 +10,8 @@ Functions carry the C names: ``qmv_int4_gs``, ``qmv_int8_row``, their bf16-outpu
 forms ``qmv_int4_gs_bf16`` and ``qmv_int8_row_bf16``,
 ``moe_route_topk``, ``moe_group``, ``moe_gate_up_silu``, ``moe_down``,
 ``moe_combine``, ``moe_workspace_bytes``, ``moe_expert_ffn_int4`` and
-``moe_expert_ffn_int4_prefill``.
+``moe_expert_ffn_int4_prefill``; ``attn_rope_append``, ``attn_tree`` and
+``attn_evict`` over a paged cache (``AttnCache``).
 """
 from __future__ import annotations
 
@@ -30,6 +31,13 @@ class QmvError(RuntimeError):
         msg = lib().qmv_status_str(status).decode() if _lib is not None else "?"
         super().__init__(f"{fn} failed: {QMV_STATUS.get(status, status)} ({msg})")
         self.status = status
+
+
+class AttnCacheDesc(ctypes.Structure):
+    """Mirror of ``qmv_attn_cache``."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("pages", ctypes.c_int32),
+                ("Hkv", ctypes.c_int32), ("page", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
 
 
 class MoeDesc(ctypes.Structure):
@@ -56,7 +64,8 @@ def lib():
             raise RuntimeError("libqmv.so is not built: call int4_group_quantized_gs64_gb300.build()")
         L = ctypes.CDLL(_build.LIB)
         vp, i32, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
-        P = ctypes.POINTER(MoeDesc)
+        i64, f32 = ctypes.c_int64, ctypes.c_float
+        P, C = ctypes.POINTER(MoeDesc), ctypes.POINTER(AttnCacheDesc)
         sig = {
             "qmv_version": ([], i32),
             "qmv_test_split_skew": ([i32], i32),
@@ -86,6 +95,13 @@ def lib():
             "moe_expert_ffn_int4_resident": ([P, vp, vp, i32, vp, vp, i32, vp, vp, vp, sz, vp], i32),
             "moe_prefill_workspace_bytes": ([P, i32, i32], sz),
             "moe_expert_ffn_int4_prefill": ([P, vp, i32, vp, vp, i32, vp, vp, sz, vp], i32),
+            "attn_rope_append": ([C, vp, i64, vp, i64, vp, i64, i32, i32, vp, vp, i32, i32, f32, vp,
+                                  i32, vp, vp, i32, i32, vp, vp, vp, vp], i32),
+            "attn_tree_workspace_bytes": ([C, i32, i32, i32, i32, i32, i32], sz),
+            "attn_tree": ([C, vp, i64, i32, vp, i32, vp, vp, i32, i32, i32, vp, i32, f32, vp, i32,
+                           vp, vp, vp, f32, vp, vp, sz, vp], i32),
+            "attn_evict": ([C, vp, vp, i32, vp, i32, i32, i32, i32, C, vp, vp, i32, vp, vp, vp, vp],
+                           i32),
         }
         for name, (args, res) in sig.items():
             if hasattr(L, name):
@@ -473,3 +489,195 @@ def moe_expert_ffn_int4_prefill(m: MoeInt4Weights, x_bf16, ids, w, out=None, ws=
         m.desc, _ptr(x_bf16), T, _ptr(ids), _ptr(w), k, _ptr(out), _ptr(ws), ws.numel(),
         _stream(stream)))
     return out
+
+
+# ------------------------------------------------------------------ attention
+
+class AttnCache:
+    """A paged key/value cache of one layer: k and v [pages][Hkv][page][D], bf16 or fp16."""
+
+    def __init__(self, k, v):
+        import torch
+        if not isinstance(k, torch.Tensor) or k.dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError("k must be a bfloat16 or float16 CUDA tensor")
+        _need(k, k.dtype, "k"); _need(v, k.dtype, "v")
+        if k.dim() != 4 or v.shape != k.shape:
+            raise ValueError("k and v must both be [pages][Hkv][page][D]")
+        self.k, self.v = k, v
+        self.pages, self.Hkv, self.page, self.D = k.shape
+        self.dtype, self.device = k.dtype, k.device
+        self.qmv_dtype = 1 if k.dtype == torch.bfloat16 else 2
+        self._desc = AttnCacheDesc(k.data_ptr(), v.data_ptr(), self.pages, self.Hkv, self.page,
+                                   self.D, self.qmv_dtype)
+        self.desc = ctypes.byref(self._desc)
+
+    @classmethod
+    def empty(cls, pages: int, Hkv: int, page: int, D: int, dtype=None, device="cuda"):
+        import torch
+        k = torch.empty((pages, Hkv, page, D), dtype=dtype or torch.bfloat16, device=device)
+        return cls(k, torch.empty_like(k))
+
+
+def _empty(shape, dtype, device, stream):
+    """An output or scratch tensor that belongs to the stream the call runs on."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _rows(t, name, heads, D):
+    """t [N][heads][D] with whole heads in a row: its elements between tokens."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D:
+        raise ValueError(f"{name} must be [N][{heads}][{D}]")
+    n, s = t.shape[0], t.stride()
+    if not t.is_cuda or s[2] != 1 or (heads > 1 and s[1] != D):
+        raise ValueError(f"{name} must be on the GPU with a token's heads contiguous")
+    return s[0] if n > 1 else max(s[0], heads * D)
+
+
+def _batch(table, ctx, cu):
+    import torch
+    _need(table, torch.int32, "table"); _need(ctx, torch.int32, "ctx")
+    if table.dim() != 2 or ctx.numel() != table.shape[0]:
+        raise ValueError("table must be [B][max_pages] with one ctx (or len) a sequence")
+    if cu is not None:
+        _need(cu, torch.int32, "cu")
+        if cu.numel() != ctx.numel() + 1:
+            raise ValueError("cu must have B + 1 entries")
+    return table.shape
+
+
+def _pool_floats(t, c: AttnCache, name):
+    import torch
+    _need(t, torch.float32, name)
+    if t.numel() != c.pages * c.Hkv * c.page:
+        raise ValueError(f"{name} must be [pages][Hkv][page]")
+
+
+def _status(status):
+    import torch
+    if status is not None:
+        _need(status, torch.int32, "status")
+
+
+def attn_rope_append(cache: AttnCache, q, k, v, pos, inv_freq, table, ctx, cu,
+                     interleaved: bool = False, mscale: float = 1.0, q_out=None, acc=None,
+                     status=None, stream=None):
+    """Rotary positions of new tokens and their append to the cache; returns the rotated queries.
+
+    q [N][Hq][D], k and v [N][Hkv][D] in fp32 or the cache's type (rows may be strided);
+    pos int32 [N]; inv_freq float64 [rot/2]; table int32 [B][max_pages]; ctx int32 [B];
+    cu int32 [B+1]. acc (fp32 [pages][Hkv][page]) is cleared for the new tokens."""
+    import torch
+    dt = q.dtype
+    if dt not in (torch.float32, cache.dtype) or k.dtype != dt or v.dtype != dt:
+        raise TypeError(f"q, k and v must all be float32 or all {cache.dtype}")
+    N, Hq, D = q.shape
+    qs = _rows(q, "q", Hq, cache.D)
+    ks, vs = _rows(k, "k", cache.Hkv, D), _rows(v, "v", cache.Hkv, D)
+    if k.shape[0] != N or v.shape[0] != N:
+        raise ValueError("q, k and v must have as many tokens")
+    _need(pos, torch.int32, "pos"); _need(inv_freq, torch.float64, "inv_freq")
+    if pos.numel() != N:
+        raise ValueError("pos must have one entry a token")
+    B, max_pages = _batch(table, ctx, cu)
+    if acc is not None:
+        _pool_floats(acc, cache, "acc")
+    _status(status)
+    if q_out is None:
+        q_out = _empty((N, Hq, D), cache.dtype, q.device, stream)
+    elif _need(q_out, cache.dtype, "q_out").shape != q.shape:
+        raise ValueError("q_out must have q's shape")
+    _check("attn_rope_append", lib().attn_rope_append(
+        cache.desc, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+        0 if dt == torch.float32 else cache.qmv_dtype, Hq, pos.data_ptr(), inv_freq.data_ptr(),
+        2 * inv_freq.numel(), int(interleaved), mscale, table.data_ptr(), max_pages,
+        ctx.data_ptr(), cu.data_ptr(), B, N, q_out.data_ptr(), _ptr(acc), _ptr(status),
+        _stream(stream)))
+    return q_out
+
+
+def attn_tree_workspace_bytes(cache: AttnCache, Hq: int, B: int, N: int, max_draft: int,
+                              max_pages: int, weights: bool = False) -> int:
+    return int(lib().attn_tree_workspace_bytes(cache.desc, Hq, B, N, max_draft, max_pages,
+                                               int(weights)))
+
+
+def attn_tree(cache: AttnCache, q, table, ctx, cu, max_draft: int, mask=None, scale=None, o=None,
+              o_dtype=None, lse=None, acc=None, acc_out=None, decay: float = 1.0, ws=None,
+              status=None, stream=None):
+    """Attention of drafted tokens over the cache; returns (o [N][Hq][D], lse fp32 [N][Hq]).
+
+    q [N][Hq][D] in the cache's type; mask int32 [N][words], bit d of a token's words set when
+    it sees draft d of its sequence (None: drafts 0..itself); scale defaults to D ** -0.5;
+    o_dtype the cache's (default) or float32. acc / acc_out (fp32 [pages][Hkv][page]):
+    acc_out = decay * acc + this call's attention weights; acc alone is updated in place."""
+    import torch
+    if q.dtype != cache.dtype:
+        raise TypeError(f"q must be {cache.dtype}, got {q.dtype}")
+    N, Hq, D = q.shape
+    qs = _rows(q, "q", Hq, cache.D)
+    B, max_pages = _batch(table, ctx, cu)
+    words = 0
+    if mask is not None:
+        _need(mask, torch.int32, "mask")
+        if mask.dim() != 2 or mask.shape[0] != N:
+            raise ValueError("mask must be [N][words]")
+        words = mask.shape[1]
+    if acc is not None:
+        _pool_floats(acc, cache, "acc")
+        if acc_out is None:
+            acc_out = acc
+    if acc_out is not None and acc_out is not acc:
+        _pool_floats(acc_out, cache, "acc_out")
+    _status(status)
+    if o is None:
+        o = _empty((N, Hq, D), o_dtype or cache.dtype, q.device, stream)
+    else:
+        _need(o, o_dtype or o.dtype, "o")
+        if o.shape != q.shape:
+            raise ValueError("o must have q's shape")
+    if o.dtype not in (torch.float32, cache.dtype):
+        raise TypeError(f"o must be float32 or {cache.dtype}")
+    if lse is None:
+        lse = _empty((N, Hq), torch.float32, q.device, stream)
+    elif _need(lse, torch.float32, "lse").numel() != N * Hq:
+        raise ValueError("lse must be [N][Hq]")
+    if ws is None:
+        ws = _empty(max(256, attn_tree_workspace_bytes(cache, Hq, B, N, max_draft, max_pages,
+                                                       acc_out is not None)),
+                    torch.uint8, q.device, stream)
+    _check("attn_tree", lib().attn_tree(
+        cache.desc, q.data_ptr(), qs, Hq, table.data_ptr(), max_pages, ctx.data_ptr(),
+        cu.data_ptr(), B, N, max_draft, _ptr(mask), words, D ** -0.5 if scale is None else scale,
+        o.data_ptr(), 0 if o.dtype == torch.float32 else cache.qmv_dtype, lse.data_ptr(),
+        _ptr(acc), _ptr(acc_out), decay, _ptr(status), ws.data_ptr(), ws.numel(),
+        _stream(stream)))
+    return o, lse
+
+
+def attn_evict(src: AttnCache, acc, table, lens, budget: int, dst: AttnCache, dst_acc, dst_table,
+               sink: int = 0, recent: int = 0, keep=None, new_lens=None, status=None, stream=None):
+    """Keeps `budget` tokens a sequence and head by accumulated weight, copied to dst's pages.
+
+    Returns (keep int32 [B][Hkv][budget], new_lens int32 [B])."""
+    import torch
+    B, max_pages = _batch(table, lens, None)
+    Bd, dst_max_pages = _batch(dst_table, lens, None)
+    _pool_floats(acc, src, "acc"); _pool_floats(dst_acc, dst, "dst_acc")
+    _status(status)
+    if keep is None:
+        keep = _empty((B, src.Hkv, max(budget, 0)), torch.int32, src.device, stream)
+    elif _need(keep, torch.int32, "keep").numel() != B * src.Hkv * budget:
+        raise ValueError("keep must be [B][Hkv][budget]")
+    if new_lens is None:
+        new_lens = _empty((B,), torch.int32, src.device, stream)
+    elif _need(new_lens, torch.int32, "new_lens").numel() != B:
+        raise ValueError("new_lens must have one entry a sequence")
+    _check("attn_evict", lib().attn_evict(
+        src.desc, acc.data_ptr(), table.data_ptr(), max_pages, lens.data_ptr(), B, budget, sink,
+        recent, dst.desc, dst_acc.data_ptr(), dst_table.data_ptr(), dst_max_pages, keep.data_ptr(),
+        new_lens.data_ptr(), _ptr(status), _stream(stream)))
+    return keep, new_lens

@@ -1,0 +1,743 @@
+// qmv_attn_tree.cu - attention of drafted tokens over a paged cache.
+//
+// For sequence b with ctx cached tokens and T drafted ones, the rows of
+// key/value head h are the T * G pairs (draft t, query head h * G + g),
+// G = Hq / Hkv: they share the keys, so one pass over the keys serves them
+// all. Row r sees key j when j < ctx, or when j = ctx + d and bit d of its
+// token's mask is set:
+//     x_j = scale * q . k_j,   o = sum_j exp(x_j - M) v_j / sum_j exp(x_j - M)
+// with the running maximum M and sum of the softmax carried along the keys
+// (in units of log2, so the exponential is one ex2), in fp32.
+//
+// Work: an item is (b, h, block of rows); its keys come in units. All items'
+// units in order are one sequence that the thread blocks share out evenly, so
+// ragged contexts and few heads fill the GPU alike. A block's part of an item
+// is a segment; a segment that is not the whole item leaves its unnormalised
+// sum, maximum and sum of exponentials in the workspace, and k_attn_join adds
+// them up in key order (the same order every time).
+#include <math.h>
+#include <string.h>
+
+#include "qmv_attn.cuh"
+#include "qmv_attn.h"
+#include "qmv_internal.h"
+#include "qmv_launch.cuh"
+
+namespace qmv {
+namespace attn {
+namespace {
+
+constexpr uint32_t kPoll = 1u << 22;  // polls of a copy's barrier before giving up
+
+struct TreeArgs {
+    Seqs s;
+    const uint16_t *q;
+    long long q_stride;
+    int Hq, Hkv, G, pages;
+    const uint32_t *mask;
+    int words;
+    // |scale| * log2(e), so that a masked score can be -inf before the scaling;
+    // the sign goes to the queries (xor), a scale of zero clears them (and)
+    float sl2;
+    uint32_t qxor, qand;
+    void *o;
+    int o_f32;
+    float *lse;
+    float *part_o;   // [grid][2][rows][D]
+    float *part_ml;  // [grid][2][rows][2]
+    int grid, rows, unit;
+    const uint16_t *kpool;
+    const float *acc_in;
+    float *acc_out;
+    float decay;
+    int32_t *status;
+};
+
+__device__ __forceinline__ int row_blocks(const Seq &q, int G, int rows) {
+    return (q.T * G + rows - 1) / rows;
+}
+__device__ __forceinline__ int key_units(const Seq &q, int unit) {
+    return (q.ctx + q.T + unit - 1) / unit;
+}
+
+// All items' units before sequence `upto` (B: all of them). One thread of the
+// block handles ceil(B / threads) sequences; sh: a long long per warp.
+template <int kThreads>
+__device__ long long units_before(const TreeArgs &a, int upto, long long *sh) {
+    const int per = (a.s.B + kThreads - 1) / kThreads;
+    long long n = 0;
+    for (int i = 0; i < per; ++i) {
+        const int b = threadIdx.x * per + i;
+        if (b >= upto) break;
+        bool ok;
+        const Seq q = get_seq(a.s, b, ok);
+        n += (long long)key_units(q, a.unit) * row_blocks(q, a.G, a.rows) * a.Hkv * (q.T > 0);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = n;
+    __syncthreads();
+    n = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) n += sh[w];
+    return n;
+}
+
+// The place of a unit: sequence, head, row block, unit of the item's keys.
+struct Cursor {
+    int b, h, rb, u;
+    int nu, nrb;
+    Seq q;
+    __device__ __forceinline__ void load(const TreeArgs &a) {
+        bool ok;
+        q = get_seq(a.s, b, ok);
+        nu = key_units(q, a.unit);
+        nrb = row_blocks(q, a.G, a.rows);
+    }
+    __device__ __forceinline__ void next_item(const TreeArgs &a) {
+        u = 0;
+        if (++rb < nrb) return;
+        rb = 0;
+        if (++h < a.Hkv) return;
+        h = 0;
+        do {
+            ++b;
+            if (b >= a.s.B) return;
+            load(a);
+        } while (q.T == 0);
+    }
+    // To unit x of all (whose sequence exists).
+    __device__ __forceinline__ void seek(const TreeArgs &a, long long x) {
+        for (b = 0; b < a.s.B; ++b) {
+            load(a);
+            const long long n = q.T > 0 ? (long long)nu * nrb * a.Hkv : 0;
+            if (x < n) break;
+            x -= n;
+        }
+        const long long item = x / nu;
+        u = (int)(x - item * nu);
+        h = (int)(item / nrb);
+        rb = (int)(item - (long long)h * nrb);
+    }
+};
+
+__device__ __forceinline__ bool draft_visible(const TreeArgs &a, const Seq &q, int t, int d) {
+    if (d >= q.T) return false;
+    if (!a.mask) return d <= t;
+    return (a.mask[(long long)(q.first + t) * a.words + (d >> 5)] >> (d & 31)) & 1u;
+}
+
+// Byte offset of 16-byte chunk c of row r in a copied slice of `rows` rows:
+// [chunk of 128 bytes][row][128 bytes], the 16-byte units XOR-ed with row mod 8.
+template <int kRows>
+__device__ __forceinline__ uint32_t slice_ofs(int r, int c) {
+    return (uint32_t)((c >> 3) * (kRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+// ------------------------------------------------------------------ few rows
+
+// Up to 16 * MT rows an item, on the warp MMA. Each of the NW warps takes 16
+// keys of every unit through its own ring of kStages copies and keeps its own
+// maximum, sum and output accumulators, so the warps meet only at a segment's
+// end. What bounds it is the stream of keys and values: 16 rows need 4 x 16
+// multiply-adds per loaded value, far below the warp MMA's rate.
+//
+// The exponentials go to the second product as two 16-bit numbers each (the
+// rounded value and the rounded rest), so the output carries no more than its
+// own rounding; the extra products are free next to the copies.
+template <int D, int MT, int NW>
+struct RowsShape {
+    static constexpr int kRows = 16 * MT;
+    static constexpr int kSlice = 16 * D * 2;         // bytes of 16 keys (or values)
+    static constexpr int kStages = 3 * 128 / D;
+    static constexpr int kRing = NW * kStages * 2 * kSlice;
+    static constexpr int kBuf = kRows * D * 4;
+    static constexpr int kMl = NW * kRows * 8;
+    static constexpr int kSmem = kRing + kBuf + kMl + NW * kStages * 12 + 8 * NW + 16;
+};
+
+template <int D, int MT, int NW, bool kBf16>
+__global__ void __launch_bounds__(32 * NW, NW == 4 ? 2 : 1)
+    k_attn_rows(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                const TreeArgs a) {
+    using S = RowsShape<D, MT, NW>;
+    constexpr int kRows = S::kRows, kStages = S::kStages, KK = D / 16;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    float *buf = reinterpret_cast<float *>(smem + S::kRing);
+    float2 *ml = reinterpret_cast<float2 *>(smem + S::kRing + S::kBuf);
+    long long *scan = reinterpret_cast<long long *>(smem + S::kRing + S::kBuf + S::kMl);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(scan + NW);
+    int *flags = reinterpret_cast<int *>(bars + NW * kStages);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    if (threadIdx.x == 0) {
+        prefetch_tmap(&kmap);
+        prefetch_tmap(&vmap);
+    }
+    uint64_t *bar = bars + warp * kStages;
+    int *flag = flags + warp * kStages;
+    if (lane == 0) {
+        for (int i = 0; i < kStages; ++i) tc05::mbar_init(bar + i, 1);
+        tc05::fence_mbar_init();
+    }
+    if (blockIdx.x == 0 && a.status) {
+        for (int b = threadIdx.x; b < a.s.B; b += 32 * NW) {
+            bool ok;
+            get_seq(a.s, b, ok);
+            if (!ok) set_status(a.status, kStLength);
+        }
+    }
+    const long long total = units_before<32 * NW>(a, a.s.B, scan);
+    const long long quota = (total + a.grid - 1) / a.grid;
+    const long long u0 = quota * blockIdx.x;
+    const long long u1 = min(u0 + quota, total);
+    if (u0 >= u1) return;
+
+    Cursor pc, cc;  // of the copies, of the products
+    cc.seek(a, u0);
+    pc = cc;
+    long long pu = u0;  // next unit to copy
+    int pstage = 0, pid = 0;
+    const uint32_t ring = tc05::smem_addr(smem) + warp * (kStages * 2 * S::kSlice);
+
+    auto fetch_page = [&]() {
+        const int s0 = pc.u * a.unit + warp * 16;
+        pid = s0 < pc.q.ctx + pc.q.T
+                  ? __ldg(a.s.table + (long long)pc.b * a.s.max_pages + (s0 >> a.s.lpage))
+                  : 0;
+    };
+    // Issues the copies of this warp's 16 keys and values of unit pu, then
+    // starts the load of the next unit's page id.
+    auto issue = [&]() {
+        const int s0 = pc.u * a.unit + warp * 16;
+        const bool live = s0 < pc.q.ctx + pc.q.T;
+        const bool good = live && (unsigned)pid < (unsigned)a.pages;
+        if (lane == 0) {
+            flag[pstage] = good;
+            uint64_t *br = bar + pstage;
+            if (good) {
+                const int row = (pid * a.Hkv + pc.h) * a.s.page + (s0 & (a.s.page - 1));
+                const uint32_t dst = ring + pstage * (2 * S::kSlice);
+                mbar_expect_tx(br, 2 * S::kSlice);
+                tma_load3(dst, &kmap, 0, row, 0, br);
+                tma_load3(dst + S::kSlice, &vmap, 0, row, 0, br);
+            } else {
+                mbar_arrive(br);
+                if (live) set_status(a.status, kStPage);
+            }
+        }
+        if (++pstage == kStages) pstage = 0;
+        ++pu;
+        if (++pc.u == pc.nu) pc.next_item(a);
+        if (pu < u1) fetch_page();
+    };
+
+    fetch_page();
+    for (int i = 0; i < kStages - 1 && pu < u1; ++i) issue();
+
+    // key and 16-byte chunk of this lane's row in the 8x8 matrices of an ldmatrix
+    const int kkey = (lane & 7) + ((lane >> 4) << 3), kchk = (lane >> 3) & 1;
+    const int vkey = (lane & 7) + (((lane >> 3) & 1) << 3), vchk = lane >> 4;
+    const int g = lane >> 2, c = lane & 3;
+
+    int stage = 0;
+    uint32_t phase = 0;
+    bool dead = false;
+    long long u = u0;
+    while (u < u1) {
+        // ---- one segment
+        const bool at_start = cc.u == 0, first_seg = u == u0;
+        const int seg_h = cc.h, seg_rb = cc.rb;
+        const Seq sq = cc.q;
+        const int nrows = sq.T * a.G;
+        uint32_t qf[MT][KK][4];
+        int rt[MT][2];  // draft of each of this lane's rows, -1: no row
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = seg_rb * kRows + m * 16 + e * 8 + g;
+                const bool have = r < nrows;
+                const int t = have ? r / a.G : 0;
+                rt[m][e] = have ? t : -1;
+                const uint16_t *p = a.q + (long long)(sq.first + t) * a.q_stride +
+                                    (long long)(seg_h * a.G + (have ? r - t * a.G : 0)) * D;
+#pragma unroll
+                for (int k = 0; k < KK; ++k) {
+                    const uint32_t *w = reinterpret_cast<const uint32_t *>(p + k * 16 + c * 2);
+                    qf[m][k][e] = have ? (w[0] ^ a.qxor) & a.qand : 0u;
+                    qf[m][k][e + 2] = have ? (w[4] ^ a.qxor) & a.qand : 0u;
+                }
+            }
+        }
+        float o[MT][D / 8][4];
+        float mx[MT][2], l[MT][2];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[m][n][i] = 0.f;
+            mx[m][0] = mx[m][1] = -INFINITY;
+            l[m][0] = l[m][1] = 0.f;
+        }
+        bool done = false;
+        while (!done) {
+            if (pu < u1 && !dead) issue();
+            if (!dead && !tc05::mbar_wait(bar + stage, phase, kPoll)) {
+                // give up: flag it, and wait (bounded as well) for the copies in flight
+                dead = true;
+                if (lane == 0) set_status(a.status, kStTimeout);
+                int ds = stage;
+                uint32_t dp = phase;
+                for (long long x = u; x < pu; ++x) {
+                    tc05::mbar_wait(bar + ds, dp, kPoll);
+                    if (++ds == kStages) {
+                        ds = 0;
+                        dp ^= 1;
+                    }
+                }
+            }
+            dead = __any_sync(0xFFFFFFFFu, dead);
+            const int s0 = cc.u * a.unit + warp * 16;
+            if (!dead && flag[stage]) {
+                const uint32_t ks = ring + stage * (2 * S::kSlice), vs = ks + S::kSlice;
+                float s[MT][2][4];
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) s[m][n][i] = 0.f;
+#pragma unroll
+                for (int k = 0; k < KK; ++k) {
+                    uint32_t kb[4];
+                    ldmatrix4(kb, ks + slice_ofs<16>(kkey, 2 * k + kchk));
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        mma16816<kBf16>(s[m][0], qf[m][k], kb[0], kb[1]);
+                        mma16816<kBf16>(s[m][1], qf[m][k], kb[2], kb[3]);
+                    }
+                }
+                if (s0 + 16 > sq.ctx) {  // drafts, or the end of the sequence, in this slice
+                    const int len = sq.ctx + sq.T;
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int n = 0; n < 2; ++n)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int j = s0 + n * 8 + c * 2 + (i & 1);
+                                if (j >= sq.ctx && !(rt[m][i >> 1] >= 0 &&
+                                                     draft_visible(a, sq, rt[m][i >> 1], j - sq.ctx)))
+                                    s[m][n][i] = -INFINITY;
+                            }
+                    // Values that some row must not see are kept out of the
+                    // product where zero times them is not zero: rows past the
+                    // end (whatever an unused slot holds) become zeros, and a
+                    // draft's infinities and NaNs are added to the rows that
+                    // see it and replaced by zeros.
+                    for (int j = 0; j < 16; ++j) {
+                        const int key = s0 + j;
+                        if (key < sq.ctx) continue;
+                        bool bad = false;
+                        for (int w = lane; w < D / 2; w += 32) {
+                            const uint32_t ad = vs + slice_ofs<16>(j, w >> 2) + (w & 3) * 4;
+                            if (key >= len)
+                                sts32(ad, 0u);
+                            else
+                                bad |= nonfinite2<kBf16>(lds32(ad));
+                        }
+                        if (__any_sync(0xFFFFFFFFu, bad)) {
+                            __syncwarp();
+#pragma unroll
+                            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e)
+                                    if (rt[m][e] >= 0 && draft_visible(a, sq, rt[m][e], key - sq.ctx))
+#pragma unroll
+                                        for (int n = 0; n < D / 8; ++n) {
+                                            const float2 f = unpack2<kBf16>(
+                                                lds32(vs + slice_ofs<16>(j, n) + c * 4));
+                                            if (!isfinite(f.x)) o[m][n][2 * e] += f.x;
+                                            if (!isfinite(f.y)) o[m][n][2 * e + 1] += f.y;
+                                        }
+                            __syncwarp();
+                            for (int w = lane; w < D / 2; w += 32) {
+                                const uint32_t ad = vs + slice_ofs<16>(j, w >> 2) + (w & 3) * 4;
+                                uint32_t v = lds32(ad);
+                                if (nonfinite2<kBf16>(v & 0xFFFFu)) v &= 0xFFFF0000u;
+                                if (nonfinite2<kBf16>(v & 0xFFFF0000u)) v &= 0x0000FFFFu;
+                                sts32(ad, v);
+                            }
+                        }
+                    }
+                    // the next copy into this slot comes from the async proxy
+                    tc05::fence_proxy_async();
+                    __syncwarp();
+                }
+                uint32_t ph[MT][4], pl[MT][4];
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float t = fmaxf(fmaxf(s[m][0][2 * e] * a.sl2, s[m][0][2 * e + 1] * a.sl2),
+                                        fmaxf(s[m][1][2 * e] * a.sl2, s[m][1][2 * e + 1] * a.sl2));
+                        t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 1));
+                        t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 2));
+                        const float mn = fmaxf(mx[m][e], t);
+                        if (__any_sync(0xFFFFFFFFu, mn > mx[m][e])) {
+                            const float al = mn == mx[m][e] ? 1.f : ex2(mx[m][e] - mn);
+                            mx[m][e] = mn;
+                            l[m][e] *= al;
+#pragma unroll
+                            for (int n = 0; n < D / 8; ++n) {
+                                o[m][n][2 * e] *= al;
+                                o[m][n][2 * e + 1] *= al;
+                            }
+                        }
+                        const float base = mx[m][e] == -INFINITY ? 0.f : mx[m][e];
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) {
+                            const float p0 = ex2(fmaf(s[m][n][2 * e], a.sl2, -base));
+                            const float p1 = ex2(fmaf(s[m][n][2 * e + 1], a.sl2, -base));
+                            l[m][e] += p0 + p1;
+                            const uint32_t hi = pack2<kBf16>(p0, p1);
+                            const float2 f = unpack2<kBf16>(hi);
+                            ph[m][2 * n + e] = hi;
+                            pl[m][2 * n + e] = pack2<kBf16>(p0 - f.x, p1 - f.y);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < KK; ++k) {
+                    uint32_t vb[4];
+                    ldmatrix4_trans(vb, vs + slice_ofs<16>(vkey, 2 * k + vchk));
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        mma16816<kBf16>(o[m][2 * k], ph[m], vb[0], vb[1]);
+                        mma16816<kBf16>(o[m][2 * k + 1], ph[m], vb[2], vb[3]);
+                        mma16816<kBf16>(o[m][2 * k], pl[m], vb[0], vb[1]);
+                        mma16816<kBf16>(o[m][2 * k + 1], pl[m], vb[2], vb[3]);
+                    }
+                }
+            }
+            __syncwarp();  // the slot may be copied into again
+            if (++stage == kStages) {
+                stage = 0;
+                phase ^= 1;
+            }
+            ++u;
+            done = ++cc.u == cc.nu || u == u1;
+        }
+        const bool whole = at_start && cc.u == cc.nu;
+        if (cc.u == cc.nu) cc.next_item(a);
+
+        // ---- the segment's end: the warps' sums, one warp after the other
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                l[m][e] += __shfl_xor_sync(0xFFFFFFFFu, l[m][e], 1);
+                l[m][e] += __shfl_xor_sync(0xFFFFFFFFu, l[m][e], 2);
+                if (c == 0) ml[warp * kRows + m * 16 + e * 8 + g] = make_float2(mx[m][e], l[m][e]);
+            }
+        __syncthreads();
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float M = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < NW; ++w)
+                    M = fmaxf(M, ml[w * kRows + m * 16 + e * 8 + g].x);
+                const float f = mx[m][e] == -INFINITY ? 1.f : ex2(mx[m][e] - M);
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n) {
+                    o[m][n][2 * e] *= f;
+                    o[m][n][2 * e + 1] *= f;
+                }
+            }
+        for (int w = 0; w < NW; ++w) {
+            if (warp == w) {
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int n = 0; n < D / 8; ++n) {
+                            const int r = m * 16 + e * 8 + g;
+                            float2 *p = reinterpret_cast<float2 *>(
+                                buf + r * D + ((n * 8 + c * 2) ^ ((r & 3) << 3)));
+                            float2 v = make_float2(o[m][n][2 * e], o[m][n][2 * e + 1]);
+                            if (w > 0) {
+                                v.x += p->x;
+                                v.y += p->y;
+                            }
+                            *p = v;
+                        }
+            }
+            __syncthreads();
+        }
+        // rows out: two columns a thread
+        const int used = min(kRows, nrows - seg_rb * kRows);
+        for (int i = threadIdx.x; i < used * (D / 2); i += 32 * NW) {
+            const int r = i / (D / 2), col = (i - r * (D / 2)) * 2;
+            float M = -INFINITY, L = 0.f;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) M = fmaxf(M, ml[w * kRows + r].x);
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                const float2 v = ml[w * kRows + r];
+                L += v.x == -INFINITY ? v.y : v.y * ex2(v.x - M);
+            }
+            float2 v = *reinterpret_cast<const float2 *>(buf + r * D + (col ^ ((r & 3) << 3)));
+            if (whole) {
+                const float inv = L == 0.f ? 0.f : 1.f / L;
+                v.x *= inv;
+                v.y *= inv;
+                const int rr = seg_rb * kRows + r, t = rr / a.G;
+                const long long row = (long long)(sq.first + t) * a.Hq + seg_h * a.G + rr - t * a.G;
+                if (a.o_f32)
+                    *reinterpret_cast<float2 *>(static_cast<float *>(a.o) + row * D + col) = v;
+                else
+                    *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.o) + row * D + col) =
+                        pack2<kBf16>(v.x, v.y);
+                if (col == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+            } else {
+                const long long slot = ((long long)blockIdx.x * 2 + (first_seg ? 0 : 1)) * kRows + r;
+                *reinterpret_cast<float2 *>(a.part_o + slot * D + col) = v;
+                if (col == 0) *reinterpret_cast<float2 *>(a.part_ml + slot * 2) = make_float2(M, L);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// ------------------------------------------------------------------ joining segments
+
+// One warp adds up the segments of one row of an item that several blocks
+// shared, in key order.
+template <int D>
+__global__ void __launch_bounds__(128) k_attn_join(const TreeArgs a, bool bf16) {
+    __shared__ long long scan[4];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int b = blockIdx.x / a.Hkv, h = blockIdx.x - b * a.Hkv, rb = blockIdx.y;
+    const long long total = units_before<128>(a, a.s.B, scan);
+    const long long before = units_before<128>(a, b, scan);
+    bool ok;
+    const Seq q = get_seq(a.s, b, ok);
+    const int nu = key_units(q, a.unit), nrb = row_blocks(q, a.G, a.rows);
+    if (q.T == 0 || rb >= nrb) return;
+    const long long quota = (total + a.grid - 1) / a.grid;
+    const long long i0 = before + ((long long)h * nrb + rb) * nu, i1 = i0 + nu;
+    const int c0 = (int)(i0 / quota), c1 = (int)((i1 - 1) / quota);
+    if (c0 == c1) return;  // one segment: written by its block
+    const int r = blockIdx.z * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int rr = rb * a.rows + r;
+    if (r >= a.rows || rr >= q.T * a.G) return;
+
+    auto slot = [&](int cta) {
+        return ((long long)cta * 2 + ((long long)cta * quota >= i0 ? 0 : 1)) * a.rows + r;
+    };
+    float M = -INFINITY;
+    for (int x = c0 + lane; x <= c1; x += 32) M = fmaxf(M, a.part_ml[slot(x) * 2]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+    constexpr int V = D / 32;
+    float acc[V], L = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.f;
+#pragma unroll 4
+    for (int x = c0; x <= c1; ++x) {
+        const long long s = slot(x);
+        const float2 v = *reinterpret_cast<const float2 *>(a.part_ml + s * 2);
+        const float f = v.x == -INFINITY ? 1.f : ex2(v.x - M);
+        L += v.y * f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] += a.part_o[s * D + lane * V + i] * f;
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const int t = rr / a.G;
+    const long long row = (long long)(q.first + t) * a.Hq + h * a.G + rr - t * a.G;
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+        const float x0 = acc[i] * inv, x1 = acc[i + 1] * inv;
+        const long long at = row * D + lane * V + i;
+        if (a.o_f32)
+            *reinterpret_cast<float2 *>(static_cast<float *>(a.o) + at) = make_float2(x0, x1);
+        else
+            *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.o) + at) =
+                bf16 ? pack2<true>(x0, x1) : pack2<false>(x0, x1);
+    }
+    if (lane == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+}
+
+// ------------------------------------------------------------------ attention weights
+
+// acc_out[slot] = decay * acc_in[slot] + sum over the head's rows of
+// exp(x - lse): a second product of queries and keys, now that every row's
+// lse is known. A warp takes 16 keys and walks the rows 16 at a time.
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(128) k_attn_weights(const TreeArgs a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int b = blockIdx.z, h = blockIdx.y;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    bool ok;
+    const Seq q = get_seq(a.s, b, ok);
+    const int len = q.ctx + q.T, s0 = blockIdx.x * 64 + warp * 16;
+    if (q.T == 0 || s0 >= len) return;
+    const int pid = a.s.table[(long long)b * a.s.max_pages + (s0 >> a.s.lpage)];
+    if ((unsigned)pid >= (unsigned)a.pages) return;
+    const long long prow = ((long long)pid * a.Hkv + h) * a.s.page + (s0 & (a.s.page - 1));
+    constexpr int KK = D / 16;
+    uint32_t kb[2][KK][2];
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int k = 0; k < KK; ++k) {
+            const uint32_t *p = reinterpret_cast<const uint32_t *>(
+                a.kpool + (prow + n * 8 + g) * D + k * 16 + c * 2);
+            kb[n][k][0] = p[0];
+            kb[n][k][1] = p[4];
+        }
+    float w[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+    const int nrows = q.T * a.G;
+    for (int r0 = 0; r0 < nrows; r0 += 16) {
+        uint32_t qf[KK][4];
+        int rt[2];
+        float e2[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = r0 + e * 8 + g;
+            const bool have = r < nrows;
+            const int t = have ? r / a.G : 0;
+            const int head = h * a.G + (have ? r - t * a.G : 0);
+            rt[e] = t;
+            e2[e] = have ? a.lse[(long long)(q.first + t) * a.Hq + head] * kLog2e : -INFINITY;
+            const uint16_t *p = a.q + (long long)(q.first + t) * a.q_stride + (long long)head * D;
+#pragma unroll
+            for (int k = 0; k < KK; ++k) {
+                const uint32_t *x = reinterpret_cast<const uint32_t *>(p + k * 16 + c * 2);
+                qf[k][e] = (x[0] ^ a.qxor) & a.qand;
+                qf[k][e + 2] = (x[4] ^ a.qxor) & a.qand;
+            }
+        }
+        float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+        for (int k = 0; k < KK; ++k) {
+            mma16816<kBf16>(s[0], qf[k], kb[0][k][0], kb[0][k][1]);
+            mma16816<kBf16>(s[1], qf[k], kb[1][k][0], kb[1][k][1]);
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int j = s0 + n * 8 + c * 2 + (i & 1);
+                const bool seen = e2[i >> 1] != -INFINITY &&
+                                  (j < q.ctx || draft_visible(a, q, rt[i >> 1], j - q.ctx));
+                if (seen) w[n][i & 1] += ex2(fmaf(s[n][i], a.sl2, -e2[i >> 1]));
+            }
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) w[n][i] += __shfl_xor_sync(0xFFFFFFFFu, w[n][i], o);
+            const int j = n * 8 + c * 2 + i;
+            if (g == 0 && s0 + j < len) {
+                const float old = a.acc_in ? a.acc_in[prow + j] : 0.f;
+                a.acc_out[prow + j] = a.decay * old + w[n][i];
+            }
+        }
+}
+
+// ------------------------------------------------------------------ host
+
+template <int D, int MT, int NW, bool kBf16>
+cudaError_t run_rows(const CUtensorMap &km, const CUtensorMap &vm, const TreeArgs &a,
+                     cudaStream_t st) {
+    auto *k = k_attn_rows<D, MT, NW, kBf16>;
+    constexpr int smem = RowsShape<D, MT, NW>::kSmem;
+    cudaError_t e = set_smem(k, smem);
+    if (e == cudaSuccess) e = launch(k, dim3(a.grid), dim3(32 * NW), smem, st, true, km, vm, a);
+    return e;
+}
+
+template <int D, bool kBf16>
+cudaError_t run_tree(const CUtensorMap &km, const CUtensorMap &vm, const TreeArgs &a, int max_rows,
+                     cudaStream_t st) {
+    cudaError_t e = a.rows == 16 ? run_rows<D, 1, 4, kBf16>(km, vm, a, st)
+                                 : run_rows<D, 2, 8, kBf16>(km, vm, a, st);
+    const int nrb = (max_rows + a.rows - 1) / a.rows;
+    const int rz = ((max_rows < a.rows ? max_rows : a.rows) + 3) / 4;
+    if (e == cudaSuccess)
+        e = launch(k_attn_join<D>, dim3(a.s.B * a.Hkv, nrb, rz), dim3(128), 0, st, true, a,
+                   (bool)kBf16);
+    if (e == cudaSuccess && a.acc_out) {
+        const unsigned tiles = (unsigned)((((long long)a.s.max_pages << a.s.lpage) + 63) / 64);
+        e = launch(k_attn_weights<D, kBf16>, dim3(tiles, a.Hkv, a.s.B), dim3(128), 0, st, true, a);
+    }
+    return e;
+}
+
+int tree_rows(int max_rows) { return max_rows <= 16 ? 16 : 32; }
+int tree_grid_max(int rows) { return sm_count() * (rows == 16 ? 2 : 1); }
+
+}  // namespace
+}  // namespace attn
+
+size_t attn_tree_ws_bytes(const AttnCache &c, int Hq, int B, int N, int max_draft, int max_pages,
+                          bool acc) {
+    (void)B; (void)N; (void)max_pages; (void)acc;
+    const int rows = attn::tree_rows(max_draft * (Hq / c.Hkv));
+    const size_t slots = (size_t)attn::tree_grid_max(rows) * 2 * rows;
+    return (slots * (c.D + 2) * 4 + 255) / 256 * 256;
+}
+
+cudaError_t launch_attn_tree(const AttnCache &c, const TreeCall &t, cudaStream_t st) {
+    using namespace attn;
+    TreeArgs a;
+    memset(&a, 0, sizeof(a));
+    int lpage = 0;
+    while ((1 << lpage) < c.page) ++lpage;
+    a.s = Seqs{t.s.table, t.s.ctx, t.s.cu, t.s.B, t.s.N, t.s.max_draft, t.s.max_pages, c.page, lpage};
+    a.q = static_cast<const uint16_t *>(t.q);
+    a.q_stride = t.q_stride;
+    a.Hq = t.Hq; a.Hkv = c.Hkv; a.G = t.Hq / c.Hkv; a.pages = c.pages;
+    a.mask = t.mask; a.words = t.words;
+    a.sl2 = t.scale == 0.f ? 1.f : fabsf(t.scale) * kLog2e;
+    a.qxor = t.scale < 0.f ? 0x80008000u : 0u;
+    a.qand = t.scale == 0.f ? 0u : 0xFFFFFFFFu;
+    a.o = t.o; a.o_f32 = t.o_f32; a.lse = t.lse;
+    a.kpool = static_cast<const uint16_t *>(c.k);
+    a.acc_in = t.acc_in; a.acc_out = t.acc_out; a.decay = t.decay;
+    a.status = t.status;
+    const int max_rows = t.s.max_draft * a.G;
+    a.rows = tree_rows(max_rows);
+    a.unit = a.rows == 16 ? 64 : 128;
+    const long long most = (long long)t.s.B * c.Hkv * ((max_rows + a.rows - 1) / a.rows) *
+                           ((((long long)t.s.max_pages << lpage) + a.unit - 1) / a.unit);
+    const int gmax = tree_grid_max(a.rows);
+    a.grid = most < gmax ? (int)most : gmax;
+    a.part_o = static_cast<float *>(t.ws);
+    a.part_ml = a.part_o + (size_t)gmax * 2 * a.rows * c.D;
+    CUtensorMap km, vm;
+    const long long rows = (long long)c.pages * c.Hkv * c.page;
+    if (!encode_rows_swizzled(&km, static_cast<const uint8_t *>(c.k), rows, c.D * 2, 16) ||
+        !encode_rows_swizzled(&vm, static_cast<const uint8_t *>(c.v), rows, c.D * 2, 16))
+        return cudaErrorNotSupported;
+    if (c.D == 64)
+        return c.bf16 ? run_tree<64, true>(km, vm, a, max_rows, st)
+                      : run_tree<64, false>(km, vm, a, max_rows, st);
+    return c.bf16 ? run_tree<128, true>(km, vm, a, max_rows, st)
+                  : run_tree<128, false>(km, vm, a, max_rows, st);
+}
+
+}  // namespace qmv
