@@ -492,6 +492,9 @@ def moe_expert_ffn_int4_prefill(m: MoeInt4Weights, x_bf16, ids, w, out=None, ws=
 
 
 # ------------------------------------------------------------------ attention
+#
+# One-token calls are as short as their host side, so these bindings check each
+# tensor with a few attribute reads and pass plain integers.
 
 class AttnCache:
     """A paged key/value cache of one layer: k and v [pages][Hkv][page][D], bf16 or fp16."""
@@ -505,17 +508,30 @@ class AttnCache:
             raise ValueError("k and v must both be [pages][Hkv][page][D]")
         self.k, self.v = k, v
         self.pages, self.Hkv, self.page, self.D = k.shape
-        self.dtype, self.device = k.dtype, k.device
+        self.slots = self.pages * self.Hkv * self.page
+        self.dtype, self.device, self.device_index = k.dtype, k.device, k.get_device()
         self.qmv_dtype = 1 if k.dtype == torch.bfloat16 else 2
         self._desc = AttnCacheDesc(k.data_ptr(), v.data_ptr(), self.pages, self.Hkv, self.page,
                                    self.D, self.qmv_dtype)
         self.desc = ctypes.byref(self._desc)
+        self.kinds = {torch.float32: 0, k.dtype: self.qmv_dtype}  # what inputs and outputs may be
 
     @classmethod
     def empty(cls, pages: int, Hkv: int, page: int, D: int, dtype=None, device="cuda"):
         import torch
         k = torch.empty((pages, Hkv, page, D), dtype=dtype or torch.bfloat16, device=device)
         return cls(k, torch.empty_like(k))
+
+
+def _stream_of(stream, device_index):
+    """The raw handle of `stream`, or of the current stream of the device."""
+    import torch
+    if stream is not None:
+        return stream.cuda_stream
+    try:
+        return torch._C._cuda_getCurrentRawStream(device_index)
+    except AttributeError:  # (the same, some microseconds slower)
+        return torch.cuda.current_stream(device_index).cuda_stream
 
 
 def _empty(shape, dtype, device, stream):
@@ -527,39 +543,32 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _rows(t, name, heads, D):
-    """t [N][heads][D] with whole heads in a row: its elements between tokens."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != D:
-        raise ValueError(f"{name} must be [N][{heads}][{D}]")
-    n, s = t.shape[0], t.stride()
-    if not t.is_cuda or s[2] != 1 or (heads > 1 and s[1] != D):
+def _addr(t, dtype, numel, name):
+    """The address of a contiguous CUDA tensor of `numel` elements."""
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+        _need(t, dtype, name)
+    if t.numel() != numel:
+        raise ValueError(f"{name} must have {numel} elements, got {t.numel()}")
+    return t.data_ptr()
+
+
+def _token_stride(t, name, n, heads, D):
+    """t [n][heads][D] with a token's heads contiguous: the elements between tokens."""
+    if t.shape != (n, heads, D):
+        raise ValueError(f"{name} must be [{n}][{heads}][{D}], got {tuple(t.shape)}")
+    a, b, c = t.stride()
+    if not t.is_cuda or (c != 1 and D > 1) or (b != D and heads > 1):
         raise ValueError(f"{name} must be on the GPU with a token's heads contiguous")
-    return s[0] if n > 1 else max(s[0], heads * D)
+    return a if n > 1 else heads * D
 
 
-def _batch(table, ctx, cu):
+def _batch(table, name):
     import torch
-    _need(table, torch.int32, "table"); _need(ctx, torch.int32, "ctx")
-    if table.dim() != 2 or ctx.numel() != table.shape[0]:
-        raise ValueError("table must be [B][max_pages] with one ctx (or len) a sequence")
-    if cu is not None:
-        _need(cu, torch.int32, "cu")
-        if cu.numel() != ctx.numel() + 1:
-            raise ValueError("cu must have B + 1 entries")
+    if table.dtype is not torch.int32 or not table.is_cuda or not table.is_contiguous():
+        _need(table, torch.int32, name)
+    if table.dim() != 2:
+        raise ValueError(f"{name} must be [B][max_pages]")
     return table.shape
-
-
-def _pool_floats(t, c: AttnCache, name):
-    import torch
-    _need(t, torch.float32, name)
-    if t.numel() != c.pages * c.Hkv * c.page:
-        raise ValueError(f"{name} must be [pages][Hkv][page]")
-
-
-def _status(status):
-    import torch
-    if status is not None:
-        _need(status, torch.int32, "status")
 
 
 def attn_rope_append(cache: AttnCache, q, k, v, pos, inv_freq, table, ctx, cu,
@@ -571,31 +580,27 @@ def attn_rope_append(cache: AttnCache, q, k, v, pos, inv_freq, table, ctx, cu,
     pos int32 [N]; inv_freq float64 [rot/2]; table int32 [B][max_pages]; ctx int32 [B];
     cu int32 [B+1]. acc (fp32 [pages][Hkv][page]) is cleared for the new tokens."""
     import torch
-    dt = q.dtype
-    if dt not in (torch.float32, cache.dtype) or k.dtype != dt or v.dtype != dt:
+    dt, i32, D, Hkv = q.dtype, torch.int32, cache.D, cache.Hkv
+    kind = cache.kinds.get(dt)
+    if kind is None or k.dtype is not dt or v.dtype is not dt:
         raise TypeError(f"q, k and v must all be float32 or all {cache.dtype}")
-    N, Hq, D = q.shape
-    qs = _rows(q, "q", Hq, cache.D)
-    ks, vs = _rows(k, "k", cache.Hkv, D), _rows(v, "v", cache.Hkv, D)
-    if k.shape[0] != N or v.shape[0] != N:
-        raise ValueError("q, k and v must have as many tokens")
-    _need(pos, torch.int32, "pos"); _need(inv_freq, torch.float64, "inv_freq")
-    if pos.numel() != N:
-        raise ValueError("pos must have one entry a token")
-    B, max_pages = _batch(table, ctx, cu)
-    if acc is not None:
-        _pool_floats(acc, cache, "acc")
-    _status(status)
+    N, Hq = q.shape[0], q.shape[1]
+    B, max_pages = _batch(table, "table")
+    half = inv_freq.numel()
     if q_out is None:
-        q_out = _empty((N, Hq, D), cache.dtype, q.device, stream)
-    elif _need(q_out, cache.dtype, "q_out").shape != q.shape:
-        raise ValueError("q_out must have q's shape")
-    _check("attn_rope_append", lib().attn_rope_append(
-        cache.desc, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
-        0 if dt == torch.float32 else cache.qmv_dtype, Hq, pos.data_ptr(), inv_freq.data_ptr(),
-        2 * inv_freq.numel(), int(interleaved), mscale, table.data_ptr(), max_pages,
-        ctx.data_ptr(), cu.data_ptr(), B, N, q_out.data_ptr(), _ptr(acc), _ptr(status),
-        _stream(stream)))
+        q_out = _empty((N, Hq, D), cache.dtype, cache.device, stream)
+    r = (_lib or lib()).attn_rope_append(
+        cache.desc, q.data_ptr(), _token_stride(q, "q", N, Hq, D),
+        k.data_ptr(), _token_stride(k, "k", N, Hkv, D),
+        v.data_ptr(), _token_stride(v, "v", N, Hkv, D), kind, Hq, _addr(pos, i32, N, "pos"),
+        _addr(inv_freq, torch.float64, half, "inv_freq"), 2 * half, 1 if interleaved else 0, mscale,
+        table.data_ptr(), max_pages, _addr(ctx, i32, B, "ctx"), _addr(cu, i32, B + 1, "cu"), B, N,
+        _addr(q_out, cache.dtype, N * Hq * D, "q_out"),
+        None if acc is None else _addr(acc, torch.float32, cache.slots, "acc"),
+        None if status is None else _addr(status, i32, 1, "status"),
+        _stream_of(stream, cache.device_index))
+    if r:
+        _check("attn_rope_append", r)
     return q_out
 
 
@@ -615,46 +620,42 @@ def attn_tree(cache: AttnCache, q, table, ctx, cu, max_draft: int, mask=None, sc
     o_dtype the cache's (default) or float32. acc / acc_out (fp32 [pages][Hkv][page]):
     acc_out = decay * acc + this call's attention weights; acc alone is updated in place."""
     import torch
-    if q.dtype != cache.dtype:
+    i32, f32, D = torch.int32, torch.float32, cache.D
+    if q.dtype is not cache.dtype:
         raise TypeError(f"q must be {cache.dtype}, got {q.dtype}")
-    N, Hq, D = q.shape
-    qs = _rows(q, "q", Hq, cache.D)
-    B, max_pages = _batch(table, ctx, cu)
+    N, Hq = q.shape[0], q.shape[1]
+    B, max_pages = _batch(table, "table")
     words = 0
     if mask is not None:
-        _need(mask, torch.int32, "mask")
-        if mask.dim() != 2 or mask.shape[0] != N:
-            raise ValueError("mask must be [N][words]")
         words = mask.shape[1]
+    acc_p = out_p = None
     if acc is not None:
-        _pool_floats(acc, cache, "acc")
-        if acc_out is None:
-            acc_out = acc
-    if acc_out is not None and acc_out is not acc:
-        _pool_floats(acc_out, cache, "acc_out")
-    _status(status)
-    if o is None:
-        o = _empty((N, Hq, D), o_dtype or cache.dtype, q.device, stream)
-    else:
-        _need(o, o_dtype or o.dtype, "o")
-        if o.shape != q.shape:
-            raise ValueError("o must have q's shape")
-    if o.dtype not in (torch.float32, cache.dtype):
+        acc_p = out_p = _addr(acc, f32, cache.slots, "acc")
+    if acc_out is not None:
+        out_p = _addr(acc_out, f32, cache.slots, "acc_out")
+    odt = o_dtype or (cache.dtype if o is None else o.dtype)
+    kind = cache.kinds.get(odt)
+    if kind is None:
         raise TypeError(f"o must be float32 or {cache.dtype}")
+    if o is None:
+        o = _empty((N, Hq, D), odt, cache.device, stream)
     if lse is None:
-        lse = _empty((N, Hq), torch.float32, q.device, stream)
-    elif _need(lse, torch.float32, "lse").numel() != N * Hq:
-        raise ValueError("lse must be [N][Hq]")
+        lse = _empty((N, Hq), f32, cache.device, stream)
     if ws is None:
         ws = _empty(max(256, attn_tree_workspace_bytes(cache, Hq, B, N, max_draft, max_pages,
-                                                       acc_out is not None)),
-                    torch.uint8, q.device, stream)
-    _check("attn_tree", lib().attn_tree(
-        cache.desc, q.data_ptr(), qs, Hq, table.data_ptr(), max_pages, ctx.data_ptr(),
-        cu.data_ptr(), B, N, max_draft, _ptr(mask), words, D ** -0.5 if scale is None else scale,
-        o.data_ptr(), 0 if o.dtype == torch.float32 else cache.qmv_dtype, lse.data_ptr(),
-        _ptr(acc), _ptr(acc_out), decay, _ptr(status), ws.data_ptr(), ws.numel(),
-        _stream(stream)))
+                                                       out_p is not None)),
+                    torch.uint8, cache.device, stream)
+    r = (_lib or lib()).attn_tree(
+        cache.desc, q.data_ptr(), _token_stride(q, "q", N, Hq, D), Hq, table.data_ptr(), max_pages,
+        _addr(ctx, i32, B, "ctx"), _addr(cu, i32, B + 1, "cu"), B, N, max_draft,
+        None if mask is None else _addr(mask, i32, N * words, "mask"), words,
+        D ** -0.5 if scale is None else scale, _addr(o, odt, N * Hq * D, "o"), kind,
+        _addr(lse, f32, N * Hq, "lse"), acc_p, out_p, decay,
+        None if status is None else _addr(status, i32, 1, "status"),
+        _addr(ws, torch.uint8, ws.numel(), "ws"), ws.numel(),
+        _stream_of(stream, cache.device_index))
+    if r:
+        _check("attn_tree", r)
     return o, lse
 
 
@@ -664,20 +665,23 @@ def attn_evict(src: AttnCache, acc, table, lens, budget: int, dst: AttnCache, ds
 
     Returns (keep int32 [B][Hkv][budget], new_lens int32 [B])."""
     import torch
-    B, max_pages = _batch(table, lens, None)
-    Bd, dst_max_pages = _batch(dst_table, lens, None)
-    _pool_floats(acc, src, "acc"); _pool_floats(dst_acc, dst, "dst_acc")
-    _status(status)
+    i32, f32 = torch.int32, torch.float32
+    B, max_pages = _batch(table, "table")
+    Bd, dst_max_pages = _batch(dst_table, "dst_table")
+    if Bd != B:
+        raise ValueError("table and dst_table must have as many rows")
+    n = max(budget, 0)
     if keep is None:
-        keep = _empty((B, src.Hkv, max(budget, 0)), torch.int32, src.device, stream)
-    elif _need(keep, torch.int32, "keep").numel() != B * src.Hkv * budget:
-        raise ValueError("keep must be [B][Hkv][budget]")
+        keep = _empty((B, src.Hkv, n), i32, src.device, stream)
     if new_lens is None:
-        new_lens = _empty((B,), torch.int32, src.device, stream)
-    elif _need(new_lens, torch.int32, "new_lens").numel() != B:
-        raise ValueError("new_lens must have one entry a sequence")
-    _check("attn_evict", lib().attn_evict(
-        src.desc, acc.data_ptr(), table.data_ptr(), max_pages, lens.data_ptr(), B, budget, sink,
-        recent, dst.desc, dst_acc.data_ptr(), dst_table.data_ptr(), dst_max_pages, keep.data_ptr(),
-        new_lens.data_ptr(), _ptr(status), _stream(stream)))
+        new_lens = _empty((B,), i32, src.device, stream)
+    r = (_lib or lib()).attn_evict(
+        src.desc, _addr(acc, f32, src.slots, "acc"), table.data_ptr(), max_pages,
+        _addr(lens, i32, B, "lens"), B, budget, sink, recent, dst.desc,
+        _addr(dst_acc, f32, dst.slots, "dst_acc"), dst_table.data_ptr(), dst_max_pages,
+        _addr(keep, i32, B * src.Hkv * n, "keep"), _addr(new_lens, i32, B, "new_lens"),
+        None if status is None else _addr(status, i32, 1, "status"),
+        _stream_of(stream, src.device_index))
+    if r:
+        _check("attn_evict", r)
     return keep, new_lens

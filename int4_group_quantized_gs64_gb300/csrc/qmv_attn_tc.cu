@@ -1,0 +1,626 @@
+// qmv_attn_tc.cu - tree attention of many rows on the tcgen05 tensor cores.
+//
+// From some tens of rows on, a key's products cost more than the warp MMA
+// gives while the key streams in (128 rows: 128 products a loaded byte; the
+// GPU's ratio of tensor rate to bandwidth is near 290), so the scores and the
+// output come from tcgen05: S = Q K^T with both operands in shared memory,
+// O += P V with P in tensor memory.
+//
+// A block keeps two streams in flight, each with its own scores S (128
+// columns of tensor memory, overwritten by the weights P) and its own O, so
+// that one stream's products run under the other's exponentials:
+//   rows <= 128: one tile of 128 rows; the streams take alternate key tiles
+//                and are joined at the segment's end (in tensor memory, where
+//                both have the same row on the same lane);
+//   rows  > 128: two tiles of 128 rows against the same key tiles.
+// Warps: 0-3 and 4-7 the streams' softmax (a thread a row: maximum and sum
+// need no exchange), 8 the copies, 9 the products. A ring of 128-key tiles
+// holds keys and values in the order in which the products use them, across
+// segments. The running maximum moves only when it grows by more than 2^8 (a
+// row's weights may then exceed 1, which fp32 sums and 16-bit weights hold),
+// since moving it means rescaling O in tensor memory.
+//
+// Weights are rounded once to 16 bits for a 16-bit output (half a step of the
+// type, like the output's own rounding, and averaged over the keys); for an
+// fp32 output they are carried as two 16-bit numbers. fp16 weights are held
+// 2^7 times larger: the small ones would lose bits below fp16's range.
+#include <string.h>
+
+#include "qmv_attn.cuh"
+#include "qmv_attn.h"
+#include "qmv_attn_plan.cuh"
+#include "qmv_internal.h"
+#include "qmv_launch.cuh"
+
+namespace qmv {
+namespace attn {
+namespace {
+
+constexpr int kThreads = 320, kKeys = 128, kMaxStages = 12;
+constexpr int kMisc = 2560;               // barriers and small tables
+constexpr int kSmemMax = 227 * 1024;
+constexpr float kLazy = 8.f;              // log2 units the maximum may lag
+
+struct Misc {
+    long long scan[kThreads / 32];
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t s_full[2], p_ready[2], o_full[2], q_full, fin;
+    uint32_t tmem, dead;
+    uint32_t nf[8];        // drafts with infinities or NaNs among their values
+    float2 ml[2][128];
+};
+static_assert(sizeof(Misc) <= kMisc, "");
+
+// Waits for a barrier's phase; gives up after a bounded time, or at once when
+// another warp has given up.
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, Misc *m, int32_t *status) {
+    volatile uint32_t *dead = &m->dead;
+    for (int i = 0; i < 64; ++i) {
+        if (*dead) return false;
+        if (tc05::mbar_wait(bar, parity, kPoll / 64)) return true;
+    }
+    *dead = 1;
+    set_status(status, kStTimeout);
+    return false;
+}
+
+__device__ __forceinline__ void pair_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ bool pair_or(bool p) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 1, 256, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)p)
+        : "memory");
+    return r != 0;
+}
+
+// A block's part of an item: tiles [j0, j0 + n) of the item's keys.
+struct Segment {
+    int j0, n;
+    bool whole;
+    __device__ __forceinline__ Segment(const Cursor &c, long long u, long long u1) {
+        j0 = c.u;
+        n = (int)min((long long)(c.nu - c.u), u1 - u);
+        whole = j0 == 0 && n == c.nu;
+    }
+};
+
+template <int D, bool kBf16, bool kSplit>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_attn_tc(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+              const TreeArgs a, int stages) {
+    constexpr int kTile = kKeys * D * 2, kHalves = D / 64;
+    constexpr uint32_t kIdescS = tc05::idesc_f16kind_f32(kBf16, 128, kKeys, false);
+    constexpr uint32_t kIdescO = tc05::idesc_f16kind_f32(kBf16, 128, D, true);
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const bool two = a.rows == 256;
+    const int lag = two ? 1 : 2;  // tiles a product P V runs behind its Q K^T
+    uint8_t *qs = smem, *ring = smem + (two ? 2 : 1) * kTile;
+    Misc *m = reinterpret_cast<Misc *>(ring + stages * kTile);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (blockIdx.x == 0 && a.status) {
+        for (int b = threadIdx.x; b < a.s.B; b += kThreads) {
+            bool ok;
+            get_seq(a.s, b, ok);
+            if (!ok) set_status(a.status, kStLength);
+        }
+    }
+    const long long total = units_before<kThreads>(a, a.s.B, m->scan);
+    const long long quota = (total + a.grid - 1) / a.grid;
+    const long long u0 = quota * blockIdx.x;
+    const long long u1 = min(u0 + quota, total);
+    if (u0 >= u1) return;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < stages; ++i) {
+            tc05::mbar_init(m->full + i, 1);
+            tc05::mbar_init(m->empty + i, 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            tc05::mbar_init(m->s_full + s, 1);
+            tc05::mbar_init(m->p_ready + s, 4);
+            tc05::mbar_init(m->o_full + s, 1);
+        }
+        tc05::mbar_init(&m->q_full, 256);
+        tc05::mbar_init(&m->fin, 1);
+        m->dead = 0;
+        tc05::fence_mbar_init();
+        prefetch_tmap(&kmap);
+        prefetch_tmap(&vmap);
+    }
+    if (warp == 9) tc05::tmem_alloc(&m->tmem, 512);
+    tc05::fence_before_sync();
+    __syncthreads();
+    tc05::fence_after_sync();
+    const uint32_t tmem = m->tmem;
+
+    Cursor c;
+    c.seek(a, u0);
+    long long u = u0;
+
+    if (warp == 8) {
+        // ------------------------------------------------------------ copies
+        const int prow = a.s.page < kKeys ? a.s.page : kKeys;  // rows a copy
+        int stage = 0, issued = 0;
+        uint32_t phase = 1;  // a fresh barrier counts as passed for parity 1
+        int pid = 0;
+        bool live = false;
+        // this lane's piece of tile j of the sequence at c: its page
+        auto page_of = [&](int j, bool &lv) {
+            const int slot = j * kKeys + lane * prow;
+            lv = lane * prow < kKeys && slot < c.q.ctx + c.q.T;
+            return lv ? __ldg(a.s.table + (long long)c.b * a.s.max_pages + (slot >> a.s.lpage)) : 0;
+        };
+        while (u < u1) {
+            const Segment sg(c, u, u1);
+            // at step x: values of tile x - lag, then keys of tile x
+            int vp[2] = {0, 0};       // pages of the last tiles' keys, for their values
+            bool vl[2] = {false, false};
+            int np = page_of(sg.j0, live);
+            bool nl = live;
+            for (int x = 0; x < sg.n + lag; ++x) {
+#pragma unroll
+                for (int kind = 0; kind < 2; ++kind) {  // 0: values, 1: keys
+                    const int t = kind ? x : x - lag;
+                    if (t < 0 || t >= sg.n) continue;
+                    const int sl = two ? 0 : t & 1;
+                    if (kind) {
+                        pid = np;
+                        live = nl;
+                        vp[sl] = pid;
+                        vl[sl] = live;
+                        if (x + 1 < sg.n) np = page_of(sg.j0 + x + 1, nl);
+                    } else {
+                        pid = vp[sl];
+                        live = vl[sl];
+                    }
+                    const bool good = live && (unsigned)pid < (unsigned)a.pages;
+                    const uint32_t n = __popc(__ballot_sync(0xFFFFFFFFu, good));
+                    const bool ok = wait(m->empty + stage, phase, m, a.status);
+                    if (__all_sync(0xFFFFFFFFu, ok)) {
+                        if (lane == 0) {
+                            if (n)
+                                mbar_expect_tx(m->full + stage, n * prow * D * 2);
+                            else
+                                mbar_arrive(m->full + stage);
+                        }
+                        __syncwarp();
+                        if (good) {
+                            const int slot = (sg.j0 + t) * kKeys + lane * prow;
+                            const int row = (pid * a.Hkv + c.h) * a.s.page + (slot & (a.s.page - 1));
+                            const uint32_t dst = tc05::smem_addr(ring) + stage * kTile + lane * prow * 128;
+#pragma unroll
+                            for (int hf = 0; hf < kHalves; ++hf)
+                                tma_load3(dst + hf * (kKeys * 128), kind ? &kmap : &vmap, 0, row, hf,
+                                          m->full + stage);
+                        } else if (live && kind) {
+                            set_status(a.status, kStPage);
+                        }
+                        ++issued;
+                        if (++stage == stages) {
+                            stage = 0;
+                            phase ^= 1;
+                        }
+                    }
+                }
+            }
+            u += sg.n;
+            if (u < u1) c.next_item(a);
+        }
+        if (*(volatile uint32_t *)&m->dead) {
+            // gave up: wait (bounded) for the copies in flight
+            for (int i = 1; i <= stages && i <= issued; ++i) {
+                const int n = issued - i;
+                tc05::mbar_wait(m->full + n % stages, (n / stages) & 1, kPoll / 64);
+            }
+        }
+    } else if (warp == 9) {
+        // ------------------------------------------------------------ products
+        if (lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0, pp[2] = {0, 0}, qp = 0;
+            bool live = true;
+            const uint32_t q0 = tc05::smem_addr(qs), r0 = tc05::smem_addr(ring);
+            while (u < u1 && live) {
+                const Segment sg(c, u, u1);
+                live = wait(&m->q_full, qp, m, a.status);
+                qp ^= 1;
+                tc05::fence_after_sync();
+                for (int x = 0; x < sg.n + lag && live; ++x) {
+                    int vstage = stage;
+                    uint32_t vphase = phase;
+                    const bool hasv = x >= lag, hask = x < sg.n;
+                    int kstage = stage;
+                    uint32_t kphase = phase;
+                    if (hasv && ++kstage == stages) {
+                        kstage = 0;
+                        kphase ^= 1;
+                    }
+                    for (int s = two ? 0 : x & 1; s < (two ? 2 : (x & 1) + 1) && live; ++s) {
+                        if (hasv) {
+                            live = wait(m->p_ready + s, pp[s], m, a.status) &&
+                                   wait(m->full + vstage, vphase, m, a.status);
+                            if (!live) break;
+                            pp[s] ^= 1;
+                            tc05::fence_after_sync();
+                            const uint32_t vb = r0 + vstage * kTile;
+                            const bool first = x - lag < (two ? 1 : 2);
+                            for (int part = 0; part < (kSplit ? 2 : 1); ++part)
+#pragma unroll
+                                for (int k = 0; k < kKeys / 16; ++k)
+                                    tc05::mma_ts(tmem + 256 + s * 128,
+                                                 tmem + s * 128 + part * 64 + k * 8,
+                                                 tc05::sdesc_sw128_mn(vb + k * 2048, kKeys * 128),
+                                                 kIdescO, !(first && part == 0 && k == 0));
+                            if (!two || s == 1) tc05::mma_commit(m->empty + vstage);
+                            if (two ? x == sg.n : x >= sg.n) tc05::mma_commit(m->o_full + s);
+                        }
+                        if (hask) {
+                            if (!(live = wait(m->full + kstage, kphase, m, a.status))) break;
+                            tc05::fence_after_sync();
+                            const uint32_t kb = r0 + kstage * kTile, qb = q0 + (two ? s : 0) * kTile;
+#pragma unroll
+                            for (int k = 0; k < D / 16; ++k) {
+                                const uint32_t of = (k >> 2) * (kKeys * 128) + (k & 3) * 32;
+                                tc05::mma_ss(tmem + s * 128, tc05::sdesc_sw128(qb + of),
+                                             tc05::sdesc_sw128(kb + of), kIdescS, k > 0);
+                            }
+                            tc05::mma_commit(m->s_full + s);
+                            if (!two || s == 1) tc05::mma_commit(m->empty + kstage);
+                        }
+                    }
+                    const int used = (int)hasv + (int)hask;
+                    for (int i = 0; i < used; ++i)
+                        if (++stage == stages) {
+                            stage = 0;
+                            phase ^= 1;
+                        }
+                }
+                u += sg.n;
+                if (u < u1) c.next_item(a);
+            }
+            // nothing of this thread's is in flight when the block ends
+            tc05::mma_commit(&m->fin);
+            tc05::mbar_wait(&m->fin, 0, kPoll);
+        }
+        __syncwarp();
+    } else if (warp < 8) {
+        // ------------------------------------------------------------ softmax
+        const int s = warp >> 2, tid = threadIdx.x & 127, wq = warp & 3;
+        const uint32_t lanes = (uint32_t)(wq * 32) << 16;
+        const uint32_t ts = tmem + lanes + s * 128, to = tmem + lanes + 256;
+        uint32_t sp = 0, op = 0;
+        long long ops = 0;  // ring entries before this segment
+        const float boost = kBf16 ? 0.f : 7.f;
+        while (u < u1) {
+            const bool first_seg = u == u0;
+            const Segment sg(c, u, u1);
+            const Seq q = c.q;
+            const int len = q.ctx + q.T, nrows = q.T * a.G;
+            const int32_t *trow = a.s.table + (long long)c.b * a.s.max_pages;
+            const int ns = two ? sg.n : (sg.n + 1 - s) / 2;  // this stream's tiles
+            // ---- queries to shared memory, rows in the products' order
+            {
+                const int r = two ? tid : s * 64 + (tid >> 1);
+                const int rr = c.rb * a.rows + (two ? s * 128 : 0) + r;
+                const bool have = rr < nrows;
+                const int t = have ? rr / a.G : 0;
+                const uint4 *p = reinterpret_cast<const uint4 *>(
+                    a.q + (long long)(q.first + t) * a.q_stride +
+                    (long long)(c.h * a.G + (have ? rr - t * a.G : 0)) * D);
+                const int c0 = two ? 0 : (tid & 1) * (D / 16), cn = two ? D / 8 : D / 16;
+                uint8_t *dst = qs + (two ? s * kTile : 0) + r * 128;
+#pragma unroll 8
+                for (int i = 0; i < cn; ++i) {
+                    const int ch = c0 + i;
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (have) {
+                        v = __ldg(p + ch);
+                        v.x = (v.x ^ a.qxor) & a.qand;
+                        v.y = (v.y ^ a.qxor) & a.qand;
+                        v.z = (v.z ^ a.qxor) & a.qand;
+                        v.w = (v.w ^ a.qxor) & a.qand;
+                    }
+                    *reinterpret_cast<uint4 *>(dst + (ch >> 3) * (kKeys * 128) +
+                                               (((ch & 7) ^ (r & 7)) << 4)) = v;
+                }
+            }
+            tc05::fence_proxy_async();
+            mbar_arrive(&m->q_full);
+            // ---- pages that do not exist, among this segment's
+            bool bad = false;
+            {
+                const int p1 = (min(len, (sg.j0 + sg.n) * kKeys) + a.s.page - 1) >> a.s.lpage;
+                for (int p = ((sg.j0 * kKeys) >> a.s.lpage) + (threadIdx.x & 255); p < p1; p += 256)
+                    bad |= (unsigned)trow[p] >= (unsigned)a.pages;
+            }
+            if (threadIdx.x < 8) m->nf[threadIdx.x] = 0;
+            bad = pair_or(bad);
+
+            const int rbase = c.rb * a.rows + (two ? s * 128 : 0);
+            const int rr = rbase + tid;
+            const bool row_live = rr < nrows, warp_live = rbase + wq * 32 < nrows;
+            const int t = row_live ? rr / a.G : 0;
+            float mx = -INFINITY, l = 0.f;  // mx: the maximum in use (log2 units)
+            for (int i = 0; i < ns; ++i) {
+                const int tile = two ? i : 2 * i + s, j = sg.j0 + tile;
+                const bool special = bad || (j + 1) * kKeys > q.ctx;
+                if (special && (!two || s == 0)) {
+                    // Values that some row must not see are kept out of the
+                    // product where zero times them is not zero: a thread a
+                    // key, zeros past the end and where there is no page, and
+                    // a draft's infinities and NaNs noted and replaced.
+                    const long long pos = ops + min(tile + lag, sg.n) + tile;
+                    const int vst = (int)(pos % stages);
+                    if (wait(m->full + vst, (uint32_t)(pos / stages) & 1u, m, a.status)) {
+                        const int key = j * kKeys + tid;
+                        uint8_t *row = ring + vst * kTile + tid * 128;
+                        const bool none =
+                            key >= len || (bad && (unsigned)trow[key >> a.s.lpage] >= (unsigned)a.pages);
+                        if (none || key >= q.ctx) {
+                            bool inf = false;
+                            for (int ch = 0; ch < D / 8; ++ch) {
+                                uint4 *w = reinterpret_cast<uint4 *>(
+                                    row + (ch >> 3) * (kKeys * 128) + (((ch & 7) ^ (tid & 7)) << 4));
+                                uint32_t x[4] = {0u, 0u, 0u, 0u};
+                                if (!none) {
+                                    const uint4 v = *w;
+                                    x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        if (nonfinite2<kBf16>(x[e] & 0xFFFFu)) { x[e] &= 0xFFFF0000u; inf = true; }
+                                        if (nonfinite2<kBf16>(x[e] & 0xFFFF0000u)) { x[e] &= 0xFFFFu; inf = true; }
+                                    }
+                                }
+                                *w = make_uint4(x[0], x[1], x[2], x[3]);
+                            }
+                            if (inf) atomicOr(&m->nf[(key - q.ctx) >> 5], 1u << ((key - q.ctx) & 31));
+                        }
+                    }
+                    tc05::fence_proxy_async();
+                }
+                wait(m->s_full + s, sp, m, a.status);
+                __syncwarp();
+                sp ^= 1;
+                tc05::fence_after_sync();
+                if (warp_live) {
+                    // Two passes over the scores in tensor memory, 64 columns
+                    // at a time: the maximum, then the weights, which
+                    // overwrite scores already read.
+                    uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
+                    if (special) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            see[k] = row_live ? seen_word(a, q, t, j * kKeys + k * 32) : 0u;
+                            for (int h = 0; bad && h < 2; ++h) {
+                                const int slot = j * kKeys + k * 32 + h * 16;
+                                if (slot < len && (unsigned)trow[slot >> a.s.lpage] >= (unsigned)a.pages)
+                                    see[k] &= h ? 0x0000FFFFu : 0xFFFF0000u;
+                            }
+                        }
+                    }
+                    float tm = -INFINITY;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t x[2][32];
+                        tc05::tmem_ld32(ts + h * 64, x[0]);
+                        tc05::tmem_ld32(ts + h * 64 + 32, x[1]);
+                        tc05::tmem_wait_ld();
+                        if (special) {
+#pragma unroll
+                            for (int e = 0; e < 64; ++e)
+                                if ((see[2 * h + (e >> 5)] >> (e & 31)) & 1u)
+                                    tm = fmaxf(tm, __uint_as_float(x[e >> 5][e & 31]));
+                        } else {
+                            float v[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(x[0][e]);
+#pragma unroll
+                            for (int e = 4; e < 64; ++e)
+                                v[e & 3] = fmaxf(v[e & 3], __uint_as_float(x[e >> 5][e & 31]));
+                            tm = fmaxf(tm, fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])));
+                        }
+                    }
+                    tm *= a.sl2;
+                    const bool move = tm > mx + kLazy || (mx == -INFINITY && tm > mx);
+                    if (__any_sync(0xFFFFFFFFu, move)) {
+                        const float al = move ? ex2(mx - tm) : 1.f;
+                        if (move) mx = tm;
+                        l *= al;
+                        if (i > 0) {
+                            // all earlier products of this stream are done: they
+                            // were issued before this tile's scores
+#pragma unroll
+                            for (int k = 0; k < D / 32; ++k) {
+                                uint32_t o[32];
+                                tc05::tmem_ld32(to + s * 128 + k * 32, o);
+                                tc05::tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+                                tc05::tmem_st32(to + s * 128 + k * 32, o);
+                            }
+                        }
+                    }
+                    const float base = mx == -INFINITY ? 0.f : mx - boost;
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    uint32_t lo0[32];  // the first half's rests wait for the second's scores
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t x[2][32], hi[32], lo[32];
+                        tc05::tmem_ld32(ts + h * 64, x[0]);
+                        tc05::tmem_ld32(ts + h * 64 + 32, x[1]);
+                        tc05::tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            float s0 = __uint_as_float(x[(2 * e) >> 5][(2 * e) & 31]);
+                            float s1 = __uint_as_float(x[(2 * e) >> 5][(2 * e + 1) & 31]);
+                            if (special) {
+                                const uint32_t w = see[2 * h + (e >> 4)] >> ((2 * e) & 31);
+                                if (!(w & 1u)) s0 = -INFINITY;
+                                if (!(w & 2u)) s1 = -INFINITY;
+                            }
+                            const float p0 = ex2(fmaf(s0, a.sl2, -base));
+                            const float p1 = ex2(fmaf(s1, a.sl2, -base));
+                            sum[(2 * e) & 3] += p0;
+                            sum[(2 * e + 1) & 3] += p1;
+                            hi[e] = pack2<kBf16>(p0, p1);
+                            if (kSplit) {
+                                const float2 f = unpack2<kBf16>(hi[e]);
+                                lo[e] = pack2<kBf16>(p0 - f.x, p1 - f.y);
+                            }
+                        }
+                        tc05::tmem_st32(ts + h * 32, hi);
+                        if (kSplit) {
+                            if (h == 0) {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) lo0[e] = lo[e];
+                            } else {
+                                tc05::tmem_st32(ts + 64, lo0);
+                                tc05::tmem_st32(ts + 96, lo);
+                            }
+                        }
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tc05::tmem_wait_st();
+                }
+                tc05::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(m->p_ready + s);
+            }
+            // ---- the segment's end
+            if (ns > 0) {
+                wait(m->o_full + s, op, m, a.status);
+                op ^= 1;
+            }
+            if (mx != -INFINITY) mx -= boost;
+            m->ml[s][tid] = make_float2(mx, l);
+            pair_sync();
+            tc05::fence_after_sync();
+            if (warp_live) {
+                float M = mx, L = l, f0 = 1.f, f1 = 0.f;
+                if (!two) {
+                    const float2 v0 = m->ml[0][tid], v1 = m->ml[1][tid];
+                    M = fmaxf(v0.x, v1.x);
+                    f0 = v0.x == -INFINITY ? 1.f : ex2(v0.x - M);
+                    f1 = v1.x == -INFINITY ? 1.f : ex2(v1.x - M);
+                    L = v0.y * f0 + v1.y * f1;
+                }
+                const bool has1 = !two && sg.n > 1;
+                const float inv = sg.whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
+                const long long row =
+                    (long long)(q.first + t) * a.Hq + c.h * a.G + (row_live ? rr - t * a.G : 0);
+                const long long slot =
+                    ((long long)blockIdx.x * 2 + (first_seg ? 0 : 1)) * a.rows + (two ? s * 128 : 0) + tid;
+                bool odd = false;  // drafts to add by hand
+                for (int w = 0; w < 8; ++w) odd |= m->nf[w] != 0;
+                const int k0 = two ? 0 : s * (D / 64), k1 = two ? D / 32 : k0 + D / 64;
+                for (int k = k0; k < k1; ++k) {  // 32 columns at a time
+                    float o[32];
+                    tc05::tmem_ld32(to + (two ? s * 128 : 0) + k * 32,
+                                    *reinterpret_cast<uint32_t(*)[32]>(o));
+                    tc05::tmem_wait_ld();
+                    if (!two) {
+                        float o1[32];
+                        if (has1) {
+                            tc05::tmem_ld32(to + 128 + k * 32, *reinterpret_cast<uint32_t(*)[32]>(o1));
+                            tc05::tmem_wait_ld();
+                        }
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = has1 ? o[e] * f0 + o1[e] * f1 : o[e] * f0;
+                    }
+                    if (odd && row_live) {
+                        for (int d = 0; d < q.T; ++d) {
+                            if (!((m->nf[d >> 5] >> (d & 31)) & 1u) ||
+                                !(seen_word(a, q, t, q.ctx + d) & 1u))
+                                continue;
+                            const int sl = q.ctx + d, pid = trow[sl >> a.s.lpage];
+                            if ((unsigned)pid >= (unsigned)a.pages) continue;
+                            const uint16_t *v =
+                                a.vpool + (((long long)pid * a.Hkv + c.h) * a.s.page +
+                                           (sl & (a.s.page - 1))) * D + k * 32;
+                            for (int e = 0; e < 32; ++e) {
+                                const float y = to_f32<kBf16>(v[e]);
+                                if (!isfinite(y)) o[e] += y;
+                            }
+                        }
+                    }
+                    if (row_live) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] *= inv;
+                        if (!sg.whole || a.o_f32) {
+                            float4 *p = reinterpret_cast<float4 *>(
+                                sg.whole ? static_cast<float *>(a.o) + row * D + k * 32
+                                         : a.part_o + slot * D + k * 32);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                p[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        } else {
+                            uint4 *p = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.o) + row * D + k * 32);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                p[e] = make_uint4(pack2<kBf16>(o[8 * e], o[8 * e + 1]),
+                                                  pack2<kBf16>(o[8 * e + 2], o[8 * e + 3]),
+                                                  pack2<kBf16>(o[8 * e + 4], o[8 * e + 5]),
+                                                  pack2<kBf16>(o[8 * e + 6], o[8 * e + 7]));
+                        }
+                    }
+                }
+                if (row_live && (two || s == 0)) {
+                    if (sg.whole)
+                        a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+                    else
+                        *reinterpret_cast<float2 *>(a.part_ml + slot * 2) = make_float2(M, L);
+                }
+            }
+            tc05::fence_before_sync();
+            pair_sync();  // O, the queries and the tables may be overwritten
+            ops += 2LL * sg.n;
+            u += sg.n;
+            if (u < u1) c.next_item(a);
+        }
+    }
+    tc05::fence_before_sync();
+    __syncthreads();
+    tc05::fence_after_sync();
+    if (warp == 9) tc05::tmem_dealloc(tmem, 512);
+}
+
+template <int D, bool kBf16>
+cudaError_t run_tc(const CUtensorMap &km, const CUtensorMap &vm, const TreeArgs &a, cudaStream_t st) {
+    constexpr int kTile = kKeys * D * 2;
+    const int q = (a.rows == 256 ? 2 : 1) * kTile;
+    int stages = (kSmemMax - kMisc - q) / kTile;
+    if (stages > kMaxStages) stages = kMaxStages;
+    auto *k = a.o_f32 ? k_attn_tc<D, kBf16, true> : k_attn_tc<D, kBf16, false>;
+    cudaError_t e = set_smem(k, kSmemMax);
+    if (e == cudaSuccess)
+        e = launch(k, dim3(a.grid), dim3(kThreads), kSmemMax, st, true, km, vm, a, stages);
+    return e;
+}
+
+// A pool as a tensor map (128 bytes, row, 128-byte chunk), boxes of one chunk
+// of box_rows rows, 128-byte swizzle.
+bool encode_chunks(CUtensorMap *map, const void *base, long long rows, int D, int box_rows) {
+    return encode_rows_swizzled(map, static_cast<const uint8_t *>(base), rows, D * 2, box_rows, 1);
+}
+
+}  // namespace
+
+cudaError_t launch_tree_tc(const AttnCache &c, const TreeArgs &a, cudaStream_t st) {
+    CUtensorMap km, vm;
+    const long long rows = (long long)c.pages * c.Hkv * c.page;
+    const int box = c.page < kKeys ? c.page : kKeys;
+    if (!encode_chunks(&km, c.k, rows, c.D, box) || !encode_chunks(&vm, c.v, rows, c.D, box))
+        return cudaErrorNotSupported;
+    if (c.D == 64)
+        return c.bf16 ? run_tc<64, true>(km, vm, a, st) : run_tc<64, false>(km, vm, a, st);
+    return c.bf16 ? run_tc<128, true>(km, vm, a, st) : run_tc<128, false>(km, vm, a, st);
+}
+
+}  // namespace attn
+}  // namespace qmv

@@ -20,113 +20,13 @@
 
 #include "qmv_attn.cuh"
 #include "qmv_attn.h"
+#include "qmv_attn_plan.cuh"
 #include "qmv_internal.h"
 #include "qmv_launch.cuh"
 
 namespace qmv {
 namespace attn {
 namespace {
-
-constexpr uint32_t kPoll = 1u << 22;  // polls of a copy's barrier before giving up
-
-struct TreeArgs {
-    Seqs s;
-    const uint16_t *q;
-    long long q_stride;
-    int Hq, Hkv, G, pages;
-    const uint32_t *mask;
-    int words;
-    // |scale| * log2(e), so that a masked score can be -inf before the scaling;
-    // the sign goes to the queries (xor), a scale of zero clears them (and)
-    float sl2;
-    uint32_t qxor, qand;
-    void *o;
-    int o_f32;
-    float *lse;
-    float *part_o;   // [grid][2][rows][D]
-    float *part_ml;  // [grid][2][rows][2]
-    int grid, rows, unit;
-    const uint16_t *kpool;
-    const float *acc_in;
-    float *acc_out;
-    float decay;
-    int32_t *status;
-};
-
-__device__ __forceinline__ int row_blocks(const Seq &q, int G, int rows) {
-    return (q.T * G + rows - 1) / rows;
-}
-__device__ __forceinline__ int key_units(const Seq &q, int unit) {
-    return (q.ctx + q.T + unit - 1) / unit;
-}
-
-// All items' units before sequence `upto` (B: all of them). One thread of the
-// block handles ceil(B / threads) sequences; sh: a long long per warp.
-template <int kThreads>
-__device__ long long units_before(const TreeArgs &a, int upto, long long *sh) {
-    const int per = (a.s.B + kThreads - 1) / kThreads;
-    long long n = 0;
-    for (int i = 0; i < per; ++i) {
-        const int b = threadIdx.x * per + i;
-        if (b >= upto) break;
-        bool ok;
-        const Seq q = get_seq(a.s, b, ok);
-        n += (long long)key_units(q, a.unit) * row_blocks(q, a.G, a.rows) * a.Hkv * (q.T > 0);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = n;
-    __syncthreads();
-    n = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) n += sh[w];
-    return n;
-}
-
-// The place of a unit: sequence, head, row block, unit of the item's keys.
-struct Cursor {
-    int b, h, rb, u;
-    int nu, nrb;
-    Seq q;
-    __device__ __forceinline__ void load(const TreeArgs &a) {
-        bool ok;
-        q = get_seq(a.s, b, ok);
-        nu = key_units(q, a.unit);
-        nrb = row_blocks(q, a.G, a.rows);
-    }
-    __device__ __forceinline__ void next_item(const TreeArgs &a) {
-        u = 0;
-        if (++rb < nrb) return;
-        rb = 0;
-        if (++h < a.Hkv) return;
-        h = 0;
-        do {
-            ++b;
-            if (b >= a.s.B) return;
-            load(a);
-        } while (q.T == 0);
-    }
-    // To unit x of all (whose sequence exists).
-    __device__ __forceinline__ void seek(const TreeArgs &a, long long x) {
-        for (b = 0; b < a.s.B; ++b) {
-            load(a);
-            const long long n = q.T > 0 ? (long long)nu * nrb * a.Hkv : 0;
-            if (x < n) break;
-            x -= n;
-        }
-        const long long item = x / nu;
-        u = (int)(x - item * nu);
-        h = (int)(item / nrb);
-        rb = (int)(item - (long long)h * nrb);
-    }
-};
-
-__device__ __forceinline__ bool draft_visible(const TreeArgs &a, const Seq &q, int t, int d) {
-    if (d >= q.T) return false;
-    if (!a.mask) return d <= t;
-    return (a.mask[(long long)(q.first + t) * a.words + (d >> 5)] >> (d & 31)) & 1u;
-}
 
 // Byte offset of 16-byte chunk c of row r in a copied slice of `rows` rows:
 // [chunk of 128 bytes][row][128 bytes], the 16-byte units XOR-ed with row mod 8.
@@ -162,6 +62,9 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? 2 : 1)
     k_attn_rows(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                 const TreeArgs a) {
     using S = RowsShape<D, MT, NW>;
+    // fp16 weights are held 2^15 times larger: the small ones would lose bits
+    // below fp16's range
+    constexpr float kBoost = kBf16 ? 0.f : 15.f;
     constexpr int kRows = S::kRows, kStages = S::kStages, KK = D / 16;
     extern __shared__ __align__(1024) uint8_t smem[];
     float *buf = reinterpret_cast<float *>(smem + S::kRing);
@@ -325,17 +228,19 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? 2 : 1)
                 }
                 if (s0 + 16 > sq.ctx) {  // drafts, or the end of the sequence, in this slice
                     const int len = sq.ctx + sq.T;
+                    uint32_t see[MT][2];  // of this slice's 16 keys, by row
 #pragma unroll
                     for (int m = 0; m < MT; ++m)
 #pragma unroll
-                        for (int n = 0; n < 2; ++n)
+                        for (int e = 0; e < 2; ++e) {
+                            see[m][e] = rt[m][e] >= 0 ? seen_word(a, sq, rt[m][e], s0) : 0u;
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int j = s0 + n * 8 + c * 2 + (i & 1);
-                                if (j >= sq.ctx && !(rt[m][i >> 1] >= 0 &&
-                                                     draft_visible(a, sq, rt[m][i >> 1], j - sq.ctx)))
-                                    s[m][n][i] = -INFINITY;
-                            }
+                            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                                for (int i = 0; i < 2; ++i)
+                                    if (!((see[m][e] >> (n * 8 + c * 2 + i)) & 1u))
+                                        s[m][n][2 * e + i] = -INFINITY;
+                        }
                     // Values that some row must not see are kept out of the
                     // product where zero times them is not zero: rows past the
                     // end (whatever an unused slot holds) become zeros, and a
@@ -358,7 +263,7 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? 2 : 1)
                             for (int m = 0; m < MT; ++m)
 #pragma unroll
                                 for (int e = 0; e < 2; ++e)
-                                    if (rt[m][e] >= 0 && draft_visible(a, sq, rt[m][e], key - sq.ctx))
+                                    if ((see[m][e] >> j) & 1u)
 #pragma unroll
                                         for (int n = 0; n < D / 8; ++n) {
                                             const float2 f = unpack2<kBf16>(
@@ -400,7 +305,7 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? 2 : 1)
                                 o[m][n][2 * e + 1] *= al;
                             }
                         }
-                        const float base = mx[m][e] == -INFINITY ? 0.f : mx[m][e];
+                        const float base = mx[m][e] == -INFINITY ? 0.f : mx[m][e] - kBoost;
 #pragma unroll
                         for (int n = 0; n < 2; ++n) {
                             const float p0 = ex2(fmaf(s[m][n][2 * e], a.sl2, -base));
@@ -442,6 +347,7 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? 2 : 1)
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
+                if (mx[m][e] != -INFINITY) mx[m][e] -= kBoost;
                 l[m][e] += __shfl_xor_sync(0xFFFFFFFFu, l[m][e], 1);
                 l[m][e] += __shfl_xor_sync(0xFFFFFFFFu, l[m][e], 2);
                 if (c == 0) ml[warp * kRows + m * 16 + e * 8 + g] = make_float2(mx[m][e], l[m][e]);
@@ -628,6 +534,7 @@ __global__ void __launch_bounds__(128) k_attn_weights(const TreeArgs a) {
                 qf[k][e + 2] = (x[4] ^ a.qxor) & a.qand;
             }
         }
+        const uint32_t see[2] = {seen_word(a, q, rt[0], s0), seen_word(a, q, rt[1], s0)};
         float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
         for (int k = 0; k < KK; ++k) {
@@ -638,10 +545,8 @@ __global__ void __launch_bounds__(128) k_attn_weights(const TreeArgs a) {
         for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int j = s0 + n * 8 + c * 2 + (i & 1);
-                const bool seen = e2[i >> 1] != -INFINITY &&
-                                  (j < q.ctx || draft_visible(a, q, rt[i >> 1], j - q.ctx));
-                if (seen) w[n][i & 1] += ex2(fmaf(s[n][i], a.sl2, -e2[i >> 1]));
+                const int j = n * 8 + c * 2 + (i & 1);
+                if (e2[i >> 1] != -INFINITY && ((see[i >> 1] >> j) & 1u)) w[n][i & 1] += ex2(fmaf(s[n][i], a.sl2, -e2[i >> 1]));
             }
     }
 #pragma unroll
@@ -671,10 +576,11 @@ cudaError_t run_rows(const CUtensorMap &km, const CUtensorMap &vm, const TreeArg
 }
 
 template <int D, bool kBf16>
-cudaError_t run_tree(const CUtensorMap &km, const CUtensorMap &vm, const TreeArgs &a, int max_rows,
-                     cudaStream_t st) {
-    cudaError_t e = a.rows == 16 ? run_rows<D, 1, 4, kBf16>(km, vm, a, st)
-                                 : run_rows<D, 2, 8, kBf16>(km, vm, a, st);
+cudaError_t run_tree(const AttnCache &c, const CUtensorMap &km, const CUtensorMap &vm,
+                     const TreeArgs &a, int max_rows, cudaStream_t st) {
+    cudaError_t e = a.rows == 16   ? run_rows<D, 1, 4, kBf16>(km, vm, a, st)
+                    : a.rows == 32 ? run_rows<D, 2, 8, kBf16>(km, vm, a, st)
+                                   : launch_tree_tc(c, a, st);
     const int nrb = (max_rows + a.rows - 1) / a.rows;
     const int rz = ((max_rows < a.rows ? max_rows : a.rows) + 3) / 4;
     if (e == cudaSuccess)
@@ -687,7 +593,10 @@ cudaError_t run_tree(const CUtensorMap &km, const CUtensorMap &vm, const TreeArg
     return e;
 }
 
-int tree_rows(int max_rows) { return max_rows <= 16 ? 16 : 32; }
+// Rows an item: up to 32 on the warp MMA, more on tcgen05 (qmv_attn_tc.cu).
+int tree_rows(int max_rows) {
+    return max_rows <= 16 ? 16 : max_rows <= 32 ? 32 : max_rows <= 128 ? 128 : 256;
+}
 int tree_grid_max(int rows) { return sm_count() * (rows == 16 ? 2 : 1); }
 
 }  // namespace
@@ -717,11 +626,12 @@ cudaError_t launch_attn_tree(const AttnCache &c, const TreeCall &t, cudaStream_t
     a.qand = t.scale == 0.f ? 0u : 0xFFFFFFFFu;
     a.o = t.o; a.o_f32 = t.o_f32; a.lse = t.lse;
     a.kpool = static_cast<const uint16_t *>(c.k);
+    a.vpool = static_cast<const uint16_t *>(c.v);
     a.acc_in = t.acc_in; a.acc_out = t.acc_out; a.decay = t.decay;
     a.status = t.status;
     const int max_rows = t.s.max_draft * a.G;
     a.rows = tree_rows(max_rows);
-    a.unit = a.rows == 16 ? 64 : 128;
+    a.unit = a.rows == 16 ? 64 : 128;  // keys a unit
     const long long most = (long long)t.s.B * c.Hkv * ((max_rows + a.rows - 1) / a.rows) *
                            ((((long long)t.s.max_pages << lpage) + a.unit - 1) / a.unit);
     const int gmax = tree_grid_max(a.rows);
@@ -734,10 +644,10 @@ cudaError_t launch_attn_tree(const AttnCache &c, const TreeCall &t, cudaStream_t
         !encode_rows_swizzled(&vm, static_cast<const uint8_t *>(c.v), rows, c.D * 2, 16))
         return cudaErrorNotSupported;
     if (c.D == 64)
-        return c.bf16 ? run_tree<64, true>(km, vm, a, max_rows, st)
-                      : run_tree<64, false>(km, vm, a, max_rows, st);
-    return c.bf16 ? run_tree<128, true>(km, vm, a, max_rows, st)
-                  : run_tree<128, false>(km, vm, a, max_rows, st);
+        return c.bf16 ? run_tree<64, true>(c, km, vm, a, max_rows, st)
+                      : run_tree<64, false>(c, km, vm, a, max_rows, st);
+    return c.bf16 ? run_tree<128, true>(c, km, vm, a, max_rows, st)
+                  : run_tree<128, false>(c, km, vm, a, max_rows, st);
 }
 
 }  // namespace qmv
