@@ -24,7 +24,9 @@ struct TreeArgs {
     void *o;
     int o_f32;
     float *lse;
-    float *part_o;   // [grid][2][rows][D]
+    // segments' sums, [grid][2][D / 4][rows][4]: a thread a row or a lane group a
+    // row, stores and loads fill their sectors
+    float *part_o;
     float *part_ml;  // [grid][2][rows][2]
     int grid, rows, unit;
     const uint16_t *kpool, *vpool;
@@ -41,28 +43,104 @@ __device__ __forceinline__ int key_units(const Seq &q, int unit) {
     return (q.ctx + q.T + unit - 1) / unit;
 }
 
-// All items' units before sequence `upto` (B: all of them). One thread of the
-// block handles ceil(B / threads) sequences; sh: a long long per warp.
+// All items' units, and those before sequence `upto`. A thread of the block
+// handles ceil(B / threads) sequences; sh: two long longs a warp.
 template <int kThreads>
-__device__ long long units_before(const TreeArgs &a, int upto, long long *sh) {
+__device__ __forceinline__ long long count_units(const TreeArgs &a, int upto, long long *sh,
+                                                 long long &before) {
     const int per = (a.s.B + kThreads - 1) / kThreads;
-    long long n = 0;
+    long long n = 0, nb = 0;
+#pragma unroll 1
     for (int i = 0; i < per; ++i) {
         const int b = threadIdx.x * per + i;
-        if (b >= upto) break;
+        if (b >= a.s.B) break;
         bool ok;
         const Seq q = get_seq(a.s, b, ok);
-        n += (long long)key_units(q, a.unit) * row_blocks(q, a.G, a.rows) * a.Hkv * (q.T > 0);
+        const long long x =
+            q.T > 0 ? (long long)key_units(q, a.unit) * row_blocks(q, a.G, a.rows) * a.Hkv : 0;
+        n += x;
+        if (b < upto) nb += x;
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = n;
+    for (int o = 16; o > 0; o >>= 1) {
+        n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
+        nb += __shfl_xor_sync(0xFFFFFFFFu, nb, o);
+    }
+    if ((threadIdx.x & 31) == 0) {
+        sh[threadIdx.x >> 5] = n;
+        sh[kThreads / 32 + (threadIdx.x >> 5)] = nb;
+    }
     __syncthreads();
     n = 0;
+    before = 0;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) n += sh[w];
+    for (int w = 0; w < kThreads / 32; ++w) {
+        n += sh[w];
+        before += sh[kThreads / 32 + w];
+    }
     return n;
+}
+
+// This block's share [u0, u1) of all units, and where it starts.
+struct Share {
+    long long u0, u1, rest;  // rest: u0's place among its sequence's units
+    int b;
+};
+template <int kWarps>
+struct ShareScratch {
+    long long sums[kWarps];
+    long long rest;
+    int b;
+};
+
+// Each thread of the block counts ceil(B / threads) sequences in a row; the
+// one whose units hold u0 says where they start.
+template <int kThreads>
+__device__ __forceinline__ Share find_share(const TreeArgs &a, ShareScratch<kThreads / 32> *sh) {
+    const int per = (a.s.B + kThreads - 1) / kThreads, b0 = threadIdx.x * per;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    auto units = [&](int b) -> long long {
+        bool ok;
+        const Seq q = get_seq(a.s, b, ok);
+        return q.T > 0 ? (long long)key_units(q, a.unit) * row_blocks(q, a.G, a.rows) * a.Hkv : 0;
+    };
+    long long n = 0;
+#pragma unroll 1
+    for (int i = 0; i < per && b0 + i < a.s.B; ++i) n += units(b0 + i);
+    long long inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+        if (lane >= o) inc += v;
+    }
+    if (lane == 31) sh->sums[warp] = inc;
+    __syncthreads();
+    long long total = 0, before = inc - n;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += sh->sums[w];
+        total += sh->sums[w];
+    }
+    Share s;
+    const long long quota = (total + a.grid - 1) / a.grid;
+    s.u0 = quota * blockIdx.x;
+    s.u1 = min(s.u0 + quota, total);
+    if (s.u0 < s.u1 && before <= s.u0 && s.u0 < before + n) {
+#pragma unroll 1
+        for (int i = 0;; ++i) {
+            const long long v = units(b0 + i);
+            if (s.u0 < before + v) {
+                sh->b = b0 + i;
+                sh->rest = s.u0 - before;
+                break;
+            }
+            before += v;
+        }
+    }
+    __syncthreads();
+    s.b = sh->b;
+    s.rest = sh->rest;
+    return s;
 }
 
 // The place of a unit: sequence, head, row block, unit of the item's keys.
@@ -88,20 +166,22 @@ struct Cursor {
             load(a);
         } while (q.T == 0);
     }
-    // To unit x of all (whose sequence exists).
-    __device__ __forceinline__ void seek(const TreeArgs &a, long long x) {
-        for (b = 0; b < a.s.B; ++b) {
-            load(a);
-            const long long n = q.T > 0 ? (long long)nu * nrb * a.Hkv : 0;
-            if (x < n) break;
-            x -= n;
-        }
-        const long long item = x / nu;
-        u = (int)(x - item * nu);
-        h = (int)(item / nrb);
-        rb = (int)(item - (long long)h * nrb);
+    __device__ __forceinline__ void start(const TreeArgs &a, const Share &s) {
+        b = s.b;
+        load(a);
+        const int item = (int)(s.rest / nu);
+        u = (int)(s.rest - (long long)item * nu);
+        h = item / nrb;
+        rb = item - h * nrb;
     }
 };
+
+// Element `col` (a multiple of 4) of row r of a block's first or last segment.
+template <int D>
+__device__ __forceinline__ float *part_at(const TreeArgs &a, int block, int last, int r, int col) {
+    return a.part_o +
+           (((long long)block * 2 + last) * (D / 4) + (col >> 2)) * (a.rows * 4LL) + r * 4;
+}
 
 // Launches the tcgen05 kernel (qmv_attn_tc.cu) for a.rows = 128 or 256.
 cudaError_t launch_tree_tc(const AttnCache &c, const TreeArgs &a, cudaStream_t st);

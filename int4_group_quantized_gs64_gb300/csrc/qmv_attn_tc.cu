@@ -14,7 +14,10 @@
 //                both have the same row on the same lane);
 //   rows  > 128: two tiles of 128 rows against the same key tiles.
 // Warps: 0-3 and 4-7 the streams' softmax (a thread a row: maximum and sum
-// need no exchange), 8 the copies, 9 the products. A ring of 128-key tiles
+// need no exchange), 8 the copies, 9 and 10 the streams' products (11 only fills
+// up their warpgroup, which passes registers on to the softmax warps: their 128
+// scores stay in registers, since reading them from tensor memory twice would
+// cost as much as the products). A ring of 128-key tiles
 // holds keys and values in the order in which the products use them, across
 // segments. The running maximum moves only when it grows by more than 2^8 (a
 // row's weights may then exceed 1, which fp32 sums and 16-bit weights hold),
@@ -36,32 +39,39 @@ namespace qmv {
 namespace attn {
 namespace {
 
-constexpr int kThreads = 320, kKeys = 128, kMaxStages = 12;
-constexpr int kMisc = 2560;               // barriers and small tables
+constexpr int kThreads = 384, kKeys = 128, kMaxStages = 12;
+constexpr int kMisc = 2816;               // barriers and small tables
 constexpr int kSmemMax = 227 * 1024;
 constexpr float kLazy = 8.f;              // log2 units the maximum may lag
 
 struct Misc {
-    long long scan[kThreads / 32];
+    ShareScratch<kThreads / 32> share;
     uint64_t full[kMaxStages], empty[kMaxStages];
-    uint64_t s_full[2], p_ready[2], o_full[2], q_full, fin;
+    uint64_t s_full[2], p_ready[2], o_full[2], q_full, fin[2], turn[2];
     uint32_t tmem, dead;
+    int tiles;             // of the segment whose queries are ready
     uint32_t nf[8];        // drafts with infinities or NaNs among their values
     float2 ml[2][128];
 };
 static_assert(sizeof(Misc) <= kMisc, "");
 
 // Waits for a barrier's phase; gives up after a bounded time, or at once when
-// another warp has given up.
-__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, Misc *m, int32_t *status) {
+// another warp has given up. (Not inlined: the softmax loop's code should
+// stay small in the instruction cache.)
+__device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, Misc *m, int32_t *status) {
     volatile uint32_t *dead = &m->dead;
-    for (int i = 0; i < 64; ++i) {
-        if (*dead) return false;
-        if (tc05::mbar_wait(bar, parity, kPoll / 64)) return true;
+#pragma unroll 1
+    for (uint32_t i = 0; i < kPoll; ++i) {
+        if (try_wait(bar, parity)) return true;
+        if ((i & 255) == 255 && *dead) return false;
     }
     *dead = 1;
     set_status(status, kStTimeout);
     return false;
+}
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, Misc *m, int32_t *status) {
+    const uint32_t b = tc05::smem_addr(bar);
+    return try_wait(b, parity) || wait_slow(b, parity, m, status);
 }
 
 __device__ __forceinline__ void pair_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
@@ -80,14 +90,14 @@ __device__ __forceinline__ bool pair_or(bool p) {
 struct Segment {
     int j0, n;
     bool whole;
-    __device__ __forceinline__ Segment(const Cursor &c, long long u, long long u1) {
+    __device__ __forceinline__ Segment(const Cursor &c, int left) {
         j0 = c.u;
-        n = (int)min((long long)(c.nu - c.u), u1 - u);
+        n = min(c.nu - c.u, left);
         whole = j0 == 0 && n == c.nu;
     }
 };
 
-template <int D, bool kBf16, bool kSplit>
+template <int D, bool kBf16, bool kTwo, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     k_attn_tc(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
               const TreeArgs a, int stages) {
@@ -95,9 +105,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t kIdescS = tc05::idesc_f16kind_f32(kBf16, 128, kKeys, false);
     constexpr uint32_t kIdescO = tc05::idesc_f16kind_f32(kBf16, 128, D, true);
     extern __shared__ __align__(1024) uint8_t smem[];
-    const bool two = a.rows == 256;
-    const int lag = two ? 1 : 2;  // tiles a product P V runs behind its Q K^T
-    uint8_t *qs = smem, *ring = smem + (two ? 2 : 1) * kTile;
+    constexpr int lag = kTwo ? 1 : 2;  // tiles a product P V runs behind its Q K^T
+    uint8_t *qs = smem, *ring = smem + (kTwo ? 2 : 1) * kTile;
     Misc *m = reinterpret_cast<Misc *>(ring + stages * kTile);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -110,23 +119,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) set_status(a.status, kStLength);
         }
     }
-    const long long total = units_before<kThreads>(a, a.s.B, m->scan);
-    const long long quota = (total + a.grid - 1) / a.grid;
-    const long long u0 = quota * blockIdx.x;
-    const long long u1 = min(u0 + quota, total);
-    if (u0 >= u1) return;
+    const Share sh = find_share<kThreads>(a, &m->share);
+    if (sh.u0 >= sh.u1) return;
     if (threadIdx.x == 0) {
         for (int i = 0; i < stages; ++i) {
             tc05::mbar_init(m->full + i, 1);
-            tc05::mbar_init(m->empty + i, 1);
+            tc05::mbar_init(m->empty + i, kTwo ? 2 : 1);  // both streams read a tile, or one
         }
         for (int s = 0; s < 2; ++s) {
             tc05::mbar_init(m->s_full + s, 1);
             tc05::mbar_init(m->p_ready + s, 4);
             tc05::mbar_init(m->o_full + s, 1);
+            tc05::mbar_init(m->fin + s, 1);
+            tc05::mbar_init(m->turn + s, 4);
         }
         tc05::mbar_init(&m->q_full, 256);
-        tc05::mbar_init(&m->fin, 1);
         m->dead = 0;
         tc05::fence_mbar_init();
         prefetch_tmap(&kmap);
@@ -138,13 +145,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc05::fence_after_sync();
     const uint32_t tmem = m->tmem;
 
-    Cursor c;
-    c.seek(a, u0);
-    long long u = u0;
+    const int units = (int)(sh.u1 - sh.u0);  // (the launcher keeps this below 2^31)
 
+    // 168 x 384 registers at launch = 216 x 256 + 72 x 128
+    if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 8) {
         // ------------------------------------------------------------ copies
         const int prow = a.s.page < kKeys ? a.s.page : kKeys;  // rows a copy
+        Cursor c;
+        c.start(a, sh);
         int stage = 0, issued = 0;
         uint32_t phase = 1;  // a fresh barrier counts as passed for parity 1
         int pid = 0;
@@ -155,19 +165,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             lv = lane * prow < kKeys && slot < c.q.ctx + c.q.T;
             return lv ? __ldg(a.s.table + (long long)c.b * a.s.max_pages + (slot >> a.s.lpage)) : 0;
         };
-        while (u < u1) {
-            const Segment sg(c, u, u1);
+        for (int left = units; left > 0;) {
+            const Segment sg(c, left);
             // at step x: values of tile x - lag, then keys of tile x
             int vp[2] = {0, 0};       // pages of the last tiles' keys, for their values
             bool vl[2] = {false, false};
             int np = page_of(sg.j0, live);
             bool nl = live;
+#pragma unroll 1
             for (int x = 0; x < sg.n + lag; ++x) {
-#pragma unroll
+#pragma unroll 1
                 for (int kind = 0; kind < 2; ++kind) {  // 0: values, 1: keys
                     const int t = kind ? x : x - lag;
                     if (t < 0 || t >= sg.n) continue;
-                    const int sl = two ? 0 : t & 1;
+                    const int sl = kTwo ? 0 : t & 1;
                     if (kind) {
                         pid = np;
                         live = nl;
@@ -208,8 +219,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            u += sg.n;
-            if (u < u1) c.next_item(a);
+            left -= sg.n;
+            if (left > 0) c.next_item(a);
         }
         if (*(volatile uint32_t *)&m->dead) {
             // gave up: wait (bounded) for the copies in flight
@@ -218,143 +229,151 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc05::mbar_wait(m->full + n % stages, (n / stages) & 1, kPoll / 64);
             }
         }
-    } else if (warp == 9) {
+    } else if (warp <= 10) {
         // ------------------------------------------------------------ products
+        // a warp a stream, so that one's waits pass under the other's products
         if (lane == 0) {
-            int stage = 0;
-            uint32_t phase = 0, pp[2] = {0, 0}, qp = 0;
+            const int s = warp - 9;
+            const uint64_t kdesc = tc05::sdesc_sw128(tc05::smem_addr(ring));
+            const uint64_t vdesc = tc05::sdesc_sw128_mn(tc05::smem_addr(ring), kKeys * 128);
+            const uint64_t qdesc =
+                tc05::sdesc_sw128(tc05::smem_addr(qs)) + (uint32_t)((kTwo ? s : 0) * (kTile >> 4));
+            const uint32_t ts = tmem + s * 128, to = tmem + 256 + s * 128;
+            int stage = 0, at = 0;                 // ring slot, and its place in the segment's entries
+            uint32_t ring_ph = 0, pp = 0, qp = 0;
             bool live = true;
-            const uint32_t q0 = tc05::smem_addr(qs), r0 = tc05::smem_addr(ring);
-            while (u < u1 && live) {
-                const Segment sg(c, u, u1);
-                live = wait(&m->q_full, qp, m, a.status);
-                qp ^= 1;
-                tc05::fence_after_sync();
-                for (int x = 0; x < sg.n + lag && live; ++x) {
-                    int vstage = stage;
-                    uint32_t vphase = phase;
-                    const bool hasv = x >= lag, hask = x < sg.n;
-                    int kstage = stage;
-                    uint32_t kphase = phase;
-                    if (hasv && ++kstage == stages) {
-                        kstage = 0;
-                        kphase ^= 1;
-                    }
-                    for (int s = two ? 0 : x & 1; s < (two ? 2 : (x & 1) + 1) && live; ++s) {
-                        if (hasv) {
-                            live = wait(m->p_ready + s, pp[s], m, a.status) &&
-                                   wait(m->full + vstage, vphase, m, a.status);
-                            if (!live) break;
-                            pp[s] ^= 1;
-                            tc05::fence_after_sync();
-                            const uint32_t vb = r0 + vstage * kTile;
-                            const bool first = x - lag < (two ? 1 : 2);
-                            for (int part = 0; part < (kSplit ? 2 : 1); ++part)
-#pragma unroll
-                                for (int k = 0; k < kKeys / 16; ++k)
-                                    tc05::mma_ts(tmem + 256 + s * 128,
-                                                 tmem + s * 128 + part * 64 + k * 8,
-                                                 tc05::sdesc_sw128_mn(vb + k * 2048, kKeys * 128),
-                                                 kIdescO, !(first && part == 0 && k == 0));
-                            if (!two || s == 1) tc05::mma_commit(m->empty + vstage);
-                            if (two ? x == sg.n : x >= sg.n) tc05::mma_commit(m->o_full + s);
-                        }
-                        if (hask) {
-                            if (!(live = wait(m->full + kstage, kphase, m, a.status))) break;
-                            tc05::fence_after_sync();
-                            const uint32_t kb = r0 + kstage * kTile, qb = q0 + (two ? s : 0) * kTile;
-#pragma unroll
-                            for (int k = 0; k < D / 16; ++k) {
-                                const uint32_t of = (k >> 2) * (kKeys * 128) + (k & 3) * 32;
-                                tc05::mma_ss(tmem + s * 128, tc05::sdesc_sw128(qb + of),
-                                             tc05::sdesc_sw128(kb + of), kIdescS, k > 0);
-                            }
-                            tc05::mma_commit(m->s_full + s);
-                            if (!two || s == 1) tc05::mma_commit(m->empty + kstage);
-                        }
-                    }
-                    const int used = (int)hasv + (int)hask;
-                    for (int i = 0; i < used; ++i)
-                        if (++stage == stages) {
-                            stage = 0;
-                            phase ^= 1;
-                        }
+            auto go = [&](int pos) {  // to a later entry of the segment
+                stage += pos - at;
+                at = pos;
+                while (stage >= stages) {
+                    stage -= stages;
+                    ring_ph ^= 1u;
                 }
-                u += sg.n;
-                if (u < u1) c.next_item(a);
+            };
+            for (int left = units; left > 0 && live;) {
+                live = wait(&m->q_full, qp, m, a.status);
+                qp ^= 1u;
+                const int n = *(volatile int *)&m->tiles;
+                left -= n;
+                // S = Q K^T of tile t, then O (+)= P V of it while the softmax
+                // of the other stream runs, and S of the stream's next tile
+                constexpr int kStep = kTwo ? 1 : 2;
+                const int t0 = kTwo ? 0 : s;
+#pragma unroll 1
+                for (int t = t0; t < n + kStep && live; t += kStep) {
+                    if (t > t0) {
+                        const int tv = t - kStep;
+                        go(min(tv + lag, n) + tv);
+                        live = wait(m->full + stage, ring_ph, m, a.status) &&
+                               wait(m->p_ready + s, pp, m, a.status);
+                        if (!live) break;
+                        pp ^= 1u;
+                        tc05::fence_after_sync();
+                        const uint64_t v = vdesc + (uint32_t)(stage * (kTile >> 4));
+#pragma unroll
+                        for (int part = 0; part < (kSplit ? 2 : 1); ++part)
+#pragma unroll
+                            for (int k = 0; k < kKeys / 16; ++k)
+                                tc05::mma_ts(to, ts + part * 64 + k * 8, v + k * (2048 >> 4), kIdescO,
+                                             !(tv == t0 && part == 0 && k == 0));
+                        tc05::mma_commit(m->empty + stage);
+                        if (t >= n) {
+                            tc05::mma_commit(m->o_full + s);
+                            break;
+                        }
+                    } else if (t >= n) {
+                        break;  // no tile for this stream
+                    }
+                    go(t == 0 ? 0 : 2 * t + 1 - lag);
+                    live = wait(m->full + stage, ring_ph, m, a.status);
+                    if (!live) break;
+                    const uint64_t kd = kdesc + (uint32_t)(stage * (kTile >> 4));
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const int of = ((k >> 2) * (kKeys * 128) + (k & 3) * 32) >> 4;
+                        tc05::mma_ss(ts, qdesc + of, kd + of, kIdescS, k > 0);
+                    }
+                    tc05::mma_commit(m->s_full + s);
+                    tc05::mma_commit(m->empty + stage);
+                }
+                go(2 * n);
+                at = 0;
             }
             // nothing of this thread's is in flight when the block ends
-            tc05::mma_commit(&m->fin);
-            tc05::mbar_wait(&m->fin, 0, kPoll);
+            tc05::mma_commit(m->fin + s);
+            tc05::mbar_wait(m->fin + s, 0, kPoll);
         }
         __syncwarp();
-    } else if (warp < 8) {
+    }
+    } else {
         // ------------------------------------------------------------ softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int s = warp >> 2, tid = threadIdx.x & 127, wq = warp & 3;
         const uint32_t lanes = (uint32_t)(wq * 32) << 16;
         const uint32_t ts = tmem + lanes + s * 128, to = tmem + lanes + 256;
-        uint32_t sp = 0, op = 0;
-        long long ops = 0;  // ring entries before this segment
+        uint32_t sp = 0, op = 0, tp = 0;
+        Cursor c;
+        c.start(a, sh);
         const float boost = kBf16 ? 0.f : 7.f;
-        while (u < u1) {
-            const bool first_seg = u == u0;
-            const Segment sg(c, u, u1);
+        for (int left = units; left > 0;) {
+            const Segment sg(c, left);
             const Seq q = c.q;
             const int len = q.ctx + q.T, nrows = q.T * a.G;
             const int32_t *trow = a.s.table + (long long)c.b * a.s.max_pages;
-            const int ns = two ? sg.n : (sg.n + 1 - s) / 2;  // this stream's tiles
+            const int ns = kTwo ? sg.n : (sg.n + 1 - s) / 2;  // this stream's tiles
             // ---- queries to shared memory, rows in the products' order
             {
-                const int r = two ? tid : s * 64 + (tid >> 1);
-                const int rr = c.rb * a.rows + (two ? s * 128 : 0) + r;
-                const bool have = rr < nrows;
-                const int t = have ? rr / a.G : 0;
-                const uint4 *p = reinterpret_cast<const uint4 *>(
-                    a.q + (long long)(q.first + t) * a.q_stride +
-                    (long long)(c.h * a.G + (have ? rr - t * a.G : 0)) * D);
-                const int c0 = two ? 0 : (tid & 1) * (D / 16), cn = two ? D / 8 : D / 16;
-                uint8_t *dst = qs + (two ? s * kTile : 0) + r * 128;
-#pragma unroll 8
-                for (int i = 0; i < cn; ++i) {
-                    const int ch = c0 + i;
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (have) {
-                        v = __ldg(p + ch);
-                        v.x = (v.x ^ a.qxor) & a.qand;
-                        v.y = (v.y ^ a.qxor) & a.qand;
-                        v.z = (v.z ^ a.qxor) & a.qand;
-                        v.w = (v.w ^ a.qxor) & a.qand;
-                    }
-                    *reinterpret_cast<uint4 *>(dst + (ch >> 3) * (kKeys * 128) +
-                                               (((ch & 7) ^ (r & 7)) << 4)) = v;
+                constexpr int kChunks = D / 8, kPass = 128 / kChunks;  // rows a pass of this warpgroup
+                const int ch = tid % kChunks, rbase = c.rb * a.rows + (kTwo ? s * 128 : 0);
+                const int r0 = (kTwo ? 0 : s * 64) + tid / kChunks;
+                uint8_t *dst = qs + (kTwo ? s * kTile : 0) + (ch >> 3) * (kKeys * 128);
+                const uint16_t *p = a.q + (long long)q.first * a.q_stride + (long long)c.h * a.G * D + ch * 8;
+                constexpr int kLoads = (kTwo ? 128 : 64) / kPass;
+                uint4 v[kLoads];  // all under way before the first is needed
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i) {
+                    const int rr = min(rbase + r0 + i * kPass, nrows - 1), t = rr / a.G;
+                    v[i] = __ldg(reinterpret_cast<const uint4 *>(p + t * a.q_stride + (rr - t * a.G) * D));
+                }
+#pragma unroll
+                for (int i = 0; i < kLoads; ++i) {
+                    const int r = r0 + i * kPass;
+                    const uint32_t keep = rbase + r < nrows ? a.qand : 0u;
+                    *reinterpret_cast<uint4 *>(dst + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) =
+                        make_uint4((v[i].x ^ a.qxor) & keep, (v[i].y ^ a.qxor) & keep,
+                                   (v[i].z ^ a.qxor) & keep, (v[i].w ^ a.qxor) & keep);
                 }
             }
             tc05::fence_proxy_async();
+            if (threadIdx.x == 0) m->tiles = sg.n;
             mbar_arrive(&m->q_full);
             // ---- pages that do not exist, among this segment's
             bool bad = false;
             {
                 const int p1 = (min(len, (sg.j0 + sg.n) * kKeys) + a.s.page - 1) >> a.s.lpage;
+#pragma unroll 1
                 for (int p = ((sg.j0 * kKeys) >> a.s.lpage) + (threadIdx.x & 255); p < p1; p += 256)
                     bad |= (unsigned)trow[p] >= (unsigned)a.pages;
             }
             if (threadIdx.x < 8) m->nf[threadIdx.x] = 0;
             bad = pair_or(bad);
 
-            const int rbase = c.rb * a.rows + (two ? s * 128 : 0);
+            const int rbase = c.rb * a.rows + (kTwo ? s * 128 : 0);
             const int rr = rbase + tid;
             const bool row_live = rr < nrows, warp_live = rbase + wq * 32 < nrows;
             const int t = row_live ? rr / a.G : 0;
             float mx = -INFINITY, l = 0.f;  // mx: the maximum in use (log2 units)
+#pragma unroll 1
             for (int i = 0; i < ns; ++i) {
-                const int tile = two ? i : 2 * i + s, j = sg.j0 + tile;
+                const int tile = kTwo ? i : 2 * i + s, j = sg.j0 + tile;
                 const bool special = bad || (j + 1) * kKeys > q.ctx;
-                if (special && (!two || s == 0)) {
+                if (special && (!kTwo || s == 0)) {
                     // Values that some row must not see are kept out of the
                     // product where zero times them is not zero: a thread a
                     // key, zeros past the end and where there is no page, and
                     // a draft's infinities and NaNs noted and replaced.
-                    const long long pos = ops + min(tile + lag, sg.n) + tile;
+                    // (two ring entries a tile of the segments before)
+                    const long long pos = 2LL * (units - left) + min(tile + lag, sg.n) + tile;
                     const int vst = (int)(pos % stages);
                     if (wait(m->full + vst, (uint32_t)(pos / stages) & 1u, m, a.status)) {
                         const int key = j * kKeys + tid;
@@ -363,6 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             key >= len || (bad && (unsigned)trow[key >> a.s.lpage] >= (unsigned)a.pages);
                         if (none || key >= q.ctx) {
                             bool inf = false;
+#pragma unroll 4
                             for (int ch = 0; ch < D / 8; ++ch) {
                                 uint4 *w = reinterpret_cast<uint4 *>(
                                     row + (ch >> 3) * (kKeys * 128) + (((ch & 7) ^ (tid & 7)) << 4));
@@ -387,45 +407,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 sp ^= 1;
                 tc05::fence_after_sync();
+                // The streams take turns: left alone they fall into step, both
+                // at their exponentials and then both waiting for products.
+                // (Stream 0 goes first; a pass of the other's is due before
+                // each tile but its first.)
+                if (i > 0 || s > 0) {
+                    wait(m->turn + s, tp ^ (uint32_t)((s ? i : i - 1) & 1), m, a.status);
+                    __syncwarp();
+                }
                 if (warp_live) {
-                    // Two passes over the scores in tensor memory, 64 columns
-                    // at a time: the maximum, then the weights, which
-                    // overwrite scores already read.
-                    uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};
-                    if (special) {
+                    if (special) {  // scores that a row must not see become -inf
+                        uint32_t see[4];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
+                        for (int k = 0; k < 4; ++k)
                             see[k] = row_live ? seen_word(a, q, t, j * kKeys + k * 32) : 0u;
-                            for (int h = 0; bad && h < 2; ++h) {
-                                const int slot = j * kKeys + k * 32 + h * 16;
+                        if (bad) {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const int slot = j * kKeys + k * 16;
                                 if (slot < len && (unsigned)trow[slot >> a.s.lpage] >= (unsigned)a.pages)
-                                    see[k] &= h ? 0x0000FFFFu : 0xFFFF0000u;
+                                    see[k >> 1] &= k & 1 ? 0x0000FFFFu : 0xFFFF0000u;
                             }
                         }
-                    }
-                    float tm = -INFINITY;
+                        __syncwarp();
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t x[2][32];
-                        tc05::tmem_ld32(ts + h * 64, x[0]);
-                        tc05::tmem_ld32(ts + h * 64 + 32, x[1]);
-                        tc05::tmem_wait_ld();
-                        if (special) {
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t x[32];
+                            tc05::tmem_ld32(ts + k * 32, x);
+                            tc05::tmem_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 64; ++e)
-                                if ((see[2 * h + (e >> 5)] >> (e & 31)) & 1u)
-                                    tm = fmaxf(tm, __uint_as_float(x[e >> 5][e & 31]));
-                        } else {
-                            float v[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(x[0][e]);
-#pragma unroll
-                            for (int e = 4; e < 64; ++e)
-                                v[e & 3] = fmaxf(v[e & 3], __uint_as_float(x[e >> 5][e & 31]));
-                            tm = fmaxf(tm, fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])));
+                            for (int e = 0; e < 32; ++e)
+                                if (!((see[k] >> e) & 1u)) x[e] = 0xFF800000u;
+                            tc05::tmem_st32(ts + k * 32, x);
                         }
+                        tc05::tmem_wait_st();
                     }
-                    tm *= a.sl2;
+                    uint32_t x[4][32];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) tc05::tmem_ld32(ts + k * 32, x[k]);
+                    tc05::tmem_wait_ld();
+                    float v[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(x[0][e]);
+#pragma unroll
+                    for (int e = 4; e < 128; ++e)
+                        v[e & 3] = fmaxf(v[e & 3], __uint_as_float(x[e >> 5][e & 31]));
+                    const float tm = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])) * a.sl2;
                     const bool move = tm > mx + kLazy || (mx == -INFINITY && tm > mx);
                     if (__any_sync(0xFFFFFFFFu, move)) {
                         const float al = move ? ex2(mx - tm) : 1.f;
@@ -434,60 +461,49 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (i > 0) {
                             // all earlier products of this stream are done: they
                             // were issued before this tile's scores
-#pragma unroll
-                            for (int k = 0; k < D / 32; ++k) {
-                                uint32_t o[32];
-                                tc05::tmem_ld32(to + s * 128 + k * 32, o);
+#pragma unroll 1
+                            for (int k = 0; k < D / 16; ++k) {
+                                uint32_t o[16];
+                                tc05::tmem_ld16(to + s * 128 + k * 16, o);
                                 tc05::tmem_wait_ld();
 #pragma unroll
-                                for (int e = 0; e < 32; ++e)
+                                for (int e = 0; e < 16; ++e)
                                     o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
-                                tc05::tmem_st32(to + s * 128 + k * 32, o);
+                                tc05::tmem_st16(to + s * 128 + k * 16, o);
                             }
                         }
                     }
                     const float base = mx == -INFINITY ? 0.f : mx - boost;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-                    uint32_t lo0[32];  // the first half's rests wait for the second's scores
+                    // two elements an instruction: weight = 2^(s * sl2 - base)
+                    const uint64_t sl2 = pack_f32x2(a.sl2, a.sl2), nb = pack_f32x2(-base, -base);
+                    uint64_t sum[2] = {0, 0};
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t x[2][32], hi[32], lo[32];
-                        tc05::tmem_ld32(ts + h * 64, x[0]);
-                        tc05::tmem_ld32(ts + h * 64 + 32, x[1]);
-                        tc05::tmem_wait_ld();
+                    for (int h = 0; h < 4; ++h) {
+                        uint32_t hi[16], lo[16];
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            float s0 = __uint_as_float(x[(2 * e) >> 5][(2 * e) & 31]);
-                            float s1 = __uint_as_float(x[(2 * e) >> 5][(2 * e + 1) & 31]);
-                            if (special) {
-                                const uint32_t w = see[2 * h + (e >> 4)] >> ((2 * e) & 31);
-                                if (!(w & 1u)) s0 = -INFINITY;
-                                if (!(w & 2u)) s1 = -INFINITY;
-                            }
-                            const float p0 = ex2(fmaf(s0, a.sl2, -base));
-                            const float p1 = ex2(fmaf(s1, a.sl2, -base));
-                            sum[(2 * e) & 3] += p0;
-                            sum[(2 * e + 1) & 3] += p1;
+                        for (int e = 0; e < 16; ++e) {
+                            float p0, p1;
+                            unpack_f32x2(fma_f32x2(pack_u32x2(x[h][2 * e], x[h][2 * e + 1]), sl2, nb), p0, p1);
+                            p0 = ex2(p0);
+                            p1 = ex2(p1);
+                            sum[e & 1] = add_f32x2(sum[e & 1], pack_f32x2(p0, p1));
                             hi[e] = pack2<kBf16>(p0, p1);
                             if (kSplit) {
                                 const float2 f = unpack2<kBf16>(hi[e]);
                                 lo[e] = pack2<kBf16>(p0 - f.x, p1 - f.y);
                             }
                         }
-                        tc05::tmem_st32(ts + h * 32, hi);
-                        if (kSplit) {
-                            if (h == 0) {
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) lo0[e] = lo[e];
-                            } else {
-                                tc05::tmem_st32(ts + 64, lo0);
-                                tc05::tmem_st32(ts + 96, lo);
-                            }
-                        }
+                        tc05::tmem_st16(ts + h * 16, hi);
+                        if (kSplit) tc05::tmem_st16(ts + 64 + h * 16, lo);
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                    tc05::tmem_wait_st();
+                    float s0, s1, s2, s3;
+                    unpack_f32x2(sum[0], s0, s1);
+                    unpack_f32x2(sum[1], s2, s3);
+                    l += (s0 + s1) + (s2 + s3);
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(m->turn + (s ^ 1));
+                tc05::tmem_wait_st();
                 tc05::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(m->p_ready + s);
@@ -503,28 +519,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc05::fence_after_sync();
             if (warp_live) {
                 float M = mx, L = l, f0 = 1.f, f1 = 0.f;
-                if (!two) {
+                if (!kTwo) {
                     const float2 v0 = m->ml[0][tid], v1 = m->ml[1][tid];
                     M = fmaxf(v0.x, v1.x);
                     f0 = v0.x == -INFINITY ? 1.f : ex2(v0.x - M);
                     f1 = v1.x == -INFINITY ? 1.f : ex2(v1.x - M);
                     L = v0.y * f0 + v1.y * f1;
                 }
-                const bool has1 = !two && sg.n > 1;
+                const bool has1 = !kTwo && sg.n > 1;
                 const float inv = sg.whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
                 const long long row =
                     (long long)(q.first + t) * a.Hq + c.h * a.G + (row_live ? rr - t * a.G : 0);
-                const long long slot =
-                    ((long long)blockIdx.x * 2 + (first_seg ? 0 : 1)) * a.rows + (two ? s * 128 : 0) + tid;
+                const int seg_last = left == units ? 0 : 1, prow = (kTwo ? s * 128 : 0) + tid;
                 bool odd = false;  // drafts to add by hand
                 for (int w = 0; w < 8; ++w) odd |= m->nf[w] != 0;
-                const int k0 = two ? 0 : s * (D / 64), k1 = two ? D / 32 : k0 + D / 64;
+                const int k0 = kTwo ? 0 : s * (D / 64), k1 = kTwo ? D / 32 : k0 + D / 64;
+#pragma unroll 1
                 for (int k = k0; k < k1; ++k) {  // 32 columns at a time
                     float o[32];
-                    tc05::tmem_ld32(to + (two ? s * 128 : 0) + k * 32,
+                    tc05::tmem_ld32(to + (kTwo ? s * 128 : 0) + k * 32,
                                     *reinterpret_cast<uint32_t(*)[32]>(o));
                     tc05::tmem_wait_ld();
-                    if (!two) {
+                    if (!kTwo) {
                         float o1[32];
                         if (has1) {
                             tc05::tmem_ld32(to + 128 + k * 32, *reinterpret_cast<uint32_t(*)[32]>(o1));
@@ -534,6 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int e = 0; e < 32; ++e) o[e] = has1 ? o[e] * f0 + o1[e] * f1 : o[e] * f0;
                     }
                     if (odd && row_live) {
+#pragma unroll 1
                         for (int d = 0; d < q.T; ++d) {
                             if (!((m->nf[d >> 5] >> (d & 31)) & 1u) ||
                                 !(seen_word(a, q, t, q.ctx + d) & 1u))
@@ -552,10 +569,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (row_live) {
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] *= inv;
-                        if (!sg.whole || a.o_f32) {
-                            float4 *p = reinterpret_cast<float4 *>(
-                                sg.whole ? static_cast<float *>(a.o) + row * D + k * 32
-                                         : a.part_o + slot * D + k * 32);
+                        if (!sg.whole) {
+                            float *p = part_at<D>(a, blockIdx.x, seg_last, prow, k * 32);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                *reinterpret_cast<float4 *>(p + e * (a.rows * 4LL)) =
+                                    make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        } else if (a.o_f32) {
+                            float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(a.o) + row * D + k * 32);
 #pragma unroll
                             for (int e = 0; e < 8; ++e)
                                 p[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
@@ -570,18 +591,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                if (row_live && (two || s == 0)) {
+                if (row_live && (kTwo || s == 0)) {
                     if (sg.whole)
                         a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
                     else
-                        *reinterpret_cast<float2 *>(a.part_ml + slot * 2) = make_float2(M, L);
+                        *reinterpret_cast<float2 *>(a.part_ml + (((long long)blockIdx.x * 2 + seg_last) * a.rows + prow) * 2) =
+                            make_float2(M, L);
                 }
             }
             tc05::fence_before_sync();
             pair_sync();  // O, the queries and the tables may be overwritten
-            ops += 2LL * sg.n;
-            u += sg.n;
-            if (u < u1) c.next_item(a);
+            // the other stream passed the turn once a tile of its own
+            tp ^= (uint32_t)(kTwo ? sg.n : (sg.n + s) / 2) & 1u;
+            left -= sg.n;
+            if (left > 0) c.next_item(a);
         }
     }
     tc05::fence_before_sync();
@@ -596,7 +619,9 @@ cudaError_t run_tc(const CUtensorMap &km, const CUtensorMap &vm, const TreeArgs 
     const int q = (a.rows == 256 ? 2 : 1) * kTile;
     int stages = (kSmemMax - kMisc - q) / kTile;
     if (stages > kMaxStages) stages = kMaxStages;
-    auto *k = a.o_f32 ? k_attn_tc<D, kBf16, true> : k_attn_tc<D, kBf16, false>;
+    auto *k = a.rows == 256
+                  ? (a.o_f32 ? k_attn_tc<D, kBf16, true, true> : k_attn_tc<D, kBf16, true, false>)
+                  : (a.o_f32 ? k_attn_tc<D, kBf16, false, true> : k_attn_tc<D, kBf16, false, false>);
     cudaError_t e = set_smem(k, kSmemMax);
     if (e == cudaSuccess)
         e = launch(k, dim3(a.grid), dim3(kThreads), kSmemMax, st, true, km, vm, a, stages);

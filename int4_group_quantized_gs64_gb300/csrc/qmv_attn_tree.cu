@@ -54,7 +54,7 @@ struct RowsShape {
     static constexpr int kRing = NW * kStages * 2 * kSlice;
     static constexpr int kBuf = kRows * D * 4;
     static constexpr int kMl = NW * kRows * 8;
-    static constexpr int kSmem = kRing + kBuf + kMl + NW * kStages * 12 + 8 * NW + 16;
+    static constexpr int kSmem = kRing + kBuf + kMl + NW * kStages * 12 + 8 * NW + 32;
 };
 
 template <int D, int MT, int NW, bool kBf16>
@@ -69,8 +69,8 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? 2 : 1)
     extern __shared__ __align__(1024) uint8_t smem[];
     float *buf = reinterpret_cast<float *>(smem + S::kRing);
     float2 *ml = reinterpret_cast<float2 *>(smem + S::kRing + S::kBuf);
-    long long *scan = reinterpret_cast<long long *>(smem + S::kRing + S::kBuf + S::kMl);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(scan + NW);
+    auto *share = reinterpret_cast<ShareScratch<NW> *>(smem + S::kRing + S::kBuf + S::kMl);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(share + 1);
     int *flags = reinterpret_cast<int *>(bars + NW * kStages);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -94,14 +94,12 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? 2 : 1)
             if (!ok) set_status(a.status, kStLength);
         }
     }
-    const long long total = units_before<32 * NW>(a, a.s.B, scan);
-    const long long quota = (total + a.grid - 1) / a.grid;
-    const long long u0 = quota * blockIdx.x;
-    const long long u1 = min(u0 + quota, total);
+    const Share sh = find_share<32 * NW>(a, share);
+    const long long u0 = sh.u0, u1 = sh.u1;
     if (u0 >= u1) return;
 
     Cursor pc, cc;  // of the copies, of the products
-    cc.seek(a, u0);
+    cc.start(a, sh);
     pc = cc;
     long long pu = u0;  // next unit to copy
     int pstage = 0, pid = 0;
@@ -415,9 +413,11 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? 2 : 1)
                         pack2<kBf16>(v.x, v.y);
                 if (col == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
             } else {
-                const long long slot = ((long long)blockIdx.x * 2 + (first_seg ? 0 : 1)) * kRows + r;
-                *reinterpret_cast<float2 *>(a.part_o + slot * D + col) = v;
-                if (col == 0) *reinterpret_cast<float2 *>(a.part_ml + slot * 2) = make_float2(M, L);
+                const int last = first_seg ? 0 : 1;
+                *reinterpret_cast<float2 *>(part_at<D>(a, blockIdx.x, last, r, col & ~3) + (col & 3)) = v;
+                if (col == 0)
+                    *reinterpret_cast<float2 *>(
+                        a.part_ml + (((long long)blockIdx.x * 2 + last) * kRows + r) * 2) = make_float2(M, L);
             }
         }
         __syncthreads();
@@ -426,62 +426,85 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? 2 : 1)
 
 // ------------------------------------------------------------------ joining segments
 
-// One warp adds up the segments of one row of an item that several blocks
-// shared, in key order.
-template <int D>
+// Adds up the segments of an item that several blocks shared, in key order,
+// kXb blocks' segments at a time (their loads in flight together). A warp takes
+// 8 rows: lane l has row l % 8 and every fourth group of 4 columns, kCols of
+// them (the rest of a row's columns are other warps').
+template <int D, int kCols, int kXb>
 __global__ void __launch_bounds__(128) k_attn_join(const TreeArgs a, bool bf16) {
-    __shared__ long long scan[4];
+    constexpr int kParts = D / 16 / kCols;  // warps a row
+    __shared__ long long scan[8];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int b = blockIdx.x / a.Hkv, h = blockIdx.x - b * a.Hkv, rb = blockIdx.y;
-    const long long total = units_before<128>(a, a.s.B, scan);
-    const long long before = units_before<128>(a, b, scan);
     bool ok;
     const Seq q = get_seq(a.s, b, ok);
     const int nu = key_units(q, a.unit), nrb = row_blocks(q, a.G, a.rows);
+    long long before;
+    const long long total = count_units<128>(a, b, scan, before);
     if (q.T == 0 || rb >= nrb) return;
     const long long quota = (total + a.grid - 1) / a.grid;
     const long long i0 = before + ((long long)h * nrb + rb) * nu, i1 = i0 + nu;
     const int c0 = (int)(i0 / quota), c1 = (int)((i1 - 1) / quota);
     if (c0 == c1) return;  // one segment: written by its block
-    const int r = blockIdx.z * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const int rr = rb * a.rows + r;
-    if (r >= a.rows || rr >= q.T * a.G) return;
+    const int rows = min(a.rows, q.T * a.G - rb * a.rows);
+    const int w = blockIdx.z * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int r = (w / kParts) * 8 + (lane & 7), col0 = (w % kParts) * (kCols * 16) + (lane >> 3) * 4;
+    if ((w / kParts) * 8 >= rows) return;
+    const bool have_row = r < rows;
 
-    auto slot = [&](int cta) {
-        return ((long long)cta * 2 + ((long long)cta * quota >= i0 ? 0 : 1)) * a.rows + r;
-    };
-    float M = -INFINITY;
-    for (int x = c0 + lane; x <= c1; x += 32) M = fmaxf(M, a.part_ml[slot(x) * 2]);
+    float M = -INFINITY, L = 0.f, acc[kCols][4];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-    constexpr int V = D / 32;
-    float acc[V], L = 0.f;
+    for (int i = 0; i < kCols; ++i)
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = 0.f;
-#pragma unroll 4
-    for (int x = c0; x <= c1; ++x) {
-        const long long s = slot(x);
-        const float2 v = *reinterpret_cast<const float2 *>(a.part_ml + s * 2);
-        const float f = v.x == -INFINITY ? 1.f : ex2(v.x - M);
-        L += v.y * f;
+        for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
+    for (int x0 = c0; x0 <= c1; x0 += kXb) {
+        float2 ml[kXb];
+        float4 v[kXb][kCols];
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] += a.part_o[s * D + lane * V + i] * f;
+        for (int j = 0; j < kXb; ++j) {
+            const int x = x0 + j, last = (long long)x * quota >= i0 ? 0 : 1;
+            const bool have = x <= c1 && have_row;
+            ml[j] = have ? *reinterpret_cast<const float2 *>(
+                               a.part_ml + (((long long)x * 2 + last) * a.rows + r) * 2)
+                         : make_float2(-INFINITY, 0.f);
+#pragma unroll
+            for (int i = 0; i < kCols; ++i)
+                v[j][i] = have ? *reinterpret_cast<const float4 *>(part_at<D>(a, x, last, r, col0 + 16 * i))
+                               : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int j = 0; j < kXb; ++j) {
+            const float mn = fmaxf(M, ml[j].x);
+            const float f0 = M == mn ? 1.f : ex2(M - mn);
+            const float f1 = ml[j].x == mn ? 1.f : ex2(ml[j].x - mn);
+            M = mn;
+            L = L * f0 + ml[j].y * f1;
+#pragma unroll
+            for (int i = 0; i < kCols; ++i) {
+                acc[i][0] = acc[i][0] * f0 + v[j][i].x * f1;
+                acc[i][1] = acc[i][1] * f0 + v[j][i].y * f1;
+                acc[i][2] = acc[i][2] * f0 + v[j][i].z * f1;
+                acc[i][3] = acc[i][3] * f0 + v[j][i].w * f1;
+            }
+        }
     }
+    if (!have_row) return;
     const float inv = L == 0.f ? 0.f : 1.f / L;
-    const int t = rr / a.G;
+    const int rr = rb * a.rows + r, t = rr / a.G;
     const long long row = (long long)(q.first + t) * a.Hq + h * a.G + rr - t * a.G;
 #pragma unroll
-    for (int i = 0; i < V; i += 2) {
-        const float x0 = acc[i] * inv, x1 = acc[i + 1] * inv;
-        const long long at = row * D + lane * V + i;
+    for (int i = 0; i < kCols; ++i) {
+        const float x0 = acc[i][0] * inv, x1 = acc[i][1] * inv, x2 = acc[i][2] * inv, x3 = acc[i][3] * inv;
+        const long long at = row * D + col0 + 16 * i;
         if (a.o_f32)
-            *reinterpret_cast<float2 *>(static_cast<float *>(a.o) + at) = make_float2(x0, x1);
+            *reinterpret_cast<float4 *>(static_cast<float *>(a.o) + at) = make_float4(x0, x1, x2, x3);
         else
-            *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.o) + at) =
-                bf16 ? pack2<true>(x0, x1) : pack2<false>(x0, x1);
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.o) + at) =
+                bf16 ? make_uint2(pack2<true>(x0, x1), pack2<true>(x2, x3))
+                     : make_uint2(pack2<false>(x0, x1), pack2<false>(x2, x3));
     }
-    if (lane == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+    if (col0 == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
 // ------------------------------------------------------------------ attention weights
@@ -582,10 +605,14 @@ cudaError_t run_tree(const AttnCache &c, const CUtensorMap &km, const CUtensorMa
                     : a.rows == 32 ? run_rows<D, 2, 8, kBf16>(km, vm, a, st)
                                    : launch_tree_tc(c, a, st);
     const int nrb = (max_rows + a.rows - 1) / a.rows;
-    const int rz = ((max_rows < a.rows ? max_rows : a.rows) + 3) / 4;
+    // many rows: a warp 8 of them whole, two blocks' segments at a time; few
+    // rows (and so more blocks an item): a warp a quarter of 8 rows, eight
+    const bool many = a.rows > 32;
+    const int warps = ((max_rows < a.rows ? max_rows : a.rows) + 7) / 8 * (many ? 1 : D / 32);
+    const int rz = (warps + 3) / 4;
+    auto *join = many ? k_attn_join<D, D / 16, 2> : k_attn_join<D, 2, 8>;
     if (e == cudaSuccess)
-        e = launch(k_attn_join<D>, dim3(a.s.B * a.Hkv, nrb, rz), dim3(128), 0, st, true, a,
-                   (bool)kBf16);
+        e = launch(join, dim3(a.s.B * a.Hkv, nrb, rz), dim3(128), 0, st, true, a, (bool)kBf16);
     if (e == cudaSuccess && a.acc_out) {
         const unsigned tiles = (unsigned)((((long long)a.s.max_pages << a.s.lpage) + 63) / 64);
         e = launch(k_attn_weights<D, kBf16>, dim3(tiles, a.Hkv, a.s.B), dim3(128), 0, st, true, a);
