@@ -33,6 +33,8 @@ struct TreeArgs {
     const float *acc_in;
     float *acc_out;
     float decay;
+    float *stash;  // scores for the weights, [B][Hkv][16 keys][max_rows][16], or null
+    int max_rows;
     int32_t *status;
 };
 
@@ -182,6 +184,16 @@ __device__ __forceinline__ float *part_at(const TreeArgs &a, int block, int last
     return a.part_o +
            (((long long)block * 2 + last) * (D / 4) + (col >> 2)) * (a.rows * 4LL) + r * 4;
 }
+
+// The scores of 16 keys from `slot` (a multiple of 16): [max_rows][16].
+__device__ __forceinline__ float *stash_at(const TreeArgs &a, int b, int h, int slot) {
+    const long long slices = ((long long)a.s.max_pages << a.s.lpage) >> 4;
+    return a.stash + (((long long)b * a.Hkv + h) * slices + (slot >> 4)) * (a.max_rows * 16LL);
+}
+
+// The attention weights, once every row's lse is there (qmv_attn_weights.cu).
+cudaError_t launch_tree_weights(const AttnCache &c, const TreeArgs &a, int max_rows,
+                                cudaStream_t st);
 
 // Launches the tcgen05 kernel (qmv_attn_tc.cu) for a.rows = 128 or 256.
 cudaError_t launch_tree_tc(const AttnCache &c, const TreeArgs &a, cudaStream_t st);

@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? 2 : 1)
     while (u < u1) {
         // ---- one segment
         const bool at_start = cc.u == 0, first_seg = u == u0;
-        const int seg_h = cc.h, seg_rb = cc.rb;
+        const int seg_b = cc.b, seg_h = cc.h, seg_rb = cc.rb;
         const Seq sq = cc.q;
         const int nrows = sq.T * a.G;
         uint32_t qf[MT][KK][4];
@@ -282,6 +282,17 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? 2 : 1)
                     // the next copy into this slot comes from the async proxy
                     tc05::fence_proxy_async();
                     __syncwarp();
+                }
+                if (a.stash) {  // the masked scores, for the weights' own pass
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            if (rt[m][e] >= 0) {
+                                float *p = stash_at(a, seg_b, seg_h, s0) + (m * 16 + e * 8 + g) * 16 + c * 2;
+                                *reinterpret_cast<float2 *>(p) = make_float2(s[m][0][2 * e], s[m][0][2 * e + 1]);
+                                *reinterpret_cast<float2 *>(p + 8) = make_float2(s[m][1][2 * e], s[m][1][2 * e + 1]);
+                            }
                 }
                 uint32_t ph[MT][4], pl[MT][4];
 #pragma unroll
@@ -507,85 +518,6 @@ __global__ void __launch_bounds__(128) k_attn_join(const TreeArgs a, bool bf16) 
     if (col0 == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
-// ------------------------------------------------------------------ attention weights
-
-// acc_out[slot] = decay * acc_in[slot] + sum over the head's rows of
-// exp(x - lse): a second product of queries and keys, now that every row's
-// lse is known. A warp takes 16 keys and walks the rows 16 at a time.
-template <int D, bool kBf16>
-__global__ void __launch_bounds__(128) k_attn_weights(const TreeArgs a) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int b = blockIdx.z, h = blockIdx.y;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    bool ok;
-    const Seq q = get_seq(a.s, b, ok);
-    const int len = q.ctx + q.T, s0 = blockIdx.x * 64 + warp * 16;
-    if (q.T == 0 || s0 >= len) return;
-    const int pid = a.s.table[(long long)b * a.s.max_pages + (s0 >> a.s.lpage)];
-    if ((unsigned)pid >= (unsigned)a.pages) return;
-    const long long prow = ((long long)pid * a.Hkv + h) * a.s.page + (s0 & (a.s.page - 1));
-    constexpr int KK = D / 16;
-    uint32_t kb[2][KK][2];
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int k = 0; k < KK; ++k) {
-            const uint32_t *p = reinterpret_cast<const uint32_t *>(
-                a.kpool + (prow + n * 8 + g) * D + k * 16 + c * 2);
-            kb[n][k][0] = p[0];
-            kb[n][k][1] = p[4];
-        }
-    float w[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
-    const int nrows = q.T * a.G;
-    for (int r0 = 0; r0 < nrows; r0 += 16) {
-        uint32_t qf[KK][4];
-        int rt[2];
-        float e2[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int r = r0 + e * 8 + g;
-            const bool have = r < nrows;
-            const int t = have ? r / a.G : 0;
-            const int head = h * a.G + (have ? r - t * a.G : 0);
-            rt[e] = t;
-            e2[e] = have ? a.lse[(long long)(q.first + t) * a.Hq + head] * kLog2e : -INFINITY;
-            const uint16_t *p = a.q + (long long)(q.first + t) * a.q_stride + (long long)head * D;
-#pragma unroll
-            for (int k = 0; k < KK; ++k) {
-                const uint32_t *x = reinterpret_cast<const uint32_t *>(p + k * 16 + c * 2);
-                qf[k][e] = (x[0] ^ a.qxor) & a.qand;
-                qf[k][e + 2] = (x[4] ^ a.qxor) & a.qand;
-            }
-        }
-        const uint32_t see[2] = {seen_word(a, q, rt[0], s0), seen_word(a, q, rt[1], s0)};
-        float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-#pragma unroll
-        for (int k = 0; k < KK; ++k) {
-            mma16816<kBf16>(s[0], qf[k], kb[0][k][0], kb[0][k][1]);
-            mma16816<kBf16>(s[1], qf[k], kb[1][k][0], kb[1][k][1]);
-        }
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int j = n * 8 + c * 2 + (i & 1);
-                if (e2[i >> 1] != -INFINITY && ((see[i >> 1] >> j) & 1u)) w[n][i & 1] += ex2(fmaf(s[n][i], a.sl2, -e2[i >> 1]));
-            }
-    }
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) w[n][i] += __shfl_xor_sync(0xFFFFFFFFu, w[n][i], o);
-            const int j = n * 8 + c * 2 + i;
-            if (g == 0 && s0 + j < len) {
-                const float old = a.acc_in ? a.acc_in[prow + j] : 0.f;
-                a.acc_out[prow + j] = a.decay * old + w[n][i];
-            }
-        }
-}
-
 // ------------------------------------------------------------------ host
 
 template <int D, int MT, int NW, bool kBf16>
@@ -613,10 +545,7 @@ cudaError_t run_tree(const AttnCache &c, const CUtensorMap &km, const CUtensorMa
     auto *join = many ? k_attn_join<D, D / 16, 2> : k_attn_join<D, 2, 8>;
     if (e == cudaSuccess)
         e = launch(join, dim3(a.s.B * a.Hkv, nrb, rz), dim3(128), 0, st, true, a, (bool)kBf16);
-    if (e == cudaSuccess && a.acc_out) {
-        const unsigned tiles = (unsigned)((((long long)a.s.max_pages << a.s.lpage) + 63) / 64);
-        e = launch(k_attn_weights<D, kBf16>, dim3(tiles, a.Hkv, a.s.B), dim3(128), 0, st, true, a);
-    }
+    if (e == cudaSuccess && a.acc_out) e = launch_tree_weights(c, a, max_rows, st);
     return e;
 }
 
@@ -629,12 +558,34 @@ int tree_grid_max(int rows) { return sm_count() * (rows == 16 ? 2 : 1); }
 }  // namespace
 }  // namespace attn
 
+namespace attn {
+namespace {
+
+// Where the weights come from with up to 32 rows: scores that the attention
+// leaves in the workspace, or a second product of queries and keys. A score
+// costs 4 bytes written and 4 read a row, a key's second reading 2 D bytes; the
+// workspace is kept within kStashMax.
+constexpr size_t kStashMax = (size_t)1 << 30;
+size_t stash_bytes(const AttnCache &c, int max_rows, int B, int max_pages) {
+    if (max_rows > 32) return 0;
+    const size_t n = (size_t)B * c.Hkv * max_pages * c.page * max_rows * 4;
+    return n <= kStashMax ? n : 0;
+}
+
+size_t part_bytes(const AttnCache &c, int rows) {
+    const size_t slots = (size_t)tree_grid_max(rows) * 2 * rows;
+    return (slots * (c.D + 2) * 4 + 255) / 256 * 256;
+}
+
+}  // namespace
+}  // namespace attn
+
 size_t attn_tree_ws_bytes(const AttnCache &c, int Hq, int B, int N, int max_draft, int max_pages,
                           bool acc) {
-    (void)B; (void)N; (void)max_pages; (void)acc;
-    const int rows = attn::tree_rows(max_draft * (Hq / c.Hkv));
-    const size_t slots = (size_t)attn::tree_grid_max(rows) * 2 * rows;
-    return (slots * (c.D + 2) * 4 + 255) / 256 * 256;
+    (void)N;
+    const int max_rows = max_draft * (Hq / c.Hkv);
+    return attn::part_bytes(c, attn::tree_rows(max_rows)) +
+           (acc ? attn::stash_bytes(c, max_rows, B, max_pages) : 0);
 }
 
 cudaError_t launch_attn_tree(const AttnCache &c, const TreeCall &t, cudaStream_t st) {
@@ -665,6 +616,9 @@ cudaError_t launch_attn_tree(const AttnCache &c, const TreeCall &t, cudaStream_t
     a.grid = most < gmax ? (int)most : gmax;
     a.part_o = static_cast<float *>(t.ws);
     a.part_ml = a.part_o + (size_t)gmax * 2 * a.rows * c.D;
+    a.max_rows = max_rows;
+    if (a.acc_out && stash_bytes(c, max_rows, t.s.B, t.s.max_pages))
+        a.stash = reinterpret_cast<float *>(static_cast<char *>(t.ws) + part_bytes(c, a.rows));
     CUtensorMap km, vm;
     const long long rows = (long long)c.pages * c.Hkv * c.page;
     if (!encode_rows_swizzled(&km, static_cast<const uint8_t *>(c.k), rows, c.D * 2, 16) ||

@@ -1,0 +1,450 @@
+// qmv_attn_weights.cu - the attention weights of the cached tokens:
+//     acc_out[j] = decay * acc_in[j] + sum over the rows of a head of exp(x_j - lse)
+//
+// A weight needs its row's lse, and so the whole pass over the keys before it.
+// What the pass can leave behind, or what has to be done again, depends on
+// the rows R of a key/value head:
+//   few rows      k_attn_rows leaves its scores (8 R bytes a key, written and
+//                 read); k_weights_stash turns them into weights, a thread a key.
+//   33 .. 512     k_weights_tc forms the scores again (2 D bytes a key), keys as
+//                 the rows of the tcgen05 product, so that a thread has one key
+//                 and sums its own columns: S^T = K Q^T, all R queries resident
+//                 in shared memory while the keys stream by once. Tiles with
+//                 drafts in them are left to k_weights_any.
+//   otherwise     k_weights_any, on the warp MMA: any rows, any masks.
+#include <string.h>
+
+#include "qmv_attn.cuh"
+#include "qmv_attn.h"
+#include "qmv_attn_plan.cuh"
+#include "qmv_internal.h"
+#include "qmv_launch.cuh"
+
+namespace qmv {
+namespace attn {
+namespace {
+
+// ------------------------------------------------------------------ from kept scores
+
+__global__ void __launch_bounds__(256) k_weights_stash(const TreeArgs a) {
+    __shared__ float e2[32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int b = blockIdx.z, h = blockIdx.y, slot = blockIdx.x * 256 + threadIdx.x;
+    bool ok;
+    const Seq q = get_seq(a.s, b, ok);
+    const int len = q.ctx + q.T, nrows = q.T * a.G;
+    if (q.T == 0 || blockIdx.x * 256 >= len) return;
+    if (threadIdx.x < nrows) {
+        const int t = threadIdx.x / a.G;
+        e2[threadIdx.x] =
+            a.lse[(long long)(q.first + t) * a.Hq + h * a.G + threadIdx.x - t * a.G] * kLog2e;
+    }
+    __syncthreads();
+    if (slot >= len) return;
+    const int pid = a.s.table[(long long)b * a.s.max_pages + (slot >> a.s.lpage)];
+    if ((unsigned)pid >= (unsigned)a.pages) return;
+    const long long at = ((long long)pid * a.Hkv + h) * a.s.page + (slot & (a.s.page - 1));
+    const float old = a.acc_in ? a.decay * a.acc_in[at] : 0.f;
+    const float *p = stash_at(a, b, h, slot & ~15) + (slot & 15);
+    float w = 0.f;
+    for (int r0 = 0; r0 < nrows; r0 += 8) {
+        float x[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) x[r] = r0 + r < nrows ? __ldcs(p + (r0 + r) * 16) : 0.f;
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+            if (r0 + r < nrows && e2[r0 + r] != -INFINITY)
+                w += ex2(fmaf(x[r], a.sl2, -e2[r0 + r]));
+    }
+    a.acc_out[at] = old + w;
+}
+
+// ------------------------------------------------------------------ any rows, any masks
+
+// Eight warps share 16 keys: each walks every eighth block of 16 rows, and
+// their sums meet in shared memory. from_drafts: only the slots from the last
+// multiple of 128 at or before ctx on.
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(256) k_weights_any(const TreeArgs a, bool from_drafts) {
+    __shared__ float sums[8][16];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int b = blockIdx.z, h = blockIdx.y;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    bool ok;
+    const Seq q = get_seq(a.s, b, ok);
+    const int len = q.ctx + q.T, s0 = (from_drafts ? q.ctx & ~127 : 0) + blockIdx.x * 16;
+    if (q.T == 0 || s0 >= len) return;
+    const int pid = a.s.table[(long long)b * a.s.max_pages + (s0 >> a.s.lpage)];
+    if ((unsigned)pid >= (unsigned)a.pages) return;
+    const long long prow = ((long long)pid * a.Hkv + h) * a.s.page + (s0 & (a.s.page - 1));
+    constexpr int KK = D / 16;
+    uint32_t kb[2][KK][2];
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int k = 0; k < KK; ++k) {
+            const uint32_t *p = reinterpret_cast<const uint32_t *>(
+                a.kpool + (prow + n * 8 + g) * D + k * 16 + c * 2);
+            kb[n][k][0] = p[0];
+            kb[n][k][1] = p[4];
+        }
+    float w[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+    const int nrows = q.T * a.G;
+    for (int r0 = warp * 16; r0 < nrows; r0 += 128) {
+        uint32_t qf[KK][4];
+        int rt[2];
+        float e2[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = r0 + e * 8 + g;
+            const bool have = r < nrows;
+            const int t = have ? r / a.G : 0;
+            const int head = h * a.G + (have ? r - t * a.G : 0);
+            rt[e] = t;
+            e2[e] = have ? a.lse[(long long)(q.first + t) * a.Hq + head] * kLog2e : -INFINITY;
+            const uint16_t *p = a.q + (long long)(q.first + t) * a.q_stride + (long long)head * D;
+#pragma unroll
+            for (int k = 0; k < KK; ++k) {
+                const uint32_t *x = reinterpret_cast<const uint32_t *>(p + k * 16 + c * 2);
+                qf[k][e] = (x[0] ^ a.qxor) & a.qand;
+                qf[k][e + 2] = (x[4] ^ a.qxor) & a.qand;
+            }
+        }
+        const uint32_t see[2] = {seen_word(a, q, rt[0], s0), seen_word(a, q, rt[1], s0)};
+        float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+        for (int k = 0; k < KK; ++k) {
+            mma16816<kBf16>(s[0], qf[k], kb[0][k][0], kb[0][k][1]);
+            mma16816<kBf16>(s[1], qf[k], kb[1][k][0], kb[1][k][1]);
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int j = n * 8 + c * 2 + (i & 1);
+                if (e2[i >> 1] != -INFINITY && ((see[i >> 1] >> j) & 1u))
+                    w[n][i & 1] += ex2(fmaf(s[n][i], a.sl2, -e2[i >> 1]));
+            }
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) w[n][i] += __shfl_xor_sync(0xFFFFFFFFu, w[n][i], o);
+            if (g == 0) sums[warp][n * 8 + c * 2 + i] = w[n][i];
+        }
+    __syncthreads();
+    if (threadIdx.x < 16 && s0 + threadIdx.x < len) {
+        float x = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x += sums[k][threadIdx.x];
+        const long long at = prow + threadIdx.x;
+        a.acc_out[at] = (a.acc_in ? a.decay * a.acc_in[at] : 0.f) + x;
+    }
+}
+
+// ------------------------------------------------------------------ many rows, tcgen05
+
+constexpr int kThreads = 320, kKeys = 128, kStages = 12, kSmemMax = 227 * 1024, kMaxRows = 512;
+
+struct Misc {
+    ShareScratch<kThreads / 32> share;
+    uint64_t full[kStages], empty[kStages], s_full[4], s_free[4], q_full, fin;
+    uint32_t tmem, dead;
+    int tiles, row_tiles;
+    float nlse[kMaxRows];  // -lse in log2 units; -inf where a row has no weights
+};
+constexpr int kMisc = 3072;
+static_assert(sizeof(Misc) <= kMisc, "");
+
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, Misc *m, int32_t *status) {
+    const uint32_t b = tc05::smem_addr(bar);
+    volatile uint32_t *dead = &m->dead;
+#pragma unroll 1
+    for (uint32_t i = 0; i < kPoll; ++i) {
+        if (try_wait(b, parity)) return true;
+        if ((i & 255) == 255 && *dead) return false;
+    }
+    *dead = 1;
+    set_status(status, kStTimeout);
+    return false;
+}
+
+// a.rows is so large that an item is a (sequence, head), and a.unit 128 keys.
+// Warps 0-3 and 4-7 take alternate key tiles, 8 copies them, 9 issues the
+// products of a tile with every 128 queries into four score tiles of tensor
+// memory in turn.
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_weights_tc(const __grid_constant__ CUtensorMap kmap, const TreeArgs a, int q_tiles, int stages) {
+    constexpr int kTile = kKeys * D * 2, kHalves = D / 64;
+    constexpr uint32_t kIdesc = tc05::idesc_f16kind_f32(kBf16, 128, 128, false);
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t *qs = smem, *ring = smem + q_tiles * kTile;
+    Misc *m = reinterpret_cast<Misc *>(ring + stages * kTile);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const Share sh = find_share<kThreads>(a, &m->share);
+    if (sh.u0 >= sh.u1) return;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < stages; ++i) {
+            tc05::mbar_init(m->full + i, 1);
+            tc05::mbar_init(m->empty + i, 1);
+        }
+        for (int i = 0; i < 4; ++i) {
+            tc05::mbar_init(m->s_full + i, 1);
+            tc05::mbar_init(m->s_free + i, 4);
+        }
+        tc05::mbar_init(&m->q_full, 256);
+        tc05::mbar_init(&m->fin, 1);
+        m->dead = 0;
+        tc05::fence_mbar_init();
+        prefetch_tmap(&kmap);
+    }
+    if (warp == 9) tc05::tmem_alloc(&m->tmem, 512);
+    tc05::fence_before_sync();
+    __syncthreads();
+    tc05::fence_after_sync();
+    const uint32_t tmem = m->tmem;
+    const int units = (int)(sh.u1 - sh.u0);
+
+    if (warp == 8) {
+        const int prow = a.s.page < kKeys ? a.s.page : kKeys;
+        Cursor c;
+        c.start(a, sh);
+        int stage = 0, issued = 0;
+        uint32_t phase = 1;
+        for (int left = units; left > 0; --left) {
+            const int slot = c.u * kKeys + lane * prow;
+            const bool live = lane * prow < kKeys && slot < c.q.ctx + c.q.T;
+            const int pid =
+                live ? __ldg(a.s.table + (long long)c.b * a.s.max_pages + (slot >> a.s.lpage)) : -1;
+            const bool good = live && (unsigned)pid < (unsigned)a.pages;
+            const uint32_t n = __popc(__ballot_sync(0xFFFFFFFFu, good));
+            const bool ok = wait(m->empty + stage, phase, m, a.status);
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            if (lane == 0) {
+                if (n)
+                    mbar_expect_tx(m->full + stage, n * prow * D * 2);
+                else
+                    mbar_arrive(m->full + stage);
+            }
+            __syncwarp();
+            if (good) {
+                const int row = (pid * a.Hkv + c.h) * a.s.page + (slot & (a.s.page - 1));
+                const uint32_t dst = tc05::smem_addr(ring) + stage * kTile + lane * prow * 128;
+#pragma unroll
+                for (int hf = 0; hf < kHalves; ++hf)
+                    tma_load3(dst + hf * (kKeys * 128), &kmap, 0, row, hf, m->full + stage);
+            }
+            ++issued;
+            if (++stage == stages) {
+                stage = 0;
+                phase ^= 1;
+            }
+            if (++c.u == c.nu && left > 1) c.next_item(a);
+        }
+        if (*(volatile uint32_t *)&m->dead) {
+            for (int i = 1; i <= stages && i <= issued; ++i) {
+                const int n = issued - i;
+                tc05::mbar_wait(m->full + n % stages, (n / stages) & 1, kPoll / 64);
+            }
+        }
+    } else if (warp == 9) {
+        if (lane == 0) {
+            const uint64_t kdesc = tc05::sdesc_sw128(tc05::smem_addr(ring));
+            const uint64_t qdesc = tc05::sdesc_sw128(tc05::smem_addr(qs));
+            int stage = 0, job = 0;
+            uint32_t phase = 0, qp = 0;
+            bool live = true;
+            for (int left = units; left > 0 && live;) {
+                live = wait(&m->q_full, qp, m, a.status);
+                qp ^= 1u;
+                const int n = *(volatile int *)&m->tiles, nq = *(volatile int *)&m->row_tiles;
+                left -= n;
+#pragma unroll 1
+                for (int t = 0; t < n && live; ++t) {
+                    live = wait(m->full + stage, phase, m, a.status);
+                    const uint64_t kd = kdesc + (uint32_t)(stage * (kTile >> 4));
+#pragma unroll 1
+                    for (int r = 0; r < nq && live; ++r, ++job) {
+                        const int buf = job & 3;
+                        if (job >= 4)
+                            live = wait(m->s_free + buf, ((job >> 2) - 1) & 1, m, a.status);
+                        if (!live) break;
+                        tc05::fence_after_sync();
+                        const uint64_t qd = qdesc + (uint32_t)(r * (kTile >> 4));
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k) {
+                            const int of = ((k >> 2) * (kKeys * 128) + (k & 3) * 32) >> 4;
+                            tc05::mma_ss(tmem + buf * 128, kd + of, qd + of, kIdesc, k > 0);
+                        }
+                        tc05::mma_commit(m->s_full + buf);
+                    }
+                    tc05::mma_commit(m->empty + stage);
+                    if (++stage == stages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            tc05::mma_commit(&m->fin);
+            tc05::mbar_wait(&m->fin, 0, kPoll);
+        }
+        __syncwarp();
+    } else {
+        const int s = warp >> 2, tid = threadIdx.x & 127;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        Cursor c;
+        c.start(a, sh);
+        int job0 = 0;
+        const uint64_t sl2 = pack_f32x2(a.sl2, a.sl2);
+        for (int left = units; left > 0;) {
+            const Seq q = c.q;
+            const int j0 = c.u, n = min(c.nu - c.u, left), nrows = q.T * a.G;
+            const int nq = (nrows + 127) / 128;
+            // queries, and -lse of each
+            constexpr int kChunks = D / 8, kPass = 256 / kChunks;
+            const int ch = threadIdx.x % kChunks;
+            const uint16_t *p = a.q + (long long)q.first * a.q_stride + (long long)c.h * a.G * D + ch * 8;
+            uint8_t *dst = qs + (ch >> 3) * (kKeys * 128);
+#pragma unroll 1
+            for (int rt = 0; rt < nq; ++rt) {
+                uint4 v[128 / kPass];
+#pragma unroll
+                for (int i = 0; i < 128 / kPass; ++i) {
+                    const int rr = min(rt * 128 + (int)threadIdx.x / kChunks + i * kPass, nrows - 1);
+                    const int t = rr / a.G;
+                    v[i] = __ldg(reinterpret_cast<const uint4 *>(p + t * a.q_stride + (rr - t * a.G) * D));
+                }
+#pragma unroll
+                for (int i = 0; i < 128 / kPass; ++i) {
+                    const int r = threadIdx.x / kChunks + i * kPass;
+                    const uint32_t keep = rt * 128 + r < nrows ? a.qand : 0u;
+                    *reinterpret_cast<uint4 *>(dst + rt * kTile + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) =
+                        make_uint4((v[i].x ^ a.qxor) & keep, (v[i].y ^ a.qxor) & keep,
+                                   (v[i].z ^ a.qxor) & keep, (v[i].w ^ a.qxor) & keep);
+                }
+            }
+            for (int r = threadIdx.x; r < nq * 128; r += 256) {
+                float e = -INFINITY;
+                if (r < nrows) {
+                    const int t = r / a.G;
+                    e = -a.lse[(long long)(q.first + t) * a.Hq + c.h * a.G + r - t * a.G] * kLog2e;
+                    if (e == INFINITY) e = -INFINITY;
+                }
+                m->nlse[r] = e;
+            }
+            tc05::fence_proxy_async();
+            if (threadIdx.x == 0) {
+                m->tiles = n;
+                m->row_tiles = nq;
+            }
+            mbar_arrive(&m->q_full);
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+#pragma unroll 1
+            for (int t = s; t < n; t += 2) {
+                const int slot = (j0 + t) * kKeys + tid;
+                // tiles with drafts are another kernel's
+                const bool mine = (j0 + t + 1) * kKeys <= q.ctx;
+                int pid = -1;
+                if (mine) pid = __ldg(a.s.table + (long long)c.b * a.s.max_pages + (slot >> a.s.lpage));
+                const bool good = (unsigned)pid < (unsigned)a.pages;
+                const long long at = ((long long)pid * a.Hkv + c.h) * a.s.page + (slot & (a.s.page - 1));
+                const float old = good && a.acc_in ? a.decay * a.acc_in[at] : 0.f;
+                uint64_t sum[2] = {0, 0};
+#pragma unroll 1
+                for (int r = 0; r < nq; ++r) {
+                    const int job = job0 + t * nq + r, buf = job & 3;
+                    wait(m->s_full + buf, (job >> 2) & 1, m, a.status);
+                    __syncwarp();
+                    tc05::fence_after_sync();
+                    uint32_t x[2][32];
+                    tc05::tmem_ld32(tmem + lanes + buf * 128, x[0]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        tc05::tmem_wait_ld();
+                        if (k < 3) tc05::tmem_ld32(tmem + lanes + buf * 128 + (k + 1) * 32, x[(k + 1) & 1]);
+                        if (!mine) continue;
+                        const ulonglong2 *nl = reinterpret_cast<const ulonglong2 *>(m->nlse + r * 128 + k * 32);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const ulonglong2 nb = nl[e];
+                            float p0, p1, p2, p3;
+                            unpack_f32x2(fma_f32x2(pack_u32x2(x[k & 1][4 * e], x[k & 1][4 * e + 1]), sl2, nb.x), p0, p1);
+                            unpack_f32x2(fma_f32x2(pack_u32x2(x[k & 1][4 * e + 2], x[k & 1][4 * e + 3]), sl2, nb.y), p2, p3);
+                            sum[0] = add_f32x2(sum[0], pack_f32x2(ex2(p0), ex2(p1)));
+                            sum[1] = add_f32x2(sum[1], pack_f32x2(ex2(p2), ex2(p3)));
+                        }
+                    }
+                    tc05::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(m->s_free + buf);
+                }
+                if (good) {
+                    float s0, s1, s2, s3;
+                    unpack_f32x2(sum[0], s0, s1);
+                    unpack_f32x2(sum[1], s2, s3);
+                    a.acc_out[at] = old + ((s0 + s1) + (s2 + s3));
+                }
+            }
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            job0 += n * nq;
+            left -= n;
+            if (left > 0) c.next_item(a);
+        }
+    }
+    tc05::fence_before_sync();
+    __syncthreads();
+    tc05::fence_after_sync();
+    if (warp == 9) tc05::tmem_dealloc(tmem, 512);
+}
+
+template <int D, bool kBf16>
+cudaError_t run(const AttnCache &c, const TreeArgs &a, int max_rows, cudaStream_t st) {
+    const long long most = (long long)a.s.max_pages << a.s.lpage;
+    if (a.stash)
+        return launch(k_weights_stash, dim3((unsigned)((most + 255) / 256), a.Hkv, a.s.B), dim3(256), 0,
+                      st, true, a);
+    if (max_rows <= 32 || max_rows > kMaxRows)
+        return launch(k_weights_any<D, kBf16>, dim3((unsigned)((most + 15) / 16), a.Hkv, a.s.B),
+                      dim3(256), 0, st, true, a, false);
+    constexpr int kTile = kKeys * D * 2;
+    TreeArgs w = a;
+    w.rows = 1 << 30;
+    w.unit = kKeys;
+    const long long units = (long long)a.s.B * a.Hkv * ((most + kKeys - 1) / kKeys);
+    w.grid = units < sm_count() ? (int)units : sm_count();
+    const int q_tiles = (max_rows + 127) / 128;
+    int stages = (kSmemMax - kMisc - q_tiles * kTile) / kTile;
+    if (stages > kStages) stages = kStages;
+    CUtensorMap km;
+    if (!encode_rows_swizzled(&km, static_cast<const uint8_t *>(c.k), (long long)c.pages * c.Hkv * c.page,
+                              D * 2, c.page < kKeys ? c.page : kKeys, 1))
+        return cudaErrorNotSupported;
+    auto *k = k_weights_tc<D, kBf16>;
+    cudaError_t e = set_smem(k, kSmemMax);
+    if (e == cudaSuccess)
+        e = launch(k, dim3(w.grid), dim3(kThreads), kSmemMax, st, true, km, w, q_tiles, stages);
+    // slots ctx - ctx % 128 .. ctx + T - 1 of each sequence
+    const int tail = (127 + a.s.max_draft + 15) / 16;
+    if (e == cudaSuccess)
+        e = launch(k_weights_any<D, kBf16>, dim3(tail, a.Hkv, a.s.B), dim3(256), 0, st, true, a, true);
+    return e;
+}
+
+}  // namespace
+
+cudaError_t launch_tree_weights(const AttnCache &c, const TreeArgs &a, int max_rows,
+                                cudaStream_t st) {
+    if (c.D == 64)
+        return c.bf16 ? run<64, true>(c, a, max_rows, st) : run<64, false>(c, a, max_rows, st);
+    return c.bf16 ? run<128, true>(c, a, max_rows, st) : run<128, false>(c, a, max_rows, st);
+}
+
+}  // namespace attn
+}  // namespace qmv
