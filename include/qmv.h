@@ -483,7 +483,7 @@ int attn_tree(const qmv_attn_cache *c, const void *q, int64_t q_stride, int Hq,
  * with their sums, to slots 0, 1, ... of the pages of dst_table (pages that
  * hold no token of `table`; dst may be src's pool or another of the same Hkv,
  * D and dtype). Rotations stay those of the tokens' own positions.
- *   acc [src pages][Hkv][page] fp32, dst_acc [dst pages][Hkv][dst page] fp32
+ *   acc [src pages][Hkv][page] fp32, 16-byte aligned, dst_acc [dst pages][Hkv][dst page] fp32
  *   dst_table [B][dst_max_pages] int32, with room for the kept tokens
  *   keep [B][Hkv][budget] int32: the kept slots, ascending, then -1 (written)
  *   new_lens [B] int32: min(lens[b], budget) (written)

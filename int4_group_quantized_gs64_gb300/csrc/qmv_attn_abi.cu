@@ -134,7 +134,7 @@ int attn_evict(const qmv_attn_cache *src, const float *acc, const int32_t *table
     if (B == 0) return QMV_OK;
     if (!acc || !table || !lens || !dst_acc || !dst_table || !keep || !new_lens) return QMV_EINVAL;
     if (dst_table == table && dst->k == src->k) return QMV_EINVAL;  // pages onto themselves
-    if (!aligned(acc, 4) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(dst_acc, 4) ||
+    if (!aligned(acc, 16) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(dst_acc, 4) ||
         !aligned(dst_table, 4) || !aligned(keep, 4) || !aligned(new_lens, 4) || !aligned(status, 4))
         return QMV_EALIGN;
     return from_cuda(qmv::launch_attn_evict(cache(src), acc, table, max_pages, lens, B, budget,

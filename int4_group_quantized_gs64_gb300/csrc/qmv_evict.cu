@@ -10,9 +10,13 @@
 // k_evict_select finds the smallest kept sum of a (sequence, head) by radix
 // selection on order-preserving 32-bit keys (11, 11 and 10 bits, a histogram
 // each, largest bins first), then lists the kept slots in order. The sums are
-// read once: their keys stay in shared memory. A cluster of blocks shares a
+// read once, four slots a load; the upper halves of their keys stay in shared
+// memory. After the first histogram a pass lists the few slots that share the
+// threshold's bin, and only those are looked at whole for the other bits (all
+// of the bin's again where too many share it). A cluster of blocks shares a
 // list, each with its own stretch of slots; histograms and counts are read
-// across the cluster. k_evict_copy moves the rows.
+// across the cluster. Half a key a slot lets two blocks share an SM: with whole
+// keys 16 clusters of 8 ran in two waves. k_evict_copy moves the rows.
 #include <cooperative_groups.h>
 
 #include "qmv_attn.cuh"
@@ -25,8 +29,9 @@ namespace qmv {
 namespace attn {
 namespace {
 
-constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32, kBins = 2048;
-constexpr int kCachedMax = 50 * 1024;  // keys a block keeps in shared memory (200 KB)
+constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32, kBins = 2048;
+constexpr uint32_t kCand = 160;         // listed slots a warp
+constexpr int kCached = 39 * 1024;      // slots a block keeps 16 key bits of (78 KB)
 
 struct EvictArgs {
     const float *acc;
@@ -52,43 +57,47 @@ __device__ __forceinline__ uint32_t sum_key(float v) {
 
 __device__ __forceinline__ uint32_t slot_key(const EvictArgs &a, const int32_t *row, int h, int i) {
     const int pid = __ldg(row + (i >> a.lpage));
-    if ((unsigned)pid >= (unsigned)a.pages) return 0u;
+    if ((unsigned)pid >= (unsigned)a.pages) return 0u;  // no page: the lowest
     return sum_key(__ldg(a.acc + ((long long)pid * a.Hkv + h) * a.page + (i & (a.page - 1))));
 }
 
-struct SelSmem {
+struct alignas(16) SelSmem {  // (the key halves after it are read 8 bytes at a time)
     uint32_t hist[3][kBins];
-    uint32_t wsum[kSelWarps];
+    uint32_t wsum[32];
     uint32_t found[2];           // bin, and how many are still wanted from it
     uint32_t mine[2];            // this block's (above the threshold, equal to it)
-    uint32_t wcnt[kSelWarps][2];
+    uint32_t wcnt[2][32];        // the same of each warp
+    // slots whose key shares the threshold's first bits, each warp its own (their
+    // numbers in ncand, while they fit)
+    uint32_t ncand[kSelWarps];
+    int32_t cand[kSelWarps][kCand];
 };
 
-// Adds one to the lanes' bins; a warp whose lanes all have the same bin (many
-// equal sums) adds once.
-__device__ __forceinline__ void count_bin(uint32_t *hist, uint32_t bin, bool valid, int lane) {
-    const uint32_t who = __ballot_sync(0xFFFFFFFFu, valid);
-    if (who == 0) return;
-    const int first = __ffs(who) - 1;
-    const uint32_t b0 = __shfl_sync(0xFFFFFFFFu, bin, first);
-    if (__all_sync(0xFFFFFFFFu, !valid || bin == b0)) {
-        if (lane == first) atomicAdd(hist + b0, (uint32_t)__popc(who));
-    } else if (valid) {
-        atomicAdd(hist + bin, 1u);
+static_assert(sizeof(SelSmem) % 16 == 0, "");
+static_assert(sizeof(SelSmem) + kCached * 2 <= 113 * 1024, "two blocks an SM");
+
+// Inclusive sum over a warp's lanes.
+__device__ __forceinline__ uint32_t warp_scan(uint32_t v, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t t = __shfl_up_sync(0xFFFFFFFFu, v, o);
+        if (lane >= o) v += t;
     }
+    return v;
 }
 
-// cached: the keys of a block's stretch that its shared memory holds (all of
-// them up to cached * blocks slots; the rest are read again where needed).
+// cached: the slots (a multiple of 4) of a block's stretch whose upper 16 key
+// bits its shared memory holds; beyond them the sums are read again.
 __global__ void __launch_bounds__(kSelThreads) k_evict_select(const EvictArgs a, int cached) {
     extern __shared__ __align__(16) uint8_t smem[];
     SelSmem *m = reinterpret_cast<SelSmem *>(smem);
-    uint32_t *keys = reinterpret_cast<uint32_t *>(m + 1);
+    uint16_t *upper = reinterpret_cast<uint16_t *>(m + 1);
     cg::cluster_group cl = cg::this_cluster();
     const int C = cl.num_blocks(), rank = cl.block_rank();
     const int bh = blockIdx.x / C, b = bh / a.Hkv, h = bh - b * a.Hkv;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     for (int i = tid; i < 3 * kBins; i += kSelThreads) (&m->hist[0][0])[i] = 0u;
+    if (tid < 64) m->wcnt[tid >> 5][tid & 31] = 0u;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     int len = a.lens[b];
@@ -112,143 +121,258 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const EvictArgs a,
 
     const int lo = a.sink, hi = len - a.recent;
     uint32_t want = a.budget - a.sink - a.recent;  // of slots [lo, hi)
-    // this warp's stretch [w0, w1), a multiple of 32 slots long; slot i's key is
-    // keys[i - c0] while that is below `cached`
-    const int per = (((hi - lo + C * kSelWarps - 1) / (C * kSelWarps)) + 31) & ~31;
-    const int c0 = (int)min((long long)lo + (long long)rank * kSelWarps * per, (long long)hi);
-    const int w0 = (int)min((long long)c0 + (long long)warp * per, (long long)hi);
-    const int w1 = (int)min((long long)w0 + per, (long long)hi);
-    auto key_at = [&](int i) {
-        return i - c0 < cached ? keys[i - c0] : slot_key(a, row, h, i);
+    // this warp's stretch [w0, w1): `per` slots from a multiple of 128 on; the
+    // block's starts at c0
+    const int base = lo & ~127;
+    const int per = (((hi - base + C * kSelWarps - 1) / (C * kSelWarps)) + 127) & ~127;
+    const int end = base + ((hi - base + 127) & ~127);
+    const int c0 = (int)min((long long)base + (long long)rank * kSelWarps * per, (long long)end);
+    const int w0 = (int)min((long long)c0 + (long long)warp * per, (long long)end);
+    const int w1 = (int)min((long long)w0 + per, (long long)end);
+    auto pack16 = [](const uint4 &k) {
+        return make_uint2(__byte_perm(k.x, k.y, 0x7632), __byte_perm(k.z, k.w, 0x7632));
     };
     __syncthreads();
 
-    // keys to shared memory, eight loads a lane under way, and the first histogram
-    constexpr int kU = 8;
-    for (int i0 = w0; i0 < w1; i0 += 32 * kU) {
-        int pid[kU];
-        float v[kU];
+    // The sums, kU groups of four slots a lane a round (loads a round ahead, their
+    // page ids two): upper halves of the keys to shared memory, and the histogram of
+    // the first 11 bits. Sums share bins, so the lanes spread over the three
+    // histograms, and a warp whose slots all have the same bin (many equal sums)
+    // adds once.
+    constexpr int kU = 4;
+    float4 v[2][kU];
+    int pid[kU];
+    auto fetch = [&](int i0) {
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+            pid[u] = __ldg(row + (min(i0 + u * 128 + lane * 4, hi - 1) >> a.lpage));
+    };
+    auto load = [&](int i0, float4 (&d)[kU]) {
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-            const int i = i0 + u * 32 + lane;
-            pid[u] = __ldg(row + (min(i, hi - 1) >> a.lpage));
+            const int i = i0 + u * 128 + lane * 4;
+            const float no = __int_as_float(0x7FC00000);  // no page: the lowest
+            d[u] = make_float4(no, no, no, no);
+            if (i < min(w1, hi) && (unsigned)pid[u] < (unsigned)a.pages)
+                d[u] = __ldg(reinterpret_cast<const float4 *>(
+                    a.acc + ((long long)pid[u] * a.Hkv + h) * a.page + (i & (a.page - 1))));
         }
+    };
+    uint32_t *h0 = m->hist[lane % 3];
+    auto count = [&](int i0, const float4 (&d)[kU]) {
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-            const int i = min(i0 + u * 32 + lane, hi - 1);
-            const bool good = (unsigned)pid[u] < (unsigned)a.pages;
-            v[u] = good ? __ldg(a.acc + ((long long)pid[u] * a.Hkv + h) * a.page + (i & (a.page - 1)))
-                        : __int_as_float(0x7FC00000);  // no page: the lowest
+            if (i0 + u * 128 >= w1) break;
+            const int i = i0 + u * 128 + lane * 4;
+            const uint4 k = make_uint4(sum_key(d[u].x), sum_key(d[u].y), sum_key(d[u].z), sum_key(d[u].w));
+            if (i - c0 < cached) *reinterpret_cast<uint2 *>(upper + (i - c0)) = pack16(k);
+            const uint32_t x[4] = {k.x >> 21, k.y >> 21, k.z >> 21, k.w >> 21};
+            const uint32_t b0 = __shfl_sync(0xFFFFFFFFu, x[0], 0);
+            const bool all_in = i >= lo && i + 4 <= hi;
+            if (__all_sync(0xFFFFFFFFu, all_in && x[0] == b0 && x[1] == b0 && x[2] == b0 && x[3] == b0)) {
+                if (lane == 0) atomicAdd(&m->hist[0][b0], 128u);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (all_in || (i + e >= lo && i + e < hi)) atomicAdd(h0 + x[e], 1u);
+            }
         }
+    };
+    constexpr int kRound = 128 * kU;
+    if (w0 < w1) {
+        fetch(w0);
+        load(w0, v[0]);
+        if (w0 + kRound < w1) fetch(w0 + kRound);
+    }
+    for (int i0 = w0; i0 < w1; i0 += 2 * kRound) {
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-            const int i = i0 + u * 32 + lane;
-            const uint32_t k = sum_key(v[u]);
-            if (i < w1 && i - c0 < cached) keys[i - c0] = k;
-            count_bin(m->hist[0], k >> 21, i < w1, lane);
+        for (int s = 0; s < 2; ++s) {
+            const int i = i0 + s * kRound;
+            if (i >= w1) break;
+            if (i + kRound < w1) load(i + kRound, v[s ^ 1]);
+            if (i + 2 * kRound < w1) fetch(i + 2 * kRound);
+            count(i, v[s]);
         }
     }
-    __syncwarp();
-    uint32_t prefix = 0, mask = 0;  // the bits found so far
+    __syncthreads();
+    {
+        uint4 *s0 = reinterpret_cast<uint4 *>(m->hist[0]) + tid, *s1 = reinterpret_cast<uint4 *>(m->hist[1]) + tid,
+              *s2 = reinterpret_cast<uint4 *>(m->hist[2]) + tid;
+        const uint4 x = *s0, y = *s1, z = *s2;
+        *s0 = make_uint4(x.x + y.x + z.x, x.y + y.y + z.y, x.z + y.z + z.z, x.w + y.w + z.w);
+        *s1 = *s2 = make_uint4(0u, 0u, 0u, 0u);
+    }
+    // The upper halves of 128 slots from i0, four a lane, 32 slots apart, and
+    // which of them are inside.
+    auto upper4 = [&](int i0, uint32_t (&x)[4], bool (&in)[4]) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int i = i0 + u * 32 + lane;
+            in[u] = i >= lo && i < hi;
+            x[u] = i - c0 < cached ? upper[i - c0] : in[u] ? slot_key(a, row, h, i) >> 16 : 0u;
+        }
+    };
+    const uint32_t below = (1u << lane) - 1;
+    uint32_t prefix = 0;  // the bits found so far
+    bool listed = false;  // the slots that share the threshold's first bits are in m->cand
+    // Their whole keys: f(slot, key).
+    auto candidates = [&](auto &&f) {
+        __syncwarp();
+        if (listed) {
+            for (uint32_t i = lane; i < m->ncand[warp]; i += 32) {
+                const int s = m->cand[warp][i];
+                f(s, slot_key(a, row, h, s));
+            }
+        } else {
+            for (int i0 = w0; i0 < w1; i0 += 128) {
+                uint32_t x[4];
+                bool in[4];
+                upper4(i0, x, in);
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    if (in[u] && x[u] >> 5 == prefix >> 21)
+                        f(i0 + u * 32 + lane, slot_key(a, row, h, i0 + u * 32 + lane));
+            }
+        }
+    };
     for (int p = 0; p < 3; ++p) {
         const int shift = p == 0 ? 21 : p == 1 ? 10 : 0, bits = p == 2 ? 10 : 11;
         if (p > 0)
-            for (int i0 = w0; i0 < w1; i0 += 32) {
-                const int i = i0 + lane;
-                const uint32_t k = i < w1 ? key_at(i) : 0u;
-                count_bin(m->hist[p], (k >> shift) & ((1u << bits) - 1), i < w1 && (k & mask) == prefix, lane);
-            }
-        cl.sync();
+            candidates([&](int, uint32_t k) {
+                if (k >> (shift + bits) == prefix >> (shift + bits))
+                    atomicAdd(&m->hist[p][(k >> shift) & ((1u << bits) - 1)], 1u);
+            });
+        if (C > 1)
+            cl.sync();
+        else
+            __syncthreads();
         // bins from the top: thread t takes the kPer below kBins - kPer * t
         constexpr int kPer = kBins / kSelThreads;
-        static_assert(kPer == 4 || kPer == 2, "");
+        static_assert(kPer == 4, "");
         const int bin0 = kBins - (tid + 1) * kPer;
-        uint32_t n[kPer], sum = 0;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) n[j] = 0;
+        uint4 n = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 8
         for (int r = 0; r < C; ++r) {
-            const uint32_t *hr = cl.map_shared_rank(&m->hist[p][0], r) + bin0;
-            if (kPer == 4) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(hr);
-                n[kPer - 1] += x.x; n[kPer - 2] += x.y; n[1] += x.z; n[0] += x.w;
-            } else {
-                const uint2 x = *reinterpret_cast<const uint2 *>(hr);
-                n[1] += x.x; n[0] += x.y;
-            }
+            const uint4 x = *reinterpret_cast<const uint4 *>(cl.map_shared_rank(&m->hist[p][0], r) + bin0);
+            n.x += x.x; n.y += x.y; n.z += x.z; n.w += x.w;
         }
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) sum += n[j];
-        uint32_t inc = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t t = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-            if (lane >= o) inc += t;
-        }
+        const uint32_t cnt[kPer] = {n.w, n.z, n.y, n.x};
+        const uint32_t sum = n.x + n.y + n.z + n.w, inc = warp_scan(sum, lane);
         if (lane == 31) m->wsum[warp] = inc;
         if (tid == 0) {  // wanted 0: a threshold above every key
             m->found[0] = (1u << bits) - 1;
             m->found[1] = 0;
         }
         __syncthreads();
-        uint32_t before = inc - sum;
-        for (int w = 0; w < warp; ++w) before += m->wsum[w];
+        const uint32_t ws = lane < kSelWarps ? m->wsum[lane] : 0u;
+        const uint32_t ahead = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? ws : 0u);
+        uint32_t before = ahead + inc - sum;
         // the bin that holds the want-th largest
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
-            if (before < want && before + n[j] >= want) {
+            if (before < want && before + cnt[j] >= want) {
                 m->found[0] = kBins - 1 - (tid * kPer + j);
                 m->found[1] = want - before;
             }
-            before += n[j];
+            before += cnt[j];
         }
         __syncthreads();
         prefix |= m->found[0] << shift;
-        mask |= ((1u << bits) - 1) << shift;
         want = m->found[1];
         __syncthreads();
+        if (p == 0) {
+            // each warp's keys above this bin, and a list of the slots in it
+            uint32_t above = 0, n = 0;
+            const uint32_t t = prefix >> 21;
+            for (int i0 = w0; i0 < w1; i0 += 128) {
+                uint32_t x[4], be[4];
+                bool in[4];
+                upper4(i0, x, in);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    above += in[u] && x[u] >> 5 > t;
+                    be[u] = __ballot_sync(0xFFFFFFFFu, in[u] && x[u] >> 5 == t);
+                }
+                if (be[0] | be[1] | be[2] | be[3]) {
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const uint32_t at = n + __popc(be[u] & below);
+                        if (((be[u] >> lane) & 1u) && at < kCand)
+                            m->cand[warp][at] = i0 + u * 32 + lane;
+                        n += __popc(be[u]);
+                    }
+                }
+            }
+            above = __reduce_add_sync(0xFFFFFFFFu, above);
+            if (lane == 0) {
+                m->wcnt[0][warp] = above;
+                m->ncand[warp] = n;
+            }
+            listed = __syncthreads_and(n <= kCand);
+        }
     }
-    // keys above `prefix` are kept, and the first `want` equal to it
-    uint32_t above = 0, equal = 0;
-    for (int i = w0 + lane; i < w1; i += 32) {
-        const uint32_t k = key_at(i);
-        above += k > prefix;
-        equal += k == prefix;
-    }
-    above = __reduce_add_sync(0xFFFFFFFFu, above);
-    equal = __reduce_add_sync(0xFFFFFFFFu, equal);
-    if (lane == 0) {
-        m->wcnt[warp][0] = above;
-        m->wcnt[warp][1] = equal;
-    }
+    // keys above `prefix` are kept, and the first `want` equal to it: both in
+    // each warp's stretch
+    candidates([&](int s, uint32_t k) {
+        const int w = (s - c0) / per;
+        if (k > prefix) atomicAdd(&m->wcnt[0][w], 1u);
+        if (k == prefix) atomicAdd(&m->wcnt[1][w], 1u);
+        // its upper half, where that alone does not decide, moves to the right side
+        if (k >> 16 == prefix >> 16 && k != prefix && s - c0 < cached)
+            upper[s - c0] = (uint16_t)((k >> 16) + (k > prefix ? 1 : -1));
+    });
     __syncthreads();
-    if (tid < 2) {
-        uint32_t s = 0;
-        for (int w = 0; w < kSelWarps; ++w) s += m->wcnt[w][tid];
-        m->mine[tid] = s;
+    const uint32_t wa = lane < kSelWarps ? m->wcnt[0][lane] : 0u, we = lane < kSelWarps ? m->wcnt[1][lane] : 0u;
+    uint32_t pa = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? wa : 0u);  // before this warp's stretch
+    uint32_t pe = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? we : 0u);
+    if (C > 1) {
+        if (warp == 0) {
+            const uint32_t ta = __reduce_add_sync(0xFFFFFFFFu, wa), te = __reduce_add_sync(0xFFFFFFFFu, we);
+            if (lane == 0) {
+                m->mine[0] = ta;
+                m->mine[1] = te;
+            }
+        }
+        cl.sync();
+        uint32_t ra = 0, re = 0;
+        if (lane < rank) {
+            const uint32_t *x = cl.map_shared_rank(&m->mine[0], lane);
+            ra = x[0];
+            re = x[1];
+        }
+        pa += __reduce_add_sync(0xFFFFFFFFu, ra);
+        pe += __reduce_add_sync(0xFFFFFFFFu, re);
+        cl.sync();  // no block leaves while its counts are read
     }
-    cl.sync();
-    uint32_t pa = 0, pe = 0;  // above / equal before this warp's stretch
-    for (int r = 0; r < rank; ++r) {
-        const uint32_t *x = cl.map_shared_rank(&m->mine[0], r);
-        pa += x[0];
-        pe += x[1];
-    }
-    for (int w = 0; w < warp; ++w) {
-        pa += m->wcnt[w][0];
-        pe += m->wcnt[w][1];
-    }
-    if (C > 1) cl.sync();  // no block leaves while its counts are read
-    for (int i0 = w0; i0 < w1; i0 += 32) {
-        const int i = i0 + lane;
-        const uint32_t k = i < w1 ? key_at(i) : 0u;
-        const uint32_t ba = __ballot_sync(0xFFFFFFFFu, i < w1 && k > prefix);
-        const uint32_t be = __ballot_sync(0xFFFFFFFFu, i < w1 && k == prefix);
-        const uint32_t below = (1u << lane) - 1;
-        const uint32_t na = pa + __popc(ba & below), ne = pe + __popc(be & below);
-        if (((ba >> lane) & 1u) || (((be >> lane) & 1u) && ne < want))
-            keep[a.sink + na + min(ne, want)] = i;
-        pa += __popc(ba);
-        pe += __popc(be);
+    const uint32_t t16 = prefix >> 16;
+    keep += a.sink;
+    for (int i0 = w0; i0 < w1; i0 += 128) {
+        uint32_t x[4], ba[4], be[4];
+        bool in[4];
+        upper4(i0, x, in);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            ba[u] = __ballot_sync(0xFFFFFFFFu, in[u] && x[u] > t16);
+            be[u] = __ballot_sync(0xFFFFFFFFu, in[u] && x[u] == t16);
+        }
+        if (i0 + 127 - c0 >= cached && (be[0] | be[1] | be[2] | be[3])) {  // the lower halves decide
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int i = i0 + u * 32 + lane;
+                const uint32_t k = (be[u] >> lane) & 1u ? slot_key(a, row, h, i) : 0u;
+                const bool eq = (be[u] >> lane) & 1u;
+                ba[u] |= __ballot_sync(0xFFFFFFFFu, eq && k > prefix);
+                be[u] = __ballot_sync(0xFFFFFFFFu, eq && k == prefix);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const uint32_t ne = pe + __popc(be[u] & below), na = pa + __popc(ba[u] & below);
+            if (((ba[u] >> lane) & 1u) || (((be[u] >> lane) & 1u) && ne < want))
+                keep[na + min(ne, want)] = i0 + u * 32 + lane;
+            pa += __popc(ba[u]);
+            pe += __popc(be[u]);
+        }
     }
 }
 
@@ -323,11 +447,11 @@ cudaError_t launch_attn_evict(const AttnCache &src, const float *acc, const int3
     // some thousand slots (a cluster's barriers cost as much as reading those).
     const long long longest = (long long)max_pages << a.lpage;
     int C = 1;
-    while (C < 8 && longest / C > 8192 && (long long)B * src.Hkv * C * 2 <= sm_count()) C *= 2;
-    // as many of its keys as fit in shared memory
-    const long long stretch = (longest + C - 1) / C + 32 * kSelWarps;
-    const int cached = (int)(stretch < kCachedMax ? stretch : kCachedMax);
-    const size_t smem = sizeof(SelSmem) + (size_t)cached * 4;
+    while (C < 8 && longest / C > 8192 && (long long)B * src.Hkv * C <= sm_count()) C *= 2;
+    // the upper halves of a block's keys, as many as leave room for two blocks an SM
+    const long long stretch = (longest + C - 1) / C + 128 * kSelWarps + 128;
+    const int cached = (int)(stretch < kCached ? stretch : kCached) & ~3;
+    const size_t smem = sizeof(SelSmem) + (size_t)cached * 2;
     cudaError_t e = set_smem(k_evict_select, smem);
     if (e != cudaSuccess) return e;
 
