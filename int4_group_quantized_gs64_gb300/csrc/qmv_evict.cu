@@ -447,12 +447,15 @@ cudaError_t launch_attn_evict(const AttnCache &src, const float *acc, const int3
     // some thousand slots (a cluster's barriers cost as much as reading those).
     const long long longest = (long long)max_pages << a.lpage;
     int C = 1;
-    while (C < 8 && longest / C > 8192 && (long long)B * src.Hkv * C <= sm_count()) C *= 2;
+    const int most = B * src.Hkv <= 8 ? 16 : 8;  // (few clusters of 16 fit at a time)
+    while (C < most && longest / C > 8192 && (long long)B * src.Hkv * C <= sm_count()) C *= 2;
     // the upper halves of a block's keys, as many as leave room for two blocks an SM
     const long long stretch = (longest + C - 1) / C + 128 * kSelWarps + 128;
     const int cached = (int)(stretch < kCached ? stretch : kCached) & ~3;
     const size_t smem = sizeof(SelSmem) + (size_t)cached * 2;
     cudaError_t e = set_smem(k_evict_select, smem);
+    if (e == cudaSuccess && C > 8)  // more than the portable size
+        e = cudaFuncSetAttribute(k_evict_select, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
 
     cudaLaunchConfig_t cfg = {};

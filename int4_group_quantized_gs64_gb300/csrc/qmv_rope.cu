@@ -9,9 +9,11 @@
 // would be off by hundredths of a radian, the fraction of a turn by 1e-10.
 // All arithmetic on the elements is fp32, rounded once to the cache's type.
 //
-// It is bound by memory at many tokens and by latency at few, so each block
-// takes a share of one token's heads (as many blocks a token as fill the GPU)
-// and issues its loads before it forms the angles.
+// A warp takes one token (or a share of its heads, so that few tokens fill the
+// GPU too). D / 16 lanes share a head, 16 elements each: a lane has the same
+// place in every head that it meets, and so the same eight angles, which stay
+// in registers: no shared memory, no barrier. The lanes that share a place
+// divide its eight angles and exchange them.
 #include "qmv_attn.cuh"
 #include "qmv_attn.h"
 #include "qmv_launch.cuh"
@@ -34,22 +36,30 @@ struct RopeArgs {
     int parts;  // blocks a token
 };
 
-constexpr int kRopeThreads = 256;
+constexpr int kWarps = 4;  // a block
+constexpr int kFill = 16;  // warps an SM that few tokens are split for
 
-// Eight consecutive elements as fp32, and back.
+// Eight consecutive elements as they lie in memory, as fp32, and rounded.
 template <bool kBf16, bool kF32>
 struct Vec8 {
-    float x[8];
+    uint4 raw[kF32 ? 2 : 1];
     __device__ __forceinline__ void load(const void *p, long long at) {
+        const uint4 *u = kF32 ? reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + at)
+                              : reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + at);
+        raw[0] = __ldcs(u);
+        if (kF32) raw[kF32 ? 1 : 0] = __ldcs(u + 1);
+    }
+    __device__ __forceinline__ void unpack(float (&x)[8]) const {
+        const uint32_t w[4] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w};
         if (kF32) {
-            const float4 *f = reinterpret_cast<const float4 *>(static_cast<const float *>(p) + at);
-            const float4 a = __ldg(f), b = __ldg(f + 1);
-            x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-            x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+            const uint4 h = raw[kF32 ? 1 : 0];
+            const uint32_t v[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[i] = __uint_as_float(w[i]);
+                x[4 + i] = __uint_as_float(v[i]);
+            }
         } else {
-            const uint4 u = __ldg(
-                reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + at));
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float2 f = unpack2<kBf16>(w[i]);
@@ -58,12 +68,13 @@ struct Vec8 {
             }
         }
     }
-    __device__ __forceinline__ void store(uint16_t *p) const {
-        *reinterpret_cast<uint4 *>(p) =
-            make_uint4(pack2<kBf16>(x[0], x[1]), pack2<kBf16>(x[2], x[3]),
-                       pack2<kBf16>(x[4], x[5]), pack2<kBf16>(x[6], x[7]));
-    }
 };
+template <bool kBf16>
+__device__ __forceinline__ void store8(uint16_t *p, const float (&x)[8]) {
+    *reinterpret_cast<uint4 *>(p) =
+        make_uint4(pack2<kBf16>(x[0], x[1]), pack2<kBf16>(x[2], x[3]), pack2<kBf16>(x[4], x[5]),
+                   pack2<kBf16>(x[6], x[7]));
+}
 
 template <bool kBf16, bool kF32>
 __device__ __forceinline__ float load1(const void *p, long long at) {
@@ -71,156 +82,187 @@ __device__ __forceinline__ float load1(const void *p, long long at) {
                 : to_f32<kBf16>(static_cast<const uint16_t *>(p)[at]);
 }
 
-// kVec: rows and strides 16-byte aligned and rot a multiple of 16, so a
-// thread takes 16 elements of a head as two vectors (the two halves of eight
-// pairs, or 16 in a row). Otherwise a thread takes one pair (or two elements
-// past rot) at a time.
-template <bool kBf16, bool kF32, bool kVec, bool kInter>
-__global__ void __launch_bounds__(kRopeThreads) k_rope_append(const RopeArgs a) {
-    extern __shared__ float2 cs[];  // [rot / 2] (cos, sin) times mscale
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int n = blockIdx.x / a.parts, part = blockIdx.x - n * a.parts;
-    const int heads = a.Hq + 2 * a.Hkv, half = a.rot >> 1;
-    const int per_head = kVec ? a.D / 16 : a.D / 2;
-    const int units = heads * per_head;
-    const int ub = (int)((long long)units * part / a.parts);
-    const int ue = (int)((long long)units * (part + 1) / a.parts);
-    // where the first vectors are, so that their loads are under way first
-    auto source = [&](int u, const void *&p, long long &at, int &hd, int &lo, int &hi, bool &turn) {
-        hd = u / per_head;
-        const int i = u - hd * per_head;
-        if (kVec) {
-            if (!kInter && i < half / 8) {
-                lo = i * 8;
-                hi = half + i * 8;
-                turn = true;
-            } else {
-                lo = i * 16;
-                hi = lo + 8;
-                turn = kInter && lo < a.rot;
-            }
-        } else {
-            turn = i < half;
-            lo = kInter || !turn ? 2 * i : i;
-            hi = kInter || !turn ? 2 * i + 1 : half + i;
-        }
-        if (hd < a.Hq) {
-            p = a.q;
-            at = (long long)n * a.qs + (long long)hd * a.D;
-        } else if (hd < a.Hq + a.Hkv) {
-            p = a.k;
-            at = (long long)n * a.ks + (long long)(hd - a.Hq) * a.D;
-        } else {
-            p = a.v;
-            at = (long long)n * a.vs + (long long)(hd - a.Hq - a.Hkv) * a.D;
-            turn = false;
-        }
-    };
-    Vec8<kBf16, kF32> x0, x1;
-    const void *p;
-    long long at;
-    int hd = 0, lo = 0, hi = 0;
-    bool turn = false;
-    int u = ub + threadIdx.x;
-    if (kVec && u < ue) {
-        source(u, p, at, hd, lo, hi, turn);
-        x0.load(p, at + lo);
-        x1.load(p, at + hi);
+// cos and sin of the angle of pair i at position pos, times mscale.
+__device__ __forceinline__ float2 turn_of(const RopeArgs &a, double pos, int i) {
+    double t = pos * (a.inv_freq[i] * 0.15915494309189533577);
+    t -= floor(t);
+    float s, c;
+    sincospif(2.f * (float)t, &s, &c);
+    return make_float2(c * a.mscale, s * a.mscale);
+}
+
+// Where a token goes in the cache: its page and row; false if nowhere (the
+// status says why). Whole warp.
+__device__ __forceinline__ bool find_slot(const RopeArgs &a, int n, int lane, int &pid, int &row) {
+    // its sequence is the last that starts at or before it
+    int b = -1;
+    for (int j0 = 0; j0 < a.s.B; j0 += 32) {
+        const int j = j0 + lane;
+        b += __popc(__ballot_sync(0xFFFFFFFFu, j < a.s.B && a.s.cu[j] <= n));
     }
-    const double pos = (double)a.pos[n];
-    for (int i = threadIdx.x; i < half; i += kRopeThreads) {
-        double t = pos * (a.inv_freq[i] * 0.15915494309189533577);
-        t -= floor(t);
-        float s, c;
-        sincospif(2.f * (float)t, &s, &c);
-        cs[i] = make_float2(c * a.mscale, s * a.mscale);
-    }
-    // the token's sequence: how many sequences start at or before it
-    int b = 0;
-    for (int i = 0; i < a.s.B; i += kRopeThreads) {
-        const int j = i + threadIdx.x;
-        b += __syncthreads_count(j < a.s.B && a.s.cu[j] <= n);
-    }
-    b -= 1;  // (the barrier also publishes cs)
     bool ok = false;
     Seq q;
     q.ctx = q.first = q.T = 0;
     if (b >= 0) q = get_seq(a.s, b, ok);
     ok = ok && n - q.first < q.T;
-    int pid = -1, row = 0;
+    pid = -1;
+    row = 0;
     if (ok) {
         const int slot = q.ctx + n - q.first;
         pid = a.s.table[(long long)b * a.s.max_pages + (slot >> a.s.lpage)];
         row = slot & (a.s.page - 1);
     }
     const bool good = ok && (unsigned)pid < (unsigned)a.pages;
-    if (threadIdx.x == 0 && part == 0 && !good) set_status(a.status, ok ? kStPage : kStLength);
-    if (good && a.acc && part == 0)
-        for (int h = threadIdx.x; h < a.Hkv; h += kRopeThreads)
-            a.acc[((long long)pid * a.Hkv + h) * a.s.page + row] = 0.f;
-    for (; u < ue; u += kRopeThreads) {
-        if (u >= ub + kRopeThreads || !kVec) {
-            source(u, p, at, hd, lo, hi, turn);
-            if (kVec) {
-                x0.load(p, at + lo);
-                x1.load(p, at + hi);
+    if (lane == 0 && !good) set_status(a.status, ok ? kStPage : kStLength);
+    return good;
+}
+
+struct Head {
+    const void *src;
+    long long at;   // its first element
+    uint16_t *dst;  // null: nowhere
+    bool turn;
+};
+__device__ __forceinline__ Head head_of(const RopeArgs &a, int n, int hd, bool good, int pid, int row) {
+    Head r;
+    r.dst = nullptr;
+    r.turn = hd < a.Hq + a.Hkv;
+    if (hd < a.Hq) {
+        r.src = a.q;
+        r.at = (long long)n * a.qs + (long long)hd * a.D;
+        r.dst = a.q_out + ((long long)n * a.Hq + hd) * a.D;
+    } else {
+        const int h = r.turn ? hd - a.Hq : hd - a.Hq - a.Hkv;
+        r.src = r.turn ? a.k : a.v;
+        r.at = (long long)n * (r.turn ? a.ks : a.vs) + (long long)h * a.D;
+        if (good)
+            r.dst = (r.turn ? a.kc : a.vc) + (((long long)pid * a.Hkv + h) * a.s.page + row) * a.D;
+    }
+    return r;
+}
+
+__device__ __forceinline__ void clear_sums(const RopeArgs &a, int lane, int pid, int row) {
+    for (int h = lane; h < a.Hkv; h += 32) a.acc[((long long)pid * a.Hkv + h) * a.s.page + row] = 0.f;
+}
+
+// Rows and strides on 16-byte boundaries, rot a multiple of 16.
+template <int D, bool kBf16, bool kF32, bool kInter>
+__global__ void __launch_bounds__(32 * kWarps) k_rope_append(const RopeArgs a) {
+    constexpr int kPerHead = D / 16, kHeads = 32 / kPerHead;  // lanes a head, heads a pass
+    constexpr int kAngles = 8 / kHeads, kAhead = kF32 ? 2 : 4;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int lane = threadIdx.x & 31;
+    const long long w = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (w >= (long long)a.s.N * a.parts) return;
+    const int n = (int)(w / a.parts), part = (int)(w - (long long)n * a.parts);
+    const int i = lane % kPerHead, g = lane / kPerHead, half = a.rot >> 1;
+    const int lo = kInter || i * 8 >= half ? i * 16 : i * 8;
+    const int hi = kInter || i * 8 >= half ? i * 16 + 8 : half + i * 8;
+    const bool place_turns = i * 8 < half;
+    const int heads = a.Hq + 2 * a.Hkv;
+    const int hb = (int)((long long)heads * part / a.parts), he = (int)((long long)heads * (part + 1) / a.parts);
+
+    int pid, row;
+    const bool good = find_slot(a, n, lane, pid, row);
+    if (good && a.acc && part == 0) clear_sums(a, lane, pid, row);
+    float2 cs[8];
+    {
+        const double pos = (double)a.pos[n];
+        float2 mine[kAngles];
+#pragma unroll
+        for (int j = 0; j < kAngles; ++j)
+            mine[j] = place_turns ? turn_of(a, pos, i * 8 + g * kAngles + j) : make_float2(1.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int from = (j / kAngles) * kPerHead + i;
+            cs[j].x = __shfl_sync(0xFFFFFFFFu, mine[j % kAngles].x, from);
+            cs[j].y = __shfl_sync(0xFFFFFFFFu, mine[j % kAngles].y, from);
+        }
+    }
+    for (int h0 = hb; h0 < he; h0 += kHeads * kAhead) {
+        Vec8<kBf16, kF32> r[kAhead][2];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+            const int hd = h0 + j * kHeads + g;
+            if (hd < he) {
+                const Head s = head_of(a, n, hd, good, pid, row);
+                r[j][0].load(s.src, s.at + lo);
+                r[j][1].load(s.src, s.at + hi);
             }
         }
-        uint16_t *d;
-        if (hd < a.Hq) {
-            d = a.q_out + ((long long)n * a.Hq + hd) * a.D;
-        } else {
-            if (!good) continue;
-            const int h = hd < a.Hq + a.Hkv ? hd - a.Hq : hd - a.Hq - a.Hkv;
-            d = (hd < a.Hq + a.Hkv ? a.kc : a.vc) +
-                (((long long)pid * a.Hkv + h) * a.s.page + row) * a.D;
-        }
-        if (kVec) {
-            if (turn) {
-                if (kInter) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 f = cs[lo / 2 + i], g = cs[lo / 2 + 4 + i];
-                        const float a0 = x0.x[2 * i], b0 = x0.x[2 * i + 1];
-                        x0.x[2 * i] = a0 * f.x - b0 * f.y;
-                        x0.x[2 * i + 1] = b0 * f.x + a0 * f.y;
-                        const float a1 = x1.x[2 * i], b1 = x1.x[2 * i + 1];
-                        x1.x[2 * i] = a1 * g.x - b1 * g.y;
-                        x1.x[2 * i + 1] = b1 * g.x + a1 * g.y;
-                    }
-                } else {
+        for (int j = 0; j < kAhead; ++j) {
+            const int hd = h0 + j * kHeads + g;
+            if (hd >= he) continue;
+            const Head s = head_of(a, n, hd, good, pid, row);
+            float x0[8], x1[8];
+            r[j][0].unpack(x0);
+            r[j][1].unpack(x1);
+            if (s.turn && place_turns) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 f = cs[lo + i];
-                        const float a0 = x0.x[i], b0 = x1.x[i];
-                        x0.x[i] = a0 * f.x - b0 * f.y;
-                        x1.x[i] = b0 * f.x + a0 * f.y;
-                    }
+                for (int e = 0; e < 8; ++e) {
+                    float &p = kInter ? (e < 4 ? x0[2 * e] : x1[2 * e - 8]) : x0[e];
+                    float &q = kInter ? (e < 4 ? x0[2 * e + 1] : x1[2 * e - 7]) : x1[e];
+                    const float u = p, v = q;
+                    p = u * cs[e].x - v * cs[e].y;
+                    q = v * cs[e].x + u * cs[e].y;
                 }
             }
-            x0.store(d + lo);
-            x1.store(d + hi);
-        } else {
-            const float va = load1<kBf16, kF32>(p, at + lo), vb = load1<kBf16, kF32>(p, at + hi);
-            float ra = va, rb = vb;
-            if (turn) {
-                const float2 f = cs[kInter ? lo / 2 : lo];
-                ra = va * f.x - vb * f.y;
-                rb = vb * f.x + va * f.y;
+            if (s.dst) {
+                store8<kBf16>(s.dst + lo, x0);
+                store8<kBf16>(s.dst + hi, x1);
             }
-            d[lo] = from_f32<kBf16>(ra);
-            d[hi] = from_f32<kBf16>(rb);
         }
     }
 }
 
-template <bool kBf16, bool kF32, bool kVec>
-cudaError_t run(const RopeArgs &a, bool inter, cudaStream_t st) {
-    const dim3 grid((unsigned)((long long)a.s.N * a.parts)), block(kRopeThreads);
-    const size_t smem = (size_t)(a.rot / 2) * sizeof(float2);
-    return inter ? launch(k_rope_append<kBf16, kF32, kVec, true>, grid, block, smem, st, true, a)
-                 : launch(k_rope_append<kBf16, kF32, kVec, false>, grid, block, smem, st, true, a);
+// Any alignment and any even rot: a lane takes a pair (or two elements past
+// rot) at a time.
+template <bool kBf16, bool kF32, bool kInter>
+__global__ void __launch_bounds__(32 * kWarps) k_rope_any(const RopeArgs a) {
+    __shared__ float2 table[kWarps][64];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int lane = threadIdx.x & 31;
+    const long long w = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (w >= (long long)a.s.N * a.parts) return;
+    const int n = (int)(w / a.parts), part = (int)(w - (long long)n * a.parts), half = a.rot >> 1;
+    const int heads = a.Hq + 2 * a.Hkv;
+    const int hb = (int)((long long)heads * part / a.parts), he = (int)((long long)heads * (part + 1) / a.parts);
+    int pid, row;
+    const bool good = find_slot(a, n, lane, pid, row);
+    if (good && a.acc && part == 0) clear_sums(a, lane, pid, row);
+    float2 *cs = table[threadIdx.x >> 5];
+    const double pos = (double)a.pos[n];
+    for (int i = lane; i < half; i += 32) cs[i] = turn_of(a, pos, i);
+    __syncwarp();
+    for (int hd = hb; hd < he; ++hd) {
+        const Head s = head_of(a, n, hd, good, pid, row);
+        for (int i = lane; i < a.D / 2; i += 32) {
+            const bool t = i < half;
+            const int lo = kInter || !t ? 2 * i : i, hi = kInter || !t ? 2 * i + 1 : half + i;
+            float u = load1<kBf16, kF32>(s.src, s.at + lo), v = load1<kBf16, kF32>(s.src, s.at + hi);
+            if (s.turn && t) {
+                const float x = u;
+                u = x * cs[i].x - v * cs[i].y;
+                v = v * cs[i].x + x * cs[i].y;
+            }
+            if (s.dst) {
+                s.dst[lo] = from_f32<kBf16>(u);
+                s.dst[hi] = from_f32<kBf16>(v);
+            }
+        }
+    }
+}
+
+template <bool kBf16, bool kF32, bool kInter>
+cudaError_t run(const RopeArgs &a, bool vec, cudaStream_t st) {
+    const dim3 grid((unsigned)(((long long)a.s.N * a.parts + kWarps - 1) / kWarps)), block(32 * kWarps);
+    return launch(!vec        ? k_rope_any<kBf16, kF32, kInter>
+                  : a.D == 64 ? k_rope_append<64, kBf16, kF32, kInter>
+                              : k_rope_append<128, kBf16, kF32, kInter>,
+                  grid, block, 0, st, true, a);
 }
 
 }  // namespace
@@ -249,20 +291,16 @@ cudaError_t launch_rope_append(const AttnCache &c, const AttnSeqs &s, const Rope
         return reinterpret_cast<uintptr_t>(r.p) % 16 == 0 && r.stride * esize % 16 == 0;
     };
     const bool v8 = vec(q) && vec(k) && vec(v) && rot % 16 == 0;
-    const int units = (Hq + 2 * c.Hkv) * (v8 ? c.D / 16 : c.D / 2);
-    // blocks a token: enough to give every SM one when tokens are few, each
-    // with at least one pass of its threads
-    const int most = (units + kRopeThreads - 1) / kRopeThreads, want = (sm_count() + s.N - 1) / s.N;
+    // Warps a token: enough to give every SM some when tokens are few, each with
+    // at least one pass over heads.
+    const int heads = Hq + 2 * c.Hkv, pass = v8 ? 32 / (c.D / 16) : 1;
+    const int most = (heads + pass - 1) / pass, want = (sm_count() * kFill + s.N - 1) / s.N;
     a.parts = want < most ? want : most;
-    if (c.bf16)
-        return in_f32 ? (v8 ? run<true, true, true>(a, interleaved, st)
-                            : run<true, true, false>(a, interleaved, st))
-                      : (v8 ? run<true, false, true>(a, interleaved, st)
-                            : run<true, false, false>(a, interleaved, st));
-    return in_f32 ? (v8 ? run<false, true, true>(a, interleaved, st)
-                        : run<false, true, false>(a, interleaved, st))
-                  : (v8 ? run<false, false, true>(a, interleaved, st)
-                        : run<false, false, false>(a, interleaved, st));
+    if (interleaved)
+        return c.bf16 ? (in_f32 ? run<true, true, true>(a, v8, st) : run<true, false, true>(a, v8, st))
+                      : (in_f32 ? run<false, true, true>(a, v8, st) : run<false, false, true>(a, v8, st));
+    return c.bf16 ? (in_f32 ? run<true, true, false>(a, v8, st) : run<true, false, false>(a, v8, st))
+                  : (in_f32 ? run<false, true, false>(a, v8, st) : run<false, false, false>(a, v8, st));
 }
 
 }  // namespace qmv
