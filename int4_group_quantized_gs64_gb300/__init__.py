@@ -493,8 +493,30 @@ def moe_expert_ffn_int4_prefill(m: MoeInt4Weights, x_bf16, ids, w, out=None, ws=
 
 # ------------------------------------------------------------------ attention
 #
-# One-token calls are as short as their host side, so these bindings check each
-# tensor with a few attribute reads and pass plain integers.
+# One-token calls are as short as their host side, so the tensors are checked
+# and passed on in csrc/qmv_torch.cpp.
+
+_torch_mod = None
+
+
+def _torch_binding():
+    """Load _qmv_torch.so (it must have been built; raises otherwise)."""
+    global _torch_mod
+    if _torch_mod is None:
+        import importlib.machinery
+        import importlib.util
+        import torch  # noqa: F401  (its libraries, which the module needs)
+        if not os.path.exists(_build.TORCH_LIB):
+            raise RuntimeError("_qmv_torch.so is not built: call int4_group_quantized_gs64_gb300.build()")
+        loader = importlib.machinery.ExtensionFileLoader("_qmv_torch", _build.TORCH_LIB)
+        mod = importlib.util.module_from_spec(importlib.util.spec_from_loader("_qmv_torch", loader))
+        loader.exec_module(mod)
+        L = lib()
+        mod.init(QmvError, *(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
+            "attn_rope_append", "attn_tree", "attn_tree_workspace_bytes", "attn_evict")))
+        _torch_mod = mod
+    return _torch_mod
+
 
 class AttnCache:
     """A paged key/value cache of one layer: k and v [pages][Hkv][page][D], bf16 or fp16."""
@@ -508,13 +530,15 @@ class AttnCache:
             raise ValueError("k and v must both be [pages][Hkv][page][D]")
         self.k, self.v = k, v
         self.pages, self.Hkv, self.page, self.D = k.shape
-        self.slots = self.pages * self.Hkv * self.page
         self.dtype, self.device, self.device_index = k.dtype, k.device, k.get_device()
-        self.qmv_dtype = 1 if k.dtype == torch.bfloat16 else 2
+        self.scale = self.D ** -0.5
         self._desc = AttnCacheDesc(k.data_ptr(), v.data_ptr(), self.pages, self.Hkv, self.page,
-                                   self.D, self.qmv_dtype)
-        self.desc = ctypes.byref(self._desc)
-        self.kinds = {torch.float32: 0, k.dtype: self.qmv_dtype}  # what inputs and outputs may be
+                                   self.D, 1 if k.dtype == torch.bfloat16 else 2)
+        self.address = ctypes.addressof(self._desc)
+
+    @property
+    def desc(self):
+        return ctypes.byref(self._desc)
 
     @classmethod
     def empty(cls, pages: int, Hkv: int, page: int, D: int, dtype=None, device="cuda"):
@@ -523,52 +547,11 @@ class AttnCache:
         return cls(k, torch.empty_like(k))
 
 
-def _stream_of(stream, device_index):
-    """The raw handle of `stream`, or of the current stream of the device."""
+def _on(stream, shape, dtype, device):
+    """An output or scratch tensor that belongs to `stream`."""
     import torch
-    if stream is not None:
-        return stream.cuda_stream
-    try:
-        return torch._C._cuda_getCurrentRawStream(device_index)
-    except AttributeError:  # (the same, some microseconds slower)
-        return torch.cuda.current_stream(device_index).cuda_stream
-
-
-def _empty(shape, dtype, device, stream):
-    """An output or scratch tensor that belongs to the stream the call runs on."""
-    import torch
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _addr(t, dtype, numel, name):
-    """The address of a contiguous CUDA tensor of `numel` elements."""
-    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
-        _need(t, dtype, name)
-    if t.numel() != numel:
-        raise ValueError(f"{name} must have {numel} elements, got {t.numel()}")
-    return t.data_ptr()
-
-
-def _token_stride(t, name, n, heads, D):
-    """t [n][heads][D] with a token's heads contiguous: the elements between tokens."""
-    if t.shape != (n, heads, D):
-        raise ValueError(f"{name} must be [{n}][{heads}][{D}], got {tuple(t.shape)}")
-    a, b, c = t.stride()
-    if not t.is_cuda or (c != 1 and D > 1) or (b != D and heads > 1):
-        raise ValueError(f"{name} must be on the GPU with a token's heads contiguous")
-    return a if n > 1 else heads * D
-
-
-def _batch(table, name):
-    import torch
-    if table.dtype is not torch.int32 or not table.is_cuda or not table.is_contiguous():
-        _need(table, torch.int32, name)
-    if table.dim() != 2:
-        raise ValueError(f"{name} must be [B][max_pages]")
-    return table.shape
 
 
 def attn_rope_append(cache: AttnCache, q, k, v, pos, inv_freq, table, ctx, cu,
@@ -579,29 +562,14 @@ def attn_rope_append(cache: AttnCache, q, k, v, pos, inv_freq, table, ctx, cu,
     q [N][Hq][D], k and v [N][Hkv][D] in fp32 or the cache's type (rows may be strided);
     pos int32 [N]; inv_freq float64 [rot/2]; table int32 [B][max_pages]; ctx int32 [B];
     cu int32 [B+1]. acc (fp32 [pages][Hkv][page]) is cleared for the new tokens."""
-    import torch
-    dt, i32, D, Hkv = q.dtype, torch.int32, cache.D, cache.Hkv
-    kind = cache.kinds.get(dt)
-    if kind is None or k.dtype is not dt or v.dtype is not dt:
-        raise TypeError(f"q, k and v must all be float32 or all {cache.dtype}")
-    N, Hq = q.shape[0], q.shape[1]
-    B, max_pages = _batch(table, "table")
-    half = inv_freq.numel()
-    if q_out is None:
-        q_out = _empty((N, Hq, D), cache.dtype, cache.device, stream)
-    r = (_lib or lib()).attn_rope_append(
-        cache.desc, q.data_ptr(), _token_stride(q, "q", N, Hq, D),
-        k.data_ptr(), _token_stride(k, "k", N, Hkv, D),
-        v.data_ptr(), _token_stride(v, "v", N, Hkv, D), kind, Hq, _addr(pos, i32, N, "pos"),
-        _addr(inv_freq, torch.float64, half, "inv_freq"), 2 * half, 1 if interleaved else 0, mscale,
-        table.data_ptr(), max_pages, _addr(ctx, i32, B, "ctx"), _addr(cu, i32, B + 1, "cu"), B, N,
-        _addr(q_out, cache.dtype, N * Hq * D, "q_out"),
-        None if acc is None else _addr(acc, torch.float32, cache.slots, "acc"),
-        None if status is None else _addr(status, i32, 1, "status"),
-        _stream_of(stream, cache.device_index))
-    if r:
-        _check("attn_rope_append", r)
-    return q_out
+    handle = None
+    if stream is not None:
+        handle = stream.cuda_stream
+        if q_out is None:
+            q_out = _on(stream, q.shape, cache.dtype, cache.device)
+    return (_torch_mod or _torch_binding()).rope_append(
+        cache.address, cache.device_index, q, k, v, pos, inv_freq, table, ctx, cu, interleaved,
+        mscale, q_out, acc, status, handle)
 
 
 def attn_tree_workspace_bytes(cache: AttnCache, Hq: int, B: int, N: int, max_draft: int,
@@ -619,44 +587,29 @@ def attn_tree(cache: AttnCache, q, table, ctx, cu, max_draft: int, mask=None, sc
     it sees draft d of its sequence (None: drafts 0..itself); scale defaults to D ** -0.5;
     o_dtype the cache's (default) or float32. acc / acc_out (fp32 [pages][Hkv][page]):
     acc_out = decay * acc + this call's attention weights; acc alone is updated in place."""
+    if acc_out is None:
+        acc_out = acc
     import torch
-    i32, f32, D = torch.int32, torch.float32, cache.D
-    if q.dtype is not cache.dtype:
-        raise TypeError(f"q must be {cache.dtype}, got {q.dtype}")
-    N, Hq = q.shape[0], q.shape[1]
-    B, max_pages = _batch(table, "table")
-    words = 0
-    if mask is not None:
-        words = mask.shape[1]
-    acc_p = out_p = None
-    if acc is not None:
-        acc_p = out_p = _addr(acc, f32, cache.slots, "acc")
-    if acc_out is not None:
-        out_p = _addr(acc_out, f32, cache.slots, "acc_out")
-    odt = o_dtype or (cache.dtype if o is None else o.dtype)
-    kind = cache.kinds.get(odt)
-    if kind is None:
+    if o_dtype is None:
+        o_dtype = cache.dtype if o is None else o.dtype
+    elif o_dtype not in (torch.float32, cache.dtype):
         raise TypeError(f"o must be float32 or {cache.dtype}")
-    if o is None:
-        o = _empty((N, Hq, D), odt, cache.device, stream)
-    if lse is None:
-        lse = _empty((N, Hq), f32, cache.device, stream)
-    if ws is None:
-        ws = _empty(max(256, attn_tree_workspace_bytes(cache, Hq, B, N, max_draft, max_pages,
-                                                       out_p is not None)),
-                    torch.uint8, cache.device, stream)
-    r = (_lib or lib()).attn_tree(
-        cache.desc, q.data_ptr(), _token_stride(q, "q", N, Hq, D), Hq, table.data_ptr(), max_pages,
-        _addr(ctx, i32, B, "ctx"), _addr(cu, i32, B + 1, "cu"), B, N, max_draft,
-        None if mask is None else _addr(mask, i32, N * words, "mask"), words,
-        D ** -0.5 if scale is None else scale, _addr(o, odt, N * Hq * D, "o"), kind,
-        _addr(lse, f32, N * Hq, "lse"), acc_p, out_p, decay,
-        None if status is None else _addr(status, i32, 1, "status"),
-        _addr(ws, torch.uint8, ws.numel(), "ws"), ws.numel(),
-        _stream_of(stream, cache.device_index))
-    if r:
-        _check("attn_tree", r)
-    return o, lse
+    handle = None
+    if stream is not None:
+        handle = stream.cuda_stream
+        N, Hq = q.shape[0], q.shape[1]
+        if o is None:
+            o = _on(stream, q.shape, o_dtype, cache.device)
+        if lse is None:
+            lse = _on(stream, (N, Hq), torch.float32, cache.device)
+        if ws is None:
+            ws = _on(stream, max(256, attn_tree_workspace_bytes(
+                cache, Hq, table.shape[0], N, max_draft, table.shape[1], acc_out is not None)),
+                torch.uint8, cache.device)
+    return (_torch_mod or _torch_binding()).tree(
+        cache.address, cache.device_index, q, table, ctx, cu, max_draft, mask,
+        cache.scale if scale is None else scale, o, o_dtype is torch.float32, lse, acc, acc_out,
+        decay, ws, status, handle)
 
 
 def attn_evict(src: AttnCache, acc, table, lens, budget: int, dst: AttnCache, dst_acc, dst_table,
@@ -664,24 +617,15 @@ def attn_evict(src: AttnCache, acc, table, lens, budget: int, dst: AttnCache, ds
     """Keeps `budget` tokens a sequence and head by accumulated weight, copied to dst's pages.
 
     Returns (keep int32 [B][Hkv][budget], new_lens int32 [B])."""
-    import torch
-    i32, f32 = torch.int32, torch.float32
-    B, max_pages = _batch(table, "table")
-    Bd, dst_max_pages = _batch(dst_table, "dst_table")
-    if Bd != B:
-        raise ValueError("table and dst_table must have as many rows")
-    n = max(budget, 0)
-    if keep is None:
-        keep = _empty((B, src.Hkv, n), i32, src.device, stream)
-    if new_lens is None:
-        new_lens = _empty((B,), i32, src.device, stream)
-    r = (_lib or lib()).attn_evict(
-        src.desc, _addr(acc, f32, src.slots, "acc"), table.data_ptr(), max_pages,
-        _addr(lens, i32, B, "lens"), B, budget, sink, recent, dst.desc,
-        _addr(dst_acc, f32, dst.slots, "dst_acc"), dst_table.data_ptr(), dst_max_pages,
-        _addr(keep, i32, B * src.Hkv * n, "keep"), _addr(new_lens, i32, B, "new_lens"),
-        None if status is None else _addr(status, i32, 1, "status"),
-        _stream_of(stream, src.device_index))
-    if r:
-        _check("attn_evict", r)
-    return keep, new_lens
+    handle = None
+    if stream is not None:
+        import torch
+        handle = stream.cuda_stream
+        B = table.shape[0]
+        if keep is None:
+            keep = _on(stream, (B, src.Hkv, max(budget, 0)), torch.int32, src.device)
+        if new_lens is None:
+            new_lens = _on(stream, (B,), torch.int32, src.device)
+    return (_torch_mod or _torch_binding()).evict(
+        src.address, src.device_index, acc, table, lens, budget, dst.address, dst_acc, dst_table,
+        sink, recent, keep, new_lens, status, handle)

@@ -185,6 +185,10 @@ __device__ __forceinline__ float *part_at(const TreeArgs &a, int block, int last
            (((long long)block * 2 + last) * (D / 4) + (col >> 2)) * (a.rows * 4LL) + r * 4;
 }
 
+// A pool as a tensor map (128 bytes, row, 128-byte chunk of a row), boxes of
+// box_rows rows of one chunk, or of all (chunks), 128-byte swizzle.
+bool encode_pool(CUtensorMap *map, const void *pool, const AttnCache &c, int box_rows, bool all_chunks);
+
 // The scores of 16 keys from `slot` (a multiple of 16): [max_rows][16].
 __device__ __forceinline__ float *stash_at(const TreeArgs &a, int b, int h, int slot) {
     const long long slices = ((long long)a.s.max_pages << a.s.lpage) >> 4;

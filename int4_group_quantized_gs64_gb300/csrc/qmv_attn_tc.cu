@@ -32,7 +32,7 @@
 #include "qmv_attn.cuh"
 #include "qmv_attn.h"
 #include "qmv_attn_plan.cuh"
-#include "qmv_internal.h"
+#include "qmv_attn_tc05.cuh"
 #include "qmv_launch.cuh"
 
 namespace qmv {
@@ -628,19 +628,12 @@ cudaError_t run_tc(const CUtensorMap &km, const CUtensorMap &vm, const TreeArgs 
     return e;
 }
 
-// A pool as a tensor map (128 bytes, row, 128-byte chunk), boxes of one chunk
-// of box_rows rows, 128-byte swizzle.
-bool encode_chunks(CUtensorMap *map, const void *base, long long rows, int D, int box_rows) {
-    return encode_rows_swizzled(map, static_cast<const uint8_t *>(base), rows, D * 2, box_rows, 1);
-}
-
 }  // namespace
 
 cudaError_t launch_tree_tc(const AttnCache &c, const TreeArgs &a, cudaStream_t st) {
     CUtensorMap km, vm;
-    const long long rows = (long long)c.pages * c.Hkv * c.page;
     const int box = c.page < kKeys ? c.page : kKeys;
-    if (!encode_chunks(&km, c.k, rows, c.D, box) || !encode_chunks(&vm, c.v, rows, c.D, box))
+    if (!encode_pool(&km, c.k, c, box, false) || !encode_pool(&vm, c.v, c, box, false))
         return cudaErrorNotSupported;
     if (c.D == 64)
         return c.bf16 ? run_tc<64, true>(km, vm, a, st) : run_tc<64, false>(km, vm, a, st);

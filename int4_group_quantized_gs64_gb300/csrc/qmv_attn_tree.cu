@@ -15,13 +15,15 @@
 // is a segment; a segment that is not the whole item leaves its unnormalised
 // sum, maximum and sum of exponentials in the workspace, and k_attn_join adds
 // them up in key order (the same order every time).
+#include <cudaTypedefs.h>
 #include <math.h>
 #include <string.h>
+
+#include <mutex>
 
 #include "qmv_attn.cuh"
 #include "qmv_attn.h"
 #include "qmv_attn_plan.cuh"
-#include "qmv_internal.h"
 #include "qmv_launch.cuh"
 
 namespace qmv {
@@ -553,12 +555,40 @@ cudaError_t run_tree(const AttnCache &c, const CUtensorMap &km, const CUtensorMa
 int tree_rows(int max_rows) {
     return max_rows <= 16 ? 16 : max_rows <= 32 ? 32 : max_rows <= 128 ? 128 : 256;
 }
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static std::once_flag once;
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                             &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    return fn;
+}
+
 int tree_grid_max(int rows) { return sm_count() * (rows == 16 ? 2 : 1); }
 
 }  // namespace
 }  // namespace attn
 
 namespace attn {
+
+bool encode_pool(CUtensorMap *map, const void *pool, const AttnCache &c, int box_rows, bool all_chunks) {
+    auto enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t row = (cuuint64_t)c.D * 2, chunks = row / 128;
+    cuuint64_t dims[3] = {128, (cuuint64_t)c.pages * c.Hkv * c.page, chunks};
+    cuuint64_t strides[2] = {row, 128};
+    cuuint32_t box[3] = {128, (cuuint32_t)box_rows, all_chunks ? (cuuint32_t)chunks : 1u};
+    cuuint32_t es[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(pool), dims, strides, box,
+               es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 namespace {
 
 // Where the weights come from with up to 32 rows: scores that the attention
@@ -620,9 +650,7 @@ cudaError_t launch_attn_tree(const AttnCache &c, const TreeCall &t, cudaStream_t
     if (a.acc_out && stash_bytes(c, max_rows, t.s.B, t.s.max_pages))
         a.stash = reinterpret_cast<float *>(static_cast<char *>(t.ws) + part_bytes(c, a.rows));
     CUtensorMap km, vm;
-    const long long rows = (long long)c.pages * c.Hkv * c.page;
-    if (!encode_rows_swizzled(&km, static_cast<const uint8_t *>(c.k), rows, c.D * 2, 16) ||
-        !encode_rows_swizzled(&vm, static_cast<const uint8_t *>(c.v), rows, c.D * 2, 16))
+    if (!encode_pool(&km, c.k, c, 16, true) || !encode_pool(&vm, c.v, c, 16, true))
         return cudaErrorNotSupported;
     if (c.D == 64)
         return c.bf16 ? run_tree<64, true>(c, km, vm, a, max_rows, st)

@@ -17,7 +17,7 @@
 #include "qmv_attn.cuh"
 #include "qmv_attn.h"
 #include "qmv_attn_plan.cuh"
-#include "qmv_internal.h"
+#include "qmv_attn_tc05.cuh"
 #include "qmv_launch.cuh"
 
 namespace qmv {
@@ -423,8 +423,7 @@ cudaError_t run(const AttnCache &c, const TreeArgs &a, int max_rows, cudaStream_
     int stages = (kSmemMax - kMisc - q_tiles * kTile) / kTile;
     if (stages > kStages) stages = kStages;
     CUtensorMap km;
-    if (!encode_rows_swizzled(&km, static_cast<const uint8_t *>(c.k), (long long)c.pages * c.Hkv * c.page,
-                              D * 2, c.page < kKeys ? c.page : kKeys, 1))
+    if (!encode_pool(&km, c.k, c, c.page < kKeys ? c.page : kKeys, false))
         return cudaErrorNotSupported;
     auto *k = k_weights_tc<D, kBf16>;
     cudaError_t e = set_smem(k, kSmemMax);

@@ -152,9 +152,8 @@ bool tma_dense_supported(const uint8_t *wq, const float *scales, int N, int K, i
 // row, 128-byte chunk), boxes of box_rows whole rows with the 128-byte
 // swizzle (in shared memory: [chunk][row][128 B], 16-byte units XOR-ed with
 // the row mod 8). row_bytes a multiple of 128, at most 32768.
-// box_chunks: the 128-byte chunks of a row that one copy brings (0: all).
 bool encode_rows_swizzled(CUtensorMap *map, const uint8_t *base, long long rows, int row_bytes,
-                          int box_rows, int box_chunks = 0);
+                          int box_rows);
 // wq2 != null: a second matrix [N2][K/2] against the same activations, its
 // row tiles after the first's in the same launch, output y2 [S][N2].
 cudaError_t launch_dense_tma(const uint8_t *wq, const float *scales, int N, int K, int S,
