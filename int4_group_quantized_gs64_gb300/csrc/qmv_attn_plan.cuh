@@ -46,10 +46,26 @@ __device__ __forceinline__ int key_units(const Seq &q, int unit) {
 }
 
 // All items' units, and those before sequence `upto`. A thread of the block
-// handles ceil(B / threads) sequences; sh: two long longs a warp.
+// handles ceil(B / threads) sequences (up to 32 of them: each warp for itself);
+// sh: two long longs a warp.
 template <int kThreads>
 __device__ __forceinline__ long long count_units(const TreeArgs &a, int upto, long long *sh,
                                                  long long &before) {
+    if (a.s.B <= 32) {
+        const int lane = threadIdx.x & 31;
+        bool ok = false;
+        Seq q;
+        q.ctx = q.first = q.T = 0;
+        if (lane < a.s.B) q = get_seq(a.s, lane, ok);
+        long long n = q.T > 0 ? (long long)key_units(q, a.unit) * row_blocks(q, a.G, a.rows) * a.Hkv : 0;
+        before = lane < upto ? n : 0;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
+            before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
+        }
+        return n;
+    }
     const int per = (a.s.B + kThreads - 1) / kThreads;
     long long n = 0, nb = 0;
 #pragma unroll 1
@@ -96,9 +112,33 @@ struct ShareScratch {
 };
 
 // Each thread of the block counts ceil(B / threads) sequences in a row; the
-// one whose units hold u0 says where they start.
+// one whose units hold u0 says where they start. Up to 32 sequences each warp
+// counts for itself, which saves two barriers.
 template <int kThreads>
 __device__ __forceinline__ Share find_share(const TreeArgs &a, ShareScratch<kThreads / 32> *sh) {
+    if (a.s.B <= 32) {
+        const int lane = threadIdx.x & 31;
+        bool ok = false;
+        Seq q;
+        q.ctx = q.first = q.T = 0;
+        if (lane < a.s.B) q = get_seq(a.s, lane, ok);
+        const long long n =
+            q.T > 0 ? (long long)key_units(q, a.unit) * row_blocks(q, a.G, a.rows) * a.Hkv : 0;
+        long long inc = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+            if (lane >= o) inc += v;
+        }
+        const long long total = __shfl_sync(0xFFFFFFFFu, inc, 31), quota = (total + a.grid - 1) / a.grid;
+        Share s;
+        s.u0 = quota * blockIdx.x;
+        s.u1 = min(s.u0 + quota, total);
+        const uint32_t who = __ballot_sync(0xFFFFFFFFu, inc > s.u0);
+        s.b = who ? __ffs(who) - 1 : 0;
+        s.rest = s.u0 - __shfl_sync(0xFFFFFFFFu, inc - n, s.b);
+        return s;
+    }
     const int per = (a.s.B + kThreads - 1) / kThreads, b0 = threadIdx.x * per;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     auto units = [&](int b) -> long long {

@@ -14,12 +14,12 @@
 //                both have the same row on the same lane);
 //   rows  > 128: two tiles of 128 rows against the same key tiles.
 // Warps: 0-3 and 4-7 the streams' softmax (a thread a row: maximum and sum
-// need no exchange), 8 the copies, 9 and 10 the streams' products (11 only fills
-// up their warpgroup, which passes registers on to the softmax warps: their 128
-// scores stay in registers, since reading them from tensor memory twice would
-// cost as much as the products). A ring of 128-key tiles
-// holds keys and values in the order in which the products use them, across
-// segments. The running maximum moves only when it grows by more than 2^8 (a
+// need no exchange), 8 the copies, 9 and 10 the streams' products, 11 brings the
+// next segment's queries to L2. These four need few registers and pass the rest
+// on to the softmax warps, whose 128 scores stay in registers: reading them from
+// tensor memory twice would cost as much as the products. A ring of 128-key
+// tiles holds keys and values in the order in which the products use them,
+// across segments. The running maximum moves only when it grows by more than 2^8 (a
 // row's weights may then exceed 1, which fp32 sums and 16-bit weights hold),
 // since moving it means rescaling O in tensor memory.
 //
@@ -50,6 +50,7 @@ struct Misc {
     uint64_t s_full[2], p_ready[2], o_full[2], q_full, fin[2], turn[2];
     uint32_t tmem, dead;
     int tiles;             // of the segment whose queries are ready
+    int segments;          // begun so far
     uint32_t nf[8];        // drafts with infinities or NaNs among their values
     float2 ml[2][128];
 };
@@ -110,17 +111,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     Misc *m = reinterpret_cast<Misc *>(ring + stages * kTile);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (blockIdx.x == 0 && a.status) {
-        for (int b = threadIdx.x; b < a.s.B; b += kThreads) {
-            bool ok;
-            get_seq(a.s, b, ok);
-            if (!ok) set_status(a.status, kStLength);
-        }
-    }
-    const Share sh = find_share<kThreads>(a, &m->share);
-    if (sh.u0 >= sh.u1) return;
     if (threadIdx.x == 0) {
         for (int i = 0; i < stages; ++i) {
             tc05::mbar_init(m->full + i, 1);
@@ -135,10 +125,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc05::mbar_init(&m->q_full, 256);
         m->dead = 0;
+        m->segments = 0;
         tc05::fence_mbar_init();
         prefetch_tmap(&kmap);
         prefetch_tmap(&vmap);
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (blockIdx.x == 0 && a.status) {
+        for (int b = threadIdx.x; b < a.s.B; b += kThreads) {
+            bool ok;
+            get_seq(a.s, b, ok);
+            if (!ok) set_status(a.status, kStLength);
+        }
+    }
+    const Share sh = find_share<kThreads>(a, &m->share);
+    if (sh.u0 >= sh.u1) return;
     if (warp == 9) tc05::tmem_alloc(&m->tmem, 512);
     tc05::fence_before_sync();
     __syncthreads();
@@ -264,8 +266,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (t > t0) {
                         const int tv = t - kStep;
                         go(min(tv + lag, n) + tv);
-                        live = wait(m->full + stage, ring_ph, m, a.status) &&
-                               wait(m->p_ready + s, pp, m, a.status);
+                        // The weights first: with alternate tiles the slot's last
+                        // entry may be the other stream's, and a phase that is two
+                        // behind looks like the awaited one. Once tile tv has its
+                        // weights the other stream is past that entry (the turns).
+                        live = wait(m->p_ready + s, pp, m, a.status) &&
+                               wait(m->full + stage, ring_ph, m, a.status);
                         if (!live) break;
                         pp ^= 1u;
                         tc05::fence_after_sync();
@@ -304,6 +310,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc05::mbar_wait(m->fin + s, 0, kPoll);
         }
         __syncwarp();
+    } else {
+        // ------------------------------------------------------------ next queries to L2
+        Cursor c;
+        c.start(a, sh);
+        int started = 0;
+        for (int left = units;;) {
+            left -= Segment(c, left).n;
+            if (left <= 0) break;
+            // a segment ahead at most (a hint only: past the limit it just stops)
+            ++started;
+            volatile int *now = &m->segments;
+            uint32_t i = 0;
+            while (*now < started && ++i < kPoll / 64) __nanosleep(256);
+            if (*now < started) break;
+            c.next_item(a);
+            constexpr int kLines = D * 2 / 128;
+            const int r0 = c.rb * a.rows, n = min(a.rows, c.q.T * a.G - r0) * kLines;
+            for (int i = lane; i < n; i += 32) {
+                const int rr = r0 + i / kLines, t = rr / a.G;
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                    a.q + (long long)(c.q.first + t) * a.q_stride +
+                    (long long)(c.h * a.G + rr - t * a.G) * D + (i % kLines) * 64));
+            }
+        }
+        __syncwarp();
     }
     } else {
         // ------------------------------------------------------------ softmax
@@ -321,6 +352,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int len = q.ctx + q.T, nrows = q.T * a.G;
             const int32_t *trow = a.s.table + (long long)c.b * a.s.max_pages;
             const int ns = kTwo ? sg.n : (sg.n + 1 - s) / 2;  // this stream's tiles
+            // ---- pages that do not exist, among this segment's
+            bool bad = false;
+            {
+                const int p1 = (min(len, (sg.j0 + sg.n) * kKeys) + a.s.page - 1) >> a.s.lpage;
+#pragma unroll 1
+                for (int p = ((sg.j0 * kKeys) >> a.s.lpage) + (threadIdx.x & 255); p < p1; p += 256)
+                    bad |= (unsigned)trow[p] >= (unsigned)a.pages;
+            }
             // ---- queries to shared memory, rows in the products' order
             {
                 constexpr int kChunks = D / 8, kPass = 128 / kChunks;  // rows a pass of this warpgroup
@@ -345,17 +384,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             tc05::fence_proxy_async();
-            if (threadIdx.x == 0) m->tiles = sg.n;
-            mbar_arrive(&m->q_full);
-            // ---- pages that do not exist, among this segment's
-            bool bad = false;
-            {
-                const int p1 = (min(len, (sg.j0 + sg.n) * kKeys) + a.s.page - 1) >> a.s.lpage;
-#pragma unroll 1
-                for (int p = ((sg.j0 * kKeys) >> a.s.lpage) + (threadIdx.x & 255); p < p1; p += 256)
-                    bad |= (unsigned)trow[p] >= (unsigned)a.pages;
+            if (threadIdx.x == 0) {
+                m->tiles = sg.n;
+                *(volatile int *)&m->segments += 1;
             }
+            mbar_arrive(&m->q_full);
             if (threadIdx.x < 8) m->nf[threadIdx.x] = 0;
+            __syncwarp();
             bad = pair_or(bad);
 
             const int rbase = c.rb * a.rows + (kTwo ? s * 128 : 0);
@@ -367,12 +402,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < ns; ++i) {
                 const int tile = kTwo ? i : 2 * i + s, j = sg.j0 + tile;
                 const bool special = bad || (j + 1) * kKeys > q.ctx;
+                wait(m->s_full + s, sp, m, a.status);
+                __syncwarp();
+                sp ^= 1;
+                tc05::fence_after_sync();
+                // The streams take turns: left alone they fall into step, both
+                // at their exponentials and then both waiting for products.
+                // (Stream 0 goes first; a pass of the other's is due before
+                // each tile but its first.)
+                if (i > 0 || s > 0) {
+                    wait(m->turn + s, tp ^ (uint32_t)((s ? i : i - 1) & 1), m, a.status);
+                    __syncwarp();
+                }
                 if (special && (!kTwo || s == 0)) {
                     // Values that some row must not see are kept out of the
                     // product where zero times them is not zero: a thread a
                     // key, zeros past the end and where there is no page, and
                     // a draft's infinities and NaNs noted and replaced.
-                    // (two ring entries a tile of the segments before)
+                    // (Two ring entries a tile of the segments before; in its
+                    // turn, since then the slot's last entry has been used.)
                     const long long pos = 2LL * (units - left) + min(tile + lag, sg.n) + tile;
                     const int vst = (int)(pos % stages);
                     if (wait(m->full + vst, (uint32_t)(pos / stages) & 1u, m, a.status)) {
@@ -403,18 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     tc05::fence_proxy_async();
                 }
-                wait(m->s_full + s, sp, m, a.status);
                 __syncwarp();
-                sp ^= 1;
-                tc05::fence_after_sync();
-                // The streams take turns: left alone they fall into step, both
-                // at their exponentials and then both waiting for products.
-                // (Stream 0 goes first; a pass of the other's is due before
-                // each tile but its first.)
-                if (i > 0 || s > 0) {
-                    wait(m->turn + s, tp ^ (uint32_t)((s ? i : i - 1) & 1), m, a.status);
-                    __syncwarp();
-                }
                 if (warp_live) {
                     if (special) {  // scores that a row must not see become -inf
                         uint32_t see[4];
@@ -513,6 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 wait(m->o_full + s, op, m, a.status);
                 op ^= 1;
             }
+            __syncwarp();
             if (mx != -INFINITY) mx -= boost;
             m->ml[s][tid] = make_float2(mx, l);
             pair_sync();
@@ -537,6 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (int k = k0; k < k1; ++k) {  // 32 columns at a time
                     float o[32];
+                    __syncwarp();
                     tc05::tmem_ld32(to + (kTwo ? s * 128 : 0) + k * 32,
                                     *reinterpret_cast<uint32_t(*)[32]>(o));
                     tc05::tmem_wait_ld();
@@ -600,6 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             tc05::fence_before_sync();
+            __syncwarp();
             pair_sync();  // O, the queries and the tables may be overwritten
             // the other stream passed the turn once a tile of its own
             tp ^= (uint32_t)(kTwo ? sg.n : (sg.n + s) / 2) & 1u;

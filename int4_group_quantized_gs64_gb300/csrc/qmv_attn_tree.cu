@@ -76,9 +76,6 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? 2 : 1)
     int *flags = reinterpret_cast<int *>(bars + NW * kStages);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-
     if (threadIdx.x == 0) {
         prefetch_tmap(&kmap);
         prefetch_tmap(&vmap);
@@ -89,6 +86,9 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? 2 : 1)
         for (int i = 0; i < kStages; ++i) tc05::mbar_init(bar + i, 1);
         tc05::fence_mbar_init();
     }
+    __syncwarp();
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (blockIdx.x == 0 && a.status) {
         for (int b = threadIdx.x; b < a.s.B; b += 32 * NW) {
             bool ok;
@@ -442,64 +442,92 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? 2 : 1)
 // Adds up the segments of an item that several blocks shared, in key order,
 // kXb blocks' segments at a time (their loads in flight together). A warp takes
 // 8 rows: lane l has row l % 8 and every fourth group of 4 columns, kCols of
-// them (the rest of a row's columns are other warps').
-template <int D, int kCols, int kXb>
-__global__ void __launch_bounds__(128) k_attn_join(const TreeArgs a, bool bf16) {
+// them (the rest of a row's columns are other warps'). kSplit warps share a
+// long row of segments and meet in shared memory. The call's inputs are older
+// than its first kernel, so everything up to the segments is read before the
+// wait for it.
+template <int D, int kCols, int kXb, int kSplit>
+__global__ void __launch_bounds__(128 * kSplit) k_attn_join(const TreeArgs a, bool bf16) {
     constexpr int kParts = D / 16 / kCols;  // warps a row
-    __shared__ long long scan[8];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __shared__ long long scan[8 * kSplit];
+    __shared__ float meet[kSplit > 1 ? (kSplit - 1) * 128 * (kCols * 4 + 2) : 1];
     const int b = blockIdx.x / a.Hkv, h = blockIdx.x - b * a.Hkv, rb = blockIdx.y;
     bool ok;
     const Seq q = get_seq(a.s, b, ok);
     const int nu = key_units(q, a.unit), nrb = row_blocks(q, a.G, a.rows);
     long long before;
-    const long long total = count_units<128>(a, b, scan, before);
-    if (q.T == 0 || rb >= nrb) return;
+    const long long total = count_units<128 * kSplit>(a, b, scan, before);
     const long long quota = (total + a.grid - 1) / a.grid;
     const long long i0 = before + ((long long)h * nrb + rb) * nu, i1 = i0 + nu;
-    const int c0 = (int)(i0 / quota), c1 = (int)((i1 - 1) / quota);
-    if (c0 == c1) return;  // one segment: written by its block
+    const bool any = q.T > 0 && rb < nrb;
+    const int c0 = any ? (int)(i0 / quota) : 0, c1 = any ? (int)((i1 - 1) / quota) : 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (c0 == c1) return;  // nothing here, or one segment, written by its block
     const int rows = min(a.rows, q.T * a.G - rb * a.rows);
-    const int w = blockIdx.z * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int w = blockIdx.z * 4 + (warp & 3), split = warp >> 2;
     const int r = (w / kParts) * 8 + (lane & 7), col0 = (w % kParts) * (kCols * 16) + (lane >> 3) * 4;
-    if ((w / kParts) * 8 >= rows) return;
     const bool have_row = r < rows;
+    // this warp's stretch of the segments
+    const int per = (c1 - c0 + kSplit) / kSplit;
+    const int x_begin = c0 + split * per, x_end = min(c1 + 1, x_begin + per);
 
     float M = -INFINITY, L = 0.f, acc[kCols][4];
 #pragma unroll
     for (int i = 0; i < kCols; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
-    for (int x0 = c0; x0 <= c1; x0 += kXb) {
+    auto add = [&](float m, float l, const float (&v)[kCols][4]) {
+        const float mn = fmaxf(M, m);
+        const float f0 = M == mn ? 1.f : ex2(M - mn), f1 = m == mn ? 1.f : ex2(m - mn);
+        M = mn;
+        L = L * f0 + l * f1;
+#pragma unroll
+        for (int i = 0; i < kCols; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][e] = acc[i][e] * f0 + v[i][e] * f1;
+    };
+    for (int x0 = x_begin; x0 < x_end; x0 += kXb) {
         float2 ml[kXb];
-        float4 v[kXb][kCols];
+        float v[kXb][kCols][4];
 #pragma unroll
         for (int j = 0; j < kXb; ++j) {
             const int x = x0 + j, last = (long long)x * quota >= i0 ? 0 : 1;
-            const bool have = x <= c1 && have_row;
+            const bool have = x < x_end && have_row;
             ml[j] = have ? *reinterpret_cast<const float2 *>(
                                a.part_ml + (((long long)x * 2 + last) * a.rows + r) * 2)
                          : make_float2(-INFINITY, 0.f);
 #pragma unroll
-            for (int i = 0; i < kCols; ++i)
-                v[j][i] = have ? *reinterpret_cast<const float4 *>(part_at<D>(a, x, last, r, col0 + 16 * i))
-                               : make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int i = 0; i < kCols; ++i) {
+                const float4 f = have ? *reinterpret_cast<const float4 *>(
+                                            part_at<D>(a, x, last, r, col0 + 16 * i))
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
+                v[j][i][0] = f.x; v[j][i][1] = f.y; v[j][i][2] = f.z; v[j][i][3] = f.w;
+            }
         }
 #pragma unroll
-        for (int j = 0; j < kXb; ++j) {
-            const float mn = fmaxf(M, ml[j].x);
-            const float f0 = M == mn ? 1.f : ex2(M - mn);
-            const float f1 = ml[j].x == mn ? 1.f : ex2(ml[j].x - mn);
-            M = mn;
-            L = L * f0 + ml[j].y * f1;
+        for (int j = 0; j < kXb; ++j) add(ml[j].x, ml[j].y, v[j]);
+    }
+    if (kSplit > 1) {
+        constexpr int kWords = kCols * 4 + 2;
+        const int at = threadIdx.x & 127;
+        if (split > 0) {
+            float *p = meet + (split - 1) * 128 * kWords + at;
+            p[0] = M;
+            p[128] = L;
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) {
-                acc[i][0] = acc[i][0] * f0 + v[j][i].x * f1;
-                acc[i][1] = acc[i][1] * f0 + v[j][i].y * f1;
-                acc[i][2] = acc[i][2] * f0 + v[j][i].z * f1;
-                acc[i][3] = acc[i][3] * f0 + v[j][i].w * f1;
-            }
+            for (int i = 0; i < kCols * 4; ++i) p[(2 + i) * 128] = acc[i >> 2][i & 3];
+        }
+        __syncthreads();
+        if (split > 0) return;
+#pragma unroll
+        for (int k = 0; k < kSplit - 1; ++k) {
+            const float *p = meet + k * 128 * kWords + at;
+            float v[kCols][4];
+#pragma unroll
+            for (int i = 0; i < kCols * 4; ++i) v[i >> 2][i & 3] = p[(2 + i) * 128];
+            add(p[0], p[128], v);
         }
     }
     if (!have_row) return;
@@ -539,14 +567,16 @@ cudaError_t run_tree(const AttnCache &c, const CUtensorMap &km, const CUtensorMa
                     : a.rows == 32 ? run_rows<D, 2, 8, kBf16>(km, vm, a, st)
                                    : launch_tree_tc(c, a, st);
     const int nrb = (max_rows + a.rows - 1) / a.rows;
-    // many rows: a warp 8 of them whole, two blocks' segments at a time; few
-    // rows (and so more blocks an item): a warp a quarter of 8 rows, eight
-    const bool many = a.rows > 32;
+    // many rows: a warp 8 of them whole, two blocks' segments at a time; few rows:
+    // a warp a part of 8 rows, four warps sharing the blocks' segments where items
+    // are so few that each has many (8 items of 38 segments: 10.8 -> 5.8 us)
+    const bool many = a.rows > 32, longs = a.grid > 8 * a.s.B * a.Hkv * nrb;
     const int warps = ((max_rows < a.rows ? max_rows : a.rows) + 7) / 8 * (many ? 1 : D / 32);
-    const int rz = (warps + 3) / 4;
-    auto *join = many ? k_attn_join<D, D / 16, 2> : k_attn_join<D, 2, 8>;
+    const dim3 grid(a.s.B * a.Hkv, nrb, (warps + 3) / 4);
     if (e == cudaSuccess)
-        e = launch(join, dim3(a.s.B * a.Hkv, nrb, rz), dim3(128), 0, st, true, a, (bool)kBf16);
+        e = many ? launch(k_attn_join<D, D / 16, 2, 1>, grid, dim3(128), 0, st, true, a, (bool)kBf16)
+            : longs ? launch(k_attn_join<D, 2, 5, 4>, grid, dim3(512), 0, st, true, a, (bool)kBf16)
+                    : launch(k_attn_join<D, 2, 8, 1>, grid, dim3(128), 0, st, true, a, (bool)kBf16);
     if (e == cudaSuccess && a.acc_out) e = launch_tree_weights(c, a, max_rows, st);
     return e;
 }

@@ -9,8 +9,7 @@
 //   33 .. 512     k_weights_tc forms the scores again (2 D bytes a key), keys as
 //                 the rows of the tcgen05 product, so that a thread has one key
 //                 and sums its own columns: S^T = K Q^T, all R queries resident
-//                 in shared memory while the keys stream by once. Tiles with
-//                 drafts in them are left to k_weights_any.
+//                 in shared memory while the keys stream by once.
 //   otherwise     k_weights_any, on the warp MMA: any rows, any masks.
 #include <string.h>
 
@@ -26,47 +25,75 @@ namespace {
 
 // ------------------------------------------------------------------ from kept scores
 
-__global__ void __launch_bounds__(256) k_weights_stash(const TreeArgs a) {
+// A thread takes four keys. vec: the sums lie on 16-byte boundaries.
+__global__ void __launch_bounds__(256) k_weights_stash(const TreeArgs a, bool vec) {
     __shared__ float e2[32];
+    const int b = blockIdx.z, h = blockIdx.y, slot = (blockIdx.x * 256 + threadIdx.x) * 4;
+    bool ok;
+    const Seq q = get_seq(a.s, b, ok);  // (a call's inputs are older than its first kernel)
+    const int len = q.ctx + q.T, nrows = q.T * a.G;
+    const bool any = q.T > 0 && blockIdx.x * 1024 < len;
+    int pid = -1;
+    if (any && slot < len) pid = a.s.table[(long long)b * a.s.max_pages + (slot >> a.s.lpage)];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int b = blockIdx.z, h = blockIdx.y, slot = blockIdx.x * 256 + threadIdx.x;
-    bool ok;
-    const Seq q = get_seq(a.s, b, ok);
-    const int len = q.ctx + q.T, nrows = q.T * a.G;
-    if (q.T == 0 || blockIdx.x * 256 >= len) return;
+    if (!any) return;
     if (threadIdx.x < nrows) {
         const int t = threadIdx.x / a.G;
         e2[threadIdx.x] =
             a.lse[(long long)(q.first + t) * a.Hq + h * a.G + threadIdx.x - t * a.G] * kLog2e;
     }
     __syncthreads();
-    if (slot >= len) return;
-    const int pid = a.s.table[(long long)b * a.s.max_pages + (slot >> a.s.lpage)];
     if ((unsigned)pid >= (unsigned)a.pages) return;
     const long long at = ((long long)pid * a.Hkv + h) * a.s.page + (slot & (a.s.page - 1));
-    const float old = a.acc_in ? a.decay * a.acc_in[at] : 0.f;
     const float *p = stash_at(a, b, h, slot & ~15) + (slot & 15);
-    float w = 0.f;
-    for (int r0 = 0; r0 < nrows; r0 += 8) {
-        float x[8];
+    const int n = min(4, len - slot);
+    const bool whole = vec && n == 4;
+    float old[4] = {0.f, 0.f, 0.f, 0.f};
+    if (a.acc_in) {
+        if (whole) {
+            const float4 f = *reinterpret_cast<const float4 *>(a.acc_in + at);
+            old[0] = f.x; old[1] = f.y; old[2] = f.z; old[3] = f.w;
+        } else {
 #pragma unroll
-        for (int r = 0; r < 8; ++r) x[r] = r0 + r < nrows ? __ldcs(p + (r0 + r) * 16) : 0.f;
+            for (int e = 0; e < 4; ++e)
+                if (e < n) old[e] = a.acc_in[at + e];
+        }
+    }
+    float w[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int r0 = 0; r0 < nrows; r0 += 8) {
+        float4 x[8];
 #pragma unroll
         for (int r = 0; r < 8; ++r)
-            if (r0 + r < nrows && e2[r0 + r] != -INFINITY)
-                w += ex2(fmaf(x[r], a.sl2, -e2[r0 + r]));
+            x[r] = r0 + r < nrows ? __ldcs(reinterpret_cast<const float4 *>(p + (r0 + r) * 16))
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+            if (r0 + r < nrows && e2[r0 + r] != -INFINITY) {
+                const float e = e2[r0 + r];
+                w[0] += ex2(fmaf(x[r].x, a.sl2, -e));
+                w[1] += ex2(fmaf(x[r].y, a.sl2, -e));
+                w[2] += ex2(fmaf(x[r].z, a.sl2, -e));
+                w[3] += ex2(fmaf(x[r].w, a.sl2, -e));
+            }
     }
-    a.acc_out[at] = old + w;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] += a.decay * old[e];
+    if (whole) {
+        *reinterpret_cast<float4 *>(a.acc_out + at) = make_float4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e < n) a.acc_out[at + e] = w[e];
+    }
 }
 
 // ------------------------------------------------------------------ any rows, any masks
 
 // Eight warps share 16 keys: each walks every eighth block of 16 rows, and
-// their sums meet in shared memory. from_drafts: only the slots from the last
-// multiple of 128 at or before ctx on.
+// their sums meet in shared memory.
 template <int D, bool kBf16>
-__global__ void __launch_bounds__(256) k_weights_any(const TreeArgs a, bool from_drafts) {
+__global__ void __launch_bounds__(256) k_weights_any(const TreeArgs a) {
     __shared__ float sums[8][16];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -74,7 +101,7 @@ __global__ void __launch_bounds__(256) k_weights_any(const TreeArgs a, bool from
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     bool ok;
     const Seq q = get_seq(a.s, b, ok);
-    const int len = q.ctx + q.T, s0 = (from_drafts ? q.ctx & ~127 : 0) + blockIdx.x * 16;
+    const int len = q.ctx + q.T, s0 = blockIdx.x * 16;
     if (q.T == 0 || s0 >= len) return;
     const int pid = a.s.table[(long long)b * a.s.max_pages + (s0 >> a.s.lpage)];
     if ((unsigned)pid >= (unsigned)a.pages) return;
@@ -156,8 +183,9 @@ struct Misc {
     uint32_t tmem, dead;
     int tiles, row_tiles;
     float nlse[kMaxRows];  // -lse in log2 units; -inf where a row has no weights
+    uint32_t seen[2][8][128];  // of a tile with drafts: the drafts that see each key
 };
-constexpr int kMisc = 3072;
+constexpr int kMisc = 11264;
 static_assert(sizeof(Misc) <= kMisc, "");
 
 __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, Misc *m, int32_t *status) {
@@ -186,10 +214,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *qs = smem, *ring = smem + q_tiles * kTile;
     Misc *m = reinterpret_cast<Misc *>(ring + stages * kTile);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // A call's inputs are older than its first kernel: only lse and the sums
+    // have to wait for the kernels before.
     const Share sh = find_share<kThreads>(a, &m->share);
-    if (sh.u0 >= sh.u1) return;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (sh.u0 >= sh.u1) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
+    }
     if (threadIdx.x == 0) {
         for (int i = 0; i < stages; ++i) {
             tc05::mbar_init(m->full + i, 1);
@@ -302,6 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         Cursor c;
         c.start(a, sh);
         int job0 = 0;
+        bool waited = false;
         const uint64_t sl2 = pack_f32x2(a.sl2, a.sl2);
         for (int left = units; left > 0;) {
             const Seq q = c.q;
@@ -330,6 +363,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                                    (v[i].z ^ a.qxor) & keep, (v[i].w ^ a.qxor) & keep);
                 }
             }
+            tc05::fence_proxy_async();
+            if (threadIdx.x == 0) {
+                m->tiles = n;
+                m->row_tiles = nq;
+            }
+            mbar_arrive(&m->q_full);
+            if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
+            waited = true;
             for (int r = threadIdx.x; r < nq * 128; r += 256) {
                 float e = -INFINITY;
                 if (r < nrows) {
@@ -339,23 +380,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 m->nlse[r] = e;
             }
-            tc05::fence_proxy_async();
-            if (threadIdx.x == 0) {
-                m->tiles = n;
-                m->row_tiles = nq;
-            }
-            mbar_arrive(&m->q_full);
+            __syncwarp();
             asm volatile("bar.sync 1, 256;" ::: "memory");
 #pragma unroll 1
             for (int t = s; t < n; t += 2) {
                 const int slot = (j0 + t) * kKeys + tid;
-                // tiles with drafts are another kernel's
-                const bool mine = (j0 + t + 1) * kKeys <= q.ctx;
+                const int d = slot - q.ctx;  // this key's draft (negative: seen by all)
+                const bool special = (j0 + t + 1) * kKeys > q.ctx;
                 int pid = -1;
-                if (mine) pid = __ldg(a.s.table + (long long)c.b * a.s.max_pages + (slot >> a.s.lpage));
+                if (slot < q.ctx + q.T) pid = __ldg(a.s.table + (long long)c.b * a.s.max_pages + (slot >> a.s.lpage));
                 const bool good = (unsigned)pid < (unsigned)a.pages;
                 const long long at = ((long long)pid * a.Hkv + c.h) * a.s.page + (slot & (a.s.page - 1));
                 const float old = good && a.acc_in ? a.decay * a.acc_in[at] : 0.f;
+                if (special) {  // which drafts see this key, as bits
+                    const bool all = d < 0 || !a.mask;
+#pragma unroll 1
+                    for (int w = 0; w < 8; ++w) {
+                        uint32_t bits = 0;
+                        for (int e = 0; e < 32 && w * 32 + e < q.T; ++e) {
+                            const int tt = w * 32 + e;
+                            const bool see = all ? d <= tt
+                                                 : d < q.T && ((__ldg(a.mask + (long long)(q.first + tt) * a.words +
+                                                                      (d >> 5)) >> (d & 31)) & 1u);
+                            bits |= (uint32_t)see << e;
+                        }
+                        m->seen[s][w][tid] = bits;
+                    }
+                    __syncwarp();
+                }
                 uint64_t sum[2] = {0, 0};
 #pragma unroll 1
                 for (int r = 0; r < nq; ++r) {
@@ -363,13 +415,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                     wait(m->s_full + buf, (job >> 2) & 1, m, a.status);
                     __syncwarp();
                     tc05::fence_after_sync();
+                    if (special) {  // scores of rows that do not see the key become -inf
+                        int tt = r * 128 / a.G, gg = r * 128 - tt * a.G;  // row's draft and head
+#pragma unroll 1
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t x[32];
+                            tc05::tmem_ld32(tmem + lanes + buf * 128 + k * 32, x);
+                            tc05::tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const uint32_t w = m->seen[s][(tt >> 5) & 7][tid];
+                                if (!((w >> (tt & 31)) & 1u)) x[e] = 0xFF800000u;
+                                if (++gg == a.G) {
+                                    gg = 0;
+                                    ++tt;
+                                }
+                            }
+                            tc05::tmem_st32(tmem + lanes + buf * 128 + k * 32, x);
+                        }
+                        tc05::tmem_wait_st();
+                    }
                     uint32_t x[2][32];
                     tc05::tmem_ld32(tmem + lanes + buf * 128, x[0]);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         tc05::tmem_wait_ld();
                         if (k < 3) tc05::tmem_ld32(tmem + lanes + buf * 128 + (k + 1) * 32, x[(k + 1) & 1]);
-                        if (!mine) continue;
                         const ulonglong2 *nl = reinterpret_cast<const ulonglong2 *>(m->nlse + r * 128 + k * 32);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
@@ -392,6 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     a.acc_out[at] = old + ((s0 + s1) + (s2 + s3));
                 }
             }
+            __syncwarp();
             asm volatile("bar.sync 1, 256;" ::: "memory");
             job0 += n * nq;
             left -= n;
@@ -408,11 +480,12 @@ template <int D, bool kBf16>
 cudaError_t run(const AttnCache &c, const TreeArgs &a, int max_rows, cudaStream_t st) {
     const long long most = (long long)a.s.max_pages << a.s.lpage;
     if (a.stash)
-        return launch(k_weights_stash, dim3((unsigned)((most + 255) / 256), a.Hkv, a.s.B), dim3(256), 0,
-                      st, true, a);
+        return launch(k_weights_stash, dim3((unsigned)((most + 1023) / 1024), a.Hkv, a.s.B), dim3(256),
+                      0, st, true, a,
+                      ((reinterpret_cast<uintptr_t>(a.acc_in) | reinterpret_cast<uintptr_t>(a.acc_out)) & 15) == 0);
     if (max_rows <= 32 || max_rows > kMaxRows)
         return launch(k_weights_any<D, kBf16>, dim3((unsigned)((most + 15) / 16), a.Hkv, a.s.B),
-                      dim3(256), 0, st, true, a, false);
+                      dim3(256), 0, st, true, a);
     constexpr int kTile = kKeys * D * 2;
     TreeArgs w = a;
     w.rows = 1 << 30;
@@ -429,10 +502,6 @@ cudaError_t run(const AttnCache &c, const TreeArgs &a, int max_rows, cudaStream_
     cudaError_t e = set_smem(k, kSmemMax);
     if (e == cudaSuccess)
         e = launch(k, dim3(w.grid), dim3(kThreads), kSmemMax, st, true, km, w, q_tiles, stages);
-    // slots ctx - ctx % 128 .. ctx + T - 1 of each sequence
-    const int tail = (127 + a.s.max_draft + 15) / 16;
-    if (e == cudaSuccess)
-        e = launch(k_weights_any<D, kBf16>, dim3(tail, a.Hkv, a.s.B), dim3(256), 0, st, true, a, true);
     return e;
 }
 

@@ -226,6 +226,55 @@ def test_tree_long_context_split_over_blocks():
         check_tree(c, o, lse, c.reference(s), p_rounding(c, s, F32))
 
 
+@pytest.mark.parametrize("D,page,G,T", [(128, 128, 5, 21), (128, 64, 5, 21), (128, 16, 8, 16),
+                                        (64, 128, 5, 21), (128, 128, 8, 40), (64, 32, 8, 40)])
+def test_tree_batches_bound_by_memory(D, page, G, T):
+    """Long contexts of many sequences: copies arrive late and rings run dry. Every
+    sequence's values are compared, on the GPU, in 64 bits."""
+    B, Hkv, n = 12, 8, 6000
+    g = torch.Generator(device="cuda").manual_seed(T)
+    ctx = [n - 211 * b for b in range(B)]
+    drafts = [T - b % 3 for b in range(B)]
+    need = [-(-(c + t) // page) for c, t in zip(ctx, drafts)]
+    k = torch.empty(sum(need), Hkv, page, D, dtype=BF, device="cuda").normal_(generator=g)
+    v = torch.empty_like(k).normal_(generator=g)
+    table = torch.zeros(B, max(need), dtype=torch.int32)
+    order = torch.randperm(sum(need), generator=torch.Generator().manual_seed(1)).int()
+    for b in range(B):
+        table[b, :need[b]] = order[sum(need[:b]):sum(need[:b + 1])]
+    cu = [0] + np.cumsum(drafts).tolist()
+    qq = torch.empty(cu[-1], Hkv * G, D, dtype=BF, device="cuda").normal_(generator=g)
+    cache = q.AttnCache(k, v)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    acc = torch.zeros(k.shape[:3], device="cuda")
+    st = torch.zeros(1, **i32)
+    runs = [q.attn_tree(cache, qq, table.cuda(), torch.tensor(ctx, **i32), torch.tensor(cu, **i32), T,
+                        acc_out=acc, status=st) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert int(st) == 0
+    for o, lse in runs[1:]:
+        assert torch.equal(o, runs[0][0]) and torch.equal(lse, runs[0][1])
+    o, lse = runs[0]
+    for b in range(B):
+        t, m = drafts[b], ctx[b] + drafts[b]
+        rows = table[b, :need[b]].long().cuda()
+        kk = k[rows].transpose(1, 2).reshape(-1, Hkv, D)[:m].double()
+        vv = v[rows].transpose(1, 2).reshape(-1, Hkv, D)[:m].double()
+        x = torch.einsum("thgd,mhd->htgm", qq[cu[b]:cu[b + 1]].view(t, Hkv, G, D).double(), kk) * D ** -0.5
+        late = torch.arange(m, device="cuda") > ctx[b] + torch.arange(t, device="cuda")[:, None]
+        x.masked_fill_(late[None, :, None], -math.inf)
+        e = x.logsumexp(-1)
+        p = torch.exp(x - e[..., None])
+        want = torch.einsum("htgm,mhd->thgd", p, vv).reshape(t, Hkv * G, D)
+        mag = torch.einsum("htgm,mhd->thgd", p, vv.abs()).reshape(t, Hkv * G, D)
+        # half a step of the weights (numerator and sum) and of the output, scores' errors beside them
+        tol = mag * (2 * half_step(BF) + 2.0 ** -14) + want.abs() * half_step(BF)
+        assert torch.all((o[cu[b]:cu[b + 1]].double() - want).abs() <= tol), b
+        assert torch.allclose(lse[cu[b]:cu[b + 1]].double(), e.permute(1, 0, 2).reshape(t, -1), atol=2.0 ** -14, rtol=0)
+        w = acc[rows].transpose(1, 2).reshape(-1, Hkv)[:m].double()
+        assert torch.allclose(w, p.sum((1, 2)).T, rtol=2.0 ** -13, atol=1e-9), b
+
+
 def test_tree_peaked_scores_and_negative_scale():
     """Scores of tens of units, rising and falling along the keys: the running maximum moves."""
     for scale in (1.0, -0.5):
