@@ -266,12 +266,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (t > t0) {
                         const int tv = t - kStep;
                         go(min(tv + lag, n) + tv);
-                        // The weights first: with alternate tiles the slot's last
+                        // With alternate tiles the weights first: the slot's last
                         // entry may be the other stream's, and a phase that is two
                         // behind looks like the awaited one. Once tile tv has its
                         // weights the other stream is past that entry (the turns).
-                        live = wait(m->p_ready + s, pp, m, a.status) &&
-                               wait(m->full + stage, ring_ph, m, a.status);
+                        if (kTwo) live = wait(m->full + stage, ring_ph, m, a.status);
+                        live = live && wait(m->p_ready + s, pp, m, a.status);
+                        if (!kTwo) live = live && wait(m->full + stage, ring_ph, m, a.status);
                         if (!live) break;
                         pp ^= 1u;
                         tc05::fence_after_sync();

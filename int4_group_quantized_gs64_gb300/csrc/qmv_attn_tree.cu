@@ -39,41 +39,47 @@ __device__ __forceinline__ uint32_t slice_ofs(int r, int c) {
 
 // ------------------------------------------------------------------ few rows
 
-// Up to 16 * MT rows an item, on the warp MMA. Each of the NW warps takes 16
-// keys of every unit through its own ring of kStages copies and keeps its own
-// maximum, sum and output accumulators, so the warps meet only at a segment's
-// end. What bounds it is the stream of keys and values: 16 rows need 4 x 16
-// multiply-adds per loaded value, far below the warp MMA's rate.
+// Up to 16 rows an item, on the warp MMA. Each of the four warps takes a slice
+// of every unit (16 keys, 32 of 64 elements) through its own ring of kStages
+// copies and keeps its own maximum, sum and output accumulators, so the warps
+// meet only at a segment's end. What bounds it is the stream of keys and
+// values: 16 rows need 4 x 16 multiply-adds per loaded value, far below the
+// warp MMA's rate. (32 rows a warp measured 452 us where the tcgen05 kernel
+// takes 248, 64 sequences of 8191 keys: registers leave one block an SM.)
 //
 // The exponentials go to the second product as two 16-bit numbers each (the
 // rounded value and the rounded rest), so the output carries no more than its
 // own rounding; the extra products are free next to the copies.
-template <int D, int MT, int NW>
+constexpr int kRows = 16, kWarps = 4;
+template <int D>
 struct RowsShape {
-    static constexpr int kRows = 16 * MT;
-    static constexpr int kSlice = 16 * D * 2;         // bytes of 16 keys (or values)
-    static constexpr int kStages = 3 * 128 / D;
-    static constexpr int kRing = NW * kStages * 2 * kSlice;
+    static constexpr int kSub = 128 / D;              // 16-key parts of a slice
+    static constexpr int kPart = 16 * D * 2;          // bytes of 16 keys (or values)
+    static constexpr int kSlice = kSub * kPart;
+    static constexpr int kStages = 3;
+    static constexpr int kUnit = kWarps * kSub * 16;  // keys a unit
+    static constexpr int kRing = kWarps * kStages * 2 * kSlice;
     static constexpr int kBuf = kRows * D * 4;
-    static constexpr int kMl = NW * kRows * 8;
-    static constexpr int kSmem = kRing + kBuf + kMl + NW * kStages * 12 + 8 * NW + 32;
+    static constexpr int kMl = kWarps * kRows * 8;
+    static constexpr int kSmem =
+        kRing + kBuf + kMl + kWarps * kStages * 12 + (int)sizeof(ShareScratch<kWarps>);
 };
 
-template <int D, int MT, int NW, bool kBf16>
-__global__ void __launch_bounds__(32 * NW, NW == 4 ? 2 : 1)
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(32 * kWarps, 2)
     k_attn_rows(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                 const TreeArgs a) {
-    using S = RowsShape<D, MT, NW>;
+    using S = RowsShape<D>;
     // fp16 weights are held 2^15 times larger: the small ones would lose bits
     // below fp16's range
     constexpr float kBoost = kBf16 ? 0.f : 15.f;
-    constexpr int kRows = S::kRows, kStages = S::kStages, KK = D / 16;
+    constexpr int kStages = S::kStages, KK = D / 16, kSub = S::kSub, kNt = 2 * kSub;
     extern __shared__ __align__(1024) uint8_t smem[];
     float *buf = reinterpret_cast<float *>(smem + S::kRing);
     float2 *ml = reinterpret_cast<float2 *>(smem + S::kRing + S::kBuf);
-    auto *share = reinterpret_cast<ShareScratch<NW> *>(smem + S::kRing + S::kBuf + S::kMl);
+    auto *share = reinterpret_cast<ShareScratch<kWarps> *>(smem + S::kRing + S::kBuf + S::kMl);
     uint64_t *bars = reinterpret_cast<uint64_t *>(share + 1);
-    int *flags = reinterpret_cast<int *>(bars + NW * kStages);
+    int *flags = reinterpret_cast<int *>(bars + kWarps * kStages);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -81,7 +87,7 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? 2 : 1)
         prefetch_tmap(&vmap);
     }
     uint64_t *bar = bars + warp * kStages;
-    int *flag = flags + warp * kStages;
+    int *flag = flags + warp * kStages;  // which 16-key parts of a slice were copied
     if (lane == 0) {
         for (int i = 0; i < kStages; ++i) tc05::mbar_init(bar + i, 1);
         tc05::fence_mbar_init();
@@ -90,114 +96,112 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? 2 : 1)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (blockIdx.x == 0 && a.status) {
-        for (int b = threadIdx.x; b < a.s.B; b += 32 * NW) {
+        for (int b = threadIdx.x; b < a.s.B; b += 32 * kWarps) {
             bool ok;
             get_seq(a.s, b, ok);
             if (!ok) set_status(a.status, kStLength);
         }
     }
-    const Share sh = find_share<32 * NW>(a, share);
-    const long long u0 = sh.u0, u1 = sh.u1;
-    if (u0 >= u1) return;
+    const Share sh = find_share<32 * kWarps>(a, share);
+    if (sh.u0 >= sh.u1) return;
+    const int units = (int)(sh.u1 - sh.u0);  // (the launcher keeps this below 2^31)
 
     Cursor pc, cc;  // of the copies, of the products
     cc.start(a, sh);
     pc = cc;
-    long long pu = u0;  // next unit to copy
-    int pstage = 0, pid = 0;
+    int to_copy = units, pstage = 0, pid = 0;
     const uint32_t ring = tc05::smem_addr(smem) + warp * (kStages * 2 * S::kSlice);
+    // this lane's 16-key part of the slice (lanes 0 .. kSub - 1 copy one each)
+    const int part = kSub > 1 ? min(lane, kSub - 1) : 0;
+    auto part_slot = [&](int u) { return (u * kWarps + warp) * (kSub * 16) + part * 16; };
 
     auto fetch_page = [&]() {
-        const int s0 = pc.u * a.unit + warp * 16;
+        const int s0 = part_slot(pc.u);
         pid = s0 < pc.q.ctx + pc.q.T
                   ? __ldg(a.s.table + (long long)pc.b * a.s.max_pages + (s0 >> a.s.lpage))
                   : 0;
     };
-    // Issues the copies of this warp's 16 keys and values of unit pu, then
-    // starts the load of the next unit's page id.
+    // Issues the copies of this warp's slice of the next unit, then starts the
+    // load of the page ids of the one after.
     auto issue = [&]() {
-        const int s0 = pc.u * a.unit + warp * 16;
-        const bool live = s0 < pc.q.ctx + pc.q.T;
+        const int s0 = part_slot(pc.u);
+        const bool mine = lane < kSub, live = mine && s0 < pc.q.ctx + pc.q.T;
         const bool good = live && (unsigned)pid < (unsigned)a.pages;
+        const uint32_t who = __ballot_sync(0xFFFFFFFFu, good);
+        uint64_t *br = bar + pstage;
         if (lane == 0) {
-            flag[pstage] = good;
-            uint64_t *br = bar + pstage;
-            if (good) {
-                const int row = (pid * a.Hkv + pc.h) * a.s.page + (s0 & (a.s.page - 1));
-                const uint32_t dst = ring + pstage * (2 * S::kSlice);
-                mbar_expect_tx(br, 2 * S::kSlice);
-                tma_load3(dst, &kmap, 0, row, 0, br);
-                tma_load3(dst + S::kSlice, &vmap, 0, row, 0, br);
-            } else {
+            flag[pstage] = (int)who;
+            if (who)
+                mbar_expect_tx(br, __popc(who) * 2 * S::kPart);
+            else
                 mbar_arrive(br);
-                if (live) set_status(a.status, kStPage);
-            }
         }
+        __syncwarp();
+        if (good) {
+            const int row = (pid * a.Hkv + pc.h) * a.s.page + (s0 & (a.s.page - 1));
+            const uint32_t dst = ring + pstage * (2 * S::kSlice) + part * S::kPart;
+            tma_load3(dst, &kmap, 0, row, 0, br);
+            tma_load3(dst + S::kSlice, &vmap, 0, row, 0, br);
+        } else if (live) {
+            set_status(a.status, kStPage);
+        }
+        __syncwarp();
         if (++pstage == kStages) pstage = 0;
-        ++pu;
+        --to_copy;
         if (++pc.u == pc.nu) pc.next_item(a);
-        if (pu < u1) fetch_page();
+        if (to_copy > 0) fetch_page();
     };
 
     fetch_page();
-    for (int i = 0; i < kStages - 1 && pu < u1; ++i) issue();
+    for (int i = 0; i < kStages - 1 && to_copy > 0; ++i) issue();
 
     // key and 16-byte chunk of this lane's row in the 8x8 matrices of an ldmatrix
     const int kkey = (lane & 7) + ((lane >> 4) << 3), kchk = (lane >> 3) & 1;
     const int vkey = (lane & 7) + (((lane >> 3) & 1) << 3), vchk = lane >> 4;
     const int g = lane >> 2, c = lane & 3;
 
-    int stage = 0;
+    int stage = 0, left = units;
     uint32_t phase = 0;
     bool dead = false;
-    long long u = u0;
-    while (u < u1) {
+    while (left > 0) {
         // ---- one segment
-        const bool at_start = cc.u == 0, first_seg = u == u0;
-        const int seg_b = cc.b, seg_h = cc.h, seg_rb = cc.rb;
+        const bool at_start = cc.u == 0, first_seg = left == units;
+        const int seg_b = cc.b, seg_h = cc.h;
         const Seq sq = cc.q;
-        const int nrows = sq.T * a.G;
-        uint32_t qf[MT][KK][4];
-        int rt[MT][2];  // draft of each of this lane's rows, -1: no row
+        const int nrows = sq.T * a.G;  // at most 16
+        uint32_t qf[KK][4];
+        int rt[2];  // draft of each of this lane's rows, -1: no row
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
+        for (int e = 0; e < 2; ++e) {
+            const int r = e * 8 + g;
+            const bool have = r < nrows;
+            const int t = have ? r / a.G : 0;
+            rt[e] = have ? t : -1;
+            const uint16_t *p = a.q + (long long)(sq.first + t) * a.q_stride +
+                                (long long)(seg_h * a.G + (have ? r - t * a.G : 0)) * D;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = seg_rb * kRows + m * 16 + e * 8 + g;
-                const bool have = r < nrows;
-                const int t = have ? r / a.G : 0;
-                rt[m][e] = have ? t : -1;
-                const uint16_t *p = a.q + (long long)(sq.first + t) * a.q_stride +
-                                    (long long)(seg_h * a.G + (have ? r - t * a.G : 0)) * D;
-#pragma unroll
-                for (int k = 0; k < KK; ++k) {
-                    const uint32_t *w = reinterpret_cast<const uint32_t *>(p + k * 16 + c * 2);
-                    qf[m][k][e] = have ? (w[0] ^ a.qxor) & a.qand : 0u;
-                    qf[m][k][e + 2] = have ? (w[4] ^ a.qxor) & a.qand : 0u;
-                }
+            for (int k = 0; k < KK; ++k) {
+                const uint32_t *w = reinterpret_cast<const uint32_t *>(p + k * 16 + c * 2);
+                qf[k][e] = have ? (w[0] ^ a.qxor) & a.qand : 0u;
+                qf[k][e + 2] = have ? (w[4] ^ a.qxor) & a.qand : 0u;
             }
         }
-        float o[MT][D / 8][4];
-        float mx[MT][2], l[MT][2];
+        float o[D / 8][4];
+        float mx[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
+        for (int n = 0; n < D / 8; ++n)
 #pragma unroll
-            for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[m][n][i] = 0.f;
-            mx[m][0] = mx[m][1] = -INFINITY;
-            l[m][0] = l[m][1] = 0.f;
-        }
+            for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
         bool done = false;
         while (!done) {
-            if (pu < u1 && !dead) issue();
+            if (to_copy > 0 && !dead) issue();
             if (!dead && !tc05::mbar_wait(bar + stage, phase, kPoll)) {
                 // give up: flag it, and wait (bounded as well) for the copies in flight
                 dead = true;
                 if (lane == 0) set_status(a.status, kStTimeout);
                 int ds = stage;
                 uint32_t dp = phase;
-                for (long long x = u; x < pu; ++x) {
+                for (int x = left; x > to_copy; --x) {
                     tc05::mbar_wait(bar + ds, dp, kPoll);
                     if (++ds == kStages) {
                         ds = 0;
@@ -206,53 +210,55 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? 2 : 1)
                 }
             }
             dead = __any_sync(0xFFFFFFFFu, dead);
-            const int s0 = cc.u * a.unit + warp * 16;
-            if (!dead && flag[stage]) {
+            const int s0 = (cc.u * kWarps + warp) * (kSub * 16);
+            const int copied = dead ? 0 : flag[stage];
+            if (copied) {
                 const uint32_t ks = ring + stage * (2 * S::kSlice), vs = ks + S::kSlice;
-                float s[MT][2][4];
+                float s[kNt][4];
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
+                for (int n = 0; n < kNt; ++n)
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
+                    for (int i = 0; i < 4; ++i) s[n][i] = 0.f;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) s[m][n][i] = 0.f;
+                for (int k = 0; k < KK; ++k)
 #pragma unroll
-                for (int k = 0; k < KK; ++k) {
-                    uint32_t kb[4];
-                    ldmatrix4(kb, ks + slice_ofs<16>(kkey, 2 * k + kchk));
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        mma16816<kBf16>(s[m][0], qf[m][k], kb[0], kb[1]);
-                        mma16816<kBf16>(s[m][1], qf[m][k], kb[2], kb[3]);
+                    for (int j = 0; j < kSub; ++j) {
+                        uint32_t kb[4];
+                        ldmatrix4(kb, ks + j * S::kPart + slice_ofs<16>(kkey, 2 * k + kchk));
+                        mma16816<kBf16>(s[2 * j], qf[k], kb[0], kb[1]);
+                        mma16816<kBf16>(s[2 * j + 1], qf[k], kb[2], kb[3]);
                     }
-                }
-                if (s0 + 16 > sq.ctx) {  // drafts, or the end of the sequence, in this slice
+                if (s0 + kSub * 16 > sq.ctx || copied != (1 << kSub) - 1) {
+                    // drafts, the end of the sequence or a missing page in this slice
                     const int len = sq.ctx + sq.T;
-                    uint32_t see[MT][2];  // of this slice's 16 keys, by row
+                    uint32_t see[2];  // of this slice's keys, by row
+                    uint32_t there = 0;
 #pragma unroll
-                    for (int m = 0; m < MT; ++m)
+                    for (int j = 0; j < kSub; ++j)
+                        if ((copied >> j) & 1) there |= 0xFFFFu << (16 * j);
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            see[m][e] = rt[m][e] >= 0 ? seen_word(a, sq, rt[m][e], s0) : 0u;
+                    for (int e = 0; e < 2; ++e) {
+                        see[e] = rt[e] >= 0 ? seen_word(a, sq, rt[e], s0) & there : 0u;
 #pragma unroll
-                            for (int n = 0; n < 2; ++n)
+                        for (int n = 0; n < kNt; ++n)
 #pragma unroll
-                                for (int i = 0; i < 2; ++i)
-                                    if (!((see[m][e] >> (n * 8 + c * 2 + i)) & 1u))
-                                        s[m][n][2 * e + i] = -INFINITY;
-                        }
+                            for (int i = 0; i < 2; ++i)
+                                if (!((see[e] >> (n * 8 + c * 2 + i)) & 1u)) s[n][2 * e + i] = -INFINITY;
+                    }
                     // Values that some row must not see are kept out of the
                     // product where zero times them is not zero: rows past the
-                    // end (whatever an unused slot holds) become zeros, and a
-                    // draft's infinities and NaNs are added to the rows that
-                    // see it and replaced by zeros.
-                    for (int j = 0; j < 16; ++j) {
+                    // end (whatever an unused slot holds) and missing ones become
+                    // zeros, and a draft's infinities and NaNs are added to the
+                    // rows that see it and replaced by zeros.
+                    for (int j = 0; j < kSub * 16; ++j) {
                         const int key = s0 + j;
-                        if (key < sq.ctx) continue;
+                        const bool none = key >= len || !((there >> j) & 1u);
+                        if (key < sq.ctx && !none) continue;
+                        const uint32_t row = vs + (j >> 4) * S::kPart;
                         bool bad = false;
                         for (int w = lane; w < D / 2; w += 32) {
-                            const uint32_t ad = vs + slice_ofs<16>(j, w >> 2) + (w & 3) * 4;
-                            if (key >= len)
+                            const uint32_t ad = row + slice_ofs<16>(j & 15, w >> 2) + (w & 3) * 4;
+                            if (none)
                                 sts32(ad, 0u);
                             else
                                 bad |= nonfinite2<kBf16>(lds32(ad));
@@ -260,20 +266,18 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? 2 : 1)
                         if (__any_sync(0xFFFFFFFFu, bad)) {
                             __syncwarp();
 #pragma unroll
-                            for (int m = 0; m < MT; ++m)
+                            for (int e = 0; e < 2; ++e)
+                                if ((see[e] >> j) & 1u)
 #pragma unroll
-                                for (int e = 0; e < 2; ++e)
-                                    if ((see[m][e] >> j) & 1u)
-#pragma unroll
-                                        for (int n = 0; n < D / 8; ++n) {
-                                            const float2 f = unpack2<kBf16>(
-                                                lds32(vs + slice_ofs<16>(j, n) + c * 4));
-                                            if (!isfinite(f.x)) o[m][n][2 * e] += f.x;
-                                            if (!isfinite(f.y)) o[m][n][2 * e + 1] += f.y;
-                                        }
+                                    for (int n = 0; n < D / 8; ++n) {
+                                        const float2 f = unpack2<kBf16>(
+                                            lds32(row + slice_ofs<16>(j & 15, n) + c * 4));
+                                        if (!isfinite(f.x)) o[n][2 * e] += f.x;
+                                        if (!isfinite(f.y)) o[n][2 * e + 1] += f.y;
+                                    }
                             __syncwarp();
                             for (int w = lane; w < D / 2; w += 32) {
-                                const uint32_t ad = vs + slice_ofs<16>(j, w >> 2) + (w & 3) * 4;
+                                const uint32_t ad = row + slice_ofs<16>(j & 15, w >> 2) + (w & 3) * 4;
                                 uint32_t v = lds32(ad);
                                 if (nonfinite2<kBf16>(v & 0xFFFFu)) v &= 0xFFFF0000u;
                                 if (nonfinite2<kBf16>(v & 0xFFFF0000u)) v &= 0x0000FFFFu;
@@ -287,128 +291,120 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? 2 : 1)
                 }
                 if (a.stash) {  // the masked scores, for the weights' own pass
 #pragma unroll
-                    for (int m = 0; m < MT; ++m)
+                    for (int e = 0; e < 2; ++e)
+                        if (rt[e] >= 0)
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            if (rt[m][e] >= 0) {
-                                float *p = stash_at(a, seg_b, seg_h, s0) + (m * 16 + e * 8 + g) * 16 + c * 2;
-                                *reinterpret_cast<float2 *>(p) = make_float2(s[m][0][2 * e], s[m][0][2 * e + 1]);
-                                *reinterpret_cast<float2 *>(p + 8) = make_float2(s[m][1][2 * e], s[m][1][2 * e + 1]);
-                            }
+                            for (int j = 0; j < kSub; ++j)
+                                if (kSub == 1 || s0 + j * 16 < sq.ctx + sq.T) {
+                                    float *p = stash_at(a, seg_b, seg_h, s0 + j * 16) + (e * 8 + g) * 16 + c * 2;
+                                    *reinterpret_cast<float2 *>(p) = make_float2(s[2 * j][2 * e], s[2 * j][2 * e + 1]);
+                                    *reinterpret_cast<float2 *>(p + 8) =
+                                        make_float2(s[2 * j + 1][2 * e], s[2 * j + 1][2 * e + 1]);
+                                }
                 }
-                uint32_t ph[MT][4], pl[MT][4];
+                uint32_t ph[kSub][4], pl[kSub][4];
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
+                for (int e = 0; e < 2; ++e) {
+                    float t = -INFINITY;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float t = fmaxf(fmaxf(s[m][0][2 * e] * a.sl2, s[m][0][2 * e + 1] * a.sl2),
-                                        fmaxf(s[m][1][2 * e] * a.sl2, s[m][1][2 * e + 1] * a.sl2));
-                        t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 1));
-                        t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 2));
-                        const float mn = fmaxf(mx[m][e], t);
-                        if (__any_sync(0xFFFFFFFFu, mn > mx[m][e])) {
-                            const float al = mn == mx[m][e] ? 1.f : ex2(mx[m][e] - mn);
-                            mx[m][e] = mn;
-                            l[m][e] *= al;
+                    for (int n = 0; n < kNt; ++n) t = fmaxf(t, fmaxf(s[n][2 * e], s[n][2 * e + 1]));
+                    t *= a.sl2;
+                    t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 1));
+                    t = fmaxf(t, __shfl_xor_sync(0xFFFFFFFFu, t, 2));
+                    const float mn = fmaxf(mx[e], t);
+                    if (__any_sync(0xFFFFFFFFu, mn > mx[e])) {
+                        const float al = mn == mx[e] ? 1.f : ex2(mx[e] - mn);
+                        mx[e] = mn;
+                        l[e] *= al;
 #pragma unroll
-                            for (int n = 0; n < D / 8; ++n) {
-                                o[m][n][2 * e] *= al;
-                                o[m][n][2 * e + 1] *= al;
-                            }
+                        for (int n = 0; n < D / 8; ++n) {
+                            o[n][2 * e] *= al;
+                            o[n][2 * e + 1] *= al;
                         }
-                        const float base = mx[m][e] == -INFINITY ? 0.f : mx[m][e] - kBoost;
+                    }
+                    const float base = mx[e] == -INFINITY ? 0.f : mx[e] - kBoost;
 #pragma unroll
-                        for (int n = 0; n < 2; ++n) {
-                            const float p0 = ex2(fmaf(s[m][n][2 * e], a.sl2, -base));
-                            const float p1 = ex2(fmaf(s[m][n][2 * e + 1], a.sl2, -base));
-                            l[m][e] += p0 + p1;
-                            const uint32_t hi = pack2<kBf16>(p0, p1);
-                            const float2 f = unpack2<kBf16>(hi);
-                            ph[m][2 * n + e] = hi;
-                            pl[m][2 * n + e] = pack2<kBf16>(p0 - f.x, p1 - f.y);
-                        }
+                    for (int n = 0; n < kNt; ++n) {
+                        const float p0 = ex2(fmaf(s[n][2 * e], a.sl2, -base));
+                        const float p1 = ex2(fmaf(s[n][2 * e + 1], a.sl2, -base));
+                        l[e] += p0 + p1;
+                        const uint32_t hi = pack2<kBf16>(p0, p1);
+                        const float2 f = unpack2<kBf16>(hi);
+                        ph[n >> 1][2 * (n & 1) + e] = hi;
+                        pl[n >> 1][2 * (n & 1) + e] = pack2<kBf16>(p0 - f.x, p1 - f.y);
                     }
                 }
 #pragma unroll
-                for (int k = 0; k < KK; ++k) {
-                    uint32_t vb[4];
-                    ldmatrix4_trans(vb, vs + slice_ofs<16>(vkey, 2 * k + vchk));
+                for (int k = 0; k < KK; ++k)
 #pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        mma16816<kBf16>(o[m][2 * k], ph[m], vb[0], vb[1]);
-                        mma16816<kBf16>(o[m][2 * k + 1], ph[m], vb[2], vb[3]);
-                        mma16816<kBf16>(o[m][2 * k], pl[m], vb[0], vb[1]);
-                        mma16816<kBf16>(o[m][2 * k + 1], pl[m], vb[2], vb[3]);
+                    for (int j = 0; j < kSub; ++j) {
+                        uint32_t vb[4];
+                        ldmatrix4_trans(vb, vs + j * S::kPart + slice_ofs<16>(vkey, 2 * k + vchk));
+                        mma16816<kBf16>(o[2 * k], ph[j], vb[0], vb[1]);
+                        mma16816<kBf16>(o[2 * k + 1], ph[j], vb[2], vb[3]);
+                        mma16816<kBf16>(o[2 * k], pl[j], vb[0], vb[1]);
+                        mma16816<kBf16>(o[2 * k + 1], pl[j], vb[2], vb[3]);
                     }
-                }
             }
             __syncwarp();  // the slot may be copied into again
             if (++stage == kStages) {
                 stage = 0;
                 phase ^= 1;
             }
-            ++u;
-            done = ++cc.u == cc.nu || u == u1;
+            --left;
+            done = ++cc.u == cc.nu || left == 0;
         }
         const bool whole = at_start && cc.u == cc.nu;
-        if (cc.u == cc.nu) cc.next_item(a);
+        if (left > 0) cc.next_item(a);
 
         // ---- the segment's end: the warps' sums, one warp after the other
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                if (mx[m][e] != -INFINITY) mx[m][e] -= kBoost;
-                l[m][e] += __shfl_xor_sync(0xFFFFFFFFu, l[m][e], 1);
-                l[m][e] += __shfl_xor_sync(0xFFFFFFFFu, l[m][e], 2);
-                if (c == 0) ml[warp * kRows + m * 16 + e * 8 + g] = make_float2(mx[m][e], l[m][e]);
-            }
+        for (int e = 0; e < 2; ++e) {
+            if (mx[e] != -INFINITY) mx[e] -= kBoost;
+            l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 1);
+            l[e] += __shfl_xor_sync(0xFFFFFFFFu, l[e], 2);
+            if (c == 0) ml[warp * kRows + e * 8 + g] = make_float2(mx[e], l[e]);
+        }
         __syncthreads();
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int e = 0; e < 2; ++e) {
+            float M = -INFINITY;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float M = -INFINITY;
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w * kRows + e * 8 + g].x);
+            const float f = mx[e] == -INFINITY ? 1.f : ex2(mx[e] - M);
 #pragma unroll
-                for (int w = 0; w < NW; ++w)
-                    M = fmaxf(M, ml[w * kRows + m * 16 + e * 8 + g].x);
-                const float f = mx[m][e] == -INFINITY ? 1.f : ex2(mx[m][e] - M);
-#pragma unroll
-                for (int n = 0; n < D / 8; ++n) {
-                    o[m][n][2 * e] *= f;
-                    o[m][n][2 * e + 1] *= f;
-                }
+            for (int n = 0; n < D / 8; ++n) {
+                o[n][2 * e] *= f;
+                o[n][2 * e + 1] *= f;
             }
-        for (int w = 0; w < NW; ++w) {
+        }
+        for (int w = 0; w < kWarps; ++w) {
             if (warp == w) {
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
+                for (int e = 0; e < 2; ++e)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
-#pragma unroll
-                        for (int n = 0; n < D / 8; ++n) {
-                            const int r = m * 16 + e * 8 + g;
-                            float2 *p = reinterpret_cast<float2 *>(
-                                buf + r * D + ((n * 8 + c * 2) ^ ((r & 3) << 3)));
-                            float2 v = make_float2(o[m][n][2 * e], o[m][n][2 * e + 1]);
-                            if (w > 0) {
-                                v.x += p->x;
-                                v.y += p->y;
-                            }
-                            *p = v;
+                    for (int n = 0; n < D / 8; ++n) {
+                        const int r = e * 8 + g;
+                        float2 *p = reinterpret_cast<float2 *>(
+                            buf + r * D + ((n * 8 + c * 2) ^ ((r & 3) << 3)));
+                        float2 v = make_float2(o[n][2 * e], o[n][2 * e + 1]);
+                        if (w > 0) {
+                            v.x += p->x;
+                            v.y += p->y;
                         }
+                        *p = v;
+                    }
             }
             __syncthreads();
         }
         // rows out: two columns a thread
-        const int used = min(kRows, nrows - seg_rb * kRows);
-        for (int i = threadIdx.x; i < used * (D / 2); i += 32 * NW) {
+        for (int i = threadIdx.x; i < nrows * (D / 2); i += 32 * kWarps) {
             const int r = i / (D / 2), col = (i - r * (D / 2)) * 2;
             float M = -INFINITY, L = 0.f;
 #pragma unroll
-            for (int w = 0; w < NW; ++w) M = fmaxf(M, ml[w * kRows + r].x);
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, ml[w * kRows + r].x);
 #pragma unroll
-            for (int w = 0; w < NW; ++w) {
+            for (int w = 0; w < kWarps; ++w) {
                 const float2 v = ml[w * kRows + r];
                 L += v.x == -INFINITY ? v.y : v.y * ex2(v.x - M);
             }
@@ -417,8 +413,8 @@ __global__ void __launch_bounds__(32 * NW, NW == 4 ? 2 : 1)
                 const float inv = L == 0.f ? 0.f : 1.f / L;
                 v.x *= inv;
                 v.y *= inv;
-                const int rr = seg_rb * kRows + r, t = rr / a.G;
-                const long long row = (long long)(sq.first + t) * a.Hq + seg_h * a.G + rr - t * a.G;
+                const int t = r / a.G;
+                const long long row = (long long)(sq.first + t) * a.Hq + seg_h * a.G + r - t * a.G;
                 if (a.o_f32)
                     *reinterpret_cast<float2 *>(static_cast<float *>(a.o) + row * D + col) = v;
                 else
@@ -550,27 +546,26 @@ __global__ void __launch_bounds__(128 * kSplit) k_attn_join(const TreeArgs a, bo
 
 // ------------------------------------------------------------------ host
 
-template <int D, int MT, int NW, bool kBf16>
-cudaError_t run_rows(const CUtensorMap &km, const CUtensorMap &vm, const TreeArgs &a,
-                     cudaStream_t st) {
-    auto *k = k_attn_rows<D, MT, NW, kBf16>;
-    constexpr int smem = RowsShape<D, MT, NW>::kSmem;
+template <int D, bool kBf16>
+cudaError_t run_rows(const AttnCache &c, const TreeArgs &a, cudaStream_t st) {
+    CUtensorMap km, vm;
+    if (!encode_pool(&km, c.k, c, 16, true) || !encode_pool(&vm, c.v, c, 16, true))
+        return cudaErrorNotSupported;
+    auto *k = k_attn_rows<D, kBf16>;
+    constexpr int smem = RowsShape<D>::kSmem;
     cudaError_t e = set_smem(k, smem);
-    if (e == cudaSuccess) e = launch(k, dim3(a.grid), dim3(32 * NW), smem, st, true, km, vm, a);
+    if (e == cudaSuccess) e = launch(k, dim3(a.grid), dim3(32 * kWarps), smem, st, true, km, vm, a);
     return e;
 }
 
 template <int D, bool kBf16>
-cudaError_t run_tree(const AttnCache &c, const CUtensorMap &km, const CUtensorMap &vm,
-                     const TreeArgs &a, int max_rows, cudaStream_t st) {
-    cudaError_t e = a.rows == 16   ? run_rows<D, 1, 4, kBf16>(km, vm, a, st)
-                    : a.rows == 32 ? run_rows<D, 2, 8, kBf16>(km, vm, a, st)
-                                   : launch_tree_tc(c, a, st);
+cudaError_t run_tree(const AttnCache &c, const TreeArgs &a, int max_rows, cudaStream_t st) {
+    cudaError_t e = a.rows == kRows ? run_rows<D, kBf16>(c, a, st) : launch_tree_tc(c, a, st);
     const int nrb = (max_rows + a.rows - 1) / a.rows;
     // many rows: a warp 8 of them whole, two blocks' segments at a time; few rows:
     // a warp a part of 8 rows, four warps sharing the blocks' segments where items
     // are so few that each has many (8 items of 38 segments: 10.8 -> 5.8 us)
-    const bool many = a.rows > 32, longs = a.grid > 8 * a.s.B * a.Hkv * nrb;
+    const bool many = a.rows > kRows, longs = a.grid > 8 * a.s.B * a.Hkv * nrb;
     const int warps = ((max_rows < a.rows ? max_rows : a.rows) + 7) / 8 * (many ? 1 : D / 32);
     const dim3 grid(a.s.B * a.Hkv, nrb, (warps + 3) / 4);
     if (e == cudaSuccess)
@@ -581,10 +576,10 @@ cudaError_t run_tree(const AttnCache &c, const CUtensorMap &km, const CUtensorMa
     return e;
 }
 
-// Rows an item: up to 32 on the warp MMA, more on tcgen05 (qmv_attn_tc.cu).
-int tree_rows(int max_rows) {
-    return max_rows <= 16 ? 16 : max_rows <= 32 ? 32 : max_rows <= 128 ? 128 : 256;
-}
+// Rows an item: up to 16 on the warp MMA, more on tcgen05 (qmv_attn_tc.cu).
+// With 16 rows the two measured 259 and 245 us (64 sequences of 8191 keys) and
+// 13.2 and 14.4 us (one of 777), with 32 rows 452 and 248.
+int tree_rows(int max_rows) { return max_rows <= kRows ? kRows : max_rows <= 128 ? 128 : 256; }
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     static std::once_flag once;
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
@@ -599,7 +594,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-int tree_grid_max(int rows) { return sm_count() * (rows == 16 ? 2 : 1); }
+int tree_grid_max(int rows) { return sm_count() * (rows == kRows ? 2 : 1); }
 
 }  // namespace
 }  // namespace attn
@@ -621,13 +616,13 @@ bool encode_pool(CUtensorMap *map, const void *pool, const AttnCache &c, int box
 
 namespace {
 
-// Where the weights come from with up to 32 rows: scores that the attention
+// Where the weights come from with up to 16 rows: scores that the attention
 // leaves in the workspace, or a second product of queries and keys. A score
 // costs 4 bytes written and 4 read a row, a key's second reading 2 D bytes; the
 // workspace is kept within kStashMax.
 constexpr size_t kStashMax = (size_t)1 << 30;
 size_t stash_bytes(const AttnCache &c, int max_rows, int B, int max_pages) {
-    if (max_rows > 32) return 0;
+    if (max_rows > kRows) return 0;
     const size_t n = (size_t)B * c.Hkv * max_pages * c.page * max_rows * 4;
     return n <= kStashMax ? n : 0;
 }
@@ -669,24 +664,22 @@ cudaError_t launch_attn_tree(const AttnCache &c, const TreeCall &t, cudaStream_t
     a.status = t.status;
     const int max_rows = t.s.max_draft * a.G;
     a.rows = tree_rows(max_rows);
-    a.unit = a.rows == 16 ? 64 : 128;  // keys a unit
+    a.unit = a.rows == kRows ? kWarps * 16 * (128 / c.D) : 128;  // keys a unit
     const long long most = (long long)t.s.B * c.Hkv * ((max_rows + a.rows - 1) / a.rows) *
                            ((((long long)t.s.max_pages << lpage) + a.unit - 1) / a.unit);
     const int gmax = tree_grid_max(a.rows);
+    if (most / gmax >= 0x7FFFFFFFLL) return cudaErrorInvalidValue;  // a block's units fit 31 bits
     a.grid = most < gmax ? (int)most : gmax;
     a.part_o = static_cast<float *>(t.ws);
     a.part_ml = a.part_o + (size_t)gmax * 2 * a.rows * c.D;
     a.max_rows = max_rows;
     if (a.acc_out && stash_bytes(c, max_rows, t.s.B, t.s.max_pages))
         a.stash = reinterpret_cast<float *>(static_cast<char *>(t.ws) + part_bytes(c, a.rows));
-    CUtensorMap km, vm;
-    if (!encode_pool(&km, c.k, c, 16, true) || !encode_pool(&vm, c.v, c, 16, true))
-        return cudaErrorNotSupported;
     if (c.D == 64)
-        return c.bf16 ? run_tree<64, true>(c, km, vm, a, max_rows, st)
-                      : run_tree<64, false>(c, km, vm, a, max_rows, st);
-    return c.bf16 ? run_tree<128, true>(c, km, vm, a, max_rows, st)
-                  : run_tree<128, false>(c, km, vm, a, max_rows, st);
+        return c.bf16 ? run_tree<64, true>(c, a, max_rows, st)
+                      : run_tree<64, false>(c, a, max_rows, st);
+    return c.bf16 ? run_tree<128, true>(c, a, max_rows, st)
+                  : run_tree<128, false>(c, a, max_rows, st);
 }
 
 }  // namespace qmv

@@ -6,7 +6,7 @@
 // the rows R of a key/value head:
 //   few rows      k_attn_rows leaves its scores (8 R bytes a key, written and
 //                 read); k_weights_stash turns them into weights, a thread a key.
-//   33 .. 512     k_weights_tc forms the scores again (2 D bytes a key), keys as
+//   17 .. 512     k_weights_tc forms the scores again (2 D bytes a key), keys as
 //                 the rows of the tcgen05 product, so that a thread has one key
 //                 and sums its own columns: S^T = K Q^T, all R queries resident
 //                 in shared memory while the keys stream by once.
@@ -27,7 +27,7 @@ namespace {
 
 // A thread takes four keys. vec: the sums lie on 16-byte boundaries.
 __global__ void __launch_bounds__(256) k_weights_stash(const TreeArgs a, bool vec) {
-    __shared__ float e2[32];
+    __shared__ float e2[16];
     const int b = blockIdx.z, h = blockIdx.y, slot = (blockIdx.x * 256 + threadIdx.x) * 4;
     bool ok;
     const Seq q = get_seq(a.s, b, ok);  // (a call's inputs are older than its first kernel)
@@ -483,7 +483,7 @@ cudaError_t run(const AttnCache &c, const TreeArgs &a, int max_rows, cudaStream_
         return launch(k_weights_stash, dim3((unsigned)((most + 1023) / 1024), a.Hkv, a.s.B), dim3(256),
                       0, st, true, a,
                       ((reinterpret_cast<uintptr_t>(a.acc_in) | reinterpret_cast<uintptr_t>(a.acc_out)) & 15) == 0);
-    if (max_rows <= 32 || max_rows > kMaxRows)
+    if (max_rows <= 16 || max_rows > kMaxRows)
         return launch(k_weights_any<D, kBf16>, dim3((unsigned)((most + 15) / 16), a.Hkv, a.s.B),
                       dim3(256), 0, st, true, a);
     constexpr int kTile = kKeys * D * 2;
