@@ -15,6 +15,7 @@ struct TreeArgs {
     const uint16_t *q;
     long long q_stride;
     int Hq, Hkv, G, pages;
+    uint32_t ginv;  // ceil(2^32 / G), for div_g (G > 1)
     const uint32_t *mask;
     int words;
     // |scale| * log2(e), so that a masked score can be -inf before the scaling;
@@ -37,6 +38,12 @@ struct TreeArgs {
     int max_rows;
     int32_t *status;
 };
+
+// r / G for a row r < 2^18 and G <= 1024: the rounding of ginv adds less than
+// r * 2^10 / 2^32 < 1 / G.
+__device__ __forceinline__ int div_g(const TreeArgs &a, int r) {
+    return a.G == 1 ? r : (int)__umulhi((uint32_t)r, a.ginv);
+}
 
 __device__ __forceinline__ int row_blocks(const Seq &q, int G, int rows) {
     return (q.T * G + rows - 1) / rows;

@@ -14,10 +14,10 @@
 //                both have the same row on the same lane);
 //   rows  > 128: two tiles of 128 rows against the same key tiles.
 // Warps: 0-3 and 4-7 the streams' softmax (a thread a row: maximum and sum
-// need no exchange), 8 the copies, 9 and 10 the streams' products, 11 brings the
-// next segment's queries to L2. These four need few registers and pass the rest
-// on to the softmax warps, whose 128 scores stay in registers: reading them from
-// tensor memory twice would cost as much as the products. A ring of 128-key
+// need no exchange), 8 and 11 the copies of keys and of values, 9 and 10 the
+// streams' products. These four need few registers and pass the rest on to the
+// softmax warps, whose 128 scores stay in registers: reading them from tensor
+// memory twice would cost as much as the products. A ring of 128-key
 // tiles holds keys and values in the order in which the products use them,
 // across segments. The running maximum moves only when it grows by more than 2^8 (a
 // row's weights may then exceed 1, which fp32 sums and 16-bit weights hold),
@@ -50,7 +50,6 @@ struct Misc {
     uint64_t s_full[2], p_ready[2], o_full[2], q_full, fin[2], turn[2];
     uint32_t tmem, dead;
     int tiles;             // of the segment whose queries are ready
-    int segments;          // begun so far
     uint32_t nf[8];        // drafts with infinities or NaNs among their values
     float2 ml[2][128];
 };
@@ -125,7 +124,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc05::mbar_init(&m->q_full, 256);
         m->dead = 0;
-        m->segments = 0;
         tc05::fence_mbar_init();
         prefetch_tmap(&kmap);
         prefetch_tmap(&vmap);
@@ -152,86 +150,88 @@ __global__ void __launch_bounds__(kThreads, 1)
     // 168 x 384 registers at launch = 216 x 256 + 72 x 128
     if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 8) {
+    if (warp == 8 || warp == 11) {
         // ------------------------------------------------------------ copies
+        // warp 8 the keys, 11 the values: a copy is a whole page at most, and
+        // with small pages one warp's issue does not keep up (16-token pages, 64
+        // elements: a tile's eight copies take some 1,100 cycles)
+        const bool keys = warp == 8;
+        const CUtensorMap *map = keys ? &kmap : &vmap;
         const int prow = a.s.page < kKeys ? a.s.page : kKeys;  // rows a copy
         Cursor c;
         c.start(a, sh);
-        int stage = 0, issued = 0;
+        int stage = 0, at = 0;
         uint32_t phase = 1;  // a fresh barrier counts as passed for parity 1
-        int pid = 0;
-        bool live = false;
+        auto go = [&](int pos) {  // to a later entry of the segment
+            stage += pos - at;
+            at = pos;
+            while (stage >= stages) {
+                stage -= stages;
+                phase ^= 1u;
+            }
+        };
         // this lane's piece of tile j of the sequence at c: its page
         auto page_of = [&](int j, bool &lv) {
             const int slot = j * kKeys + lane * prow;
             lv = lane * prow < kKeys && slot < c.q.ctx + c.q.T;
             return lv ? __ldg(a.s.table + (long long)c.b * a.s.max_pages + (slot >> a.s.lpage)) : 0;
         };
+        bool live;
+        int pid = page_of(c.u, live);
+        bool ok = true;
+        uint32_t pending = 0, pending_ph = 0;  // slots this warp copied to, and the phase that ends it
         for (int left = units; left > 0;) {
             const Segment sg(c, left);
-            // at step x: values of tile x - lag, then keys of tile x
-            int vp[2] = {0, 0};       // pages of the last tiles' keys, for their values
-            bool vl[2] = {false, false};
-            int np = page_of(sg.j0, live);
-            bool nl = live;
 #pragma unroll 1
-            for (int x = 0; x < sg.n + lag; ++x) {
-#pragma unroll 1
-                for (int kind = 0; kind < 2; ++kind) {  // 0: values, 1: keys
-                    const int t = kind ? x : x - lag;
-                    if (t < 0 || t >= sg.n) continue;
-                    const int sl = kTwo ? 0 : t & 1;
-                    if (kind) {
-                        pid = np;
-                        live = nl;
-                        vp[sl] = pid;
-                        vl[sl] = live;
-                        if (x + 1 < sg.n) np = page_of(sg.j0 + x + 1, nl);
-                    } else {
-                        pid = vp[sl];
-                        live = vl[sl];
-                    }
-                    const bool good = live && (unsigned)pid < (unsigned)a.pages;
-                    const uint32_t n = __popc(__ballot_sync(0xFFFFFFFFu, good));
-                    const bool ok = wait(m->empty + stage, phase, m, a.status);
-                    if (__all_sync(0xFFFFFFFFu, ok)) {
-                        if (lane == 0) {
-                            if (n)
-                                mbar_expect_tx(m->full + stage, n * prow * D * 2);
-                            else
-                                mbar_arrive(m->full + stage);
-                        }
-                        __syncwarp();
-                        if (good) {
-                            const int slot = (sg.j0 + t) * kKeys + lane * prow;
-                            const int row = (pid * a.Hkv + c.h) * a.s.page + (slot & (a.s.page - 1));
-                            const uint32_t dst = tc05::smem_addr(ring) + stage * kTile + lane * prow * 128;
+            for (int t = 0; t < sg.n; ++t) {
+                go(keys ? (t == 0 ? 0 : 2 * t + 1 - lag) : min(t + lag, sg.n) + t);
+                const bool good = live && (unsigned)pid < (unsigned)a.pages;
+                const int row =
+                    (pid * a.Hkv + c.h) * a.s.page + (((sg.j0 + t) * kKeys + lane * prow) & (a.s.page - 1));
+                if (live && !good && keys) set_status(a.status, kStPage);
+                if (t + 1 < sg.n) pid = page_of(sg.j0 + t + 1, live);
+                const uint32_t n = __popc(__ballot_sync(0xFFFFFFFFu, good));
+                ok = ok && wait(m->empty + stage, phase, m, a.status);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) continue;
+                if (lane == 0) {
+                    if (n)
+                        mbar_expect_tx(m->full + stage, n * prow * D * 2);
+                    else
+                        mbar_arrive(m->full + stage);
+                }
+                __syncwarp();
+                if (good) {
+                    const uint32_t dst = tc05::smem_addr(ring) + stage * kTile + lane * prow * 128;
 #pragma unroll
-                            for (int hf = 0; hf < kHalves; ++hf)
-                                tma_load3(dst + hf * (kKeys * 128), kind ? &kmap : &vmap, 0, row, hf,
-                                          m->full + stage);
-                        } else if (live && kind) {
-                            set_status(a.status, kStPage);
-                        }
-                        ++issued;
-                        if (++stage == stages) {
-                            stage = 0;
-                            phase ^= 1;
-                        }
+                    for (int hf = 0; hf < kHalves; ++hf)
+                        tma_load3(dst + hf * (kKeys * 128), map, 0, row, hf, m->full + stage);
+                }
+                pending |= 1u << stage;
+                pending_ph = (pending_ph & ~(1u << stage)) | ((phase ^ 1u) & 1u) << stage;
+            }
+            go(2 * sg.n);
+            at = 0;
+            left -= sg.n;
+            if (left > 0) {
+                c.next_item(a);
+                pid = page_of(c.u, live);
+                if (!keys) {  // the next segment's queries to L2
+                    constexpr int kLines = D * 2 / 128;
+                    const int r0 = c.rb * a.rows, n = min(a.rows, c.q.T * a.G - r0) * kLines;
+                    for (int i = lane; i < n; i += 32) {
+                        const int rr = r0 + i / kLines, t = div_g(a, rr);
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                            a.q + (long long)(c.q.first + t) * a.q_stride +
+                            (long long)(c.h * a.G + rr - t * a.G) * D + (i % kLines) * 64));
                     }
                 }
             }
-            left -= sg.n;
-            if (left > 0) c.next_item(a);
         }
-        if (*(volatile uint32_t *)&m->dead) {
-            // gave up: wait (bounded) for the copies in flight
-            for (int i = 1; i <= stages && i <= issued; ++i) {
-                const int n = issued - i;
-                tc05::mbar_wait(m->full + n % stages, (n / stages) & 1, kPoll / 64);
-            }
-        }
-    } else if (warp <= 10) {
+        if (!ok)  // gave up: wait (bounded) for this warp's copies in flight
+            for (int i = 0; i < stages; ++i)
+                if ((pending >> i) & 1u) tc05::mbar_wait(m->full + i, (pending_ph >> i) & 1u, kPoll / 64);
+    } else {
         // ------------------------------------------------------------ products
         // a warp a stream, so that one's waits pass under the other's products
         if (lane == 0) {
@@ -311,31 +311,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc05::mbar_wait(m->fin + s, 0, kPoll);
         }
         __syncwarp();
-    } else {
-        // ------------------------------------------------------------ next queries to L2
-        Cursor c;
-        c.start(a, sh);
-        int started = 0;
-        for (int left = units;;) {
-            left -= Segment(c, left).n;
-            if (left <= 0) break;
-            // a segment ahead at most (a hint only: past the limit it just stops)
-            ++started;
-            volatile int *now = &m->segments;
-            uint32_t i = 0;
-            while (*now < started && ++i < kPoll / 64) __nanosleep(256);
-            if (*now < started) break;
-            c.next_item(a);
-            constexpr int kLines = D * 2 / 128;
-            const int r0 = c.rb * a.rows, n = min(a.rows, c.q.T * a.G - r0) * kLines;
-            for (int i = lane; i < n; i += 32) {
-                const int rr = r0 + i / kLines, t = rr / a.G;
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(
-                    a.q + (long long)(c.q.first + t) * a.q_stride +
-                    (long long)(c.h * a.G + rr - t * a.G) * D + (i % kLines) * 64));
-            }
-        }
-        __syncwarp();
     }
     } else {
         // ------------------------------------------------------------ softmax
@@ -372,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint4 v[kLoads];  // all under way before the first is needed
 #pragma unroll
                 for (int i = 0; i < kLoads; ++i) {
-                    const int rr = min(rbase + r0 + i * kPass, nrows - 1), t = rr / a.G;
+                    const int rr = min(rbase + r0 + i * kPass, nrows - 1), t = div_g(a, rr);
                     v[i] = __ldg(reinterpret_cast<const uint4 *>(p + t * a.q_stride + (rr - t * a.G) * D));
                 }
 #pragma unroll
@@ -385,10 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             tc05::fence_proxy_async();
-            if (threadIdx.x == 0) {
-                m->tiles = sg.n;
-                *(volatile int *)&m->segments += 1;
-            }
+            if (threadIdx.x == 0) m->tiles = sg.n;
             mbar_arrive(&m->q_full);
             if (threadIdx.x < 8) m->nf[threadIdx.x] = 0;
             __syncwarp();
@@ -397,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int rbase = c.rb * a.rows + (kTwo ? s * 128 : 0);
             const int rr = rbase + tid;
             const bool row_live = rr < nrows, warp_live = rbase + wq * 32 < nrows;
-            const int t = row_live ? rr / a.G : 0;
+            const int t = row_live ? div_g(a, rr) : 0;
             float mx = -INFINITY, l = 0.f;  // mx: the maximum in use (log2 units)
 #pragma unroll 1
             for (int i = 0; i < ns; ++i) {

@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
         for (int e = 0; e < 2; ++e) {
             const int r = e * 8 + g;
             const bool have = r < nrows;
-            const int t = have ? r / a.G : 0;
+            const int t = have ? div_g(a, r) : 0;
             rt[e] = have ? t : -1;
             const uint16_t *p = a.q + (long long)(sq.first + t) * a.q_stride +
                                 (long long)(seg_h * a.G + (have ? r - t * a.G : 0)) * D;
@@ -413,7 +413,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
                 const float inv = L == 0.f ? 0.f : 1.f / L;
                 v.x *= inv;
                 v.y *= inv;
-                const int t = r / a.G;
+                const int t = div_g(a, r);
                 const long long row = (long long)(sq.first + t) * a.Hq + seg_h * a.G + r - t * a.G;
                 if (a.o_f32)
                     *reinterpret_cast<float2 *>(static_cast<float *>(a.o) + row * D + col) = v;
@@ -528,7 +528,7 @@ __global__ void __launch_bounds__(128 * kSplit) k_attn_join(const TreeArgs a, bo
     }
     if (!have_row) return;
     const float inv = L == 0.f ? 0.f : 1.f / L;
-    const int rr = rb * a.rows + r, t = rr / a.G;
+    const int rr = rb * a.rows + r, t = div_g(a, rr);
     const long long row = (long long)(q.first + t) * a.Hq + h * a.G + rr - t * a.G;
 #pragma unroll
     for (int i = 0; i < kCols; ++i) {
@@ -653,6 +653,7 @@ cudaError_t launch_attn_tree(const AttnCache &c, const TreeCall &t, cudaStream_t
     a.q = static_cast<const uint16_t *>(t.q);
     a.q_stride = t.q_stride;
     a.Hq = t.Hq; a.Hkv = c.Hkv; a.G = t.Hq / c.Hkv; a.pages = c.pages;
+    a.ginv = (uint32_t)(((1ull << 32) + a.G - 1) / a.G);
     a.mask = t.mask; a.words = t.words;
     a.sl2 = t.scale == 0.f ? 1.f : fabsf(t.scale) * kLog2e;
     a.qxor = t.scale < 0.f ? 0x80008000u : 0u;

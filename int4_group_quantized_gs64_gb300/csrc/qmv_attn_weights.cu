@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(256) k_weights_stash(const TreeArgs a, bool ve
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (!any) return;
     if (threadIdx.x < nrows) {
-        const int t = threadIdx.x / a.G;
+        const int t = div_g(a, threadIdx.x);
         e2[threadIdx.x] =
             a.lse[(long long)(q.first + t) * a.Hq + h * a.G + threadIdx.x - t * a.G] * kLog2e;
     }
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(256) k_weights_any(const TreeArgs a) {
         for (int e = 0; e < 2; ++e) {
             const int r = r0 + e * 8 + g;
             const bool have = r < nrows;
-            const int t = have ? r / a.G : 0;
+            const int t = have ? div_g(a, r) : 0;
             const int head = h * a.G + (have ? r - t * a.G : 0);
             rt[e] = t;
             e2[e] = have ? a.lse[(long long)(q.first + t) * a.Hq + head] * kLog2e : -INFINITY;
@@ -175,14 +175,14 @@ __global__ void __launch_bounds__(256) k_weights_any(const TreeArgs a) {
 
 // ------------------------------------------------------------------ many rows, tcgen05
 
-constexpr int kThreads = 320, kKeys = 128, kStages = 12, kSmemMax = 227 * 1024, kMaxRows = 512;
+constexpr int kThreads = 352, kKeys = 128, kStages = 12, kSmemMax = 227 * 1024, kMaxRows = 512;
 
-struct Misc {
+struct alignas(16) Misc {
     ShareScratch<kThreads / 32> share;
     uint64_t full[kStages], empty[kStages], s_full[4], s_free[4], q_full, fin;
     uint32_t tmem, dead;
     int tiles, row_tiles;
-    float nlse[kMaxRows];  // -lse in log2 units; -inf where a row has no weights
+    alignas(16) float nlse[kMaxRows];  // -lse in log2 units; -inf where a row has no weights
     uint32_t seen[2][8][128];  // of a tile with drafts: the drafts that see each key
 };
 constexpr int kMisc = 11264;
@@ -202,7 +202,7 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, Misc *m, in
 }
 
 // a.rows is so large that an item is a (sequence, head), and a.unit 128 keys.
-// Warps 0-3 and 4-7 take alternate key tiles, 8 copies them, 9 issues the
+// Warps 0-3 and 4-7 take alternate key tiles, 8 and 10 copy them, 9 issues the
 // products of a tile with every 128 queries into four score tiles of tensor
 // memory in turn.
 template <int D, bool kBf16>
@@ -244,48 +244,51 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = m->tmem;
     const int units = (int)(sh.u1 - sh.u0);
 
-    if (warp == 8) {
+    if (warp == 8 || warp == 10) {
+        // (two warps, a tile each in turn: with small pages one's issue does not keep up)
         const int prow = a.s.page < kKeys ? a.s.page : kKeys;
         Cursor c;
         c.start(a, sh);
-        int stage = 0, issued = 0;
-        uint32_t phase = 1;
-        for (int left = units; left > 0; --left) {
-            const int slot = c.u * kKeys + lane * prow;
-            const bool live = lane * prow < kKeys && slot < c.q.ctx + c.q.T;
-            const int pid =
-                live ? __ldg(a.s.table + (long long)c.b * a.s.max_pages + (slot >> a.s.lpage)) : -1;
-            const bool good = live && (unsigned)pid < (unsigned)a.pages;
-            const uint32_t n = __popc(__ballot_sync(0xFFFFFFFFu, good));
-            const bool ok = wait(m->empty + stage, phase, m, a.status);
-            if (!__all_sync(0xFFFFFFFFu, ok)) break;
-            if (lane == 0) {
-                if (n)
-                    mbar_expect_tx(m->full + stage, n * prow * D * 2);
-                else
-                    mbar_arrive(m->full + stage);
-            }
-            __syncwarp();
-            if (good) {
-                const int row = (pid * a.Hkv + c.h) * a.s.page + (slot & (a.s.page - 1));
-                const uint32_t dst = tc05::smem_addr(ring) + stage * kTile + lane * prow * 128;
+        int stage = 0;
+        uint32_t phase = 1, pending = 0, pending_ph = 0;
+        bool ok = true;
+        for (int x = 0; x < units; ++x) {
+            if ((x & 1) == (warp == 10)) {
+                const int slot = c.u * kKeys + lane * prow;
+                const bool live = lane * prow < kKeys && slot < c.q.ctx + c.q.T;
+                const int pid =
+                    live ? __ldg(a.s.table + (long long)c.b * a.s.max_pages + (slot >> a.s.lpage)) : -1;
+                const bool good = live && (unsigned)pid < (unsigned)a.pages;
+                const uint32_t n = __popc(__ballot_sync(0xFFFFFFFFu, good));
+                ok = ok && wait(m->empty + stage, phase, m, a.status);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) break;
+                if (lane == 0) {
+                    if (n)
+                        mbar_expect_tx(m->full + stage, n * prow * D * 2);
+                    else
+                        mbar_arrive(m->full + stage);
+                }
+                __syncwarp();
+                if (good) {
+                    const int row = (pid * a.Hkv + c.h) * a.s.page + (slot & (a.s.page - 1));
+                    const uint32_t dst = tc05::smem_addr(ring) + stage * kTile + lane * prow * 128;
 #pragma unroll
-                for (int hf = 0; hf < kHalves; ++hf)
-                    tma_load3(dst + hf * (kKeys * 128), &kmap, 0, row, hf, m->full + stage);
+                    for (int hf = 0; hf < kHalves; ++hf)
+                        tma_load3(dst + hf * (kKeys * 128), &kmap, 0, row, hf, m->full + stage);
+                }
+                pending |= 1u << stage;
+                pending_ph = (pending_ph & ~(1u << stage)) | ((phase ^ 1u) & 1u) << stage;
             }
-            ++issued;
             if (++stage == stages) {
                 stage = 0;
                 phase ^= 1;
             }
-            if (++c.u == c.nu && left > 1) c.next_item(a);
+            if (++c.u == c.nu && x + 1 < units) c.next_item(a);
         }
-        if (*(volatile uint32_t *)&m->dead) {
-            for (int i = 1; i <= stages && i <= issued; ++i) {
-                const int n = issued - i;
-                tc05::mbar_wait(m->full + n % stages, (n / stages) & 1, kPoll / 64);
-            }
-        }
+        if (!ok)  // gave up: wait (bounded) for this warp's copies in flight
+            for (int i = 0; i < stages; ++i)
+                if ((pending >> i) & 1u) tc05::mbar_wait(m->full + i, (pending_ph >> i) & 1u, kPoll / 64);
     } else if (warp == 9) {
         if (lane == 0) {
             const uint64_t kdesc = tc05::sdesc_sw128(tc05::smem_addr(ring));
@@ -351,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 128 / kPass; ++i) {
                     const int rr = min(rt * 128 + (int)threadIdx.x / kChunks + i * kPass, nrows - 1);
-                    const int t = rr / a.G;
+                    const int t = div_g(a, rr);
                     v[i] = __ldg(reinterpret_cast<const uint4 *>(p + t * a.q_stride + (rr - t * a.G) * D));
                 }
 #pragma unroll
@@ -374,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int r = threadIdx.x; r < nq * 128; r += 256) {
                 float e = -INFINITY;
                 if (r < nrows) {
-                    const int t = r / a.G;
+                    const int t = div_g(a, r);
                     e = -a.lse[(long long)(q.first + t) * a.Hq + c.h * a.G + r - t * a.G] * kLog2e;
                     if (e == INFINITY) e = -INFINITY;
                 }
@@ -416,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     tc05::fence_after_sync();
                     if (special) {  // scores of rows that do not see the key become -inf
-                        int tt = r * 128 / a.G, gg = r * 128 - tt * a.G;  // row's draft and head
+                        int tt = div_g(a, r * 128), gg = r * 128 - tt * a.G;  // row's draft and head
 #pragma unroll 1
                         for (int k = 0; k < 4; ++k) {
                             uint32_t x[32];
