@@ -249,42 +249,53 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int prow = a.s.page < kKeys ? a.s.page : kKeys;
         Cursor c;
         c.start(a, sh);
-        int stage = 0;
+        int stage = 0, x = 0;  // the tile that the cursor is at
         uint32_t phase = 1, pending = 0, pending_ph = 0;
         bool ok = true;
-        for (int x = 0; x < units; ++x) {
-            if ((x & 1) == (warp == 10)) {
-                const int slot = c.u * kKeys + lane * prow;
-                const bool live = lane * prow < kKeys && slot < c.q.ctx + c.q.T;
-                const int pid =
-                    live ? __ldg(a.s.table + (long long)c.b * a.s.max_pages + (slot >> a.s.lpage)) : -1;
-                const bool good = live && (unsigned)pid < (unsigned)a.pages;
-                const uint32_t n = __popc(__ballot_sync(0xFFFFFFFFu, good));
-                ok = ok && wait(m->empty + stage, phase, m, a.status);
-                ok = __all_sync(0xFFFFFFFFu, ok);
-                if (!ok) break;
-                if (lane == 0) {
-                    if (n)
-                        mbar_expect_tx(m->full + stage, n * prow * D * 2);
-                    else
-                        mbar_arrive(m->full + stage);
-                }
-                __syncwarp();
-                if (good) {
-                    const int row = (pid * a.Hkv + c.h) * a.s.page + (slot & (a.s.page - 1));
-                    const uint32_t dst = tc05::smem_addr(ring) + stage * kTile + lane * prow * 128;
-#pragma unroll
-                    for (int hf = 0; hf < kHalves; ++hf)
-                        tma_load3(dst + hf * (kKeys * 128), &kmap, 0, row, hf, m->full + stage);
-                }
-                pending |= 1u << stage;
-                pending_ph = (pending_ph & ~(1u << stage)) | ((phase ^ 1u) & 1u) << stage;
-            }
+        auto step = [&]() {
+            ++x;
             if (++stage == stages) {
                 stage = 0;
                 phase ^= 1;
             }
-            if (++c.u == c.nu && x + 1 < units) c.next_item(a);
+            if (++c.u == c.nu && x < units) c.next_item(a);
+        };
+        int slot = 0, pid = -1;
+        auto fetch = [&]() {  // this lane's piece of the cursor's tile: its page
+            slot = c.u * kKeys + lane * prow;
+            pid = lane * prow < kKeys && slot < c.q.ctx + c.q.T
+                      ? __ldg(a.s.table + (long long)c.b * a.s.max_pages + (slot >> a.s.lpage))
+                      : -1;
+        };
+        if (warp == 10) step();
+        if (x < units) fetch();
+        while (x < units) {
+            // this tile's, then the next one's page ids are under way
+            const bool good = (unsigned)pid < (unsigned)a.pages;
+            const int row = (pid * a.Hkv + c.h) * a.s.page + (slot & (a.s.page - 1)), st = stage;
+            const uint32_t ph = phase;
+            step();
+            if (x < units) step();
+            if (x < units) fetch();
+            const uint32_t n = __popc(__ballot_sync(0xFFFFFFFFu, good));
+            ok = wait(m->empty + st, ph, m, a.status);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok) break;
+            if (lane == 0) {
+                if (n)
+                    mbar_expect_tx(m->full + st, n * prow * D * 2);
+                else
+                    mbar_arrive(m->full + st);
+            }
+            __syncwarp();
+            if (good) {
+                const uint32_t dst = tc05::smem_addr(ring) + st * kTile + lane * prow * 128;
+#pragma unroll
+                for (int hf = 0; hf < kHalves; ++hf)
+                    tma_load3(dst + hf * (kKeys * 128), &kmap, 0, row, hf, m->full + st);
+            }
+            pending |= 1u << st;
+            pending_ph = (pending_ph & ~(1u << st)) | ((ph ^ 1u) & 1u) << st;
         }
         if (!ok)  // gave up: wait (bounded) for this warp's copies in flight
             for (int i = 0; i < stages; ++i)
@@ -385,16 +396,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             asm volatile("bar.sync 1, 256;" ::: "memory");
+            // a tile's page id is loaded two of this warpgroup's tiles ahead, its
+            // old sum one ahead
+            auto page_of = [&](int t) {
+                const int slot = (j0 + t) * kKeys + tid;
+                return t < n && slot < q.ctx + q.T
+                           ? __ldg(a.s.table + (long long)c.b * a.s.max_pages + (slot >> a.s.lpage))
+                           : -1;
+            };
+            auto place_of = [&](int t, int pid) {
+                const int slot = (j0 + t) * kKeys + tid;
+                return (unsigned)pid < (unsigned)a.pages
+                           ? ((long long)pid * a.Hkv + c.h) * a.s.page + (slot & (a.s.page - 1))
+                           : -1LL;
+            };
+            int pid1 = page_of(s + 2);
+            long long at1 = place_of(s, page_of(s));
+            float old1 = at1 >= 0 && a.acc_in ? a.acc_in[at1] : 0.f;
 #pragma unroll 1
             for (int t = s; t < n; t += 2) {
                 const int slot = (j0 + t) * kKeys + tid;
                 const int d = slot - q.ctx;  // this key's draft (negative: seen by all)
                 const bool special = (j0 + t + 1) * kKeys > q.ctx;
-                int pid = -1;
-                if (slot < q.ctx + q.T) pid = __ldg(a.s.table + (long long)c.b * a.s.max_pages + (slot >> a.s.lpage));
-                const bool good = (unsigned)pid < (unsigned)a.pages;
-                const long long at = ((long long)pid * a.Hkv + c.h) * a.s.page + (slot & (a.s.page - 1));
-                const float old = good && a.acc_in ? a.decay * a.acc_in[at] : 0.f;
+                const long long at = at1;
+                const float old = old1;
+                at1 = place_of(t + 2, pid1);
+                old1 = at1 >= 0 && a.acc_in ? a.acc_in[at1] : 0.f;
+                pid1 = page_of(t + 4);
                 if (special) {  // which drafts see this key, as bits
                     const bool all = d < 0 || !a.mask;
 #pragma unroll 1
@@ -459,11 +487,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(m->s_free + buf);
                 }
-                if (good) {
+                if (at >= 0) {
                     float s0, s1, s2, s3;
                     unpack_f32x2(sum[0], s0, s1);
                     unpack_f32x2(sum[1], s2, s3);
-                    a.acc_out[at] = old + ((s0 + s1) + (s2 + s3));
+                    a.acc_out[at] = a.decay * old + ((s0 + s1) + (s2 + s3));
                 }
             }
             __syncwarp();
