@@ -59,7 +59,7 @@ struct RowsShape {
     static constexpr int kStages = 3;
     static constexpr int kUnit = kWarps * kSub * 16;  // keys a unit
     static constexpr int kRing = kWarps * kStages * 2 * kSlice;
-    static constexpr int kBuf = kRows * D * 4;
+    static constexpr int kBuf = 2 * kRows * D * 4;    // two warps' sums
     static constexpr int kMl = kWarps * kRows * 8;
     static constexpr int kSmem =
         kRing + kBuf + kMl + kWarps * kStages * 12 + (int)sizeof(ShareScratch<kWarps>);
@@ -378,25 +378,44 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
                 o[n][2 * e + 1] *= f;
             }
         }
-        for (int w = 0; w < kWarps; ++w) {
-            if (warp == w) {
+        // (in pairs: 2 and 3 to 0 and 1, then 1 to 0; rows that do not exist are left out)
+        auto place = [&](int half, int e, int n) {
+            const int r = e * 8 + g;
+            return reinterpret_cast<float2 *>(buf + (half * kRows + r) * D +
+                                              ((n * 8 + c * 2) ^ ((r & 3) << 3)));
+        };
+        auto give = [&](int half) {
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
+            for (int e = 0; e < 2; ++e)
+                if (e * 8 < nrows)
+#pragma unroll
+                    for (int n = 0; n < D / 8; ++n)
+                        *place(half, e, n) = make_float2(o[n][2 * e], o[n][2 * e + 1]);
+        };
+        auto take = [&](int half) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                if (e * 8 < nrows) {
+                    float2 v[D / 8];
+#pragma unroll
+                    for (int n = 0; n < D / 8; ++n) v[n] = *place(half, e, n);
 #pragma unroll
                     for (int n = 0; n < D / 8; ++n) {
-                        const int r = e * 8 + g;
-                        float2 *p = reinterpret_cast<float2 *>(
-                            buf + r * D + ((n * 8 + c * 2) ^ ((r & 3) << 3)));
-                        float2 v = make_float2(o[n][2 * e], o[n][2 * e + 1]);
-                        if (w > 0) {
-                            v.x += p->x;
-                            v.y += p->y;
-                        }
-                        *p = v;
+                        o[n][2 * e] += v[n].x;
+                        o[n][2 * e + 1] += v[n].y;
                     }
-            }
-            __syncthreads();
+                }
+        };
+        if (warp >= 2) give(warp - 2);
+        __syncthreads();
+        if (warp < 2) take(warp);
+        if (warp == 1) give(1);
+        __syncthreads();
+        if (warp == 0) {
+            take(1);
+            give(0);
         }
+        __syncthreads();
         // rows out: two columns a thread
         for (int i = threadIdx.x; i < nrows * (D / 2); i += 32 * kWarps) {
             const int r = i / (D / 2), col = (i - r * (D / 2)) * 2;
