@@ -138,6 +138,22 @@ __device__ __forceinline__ void tma_load3(uint32_t dst, const CUtensorMap *map, 
         : "memory");
 }
 
+// The same, its lines the first to leave L2 (data read once).
+__device__ __forceinline__ void tma_load3_once(uint32_t dst, const CUtensorMap *map, int c0, int c1,
+                                               int c2, uint64_t *mbar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(tc05::smem_addr(mbar)),
+        "l"(policy)
+        : "memory");
+}
+__device__ __forceinline__ uint64_t evict_first_policy() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+
 __device__ __forceinline__ void mbar_expect_tx(uint64_t *mbar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(
                      tc05::smem_addr(mbar)),

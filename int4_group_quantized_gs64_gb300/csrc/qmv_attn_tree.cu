@@ -106,6 +106,9 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
     if (sh.u0 >= sh.u1) return;
     const int units = (int)(sh.u1 - sh.u0);  // (the launcher keeps this below 2^31)
 
+    // keys and values are read once here, and must not push the scores kept for
+    // the weights out of L2
+    const uint64_t policy = evict_first_policy();
     Cursor pc, cc;  // of the copies, of the products
     cc.start(a, sh);
     pc = cc;
@@ -140,8 +143,8 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
         if (good) {
             const int row = (pid * a.Hkv + pc.h) * a.s.page + (s0 & (a.s.page - 1));
             const uint32_t dst = ring + pstage * (2 * S::kSlice) + part * S::kPart;
-            tma_load3(dst, &kmap, 0, row, 0, br);
-            tma_load3(dst + S::kSlice, &vmap, 0, row, 0, br);
+            tma_load3_once(dst, &kmap, 0, row, 0, br, policy);
+            tma_load3_once(dst + S::kSlice, &vmap, 0, row, 0, br, policy);
         } else if (live) {
             set_status(a.status, kStPage);
         }
