@@ -40,14 +40,14 @@ namespace attn {
 namespace {
 
 constexpr int kThreads = 384, kKeys = 128, kMaxStages = 12;
-constexpr int kMisc = 2816;               // barriers and small tables
+constexpr int kMisc = 2880;               // barriers and small tables
 constexpr int kSmemMax = 227 * 1024;
 constexpr float kLazy = 8.f;              // log2 units the maximum may lag
 
 struct Misc {
     ShareScratch<kThreads / 32> share;
     uint64_t full[kMaxStages], empty[kMaxStages];
-    uint64_t s_full[2], p_ready[2], o_full[2], q_full, fin[2], turn[2];
+    uint64_t s_full[2], p_ready[2], o_full[2], q_full, fin[2], turn[2], s_free[2], pv_done[2];
     uint32_t tmem, dead;
     int tiles;             // of the segment whose queries are ready
     uint32_t nf[8];        // drafts with infinities or NaNs among their values
@@ -106,6 +106,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t kIdescO = tc05::idesc_f16kind_f32(kBf16, 128, D, true);
     extern __shared__ __align__(1024) uint8_t smem[];
     constexpr int lag = kTwo ? 1 : 2;  // tiles a product P V runs behind its Q K^T
+    // Tensor memory columns. Where they suffice (64 elements, one 16-bit number a
+    // weight) P lies apart from S, and a stream's next S is formed while its
+    // exponentials run (16 sequences of 8191 keys, 320 rows: 122 us, 150 with P
+    // over S; 64 sequences, 128 rows: 168 and 182). Otherwise P overwrites S.
+    constexpr bool kApart = D == 64 && !kSplit;
+    constexpr int kPcol = kApart ? 256 : 0, kPstep = kApart ? 64 : 128;   // P of stream s at kPcol + s * kPstep
+    constexpr int kOcol = kApart ? 384 : 256, kOstep = kApart ? 64 : 128;
+    // The ring's entries of a segment of n tiles: keys of the first `lag` tiles,
+    // then values of tile t and keys of tile t + lag by turns (apart: keys first).
+    auto entry_k = [](int t) { return t < lag ? t : 2 * t + (kApart ? 0 : 1) - lag; };
+    auto entry_v = [](int t, int n) { return min(t + lag + (kApart ? 1 : 0), n) + t; };
     uint8_t *qs = smem, *ring = smem + (kTwo ? 2 : 1) * kTile;
     Misc *m = reinterpret_cast<Misc *>(ring + stages * kTile);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -121,6 +132,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc05::mbar_init(m->o_full + s, 1);
             tc05::mbar_init(m->fin + s, 1);
             tc05::mbar_init(m->turn + s, 4);
+            tc05::mbar_init(m->s_free + s, 4);
+            tc05::mbar_init(m->pv_done + s, 1);
         }
         tc05::mbar_init(&m->q_full, 256);
         m->dead = 0;
@@ -157,6 +170,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // elements: a tile's eight copies take some 1,100 cycles)
         const bool keys = warp == 8;
         const CUtensorMap *map = keys ? &kmap : &vmap;
+        // read once: first to leave L2 (not by several row blocks, nor keys that
+        // the weights' pass reads again)
+        const bool once = a.max_rows <= a.rows && !(keys && a.acc_out);
+        const uint64_t policy = evict_first_policy();
         const int prow = a.s.page < kKeys ? a.s.page : kKeys;  // rows a copy
         Cursor c;
         c.start(a, sh);
@@ -184,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Segment sg(c, left);
 #pragma unroll 1
             for (int t = 0; t < sg.n; ++t) {
-                go(keys ? (t == 0 ? 0 : 2 * t + 1 - lag) : min(t + lag, sg.n) + t);
+                go(keys ? entry_k(t) : entry_v(t, sg.n));
                 const bool good = live && (unsigned)pid < (unsigned)a.pages;
                 const int row =
                     (pid * a.Hkv + c.h) * a.s.page + (((sg.j0 + t) * kKeys + lane * prow) & (a.s.page - 1));
@@ -205,7 +222,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t dst = tc05::smem_addr(ring) + stage * kTile + lane * prow * 128;
 #pragma unroll
                     for (int hf = 0; hf < kHalves; ++hf)
-                        tma_load3(dst + hf * (kKeys * 128), map, 0, row, hf, m->full + stage);
+                        if (once)
+                            tma_load3_once(dst + hf * (kKeys * 128), map, 0, row, hf, m->full + stage, policy);
+                        else
+                            tma_load3(dst + hf * (kKeys * 128), map, 0, row, hf, m->full + stage);
                 }
                 pending |= 1u << stage;
                 pending_ph = (pending_ph & ~(1u << stage)) | ((phase ^ 1u) & 1u) << stage;
@@ -240,9 +260,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t vdesc = tc05::sdesc_sw128_mn(tc05::smem_addr(ring), kKeys * 128);
             const uint64_t qdesc =
                 tc05::sdesc_sw128(tc05::smem_addr(qs)) + (uint32_t)((kTwo ? s : 0) * (kTile >> 4));
-            const uint32_t ts = tmem + s * 128, to = tmem + 256 + s * 128;
+            const uint32_t ts = tmem + s * 128, tp = tmem + kPcol + s * kPstep, to = tmem + kOcol + s * kOstep;
             int stage = 0, at = 0;                 // ring slot, and its place in the segment's entries
-            uint32_t ring_ph = 0, pp = 0, qp = 0;
+            uint32_t ring_ph = 0, pp = 0, qp = 0, fp = 0;
             bool live = true;
             auto go = [&](int pos) {  // to a later entry of the segment
                 stage += pos - at;
@@ -252,56 +272,65 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ring_ph ^= 1u;
                 }
             };
+            auto scores = [&](int t) {  // S = Q K^T
+                go(entry_k(t));
+                live = live && wait(m->full + stage, ring_ph, m, a.status);
+                if (!live) return;
+                const uint64_t kd = kdesc + (uint32_t)(stage * (kTile >> 4));
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const int of = ((k >> 2) * (kKeys * 128) + (k & 3) * 32) >> 4;
+                    tc05::mma_ss(ts, qdesc + of, kd + of, kIdescS, k > 0);
+                }
+                tc05::mma_commit(m->s_full + s);
+                tc05::mma_commit(m->empty + stage);
+            };
             for (int left = units; left > 0 && live;) {
                 live = wait(&m->q_full, qp, m, a.status);
                 qp ^= 1u;
                 const int n = *(volatile int *)&m->tiles;
                 left -= n;
-                // S = Q K^T of tile t, then O (+)= P V of it while the softmax
-                // of the other stream runs, and S of the stream's next tile
                 constexpr int kStep = kTwo ? 1 : 2;
                 const int t0 = kTwo ? 0 : s;
+                if (t0 < n) scores(t0);
 #pragma unroll 1
-                for (int t = t0; t < n + kStep && live; t += kStep) {
-                    if (t > t0) {
-                        const int tv = t - kStep;
-                        go(min(tv + lag, n) + tv);
-                        // With alternate tiles the weights first: the slot's last
-                        // entry may be the other stream's, and a phase that is two
-                        // behind looks like the awaited one. Once tile tv has its
-                        // weights the other stream is past that entry (the turns).
-                        if (kTwo) live = wait(m->full + stage, ring_ph, m, a.status);
-                        live = live && wait(m->p_ready + s, pp, m, a.status);
-                        if (!kTwo) live = live && wait(m->full + stage, ring_ph, m, a.status);
-                        if (!live) break;
-                        pp ^= 1u;
+                for (int t = t0; t < n && live; t += kStep) {
+                    // S of the stream's next tile, once its softmax holds this one's
+                    if (kApart && t + kStep < n) {
+                        live = wait(m->s_free + s, fp, m, a.status);
+                        fp ^= 1u;
                         tc05::fence_after_sync();
-                        const uint64_t v = vdesc + (uint32_t)(stage * (kTile >> 4));
-#pragma unroll
-                        for (int part = 0; part < (kSplit ? 2 : 1); ++part)
-#pragma unroll
-                            for (int k = 0; k < kKeys / 16; ++k)
-                                tc05::mma_ts(to, ts + part * 64 + k * 8, v + k * (2048 >> 4), kIdescO,
-                                             !(tv == t0 && part == 0 && k == 0));
-                        tc05::mma_commit(m->empty + stage);
-                        if (t >= n) {
-                            tc05::mma_commit(m->o_full + s);
-                            break;
-                        }
-                    } else if (t >= n) {
-                        break;  // no tile for this stream
+                        scores(t + kStep);
                     }
-                    go(t == 0 ? 0 : 2 * t + 1 - lag);
-                    live = wait(m->full + stage, ring_ph, m, a.status);
+                    // O (+)= P V
+                    go(entry_v(t, n));
+                    // With alternate tiles the weights first: the slot's last
+                    // entry may be the other stream's, and a phase that is two
+                    // behind looks like the awaited one. Once tile t has its
+                    // weights the other stream is past that entry (the turns).
+                    if (kTwo) live = live && wait(m->full + stage, ring_ph, m, a.status);
+                    live = live && wait(m->p_ready + s, pp, m, a.status);
+                    if (!kTwo) live = live && wait(m->full + stage, ring_ph, m, a.status);
                     if (!live) break;
-                    const uint64_t kd = kdesc + (uint32_t)(stage * (kTile >> 4));
+                    pp ^= 1u;
+                    tc05::fence_after_sync();
+                    const uint64_t v = vdesc + (uint32_t)(stage * (kTile >> 4));
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const int of = ((k >> 2) * (kKeys * 128) + (k & 3) * 32) >> 4;
-                        tc05::mma_ss(ts, qdesc + of, kd + of, kIdescS, k > 0);
-                    }
-                    tc05::mma_commit(m->s_full + s);
+                    for (int part = 0; part < (kSplit ? 2 : 1); ++part)
+#pragma unroll
+                        for (int k = 0; k < kKeys / 16; ++k)
+                            tc05::mma_ts(to, tp + part * 64 + k * 8, v + k * (2048 >> 4), kIdescO,
+                                         !(t == t0 && part == 0 && k == 0));
                     tc05::mma_commit(m->empty + stage);
+                    if (kApart) tc05::mma_commit(m->pv_done + s);
+                    if (t + kStep >= n)
+                        tc05::mma_commit(m->o_full + s);
+                    else if (!kApart)
+                        scores(t + kStep);
+                }
+                if (kApart && live && t0 < n) {  // (the last tile's hand-over, with nothing to follow)
+                    live = wait(m->s_free + s, fp, m, a.status);
+                    fp ^= 1u;
                 }
                 go(2 * n);
                 at = 0;
@@ -317,10 +346,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int s = warp >> 2, tid = threadIdx.x & 127, wq = warp & 3;
         const uint32_t lanes = (uint32_t)(wq * 32) << 16;
-        const uint32_t ts = tmem + lanes + s * 128, to = tmem + lanes + 256;
-        uint32_t sp = 0, op = 0, tp = 0;
+        const uint32_t ts = tmem + lanes + s * 128, to = tmem + lanes + kOcol;
+        const uint32_t tw = tmem + lanes + kPcol + s * kPstep;  // weights
+        uint32_t sp = 0, op = 0, tp = 0, vp = 0;
         Cursor c;
         c.start(a, sh);
+        // this thread's 16-byte pieces of a segment's queries, loaded a segment ahead
+        constexpr int kChunks = D / 8, kPass = 128 / kChunks;  // rows a pass of this warpgroup
+        constexpr int kLoads = (kTwo ? 128 : 64) / kPass;
+        const int qch = tid % kChunks, qr0 = (kTwo ? 0 : s * 64) + tid / kChunks;
+        uint4 qv[kLoads];
+        auto load_queries = [&](const Cursor &k) {
+            const int rbase = k.rb * a.rows + (kTwo ? s * 128 : 0), last = k.q.T * a.G - 1;
+            const uint16_t *p =
+                a.q + (long long)k.q.first * a.q_stride + (long long)k.h * a.G * D + qch * 8;
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int rr = min(rbase + qr0 + i * kPass, last), t = div_g(a, rr);
+                qv[i] = __ldg(reinterpret_cast<const uint4 *>(p + t * a.q_stride + (rr - t * a.G) * D));
+            }
+        };
+        constexpr bool kAhead = kLoads <= 8;  // (16 pieces would push other values to local memory)
+        if (kAhead) load_queries(c);
         const float boost = kBf16 ? 0.f : 7.f;
         for (int left = units; left > 0;) {
             const Segment sg(c, left);
@@ -337,26 +384,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     bad |= (unsigned)trow[p] >= (unsigned)a.pages;
             }
             // ---- queries to shared memory, rows in the products' order
+            if (!kAhead) load_queries(c);
             {
-                constexpr int kChunks = D / 8, kPass = 128 / kChunks;  // rows a pass of this warpgroup
-                const int ch = tid % kChunks, rbase = c.rb * a.rows + (kTwo ? s * 128 : 0);
-                const int r0 = (kTwo ? 0 : s * 64) + tid / kChunks;
-                uint8_t *dst = qs + (kTwo ? s * kTile : 0) + (ch >> 3) * (kKeys * 128);
-                const uint16_t *p = a.q + (long long)q.first * a.q_stride + (long long)c.h * a.G * D + ch * 8;
-                constexpr int kLoads = (kTwo ? 128 : 64) / kPass;
-                uint4 v[kLoads];  // all under way before the first is needed
+                const int rbase = c.rb * a.rows + (kTwo ? s * 128 : 0);
+                uint8_t *dst = qs + (kTwo ? s * kTile : 0) + (qch >> 3) * (kKeys * 128);
 #pragma unroll
                 for (int i = 0; i < kLoads; ++i) {
-                    const int rr = min(rbase + r0 + i * kPass, nrows - 1), t = div_g(a, rr);
-                    v[i] = __ldg(reinterpret_cast<const uint4 *>(p + t * a.q_stride + (rr - t * a.G) * D));
-                }
-#pragma unroll
-                for (int i = 0; i < kLoads; ++i) {
-                    const int r = r0 + i * kPass;
+                    const int r = qr0 + i * kPass;
                     const uint32_t keep = rbase + r < nrows ? a.qand : 0u;
-                    *reinterpret_cast<uint4 *>(dst + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) =
-                        make_uint4((v[i].x ^ a.qxor) & keep, (v[i].y ^ a.qxor) & keep,
-                                   (v[i].z ^ a.qxor) & keep, (v[i].w ^ a.qxor) & keep);
+                    *reinterpret_cast<uint4 *>(dst + r * 128 + (((qch & 7) ^ (r & 7)) << 4)) =
+                        make_uint4((qv[i].x ^ a.qxor) & keep, (qv[i].y ^ a.qxor) & keep,
+                                   (qv[i].z ^ a.qxor) & keep, (qv[i].w ^ a.qxor) & keep);
                 }
             }
             tc05::fence_proxy_async();
@@ -394,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // a draft's infinities and NaNs noted and replaced.
                     // (Two ring entries a tile of the segments before; in its
                     // turn, since then the slot's last entry has been used.)
-                    const long long pos = 2LL * (units - left) + min(tile + lag, sg.n) + tile;
+                    const long long pos = 2LL * (units - left) + entry_v(tile, sg.n);
                     const int vst = (int)(pos % stages);
                     if (wait(m->full + vst, (uint32_t)(pos / stages) & 1u, m, a.status)) {
                         const int key = j * kKeys + tid;
@@ -425,6 +463,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc05::fence_proxy_async();
                 }
                 __syncwarp();
+                auto hand_over = [&]() {  // the scores are in registers: S is free, and the turn passes
+                    tc05::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(m->turn + (s ^ 1));
+                        mbar_arrive(m->s_free + s);
+                    }
+                };
+                // P is free again, and O complete so far. Warps without rows wait
+                // too: the next scores come before this tile's weights are all in,
+                // and a second arrival of such a warp would stand for a slow one's.
+                auto products_done = [&]() {
+                    wait(m->pv_done + s, vp, m, a.status);
+                    __syncwarp();
+                    tc05::fence_after_sync();
+                    vp ^= 1u;
+                };
                 if (warp_live) {
                     if (special) {  // scores that a row must not see become -inf
                         uint32_t see[4];
@@ -456,6 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) tc05::tmem_ld32(ts + k * 32, x[k]);
                     tc05::tmem_wait_ld();
+                    if (kApart) hand_over();
                     float v[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(x[0][e]);
@@ -463,6 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int e = 4; e < 128; ++e)
                         v[e & 3] = fmaxf(v[e & 3], __uint_as_float(x[e >> 5][e & 31]));
                     const float tm = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])) * a.sl2;
+                    if (kApart && i > 0) products_done();
                     const bool move = tm > mx + kLazy || (mx == -INFINITY && tm > mx);
                     if (__any_sync(0xFFFFFFFFu, move)) {
                         const float al = move ? ex2(mx - tm) : 1.f;
@@ -474,12 +531,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                             for (int k = 0; k < D / 16; ++k) {
                                 uint32_t o[16];
-                                tc05::tmem_ld16(to + s * 128 + k * 16, o);
+                                tc05::tmem_ld16(to + s * kOstep + k * 16, o);
                                 tc05::tmem_wait_ld();
 #pragma unroll
                                 for (int e = 0; e < 16; ++e)
                                     o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
-                                tc05::tmem_st16(to + s * 128 + k * 16, o);
+                                tc05::tmem_st16(to + s * kOstep + k * 16, o);
                             }
                         }
                     }
@@ -503,25 +560,38 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 lo[e] = pack2<kBf16>(p0 - f.x, p1 - f.y);
                             }
                         }
-                        tc05::tmem_st16(ts + h * 16, hi);
-                        if (kSplit) tc05::tmem_st16(ts + 64 + h * 16, lo);
+                        tc05::tmem_st16(tw + h * 16, hi);
+                        if (kSplit) tc05::tmem_st16(tw + 64 + h * 16, lo);
                     }
                     float s0, s1, s2, s3;
                     unpack_f32x2(sum[0], s0, s1);
                     unpack_f32x2(sum[1], s2, s3);
                     l += (s0 + s1) + (s2 + s3);
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(m->turn + (s ^ 1));
+                if (kApart) {
+                    if (!warp_live) {
+                        hand_over();
+                        if (i > 0) products_done();
+                    }
+                } else {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(m->turn + (s ^ 1));
+                }
                 tc05::tmem_wait_st();
                 tc05::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(m->p_ready + s);
             }
             // ---- the segment's end
+            Cursor next = c;
+            if (left > sg.n) {
+                next.next_item(a);
+                if (kAhead) load_queries(next);
+            }
             if (ns > 0) {
                 wait(m->o_full + s, op, m, a.status);
                 op ^= 1;
+                if (kApart) vp ^= 1u;  // the last product's, which o_full covers
             }
             __syncwarp();
             if (mx != -INFINITY) mx -= boost;
@@ -549,13 +619,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int k = k0; k < k1; ++k) {  // 32 columns at a time
                     float o[32];
                     __syncwarp();
-                    tc05::tmem_ld32(to + (kTwo ? s * 128 : 0) + k * 32,
+                    tc05::tmem_ld32(to + (kTwo ? s * kOstep : 0) + k * 32,
                                     *reinterpret_cast<uint32_t(*)[32]>(o));
                     tc05::tmem_wait_ld();
                     if (!kTwo) {
                         float o1[32];
                         if (has1) {
-                            tc05::tmem_ld32(to + 128 + k * 32, *reinterpret_cast<uint32_t(*)[32]>(o1));
+                            tc05::tmem_ld32(to + kOstep + k * 32, *reinterpret_cast<uint32_t(*)[32]>(o1));
                             tc05::tmem_wait_ld();
                         }
 #pragma unroll
@@ -617,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the other stream passed the turn once a tile of its own
             tp ^= (uint32_t)(kTwo ? sg.n : (sg.n + s) / 2) & 1u;
             left -= sg.n;
-            if (left > 0) c.next_item(a);
+            c = next;
         }
     }
     tc05::fence_before_sync();

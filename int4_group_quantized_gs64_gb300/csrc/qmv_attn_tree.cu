@@ -189,6 +189,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
                 qf[k][e + 2] = have ? (w[4] ^ a.qxor) & a.qand : 0u;
             }
         }
+        float *kept = a.stash ? stash_at(a, seg_b, seg_h, 0) + g * 16 + c * 2 : nullptr;
         float o[D / 8][4];
         float mx[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
@@ -299,7 +300,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
 #pragma unroll
                             for (int j = 0; j < kSub; ++j)
                                 if (kSub == 1 || s0 + j * 16 < sq.ctx + sq.T) {
-                                    float *p = stash_at(a, seg_b, seg_h, s0 + j * 16) + (e * 8 + g) * 16 + c * 2;
+                                    float *p = kept + (long long)((s0 >> 4) + j) * (a.max_rows * 16) + e * 128;
                                     *reinterpret_cast<float2 *>(p) = make_float2(s[2 * j][2 * e], s[2 * j][2 * e + 1]);
                                     *reinterpret_cast<float2 *>(p + 8) =
                                         make_float2(s[2 * j + 1][2 * e], s[2 * j + 1][2 * e + 1]);
