@@ -24,9 +24,12 @@
 // since moving it means rescaling O in tensor memory.
 //
 // Weights are rounded once to 16 bits for a 16-bit output (half a step of the
-// type, like the output's own rounding, and averaged over the keys); for an
-// fp32 output they are carried as two 16-bit numbers. fp16 weights are held
-// 2^7 times larger: the small ones would lose bits below fp16's range.
+// type, like the output's own rounding, and averaged over the keys). For an
+// fp32 output they are carried as two fp16 or three bf16 numbers (two bf16 ones:
+// 2.3e-6 of the output's norm; fp32 weights and sums: 1.5e-6), and O is summed up
+// in registers, tile by tile: a product's own sums cut off what falls below
+// their last bit, which over 8191 keys came to 1.1e-5 of the norm. fp16 weights are held 2^7 times larger: the
+// small ones would lose bits below fp16's range.
 #include <string.h>
 
 #include "qmv_attn.cuh"
@@ -86,6 +89,14 @@ __device__ __forceinline__ bool pair_or(bool p) {
     return r != 0;
 }
 
+// The upper halves of two floats, which are bf16 numbers, and what they leave.
+__device__ __forceinline__ uint32_t cut_bf16x2(float &x, float &y) {
+    const uint32_t u = __float_as_uint(x), v = __float_as_uint(y);
+    x -= __uint_as_float(u & 0xFFFF0000u);
+    y -= __uint_as_float(v & 0xFFFF0000u);
+    return __byte_perm(u, v, 0x7632);
+}
+
 // A block's part of an item: tiles [j0, j0 + n) of the item's keys.
 struct Segment {
     int j0, n;
@@ -111,6 +122,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     // exponentials run (16 sequences of 8191 keys, 320 rows: 122 us, 150 with P
     // over S; 64 sequences, 128 rows: 168 and 182). Otherwise P overwrites S.
     constexpr bool kApart = D == 64 && !kSplit;
+    // The third number of a bf16 weight: in columns that O leaves, or over the
+    // other two once their products are done.
+    constexpr bool kThird = kSplit && kBf16, kAfter = kThird && D == 128;
+    // The turn passes once the maximum is known, not after the exponentials
+    // (21-node trees over 16 x 6000 keys: 83 us and 98; 128 elements, whose O
+    // fills the registers: 316 us and 326 for 256 rows over 16 x 8191 keys).
+    constexpr bool kEarly = kSplit && D == 64;
     constexpr int kPcol = kApart ? 256 : 0, kPstep = kApart ? 64 : 128;   // P of stream s at kPcol + s * kPstep
     constexpr int kOcol = kApart ? 384 : 256, kOstep = kApart ? 64 : 128;
     // The ring's entries of a segment of n tiles: keys of the first `lag` tiles,
@@ -315,14 +333,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                     pp ^= 1u;
                     tc05::fence_after_sync();
                     const uint64_t v = vdesc + (uint32_t)(stage * (kTile >> 4));
+                    if (kSplit) {  // the rests, then the weights: a sum of this tile alone
+                        if (kThird && !kAfter)
 #pragma unroll
-                    for (int part = 0; part < (kSplit ? 2 : 1); ++part)
+                            for (int k = 0; k < kKeys / 16; ++k)
+                                tc05::mma_ts(to, to + 64 + k * 8, v + k * (2048 >> 4), kIdescO, k > 0);
+#pragma unroll
+                        for (int i = 0; i < kKeys / 8; ++i) {
+                            const int k = i & (kKeys / 16 - 1), rest = i < kKeys / 16 ? 16 : 0;
+                            tc05::mma_ts(to, tp + (k >> 1) * 32 + rest + (k & 1) * 8, v + k * (2048 >> 4),
+                                         kIdescO, (kThird && !kAfter) || i > 0);
+                        }
+                        if (kAfter) {
+                            tc05::mma_commit(m->pv_done + s);
+                            live = wait(m->p_ready + s, pp, m, a.status);
+                            if (!live) break;
+                            pp ^= 1u;
+                            tc05::fence_after_sync();
+#pragma unroll
+                            for (int k = 0; k < kKeys / 16; ++k)
+                                tc05::mma_ts(to, tp + k * 8, v + k * (2048 >> 4), kIdescO, 1);
+                        }
+                    } else
 #pragma unroll
                         for (int k = 0; k < kKeys / 16; ++k)
-                            tc05::mma_ts(to, tp + part * 64 + k * 8, v + k * (2048 >> 4), kIdescO,
-                                         !(t == t0 && part == 0 && k == 0));
+                            tc05::mma_ts(to, tp + k * 8, v + k * (2048 >> 4), kIdescO, !(t == t0 && k == 0));
                     tc05::mma_commit(m->empty + stage);
-                    if (kApart) tc05::mma_commit(m->pv_done + s);
+                    if (kApart || kSplit) tc05::mma_commit(m->pv_done + s);
                     if (t + kStep >= n)
                         tc05::mma_commit(m->o_full + s);
                     else if (!kApart)
@@ -409,6 +446,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool row_live = rr < nrows, warp_live = rbase + wq * 32 < nrows;
             const int t = row_live ? div_g(a, rr) : 0;
             float mx = -INFINITY, l = 0.f;  // mx: the maximum in use (log2 units)
+            uint64_t acc[kSplit ? D / 2 : 1];  // for an fp32 output: O, two columns each
+            if (kSplit)
+#pragma unroll
+                for (int e = 0; e < D / 2; ++e) acc[e] = 0;
 #pragma unroll 1
             for (int i = 0; i < ns; ++i) {
                 const int tile = kTwo ? i : 2 * i + s, j = sg.j0 + tile;
@@ -463,6 +504,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc05::fence_proxy_async();
                 }
                 __syncwarp();
+                auto pass_turn = [&]() {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(m->turn + (s ^ 1));
+                };
                 auto hand_over = [&]() {  // the scores are in registers: S is free, and the turn passes
                     tc05::fence_before_sync();
                     __syncwarp();
@@ -472,14 +517,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 };
                 // P is free again, and O complete so far. Warps without rows wait
-                // too: the next scores come before this tile's weights are all in,
-                // and a second arrival of such a warp would stand for a slow one's.
+                // too: nothing else keeps their next arrival with weights behind
+                // the others' last, and it would stand for a slow warp's.
                 auto products_done = [&]() {
                     wait(m->pv_done + s, vp, m, a.status);
                     __syncwarp();
                     tc05::fence_after_sync();
                     vp ^= 1u;
                 };
+                uint32_t third[kAfter ? 4 : 1][16];
                 if (warp_live) {
                     if (special) {  // scores that a row must not see become -inf
                         uint32_t see[4];
@@ -507,6 +553,60 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         tc05::tmem_wait_st();
                     }
+                    // two elements an instruction: weight = 2^(s * sl2 - base)
+                    const uint64_t sl2 = pack_f32x2(a.sl2, a.sl2);
+                    uint64_t sum[2] = {0, 0};
+                    if constexpr (kSplit) {
+                        // The scores twice from tensor memory, 32 at a time: O has the registers.
+                        float tm = -INFINITY;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t x[32];
+                            tc05::tmem_ld32(ts + k * 32, x);
+                            tc05::tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) tm = fmaxf(tm, __uint_as_float(x[e]));
+                        }
+                        tm *= a.sl2;
+                        if (kEarly) pass_turn();
+                        const bool move = tm > mx + kLazy || (mx == -INFINITY && tm > mx);
+                        if (__any_sync(0xFFFFFFFFu, move)) {
+                            const float al = move ? ex2(mx - tm) : 1.f;
+                            if (move) mx = tm;
+                            l *= al;
+                            const uint64_t al2 = pack_f32x2(al, al);
+#pragma unroll
+                            for (int e = 0; e < D / 2; ++e) acc[e] = fma_f32x2(acc[e], al2, 0);
+                        }
+                        const float base = mx == -INFINITY ? 0.f : mx - boost;
+                        const uint64_t nb = pack_f32x2(-base, -base);
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            uint32_t x[32], hi[16], lo[16], (&th)[16] = third[kAfter ? h : 0];
+                            tc05::tmem_ld32(ts + h * 32, x);
+                            tc05::tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                float p0, p1;
+                                unpack_f32x2(fma_f32x2(pack_u32x2(x[2 * e], x[2 * e + 1]), sl2, nb), p0, p1);
+                                p0 = ex2(p0);
+                                p1 = ex2(p1);
+                                sum[e & 1] = add_f32x2(sum[e & 1], pack_f32x2(p0, p1));
+                                if (kThird) {  // cut, not rounded: 3 x 8 bits hold all 24
+                                    hi[e] = cut_bf16x2(p0, p1);
+                                    lo[e] = cut_bf16x2(p0, p1);
+                                    th[e] = cut_bf16x2(p0, p1);
+                                } else {
+                                    hi[e] = pack2<kBf16>(p0, p1);
+                                    const float2 f = unpack2<kBf16>(hi[e]);
+                                    lo[e] = pack2<kBf16>(p0 - f.x, p1 - f.y);
+                                }
+                            }
+                            tc05::tmem_st16(tw + h * 32, hi);
+                            tc05::tmem_st16(tw + h * 32 + 16, lo);
+                            if (kThird && !kAfter) tc05::tmem_st16(to + s * kOstep + 64 + h * 16, th);
+                        }
+                    } else {
                     uint32_t x[4][32];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) tc05::tmem_ld32(ts + k * 32, x[k]);
@@ -541,12 +641,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     const float base = mx == -INFINITY ? 0.f : mx - boost;
-                    // two elements an instruction: weight = 2^(s * sl2 - base)
-                    const uint64_t sl2 = pack_f32x2(a.sl2, a.sl2), nb = pack_f32x2(-base, -base);
-                    uint64_t sum[2] = {0, 0};
+                    const uint64_t nb = pack_f32x2(-base, -base);
 #pragma unroll
                     for (int h = 0; h < 4; ++h) {
-                        uint32_t hi[16], lo[16];
+                        uint32_t hi[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             float p0, p1;
@@ -555,13 +653,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             p1 = ex2(p1);
                             sum[e & 1] = add_f32x2(sum[e & 1], pack_f32x2(p0, p1));
                             hi[e] = pack2<kBf16>(p0, p1);
-                            if (kSplit) {
-                                const float2 f = unpack2<kBf16>(hi[e]);
-                                lo[e] = pack2<kBf16>(p0 - f.x, p1 - f.y);
-                            }
                         }
                         tc05::tmem_st16(tw + h * 16, hi);
-                        if (kSplit) tc05::tmem_st16(tw + 64 + h * 16, lo);
+                    }
                     }
                     float s0, s1, s2, s3;
                     unpack_f32x2(sum[0], s0, s1);
@@ -573,14 +667,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                         hand_over();
                         if (i > 0) products_done();
                     }
-                } else {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(m->turn + (s ^ 1));
+                } else if (!kEarly || !warp_live) {
+                    pass_turn();
                 }
                 tc05::tmem_wait_st();
                 tc05::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(m->p_ready + s);
+                if constexpr (kAfter) {
+                    products_done();
+                    if (warp_live)
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) tc05::tmem_st16(tw + h * 16, third[h]);
+                    tc05::tmem_wait_st();
+                    tc05::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(m->p_ready + s);
+                }
+                if constexpr (kSplit) {  // this tile's share of O
+                    products_done();
+                    if (warp_live)
+#pragma unroll
+                        for (int k = 0; k < D / 32; ++k) {
+                            uint32_t o[32];
+                            tc05::tmem_ld32(to + s * kOstep + k * 32, o);
+                            tc05::tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                acc[k * 16 + e] = add_f32x2(acc[k * 16 + e], pack_u32x2(o[2 * e], o[2 * e + 1]));
+                        }
+                }
             }
             // ---- the segment's end
             Cursor next = c;
@@ -592,6 +708,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 wait(m->o_full + s, op, m, a.status);
                 op ^= 1;
                 if (kApart) vp ^= 1u;  // the last product's, which o_full covers
+                if constexpr (kSplit) {
+                    __syncwarp();
+                    tc05::fence_after_sync();
+#pragma unroll
+                    for (int k = 0; k < D / 32; ++k) {
+                        float o[32];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) unpack_f32x2(acc[k * 16 + e], o[2 * e], o[2 * e + 1]);
+                        tc05::tmem_st32(to + s * kOstep + k * 32, *reinterpret_cast<uint32_t(*)[32]>(o));
+                    }
+                    tc05::tmem_wait_st();
+                    tc05::fence_before_sync();
+                }
             }
             __syncwarp();
             if (mx != -INFINITY) mx -= boost;

@@ -48,8 +48,13 @@ __device__ __forceinline__ uint32_t slice_ofs(int r, int c) {
 // takes 248, 64 sequences of 8191 keys: registers leave one block an SM.)
 //
 // The exponentials go to the second product as two 16-bit numbers each (the
-// rounded value and the rounded rest), so the output carries no more than its
-// own rounding; the extra products are free next to the copies.
+// rounded value and the rounded rest), so that a 16-bit output carries no more
+// than its own rounding; the extra products are free next to the copies. For an
+// fp32 output (kExact) there is a third bf16 number, and a slice's products are
+// summed up by themselves and then added: the MMA cuts off what falls below its
+// sum's last bit, and with that carried along all keys the output was three
+// times as far off as with fp32 sums (one token over 200,000 keys: 3.9e-6 of the
+// output's norm, against 1.4e-6).
 constexpr int kRows = 16, kWarps = 4;
 template <int D>
 struct RowsShape {
@@ -65,7 +70,7 @@ struct RowsShape {
         kRing + kBuf + kMl + kWarps * kStages * 12 + (int)sizeof(ShareScratch<kWarps>);
 };
 
-template <int D, bool kBf16>
+template <int D, bool kBf16, bool kExact>
 __global__ void __launch_bounds__(32 * kWarps, 2)
     k_attn_rows(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                 const TreeArgs a) {
@@ -306,7 +311,8 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
                                         make_float2(s[2 * j + 1][2 * e], s[2 * j + 1][2 * e + 1]);
                                 }
                 }
-                uint32_t ph[kSub][4], pl[kSub][4];
+                constexpr int kTerms = kExact && kBf16 ? 3 : 2;
+                uint32_t ph[kTerms][kSub][4];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     float t = -INFINITY;
@@ -329,26 +335,41 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
                     const float base = mx[e] == -INFINITY ? 0.f : mx[e] - kBoost;
 #pragma unroll
                     for (int n = 0; n < kNt; ++n) {
-                        const float p0 = ex2(fmaf(s[n][2 * e], a.sl2, -base));
-                        const float p1 = ex2(fmaf(s[n][2 * e + 1], a.sl2, -base));
+                        float p0 = ex2(fmaf(s[n][2 * e], a.sl2, -base));
+                        float p1 = ex2(fmaf(s[n][2 * e + 1], a.sl2, -base));
                         l[e] += p0 + p1;
-                        const uint32_t hi = pack2<kBf16>(p0, p1);
-                        const float2 f = unpack2<kBf16>(hi);
-                        ph[n >> 1][2 * (n & 1) + e] = hi;
-                        pl[n >> 1][2 * (n & 1) + e] = pack2<kBf16>(p0 - f.x, p1 - f.y);
+#pragma unroll
+                        for (int i = 0; i < kTerms; ++i) {
+                            const uint32_t w = pack2<kBf16>(p0, p1);
+                            const float2 f = unpack2<kBf16>(w);
+                            ph[i][n >> 1][2 * (n & 1) + e] = w;
+                            p0 -= f.x;
+                            p1 -= f.y;
+                        }
                     }
                 }
 #pragma unroll
-                for (int k = 0; k < KK; ++k)
+                for (int k = 0; k < KK; ++k) {
+                    float part[2][4] = {};
+                    float(&o0)[4] = kExact ? part[0] : o[2 * k], (&o1)[4] = kExact ? part[1] : o[2 * k + 1];
+                    uint32_t vb[kSub][4];
 #pragma unroll
-                    for (int j = 0; j < kSub; ++j) {
-                        uint32_t vb[4];
-                        ldmatrix4_trans(vb, vs + j * S::kPart + slice_ofs<16>(vkey, 2 * k + vchk));
-                        mma16816<kBf16>(o[2 * k], ph[j], vb[0], vb[1]);
-                        mma16816<kBf16>(o[2 * k + 1], ph[j], vb[2], vb[3]);
-                        mma16816<kBf16>(o[2 * k], pl[j], vb[0], vb[1]);
-                        mma16816<kBf16>(o[2 * k + 1], pl[j], vb[2], vb[3]);
-                    }
+                    for (int j = 0; j < kSub; ++j)
+                        ldmatrix4_trans(vb[j], vs + j * S::kPart + slice_ofs<16>(vkey, 2 * k + vchk));
+#pragma unroll
+                    for (int i = kTerms - 1; i >= 0; --i)  // small ones first
+#pragma unroll
+                        for (int j = 0; j < kSub; ++j) {
+                            mma16816<kBf16>(o0, ph[i][j], vb[j][0], vb[j][1]);
+                            mma16816<kBf16>(o1, ph[i][j], vb[j][2], vb[j][3]);
+                        }
+                    if (kExact)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            o[2 * k][i] += o0[i];
+                            o[2 * k + 1][i] += o1[i];
+                        }
+                }
             }
             __syncwarp();  // the slot may be copied into again
             if (++stage == kStages) {
@@ -574,7 +595,7 @@ cudaError_t run_rows(const AttnCache &c, const TreeArgs &a, cudaStream_t st) {
     CUtensorMap km, vm;
     if (!encode_pool(&km, c.k, c, 16, true) || !encode_pool(&vm, c.v, c, 16, true))
         return cudaErrorNotSupported;
-    auto *k = k_attn_rows<D, kBf16>;
+    auto *k = a.o_f32 ? k_attn_rows<D, kBf16, true> : k_attn_rows<D, kBf16, false>;
     constexpr int smem = RowsShape<D>::kSmem;
     cudaError_t e = set_smem(k, smem);
     if (e == cudaSuccess) e = launch(k, dim3(a.grid), dim3(32 * kWarps), smem, st, true, km, vm, a);

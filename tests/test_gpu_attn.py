@@ -275,6 +275,46 @@ def test_tree_batches_bound_by_memory(D, page, G, T):
         assert torch.allclose(w, p.sum((1, 2)).T, rtol=2.0 ** -13, atol=1e-9), b
 
 
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("D,page,G,T", [(128, 64, 5, 1), (64, 64, 4, 4), (128, 16, 5, 21), (64, 128, 5, 21),
+                                        (128, 128, 8, 40), (64, 32, 8, 40)])
+def test_tree_fp32_outputs_of_long_contexts(D, page, G, T, dtype):
+    """An fp32 output is as near as fp32 weights and sums are. In the norm: a score
+    (rms 1) off by up to 10 steps of 2^-24, a weight by about that much, each by
+    itself (1.2e-6); a tile's 24 partial products cut by 2^-25 on average, all one
+    way (7e-7). Together under 2^-19."""
+    B, Hkv, n = 9, 4, 5000
+    g = torch.Generator(device="cuda").manual_seed(T + D)
+    ctx, drafts = [n - 411 * b for b in range(B)], [max(1, T - b % 3) for b in range(B)]
+    need = [-(-(c + t) // page) for c, t in zip(ctx, drafts)]
+    k = torch.empty(sum(need), Hkv, page, D, dtype=dtype, device="cuda").normal_(generator=g)
+    v = torch.empty_like(k).normal_(generator=g)
+    table = torch.zeros(B, max(need), dtype=torch.int32)
+    order = torch.randperm(sum(need), generator=torch.Generator().manual_seed(1)).int()
+    for b in range(B):
+        table[b, :need[b]] = order[sum(need[:b]):sum(need[:b + 1])]
+    cu = [0] + np.cumsum(drafts).tolist()
+    qq = torch.empty(cu[-1], Hkv * G, D, dtype=dtype, device="cuda").normal_(generator=g)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    st = torch.zeros(1, **i32)
+    runs = [q.attn_tree(q.AttnCache(k, v), qq, table.cuda(), torch.tensor(ctx, **i32), torch.tensor(cu, **i32), T,
+                        o_dtype=F32, status=st) for _ in range(3)]
+    torch.cuda.synchronize()
+    assert int(st) == 0
+    for o, lse in runs[1:]:
+        assert torch.equal(o, runs[0][0]) and torch.equal(lse, runs[0][1])
+    for b in range(B):
+        t, m = drafts[b], ctx[b] + drafts[b]
+        rows = table[b, :need[b]].long().cuda()
+        kk = k[rows].transpose(1, 2).reshape(-1, Hkv, D)[:m].double()
+        vv = v[rows].transpose(1, 2).reshape(-1, Hkv, D)[:m].double()
+        x = torch.einsum("thgd,mhd->htgm", qq[cu[b]:cu[b + 1]].view(t, Hkv, G, D).double(), kk) * D ** -0.5
+        late = torch.arange(m, device="cuda") > ctx[b] + torch.arange(t, device="cuda")[:, None]
+        want = torch.einsum("htgm,mhd->thgd", torch.softmax(x.masked_fill(late[None, :, None], -math.inf), -1), vv)
+        got = runs[0][0][cu[b]:cu[b + 1]].double().view_as(want)
+        assert (got - want).norm() <= 2.0 ** -19 * want.norm(), b
+
+
 def test_tree_peaked_scores_and_negative_scale():
     """Scores of tens of units, rising and falling along the keys: the running maximum moves."""
     for scale in (1.0, -0.5):
