@@ -11,12 +11,20 @@
 // selection on order-preserving 32-bit keys (11, 11 and 10 bits, a histogram
 // each, largest bins first), then lists the kept slots in order. The sums are
 // read once, four slots a load; the upper halves of their keys stay in shared
-// memory. After the first histogram a pass lists the few slots that share the
-// threshold's bin, and only those are looked at whole for the other bits (all
-// of the bin's again where too many share it). A cluster of blocks shares a
-// list, each with its own stretch of slots; histograms and counts are read
-// across the cluster. Half a key a slot lets two blocks share an SM: with whole
-// keys 16 clusters of 8 ran in two waves. k_evict_copy moves the rows.
+// memory, eight of which a lane looks at together. After the first histogram a
+// pass lists the few slots that share the threshold's bin, and only those are
+// looked at whole for the other bits (all of the bin's again where too many
+// share it). A cluster of blocks shares a list, each with its own stretch of
+// slots; sums of 32 bins, and then one such group, are read across the cluster.
+// Half a key a slot lets two blocks share an SM: with whole keys 16 clusters of
+// 8 ran in two waves.
+//
+// What bounds it: the latencies of its steps. 16 lists of 300,007 sums (19 MB)
+// take 33 us of which reading and counting 11, the pass that lists 8 and the one
+// that writes 7; 4,099 sums take 8 us in one block a list, 2 of them the first
+// sums' way from memory. k_evict_copy moves the rows, 16 bytes a lane and four
+// rows in flight: 82 us for the 549 MB of a batch of 16 with 4096 kept a head,
+// which is the rate of a plain copy.
 #include <cooperative_groups.h>
 
 #include "qmv_attn.cuh"
@@ -31,7 +39,7 @@ namespace {
 
 constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32, kBins = 2048;
 constexpr uint32_t kCand = 160;         // listed slots a warp
-constexpr int kCached = 39 * 1024;      // slots a block keeps 16 key bits of (78 KB)
+constexpr int kCached = 39552;          // slots a block keeps 16 key bits of (77 KB)
 
 struct EvictArgs {
     const float *acc;
@@ -61,15 +69,14 @@ __device__ __forceinline__ uint32_t slot_key(const EvictArgs &a, const int32_t *
     return sum_key(__ldg(a.acc + ((long long)pid * a.Hkv + h) * a.page + (i & (a.page - 1))));
 }
 
-struct alignas(16) SelSmem {  // (the key halves after it are read 8 bytes at a time)
+struct alignas(16) SelSmem {  // (the key halves after it are read 16 bytes at a time)
     uint32_t hist[3][kBins];
-    uint32_t wsum[32];
+    uint32_t group[3][kBins / 32];  // sums of 32 bins
     uint32_t found[2];           // bin, and how many are still wanted from it
     uint32_t mine[2];            // this block's (above the threshold, equal to it)
     uint32_t wcnt[2][32];        // the same of each warp
-    // slots whose key shares the threshold's first bits, each warp its own (their
-    // numbers in ncand, while they fit)
-    uint32_t ncand[kSelWarps];
+    // slots whose key shares the threshold's first bits, each warp its own, while
+    // they fit
     int32_t cand[kSelWarps][kCand];
 };
 
@@ -86,7 +93,7 @@ __device__ __forceinline__ uint32_t warp_scan(uint32_t v, int lane) {
     return v;
 }
 
-// cached: the slots (a multiple of 4) of a block's stretch whose upper 16 key
+// cached: the slots (a multiple of 8) of a block's stretch whose upper 16 key
 // bits its shared memory holds; beyond them the sums are read again.
 __global__ void __launch_bounds__(kSelThreads) k_evict_select(const EvictArgs a, int cached) {
     extern __shared__ __align__(16) uint8_t smem[];
@@ -195,120 +202,164 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const EvictArgs a,
         }
     }
     __syncthreads();
+    // Sums of 32 bins, eight threads' n each.
+    auto group_sum = [&](int p, const uint4 &n) {
+        uint32_t x = n.x + n.y + n.z + n.w;
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, o);
+        if ((lane & 7) == 0) m->group[p][tid >> 3] = x;
+    };
+    static_assert(kBins == 4 * kSelThreads, "");
     {
         uint4 *s0 = reinterpret_cast<uint4 *>(m->hist[0]) + tid, *s1 = reinterpret_cast<uint4 *>(m->hist[1]) + tid,
               *s2 = reinterpret_cast<uint4 *>(m->hist[2]) + tid;
         const uint4 x = *s0, y = *s1, z = *s2;
-        *s0 = make_uint4(x.x + y.x + z.x, x.y + y.y + z.y, x.z + y.z + z.z, x.w + y.w + z.w);
+        const uint4 n = make_uint4(x.x + y.x + z.x, x.y + y.y + z.y, x.z + y.z + z.z, x.w + y.w + z.w);
+        *s0 = n;
         *s1 = *s2 = make_uint4(0u, 0u, 0u, 0u);
+        group_sum(0, n);
     }
-    // The upper halves of 128 slots from i0, four a lane, 32 slots apart, and
-    // which of them are inside.
-    auto upper4 = [&](int i0, uint32_t (&x)[4], bool (&in)[4]) {
+    // Which of eight slots from i are inside and have upper halves in [from, to) (eq)
+    // or from `to` on (above), bit e for slot i + e; where the halves are not kept,
+    // f(slot) says it: 1, 2, or 0.
+    auto classes = [&](int i, uint32_t from, uint32_t to, uint32_t &above, uint32_t &eq, auto &&f) {
+        above = eq = 0;
+        if (i >= w1) return;
+        if (i - c0 + 8 <= cached) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(upper + (i - c0));
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w}, f = from << 16, t = to << 16;
+            uint32_t some = 0;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int i = i0 + u * 32 + lane;
-            in[u] = i >= lo && i < hi;
-            x[u] = i - c0 < cached ? upper[i - c0] : in[u] ? slot_key(a, row, h, i) >> 16 : 0u;
+            for (int e = 0; e < 8; ++e) {  // the half in the upper 16 bits (an odd slot's with its neighbour's below)
+                const uint32_t v = e & 1 ? w[e >> 1] : w[e >> 1] << 16;
+                if (v >= f) some |= 1u << e;
+                if (v >= t) above |= 1u << e;
+            }
+            if (to > 0xFFFFu) above = 0;
+            eq = some & ~above;
+        } else {
+#pragma unroll 1
+            for (int e = 0; e < 8; ++e) {
+                const int c = i + e >= lo && i + e < hi ? f(i + e) : 0;
+                if (c == 1) eq |= 1u << e;
+                if (c == 2) above |= 1u << e;
+            }
+        }
+        if (i < lo || i + 8 > hi) {
+            uint32_t in = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (i + e >= lo && i + e < hi) in |= 1u << e;
+            above &= in;
+            eq &= in;
         }
     };
-    const uint32_t below = (1u << lane) - 1;
     uint32_t prefix = 0;  // the bits found so far
-    bool listed = false;  // the slots that share the threshold's first bits are in m->cand
+    // The slots that share the threshold's first bits, where they are listed: this
+    // lane's, with their whole keys.
+    bool listed = false;
+    constexpr int kMine = kCand / 32;
+    int cslot[kMine];
+    uint32_t ckey[kMine];
     // Their whole keys: f(slot, key).
     auto candidates = [&](auto &&f) {
         __syncwarp();
         if (listed) {
-            for (uint32_t i = lane; i < m->ncand[warp]; i += 32) {
-                const int s = m->cand[warp][i];
-                f(s, slot_key(a, row, h, s));
-            }
-        } else {
-            for (int i0 = w0; i0 < w1; i0 += 128) {
-                uint32_t x[4];
-                bool in[4];
-                upper4(i0, x, in);
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    if (in[u] && x[u] >> 5 == prefix >> 21)
-                        f(i0 + u * 32 + lane, slot_key(a, row, h, i0 + u * 32 + lane));
+            for (int j = 0; j < kMine; ++j)
+                if (cslot[j] >= 0) f(cslot[j], ckey[j]);
+        } else {
+            const uint32_t t = prefix >> 21;
+            for (int i = w0 + lane * 8; i < w1; i += 256) {
+                uint32_t above, eq;
+                classes(i, t << 5, (t + 1) << 5, above, eq, [&](int s) { return slot_key(a, row, h, s) >> 21 == t; });
+                for (; eq; eq &= eq - 1) {
+                    const int s = i + __ffs(eq) - 1;
+                    f(s, slot_key(a, row, h, s));
+                }
             }
         }
     };
     for (int p = 0; p < 3; ++p) {
         const int shift = p == 0 ? 21 : p == 1 ? 10 : 0, bits = p == 2 ? 10 : 11;
-        if (p > 0)
+        if (p > 0) {
             candidates([&](int, uint32_t k) {
                 if (k >> (shift + bits) == prefix >> (shift + bits))
                     atomicAdd(&m->hist[p][(k >> shift) & ((1u << bits) - 1)], 1u);
             });
+            __syncthreads();
+            group_sum(p, *(reinterpret_cast<const uint4 *>(m->hist[p]) + tid));
+        }
         if (C > 1)
             cl.sync();
         else
             __syncthreads();
-        // bins from the top: thread t takes the kPer below kBins - kPer * t
-        constexpr int kPer = kBins / kSelThreads;
-        static_assert(kPer == 4, "");
-        const int bin0 = kBins - (tid + 1) * kPer;
-        uint4 n = make_uint4(0u, 0u, 0u, 0u);
+        // the bin that holds the want-th largest: its group of 32 first (a block
+        // that read all the others' bins took 5,000 to 9,000 cycles a histogram)
+        if (warp == 0) {
+            uint32_t bin = (1u << bits) - 1, left = 0;  // wanted 0: a threshold above every key
+            if (want > 0) {
+                uint2 n = make_uint2(0u, 0u);  // groups from the top, two a lane
 #pragma unroll 8
-        for (int r = 0; r < C; ++r) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(cl.map_shared_rank(&m->hist[p][0], r) + bin0);
-            n.x += x.x; n.y += x.y; n.z += x.z; n.w += x.w;
-        }
-        const uint32_t cnt[kPer] = {n.w, n.z, n.y, n.x};
-        const uint32_t sum = n.x + n.y + n.z + n.w, inc = warp_scan(sum, lane);
-        if (lane == 31) m->wsum[warp] = inc;
-        if (tid == 0) {  // wanted 0: a threshold above every key
-            m->found[0] = (1u << bits) - 1;
-            m->found[1] = 0;
-        }
-        __syncthreads();
-        const uint32_t ws = lane < kSelWarps ? m->wsum[lane] : 0u;
-        const uint32_t ahead = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? ws : 0u);
-        uint32_t before = ahead + inc - sum;
-        // the bin that holds the want-th largest
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            if (before < want && before + cnt[j] >= want) {
-                m->found[0] = kBins - 1 - (tid * kPer + j);
-                m->found[1] = want - before;
+                for (int r = 0; r < C; ++r) {
+                    const uint2 x = *reinterpret_cast<const uint2 *>(cl.map_shared_rank(&m->group[p][0], r) + 62 - 2 * lane);
+                    n.x += x.x;
+                    n.y += x.y;
+                }
+                uint32_t before = warp_scan(n.x + n.y, lane) - n.x - n.y;
+                const uint32_t who = __ballot_sync(0xFFFFFFFFu, before + n.x + n.y >= want);
+                const int src = __ffs(who) - 1;
+                const bool second = before + n.y < want;
+                const int grp = __shfl_sync(0xFFFFFFFFu, 63 - 2 * lane - (second ? 1 : 0), src);
+                left = want - __shfl_sync(0xFFFFFFFFu, before + (second ? n.y : 0u), src);
+                uint32_t c = 0;
+#pragma unroll 8
+                for (int r = 0; r < C; ++r)
+                    c += cl.map_shared_rank(&m->hist[p][0], r)[grp * 32 + 31 - lane];
+                const uint32_t inc = warp_scan(c, lane);
+                const int at = __ffs(__ballot_sync(0xFFFFFFFFu, inc >= left)) - 1;
+                left -= __shfl_sync(0xFFFFFFFFu, inc - c, at);
+                bin = grp * 32 + 31 - at;
             }
-            before += cnt[j];
+            if (lane == 0) {
+                m->found[0] = bin;
+                m->found[1] = left;
+            }
         }
         __syncthreads();
         prefix |= m->found[0] << shift;
         want = m->found[1];
-        __syncthreads();
         if (p == 0) {
             // each warp's keys above this bin, and a list of the slots in it
             uint32_t above = 0, n = 0;
             const uint32_t t = prefix >> 21;
-            for (int i0 = w0; i0 < w1; i0 += 128) {
-                uint32_t x[4], be[4];
-                bool in[4];
-                upper4(i0, x, in);
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    above += in[u] && x[u] >> 5 > t;
-                    be[u] = __ballot_sync(0xFFFFFFFFu, in[u] && x[u] >> 5 == t);
-                }
-                if (be[0] | be[1] | be[2] | be[3]) {
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const uint32_t at = n + __popc(be[u] & below);
-                        if (((be[u] >> lane) & 1u) && at < kCand)
-                            m->cand[warp][at] = i0 + u * 32 + lane;
-                        n += __popc(be[u]);
-                    }
+            for (int i0 = w0; i0 < w1; i0 += 256) {
+                uint32_t ab, eq;
+                const int i = i0 + lane * 8;
+                classes(i, t << 5, (t + 1) << 5, ab, eq, [&](int s) {
+                    const uint32_t x = slot_key(a, row, h, s) >> 21;
+                    return x > t ? 2 : x == t;
+                });
+                above += __popc(ab);
+                if (__any_sync(0xFFFFFFFFu, eq != 0)) {
+                    const uint32_t mine = __popc(eq), inc = warp_scan(mine, lane);
+                    uint32_t at = n + inc - mine;
+                    for (; eq; eq &= eq - 1, ++at)
+                        if (at < kCand) m->cand[warp][at] = i + __ffs(eq) - 1;
+                    n += __shfl_sync(0xFFFFFFFFu, inc, 31);
                 }
             }
             above = __reduce_add_sync(0xFFFFFFFFu, above);
-            if (lane == 0) {
-                m->wcnt[0][warp] = above;
-                m->ncand[warp] = n;
-            }
+            if (lane == 0) m->wcnt[0][warp] = above;
             listed = __syncthreads_and(n <= kCand);
+            if (listed) {
+#pragma unroll
+                for (int j = 0; j < kMine; ++j) {
+                    const bool have = lane + j * 32 < n;
+                    cslot[j] = have ? m->cand[warp][lane + j * 32] : -1;
+                    ckey[j] = have ? slot_key(a, row, h, cslot[j]) : 0u;
+                }
+            }
         }
     }
     // keys above `prefix` are kept, and the first `want` equal to it: both in
@@ -346,32 +397,26 @@ __global__ void __launch_bounds__(kSelThreads) k_evict_select(const EvictArgs a,
     }
     const uint32_t t16 = prefix >> 16;
     keep += a.sink;
-    for (int i0 = w0; i0 < w1; i0 += 128) {
-        uint32_t x[4], ba[4], be[4];
-        bool in[4];
-        upper4(i0, x, in);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            ba[u] = __ballot_sync(0xFFFFFFFFu, in[u] && x[u] > t16);
-            be[u] = __ballot_sync(0xFFFFFFFFu, in[u] && x[u] == t16);
-        }
-        if (i0 + 127 - c0 >= cached && (be[0] | be[1] | be[2] | be[3])) {  // the lower halves decide
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int i = i0 + u * 32 + lane;
-                const uint32_t k = (be[u] >> lane) & 1u ? slot_key(a, row, h, i) : 0u;
-                const bool eq = (be[u] >> lane) & 1u;
-                ba[u] |= __ballot_sync(0xFFFFFFFFu, eq && k > prefix);
-                be[u] = __ballot_sync(0xFFFFFFFFu, eq && k == prefix);
+    for (int i0 = w0; i0 < w1; i0 += 256) {
+        uint32_t ab, eq;
+        const int i = i0 + lane * 8;
+        classes(i, t16, t16 + 1, ab, eq, [&](int s) {  // (not kept: the whole key decides)
+            const uint32_t k = slot_key(a, row, h, s);
+            return k > prefix ? 2 : k == prefix;
+        });
+        if (__any_sync(0xFFFFFFFFu, (ab | eq) != 0)) {
+            const uint32_t mine = __popc(ab) | __popc(eq) << 16, inc = warp_scan(mine, lane);
+            uint32_t na = pa + ((inc - mine) & 0xFFFFu), ne = pe + ((inc - mine) >> 16);
+            for (uint32_t some = ab | eq; some; some &= some - 1) {
+                const int e = __ffs(some) - 1;
+                const bool tie = (eq >> e) & 1u;
+                if (!tie || ne < want) keep[na + min(ne, want)] = i + e;
+                na += !tie;
+                ne += tie;
             }
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const uint32_t ne = pe + __popc(be[u] & below), na = pa + __popc(ba[u] & below);
-            if (((ba[u] >> lane) & 1u) || (((be[u] >> lane) & 1u) && ne < want))
-                keep[na + min(ne, want)] = i0 + u * 32 + lane;
-            pa += __popc(ba[u]);
-            pe += __popc(be[u]);
+            const uint32_t all = __shfl_sync(0xFFFFFFFFu, inc, 31);
+            pa += all & 0xFFFFu;
+            pe += all >> 16;
         }
     }
 }
@@ -451,7 +496,7 @@ cudaError_t launch_attn_evict(const AttnCache &src, const float *acc, const int3
     while (C < most && longest / C > 8192 && (long long)B * src.Hkv * C <= sm_count()) C *= 2;
     // the upper halves of a block's keys, as many as leave room for two blocks an SM
     const long long stretch = (longest + C - 1) / C + 128 * kSelWarps + 128;
-    const int cached = (int)(stretch < kCached ? stretch : kCached) & ~3;
+    const int cached = (int)(stretch < kCached ? stretch : kCached) & ~7;
     const size_t smem = sizeof(SelSmem) + (size_t)cached * 2;
     cudaError_t e = set_smem(k_evict_select, smem);
     if (e == cudaSuccess && C > 8)  // more than the portable size
