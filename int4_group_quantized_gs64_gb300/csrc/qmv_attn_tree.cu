@@ -622,7 +622,8 @@ cudaError_t run_tree(const AttnCache &c, const TreeArgs &a, int max_rows, cudaSt
 
 // Rows an item: up to 16 on the warp MMA, more on tcgen05 (qmv_attn_tc.cu).
 // With 16 rows the two measured 259 and 245 us (64 sequences of 8191 keys) and
-// 13.2 and 14.4 us (one of 777), with 32 rows 452 and 248.
+// 13.2 and 14.4 us (one of 777), with 32 rows 452 and 248. Above 128 rows two
+// tiles share the keys: 192 rows over 16 x 8191 keys 109 us, in blocks of 128 150.
 int tree_rows(int max_rows) { return max_rows <= kRows ? kRows : max_rows <= 128 ? 128 : 256; }
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     static std::once_flag once;

@@ -4,13 +4,21 @@
 // A weight needs its row's lse, and so the whole pass over the keys before it.
 // What the pass can leave behind, or what has to be done again, depends on
 // the rows R of a key/value head:
-//   few rows      k_attn_rows leaves its scores (8 R bytes a key, written and
+//   up to 16      k_attn_rows leaves its scores (8 R bytes a key, written and
 //                 read); k_weights_stash turns them into weights, a thread a key.
-//   17 .. 512     k_weights_tc forms the scores again (2 D bytes a key), keys as
+//                 32 sequences of 10,007 keys, 6 rows: 181 us with the attention,
+//                 243 with the scores formed again.
+//   more, or scores too many to keep
+//                 k_weights_tc forms the scores again (2 D bytes a key), keys as
 //                 the rows of the tcgen05 product, so that a thread has one key
-//                 and sums its own columns: S^T = K Q^T, all R queries resident
-//                 in shared memory while the keys stream by once.
-//   otherwise     k_weights_any, on the warp MMA: any rows, any masks.
+//                 and sums its own columns: S^T = K Q^T, up to 512 queries resident
+//                 in shared memory while the keys stream by once (a launch for
+//                 every 512, each adding to the last one's sums).
+// What bounds k_weights_tc: 64 sequences of 8191 keys, 128 rows: 195 us, 5.5 TB/s
+// of keys. Small trees pay for the start of a block's parts (16 sequences of up to
+// 6000 keys of 64 elements, 105 rows: 35 us, a third of which is the first copies
+// and queries); the exponentials are not the limit (some of them as polynomials on
+// the fp32 pipe: 82.8 -> 84.5 us with the attention).
 #include <string.h>
 
 #include "qmv_attn.cuh"
@@ -88,92 +96,7 @@ __global__ void __launch_bounds__(256) k_weights_stash(const TreeArgs a, bool ve
     }
 }
 
-// ------------------------------------------------------------------ any rows, any masks
-
-// Eight warps share 16 keys: each walks every eighth block of 16 rows, and
-// their sums meet in shared memory.
-template <int D, bool kBf16>
-__global__ void __launch_bounds__(256) k_weights_any(const TreeArgs a) {
-    __shared__ float sums[8][16];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int b = blockIdx.z, h = blockIdx.y;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    bool ok;
-    const Seq q = get_seq(a.s, b, ok);
-    const int len = q.ctx + q.T, s0 = blockIdx.x * 16;
-    if (q.T == 0 || s0 >= len) return;
-    const int pid = a.s.table[(long long)b * a.s.max_pages + (s0 >> a.s.lpage)];
-    if ((unsigned)pid >= (unsigned)a.pages) return;
-    const long long prow = ((long long)pid * a.Hkv + h) * a.s.page + (s0 & (a.s.page - 1));
-    constexpr int KK = D / 16;
-    uint32_t kb[2][KK][2];
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int k = 0; k < KK; ++k) {
-            const uint32_t *p = reinterpret_cast<const uint32_t *>(
-                a.kpool + (prow + n * 8 + g) * D + k * 16 + c * 2);
-            kb[n][k][0] = p[0];
-            kb[n][k][1] = p[4];
-        }
-    float w[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
-    const int nrows = q.T * a.G;
-    for (int r0 = warp * 16; r0 < nrows; r0 += 128) {
-        uint32_t qf[KK][4];
-        int rt[2];
-        float e2[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int r = r0 + e * 8 + g;
-            const bool have = r < nrows;
-            const int t = have ? div_g(a, r) : 0;
-            const int head = h * a.G + (have ? r - t * a.G : 0);
-            rt[e] = t;
-            e2[e] = have ? a.lse[(long long)(q.first + t) * a.Hq + head] * kLog2e : -INFINITY;
-            const uint16_t *p = a.q + (long long)(q.first + t) * a.q_stride + (long long)head * D;
-#pragma unroll
-            for (int k = 0; k < KK; ++k) {
-                const uint32_t *x = reinterpret_cast<const uint32_t *>(p + k * 16 + c * 2);
-                qf[k][e] = (x[0] ^ a.qxor) & a.qand;
-                qf[k][e + 2] = (x[4] ^ a.qxor) & a.qand;
-            }
-        }
-        const uint32_t see[2] = {seen_word(a, q, rt[0], s0), seen_word(a, q, rt[1], s0)};
-        float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-#pragma unroll
-        for (int k = 0; k < KK; ++k) {
-            mma16816<kBf16>(s[0], qf[k], kb[0][k][0], kb[0][k][1]);
-            mma16816<kBf16>(s[1], qf[k], kb[1][k][0], kb[1][k][1]);
-        }
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int j = n * 8 + c * 2 + (i & 1);
-                if (e2[i >> 1] != -INFINITY && ((see[i >> 1] >> j) & 1u))
-                    w[n][i & 1] += ex2(fmaf(s[n][i], a.sl2, -e2[i >> 1]));
-            }
-    }
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) w[n][i] += __shfl_xor_sync(0xFFFFFFFFu, w[n][i], o);
-            if (g == 0) sums[warp][n * 8 + c * 2 + i] = w[n][i];
-        }
-    __syncthreads();
-    if (threadIdx.x < 16 && s0 + threadIdx.x < len) {
-        float x = 0.f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x += sums[k][threadIdx.x];
-        const long long at = prow + threadIdx.x;
-        a.acc_out[at] = (a.acc_in ? a.decay * a.acc_in[at] : 0.f) + x;
-    }
-}
-
-// ------------------------------------------------------------------ many rows, tcgen05
+// ------------------------------------------------------------------ from the keys again
 
 constexpr int kThreads = 352, kKeys = 128, kStages = 12, kSmemMax = 227 * 1024, kMaxRows = 512;
 
@@ -207,7 +130,7 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, Misc *m, in
 // memory in turn.
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_weights_tc(const __grid_constant__ CUtensorMap kmap, const TreeArgs a, int q_tiles, int stages) {
+    k_weights_tc(const __grid_constant__ CUtensorMap kmap, const TreeArgs a, int row0, int q_tiles, int stages) {
     constexpr int kTile = kKeys * D * 2, kHalves = D / 64;
     constexpr uint32_t kIdesc = tc05::idesc_f16kind_f32(kBf16, 128, 128, false);
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -352,8 +275,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t sl2 = pack_f32x2(a.sl2, a.sl2);
         for (int left = units; left > 0;) {
             const Seq q = c.q;
-            const int j0 = c.u, n = min(c.nu - c.u, left), nrows = q.T * a.G;
-            const int nq = (nrows + 127) / 128;
+            const int j0 = c.u, n = min(c.nu - c.u, left), nrows = min(q.T * a.G - row0, kMaxRows);
+            const int nq = nrows > 0 ? (nrows + 127) / 128 : 0;
             // queries, and -lse of each
             constexpr int kChunks = D / 8, kPass = 256 / kChunks;
             const int ch = threadIdx.x % kChunks;
@@ -364,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint4 v[128 / kPass];
 #pragma unroll
                 for (int i = 0; i < 128 / kPass; ++i) {
-                    const int rr = min(rt * 128 + (int)threadIdx.x / kChunks + i * kPass, nrows - 1);
+                    const int rr = row0 + min(rt * 128 + (int)threadIdx.x / kChunks + i * kPass, nrows - 1);
                     const int t = div_g(a, rr);
                     v[i] = __ldg(reinterpret_cast<const uint4 *>(p + t * a.q_stride + (rr - t * a.G) * D));
                 }
@@ -388,8 +311,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int r = threadIdx.x; r < nq * 128; r += 256) {
                 float e = -INFINITY;
                 if (r < nrows) {
-                    const int t = div_g(a, r);
-                    e = -a.lse[(long long)(q.first + t) * a.Hq + c.h * a.G + r - t * a.G] * kLog2e;
+                    const int t = div_g(a, row0 + r);
+                    e = -a.lse[(long long)(q.first + t) * a.Hq + c.h * a.G + row0 + r - t * a.G] * kLog2e;
                     if (e == INFINITY) e = -INFINITY;
                 }
                 m->nlse[r] = e;
@@ -447,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     tc05::fence_after_sync();
                     if (special) {  // scores of rows that do not see the key become -inf
-                        int tt = div_g(a, r * 128), gg = r * 128 - tt * a.G;  // row's draft and head
+                        int tt = div_g(a, row0 + r * 128), gg = row0 + r * 128 - tt * a.G;  // row's draft and head
 #pragma unroll 1
                         for (int k = 0; k < 4; ++k) {
                             uint32_t x[32];
@@ -514,25 +437,26 @@ cudaError_t run(const AttnCache &c, const TreeArgs &a, int max_rows, cudaStream_
         return launch(k_weights_stash, dim3((unsigned)((most + 1023) / 1024), a.Hkv, a.s.B), dim3(256),
                       0, st, true, a,
                       ((reinterpret_cast<uintptr_t>(a.acc_in) | reinterpret_cast<uintptr_t>(a.acc_out)) & 15) == 0);
-    if (max_rows <= 16 || max_rows > kMaxRows)
-        return launch(k_weights_any<D, kBf16>, dim3((unsigned)((most + 15) / 16), a.Hkv, a.s.B),
-                      dim3(256), 0, st, true, a);
     constexpr int kTile = kKeys * D * 2;
     TreeArgs w = a;
     w.rows = 1 << 30;
     w.unit = kKeys;
     const long long units = (long long)a.s.B * a.Hkv * ((most + kKeys - 1) / kKeys);
     w.grid = units < sm_count() ? (int)units : sm_count();
-    const int q_tiles = (max_rows + 127) / 128;
-    int stages = (kSmemMax - kMisc - q_tiles * kTile) / kTile;
-    if (stages > kStages) stages = kStages;
     CUtensorMap km;
     if (!encode_pool(&km, c.k, c, c.page < kKeys ? c.page : kKeys, false))
         return cudaErrorNotSupported;
     auto *k = k_weights_tc<D, kBf16>;
     cudaError_t e = set_smem(k, kSmemMax);
-    if (e == cudaSuccess)
-        e = launch(k, dim3(w.grid), dim3(kThreads), kSmemMax, st, true, km, w, q_tiles, stages);
+    for (int row0 = 0; row0 < max_rows && e == cudaSuccess; row0 += kMaxRows) {
+        const int rows = max_rows - row0 < kMaxRows ? max_rows - row0 : kMaxRows;
+        const int q_tiles = (rows + 127) / 128;
+        int stages = (kSmemMax - kMisc - q_tiles * kTile) / kTile;
+        if (stages > kStages) stages = kStages;
+        e = launch(k, dim3(w.grid), dim3(kThreads), kSmemMax, st, true, km, w, row0, q_tiles, stages);
+        w.acc_in = w.acc_out;  // further rows add to what these leave
+        w.decay = 1.f;
+    }
     return e;
 }
 

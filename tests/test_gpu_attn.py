@@ -392,6 +392,37 @@ def test_tree_weights(drafts, G, D):
     assert torch.all((out2.cpu().double() - ref[4])[t].abs() <= ref[5][t])
 
 
+@pytest.mark.parametrize("drafts,G,D", [([200, 3], 8, 128), ([256, 130], 5, 64), ([65, 64], 8, 128)])
+def test_tree_weights_of_many_rows(drafts, G, D):
+    """More rows than a pass over the keys holds, and sequences that have none in the later passes."""
+    c = Case([300, 45], drafts, 2, G, D, 32, BF, seed=6, qscale=2.0)
+    acc, out = c.acc.cuda(), torch.full(c.acc.shape, 5.0, device="cuda")
+    run_tree(c, acc=acc, acc_out=out, decay=0.75)
+    assert torch.equal(acc.cpu(), c.acc)
+    ref = c.reference(D ** -0.5, 0.75, c.acc)
+    t = ref[6]
+    assert torch.all((out.cpu().double() - ref[4])[t].abs() <= ref[5][t])
+    assert torch.all(out.cpu()[~t] == 5.0)
+    run_tree(c, acc=acc, decay=0.75)  # in place
+    assert torch.equal(acc.cpu()[t], out.cpu()[t]) and torch.equal(acc.cpu()[~t], c.acc[~t])
+
+
+@pytest.mark.parametrize("drafts,G,D,width", [([4, 3], 4, 128, 16400), ([1, 1], 1, 64, 262200), ([2, 2], 3, 64, 43700)])
+def test_tree_weights_of_few_rows_in_wide_tables(drafts, G, D, width):
+    """Tables so wide that the scores of a call are not kept."""
+    c = Case([700, 20], drafts, 2, G, D, 256, BF, seed=7, qscale=2.0)
+    more = torch.full((2, width - c.table.shape[1]), -7, dtype=torch.int32)
+    c.table = torch.cat([c.table, more], 1).contiguous()
+    c.dev()
+    assert q.attn_tree_workspace_bytes(c.cache, c.Hq, 2, c.N, c.T, width, True) < 1 << 29
+    out = torch.full(c.acc.shape, 5.0, device="cuda")
+    run_tree(c, acc=c.acc.cuda(), acc_out=out, decay=0.75)
+    ref = c.reference(D ** -0.5, 0.75, c.acc)
+    t = ref[6]
+    assert torch.all((out.cpu().double() - ref[4])[t].abs() <= ref[5][t])
+    assert torch.all(out.cpu()[~t] == 5.0)
+
+
 def test_tree_weights_of_rows_that_see_nothing():
     c = Case([0], [4], 1, 2, 64, 16, BF, seed=1)
     c.mask[:] = 0
