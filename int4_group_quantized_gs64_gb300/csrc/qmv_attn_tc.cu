@@ -454,6 +454,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < ns; ++i) {
                 const int tile = kTwo ? i : 2 * i + s, j = sg.j0 + tile;
                 const bool special = bad || (j + 1) * kKeys > q.ctx;
+                uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};  // this tile's keys that the row sees
+                if (special && warp_live) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        see[k] = row_live ? seen_word(a, q, t, j * kKeys + k * 32) : 0u;
+                    if (bad) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int slot = j * kKeys + k * 16;
+                            if (slot < len && (unsigned)trow[slot >> a.s.lpage] >= (unsigned)a.pages)
+                                see[k >> 1] &= k & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+                        }
+                    }
+                }
                 wait(m->s_full + s, sp, m, a.status);
                 __syncwarp();
                 sp ^= 1;
@@ -527,19 +541,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 };
                 uint32_t third[kAfter ? 4 : 1][16];
                 if (warp_live) {
-                    if (special) {  // scores that a row must not see become -inf
-                        uint32_t see[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            see[k] = row_live ? seen_word(a, q, t, j * kKeys + k * 32) : 0u;
-                        if (bad) {
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                const int slot = j * kKeys + k * 16;
-                                if (slot < len && (unsigned)trow[slot >> a.s.lpage] >= (unsigned)a.pages)
-                                    see[k >> 1] &= k & 1 ? 0x0000FFFFu : 0xFFFF0000u;
-                            }
-                        }
+                    if (kSplit && special) {  // scores that a row must not see become -inf
                         __syncwarp();
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
@@ -612,6 +614,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int k = 0; k < 4; ++k) tc05::tmem_ld32(ts + k * 32, x[k]);
                     tc05::tmem_wait_ld();
                     if (kApart) hand_over();
+                    if (special)  // scores that a row must not see become -inf
+#pragma unroll
+                        for (int e = 0; e < 128; ++e)
+                            if (!((see[e >> 5] >> (e & 31)) & 1u)) x[e >> 5][e & 31] = 0xFF800000u;
                     float v[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(x[0][e]);
