@@ -28,8 +28,8 @@
 // fp32 output they are carried as two fp16 or three bf16 numbers (two bf16 ones:
 // 2.3e-6 of the output's norm; fp32 weights and sums: 1.5e-6), and O is summed up
 // in registers, tile by tile: a product's own sums cut off what falls below
-// their last bit, which over 8191 keys came to 1.1e-5 of the norm. fp16 weights are held 2^7 times larger: the
-// small ones would lose bits below fp16's range.
+// their last bit, which over 8191 keys came to 1.1e-5 of the norm. fp16 weights
+// are held 2^7 times larger: the small ones would lose bits below fp16's range.
 #include <string.h>
 
 #include "qmv_attn.cuh"
@@ -114,7 +114,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               const TreeArgs a, int stages) {
     constexpr int kTile = kKeys * D * 2, kHalves = D / 64;
     constexpr uint32_t kIdescS = tc05::idesc_f16kind_f32(kBf16, 128, kKeys, false);
-    constexpr uint32_t kIdescO = tc05::idesc_f16kind_f32(kBf16, 128, D, true);
     extern __shared__ __align__(1024) uint8_t smem[];
     constexpr int lag = kTwo ? 1 : 2;  // tiles a product P V runs behind its Q K^T
     // Tensor memory columns. Where they suffice (64 elements, one 16-bit number a
@@ -122,13 +121,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // exponentials run (16 sequences of 8191 keys, 320 rows: 122 us, 150 with P
     // over S; 64 sequences, 128 rows: 168 and 182). Otherwise P overwrites S.
     constexpr bool kApart = D == 64 && !kSplit;
-    // The third number of a bf16 weight: in columns that O leaves, or over the
-    // other two once their products are done.
-    constexpr bool kThird = kSplit && kBf16, kAfter = kThird && D == 128;
-    // The turn passes once the maximum is known, not after the exponentials
-    // (21-node trees over 16 x 6000 keys: 83 us and 98; 128 elements, whose O
-    // fills the registers: 316 us and 326 for 256 rows over 16 x 8191 keys).
-    constexpr bool kEarly = kSplit && D == 64;
+    // The third number of a bf16 weight lies in columns that O leaves: with 128
+    // elements O comes in two halves, one after the other.
+    constexpr bool kThird = kSplit && kBf16, kParted = kThird && D == 128;
+    constexpr int kOcols = kParted ? 64 : D;  // columns a product gives
+    constexpr uint32_t kIdescO = tc05::idesc_f16kind_f32(kBf16, 128, kOcols, true);
     constexpr int kPcol = kApart ? 256 : 0, kPstep = kApart ? 64 : 128;   // P of stream s at kPcol + s * kPstep
     constexpr int kOcol = kApart ? 384 : 256, kOstep = kApart ? 64 : 128;
     // The ring's entries of a segment of n tiles: keys of the first `lag` tiles,
@@ -334,25 +331,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc05::fence_after_sync();
                     const uint64_t v = vdesc + (uint32_t)(stage * (kTile >> 4));
                     if (kSplit) {  // the rests, then the weights: a sum of this tile alone
-                        if (kThird && !kAfter)
 #pragma unroll
-                            for (int k = 0; k < kKeys / 16; ++k)
-                                tc05::mma_ts(to, to + 64 + k * 8, v + k * (2048 >> 4), kIdescO, k > 0);
+                        for (int hf = 0; hf < D / kOcols; ++hf) {
+                            if (hf) {  // (the first half has been taken)
+                                tc05::mma_commit(m->pv_done + s);
+                                live = wait(m->p_ready + s, pp, m, a.status);
+                                if (!live) break;
+                                pp ^= 1u;
+                                tc05::fence_after_sync();
+                            }
 #pragma unroll
-                        for (int i = 0; i < kKeys / 8; ++i) {
-                            const int k = i & (kKeys / 16 - 1), rest = i < kKeys / 16 ? 16 : 0;
-                            tc05::mma_ts(to, tp + (k >> 1) * 32 + rest + (k & 1) * 8, v + k * (2048 >> 4),
-                                         kIdescO, (kThird && !kAfter) || i > 0);
-                        }
-                        if (kAfter) {
-                            tc05::mma_commit(m->pv_done + s);
-                            live = wait(m->p_ready + s, pp, m, a.status);
-                            if (!live) break;
-                            pp ^= 1u;
-                            tc05::fence_after_sync();
+                            for (int part = kThird ? 2 : 1; part >= 0; --part)
 #pragma unroll
-                            for (int k = 0; k < kKeys / 16; ++k)
-                                tc05::mma_ts(to, tp + k * 8, v + k * (2048 >> 4), kIdescO, 1);
+                                for (int k = 0; k < kKeys / 16; ++k)
+                                    tc05::mma_ts(to, part == 2 ? to + 64 + k * 8 : tp + k * 16 + part * 8,
+                                                 v + (hf * (kKeys * 128) + k * 2048 >> 4), kIdescO,
+                                                 part < (kThird ? 2 : 1) || k > 0);
                         }
                     } else
 #pragma unroll
@@ -518,10 +512,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc05::fence_proxy_async();
                 }
                 __syncwarp();
-                auto pass_turn = [&]() {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(m->turn + (s ^ 1));
-                };
                 auto hand_over = [&]() {  // the scores are in registers: S is free, and the turn passes
                     tc05::fence_before_sync();
                     __syncwarp();
@@ -539,7 +529,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc05::fence_after_sync();
                     vp ^= 1u;
                 };
-                uint32_t third[kAfter ? 4 : 1][16];
                 if (warp_live) {
                     if (kSplit && special) {  // scores that a row must not see become -inf
                         __syncwarp();
@@ -570,7 +559,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int e = 0; e < 32; ++e) tm = fmaxf(tm, __uint_as_float(x[e]));
                         }
                         tm *= a.sl2;
-                        if (kEarly) pass_turn();
                         const bool move = tm > mx + kLazy || (mx == -INFINITY && tm > mx);
                         if (__any_sync(0xFFFFFFFFu, move)) {
                             const float al = move ? ex2(mx - tm) : 1.f;
@@ -582,13 +570,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         const float base = mx == -INFINITY ? 0.f : mx - boost;
                         const uint64_t nb = pack_f32x2(-base, -base);
-#pragma unroll
-                        for (int h = 0; h < 4; ++h) {
-                            uint32_t x[32], hi[16], lo[16], (&th)[16] = third[kAfter ? h : 0];
-                            tc05::tmem_ld32(ts + h * 32, x);
+#pragma unroll 2
+                        for (int h = 0; h < 8; ++h) {  // 16 at a time: one step of the product
+                            // (not unrolled whole: fetching that much code took 16,000 cycles
+                            // at a block's first tile)
+                            uint32_t x[16], hi[8], lo[8], third[8];
+                            tc05::tmem_ld16(ts + h * 16, x);
                             tc05::tmem_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) {
+                            for (int e = 0; e < 8; ++e) {
                                 float p0, p1;
                                 unpack_f32x2(fma_f32x2(pack_u32x2(x[2 * e], x[2 * e + 1]), sl2, nb), p0, p1);
                                 p0 = ex2(p0);
@@ -597,16 +587,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 if (kThird) {  // cut, not rounded: 3 x 8 bits hold all 24
                                     hi[e] = cut_bf16x2(p0, p1);
                                     lo[e] = cut_bf16x2(p0, p1);
-                                    th[e] = cut_bf16x2(p0, p1);
+                                    third[e] = cut_bf16x2(p0, p1);
                                 } else {
                                     hi[e] = pack2<kBf16>(p0, p1);
                                     const float2 f = unpack2<kBf16>(hi[e]);
                                     lo[e] = pack2<kBf16>(p0 - f.x, p1 - f.y);
                                 }
                             }
-                            tc05::tmem_st16(tw + h * 32, hi);
-                            tc05::tmem_st16(tw + h * 32 + 16, lo);
-                            if (kThird && !kAfter) tc05::tmem_st16(to + s * kOstep + 64 + h * 16, th);
+                            tc05::tmem_st8(tw + h * 16, hi);
+                            tc05::tmem_st8(tw + h * 16 + 8, lo);
+                            if (kThird) tc05::tmem_st8(to + s * kOstep + 64 + h * 8, third);
                         }
                     } else {
                     uint32_t x[4][32];
@@ -673,35 +663,49 @@ __global__ void __launch_bounds__(kThreads, 1)
                         hand_over();
                         if (i > 0) products_done();
                     }
-                } else if (!kEarly || !warp_live) {
-                    pass_turn();
+                } else {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(m->turn + (s ^ 1));
                 }
                 tc05::tmem_wait_st();
                 tc05::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(m->p_ready + s);
-                if constexpr (kAfter) {
-                    products_done();
-                    if (warp_live)
+                if constexpr (kSplit) {  // this tile's share of O
 #pragma unroll
-                        for (int h = 0; h < 4; ++h) tc05::tmem_st16(tw + h * 16, third[h]);
+                    for (int hf = 0; hf < D / kOcols; ++hf) {
+                        products_done();
+                        if (warp_live)
+#pragma unroll
+                            for (int k = 0; k < kOcols / 32; ++k) {
+                                uint32_t o[32];
+                                tc05::tmem_ld32(to + s * kOstep + k * 32, o);
+                                tc05::tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) {
+                                    uint64_t &x = acc[hf * 32 + k * 16 + e];
+                                    x = add_f32x2(x, pack_u32x2(o[2 * e], o[2 * e + 1]));
+                                }
+                            }
+                        if (hf + 1 < D / kOcols) {  // the other half may come
+                            tc05::fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(m->p_ready + s);
+                        }
+                    }
+                }
+            }
+            if constexpr (kSplit) {  // O to where the segment's end takes it from
+                if (ns > 0) {
+#pragma unroll
+                    for (int k = 0; k < D / 32; ++k) {
+                        float o[32];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) unpack_f32x2(acc[k * 16 + e], o[2 * e], o[2 * e + 1]);
+                        tc05::tmem_st32(to + s * kOstep + k * 32, *reinterpret_cast<uint32_t(*)[32]>(o));
+                    }
                     tc05::tmem_wait_st();
                     tc05::fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(m->p_ready + s);
-                }
-                if constexpr (kSplit) {  // this tile's share of O
-                    products_done();
-                    if (warp_live)
-#pragma unroll
-                        for (int k = 0; k < D / 32; ++k) {
-                            uint32_t o[32];
-                            tc05::tmem_ld32(to + s * kOstep + k * 32, o);
-                            tc05::tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                acc[k * 16 + e] = add_f32x2(acc[k * 16 + e], pack_u32x2(o[2 * e], o[2 * e + 1]));
-                        }
                 }
             }
             // ---- the segment's end
@@ -714,19 +718,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 wait(m->o_full + s, op, m, a.status);
                 op ^= 1;
                 if (kApart) vp ^= 1u;  // the last product's, which o_full covers
-                if constexpr (kSplit) {
-                    __syncwarp();
-                    tc05::fence_after_sync();
-#pragma unroll
-                    for (int k = 0; k < D / 32; ++k) {
-                        float o[32];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) unpack_f32x2(acc[k * 16 + e], o[2 * e], o[2 * e + 1]);
-                        tc05::tmem_st32(to + s * kOstep + k * 32, *reinterpret_cast<uint32_t(*)[32]>(o));
-                    }
-                    tc05::tmem_wait_st();
-                    tc05::fence_before_sync();
-                }
             }
             __syncwarp();
             if (mx != -INFINITY) mx -= boost;
