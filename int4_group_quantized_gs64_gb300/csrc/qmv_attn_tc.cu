@@ -26,8 +26,8 @@
 // What bounds it: a stream's chain of scores, exponentials, weights and product,
 // 3,380 cycles for a 128-key tile and 256 rows of 128 elements (the products alone
 // are 2,048), and some 15,000 cycles at the start and end of a block's parts.
-// 8 trees of 64 nodes, 8 query heads a head, up to 8200 keys: 116 us with the
-// join (820 TFLOP/s); 64 sequences of 8191 keys, 32 rows: 248 us, the rate of a copy.
+// 8 trees of 64 nodes, 8 query heads a head, up to 8200 keys: 114 us with the
+// join (830 TFLOP/s); 64 sequences of 8191 keys, 32 rows: 248 us, the rate of a copy.
 //
 // Weights are rounded once to 16 bits for a 16-bit output (half a step of the
 // type, like the output's own rounding, and averaged over the keys). For an
