@@ -17,9 +17,12 @@
 // need no exchange), 8 and 11 the copies of keys and of values, 9 and 10 the
 // streams' products. These four need few registers and pass the rest on to the
 // softmax warps, whose 128 scores stay in registers: reading them from tensor
-// memory twice would cost as much as the products. A ring of 128-key
-// tiles holds keys and values in the order in which the products use them,
-// across segments. The running maximum moves only when it grows by more than 2^8 (a
+// memory twice would cost as much as the products. A ring of 128-key tiles holds
+// keys and another one values, across segments; a copying warp comes to every slot
+// of its ring in turn, and so never waits for a phase that is not the next. (In one
+// ring for both it would know of its own entries only, and those that other slots
+// imply are the other stream's: a wait two phases behind passes at once.) The
+// running maximum moves only when it grows by more than 2^8 (a
 // row's weights may then exceed 1, which fp32 sums and 16-bit weights hold),
 // since moving it means rescaling O in tensor memory.
 //
@@ -123,7 +126,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kTile = kKeys * D * 2, kHalves = D / 64;
     constexpr uint32_t kIdescS = tc05::idesc_f16kind_f32(kBf16, 128, kKeys, false);
     extern __shared__ __align__(1024) uint8_t smem[];
-    constexpr int lag = kTwo ? 1 : 2;  // tiles a product P V runs behind its Q K^T
     // Tensor memory columns. Where they suffice (64 elements, one 16-bit number a
     // weight) P lies apart from S, and a stream's next S is formed while its
     // exponentials run (16 sequences of 8191 keys, 320 rows: 122 us, 150 with P
@@ -136,10 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t kIdescO = tc05::idesc_f16kind_f32(kBf16, 128, kOcols, true);
     constexpr int kPcol = kApart ? 256 : 0, kPstep = kApart ? 64 : 128;   // P of stream s at kPcol + s * kPstep
     constexpr int kOcol = kApart ? 384 : 256, kOstep = kApart ? 64 : 128;
-    // The ring's entries of a segment of n tiles: keys of the first `lag` tiles,
-    // then values of tile t and keys of tile t + lag by turns (apart: keys first).
-    auto entry_k = [](int t) { return t < lag ? t : 2 * t + (kApart ? 0 : 1) - lag; };
-    auto entry_v = [](int t, int n) { return min(t + lag + (kApart ? 1 : 0), n) + t; };
+    const int kstages = stages / 2, vstages = stages - kstages;  // slots for keys, then those for values
     uint8_t *qs = smem, *ring = smem + (kTwo ? 2 : 1) * kTile;
     Misc *m = reinterpret_cast<Misc *>(ring + stages * kTile);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -200,16 +199,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int prow = a.s.page < kKeys ? a.s.page : kKeys;  // rows a copy
         Cursor c;
         c.start(a, sh);
-        int stage = 0, at = 0;
+        const int slot0 = keys ? 0 : kstages, slot1 = keys ? kstages : stages;  // this warp's ring
+        int stage = slot0;
         uint32_t phase = 1;  // a fresh barrier counts as passed for parity 1
-        auto go = [&](int pos) {  // to a later entry of the segment
-            stage += pos - at;
-            at = pos;
-            while (stage >= stages) {
-                stage -= stages;
-                phase ^= 1u;
-            }
-        };
         // this lane's piece of tile j of the sequence at c: its page
         auto page_of = [&](int j, bool &lv) {
             const int slot = j * kKeys + lane * prow;
@@ -224,7 +216,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Segment sg(c, left);
 #pragma unroll 1
             for (int t = 0; t < sg.n; ++t) {
-                go(keys ? entry_k(t) : entry_v(t, sg.n));
                 const bool good = live && (unsigned)pid < (unsigned)a.pages;
                 const int row =
                     (pid * a.Hkv + c.h) * a.s.page + (((sg.j0 + t) * kKeys + lane * prow) & (a.s.page - 1));
@@ -252,9 +243,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 pending |= 1u << stage;
                 pending_ph = (pending_ph & ~(1u << stage)) | ((phase ^ 1u) & 1u) << stage;
+                if (++stage == slot1) {
+                    stage = slot0;
+                    phase ^= 1u;
+                }
             }
-            go(2 * sg.n);
-            at = 0;
             left -= sg.n;
             if (left > 0) {
                 c.next_item(a);
@@ -280,33 +273,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             const int s = warp - 9;
             const uint64_t kdesc = tc05::sdesc_sw128(tc05::smem_addr(ring));
-            const uint64_t vdesc = tc05::sdesc_sw128_mn(tc05::smem_addr(ring), kKeys * 128);
+            const uint64_t vdesc = tc05::sdesc_sw128_mn(tc05::smem_addr(ring + kstages * kTile), kKeys * 128);
             const uint64_t qdesc =
                 tc05::sdesc_sw128(tc05::smem_addr(qs)) + (uint32_t)((kTwo ? s : 0) * (kTile >> 4));
             const uint32_t ts = tmem + s * 128, tp = tmem + kPcol + s * kPstep, to = tmem + kOcol + s * kOstep;
-            int stage = 0, at = 0;                 // ring slot, and its place in the segment's entries
-            uint32_t ring_ph = 0, pp = 0, qp = 0, fp = 0;
-            bool live = true;
-            auto go = [&](int pos) {  // to a later entry of the segment
-                stage += pos - at;
-                at = pos;
-                while (stage >= stages) {
-                    stage -= stages;
-                    ring_ph ^= 1u;
+            struct Place {  // in a ring: the slot of the segment's tile `at`, and its phase
+                int slot = 0, at = 0;
+                uint32_t ph = 0;
+                __device__ __forceinline__ void go(int tile, int slots) {
+                    slot += tile - at;
+                    at = tile;
+                    while (slot >= slots) {
+                        slot -= slots;
+                        ph ^= 1u;
+                    }
                 }
-            };
+            } kp, vp;
+            uint32_t pp = 0, qp = 0, fp = 0;
+            bool live = true;
             auto scores = [&](int t) {  // S = Q K^T
-                go(entry_k(t));
-                live = live && wait(m->full + stage, ring_ph, m, a.status);
+                kp.go(t, kstages);
+                live = live && wait(m->full + kp.slot, kp.ph, m, a.status);
                 if (!live) return;
-                const uint64_t kd = kdesc + (uint32_t)(stage * (kTile >> 4));
+                const uint64_t kd = kdesc + (uint32_t)(kp.slot * (kTile >> 4));
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k) {
                     const int of = ((k >> 2) * (kKeys * 128) + (k & 3) * 32) >> 4;
                     tc05::mma_ss(ts, qdesc + of, kd + of, kIdescS, k > 0);
                 }
                 tc05::mma_commit(m->s_full + s);
-                tc05::mma_commit(m->empty + stage);
+                tc05::mma_commit(m->empty + kp.slot);
             };
             for (int left = units; left > 0 && live;) {
                 live = wait(&m->q_full, qp, m, a.status);
@@ -326,18 +322,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                         scores(t + kStep);
                     }
                     // O (+)= P V
-                    go(entry_v(t, n));
+                    vp.go(t, vstages);
                     // With alternate tiles the weights first: the slot's last
-                    // entry may be the other stream's, and a phase that is two
+                    // tile may be the other stream's, and a phase that is two
                     // behind looks like the awaited one. Once tile t has its
-                    // weights the other stream is past that entry (the turns).
-                    if (kTwo) live = live && wait(m->full + stage, ring_ph, m, a.status);
+                    // weights the other stream is past that tile (the turns).
+                    uint64_t *vfull = m->full + kstages + vp.slot;
+                    if (kTwo) live = live && wait(vfull, vp.ph, m, a.status);
                     live = live && wait(m->p_ready + s, pp, m, a.status);
-                    if (!kTwo) live = live && wait(m->full + stage, ring_ph, m, a.status);
+                    if (!kTwo) live = live && wait(vfull, vp.ph, m, a.status);
                     if (!live) break;
                     pp ^= 1u;
                     tc05::fence_after_sync();
-                    const uint64_t v = vdesc + (uint32_t)(stage * (kTile >> 4));
+                    const uint64_t v = vdesc + (uint32_t)(vp.slot * (kTile >> 4));
                     if (kSplit) {  // the rests, then the weights: a sum of this tile alone
 #pragma unroll
                         for (int hf = 0; hf < D / kOcols; ++hf) {
@@ -360,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int k = 0; k < kKeys / 16; ++k)
                             tc05::mma_ts(to, tp + k * 8, v + k * (2048 >> 4), kIdescO, !(t == t0 && k == 0));
-                    tc05::mma_commit(m->empty + stage);
+                    tc05::mma_commit(m->empty + kstages + vp.slot);
                     if (kApart || kSplit) tc05::mma_commit(m->pv_done + s);
                     if (t + kStep >= n)
                         tc05::mma_commit(m->o_full + s);
@@ -371,8 +368,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     live = wait(m->s_free + s, fp, m, a.status);
                     fp ^= 1u;
                 }
-                go(2 * n);
-                at = 0;
+                kp.go(n, kstages);
+                vp.go(n, vstages);
+                kp.at = vp.at = 0;
             }
             // nothing of this thread's is in flight when the block ends
             tc05::mma_commit(m->fin + s);
@@ -487,11 +485,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // product where zero times them is not zero: a thread a
                     // key, zeros past the end and where there is no page, and
                     // a draft's infinities and NaNs noted and replaced.
-                    // (Two ring entries a tile of the segments before; in its
-                    // turn, since then the slot's last entry has been used.)
-                    const long long pos = 2LL * (units - left) + entry_v(tile, sg.n);
-                    const int vst = (int)(pos % stages);
-                    if (wait(m->full + vst, (uint32_t)(pos / stages) & 1u, m, a.status)) {
+                    // (In its turn, since then the slot's last tile has come.)
+                    const int pos = units - left + tile, vst = kstages + pos % vstages;
+                    if (wait(m->full + vst, (uint32_t)(pos / vstages) & 1u, m, a.status)) {
                         const int key = j * kKeys + tid;
                         uint8_t *row = ring + vst * kTile + tid * 128;
                         const bool none =

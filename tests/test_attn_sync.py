@@ -1,0 +1,52 @@
+"""The barriers of the tcgen05 attention kernels under drawn delays, on a host model: no wait
+passes for another phase than the one it means, no slot is copied into before its last use,
+no block gets stuck. (Such a fault shows on a GPU only when copies are late, if ever.)"""
+import random
+
+import pytest
+
+import attn_sync_model as model
+
+FORMS = {  # what run_tc picks by rows, elements a head and output type
+    "rows128_d128": dict(stages=(3, 3), two=False),
+    "rows128_d128_fp32_from_bf16": dict(stages=(3, 3), two=False, split=True, parted=True),
+    "rows128_d128_fp32_from_fp16": dict(stages=(3, 3), two=False, split=True),
+    "rows128_d64": dict(stages=(6, 6), two=False, apart=True),
+    "rows128_d64_fp32": dict(stages=(6, 6), two=False, split=True),
+    "rows256_d128": dict(stages=(2, 3), two=True),
+    "rows256_d128_fp32_from_bf16": dict(stages=(2, 3), two=True, split=True, parted=True),
+    "rows256_d128_fp32_from_fp16": dict(stages=(2, 3), two=True, split=True),
+    "rows256_d64": dict(stages=(6, 6), two=True, apart=True),
+    "rows256_d64_fp32": dict(stages=(6, 6), two=True, split=True),
+}
+TIMES = [dict(copy=2000, slow=20), dict(copy=3000, slow=5), dict(copy=300, slow=100)]
+
+
+def segments(seed):
+    """Key tiles of the parts of items that a block gets, many of them short (of two tiles at least)."""
+    r = random.Random(seed)
+    return [r.choice([2, 2, 3, 4, 5, 9, 14]) for _ in range(r.randint(1, 5))]
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_attention(form):
+    for times in TIMES:
+        for seed in range(60):
+            model.attn_tc(seed, segments(seed), **FORMS[form], **times)
+
+
+def broken(run, seeds):
+    """The seeds for which the model finds a fault."""
+    bad = []
+    for seed in seeds:
+        try:
+            run(seed)
+        except model.Broken:
+            bad.append(seed)
+    return bad
+
+
+def test_one_ring_for_keys_and_values_is_noticed():
+    """Copiers that know of their own entries only run into entries of the other stream."""
+    assert broken(lambda seed: model.attn_tc(seed, segments(seed), **FORMS["rows128_d128_fp32_from_bf16"], copy=300,
+                                             slow=100, rings=1), range(130, 250))
