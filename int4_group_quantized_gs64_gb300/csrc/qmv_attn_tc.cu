@@ -368,6 +368,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     live = wait(m->s_free + s, fp, m, a.status);
                     fp ^= 1u;
                 }
+                // A stream without tiles here answers too: the segment's table has been
+                // read, and its queries' phase was not missed.
+                if (t0 >= n) mbar_arrive(m->o_full + s);
                 kp.go(n, kstages);
                 vp.go(n, vstages);
                 kp.at = vp.at = 0;
@@ -718,11 +721,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 next.next_item(a);
                 if (kAhead) load_queries(next);
             }
-            if (ns > 0) {
-                wait(m->o_full + s, op, m, a.status);
-                op ^= 1;
-                if (kApart) vp ^= 1u;  // the last product's, which o_full covers
-            }
+            wait(m->o_full + s, op, m, a.status);
+            op ^= 1;
+            if (kApart && ns > 0) vp ^= 1u;  // the last product's, which o_full covers
             __syncwarp();
             if (mx != -INFINITY) mx -= boost;
             m->ml[s][tid] = make_float2(mx, l);

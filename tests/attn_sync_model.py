@@ -150,13 +150,14 @@ class Ring:
 
 
 def attn_tc(seed, segments, stages, two, apart=False, split=False, parted=False, copy=2000.0,
-            slow=20.0, rings=2):
+            slow=20.0, rings=2, ack=True):
     """One block of k_attn_tc over segments of the given numbers of key tiles.
 
     stages: slots for keys and for values; two: both streams take every tile (more than
     128 rows); apart: weights beside the scores (64-element heads); split, parted: fp32
     outputs, O in two halves. rings 1: keys and values by turns in one ring of both's
-    slots, in the order of the products."""
+    slots, in the order of the products. ack False: a stream without tiles in a segment
+    does not answer."""
     rng = random.Random(seed)
     sim = Sim(rng, slow)
     readers = 2 if two else 1
@@ -244,6 +245,8 @@ def attn_tc(seed, segments, stages, two, apart=False, split=False, parted=False,
             if apart and t0 < n:
                 yield s_free[s], fp
                 fp += 1
+            if ack and t0 >= n:
+                sim.arrive(o_full[s])
             base += n
 
     def softmax(s, w):
@@ -283,7 +286,7 @@ def attn_tc(seed, segments, stages, two, apart=False, split=False, parted=False,
                         sim.arrive(p_ready[s])
                         yield pv_done[s], vp
                         vp += 1
-            if ns > 0:
+            if ns > 0 or ack:
                 yield o_full[s], op
                 op += 1
             if apart and ns > 0:

@@ -23,9 +23,9 @@ TIMES = [dict(copy=2000, slow=20), dict(copy=3000, slow=5), dict(copy=300, slow=
 
 
 def segments(seed):
-    """Key tiles of the parts of items that a block gets, many of them short (of two tiles at least)."""
+    """Key tiles of the parts of items that a block gets, many of them short."""
     r = random.Random(seed)
-    return [r.choice([2, 2, 3, 4, 5, 9, 14]) for _ in range(r.randint(1, 5))]
+    return [r.choice([1, 1, 2, 3, 4, 5, 9, 14]) for _ in range(r.randint(1, 5))]
 
 
 @pytest.mark.parametrize("form", FORMS)
@@ -35,18 +35,23 @@ def test_attention(form):
             model.attn_tc(seed, segments(seed), **FORMS[form], **times)
 
 
-def broken(run, seeds):
-    """The seeds for which the model finds a fault."""
-    bad = []
-    for seed in seeds:
+def noticed(run, seeds=1000):
+    """Whether the model finds a fault for one of the seeds."""
+    for seed in range(seeds):
         try:
             run(seed)
         except model.Broken:
-            bad.append(seed)
-    return bad
+            return True
+    return False
 
 
 def test_one_ring_for_keys_and_values_is_noticed():
     """Copiers that know of their own entries only run into entries of the other stream."""
-    assert broken(lambda seed: model.attn_tc(seed, segments(seed), **FORMS["rows128_d128_fp32_from_bf16"], copy=300,
-                                             slow=100, rings=1), range(130, 250))
+    assert noticed(lambda seed: model.attn_tc(seed, segments(seed), **FORMS["rows128_d128_fp32_from_bf16"], copy=300,
+                                              slow=100, rings=1))
+
+
+def test_a_stream_that_does_not_answer_is_noticed():
+    """In a part of one tile the second stream has none; nothing else holds it to that part."""
+    assert noticed(lambda seed: model.attn_tc(seed, segments(seed), **FORMS["rows128_d128"], copy=300, slow=100,
+                                              ack=False))

@@ -739,3 +739,65 @@ def test_steps_of_a_cache_that_is_evicted():
             k, v = cache.k[pg, h, s % page].double(), cache.v[pg, h, s % page].double()
             p = torch.softmax(qq[b, h * G:(h + 1) * G].double() @ k.T * D ** -0.5, 1)
             assert torch.allclose(o2[b, h * G:(h + 1) * G].double(), p @ v, atol=2.0 ** -7, rtol=0)
+
+
+# ------------------------------------------------------------------ many sequences, short items
+
+def check_batch(ctx, drafts, Hkv, G, D, page, dtype, out=None, weights=True, runs=3):
+    """A batch of any number of sequences against 64 bits on the GPU, a chain each; repeats are bit-equal."""
+    g = torch.Generator(device="cuda").manual_seed(len(ctx) + D)
+    B, T = len(ctx), max(drafts)
+    need = [-(-(c + t) // page) for c, t in zip(ctx, drafts)]
+    k = torch.empty(sum(need), Hkv, page, D, dtype=dtype, device="cuda").normal_(generator=g)
+    v = torch.empty_like(k).normal_(generator=g)
+    table = torch.full((B, max(need)), -3, dtype=torch.int32)
+    order = torch.randperm(sum(need), generator=torch.Generator().manual_seed(1)).int()
+    at = np.concatenate([[0], np.cumsum(need)])
+    for b in range(B):
+        table[b, :need[b]] = order[at[b]:at[b + 1]]
+    cu = [0] + np.cumsum(drafts).tolist()
+    qq = torch.empty(cu[-1], Hkv * G, D, dtype=dtype, device="cuda").normal_(generator=g)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    st, cache = torch.zeros(1, **i32), q.AttnCache(k, v)
+    args = (qq, table.cuda(), torch.tensor(ctx, **i32), torch.tensor(cu, **i32), T)
+    first = None
+    for _ in range(runs):
+        acc = torch.full(k.shape[:3], 7.0, device="cuda")
+        o, lse = q.attn_tree(cache, *args, o_dtype=out, acc_out=acc if weights else None, status=st)
+        torch.cuda.synchronize()
+        assert int(st) == 0
+        if first is None:
+            first = (o, lse, acc)
+        assert all(torch.equal(x, y) for x, y in zip(first, (o, lse, acc)))
+    o, lse, acc = first
+    hs = half_step(o.dtype)
+    for b in range(B):
+        t, m = drafts[b], ctx[b] + drafts[b]
+        rows = table[b, :need[b]].long().cuda()
+        kk = k[rows].transpose(1, 2).reshape(-1, Hkv, D)[:m].double()
+        vv = v[rows].transpose(1, 2).reshape(-1, Hkv, D)[:m].double()
+        w = acc[rows].transpose(1, 2).reshape(-1, Hkv).double()
+        if t == 0:
+            assert torch.all(w == 7)       # no step: its sums stay as they are
+            continue
+        x = torch.einsum("thgd,mhd->htgm", qq[cu[b]:cu[b + 1]].view(t, Hkv, G, D).double(), kk) * D ** -0.5
+        late = torch.arange(m, device="cuda") > ctx[b] + torch.arange(t, device="cuda")[:, None]
+        x.masked_fill_(late[None, :, None], -math.inf)
+        e = x.logsumexp(-1)
+        p = torch.exp(x - e[..., None])
+        want = torch.einsum("htgm,mhd->thgd", p, vv).reshape(t, Hkv * G, D)
+        mag = torch.einsum("htgm,mhd->thgd", p, vv.abs()).reshape(t, Hkv * G, D)
+        # the weights' roundings (numerator and sum), scores of rms 1 off by up to 2^-15, the output's rounding
+        tol = mag * (2 * half_step(dtype) + 2.0 ** -14) + want.abs() * hs
+        assert torch.all((o[cu[b]:cu[b + 1]].double() - want).abs() <= tol), b
+        assert torch.allclose(lse[cu[b]:cu[b + 1]].double(), e.permute(1, 0, 2).reshape(t, -1), atol=2.0 ** -14, rtol=0), b
+        if weights:
+            assert torch.allclose(w[:m], p.sum((1, 2)).T, rtol=2.0 ** -13, atol=1e-9), b
+            assert torch.all(w[m:] == 7), b
+
+
+@pytest.mark.parametrize("D,dtype,out", [(128, BF, BF), (64, FP, FP), (128, FP, F32), (128, BF, F32)])
+def test_tree_many_short_items(D, dtype, out):
+    """Items of one key tile and of two, several of them a block: a stream has none in some."""
+    ctx = [[90, 30, 200, 0, 101, 250][b % 6] for b in range(120)]
+    check_batch(ctx, [5 + b % 3 for b in range(120)], 4, 4, D, 32, dtype, out, weights=False)
