@@ -127,7 +127,9 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, Misc *m, in
 // a.rows is so large that an item is a (sequence, head), and a.unit 128 keys.
 // Warps 0-3 and 4-7 take alternate key tiles, 8 and 10 copy them, 9 issues the
 // products of a tile with every 128 queries into four score tiles of tensor
-// memory in turn.
+// memory: two for each group of warps, by turns. (With all four by turns, a tile
+// with four products would lie in the buffers of the other group's last one, whose
+// phases this group has not seen: a wait two phases behind passes at once.)
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1)
     k_weights_tc(const __grid_constant__ CUtensorMap kmap, const TreeArgs a, int row0, int q_tiles, int stages) {
@@ -227,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             const uint64_t kdesc = tc05::sdesc_sw128(tc05::smem_addr(ring));
             const uint64_t qdesc = tc05::sdesc_sw128(tc05::smem_addr(qs));
-            int stage = 0, job = 0;
+            int stage = 0, jobs[2] = {0, 0};  // products so far, of each group
             uint32_t phase = 0, qp = 0;
             bool live = true;
             for (int left = units; left > 0 && live;) {
@@ -239,11 +241,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int t = 0; t < n && live; ++t) {
                     live = wait(m->full + stage, phase, m, a.status);
                     const uint64_t kd = kdesc + (uint32_t)(stage * (kTile >> 4));
+                    const int grp = t & 1;
+                    int job = grp ? jobs[1] : jobs[0];
 #pragma unroll 1
                     for (int r = 0; r < nq && live; ++r, ++job) {
-                        const int buf = job & 3;
-                        if (job >= 4)
-                            live = wait(m->s_free + buf, ((job >> 2) - 1) & 1, m, a.status);
+                        const int buf = 2 * grp + (job & 1);
+                        if (job >= 2)
+                            live = wait(m->s_free + buf, ((job >> 1) - 1) & 1, m, a.status);
                         if (!live) break;
                         tc05::fence_after_sync();
                         const uint64_t qd = qdesc + (uint32_t)(r * (kTile >> 4));
@@ -254,6 +258,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         tc05::mma_commit(m->s_full + buf);
                     }
+                    if (grp)
+                        jobs[1] = job;
+                    else
+                        jobs[0] = job;
                     tc05::mma_commit(m->empty + stage);
                     if (++stage == stages) {
                         stage = 0;
@@ -270,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         Cursor c;
         c.start(a, sh);
-        int job0 = 0;
+        int job = 0;  // this group's products so far
         bool waited = false;
         const uint64_t sl2 = pack_f32x2(a.sl2, a.sl2);
         for (int left = units; left > 0;) {
@@ -364,9 +372,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 uint64_t sum[2] = {0, 0};
 #pragma unroll 1
-                for (int r = 0; r < nq; ++r) {
-                    const int job = job0 + t * nq + r, buf = job & 3;
-                    wait(m->s_full + buf, (job >> 2) & 1, m, a.status);
+                for (int r = 0; r < nq; ++r, ++job) {
+                    const int buf = 2 * s + (job & 1);
+                    wait(m->s_full + buf, (job >> 1) & 1, m, a.status);
                     __syncwarp();
                     tc05::fence_after_sync();
                     if (special) {  // scores of rows that do not see the key become -inf
@@ -419,7 +427,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             asm volatile("bar.sync 1, 256;" ::: "memory");
-            job0 += n * nq;
             left -= n;
             if (left > 0) c.next_item(a);
         }

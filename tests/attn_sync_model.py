@@ -1,4 +1,4 @@
-"""A host model of the warps, copies, products and barriers of a tcgen05 attention kernel.
+"""A host model of the warps, copies, products and barriers of the tcgen05 attention kernels.
 
 Every warp is a generator that yields what it waits for; the times of copies, products
 and steps are drawn. A barrier knows how many of its phases are complete, and a wait
@@ -6,8 +6,9 @@ is the hardware's: it passes when the phase's parity says so. Each wait also car
 the phase that it means, so that one which passes for another phase, a slot that is
 copied into before its last use, or a table that is read too late raises Broken.
 
-`attn_tc` follows csrc/qmv_attn_tc.cu (k_attn_tc). Its keyword arguments can choose a
-protocol that was found wanting, which the model has to notice.
+`attn_tc` follows csrc/qmv_attn_tc.cu (k_attn_tc), `weights_tc` csrc/qmv_attn_weights.cu
+(k_weights_tc). Their keyword arguments can choose a protocol that was found wanting,
+which the model has to notice.
 """
 import heapq
 import random
@@ -301,6 +302,91 @@ def attn_tc(seed, segments, stages, two, apart=False, split=False, parted=False,
     sim.start("copies of values", copier(vring, entry_v))
     for s in range(2):
         sim.start(f"products {s}", products(s))
+        for w in range(4):
+            sim.start(f"softmax {s}.{w}", softmax(s, w))
+    sim.run()
+
+
+def weights_tc(seed, segments, stages, copy=2000.0, slow=20.0, own_buffers=True):
+    """One block of k_weights_tc over segments of (key tiles, row tiles).
+
+    own_buffers False: score buffers in the order of all products, whichever group takes
+    them."""
+    rng = random.Random(seed)
+    sim = Sim(rng, slow)
+    ring = Ring(sim, "keys'", stages, 1)
+    s_full = [Barrier(f"s_full[{i}]", 1) for i in range(4)]
+    s_free = [Barrier(f"s_free[{i}]", 4) for i in range(4)]
+    held = [None] * 4
+    q_full = Barrier("q_full", 8)
+    tables = {}
+    crowd = []
+    units = sum(n for n, _ in segments)
+
+    def place(group, mine, job):
+        return (2 * group + (mine & 1), mine >> 1) if own_buffers else (job & 3, job >> 2)
+
+    def copier(first):
+        for x in range(first, units, 2):
+            yield ring.may_copy(x)
+            ring.copy(x, copy)
+            yield sim.jitter(60)
+
+    def products():
+        unit = Issuer(sim)
+        x = job = 0
+        count = [0, 0]
+        for k, (n, nq) in enumerate(segments):
+            yield q_full, k
+            if tables.get("now") != (k, n, nq):
+                raise Broken(f"products of segment {k} read the tables of {tables.get('now')}")
+            for t in range(n):
+                yield ring.landed_wait(x)
+                ring.read(x)
+                for _ in range(nq):
+                    buf, phase = place(t & 1, count[t & 1], job)
+                    if phase > 0:
+                        yield s_free[buf], phase - 1
+                    if held[buf] is not None:
+                        raise Broken(f"scores {held[buf]} are overwritten in use")
+                    held[buf] = job
+                    unit.product(256)
+                    unit.commit(s_full[buf])
+                    count[t & 1] += 1
+                    job += 1
+                    yield sim.jitter(20)
+                ring.release(x, unit)
+                x += 1
+
+    def softmax(s, w):
+        job0 = mine = 0
+        for k, (n, nq) in enumerate(segments):
+            yield sim.jitter(400)
+            if s == 0 and w == 0:
+                tables["now"] = (k, n, nq)
+            sim.arrive(q_full)
+            yield crowd, 8
+            for t in range(s, n, 2):
+                yield sim.jitter(50)
+                for r in range(nq):
+                    job = job0 + t * nq + r
+                    buf, phase = place(s, mine, job)
+                    yield s_full[buf], phase
+                    if held[buf] != job:
+                        raise Broken(f"scores {job} are read, the buffer holds {held[buf]}")
+                    yield sim.jitter(600)
+                    mine += 1
+                    # (the warps' reads end together with the last arrival)
+                    if s_free[buf].left == 1:
+                        held[buf] = None
+                    sim.arrive(s_free[buf])
+            yield crowd, 8
+            job0 += n * nq
+
+    for first in range(2):
+        sim.start(f"copies {first}", copier(first))
+    sim.start("products", products())
+    for s in range(2):
         for w in range(4):
             sim.start(f"softmax {s}.{w}", softmax(s, w))
     sim.run()

@@ -55,3 +55,26 @@ def test_a_stream_that_does_not_answer_is_noticed():
     """In a part of one tile the second stream has none; nothing else holds it to that part."""
     assert noticed(lambda seed: model.attn_tc(seed, segments(seed), **FORMS["rows128_d128"], copy=300, slow=100,
                                               ack=False))
+
+
+# Ring slots that run puts beside the queries of 1 to 4 row tiles.
+RINGS = [(1, 5), (2, 4), (3, 3), (4, 2), (1, 12), (2, 11), (3, 10), (4, 9)]
+
+
+def rows(seed, most):
+    """Key tiles and row tiles of a block's parts: ragged trees have up to `most`."""
+    r = random.Random(seed)
+    return [(n, r.randint(1, most)) for n in segments(seed)]
+
+
+@pytest.mark.parametrize("most,stages", RINGS)
+def test_weights(most, stages):
+    for times in TIMES:
+        for seed in range(60):
+            model.weights_tc(seed, rows(seed, most), stages, **times)
+            model.weights_tc(seed, [(n, most) for n in segments(seed)], stages, **times)
+
+
+def test_score_buffers_of_both_groups_by_turns_are_noticed():
+    """Four products a tile: a group's buffers were last the other group's."""
+    assert noticed(lambda seed: model.weights_tc(seed, [(n, 4) for n in segments(seed)], 2, own_buffers=False))

@@ -801,3 +801,15 @@ def test_tree_many_short_items(D, dtype, out):
     """Items of one key tile and of two, several of them a block: a stream has none in some."""
     ctx = [[90, 30, 200, 0, 101, 250][b % 6] for b in range(120)]
     check_batch(ctx, [5 + b % 3 for b in range(120)], 4, 4, D, 32, dtype, out, weights=False)
+
+
+@pytest.mark.parametrize("D,page,dtype", [(128, 64, BF), (64, 32, FP)])
+def test_tree_weights_of_four_row_tiles_over_long_contexts(D, page, dtype):
+    """385 to 512 rows: four products a key tile, score buffers used over and over, ring of two slots."""
+    check_batch([2500 - 171 * b for b in range(12)], [64 - b % 16 for b in range(12)], 8, 8, D, page, dtype)
+
+
+def test_tree_weights_of_ragged_row_tiles():
+    """One to four products a tile, parts of one tile and of many in a block."""
+    check_batch([[120, 40, 700, 3][b % 4] for b in range(60)], [[64, 5, 33, 20, 50][b % 5] for b in range(60)],
+                4, 8, 128, 64, BF)
