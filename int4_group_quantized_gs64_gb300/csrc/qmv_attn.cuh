@@ -106,6 +106,7 @@ struct Seqs {
     const int32_t *ctx;    // [B] cached tokens before the call
     const int32_t *cu;     // [B + 1] first new token of each sequence
     int B, N, max_draft, max_pages, page, lpage;  // page = 1 << lpage
+    int min_draft;  // sequences of fewer new tokens count as empty
 };
 
 struct Seq {
@@ -122,7 +123,7 @@ __device__ __forceinline__ Seq get_seq(const Seqs &s, int b, bool &ok) {
     ok = q.ctx >= 0 && q.first >= 0 && end >= q.first && end <= s.N &&
          (s.max_draft == 0 || end - q.first <= s.max_draft) &&
          (long long)q.ctx + (end - q.first) <= ((long long)s.max_pages << s.lpage);
-    q.T = ok ? end - q.first : 0;
+    q.T = ok && end - q.first >= s.min_draft ? end - q.first : 0;
     if (!ok) q.ctx = 0;
     return q;
 }

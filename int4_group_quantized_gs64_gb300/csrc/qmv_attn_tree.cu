@@ -697,7 +697,7 @@ cudaError_t launch_attn_tree(const AttnCache &c, const TreeCall &t, cudaStream_t
     memset(&a, 0, sizeof(a));
     int lpage = 0;
     while ((1 << lpage) < c.page) ++lpage;
-    a.s = Seqs{t.s.table, t.s.ctx, t.s.cu, t.s.B, t.s.N, t.s.max_draft, t.s.max_pages, c.page, lpage};
+    a.s = Seqs{t.s.table, t.s.ctx, t.s.cu, t.s.B, t.s.N, t.s.max_draft, t.s.max_pages, c.page, lpage, 0};
     a.q = static_cast<const uint16_t *>(t.q);
     a.q_stride = t.q_stride;
     a.Hq = t.Hq; a.Hkv = c.Hkv; a.G = t.Hq / c.Hkv; a.pages = c.pages;

@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int left = units; left > 0;) {
             const Seq q = c.q;
             const int j0 = c.u, n = min(c.nu - c.u, left), nrows = min(q.T * a.G - row0, kMaxRows);
-            const int nq = nrows > 0 ? (nrows + 127) / 128 : 0;
+            const int nq = (nrows + 127) / 128;
             // queries, and -lse of each
             constexpr int kChunks = D / 8, kPass = 256 / kChunks;
             const int ch = threadIdx.x % kChunks;
@@ -456,6 +456,9 @@ cudaError_t run(const AttnCache &c, const TreeArgs &a, int max_rows, cudaStream_
     auto *k = k_weights_tc<D, kBf16>;
     cudaError_t e = set_smem(k, kSmemMax);
     for (int row0 = 0; row0 < max_rows && e == cudaSuccess; row0 += kMaxRows) {
+        // Only sequences that have rows from row0 on: in a part without products
+        // nothing would hold the softmax warps until its tables have been read.
+        w.s.min_draft = row0 / w.G + 1;
         const int rows = max_rows - row0 < kMaxRows ? max_rows - row0 : kMaxRows;
         const int q_tiles = (rows + 127) / 128;
         int stages = (kSmemMax - kMisc - q_tiles * kTile) / kTile;

@@ -281,7 +281,7 @@ cudaError_t launch_rope_append(const AttnCache &c, const AttnSeqs &s, const Rope
     int lpage = 0;
     while ((1 << lpage) < c.page) ++lpage;
     RopeArgs a;
-    a.s = Seqs{s.table, s.ctx, s.cu, s.B, s.N, 0, s.max_pages, c.page, lpage};
+    a.s = Seqs{s.table, s.ctx, s.cu, s.B, s.N, 0, s.max_pages, c.page, lpage, 0};
     a.q = q.p; a.k = k.p; a.v = v.p;
     a.qs = q.stride; a.ks = k.stride; a.vs = v.stride;
     a.Hq = Hq; a.Hkv = c.Hkv; a.D = c.D; a.rot = rot; a.pages = c.pages;

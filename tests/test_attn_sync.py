@@ -78,3 +78,8 @@ def test_weights(most, stages):
 def test_score_buffers_of_both_groups_by_turns_are_noticed():
     """Four products a tile: a group's buffers were last the other group's."""
     assert noticed(lambda seed: model.weights_tc(seed, [(n, 4) for n in segments(seed)], 2, own_buffers=False))
+
+
+def test_parts_without_products_are_noticed():
+    """(The plan leaves out sequences that have no rows in a launch.)"""
+    assert noticed(lambda seed: model.weights_tc(seed, [(n, nq - 1) for n, nq in rows(seed, 3)], 3))

@@ -813,3 +813,10 @@ def test_tree_weights_of_ragged_row_tiles():
     """One to four products a tile, parts of one tile and of many in a block."""
     check_batch([[120, 40, 700, 3][b % 4] for b in range(60)], [[64, 5, 33, 20, 50][b % 5] for b in range(60)],
                 4, 8, 128, 64, BF)
+
+
+@pytest.mark.parametrize("D,G,big", [(128, 8, 100), (64, 5, 250)])
+def test_tree_weights_of_ragged_batches_beyond_one_launch(D, G, big):
+    """A few large trees among many small ones: most sequences have no rows beyond the first 512."""
+    check_batch([[70, 900, 130, 20][b % 4] for b in range(64)], [big if b % 21 == 3 else 3 for b in range(64)],
+                8, G, D, 32, BF)
