@@ -404,7 +404,9 @@ typedef struct {
  *   ctx     [B] int32: the tokens of each sequence already in the cache.
  *   cu      [B + 1] int32: the first new token of each sequence, cu[B] = N;
  *           sequence b's new tokens cu[b] .. cu[b + 1] - 1 have slots
- *           ctx[b], ctx[b] + 1, ...
+ *           ctx[b], ctx[b] + 1, ... (A descending cu gives a sequence of
+ *           negative length, which is left out, and tokens of several: such a
+ *           token's keys and values go to the last of these.)
  *   status  [1] int32 or NULL, OR-ed (not cleared) with
  *             1  a page id outside [0, pages): its tokens are left out;
  *             2  a sequence whose lengths are negative, do not fit its row of

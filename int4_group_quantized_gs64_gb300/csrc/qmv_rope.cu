@@ -98,11 +98,13 @@ __device__ __forceinline__ float2 turn_of(const RopeArgs &a, double pos, int i) 
 // Where a token goes in the cache: its page and row; false if nowhere (the
 // status says why). Whole warp.
 __device__ __forceinline__ bool find_slot(const RopeArgs &a, int n, int lane, int &pid, int &row) {
-    // its sequence is the last that starts at or before it
+    // its sequence holds it (the last of them, where cu is not ascending)
     int b = -1;
     for (int j0 = 0; j0 < a.s.B; j0 += 32) {
         const int j = j0 + lane;
-        b += __popc(__ballot_sync(0xFFFFFFFFu, j < a.s.B && a.s.cu[j] <= n));
+        const uint32_t who =
+            __ballot_sync(0xFFFFFFFFu, j < a.s.B && a.s.cu[j] <= n && n < a.s.cu[j + 1]);
+        if (who) b = j0 + 31 - __clz(who);
     }
     bool ok = false;
     Seq q;
@@ -119,6 +121,17 @@ __device__ __forceinline__ bool find_slot(const RopeArgs &a, int n, int lane, in
     const bool good = ok && (unsigned)pid < (unsigned)a.pages;
     if (lane == 0 && !good) set_status(a.status, ok ? kStPage : kStLength);
     return good;
+}
+
+// Lengths that do not fit, of sequences without tokens too (one warp of the
+// grid, when its rows are on their way).
+__device__ __forceinline__ void check_lengths(const RopeArgs &a, int lane) {
+    if (!a.status) return;
+    for (int b = lane; b < a.s.B; b += 32) {
+        bool ok;
+        get_seq(a.s, b, ok);
+        if (!ok) set_status(a.status, kStLength);
+    }
 }
 
 struct Head {
@@ -219,6 +232,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_rope_append(const RopeArgs a) {
             }
         }
     }
+    if (w == 0) check_lengths(a, lane);
 }
 
 // Any alignment and any even rot: a lane takes a pair (or two elements past
@@ -258,6 +272,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_rope_any(const RopeArgs a) {
             }
         }
     }
+    if (w == 0) check_lengths(a, lane);
 }
 
 template <bool kBf16, bool kF32, bool kInter>

@@ -820,3 +820,59 @@ def test_tree_weights_of_ragged_batches_beyond_one_launch(D, G, big):
     """A few large trees among many small ones: most sequences have no rows beyond the first 512."""
     check_batch([[70, 900, 130, 20][b % 4] for b in range(64)], [big if b % 21 == 3 else 3 for b in range(64)],
                 8, G, D, 32, BF)
+
+
+# ------------------------------------------------------------------ first tokens out of order
+
+@pytest.mark.parametrize("cu,ctx", [([0, 10, 20, 0, 30], [0, 30, 0, 0]), ([5, 10, 0, 10], [0, 0, 0]),
+                                    ([3, 7, 7, 2], [4, 9, 0]), ([-4, 6, 12], [3, 8]), ([0, 9, 40, 12], [0, 2, 5])])
+@pytest.mark.parametrize("rot", [32, 6])
+def test_rope_first_tokens_out_of_order(cu, ctx, rot):
+    """A token goes to the last sequence that holds it and nowhere else; sequences of negative length
+    or beyond N are left out. (A guard page on each side of the sequences' own stays as it was.)"""
+    B, Hkv, G, D, page, N = len(ctx), 2, 2, 64, 16, 30 if max(cu) > 20 else 12
+    c = Case([48] * B, [0] * B, Hkv, G, D, page, BF, seed=B, mask=None, spare=6).dev()
+    g = torch.Generator().manual_seed(5)
+    qkv = torch.randn(N, c.Hq + 2 * Hkv, D, generator=g).to(BF).cuda()
+    i32 = dict(dtype=torch.int32, device="cuda")
+    # the table in the middle of a larger one: what lies beside it names pages too
+    pages = c.k.shape[0]
+    used = {p for r in c.table_l for p in r}
+    free = [p for p in range(pages) if p not in used]
+    wide = torch.tensor([[free[0]] * 3] * 2 + c.table_l + [[free[1]] * 3] * 2, **i32)
+    table = wide[2:2 + B]
+    st = torch.zeros(1, **i32)
+    q.attn_rope_append(c.cache, qkv[:, :c.Hq], qkv[:, c.Hq:c.Hq + Hkv], qkv[:, c.Hq + Hkv:],
+                       torch.zeros(N, **i32), torch.ones(rot // 2, dtype=torch.float64, device="cuda"), table,
+                       torch.tensor(ctx, **i32), torch.tensor(cu, **i32), status=st)
+    torch.cuda.synchronize()
+    assert int(st) == 2
+    want = c.v.clone()
+    for n in range(N):
+        held = [b for b in range(B) if cu[b] <= n < cu[b + 1]]
+        if held and cu[held[-1]] >= 0 and cu[held[-1] + 1] <= N:
+            b = held[-1]
+            slot = ctx[b] + n - cu[b]
+            want[c.table_l[b][slot // page], :, slot % page] = qkv[n, c.Hq + Hkv:].cpu()
+    assert torch.equal(c.cache.v.cpu(), want)
+
+
+def test_rope_many_sequences():
+    """More than 32 sequences, some without tokens."""
+    lens = [(7 * b) % 50 for b in range(150)]
+    drafts = [b % 4 for b in range(150)]
+    c = Case(lens, drafts, 2, 2, 64, 16, FP, seed=1, mask=None).dev()
+    g = torch.Generator().manual_seed(6)
+    qkv = torch.randn(c.N, c.Hq + 4, 64, generator=g).to(FP).cuda()
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = q.attn_rope_append(c.cache, qkv[:, :4], qkv[:, 4:6], qkv[:, 6:], torch.zeros(c.N, dtype=torch.int32).cuda(),
+                             torch.ones(32, dtype=torch.float64).cuda(), c.table.cuda(), c.ctx, c.cu, status=st)
+    torch.cuda.synchronize()
+    assert int(st) == 0 and torch.equal(out, qkv[:, :4])      # positions 0: nothing turns
+    k, v = c.k.clone(), c.v.clone()
+    for b in range(c.B):
+        for t in range(drafts[b]):
+            s = lens[b] + t
+            k[c.table_l[b][s // 16], :, s % 16] = qkv[c.cu_l[b] + t, 4:6].cpu()
+            v[c.table_l[b][s // 16], :, s % 16] = qkv[c.cu_l[b] + t, 6:].cpu()
+    assert torch.equal(c.cache.k.cpu(), k) and torch.equal(c.cache.v.cpu(), v)
