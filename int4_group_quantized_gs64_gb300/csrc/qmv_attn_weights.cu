@@ -285,7 +285,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Seq q = c.q;
             const int j0 = c.u, n = min(c.nu - c.u, left), nrows = min(q.T * a.G - row0, kMaxRows);
             const int nq = (nrows + 127) / 128;
-            // queries, and -lse of each
+            // queries, and -lse of each. Past the last row its query again, with no
+            // weight: zeros there would make a NaN of a key's infinity, where the
+            // last row's score is one that counts anyway.
             constexpr int kChunks = D / 8, kPass = 256 / kChunks;
             const int ch = threadIdx.x % kChunks;
             const uint16_t *p = a.q + (long long)q.first * a.q_stride + (long long)c.h * a.G * D + ch * 8;
@@ -302,10 +304,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 128 / kPass; ++i) {
                     const int r = threadIdx.x / kChunks + i * kPass;
-                    const uint32_t keep = rt * 128 + r < nrows ? a.qand : 0u;
                     *reinterpret_cast<uint4 *>(dst + rt * kTile + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) =
-                        make_uint4((v[i].x ^ a.qxor) & keep, (v[i].y ^ a.qxor) & keep,
-                                   (v[i].z ^ a.qxor) & keep, (v[i].w ^ a.qxor) & keep);
+                        make_uint4((v[i].x ^ a.qxor) & a.qand, (v[i].y ^ a.qxor) & a.qand,
+                                   (v[i].z ^ a.qxor) & a.qand, (v[i].w ^ a.qxor) & a.qand);
                 }
             }
             tc05::fence_proxy_async();

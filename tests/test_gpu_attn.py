@@ -876,3 +876,35 @@ def test_rope_many_sequences():
             k[c.table_l[b][s // 16], :, s % 16] = qkv[c.cu_l[b] + t, 4:6].cpu()
             v[c.table_l[b][s // 16], :, s % 16] = qkv[c.cu_l[b] + t, 6:].cpu()
     assert torch.equal(c.cache.k.cpu(), k) and torch.equal(c.cache.v.cpu(), v)
+
+
+# ------------------------------------------------------------------ infinities in cached keys and values
+
+@pytest.mark.parametrize("T,G,D", [(1, 4, 64), (7, 3, 64), (5, 8, 128), (20, 8, 128)])
+def test_tree_weights_with_infinite_keys(T, G, D):
+    """A cached key that scores -inf in every row adds no weight, whatever the number of rows (queries
+    beside the last row's must not add a NaN); the others' weights are those without it."""
+    c = Case([150, 40], [T, T], 2, G, D, 16, BF, seed=11, qscale=2.0, mask=None)
+    c.q[..., 0] = c.q[..., 0].abs() + 0.5
+    spot = [(0, 17), (1, 0), (0, 149)]
+    for b, j in spot:
+        c.k[c.table_l[b][j // 16], :, j % 16] = 0.0
+        c.k[c.table_l[b][j // 16], :, j % 16, 0] = -math.inf
+    out = torch.full(c.acc.shape, 5.0, device="cuda")
+    o, lse = run_tree(c, acc=c.acc.cuda(), acc_out=out, decay=0.5)
+    for b, j in spot:   # 64-bit form: such keys are not seen
+        c.k[c.table_l[b][j // 16], :, j % 16] = 0.0
+    seen = c.seen
+
+    def without(b):
+        m = seen(b)
+        for bb, j in spot:
+            if bb == b:
+                m[:, j] = False
+        return m
+    c.seen = without
+    s = D ** -0.5
+    ref = c.reference(s, 0.5, c.acc)
+    check_tree(c, o, lse, ref, p_rounding(c, s, BF))
+    t = ref[6]
+    assert torch.all((out.cpu().double() - ref[4])[t].abs() <= ref[5][t])
