@@ -739,7 +739,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     L = v0.y * f0 + v1.y * f1;
                 }
                 const bool has1 = !kTwo && sg.n > 1;
-                const float inv = sg.whole ? (L == 0.f ? 0.f : 1.f / L) : 1.f;
+                const float inv = sg.whole ? 1.f / L : 1.f;
+                const bool none = sg.whole && L == 0.f;  // no weight: zero, also where a value is infinite
                 const long long row =
                     (long long)(q.first + t) * a.Hq + c.h * a.G + (row_live ? rr - t * a.G : 0);
                 const int seg_last = left == units ? 0 : 1, prow = (kTwo ? s * 128 : 0) + tid;
@@ -781,7 +782,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (row_live) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] *= inv;
+                        for (int e = 0; e < 32; ++e) o[e] = none ? 0.f : o[e] * inv;
                         if (!sg.whole) {
                             float *p = part_at<D>(a, blockIdx.x, seg_last, prow, k * 32);
 #pragma unroll

@@ -456,9 +456,9 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
             }
             float2 v = *reinterpret_cast<const float2 *>(buf + r * D + (col ^ ((r & 3) << 3)));
             if (whole) {
-                const float inv = L == 0.f ? 0.f : 1.f / L;
-                v.x *= inv;
-                v.y *= inv;
+                // (no weight: zero, where a value's infinity has made a NaN of 0 x inf too)
+                v.x = L == 0.f ? 0.f : v.x * (1.f / L);
+                v.y = L == 0.f ? 0.f : v.y * (1.f / L);
                 const int t = div_g(a, r);
                 const long long row = (long long)(sq.first + t) * a.Hq + seg_h * a.G + r - t * a.G;
                 if (a.o_f32)
@@ -574,6 +574,11 @@ __global__ void __launch_bounds__(128 * kSplit) k_attn_join(const TreeArgs a, bo
         }
     }
     if (!have_row) return;
+    if (L == 0.f)  // no weight: zero, where a value's infinity has made a NaN of 0 x inf too
+#pragma unroll
+        for (int i = 0; i < kCols; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
     const float inv = L == 0.f ? 0.f : 1.f / L;
     const int rr = rb * a.rows + r, t = div_g(a, rr);
     const long long row = (long long)(q.first + t) * a.Hq + h * a.G + rr - t * a.G;

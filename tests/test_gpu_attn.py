@@ -908,3 +908,24 @@ def test_tree_weights_with_infinite_keys(T, G, D):
     check_tree(c, o, lse, ref, p_rounding(c, s, BF))
     t = ref[6]
     assert torch.all((out.cpu().double() - ref[4])[t].abs() <= ref[5][t])
+
+
+@pytest.mark.parametrize("out", [BF, F32])
+@pytest.mark.parametrize("T,G,D,ctx", [(1, 4, 64, 40), (2, 4, 128, 3000), (20, 8, 128, 40), (9, 4, 64, 3000),
+                                       (40, 8, 128, 300), (40, 8, 64, 300)])
+def test_tree_rows_of_scores_minus_inf(T, G, D, ctx, out):
+    """A row whose keys all score -inf gets zeros, whatever the values are, one block a row or several."""
+    c = Case([ctx], [T], 1, G, D, 64, BF, seed=12)
+    c.q[..., 0] = c.q[..., 0].abs() + 0.5
+    c.k.zero_()
+    c.k[..., 0] = -math.inf
+    c.v[:, :, ::3] = math.inf
+    c.v[:, :, 1::3, ::2] = math.nan
+    weights = torch.full(c.acc.shape, 5.0, device="cuda")
+    o, lse = run_tree(c, o_dtype=out, acc=c.acc.cuda(), acc_out=weights)
+    assert torch.all(o == 0) and torch.all(lse == -math.inf)
+    held = torch.zeros(c.k.shape[0], 64, dtype=torch.bool)
+    for j in range(ctx + T):
+        held[c.table_l[0][j // 64], j % 64] = True
+    held = held[:, None].expand(-1, 1, -1)
+    assert torch.equal(weights.cpu()[held], c.acc[held])
