@@ -239,66 +239,28 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
                         mma16816<kBf16>(s[2 * j], qf[k], kb[0], kb[1]);
                         mma16816<kBf16>(s[2 * j + 1], qf[k], kb[2], kb[3]);
                     }
-                if (s0 + kSub * 16 > sq.ctx || copied != (1 << kSub) - 1) {
-                    // drafts, the end of the sequence or a missing page in this slice
-                    const int len = sq.ctx + sq.T;
-                    uint32_t see[2];  // of this slice's keys, by row
-                    uint32_t there = 0;
+                // drafts, the end of the sequence or a missing page in this slice
+                const bool special = s0 + kSub * 16 > sq.ctx || copied != (1 << kSub) - 1;
+                auto there = [&]() {  // its keys that were copied
+                    uint32_t w = 0;
 #pragma unroll
                     for (int j = 0; j < kSub; ++j)
-                        if ((copied >> j) & 1) there |= 0xFFFFu << (16 * j);
+                        if ((copied >> j) & 1) w |= 0xFFFFu << (16 * j);
+                    return w;
+                };
+                auto sees = [&](int e) {  // and those that this lane's row sees
+                    return rt[e] >= 0 ? seen_word(a, sq, rt[e], s0) & there() : 0u;
+                };
+                if (special) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        see[e] = rt[e] >= 0 ? seen_word(a, sq, rt[e], s0) & there : 0u;
+                        const uint32_t see = sees(e);
 #pragma unroll
                         for (int n = 0; n < kNt; ++n)
 #pragma unroll
                             for (int i = 0; i < 2; ++i)
-                                if (!((see[e] >> (n * 8 + c * 2 + i)) & 1u)) s[n][2 * e + i] = -INFINITY;
+                                if (!((see >> (n * 8 + c * 2 + i)) & 1u)) s[n][2 * e + i] = -INFINITY;
                     }
-                    // Values that some row must not see are kept out of the
-                    // product where zero times them is not zero: rows past the
-                    // end (whatever an unused slot holds) and missing ones become
-                    // zeros, and a draft's infinities and NaNs are added to the
-                    // rows that see it and replaced by zeros.
-                    for (int j = 0; j < kSub * 16; ++j) {
-                        const int key = s0 + j;
-                        const bool none = key >= len || !((there >> j) & 1u);
-                        if (key < sq.ctx && !none) continue;
-                        const uint32_t row = vs + (j >> 4) * S::kPart;
-                        bool bad = false;
-                        for (int w = lane; w < D / 2; w += 32) {
-                            const uint32_t ad = row + slice_ofs<16>(j & 15, w >> 2) + (w & 3) * 4;
-                            if (none)
-                                sts32(ad, 0u);
-                            else
-                                bad |= nonfinite2<kBf16>(lds32(ad));
-                        }
-                        if (__any_sync(0xFFFFFFFFu, bad)) {
-                            __syncwarp();
-#pragma unroll
-                            for (int e = 0; e < 2; ++e)
-                                if ((see[e] >> j) & 1u)
-#pragma unroll
-                                    for (int n = 0; n < D / 8; ++n) {
-                                        const float2 f = unpack2<kBf16>(
-                                            lds32(row + slice_ofs<16>(j & 15, n) + c * 4));
-                                        if (!isfinite(f.x)) o[n][2 * e] += f.x;
-                                        if (!isfinite(f.y)) o[n][2 * e + 1] += f.y;
-                                    }
-                            __syncwarp();
-                            for (int w = lane; w < D / 2; w += 32) {
-                                const uint32_t ad = row + slice_ofs<16>(j & 15, w >> 2) + (w & 3) * 4;
-                                uint32_t v = lds32(ad);
-                                if (nonfinite2<kBf16>(v & 0xFFFFu)) v &= 0xFFFF0000u;
-                                if (nonfinite2<kBf16>(v & 0xFFFF0000u)) v &= 0x0000FFFFu;
-                                sts32(ad, v);
-                            }
-                        }
-                    }
-                    // the next copy into this slot comes from the async proxy
-                    tc05::fence_proxy_async();
-                    __syncwarp();
                 }
                 if (a.stash) {  // the masked scores, for the weights' own pass
 #pragma unroll
@@ -349,6 +311,54 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
                             p1 -= f.y;
                         }
                     }
+                }
+                if (special) {
+                    // Values that some row must not see are kept out of the
+                    // product where zero times them is not zero: rows past the
+                    // end (whatever an unused slot holds) and missing ones become
+                    // zeros, and a draft's infinities and NaNs are added to the
+                    // rows that see it (after the move of the maximum, whose factor
+                    // may be zero) and replaced by zeros.
+                    const int len = sq.ctx + sq.T;
+                    const uint32_t all = there(), see[2] = {sees(0), sees(1)};
+                    for (int j = 0; j < kSub * 16; ++j) {
+                        const int key = s0 + j;
+                        const bool none = key >= len || !((all >> j) & 1u);
+                        if (key < sq.ctx && !none) continue;
+                        const uint32_t row = vs + (j >> 4) * S::kPart;
+                        bool bad = false;
+                        for (int w = lane; w < D / 2; w += 32) {
+                            const uint32_t ad = row + slice_ofs<16>(j & 15, w >> 2) + (w & 3) * 4;
+                            if (none)
+                                sts32(ad, 0u);
+                            else
+                                bad |= nonfinite2<kBf16>(lds32(ad));
+                        }
+                        if (__any_sync(0xFFFFFFFFu, bad)) {
+                            __syncwarp();
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                if ((see[e] >> j) & 1u)
+#pragma unroll
+                                    for (int n = 0; n < D / 8; ++n) {
+                                        const float2 f = unpack2<kBf16>(
+                                            lds32(row + slice_ofs<16>(j & 15, n) + c * 4));
+                                        if (!isfinite(f.x)) o[n][2 * e] += f.x;
+                                        if (!isfinite(f.y)) o[n][2 * e + 1] += f.y;
+                                    }
+                            __syncwarp();
+                            for (int w = lane; w < D / 2; w += 32) {
+                                const uint32_t ad = row + slice_ofs<16>(j & 15, w >> 2) + (w & 3) * 4;
+                                uint32_t v = lds32(ad);
+                                if (nonfinite2<kBf16>(v & 0xFFFFu)) v &= 0xFFFF0000u;
+                                if (nonfinite2<kBf16>(v & 0xFFFF0000u)) v &= 0x0000FFFFu;
+                                sts32(ad, v);
+                            }
+                        }
+                    }
+                    // the next copy into this slot comes from the async proxy
+                    tc05::fence_proxy_async();
+                    __syncwarp();
                 }
 #pragma unroll
                 for (int k = 0; k < KK; ++k) {

@@ -929,3 +929,23 @@ def test_tree_rows_of_scores_minus_inf(T, G, D, ctx, out):
         held[c.table_l[0][j // 64], j % 64] = True
     held = held[:, None].expand(-1, 1, -1)
     assert torch.equal(weights.cpu()[held], c.acc[held])
+
+
+@pytest.mark.parametrize("dt", [BF, FP])
+@pytest.mark.parametrize("out", ["same", "fp32"])
+@pytest.mark.parametrize("T,G,D,ctx", [(1, 4, 64, 0), (3, 4, 128, 37), (3, 4, 128, 200), (20, 8, 128, 37), (40, 8, 64, 130)])
+def test_tree_infinite_values_of_drafts_that_are_seen(T, G, D, ctx, out, dt):
+    """An infinity among a seen draft's values is the output's too, where nothing else moves it: also in a
+    row's first keys, and where the draft's score is far above the keys' before it."""
+    c = Case([ctx], [T], 1, G, D, 16, dt, seed=13, mask=None)
+    c.q[..., 0] = 30.0
+    c.k[..., 0] = -30.0 if ctx else 1.0
+    j = ctx
+    pg, rw = c.table_l[0][j // 16], j % 16
+    c.k[pg, 0, rw, 0] = 30.0       # the first draft, which every row sees, has by far the largest score
+    c.v[pg, 0, rw, 0::2] = math.inf
+    c.v[pg, 0, rw, 1] = -math.inf
+    o, lse = run_tree(c, o_dtype=F32 if out == "fp32" else dt, scale=1.0)
+    assert torch.isfinite(lse).all()
+    assert torch.all(o[..., 0::2] == math.inf) and torch.all(o[..., 1] == -math.inf)
+    assert torch.isfinite(o[..., 3::2]).all()
