@@ -459,16 +459,24 @@ size_t attn_tree_workspace_bytes(const qmv_attn_cache *c, int Hq, int B, int N, 
  * A row that sees no key, or only keys of score -inf, gets o = 0 and
  * lse = -inf and adds no weight. What it does not see never reaches a row:
  * not stale slots after the end, nor infinities or NaNs in masked drafts.
- * Results do not depend on the order in which thread blocks finish.
+ * (Infinities and NaNs among the values of a key that it does see leave these
+ * elements of its output infinite or NaN.)
+ * Sequences may share pages (a common prefix) as long as acc_out is NULL: with
+ * running weights a page belongs to one sequence of the call, since a sum has
+ * one decay and one set of rows; the sums of a shared page are not defined.
+ * Otherwise results do not depend on the order in which thread blocks finish.
  *   q [N] rows of Hq * D in the cache's type, 16-byte aligned, q_stride
  *     elements apart (a multiple of 8)
- *   max_draft  an upper bound of the drafts of a sequence, 1 .. 256
+ *   max_draft  an upper bound of the drafts of a sequence, 1 .. 256 (a longer
+ *     prompt takes several calls, chains over the ones before; each reads all
+ *     keys so far)
  *   mask  [N][mask_words] uint32, mask_words * 32 >= max_draft, or NULL
  *   o     [N][Hq][D] in o_dtype (QMV_F32 or the cache's), 16-byte aligned
  *   lse   [N][Hq] fp32
  *   acc_in, acc_out  [pages][Hkv][page] fp32: acc_out NULL: no weights; acc_in
  *     NULL: counts as zeros; both may be the same array. Slots that no
- *     sequence of the call holds are not touched.
+ *     sequence with new tokens holds are not touched: a sequence without any
+ *     takes no step, and its sums do not decay.
  *   ws  at least attn_tree_workspace_bytes(...) bytes, 256-byte aligned, not
  *     shared with a concurrent call. */
 int attn_tree(const qmv_attn_cache *c, const void *q, int64_t q_stride, int Hq,

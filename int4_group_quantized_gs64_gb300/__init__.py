@@ -586,7 +586,8 @@ def attn_tree(cache: AttnCache, q, table, ctx, cu, max_draft: int, mask=None, sc
     q [N][Hq][D] in the cache's type; mask int32 [N][words], bit d of a token's words set when
     it sees draft d of its sequence (None: drafts 0..itself); scale defaults to D ** -0.5;
     o_dtype the cache's (default) or float32. acc / acc_out (fp32 [pages][Hkv][page]):
-    acc_out = decay * acc + this call's attention weights; acc alone is updated in place."""
+    acc_out = decay * acc + this call's attention weights; acc alone is updated in place. With
+    weights, a page belongs to one sequence of the call; without, sequences may share pages."""
     if acc_out is None:
         acc_out = acc
     import torch

@@ -4,8 +4,8 @@
 // `sink`, the last `recent`, and of those between the ones with the largest
 // sums, equal sums keeping the lower slot (a NaN sum counts as the lowest, -0
 // as +0). The kept tokens keep their order and are copied, with their sums,
-// to fresh pages: source pages may be shared with other sequences, and a
-// token keeps the rotation of its own position, so its slot may change.
+// to fresh pages: the source stays as it is (other sequences may read its pages),
+// and a token keeps the rotation of its own position, so its slot may change.
 //
 // k_evict_select finds the smallest kept sum of a (sequence, head) by radix
 // selection on order-preserving 32-bit keys (11, 11 and 10 bits, a histogram

@@ -949,3 +949,37 @@ def test_tree_infinite_values_of_drafts_that_are_seen(T, G, D, ctx, out, dt):
     assert torch.isfinite(lse).all()
     assert torch.all(o[..., 0::2] == math.inf) and torch.all(o[..., 1] == -math.inf)
     assert torch.isfinite(o[..., 3::2]).all()
+
+
+@pytest.mark.parametrize("T,G", [(1, 4), (6, 8)])
+def test_tree_pages_that_sequences_share(T, G):
+    """Without running weights sequences may share the pages of a common prefix."""
+    c = Case([200, 170, 300], [T] * 3, 2, G, 64, 32, BF, seed=21, qscale=2.0)
+    o0, l0 = run_tree(c)
+    table, k, v = c.table.clone(), c.k.clone(), c.v.clone()
+    for b in (1, 2):        # the first 160 tokens are sequence 0's
+        for i in range(5):
+            k[c.table_l[b][i]], v[c.table_l[b][i]] = c.k[c.table_l[0][i]], c.v[c.table_l[0][i]]
+            table[b, i] = c.table_l[0][i]
+    own, shared = c.table, table
+    c.k, c.v = k, v
+    apart = run_tree(c)
+    c.table = shared
+    together = run_tree(c)
+    c.table = own
+    assert torch.equal(apart[0], together[0]) and torch.equal(apart[1], together[1])
+    assert torch.equal(apart[0][:T], o0[:T]) and torch.equal(apart[1][:T], l0[:T])
+
+
+@pytest.mark.parametrize("T,G", [(1, 4), (6, 8), (70, 8)])
+def test_tree_weights_of_sequences_without_new_tokens(T, G):
+    """A sequence that takes no step keeps its sums, without a decay."""
+    c = Case([200, 170, 90], [T, 0, T], 2, G, 64, 32, BF, seed=22, mask=None)
+    out = torch.full(c.acc.shape, 5.0, device="cuda")
+    run_tree(c, acc=c.acc.cuda(), acc_out=out, decay=0.5)
+    ref = c.reference(64 ** -0.5, 0.5, c.acc)
+    t = ref[6]
+    assert torch.all((out.cpu().double() - ref[4])[t].abs() <= ref[5][t])
+    assert torch.all(out.cpu()[~t] == 5.0)
+    for p in c.table_l[1][:6]:
+        assert torch.all(out[p] == 5.0)
