@@ -574,8 +574,10 @@ def attn_rope_append(cache: AttnCache, q, k, v, pos, inv_freq, table, ctx, cu,
 
 def attn_tree_workspace_bytes(cache: AttnCache, Hq: int, B: int, N: int, max_draft: int,
                               max_pages: int, weights: bool = False) -> int:
-    return int(lib().attn_tree_workspace_bytes(cache.desc, Hq, B, N, max_draft, max_pages,
-                                               int(weights)))
+    import torch
+    with torch.cuda.device(cache.device_index):
+        return int(lib().attn_tree_workspace_bytes(cache.desc, Hq, B, N, max_draft, max_pages,
+                                                   int(weights)))
 
 
 def attn_tree(cache: AttnCache, q, table, ctx, cu, max_draft: int, mask=None, scale=None, o=None,

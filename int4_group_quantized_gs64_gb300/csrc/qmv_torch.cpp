@@ -7,6 +7,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -90,6 +91,15 @@ Table table(PyObject *o, int device, const char *name) {
     return Table{x.data_ptr<int32_t>(), (int)x.size(0), (int)x.size(1)};
 }
 
+// The device of a call's cache, which the calls below launch on and ask for
+// its number of SMs: current from here to the end of the call.
+struct Device {
+    int index;
+    c10::cuda::CUDAGuard guard;
+    explicit Device(int i) : index(i), guard((c10::DeviceIndex)i) {}
+    operator int() const { return index; }
+};
+
 int as_int(PyObject *o) {
     const long v = PyLong_AsLong(o);
     if (v == -1 && PyErr_Occurred()) throw Bad();
@@ -172,7 +182,7 @@ PyObject *pair(PyObject *a, PyObject *b) {
 PyObject *rope_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded<16>(n, [&]() -> PyObject * {
         const qmv_attn_cache *c = as_cache(a[0]);
-        const int dev = as_int(a[1]);
+        const Device dev(as_int(a[1]));
         const at::ScalarType kind = kind_of(c);
         if (!THPVariable_Check(a[2])) type_error("q", "a tensor");
         const at::ScalarType in = THPVariable_Unpack(a[2]).scalar_type();
@@ -219,7 +229,7 @@ PyObject *rope_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
 PyObject *tree(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded<18>(n, [&]() -> PyObject * {
         const qmv_attn_cache *c = as_cache(a[0]);
-        const int dev = as_int(a[1]);
+        const Device dev(as_int(a[1]));
         const at::ScalarType kind = kind_of(c);
         const at::Tensor &q = tensor(a[2], kind, dev, "q");
         if (q.dim() != 3) value_error("q", "[N][Hq][D]");
@@ -282,7 +292,7 @@ PyObject *tree(PyObject *, PyObject *const *a, Py_ssize_t n) {
 PyObject *evict(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded<15>(n, [&]() -> PyObject * {
         const qmv_attn_cache *c = as_cache(a[0]), *d = as_cache(a[6]);
-        const int dev = as_int(a[1]);
+        const Device dev(as_int(a[1]));
         const auto *acc = static_cast<const float *>(addr(a[2], at::kFloat, slots(c), dev, "acc"));
         const Table t = table(a[3], dev, "table");
         const auto *lens = static_cast<const int32_t *>(addr(a[4], at::kInt, t.B, dev, "lens"));

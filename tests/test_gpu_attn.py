@@ -983,3 +983,12 @@ def test_tree_weights_of_sequences_without_new_tokens(T, G):
     assert torch.all(out.cpu()[~t] == 5.0)
     for p in c.table_l[1][:6]:
         assert torch.all(out[p] == 5.0)
+
+
+def test_calls_leave_the_current_device():
+    c = Case([30], [1], 1, 2, 64, 16, BF, seed=25, mask=None)
+    before = torch.cuda.current_device()
+    run_tree(c)
+    with pytest.raises(TypeError):
+        q.attn_tree(c.cache, c.q, c.table.cuda(), c.ctx, c.cu, 1)    # refused in the middle of its checks
+    assert torch.cuda.current_device() == before
