@@ -422,8 +422,10 @@ typedef struct {
  *     (a, b) -> mscale * (a cos - b sin, b cos + a sin)
  * on elements (i, i + rot/2) of a head, or (2i, 2i + 1) when interleaved != 0;
  * elements rot .. D - 1 pass unchanged. Queries go to q_out, keys and values
- * to the tokens' slots. Angles are formed in 64 bits (exact for any int32
- * position), the rest in fp32, rounded once to the cache's type. Scaled
+ * to the tokens' slots. Angles are formed in 64 bits and
+ * the fraction of a turn is rounded to fp32 (off by 3 * 2^-53 of the angle, 7e-7
+ * at position 2^31, and 2 pi 2^-25), the rest is fp32, rounded once to the
+ * cache's type. Scaled
  * positions for long contexts are a matter of inv_freq and mscale.
  *   q [N] rows of Hq * D, k and v [N] rows of Hkv * D, q_stride, k_stride and
  *     v_stride elements apart (so they may be parts of one projection's rows);

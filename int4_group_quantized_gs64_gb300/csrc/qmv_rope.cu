@@ -5,8 +5,9 @@
 //     (a, b) -> m * (a cos - b sin, b cos + a sin)
 // with the pair at elements (i, i + rot/2), or (2i, 2i + 1) when interleaved;
 // elements from rot on pass unchanged. The angle is formed in turns in 64
-// bits and only its fraction is rounded to 32: at position 10^6 an fp32 angle
-// would be off by hundredths of a radian, the fraction of a turn by 1e-10.
+// bits (off by 3 x 2^-53 of the angle) and only its fraction is rounded to 32: at
+// position 10^6 an fp32 angle would be off by hundredths of a radian, the turns by
+// 1e-10, their fraction by 3e-8.
 // All arithmetic on the elements is fp32, rounded once to the cache's type.
 //
 // A warp takes one token (or a share of its heads, so that few tokens fill the

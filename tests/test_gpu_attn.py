@@ -992,3 +992,28 @@ def test_calls_leave_the_current_device():
     with pytest.raises(TypeError):
         q.attn_tree(c.cache, c.q, c.table.cuda(), c.ctx, c.cu, 1)    # refused in the middle of its checks
     assert torch.cuda.current_device() == before
+
+
+@pytest.mark.parametrize("rot,inter", [(64, False), (32, True), (6, False)])
+def test_rope_positions_to_the_ends_of_int32(rot, inter):
+    """Negative positions and those near 2^31: the angle's bound grows with the position."""
+    edge = [2 ** 31 - 1, -2 ** 31, 2 ** 31 - 12345, -2 ** 30 - 7, 2 ** 30 + 1, 123456789, -1, -99999, 0, 1]
+    c = Case([0], [len(edge)], 1, 2, 64, 16, FP, seed=26, mask=None).dev()
+    g = torch.Generator().manual_seed(7)
+    qkv = torch.randn(c.N, 4, 64, generator=g)
+    pos = torch.tensor(edge, dtype=torch.int32)
+    inv = torch.tensor([10000.0 ** (-2 * i / rot) for i in range(rot // 2)], dtype=torch.float64)
+    d = qkv.cuda()
+    out = q.attn_rope_append(c.cache, d[:, :2], d[:, 2:3], d[:, 3:], pos.cuda(), inv.cuda(), c.table.cuda(), c.ctx,
+                             c.cu, interleaved=inter)
+    y, bound = rope_reference(qkv[:, :3], pos, inv, rot, inter, 1.0)
+    i, j = (slice(0, rot, 2), slice(1, rot, 2)) if inter else (slice(0, rot // 2), slice(rot // 2, rot))
+    x = qkv[:, :3].double()
+    # 3 roundings of 2^-53 here, and one in the reference's own product
+    more = (x[..., i].abs() + x[..., j].abs()) * torch.outer(pos.double().abs(), inv)[:, None] * 4 * 2.0 ** -53
+    bound[..., i] += more
+    bound[..., j] += more
+    tol = bound + y.abs() * half_step(FP) + 2.0 ** -25
+    assert torch.all((out.double().cpu() - y[:, :2]).abs() <= tol[:, :2])
+    k = torch.stack([c.cache.k[c.table_l[0][s // 16], 0, s % 16] for s in range(c.N)]).double().cpu()
+    assert torch.all((k - y[:, 2]).abs() <= tol[:, 2])
