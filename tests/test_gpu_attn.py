@@ -1017,3 +1017,85 @@ def test_rope_positions_to_the_ends_of_int32(rot, inter):
     assert torch.all((out.double().cpu() - y[:, :2]).abs() <= tol[:, :2])
     k = torch.stack([c.cache.k[c.table_l[0][s // 16], 0, s % 16] for s in range(c.N)]).double().cpu()
     assert torch.all((k - y[:, 2]).abs() <= tol[:, 2])
+
+
+@pytest.mark.parametrize("T,G", [(3, 2), (40, 4)])
+def test_tree_more_drafts_than_the_bound(T, G):
+    """A sequence with more drafts than max_draft is left out; the others are as ever."""
+    c = Case([100, 90, 60], [T - 1, T, T - 1], 2, G, 64, 16, FP, seed=23)
+    full, lse = run_tree(c)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o, l = torch.full_like(full, 9.0), torch.full_like(lse, 9.0)
+    acc = torch.full(c.acc.shape, 5.0, device="cuda")
+    q.attn_tree(c.cache, c.q.cuda(), c.table.cuda(), c.ctx, c.cu, T - 1, mask=c.mask.cuda(), status=st, o=o, lse=l,
+                acc_out=acc)
+    torch.cuda.synchronize()
+    assert int(st) == 2
+    left = slice(T - 1, 2 * T - 1)
+    assert torch.all(o[left] == 9.0) and torch.all(l[left] == 9.0)
+    for p in c.table_l[1][: (90 + T + 15) // 16]:
+        assert torch.all(acc[p] == 5.0)
+    keep = [n for n in range(c.N) if not T - 1 <= n < 2 * T - 1]
+    e, le = full[keep].double(), lse[keep].double()
+    # the same keys in other shares: a few steps of fp32 apart, and each a rounding of the output
+    assert torch.all((o[keep].double() - e).abs() <= e.abs() * 2 * half_step(FP) + 2.0 ** -12)
+    assert torch.all((l[keep].double() - le).abs() <= 2.0 ** -18 * (1 + le.abs()))
+
+
+# ------------------------------------------------------------------ eviction of many long lists
+
+@pytest.mark.parametrize("kind", ["spread", "ties", "equal"])
+def test_evict_more_lists_than_sms_longer_than_a_block_keeps(kind):
+    """160 lists of up to 45,000 sums: a block a list, whose last slots are read again from memory."""
+    B, Hkv, D, page, n = 20, 8, 64, 64, 45000
+    lens = [n - 137 * b for b in range(B)]
+    budget, sink, recent = 4100, 5, 333
+    g = torch.Generator(device="cuda").manual_seed(3)
+    need = [-(-x // page) for x in lens]
+    table = torch.zeros(B, max(need), dtype=torch.int32)
+    order = torch.randperm(sum(need), generator=torch.Generator().manual_seed(1)).int()
+    at = np.concatenate([[0], np.cumsum(need)])
+    for b in range(B):
+        table[b, :need[b]] = order[at[b]:at[b + 1]]
+    src = q.AttnCache.empty(sum(need), Hkv, page, D)
+    src.k.view(torch.int16).random_(generator=g)
+    src.v.view(torch.int16).random_(generator=g)
+    acc = torch.empty(sum(need), Hkv, page, device="cuda")
+    if kind == "spread":
+        acc.normal_(0.0, 2.0, generator=g).exp_()
+    elif kind == "ties":
+        acc.random_(0, 7, generator=g)
+    else:
+        acc.fill_(0.25)
+    dp = -(-budget // page)
+    dst, dacc = q.AttnCache.empty(B * dp, Hkv, page, D), torch.full((B * dp, Hkv, page), 9.0, device="cuda")
+    dt = torch.arange(B * dp, dtype=torch.int32, device="cuda").view(B, dp)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    keep, new = q.attn_evict(src, acc, table.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"), budget,
+                             dst, dacc, dt, sink=sink, recent=recent, status=st)
+    torch.cuda.synchronize()
+    assert int(st) == 0 and new.tolist() == [budget] * B
+    i = torch.arange(budget, device="cuda")
+    for b in range(B):
+        rows, m = table[b, :need[b]].long().cuda(), lens[b]
+        a = acc[rows].transpose(0, 1).reshape(Hkv, -1)[:, :m]
+        mid = a[:, sink:m - recent].sort(dim=-1, descending=True, stable=True).indices[:, :budget - sink - recent] + sink
+        fixed = torch.cat([torch.arange(sink, device="cuda"), torch.arange(m - recent, m, device="cuda")])
+        want = torch.cat([mid, fixed.expand(Hkv, -1)], 1).sort(-1).values
+        assert torch.equal(keep[b].long(), want), b
+        h = torch.arange(Hkv, device="cuda")[:, None]
+        pg, to = rows[want // page], dt[b].long()[i // page].expand(Hkv, -1)
+        for x, y in ((src.k, dst.k), (src.v, dst.v)):
+            assert torch.equal(x[pg, h, want % page].view(torch.int16), y[to, h, i % page].view(torch.int16)), b
+        assert torch.equal(acc[pg, h, want % page], dacc[to, h, i % page]), b
+
+
+# ------------------------------------------------------------------ batches of more than 32 sequences
+
+@pytest.mark.parametrize("D,dtype,drafts,G", [(128, BF, [1], 4), (64, FP, [1, 0, 2], 5), (128, FP, [1, 3, 0, 2], 4),
+                                              (64, BF, [30, 7, 0, 1], 5), (128, BF, [40, 1], 8)])
+@pytest.mark.parametrize("B", [33, 300])
+def test_tree_batches_of_many_sequences(D, dtype, drafts, G, B):
+    """Shares counted by the whole block, several sequences a thread, some without tokens."""
+    check_batch([(b * 71) % 640 for b in range(B)], [drafts[b % len(drafts)] for b in range(B)], 2, G, D, 32, dtype,
+                runs=2)
