@@ -30,7 +30,7 @@ struct TreeArgs {
     float *part_o;
     float *part_ml;  // [grid][2][rows][2]
     int grid, rows, unit;
-    const uint16_t *kpool, *vpool;
+    const uint16_t *vpool;
     const float *acc_in;
     float *acc_out;
     float decay;

@@ -722,7 +722,6 @@ cudaError_t launch_attn_tree(const AttnCache &c, const TreeCall &t, cudaStream_t
     a.qxor = t.scale < 0.f ? 0x80008000u : 0u;
     a.qand = t.scale == 0.f ? 0u : 0xFFFFFFFFu;
     a.o = t.o; a.o_f32 = t.o_f32; a.lse = t.lse;
-    a.kpool = static_cast<const uint16_t *>(c.k);
     a.vpool = static_cast<const uint16_t *>(c.v);
     a.acc_in = t.acc_in; a.acc_out = t.acc_out; a.decay = t.decay;
     a.status = t.status;
