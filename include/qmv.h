@@ -443,7 +443,8 @@ int attn_rope_append(const qmv_attn_cache *c, const void *q, int64_t q_stride, c
                      qmv_stream_t stream);
 
 /* Workspace of attn_tree, in bytes (0 for unsupported sizes). weights != 0:
- * with acc_out. */
+ * with acc_out, which with up to 16 rows a key/value head keeps a score for each
+ * of them and every slot of the table, up to 1 GiB. */
 size_t attn_tree_workspace_bytes(const qmv_attn_cache *c, int Hq, int B, int N, int max_draft,
                                  int max_pages, int weights);
 

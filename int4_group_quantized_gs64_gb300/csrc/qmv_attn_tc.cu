@@ -16,21 +16,26 @@
 // Warps: 0-3 and 4-7 the streams' softmax (a thread a row: maximum and sum
 // need no exchange), 8 and 11 the copies of keys and of values, 9 and 10 the
 // streams' products. These four need few registers and pass the rest on to the
-// softmax warps, whose 128 scores stay in registers: reading them from tensor
-// memory twice would cost as much as the products. A ring of 128-key tiles holds
-// keys and another one values, across segments; a copying warp comes to every slot
-// of its ring in turn, and so never waits for a phase that is not the next. (In one
-// ring for both it would know of its own entries only, and those that other slots
-// imply are the other stream's: a wait two phases behind passes at once.) The
-// running maximum moves only when it grows by more than 2^8 (a
-// row's weights may then exceed 1, which fp32 sums and 16-bit weights hold),
+// softmax warps, whose 128 scores stay in registers (reading them from tensor
+// memory twice would cost as much as the products). That is more than 216
+// registers hold with everything else: 16-bit outputs spill some 50 bytes a thread
+// with more than 128 rows and some 200 with up to 128. For fp32 outputs, whose O
+// takes 128 registers at 128 elements, the scores are read 32 at a time twice, and
+// 550 bytes are spilled with more than 128 rows, 1.2 to 1.4 KB with up to 128.
+//
+// A ring of 128-key tiles holds keys and another one values, across segments; a
+// copying warp comes to every slot of its ring in turn, and so never waits for a
+// phase that is not the next. (In one ring for both it would know of its own entries
+// only, and those that other slots imply are the other stream's: a wait two phases
+// behind passes at once.) The running maximum moves only when it grows by more than
+// 2^8 (a row's weights may then exceed 1, which fp32 sums and 16-bit weights hold),
 // since moving it means rescaling O in tensor memory.
 //
 // What bounds it: a stream's chain of scores, exponentials, weights and product,
 // 3,380 cycles for a 128-key tile and 256 rows of 128 elements (the products alone
 // are 2,048), and some 15,000 cycles at the start and end of a block's parts.
 // 8 trees of 64 nodes, 8 query heads a head, up to 8200 keys: 114 us with the
-// join (830 TFLOP/s); 64 sequences of 8191 keys, 32 rows: 248 us, the rate of a copy.
+// join (830 TFLOP/s); 64 sequences of 8191 keys, 32 rows: 244 us, the rate of a copy.
 //
 // Weights are rounded once to 16 bits for a 16-bit output (half a step of the
 // type, like the output's own rounding, and averaged over the keys). For an
@@ -39,7 +44,7 @@
 // in registers, tile by tile: a product's own sums cut off what falls below
 // their last bit, which over 8191 keys came to 1.1e-5 of the norm. fp16 weights
 // are held 2^7 times larger: the small ones would lose bits below fp16's range.
-// (256 rows over 16 x 8191 keys: 113 us with a 16-bit output, 211 and 273 with an
+// (256 rows over 16 x 8191 keys: 111 us with a 16-bit output, 205 and 285 with an
 // fp32 one from fp16 and bf16.)
 #include <string.h>
 
@@ -128,8 +133,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem[];
     // Tensor memory columns. Where they suffice (64 elements, one 16-bit number a
     // weight) P lies apart from S, and a stream's next S is formed while its
-    // exponentials run (16 sequences of 8191 keys, 320 rows: 122 us, 150 with P
-    // over S; 64 sequences, 128 rows: 168 and 182). Otherwise P overwrites S.
+    // exponentials run (16 sequences of 8191 keys, 320 rows: 124 us, 150 with P
+    // over S; 64 sequences, 128 rows: 165 and 182). Otherwise P overwrites S.
     constexpr bool kApart = D == 64 && !kSplit;
     // The third number of a bf16 weight lies in columns that O leaves: with 128
     // elements O comes in two halves, one after the other.
@@ -138,7 +143,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t kIdescO = tc05::idesc_f16kind_f32(kBf16, 128, kOcols, true);
     constexpr int kPcol = kApart ? 256 : 0, kPstep = kApart ? 64 : 128;   // P of stream s at kPcol + s * kPstep
     constexpr int kOcol = kApart ? 384 : 256, kOstep = kApart ? 64 : 128;
-    const int kstages = stages / 2, vstages = stages - kstages;  // slots for keys, then those for values
+    // Slots for keys, then those for values: half of them each. (Of five, three for
+    // keys or three for values measured the same.)
+    const int kstages = stages / 2, vstages = stages - kstages;
     uint8_t *qs = smem, *ring = smem + (kTwo ? 2 : 1) * kTile;
     Misc *m = reinterpret_cast<Misc *>(ring + stages * kTile);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

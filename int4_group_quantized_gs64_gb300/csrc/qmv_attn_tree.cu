@@ -44,9 +44,9 @@ __device__ __forceinline__ uint32_t slice_ofs(int r, int c) {
 // copies and keeps its own maximum, sum and output accumulators, so the warps
 // meet only at a segment's end. What bounds it is the stream of keys and
 // values: 16 rows need 4 x 16 multiply-adds per loaded value, far below the
-// warp MMA's rate. 64 sequences of up to 8191 keys, 4 rows, take 246 us (6.3
-// TB/s), one of 200,003 keys, 6 rows, 133 (6.2 TB/s), one of 777 10.9, joins
-// included. (32 rows a warp measured 452 us where the tcgen05 kernel takes 248,
+// warp MMA's rate. 64 sequences of up to 8191 keys, 4 rows, take 247 us (6.3
+// TB/s), one of 200,003 keys, 6 rows, 133 (6.2 TB/s), one of 777 10.6, joins
+// included. (32 rows a warp measured 452 us where the tcgen05 kernel takes 244,
 // 64 sequences of 8191 keys: registers leave one block an SM.)
 //
 // The exponentials go to the second product as two 16-bit numbers each (the
@@ -639,9 +639,10 @@ cudaError_t run_tree(const AttnCache &c, const TreeArgs &a, int max_rows, cudaSt
 }
 
 // Rows an item: up to 16 on the warp MMA, more on tcgen05 (qmv_attn_tc.cu).
-// With 16 rows the two measured 259 and 245 us (64 sequences of 8191 keys) and
-// 13.2 and 14.4 us (one of 777), with 32 rows 452 and 248. Above 128 rows two
-// tiles share the keys: 192 rows over 16 x 8191 keys 109 us, in blocks of 128 150.
+// With 16 rows the two measured 250 and 240 us (64 sequences of 8191 keys), 124
+// and 156 with 64 elements a head, and 12.3 and 15.4 us (one of 777 keys); with 32
+// rows 452 and 244. Above 128 rows two tiles share the keys: 192 rows over 16 x
+// 8191 keys 106 us, in blocks of 128 150.
 int tree_rows(int max_rows) { return max_rows <= kRows ? kRows : max_rows <= 128 ? 128 : 256; }
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     static std::once_flag once;
