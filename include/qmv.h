@@ -442,6 +442,23 @@ int attn_rope_append(const qmv_attn_cache *c, const void *q, int64_t q_stride, c
                      const int32_t *cu, int B, int N, void *q_out, float *acc, int32_t *status,
                      qmv_stream_t stream);
 
+/* attn_rope_append with norms: every query and key head x first becomes
+ *     x_i * w_i / sqrt(mean(x^2) + eps)
+ * (the mean over its D elements, all of them, also where rot < D), then is turned
+ * and goes to q_out or the cache as above; values pass unchanged. In fp32 from the
+ * inputs to the one rounding at the end. A head of zeros stays zeros, also with
+ * eps = 0; one whose squares add up to more than fp32 holds becomes zeros.
+ *   q_weight, k_weight [D] in w_dtype (QMV_F32 or the cache's), aligned to it, or
+ *     NULL: ones; 16-byte aligned ones keep the vector path
+ *   eps finite, >= 0; everything else as attn_rope_append. */
+int attn_norm_rope_append(const qmv_attn_cache *c, const void *q, int64_t q_stride, const void *k,
+                          int64_t k_stride, const void *v, int64_t v_stride, int in_dtype, int Hq,
+                          const void *q_weight, const void *k_weight, int w_dtype, float eps,
+                          const int32_t *pos, const double *inv_freq, int rot, int interleaved,
+                          float mscale, const int32_t *table, int max_pages, const int32_t *ctx,
+                          const int32_t *cu, int B, int N, void *q_out, float *acc,
+                          int32_t *status, qmv_stream_t stream);
+
 /* Workspace of attn_tree, in bytes (0 for unsupported sizes). weights != 0:
  * with acc_out, which with up to 16 rows a key/value head keeps a score for each
  * of them and every slot of the table, up to 1 GiB. */

@@ -10,8 +10,8 @@ Functions carry the C names: ``qmv_int4_gs``, ``qmv_int8_row``, their bf16-outpu
 forms ``qmv_int4_gs_bf16`` and ``qmv_int8_row_bf16``,
 ``moe_route_topk``, ``moe_group``, ``moe_gate_up_silu``, ``moe_down``,
 ``moe_combine``, ``moe_workspace_bytes``, ``moe_expert_ffn_int4`` and
-``moe_expert_ffn_int4_prefill``; ``attn_rope_append``, ``attn_tree`` and
-``attn_evict`` over a paged cache (``AttnCache``).
+``moe_expert_ffn_int4_prefill``; ``attn_rope_append``, ``attn_norm_rope_append``,
+``attn_tree`` and ``attn_evict`` over a paged cache (``AttnCache``).
 """
 from __future__ import annotations
 
@@ -97,6 +97,9 @@ def lib():
             "moe_expert_ffn_int4_prefill": ([P, vp, i32, vp, vp, i32, vp, vp, sz, vp], i32),
             "attn_rope_append": ([C, vp, i64, vp, i64, vp, i64, i32, i32, vp, vp, i32, i32, f32, vp,
                                   i32, vp, vp, i32, i32, vp, vp, vp, vp], i32),
+            "attn_norm_rope_append": ([C, vp, i64, vp, i64, vp, i64, i32, i32, vp, vp, i32, f32, vp,
+                                       vp, i32, i32, f32, vp, i32, vp, vp, i32, i32, vp, vp, vp,
+                                       vp], i32),
             "attn_tree_workspace_bytes": ([C, i32, i32, i32, i32, i32, i32], sz),
             "attn_tree": ([C, vp, i64, i32, vp, i32, vp, vp, i32, i32, i32, vp, i32, f32, vp, i32,
                            vp, vp, vp, f32, vp, vp, sz, vp], i32),
@@ -513,7 +516,7 @@ def _torch_binding():
         loader.exec_module(mod)
         L = lib()
         mod.init(QmvError, *(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
-            "attn_rope_append", "attn_tree", "attn_tree_workspace_bytes", "attn_evict")))
+            "attn_rope_append", "attn_norm_rope_append", "attn_tree", "attn_tree_workspace_bytes", "attn_evict")))
         _torch_mod = mod
     return _torch_mod
 
@@ -570,6 +573,23 @@ def attn_rope_append(cache: AttnCache, q, k, v, pos, inv_freq, table, ctx, cu,
     return (_torch_mod or _torch_binding()).rope_append(
         cache.address, cache.device_index, q, k, v, pos, inv_freq, table, ctx, cu, interleaved,
         mscale, q_out, acc, status, handle)
+
+
+def attn_norm_rope_append(cache: AttnCache, q, k, v, q_weight, k_weight, pos, inv_freq, table, ctx,
+                          cu, eps: float = 1e-6, interleaved: bool = False, mscale: float = 1.0,
+                          q_out=None, acc=None, status=None, stream=None):
+    """attn_rope_append with norms: every query and key head x becomes
+    x * weight / sqrt(mean(x ** 2) + eps) before it is turned; returns the queries.
+
+    q_weight and k_weight [D], both fp32 or both of the cache's type, or None (ones)."""
+    handle = None
+    if stream is not None:
+        handle = stream.cuda_stream
+        if q_out is None:
+            q_out = _on(stream, q.shape, cache.dtype, cache.device)
+    return (_torch_mod or _torch_binding()).norm_rope_append(
+        cache.address, cache.device_index, q, k, v, q_weight, k_weight, eps, pos, inv_freq, table,
+        ctx, cu, interleaved, mscale, q_out, acc, status, handle)
 
 
 def attn_tree_workspace_bytes(cache: AttnCache, Hq: int, B: int, N: int, max_draft: int,

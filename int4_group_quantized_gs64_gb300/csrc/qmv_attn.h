@@ -24,12 +24,20 @@ struct RopeIn {
     long long stride;  // elements between tokens
 };
 
+// Norms of query and key heads before the turn.
+struct RopeNorm {
+    const void *qw, *kw;  // [D], or null: ones
+    int w_f32;            // else of the cache's type
+    float eps;
+};
+
 // in_type: 0 fp32, else the cache's type. acc (optional): cleared for the new tokens.
+// norm (optional): query and key heads are normed first.
 cudaError_t launch_rope_append(const AttnCache &c, const AttnSeqs &s, const RopeIn &q,
                                const RopeIn &k, const RopeIn &v, int in_f32, int Hq,
                                const int32_t *pos, const double *inv_freq, int rot,
                                bool interleaved, float mscale, void *q_out, float *acc,
-                               int32_t *status, cudaStream_t st);
+                               int32_t *status, cudaStream_t st, const RopeNorm *norm = nullptr);
 
 struct TreeCall {
     AttnSeqs s;

@@ -42,22 +42,21 @@ bool heads_ok(const qmv_attn_cache *c, int Hq) {
     return Hq >= 1 && Hq <= kMaxHeads && Hq % c->Hkv == 0;
 }
 
-}  // namespace
-
-extern "C" {
-
-int attn_rope_append(const qmv_attn_cache *c, const void *q, int64_t q_stride, const void *k,
-                     int64_t k_stride, const void *v, int64_t v_stride, int in_dtype, int Hq,
-                     const int32_t *pos, const double *inv_freq, int rot, int interleaved,
-                     float mscale, const int32_t *table, int max_pages, const int32_t *ctx,
-                     const int32_t *cu, int B, int N, void *q_out, float *acc, int32_t *status,
-                     qmv_stream_t stream) {
+// Both rotary appends; norm null: without norms.
+int rope_append(const qmv_attn_cache *c, const void *q, int64_t q_stride, const void *k,
+                int64_t k_stride, const void *v, int64_t v_stride, int in_dtype, int Hq,
+                const qmv::RopeNorm *norm, int w_dtype, const int32_t *pos, const double *inv_freq,
+                int rot, int interleaved, float mscale, const int32_t *table, int max_pages,
+                const int32_t *ctx, const int32_t *cu, int B, int N, void *q_out, float *acc,
+                int32_t *status, qmv_stream_t stream) {
     int r = check_cache(c);
     if (r) return r;
     if ((r = check_batch(c, B, max_pages))) return r;
     if (N < 0 || !heads_ok(c, Hq) || rot < 2 || rot > c->D || rot % 2 || !isfinite(mscale))
         return QMV_EINVAL;
     if (in_dtype != QMV_F32 && in_dtype != c->dtype) return QMV_EINVAL;
+    if (norm && ((w_dtype != QMV_F32 && w_dtype != c->dtype) || !isfinite(norm->eps) || norm->eps < 0.f))
+        return QMV_EINVAL;
     if (N > 1 << 22) return QMV_ESHAPE;
     if (q_stride < (int64_t)Hq * c->D || k_stride < (int64_t)c->Hkv * c->D ||
         v_stride < (int64_t)c->Hkv * c->D)
@@ -69,10 +68,40 @@ int attn_rope_append(const qmv_attn_cache *c, const void *q, int64_t q_stride, c
         !aligned(inv_freq, 8) || !aligned(table, 4) || !aligned(ctx, 4) || !aligned(cu, 4) ||
         !aligned(q_out, 16) || !aligned(acc, 4) || !aligned(status, 4))
         return QMV_EALIGN;
+    const uintptr_t we = norm && norm->w_f32 ? 4 : 2;
+    if (norm && (!aligned(norm->qw, we) || !aligned(norm->kw, we))) return QMV_EALIGN;
     return from_cuda(qmv::launch_rope_append(
         cache(c), qmv::AttnSeqs{table, ctx, cu, B, N, 0, max_pages}, qmv::RopeIn{q, q_stride},
         qmv::RopeIn{k, k_stride}, qmv::RopeIn{v, v_stride}, in_dtype == QMV_F32, Hq, pos, inv_freq,
-        rot, interleaved != 0, mscale, q_out, acc, status, cs(stream)));
+        rot, interleaved != 0, mscale, q_out, acc, status, cs(stream), norm));
+}
+
+}  // namespace
+
+extern "C" {
+
+int attn_rope_append(const qmv_attn_cache *c, const void *q, int64_t q_stride, const void *k,
+                     int64_t k_stride, const void *v, int64_t v_stride, int in_dtype, int Hq,
+                     const int32_t *pos, const double *inv_freq, int rot, int interleaved,
+                     float mscale, const int32_t *table, int max_pages, const int32_t *ctx,
+                     const int32_t *cu, int B, int N, void *q_out, float *acc, int32_t *status,
+                     qmv_stream_t stream) {
+    return rope_append(c, q, q_stride, k, k_stride, v, v_stride, in_dtype, Hq, nullptr, QMV_F32, pos,
+                       inv_freq, rot, interleaved, mscale, table, max_pages, ctx, cu, B, N, q_out,
+                       acc, status, stream);
+}
+
+int attn_norm_rope_append(const qmv_attn_cache *c, const void *q, int64_t q_stride, const void *k,
+                          int64_t k_stride, const void *v, int64_t v_stride, int in_dtype, int Hq,
+                          const void *q_weight, const void *k_weight, int w_dtype, float eps,
+                          const int32_t *pos, const double *inv_freq, int rot, int interleaved,
+                          float mscale, const int32_t *table, int max_pages, const int32_t *ctx,
+                          const int32_t *cu, int B, int N, void *q_out, float *acc,
+                          int32_t *status, qmv_stream_t stream) {
+    const qmv::RopeNorm norm{q_weight, k_weight, w_dtype == QMV_F32, eps};
+    return rope_append(c, q, q_stride, k, k_stride, v, v_stride, in_dtype, Hq, &norm, w_dtype, pos,
+                       inv_freq, rot, interleaved, mscale, table, max_pages, ctx, cu, B, N, q_out,
+                       acc, status, stream);
 }
 
 size_t attn_tree_workspace_bytes(const qmv_attn_cache *c, int Hq, int B, int N, int max_draft,

@@ -10,6 +10,12 @@
 // 1e-10, their fraction by 3e-8.
 // All arithmetic on the elements is fp32, rounded once to the cache's type.
 //
+// With norms (kNorm) a query or key head x first becomes x * w / sqrt(mean(x^2) +
+// eps), the mean over its D elements, w a weight an element: the lanes that share
+// the head add up their squares and exchange them (three shuffles at 128 elements),
+// and the result goes on to the turn in fp32. The head is in registers either way,
+// so the norm costs no traffic.
+//
 // A warp takes one token (or a share of its heads, so that few tokens fill the
 // GPU too). D / 16 lanes share a head, 16 elements each: a lane has the same
 // place in every head that it meets, and so the same eight angles, which stay
@@ -37,6 +43,9 @@ struct RopeArgs {
     float *acc;
     int32_t *status;
     int parts;  // blocks a token
+    const void *qw, *kw;  // norms' weights [D], null: ones
+    int w_f32;            // they are fp32, else of the cache's type
+    float eps;
 };
 
 constexpr int kWarps = 4;  // a block
@@ -85,6 +94,40 @@ template <bool kBf16, bool kF32>
 __device__ __forceinline__ float load1(const void *p, long long at) {
     return kF32 ? static_cast<const float *>(p)[at]
                 : to_f32<kBf16>(static_cast<const uint16_t *>(p)[at]);
+}
+
+// The factor that makes a head's mean square (its sum / D, plus eps) one. A head
+// of zeros stays zeros.
+__device__ __forceinline__ float norm_of(float sum, int D, float eps) {
+    const float m = fmaf(sum, 1.f / (float)D, eps);
+    return m == 0.f ? 0.f : rsqrtf(m);
+}
+template <bool kBf16>
+__device__ __forceinline__ float weight1(const RopeArgs &a, const void *w, int i) {
+    if (!w) return 1.f;
+    return a.w_f32 ? static_cast<const float *>(w)[i] : to_f32<kBf16>(static_cast<const uint16_t *>(w)[i]);
+}
+// Eight weights from element i on, on a 16-byte boundary.
+template <bool kBf16>
+__device__ __forceinline__ void weights8(const RopeArgs &a, const void *w, int i, float (&x)[8]) {
+    if (!w) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = 1.f;
+    } else if (a.w_f32) {
+        const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(w) + i);
+        const float4 u = __ldg(p), v = __ldg(p + 1);
+        x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+        x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+    } else {
+        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(w) + i));
+        const uint32_t r[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 f = unpack2<kBf16>(r[e]);
+            x[2 * e] = f.x;
+            x[2 * e + 1] = f.y;
+        }
+    }
 }
 
 // cos and sin of the angle of pair i at position pos, times mscale.
@@ -164,7 +207,7 @@ __device__ __forceinline__ void clear_sums(const RopeArgs &a, int lane, int pid,
 }
 
 // Rows and strides on 16-byte boundaries, rot a multiple of 16.
-template <int D, bool kBf16, bool kF32, bool kInter>
+template <int D, bool kBf16, bool kF32, bool kInter, bool kNorm>
 __global__ void __launch_bounds__(32 * kWarps) k_rope_append(const RopeArgs a) {
     constexpr int kPerHead = D / 16, kHeads = 32 / kPerHead;  // lanes a head, heads a pass
     constexpr int kAngles = 8 / kHeads, kAhead = kF32 ? 2 : 4;
@@ -198,6 +241,11 @@ __global__ void __launch_bounds__(32 * kWarps) k_rope_append(const RopeArgs a) {
             cs[j].y = __shfl_sync(0xFFFFFFFFu, mine[j % kAngles].y, from);
         }
     }
+    float w0[8], w1[8];  // queries' weights (the few key heads load theirs when they come)
+    if (kNorm) {
+        weights8<kBf16>(a, a.qw, lo, w0);
+        weights8<kBf16>(a, a.qw, hi, w1);
+    }
     for (int h0 = hb; h0 < he; h0 += kHeads * kAhead) {
         Vec8<kBf16, kF32> r[kAhead][2];
 #pragma unroll
@@ -212,11 +260,36 @@ __global__ void __launch_bounds__(32 * kWarps) k_rope_append(const RopeArgs a) {
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
             const int hd = h0 + j * kHeads + g;
-            if (hd >= he) continue;
-            const Head s = head_of(a, n, hd, good, pid, row);
+            if (!kNorm && hd >= he) continue;
             float x0[8], x1[8];
             r[j][0].unpack(x0);
             r[j][1].unpack(x1);
+            if (kNorm) {  // (the whole warp: lanes past the last head take part)
+                float sum = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum = fmaf(x0[e], x0[e], fmaf(x1[e], x1[e], sum));
+#pragma unroll
+                for (int o = kPerHead / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+                if (hd >= he) continue;
+                const float f = norm_of(sum, D, a.eps);
+                if (hd < a.Hq) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        x0[e] *= f * w0[e];
+                        x1[e] *= f * w1[e];
+                    }
+                } else if (hd < a.Hq + a.Hkv) {
+                    float k0[8], k1[8];
+                    weights8<kBf16>(a, a.kw, lo, k0);
+                    weights8<kBf16>(a, a.kw, hi, k1);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        x0[e] *= f * k0[e];
+                        x1[e] *= f * k1[e];
+                    }
+                }
+            }
+            const Head s = head_of(a, n, hd, good, pid, row);
             if (s.turn && place_turns) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
@@ -238,7 +311,7 @@ __global__ void __launch_bounds__(32 * kWarps) k_rope_append(const RopeArgs a) {
 
 // Any alignment and any even rot: a lane takes a pair (or two elements past
 // rot) at a time.
-template <bool kBf16, bool kF32, bool kInter>
+template <bool kBf16, bool kF32, bool kInter, bool kNorm>
 __global__ void __launch_bounds__(32 * kWarps) k_rope_any(const RopeArgs a) {
     __shared__ float2 table[kWarps][64];
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -258,10 +331,26 @@ __global__ void __launch_bounds__(32 * kWarps) k_rope_any(const RopeArgs a) {
     __syncwarp();
     for (int hd = hb; hd < he; ++hd) {
         const Head s = head_of(a, n, hd, good, pid, row);
+        const void *w = hd < a.Hq ? a.qw : a.kw;
+        float f = 1.f;
+        if (kNorm && s.turn) {
+            float sum = 0.f;
+            for (int i = lane; i < a.D; i += 32) {
+                const float x = load1<kBf16, kF32>(s.src, s.at + i);
+                sum = fmaf(x, x, sum);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+            f = norm_of(sum, a.D, a.eps);
+        }
         for (int i = lane; i < a.D / 2; i += 32) {
             const bool t = i < half;
             const int lo = kInter || !t ? 2 * i : i, hi = kInter || !t ? 2 * i + 1 : half + i;
             float u = load1<kBf16, kF32>(s.src, s.at + lo), v = load1<kBf16, kF32>(s.src, s.at + hi);
+            if (kNorm && s.turn) {
+                u *= f * weight1<kBf16>(a, w, lo);
+                v *= f * weight1<kBf16>(a, w, hi);
+            }
             if (s.turn && t) {
                 const float x = u;
                 u = x * cs[i].x - v * cs[i].y;
@@ -276,13 +365,22 @@ __global__ void __launch_bounds__(32 * kWarps) k_rope_any(const RopeArgs a) {
     if (w == 0) check_lengths(a, lane);
 }
 
-template <bool kBf16, bool kF32, bool kInter>
+template <bool kBf16, bool kF32, bool kInter, bool kNorm>
 cudaError_t run(const RopeArgs &a, bool vec, cudaStream_t st) {
     const dim3 grid((unsigned)(((long long)a.s.N * a.parts + kWarps - 1) / kWarps)), block(32 * kWarps);
-    return launch(!vec        ? k_rope_any<kBf16, kF32, kInter>
-                  : a.D == 64 ? k_rope_append<64, kBf16, kF32, kInter>
-                              : k_rope_append<128, kBf16, kF32, kInter>,
+    return launch(!vec        ? k_rope_any<kBf16, kF32, kInter, kNorm>
+                  : a.D == 64 ? k_rope_append<64, kBf16, kF32, kInter, kNorm>
+                              : k_rope_append<128, kBf16, kF32, kInter, kNorm>,
                   grid, block, 0, st, true, a);
+}
+
+template <bool kNorm>
+cudaError_t run(const RopeArgs &a, bool bf16, bool f32, bool inter, bool vec, cudaStream_t st) {
+    if (inter)
+        return bf16 ? (f32 ? run<true, true, true, kNorm>(a, vec, st) : run<true, false, true, kNorm>(a, vec, st))
+                    : (f32 ? run<false, true, true, kNorm>(a, vec, st) : run<false, false, true, kNorm>(a, vec, st));
+    return bf16 ? (f32 ? run<true, true, false, kNorm>(a, vec, st) : run<true, false, false, kNorm>(a, vec, st))
+                : (f32 ? run<false, true, false, kNorm>(a, vec, st) : run<false, false, false, kNorm>(a, vec, st));
 }
 
 }  // namespace
@@ -292,7 +390,7 @@ cudaError_t launch_rope_append(const AttnCache &c, const AttnSeqs &s, const Rope
                                const RopeIn &k, const RopeIn &v, int in_f32, int Hq,
                                const int32_t *pos, const double *inv_freq, int rot,
                                bool interleaved, float mscale, void *q_out, float *acc,
-                               int32_t *status, cudaStream_t st) {
+                               int32_t *status, cudaStream_t st, const RopeNorm *norm) {
     using namespace attn;
     int lpage = 0;
     while ((1 << lpage) < c.page) ++lpage;
@@ -306,21 +404,23 @@ cudaError_t launch_rope_append(const AttnCache &c, const AttnSeqs &s, const Rope
     a.kc = static_cast<uint16_t *>(c.k);
     a.vc = static_cast<uint16_t *>(c.v);
     a.acc = acc; a.status = status;
+    a.qw = norm ? norm->qw : nullptr;
+    a.kw = norm ? norm->kw : nullptr;
+    a.w_f32 = norm ? norm->w_f32 : 0;
+    a.eps = norm ? norm->eps : 0.f;
     const int esize = in_f32 ? 4 : 2;
     auto vec = [&](const RopeIn &r) {
         return reinterpret_cast<uintptr_t>(r.p) % 16 == 0 && r.stride * esize % 16 == 0;
     };
-    const bool v8 = vec(q) && vec(k) && vec(v) && rot % 16 == 0;
+    const bool v8 = vec(q) && vec(k) && vec(v) && rot % 16 == 0 &&
+                    reinterpret_cast<uintptr_t>(a.qw) % 16 == 0 && reinterpret_cast<uintptr_t>(a.kw) % 16 == 0;
     // Warps a token: enough to give every SM some when tokens are few, each with
     // at least one pass over heads.
     const int heads = Hq + 2 * c.Hkv, pass = v8 ? 32 / (c.D / 16) : 1;
     const int most = (heads + pass - 1) / pass, want = (sm_count() * kFill + s.N - 1) / s.N;
     a.parts = want < most ? want : most;
-    if (interleaved)
-        return c.bf16 ? (in_f32 ? run<true, true, true>(a, v8, st) : run<true, false, true>(a, v8, st))
-                      : (in_f32 ? run<false, true, true>(a, v8, st) : run<false, false, true>(a, v8, st));
-    return c.bf16 ? (in_f32 ? run<true, true, false>(a, v8, st) : run<true, false, false>(a, v8, st))
-                  : (in_f32 ? run<false, true, false>(a, v8, st) : run<false, false, false>(a, v8, st));
+    return norm ? run<true>(a, c.bf16, in_f32, interleaved, v8, st)
+                : run<false>(a, c.bf16, in_f32, interleaved, v8, st);
 }
 
 }  // namespace qmv

@@ -12,12 +12,14 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <exception>
+#include <type_traits>
 
 #include "../../include/qmv.h"
 
 namespace {
 
 decltype(&attn_rope_append) g_rope;
+decltype(&attn_norm_rope_append) g_norm_rope;
 decltype(&attn_tree) g_tree;
 decltype(&attn_tree_workspace_bytes) g_tree_ws;
 decltype(&attn_evict) g_evict;
@@ -177,50 +179,100 @@ PyObject *pair(PyObject *a, PyObject *b) {
     return r;
 }
 
+// The tensors that both rotary appends take, checked: a[at] .. a[at + 10] are
+// pos, inv_freq, table, ctx, cu, interleaved, mscale, q_out, acc, status, stream.
+struct Append {
+    const qmv_attn_cache *c;
+    Device dev;
+    at::ScalarType kind;
+    int64_t N, Hq;
+    const void *q, *k, *v;
+    int64_t qs, ks, vs;
+    int in_dtype, rot, inter;
+    const int32_t *pos, *ctx, *cu;
+    const double *f;
+    Table t;
+    float mscale;
+    at::Tensor made;
+    void *out;
+    float *acc;
+    int32_t *status;
+    qmv_stream_t stream;
+
+    Append(PyObject *const *a, int at)
+        : c(as_cache(a[0])), dev(as_int(a[1])), kind(kind_of(c)) {
+        if (!THPVariable_Check(a[2])) type_error("q", "a tensor");
+        const at::ScalarType in = THPVariable_Unpack(a[2]).scalar_type();
+        if (in != at::kFloat && in != kind) type_error("q", "float32 or of the cache's type");
+        const at::Tensor &qt = tensor(a[2], in, dev, "q"), &kt = tensor(a[3], in, dev, "k"),
+                         &vt = tensor(a[4], in, dev, "v");
+        if (qt.dim() != 3) value_error("q", "[N][Hq][D]");
+        N = qt.size(0);
+        Hq = qt.size(1);
+        if (N > INT32_MAX || Hq > INT32_MAX) value_error("q", "smaller");
+        qs = token_stride(qt, N, Hq, c->D, "q");
+        ks = token_stride(kt, N, c->Hkv, c->D, "k");
+        vs = token_stride(vt, N, c->Hkv, c->D, "v");
+        q = qt.data_ptr();
+        k = kt.data_ptr();
+        v = vt.data_ptr();
+        in_dtype = in == at::kFloat ? QMV_F32 : c->dtype;
+        a += at;
+        pos = static_cast<const int32_t *>(addr(a[0], at::kInt, N, dev, "pos"));
+        f = static_cast<const double *>(addr(a[1], at::kDouble, -1, dev, "inv_freq"));
+        const int64_t half = THPVariable_Unpack(a[1]).numel();
+        rot = half > 65536 ? 1 << 17 : (int)(2 * half);
+        t = table(a[2], dev, "table");
+        ctx = static_cast<const int32_t *>(addr(a[3], at::kInt, t.B, dev, "ctx"));
+        cu = static_cast<const int32_t *>(addr(a[4], at::kInt, t.B + 1, dev, "cu"));
+        inter = PyObject_IsTrue(a[5]);
+        if (inter < 0) throw Bad();
+        mscale = (float)as_double(a[6]);
+        acc = static_cast<float *>(opt(a[8], at::kFloat, slots(c), dev, "acc"));
+        status = static_cast<int32_t *>(opt(a[9], at::kInt, 1, dev, "status"));
+        if (a[7] == Py_None) {
+            made = make({N, Hq, c->D}, kind, dev);
+            out = made.data_ptr();
+        } else {
+            out = addr(a[7], kind, N * Hq * c->D, dev, "q_out");
+        }
+        stream = as_stream(a[10], dev);
+    }
+};
+
 // (cache, device, q, k, v, pos, inv_freq, table, ctx, cu, interleaved, mscale,
 //  q_out, acc, status, stream)
 PyObject *rope_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded<16>(n, [&]() -> PyObject * {
-        const qmv_attn_cache *c = as_cache(a[0]);
-        const Device dev(as_int(a[1]));
-        const at::ScalarType kind = kind_of(c);
-        if (!THPVariable_Check(a[2])) type_error("q", "a tensor");
-        const at::ScalarType in = THPVariable_Unpack(a[2]).scalar_type();
-        if (in != at::kFloat && in != kind) type_error("q", "float32 or of the cache's type");
-        const at::Tensor &q = tensor(a[2], in, dev, "q"), &k = tensor(a[3], in, dev, "k"),
-                         &v = tensor(a[4], in, dev, "v");
-        if (q.dim() != 3) value_error("q", "[N][Hq][D]");
-        const int64_t N = q.size(0), Hq = q.size(1);
-        if (N > INT32_MAX || Hq > INT32_MAX) value_error("q", "smaller");
-        const int64_t qs = token_stride(q, N, Hq, c->D, "q"),
-                      ks = token_stride(k, N, c->Hkv, c->D, "k"),
-                      vs = token_stride(v, N, c->Hkv, c->D, "v");
-        const auto *pos = static_cast<const int32_t *>(addr(a[5], at::kInt, N, dev, "pos"));
-        const auto *f = static_cast<const double *>(addr(a[6], at::kDouble, -1, dev, "inv_freq"));
-        const int64_t half = THPVariable_Unpack(a[6]).numel();
-        const Table t = table(a[7], dev, "table");
-        const auto *ctx = static_cast<const int32_t *>(addr(a[8], at::kInt, t.B, dev, "ctx"));
-        const auto *cu = static_cast<const int32_t *>(addr(a[9], at::kInt, t.B + 1, dev, "cu"));
-        const int inter = PyObject_IsTrue(a[10]);
-        if (inter < 0) throw Bad();
-        const float mscale = (float)as_double(a[11]);
-        void *acc = opt(a[13], at::kFloat, slots(c), dev, "acc");
-        void *status = opt(a[14], at::kInt, 1, dev, "status");
-        at::Tensor made;
-        void *out;
-        if (a[12] == Py_None) {
-            made = make({N, Hq, c->D}, kind, dev);
-            out = made.data_ptr();
-        } else {
-            out = addr(a[12], kind, N * Hq * c->D, dev, "q_out");
-        }
+        const Append x(a, 5);
         check("attn_rope_append",
-              g_rope(c, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
-                     in == at::kFloat ? QMV_F32 : c->dtype, (int)Hq, pos, f,
-                     half > 65536 ? 1 << 17 : (int)(2 * half), inter, mscale, t.p, t.width, ctx, cu,
-                     t.B, (int)N, out, static_cast<float *>(acc), static_cast<int32_t *>(status),
-                     as_stream(a[15], dev)));
-        return wrap(a[12], made);
+              g_rope(x.c, x.q, x.qs, x.k, x.ks, x.v, x.vs, x.in_dtype, (int)x.Hq, x.pos, x.f, x.rot,
+                     x.inter, x.mscale, x.t.p, x.t.width, x.ctx, x.cu, x.t.B, (int)x.N, x.out, x.acc,
+                     x.status, x.stream));
+        return wrap(a[12], x.made);
+    });
+}
+
+// (cache, device, q, k, v, q_weight, k_weight, eps, pos, inv_freq, table, ctx, cu,
+//  interleaved, mscale, q_out, acc, status, stream)
+PyObject *norm_rope_append(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded<19>(n, [&]() -> PyObject * {
+        const Append x(a, 8);
+        // both weights in one type (that of the first that is there)
+        at::ScalarType wk = at::kFloat;
+        for (int i = 6; i >= 5; --i)
+            if (a[i] != Py_None) {
+                if (!THPVariable_Check(a[i])) type_error(i == 5 ? "q_weight" : "k_weight", "a tensor");
+                wk = THPVariable_Unpack(a[i]).scalar_type();
+            }
+        if (wk != at::kFloat && wk != x.kind) type_error("q_weight and k_weight", "float32 or of the cache's type");
+        const void *qw = opt(a[5], wk, x.c->D, x.dev, "q_weight"), *kw = opt(a[6], wk, x.c->D, x.dev, "k_weight");
+        check("attn_norm_rope_append",
+              g_norm_rope(x.c, x.q, x.qs, x.k, x.ks, x.v, x.vs, x.in_dtype, (int)x.Hq, qw, kw,
+                          wk == at::kFloat ? QMV_F32 : x.c->dtype, (float)as_double(a[7]), x.pos, x.f,
+                          x.rot, x.inter, x.mscale, x.t.p, x.t.width, x.ctx, x.cu, x.t.B, (int)x.N,
+                          x.out, x.acc, x.status, x.stream));
+        return wrap(a[15], x.made);
     });
 }
 
@@ -327,14 +379,17 @@ PyObject *evict(PyObject *, PyObject *const *a, Py_ssize_t n) {
 
 // (QmvError, address of each entry point)
 PyObject *init(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    return guarded<5>(n, [&]() -> PyObject * {
+    return guarded<6>(n, [&]() -> PyObject * {
         Py_XDECREF(g_error);
         Py_INCREF(a[0]);
         g_error = a[0];
-        g_rope = reinterpret_cast<decltype(g_rope)>(PyLong_AsVoidPtr(a[1]));
-        g_tree = reinterpret_cast<decltype(g_tree)>(PyLong_AsVoidPtr(a[2]));
-        g_tree_ws = reinterpret_cast<decltype(g_tree_ws)>(PyLong_AsVoidPtr(a[3]));
-        g_evict = reinterpret_cast<decltype(g_evict)>(PyLong_AsVoidPtr(a[4]));
+        int i = 1;
+        auto take = [&](auto &f) { f = reinterpret_cast<std::decay_t<decltype(f)>>(PyLong_AsVoidPtr(a[i++])); };
+        take(g_rope);
+        take(g_norm_rope);
+        take(g_tree);
+        take(g_tree_ws);
+        take(g_evict);
         if (PyErr_Occurred()) throw Bad();
         Py_RETURN_NONE;
     });
@@ -346,6 +401,7 @@ PyCFunction fast(PyObject *(*f)(PyObject *, PyObject *const *, Py_ssize_t)) {
 
 PyMethodDef methods[] = {{"init", fast(init), METH_FASTCALL, nullptr},
                          {"rope_append", fast(rope_append), METH_FASTCALL, nullptr},
+                         {"norm_rope_append", fast(norm_rope_append), METH_FASTCALL, nullptr},
                          {"tree", fast(tree), METH_FASTCALL, nullptr},
                          {"evict", fast(evict), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};

@@ -1,0 +1,70 @@
+"""Normed append, windowed attention and the upkeep of pages refuse bad arguments on the host,
+before any CUDA call."""
+import ctypes
+
+import pytest
+
+import int4_group_quantized_gs64_gb300 as q
+
+EINVAL, ESHAPE, EWORKSPACE, EALIGN = -1, -2, -3, -6
+FAKE = 0x10000  # aligned and never dereferenced: validation fails first
+P = ctypes.c_void_p(FAKE)
+ODD = ctypes.c_void_p(FAKE + 2)
+
+
+@pytest.fixture(scope="module")
+def L():
+    q.build()
+    return q.lib()
+
+
+def desc(k=FAKE, v=FAKE, pages=8, Hkv=2, page=16, D=64, dtype=1):
+    return q.AttnCacheDesc(k, v, pages, Hkv, page, D, dtype)
+
+
+def norm(L, d=None, **kw):
+    a = dict(q=P, qs=256, k=P, ks=128, v=P, vs=128, t=1, Hq=4, qw=P, kw=P, wt=0, eps=1e-6, pos=P, f=P,
+             rot=64, inter=0, m=1.0, table=P, mp=4, ctx=P, cu=P, B=2, N=3, out=P, acc=None, st=None)
+    a.update(kw)
+    return L.attn_norm_rope_append(ctypes.byref(d or desc()), a["q"], a["qs"], a["k"], a["ks"], a["v"],
+                                   a["vs"], a["t"], a["Hq"], a["qw"], a["kw"], a["wt"], a["eps"],
+                                   a["pos"], a["f"], a["rot"], a["inter"], a["m"], a["table"], a["mp"],
+                                   a["ctx"], a["cu"], a["B"], a["N"], a["out"], a["acc"], a["st"], None)
+
+
+CACHE_CALLS = {"norm": norm}
+
+
+@pytest.mark.parametrize("call", CACHE_CALLS.values(), ids=CACHE_CALLS.keys())
+@pytest.mark.parametrize("bad,want", [
+    (dict(k=None), EINVAL), (dict(v=None), EINVAL), (dict(pages=0), EINVAL), (dict(Hkv=0), EINVAL),
+    (dict(dtype=0), EINVAL), (dict(dtype=3), EINVAL), (dict(D=96), ESHAPE), (dict(D=256), ESHAPE),
+    (dict(page=8), ESHAPE), (dict(page=48), ESHAPE), (dict(page=512), ESHAPE),
+    (dict(pages=1 << 26), ESHAPE), (dict(k=FAKE + 8), EALIGN), (dict(v=FAKE + 2), EALIGN)])
+def test_cache_descriptor(L, call, bad, want):
+    assert call(L, desc(**bad)) == want
+
+
+@pytest.mark.parametrize("call", CACHE_CALLS.values(), ids=CACHE_CALLS.keys())
+def test_batch_limits(L, call):
+    assert call(L, B=-1) == EINVAL
+    assert call(L, mp=0) == EINVAL
+    assert call(L, B=40000) == ESHAPE          # 40000 * 2 heads
+    assert call(L, mp=(1 << 26) + 1) == ESHAPE  # * 16 > 2^30
+    assert call(L, B=0) == 0                    # nothing to do
+
+
+def test_norm(L):
+    for k in ("q", "k", "v", "pos", "f", "table", "ctx", "cu", "out"):
+        assert norm(L, **{k: None}) == EINVAL, k
+    assert norm(L, N=0) == 0 and norm(L, N=-1) == EINVAL and norm(L, N=(1 << 22) + 1) == ESHAPE
+    assert norm(L, wt=2) == EINVAL and norm(L, wt=5) == EINVAL    # fp16 weights of a bf16 cache
+    for eps in (-1e-9, float("inf"), float("nan")):
+        assert norm(L, eps=eps) == EINVAL
+    assert norm(L, rot=33) == EINVAL and norm(L, t=2) == EINVAL and norm(L, Hq=3) == EINVAL
+    assert norm(L, qs=255) == ESHAPE
+    assert norm(L, qw=ODD) == EALIGN and norm(L, kw=ODD) == EALIGN
+    odd1 = ctypes.c_void_p(FAKE + 1)
+    assert norm(L, qw=odd1, wt=1) == EALIGN and norm(L, kw=odd1, wt=1) == EALIGN
+    for k in ("pos", "table", "ctx", "cu", "acc", "st"):
+        assert norm(L, **{k: ODD}) == EALIGN, k
