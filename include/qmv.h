@@ -505,6 +505,41 @@ int attn_tree(const qmv_attn_cache *c, const void *q, int64_t q_stride, int Hq,
               int o_dtype, float *lse, const float *acc_in, float *acc_out, float decay,
               int32_t *status, void *ws, size_t ws_bytes, qmv_stream_t stream);
 
+/* Workspace of attn_window, in bytes (0 for unsupported sizes). It depends on the
+ * heads and on max_new alone. */
+size_t attn_window_workspace_bytes(const qmv_attn_cache *c, int Hq, int B, int N, int max_new,
+                                   int max_pages);
+
+/* Causal attention of each sequence's new tokens, any number of them (a prompt,
+ * a chunk of one, a single token), over its cache, new tokens included (their
+ * keys and values are in their slots: attn_rope_append), with a sliding window
+ * and first tokens that stay visible. Head hq reads key/value head
+ * hq / (Hq / Hkv). Token n = cu[b] + t, at slot p = ctx[b] + t, sees the slots
+ *     j <= p with j > p - window or j < sinks
+ * (its own among them), and
+ *     x_j = scale * q[n][hq] . k_j      over the slots j that it sees
+ *     lse[n][hq] = log sum_j exp(x_j),  o[n][hq] = sum_j exp(x_j - lse) v_j
+ * A row whose scores are all -inf gets o = 0 and lse = -inf. What a token does
+ * not see never reaches its row, infinities and NaNs in stale or hidden slots
+ * included. (Infinities and NaNs among the values of a key that it does see
+ * leave these elements of its output infinite or NaN.) Pages without a slot that
+ * one of the sequence's new tokens sees are not looked at: their table entries
+ * may be anything, and they may belong to others by now. Sequences may share
+ * pages. Results do not depend on the order in which thread blocks finish.
+ *   q [N] rows of Hq * D in the cache's type, 16-byte aligned, q_stride
+ *     elements apart (a multiple of 8); N <= 2^22
+ *   max_new  an upper bound of a sequence's new tokens, >= 1, at most 2^22 and
+ *     2^30 / (Hq / Hkv); calls of up to 16 / (Hq / Hkv) take a kernel made for few rows
+ *   window >= 1 (INT32_MAX: all tokens before), sinks >= 0
+ *   o     [N][Hq][D] in o_dtype (QMV_F32 or the cache's), 16-byte aligned
+ *   lse   [N][Hq] fp32
+ *   ws  at least attn_window_workspace_bytes(...) bytes, 256-byte aligned, not
+ *     shared with a concurrent call. */
+int attn_window(const qmv_attn_cache *c, const void *q, int64_t q_stride, int Hq,
+                const int32_t *table, int max_pages, const int32_t *ctx, const int32_t *cu, int B,
+                int N, int max_new, int window, int sinks, float scale, void *o, int o_dtype,
+                float *lse, int32_t *status, void *ws, size_t ws_bytes, qmv_stream_t stream);
+
 /* Eviction by accumulated attention weight. Each key/value head of a sequence
  * of lens[b] tokens keeps min(lens[b], budget) of them: all when they fit,
  * else the first `sink`, the last `recent` and, of those between, the

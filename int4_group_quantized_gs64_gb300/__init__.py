@@ -11,7 +11,7 @@ forms ``qmv_int4_gs_bf16`` and ``qmv_int8_row_bf16``,
 ``moe_route_topk``, ``moe_group``, ``moe_gate_up_silu``, ``moe_down``,
 ``moe_combine``, ``moe_workspace_bytes``, ``moe_expert_ffn_int4`` and
 ``moe_expert_ffn_int4_prefill``; ``attn_rope_append``, ``attn_norm_rope_append``,
-``attn_tree`` and ``attn_evict`` over a paged cache (``AttnCache``).
+``attn_tree``, ``attn_window`` and ``attn_evict`` over a paged cache (``AttnCache``).
 """
 from __future__ import annotations
 
@@ -103,6 +103,9 @@ def lib():
             "attn_tree_workspace_bytes": ([C, i32, i32, i32, i32, i32, i32], sz),
             "attn_tree": ([C, vp, i64, i32, vp, i32, vp, vp, i32, i32, i32, vp, i32, f32, vp, i32,
                            vp, vp, vp, f32, vp, vp, sz, vp], i32),
+            "attn_window_workspace_bytes": ([C, i32, i32, i32, i32, i32], sz),
+            "attn_window": ([C, vp, i64, i32, vp, i32, vp, vp, i32, i32, i32, i32, i32, f32, vp, i32,
+                             vp, vp, vp, sz, vp], i32),
             "attn_evict": ([C, vp, vp, i32, vp, i32, i32, i32, i32, C, vp, vp, i32, vp, vp, vp, vp],
                            i32),
         }
@@ -516,7 +519,8 @@ def _torch_binding():
         loader.exec_module(mod)
         L = lib()
         mod.init(QmvError, *(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
-            "attn_rope_append", "attn_norm_rope_append", "attn_tree", "attn_tree_workspace_bytes", "attn_evict")))
+            "attn_rope_append", "attn_norm_rope_append", "attn_tree", "attn_tree_workspace_bytes", "attn_window",
+            "attn_window_workspace_bytes", "attn_evict")))
         _torch_mod = mod
     return _torch_mod
 
@@ -548,6 +552,9 @@ class AttnCache:
         import torch
         k = torch.empty((pages, Hkv, page, D), dtype=dtype or torch.bfloat16, device=device)
         return cls(k, torch.empty_like(k))
+
+
+_ALL = 2 ** 31 - 1  # a window that hides nothing
 
 
 def _on(stream, shape, dtype, device):
@@ -633,6 +640,43 @@ def attn_tree(cache: AttnCache, q, table, ctx, cu, max_draft: int, mask=None, sc
         cache.address, cache.device_index, q, table, ctx, cu, max_draft, mask,
         cache.scale if scale is None else scale, o, o_dtype is torch.float32, lse, acc, acc_out,
         decay, ws, status, handle)
+
+
+def attn_window_workspace_bytes(cache: AttnCache, Hq: int, B: int, N: int, max_new: int,
+                                max_pages: int) -> int:
+    import torch
+    with torch.cuda.device(cache.device_index):
+        return int(lib().attn_window_workspace_bytes(cache.desc, Hq, B, N, max_new, max_pages))
+
+
+def attn_window(cache: AttnCache, q, table, ctx, cu, max_new: int, window=None, sinks: int = 0,
+                scale=None, o=None, o_dtype=None, lse=None, ws=None, status=None, stream=None):
+    """Causal attention of new tokens over the cache; returns (o [N][Hq][D], lse fp32 [N][Hq]).
+
+    q [N][Hq][D] in the cache's type; max_new an upper bound of a sequence's new tokens (any
+    number). The token at slot p sees the slots j <= p with j > p - window (None: all) or
+    j < sinks; pages that no new token of a sequence sees may be missing from its table. scale
+    defaults to D ** -0.5; o_dtype the cache's (default) or float32."""
+    import torch
+    if o_dtype is None:
+        o_dtype = cache.dtype if o is None else o.dtype
+    elif o_dtype not in (torch.float32, cache.dtype):
+        raise TypeError(f"o must be float32 or {cache.dtype}")
+    handle = None
+    if stream is not None:
+        handle = stream.cuda_stream
+        N, Hq = q.shape[0], q.shape[1]
+        if o is None:
+            o = _on(stream, q.shape, o_dtype, cache.device)
+        if lse is None:
+            lse = _on(stream, (N, Hq), torch.float32, cache.device)
+        if ws is None:
+            ws = _on(stream, max(256, attn_window_workspace_bytes(
+                cache, Hq, table.shape[0], N, max_new, table.shape[1])), torch.uint8, cache.device)
+    return (_torch_mod or _torch_binding()).window(
+        cache.address, cache.device_index, q, table, ctx, cu, max_new,
+        _ALL if window is None else window, sinks, cache.scale if scale is None else scale, o,
+        o_dtype is torch.float32, lse, ws, status, handle)
 
 
 def attn_evict(src: AttnCache, acc, table, lens, budget: int, dst: AttnCache, dst_acc, dst_table,

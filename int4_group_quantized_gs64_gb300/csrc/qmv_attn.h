@@ -60,6 +60,21 @@ size_t attn_tree_ws_bytes(const AttnCache &c, int Hq, int B, int N, int max_draf
                           bool acc);
 cudaError_t launch_attn_tree(const AttnCache &c, const TreeCall &t, cudaStream_t st);
 
+struct WindowCall {
+    AttnSeqs s;  // max_draft: the new tokens of a sequence, at most
+    const void *q;
+    long long q_stride;
+    int Hq, window, sinks;
+    float scale;
+    void *o;
+    int o_f32;
+    float *lse;
+    int32_t *status;
+    void *ws;
+};
+size_t attn_window_ws_bytes(const AttnCache &c, int Hq, int max_new);
+cudaError_t launch_attn_window(const AttnCache &c, const WindowCall &t, cudaStream_t st);
+
 cudaError_t launch_attn_evict(const AttnCache &src, const float *acc, const int32_t *table,
                               int max_pages, const int32_t *lens, int B, int budget, int sink,
                               int recent, const AttnCache &dst, float *dst_acc,

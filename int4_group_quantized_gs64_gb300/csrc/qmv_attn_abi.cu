@@ -42,6 +42,11 @@ bool heads_ok(const qmv_attn_cache *c, int Hq) {
     return Hq >= 1 && Hq <= kMaxHeads && Hq % c->Hkv == 0;
 }
 
+// A bound of a sequence's new tokens: its rows a key/value head are counted in 31 bits.
+bool new_ok(const qmv_attn_cache *c, int Hq, int max_new) {
+    return max_new >= 1 && max_new <= 1 << 22 && (int64_t)max_new * (Hq / c->Hkv) <= (int64_t)1 << 30;
+}
+
 // Both rotary appends; norm null: without norms.
 int rope_append(const qmv_attn_cache *c, const void *q, int64_t q_stride, const void *k,
                 int64_t k_stride, const void *v, int64_t v_stride, int in_dtype, int Hq,
@@ -146,6 +151,42 @@ int attn_tree(const qmv_attn_cache *c, const void *q, int64_t q_stride, int Hq,
     t.acc_in = acc_in; t.acc_out = acc_out; t.decay = decay;
     t.status = status; t.ws = ws;
     return from_cuda(qmv::launch_attn_tree(cache(c), t, cs(stream)));
+}
+
+size_t attn_window_workspace_bytes(const qmv_attn_cache *c, int Hq, int B, int N, int max_new,
+                                   int max_pages) {
+    if (check_cache(c) || check_batch(c, B, max_pages) || !heads_ok(c, Hq) || N < 0 ||
+        !new_ok(c, Hq, max_new))
+        return 0;
+    return qmv::attn_window_ws_bytes(cache(c), Hq, max_new);
+}
+
+int attn_window(const qmv_attn_cache *c, const void *q, int64_t q_stride, int Hq,
+                const int32_t *table, int max_pages, const int32_t *ctx, const int32_t *cu, int B,
+                int N, int max_new, int window, int sinks, float scale, void *o, int o_dtype,
+                float *lse, int32_t *status, void *ws, size_t ws_bytes, qmv_stream_t stream) {
+    int r = check_cache(c);
+    if (r) return r;
+    if ((r = check_batch(c, B, max_pages))) return r;
+    if (N < 0 || !heads_ok(c, Hq) || max_new < 1 || window < 1 || sinks < 0 || !isfinite(scale))
+        return QMV_EINVAL;
+    if (o_dtype != QMV_F32 && o_dtype != c->dtype) return QMV_EINVAL;
+    if (N > 1 << 22 || !new_ok(c, Hq, max_new)) return QMV_ESHAPE;
+    if (q_stride < (int64_t)Hq * c->D) return QMV_ESHAPE;
+    if (B == 0 || N == 0) return QMV_OK;
+    if (!q || !table || !ctx || !cu || !o || !lse) return QMV_EINVAL;
+    if (!aligned(q, 16) || q_stride % 8 || !aligned(table, 4) || !aligned(ctx, 4) ||
+        !aligned(cu, 4) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(status, 4))
+        return QMV_EALIGN;
+    if (!ws || !aligned(ws, 256) || ws_bytes < qmv::attn_window_ws_bytes(cache(c), Hq, max_new))
+        return QMV_EWORKSPACE;
+    qmv::WindowCall t;
+    t.s = qmv::AttnSeqs{table, ctx, cu, B, N, max_new, max_pages};
+    t.q = q; t.q_stride = q_stride; t.Hq = Hq;
+    t.window = window; t.sinks = sinks; t.scale = scale;
+    t.o = o; t.o_f32 = o_dtype == QMV_F32; t.lse = lse;
+    t.status = status; t.ws = ws;
+    return from_cuda(qmv::launch_attn_window(cache(c), t, cs(stream)));
 }
 
 int attn_evict(const qmv_attn_cache *src, const float *acc, const int32_t *table, int max_pages,

@@ -1,5 +1,11 @@
-// qmv_attn_plan.cuh - the arguments of the tree attention kernels, how the
-// thread blocks share the work out, and which drafts a row sees.
+// qmv_attn_plan.cuh - the arguments of the attention kernels, how the thread
+// blocks share the work out, and which keys a row sees.
+//
+// The kernels come in two forms (kWin): trees of drafts, whose rows see all
+// cached keys and the drafts of a mask, and causal rows with a sliding window
+// and a few first keys. In the second form the keys of an item (and their
+// number) depend on its block of rows, and slots that none of its rows sees are
+// not looked at, nor are their page ids.
 #pragma once
 
 #include "qmv_attn.cuh"
@@ -9,6 +15,11 @@ namespace qmv {
 namespace attn {
 
 constexpr uint32_t kPoll = 1u << 22;  // polls of a copy's barrier before giving up
+
+// A segment that is not its whole item: units [u0, u0 + n) of nu (n 0: none).
+struct PartInfo {
+    int b, h, rb, u0, n, nu, quota, pad;
+};
 
 struct TreeArgs {
     Seqs s;
@@ -37,6 +48,10 @@ struct TreeArgs {
     float *stash;  // scores for the weights, [B][Hkv][16 keys][max_rows][16], or null
     int max_rows;
     int32_t *status;
+    // kWin: a row at slot p sees j <= p with j > p - window or j < sinks
+    int window, sinks;
+    int lunit;       // kWin: unit = 1 << lunit
+    PartInfo *info;  // kWin: which items the segments in part_o belong to, [grid][2]
 };
 
 // r / G for a row r < 2^18 and G <= 1024: the rounding of ginv adds less than
@@ -50,6 +65,84 @@ __device__ __forceinline__ int row_blocks(const Seq &q, int G, int rows) {
 }
 __device__ __forceinline__ int key_units(const Seq &q, int unit) {
     return (q.ctx + q.T + unit - 1) / unit;
+}
+
+// kWin: the keys that some row of a block of rows sees: slots [lo, p1] and those
+// below a.sinks. They are looked at in units of a.unit slots on a grid from slot
+// 0; `us` units hold first keys only, the rest begin at `shift` units more.
+struct Reach {
+    int p0, p1, lo, us, shift, nu;
+    int t0, r0;  // the block's first row is row r0 of token t0's G
+    __device__ __forceinline__ void set(const TreeArgs &a, const Seq &q, int rb) {
+        const int first = rb * a.rows, n = min(a.rows, q.T * a.G - first);
+        t0 = first / a.G;
+        r0 = first - t0 * a.G;
+        p0 = q.ctx + t0;
+        p1 = p0 + div_g(a, r0 + n - 1);
+        lo = max(0, p0 - a.window + 1);
+        const int w0 = lo >> a.lunit;
+        us = min((min(a.sinks, lo) + a.unit - 1) >> a.lunit, w0);
+        shift = w0 - us;
+        nu = (p1 >> a.lunit) - shift + 1;
+    }
+    // Whether some row sees a slot of [s0, s1), and whether all rows see all of them.
+    __device__ __forceinline__ bool some(const TreeArgs &a, int s0, int s1) const {
+        return s0 <= p1 && (s1 > lo || s0 < a.sinks);
+    }
+    __device__ __forceinline__ bool all(const TreeArgs &a, int s0, int s1) const {
+        return s1 - 1 <= p0 && (s0 > p1 - a.window || s1 <= a.sinks);
+    }
+};
+
+__device__ __forceinline__ uint32_t bits_below(int n) {
+    return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
+}
+// kWin: which of the 32 slots from `slot` on a row at slot p sees.
+__device__ __forceinline__ uint32_t window_word(const TreeArgs &a, int p, int slot) {
+    const int lo = max(0, p - a.window + 1);
+    return bits_below(p + 1 - slot) & (~bits_below(lo - slot) | bits_below(a.sinks - slot));
+}
+
+// kWin: the units of one head of a sequence. A thread adds up the blocks of
+// rows `from`, `from` + step, ...
+__device__ __forceinline__ long long window_units(const TreeArgs &a, const Seq &q, int from, int step) {
+    long long n = 0;
+    const int nrb = row_blocks(q, a.G, a.rows);
+#pragma unroll 1
+    for (int rb = from; rb < nrb; rb += step) {
+        Reach r;
+        r.set(a, q, rb);
+        n += r.nu;
+    }
+    return n;
+}
+constexpr int kAlone = 4;  // blocks of rows that a thread adds up by itself
+
+// All units of a sequence, by one thread.
+template <bool kWin>
+__device__ __forceinline__ long long seq_units(const TreeArgs &a, const Seq &q) {
+    if (q.T <= 0) return 0;
+    if (kWin) return window_units(a, q, 0, 1) * a.Hkv;
+    return (long long)key_units(q, a.unit) * row_blocks(q, a.G, a.rows) * a.Hkv;
+}
+// A lane's sequence each; the whole warp helps with long ones.
+template <bool kWin>
+__device__ __forceinline__ long long lane_units(const TreeArgs &a, const Seq &q) {
+    if (!kWin) return seq_units<false>(a, q);
+    const bool big = q.T > 0 && row_blocks(q, a.G, a.rows) > kAlone;
+    long long n = big ? 0 : seq_units<true>(a, q);
+    for (uint32_t who = __ballot_sync(0xFFFFFFFFu, big); who; who &= who - 1) {
+        const int from = __ffs(who) - 1, lane = threadIdx.x & 31;
+        Seq o;
+        o.ctx = __shfl_sync(0xFFFFFFFFu, q.ctx, from);
+        o.first = 0;
+        o.T = __shfl_sync(0xFFFFFFFFu, q.T, from);
+        long long x = window_units(a, o, lane, 32);
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, k);
+        if (lane == from) n = x * a.Hkv;
+    }
+    return n;
 }
 
 // All items' units, and those before sequence `upto`. A thread of the block
@@ -108,7 +201,7 @@ __device__ __forceinline__ long long count_units(const TreeArgs &a, int upto, lo
 
 // This block's share [u0, u1) of all units, and where it starts.
 struct Share {
-    long long u0, u1, rest;  // rest: u0's place among its sequence's units
+    long long u0, u1, rest, quota;  // rest: u0's place among its sequence's units
     int b;
 };
 template <int kWarps>
@@ -121,7 +214,7 @@ struct ShareScratch {
 // Each thread of the block counts ceil(B / threads) sequences in a row; the
 // one whose units hold u0 says where they start. Up to 32 sequences each warp
 // counts for itself, which saves two barriers.
-template <int kThreads>
+template <int kThreads, bool kWin = false>
 __device__ __forceinline__ Share find_share(const TreeArgs &a, ShareScratch<kThreads / 32> *sh) {
     if (a.s.B <= 32) {
         const int lane = threadIdx.x & 31;
@@ -129,8 +222,7 @@ __device__ __forceinline__ Share find_share(const TreeArgs &a, ShareScratch<kThr
         Seq q;
         q.ctx = q.first = q.T = 0;
         if (lane < a.s.B) q = get_seq(a.s, lane, ok);
-        const long long n =
-            q.T > 0 ? (long long)key_units(q, a.unit) * row_blocks(q, a.G, a.rows) * a.Hkv : 0;
+        const long long n = lane_units<kWin>(a, q);
         long long inc = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -139,6 +231,7 @@ __device__ __forceinline__ Share find_share(const TreeArgs &a, ShareScratch<kThr
         }
         const long long total = __shfl_sync(0xFFFFFFFFu, inc, 31), quota = (total + a.grid - 1) / a.grid;
         Share s;
+        s.quota = quota;
         s.u0 = quota * blockIdx.x;
         s.u1 = min(s.u0 + quota, total);
         const uint32_t who = __ballot_sync(0xFFFFFFFFu, inc > s.u0);
@@ -151,7 +244,7 @@ __device__ __forceinline__ Share find_share(const TreeArgs &a, ShareScratch<kThr
     auto units = [&](int b) -> long long {
         bool ok;
         const Seq q = get_seq(a.s, b, ok);
-        return q.T > 0 ? (long long)key_units(q, a.unit) * row_blocks(q, a.G, a.rows) * a.Hkv : 0;
+        return seq_units<kWin>(a, q);
     };
     long long n = 0;
 #pragma unroll 1
@@ -172,6 +265,7 @@ __device__ __forceinline__ Share find_share(const TreeArgs &a, ShareScratch<kThr
     }
     Share s;
     const long long quota = (total + a.grid - 1) / a.grid;
+    s.quota = quota;
     s.u0 = quota * blockIdx.x;
     s.u1 = min(s.u0 + quota, total);
     if (s.u0 < s.u1 && before <= s.u0 && s.u0 < before + n) {
@@ -193,37 +287,99 @@ __device__ __forceinline__ Share find_share(const TreeArgs &a, ShareScratch<kThr
 }
 
 // The place of a unit: sequence, head, row block, unit of the item's keys.
-struct Cursor {
+template <bool kWin>
+struct CursorOf {
     int b, h, rb, u;
     int nu, nrb;
     Seq q;
+    Reach r;  // kWin
     __device__ __forceinline__ void load(const TreeArgs &a) {
         bool ok;
         q = get_seq(a.s, b, ok);
-        nu = key_units(q, a.unit);
         nrb = row_blocks(q, a.G, a.rows);
+        if (!kWin) nu = key_units(q, a.unit);
+    }
+    __device__ __forceinline__ void reach(const TreeArgs &a) {
+        if (kWin) {
+            r.set(a, q, rb);
+            nu = r.nu;
+        }
+    }
+    // The place of unit x of the item on the grid of units.
+    __device__ __forceinline__ int at(int x) const { return kWin && x >= r.us ? x + r.shift : x; }
+    // Rows of this block, and of row i its token and its head among the G.
+    __device__ __forceinline__ int rows_left(const TreeArgs &a) const { return q.T * a.G - rb * a.rows; }
+    __device__ __forceinline__ int token(const TreeArgs &a, int i, int &g) const {
+        const int x = kWin ? r.r0 + i : rb * a.rows + i, t = div_g(a, x);
+        g = x - t * a.G;
+        return kWin ? r.t0 + t : t;
+    }
+    // Whether some row of the item may see a slot of [s0, s1).
+    __device__ __forceinline__ bool some(const TreeArgs &a, int s0, int s1) const {
+        return kWin ? r.some(a, s0, s1) : s0 < q.ctx + q.T;
     }
     __device__ __forceinline__ void next_item(const TreeArgs &a) {
         u = 0;
-        if (++rb < nrb) return;
+        if (++rb < nrb) return reach(a);
         rb = 0;
-        if (++h < a.Hkv) return;
+        if (++h < a.Hkv) return reach(a);
         h = 0;
         do {
             ++b;
             if (b >= a.s.B) return;
             load(a);
         } while (q.T == 0);
+        reach(a);
     }
     __device__ __forceinline__ void start(const TreeArgs &a, const Share &s) {
         b = s.b;
         load(a);
+        if (kWin) return start_window(a, s.rest);
         const int item = (int)(s.rest / nu);
         u = (int)(s.rest - (long long)item * nu);
         h = item / nrb;
         rb = item - h * nrb;
     }
+    // kWin, whole warp: the head from the units of one, then its block of rows, 32 at a time.
+    __device__ __forceinline__ void start_window(const TreeArgs &a, long long rest) {
+        const int lane = threadIdx.x & 31;
+        if (nrb == 1) {
+            rb = 0;
+            reach(a);
+            h = (int)(rest / nu);
+            u = (int)(rest - (long long)h * nu);
+            return;
+        }
+        long long n = window_units(a, q, lane, 32);
+#pragma unroll
+        for (int k = 16; k > 0; k >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, k);
+        h = (int)(rest / n);
+        rest -= h * n;
+#pragma unroll 1
+        for (rb = 0;; rb += 32) {
+            Reach x;
+            x.nu = 0;
+            if (rb + lane < nrb) x.set(a, q, rb + lane);
+            int inc = x.nu;
+#pragma unroll
+            for (int k = 1; k < 32; k <<= 1) {
+                const int v = __shfl_up_sync(0xFFFFFFFFu, inc, k);
+                if (lane >= k) inc += v;
+            }
+            const uint32_t who = __ballot_sync(0xFFFFFFFFu, inc > rest);
+            if (who || rb + 32 >= nrb) {
+                const int l = who ? __ffs(who) - 1 : 0;
+                rest -= __shfl_sync(0xFFFFFFFFu, inc - x.nu, l);
+                rb += l;
+                break;
+            }
+            rest -= __shfl_sync(0xFFFFFFFFu, inc, 31);
+        }
+        u = (int)rest;
+        reach(a);
+    }
 };
+using Cursor = CursorOf<false>;
 
 // Element `col` (a multiple of 4) of row r of a block's first or last segment.
 template <int D>

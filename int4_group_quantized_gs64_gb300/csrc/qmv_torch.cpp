@@ -22,6 +22,8 @@ decltype(&attn_rope_append) g_rope;
 decltype(&attn_norm_rope_append) g_norm_rope;
 decltype(&attn_tree) g_tree;
 decltype(&attn_tree_workspace_bytes) g_tree_ws;
+decltype(&attn_window) g_window;
+decltype(&attn_window_workspace_bytes) g_window_ws;
 decltype(&attn_evict) g_evict;
 PyObject *g_error;  // QmvError(name, status)
 
@@ -339,6 +341,58 @@ PyObject *tree(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+// (cache, device, q, table, ctx, cu, max_new, window, sinks, scale, o, o_float32,
+//  lse, ws, status, stream)
+PyObject *window(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded<16>(n, [&]() -> PyObject * {
+        const qmv_attn_cache *c = as_cache(a[0]);
+        const Device dev(as_int(a[1]));
+        const at::ScalarType kind = kind_of(c);
+        const at::Tensor &q = tensor(a[2], kind, dev, "q");
+        if (q.dim() != 3) value_error("q", "[N][Hq][D]");
+        const int64_t N = q.size(0), Hq = q.size(1);
+        if (N > INT32_MAX || Hq > INT32_MAX) value_error("q", "smaller");
+        const int64_t qs = token_stride(q, N, Hq, c->D, "q");
+        const Table t = table(a[3], dev, "table");
+        const auto *ctx = static_cast<const int32_t *>(addr(a[4], at::kInt, t.B, dev, "ctx"));
+        const auto *cu = static_cast<const int32_t *>(addr(a[5], at::kInt, t.B + 1, dev, "cu"));
+        const int max_new = as_int(a[6]), win = as_int(a[7]), sinks = as_int(a[8]);
+        const float scale = (float)as_double(a[9]);
+        const int f32 = PyObject_IsTrue(a[11]);
+        if (f32 < 0) throw Bad();
+        const at::ScalarType okind = f32 ? at::kFloat : kind;
+        void *status = opt(a[14], at::kInt, 1, dev, "status");
+        at::Tensor made_o, made_lse, made_ws;
+        void *o, *lse, *ws;
+        size_t ws_bytes;
+        if (a[10] == Py_None) {
+            made_o = make({N, Hq, c->D}, okind, dev);
+            o = made_o.data_ptr();
+        } else {
+            o = addr(a[10], okind, N * Hq * c->D, dev, "o");
+        }
+        if (a[12] == Py_None) {
+            made_lse = make({N, Hq}, at::kFloat, dev);
+            lse = made_lse.data_ptr();
+        } else {
+            lse = addr(a[12], at::kFloat, N * Hq, dev, "lse");
+        }
+        if (a[13] == Py_None) {
+            ws_bytes = g_window_ws(c, (int)Hq, t.B, (int)N, max_new, t.width);
+            made_ws = make({(int64_t)(ws_bytes < 256 ? 256 : ws_bytes)}, at::kByte, dev);
+            ws = made_ws.data_ptr();
+        } else {
+            ws = addr(a[13], at::kByte, -1, dev, "ws");
+            ws_bytes = (size_t)THPVariable_Unpack(a[13]).numel();
+        }
+        check("attn_window",
+              g_window(c, q.data_ptr(), qs, (int)Hq, t.p, t.width, ctx, cu, t.B, (int)N, max_new, win,
+                       sinks, scale, o, f32 ? QMV_F32 : c->dtype, static_cast<float *>(lse),
+                       static_cast<int32_t *>(status), ws, ws_bytes, as_stream(a[15], dev)));
+        return pair(wrap(a[10], made_o), wrap(a[12], made_lse));
+    });
+}
+
 // (src, device, acc, table, lens, budget, dst, dst_acc, dst_table, sink, recent,
 //  keep, new_lens, status, stream)
 PyObject *evict(PyObject *, PyObject *const *a, Py_ssize_t n) {
@@ -379,7 +433,7 @@ PyObject *evict(PyObject *, PyObject *const *a, Py_ssize_t n) {
 
 // (QmvError, address of each entry point)
 PyObject *init(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    return guarded<6>(n, [&]() -> PyObject * {
+    return guarded<8>(n, [&]() -> PyObject * {
         Py_XDECREF(g_error);
         Py_INCREF(a[0]);
         g_error = a[0];
@@ -389,6 +443,8 @@ PyObject *init(PyObject *, PyObject *const *a, Py_ssize_t n) {
         take(g_norm_rope);
         take(g_tree);
         take(g_tree_ws);
+        take(g_window);
+        take(g_window_ws);
         take(g_evict);
         if (PyErr_Occurred()) throw Bad();
         Py_RETURN_NONE;
@@ -403,6 +459,7 @@ PyMethodDef methods[] = {{"init", fast(init), METH_FASTCALL, nullptr},
                          {"rope_append", fast(rope_append), METH_FASTCALL, nullptr},
                          {"norm_rope_append", fast(norm_rope_append), METH_FASTCALL, nullptr},
                          {"tree", fast(tree), METH_FASTCALL, nullptr},
+                         {"window", fast(window), METH_FASTCALL, nullptr},
                          {"evict", fast(evict), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_qmv_torch", nullptr, -1, methods};

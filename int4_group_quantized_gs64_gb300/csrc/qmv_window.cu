@@ -1,0 +1,97 @@
+// qmv_window.cu - causal attention of new tokens over a paged cache, with a
+// sliding window and a few first tokens that stay visible.
+//
+// The token at slot p sees the slots j <= p with j > p - window or j < sinks;
+//     x_j = scale * q . k_j,   o = sum_j exp(x_j - M) v_j / sum_j exp(x_j - M)
+// as in qmv_attn_tree.cu, whose kernels these are in their second form (kWin):
+// the rows of a key/value head are its tokens times G query heads, a block of
+// rows is an item, and its keys are the union of what its rows see, in two
+// stretches of units (Reach): those with first tokens, and those from the first
+// row's window to the last row's slot. Units that every row sees whole need no
+// mask; the others (the edges: at most 255 slots a side) are masked row by row.
+// Units are shared out evenly over the blocks, so a prompt's early rows (short
+// reach) and late ones, and sequences of any length, fill the GPU alike.
+//
+// Up to 16 rows a sequence: k_attn_rows (warp MMA, bound by the copy of keys
+// and values); more: k_attn_tc (tcgen05).
+#include <math.h>
+#include <string.h>
+
+#include "qmv_attn.cuh"
+#include "qmv_attn.h"
+#include "qmv_attn_join.cuh"
+#include "qmv_attn_plan.cuh"
+#include "qmv_attn_rows.cuh"
+#include "qmv_launch.cuh"
+
+namespace qmv {
+namespace attn {
+
+// Launches the tcgen05 kernel (qmv_attn_tc.cuh) for a.rows = 128 or 256.
+cudaError_t launch_window_tc(const AttnCache &c, const TreeArgs &a, cudaStream_t st);
+
+namespace {
+
+template <int D, bool kBf16>
+cudaError_t run_window(const AttnCache &c, const TreeArgs &a, cudaStream_t st) {
+    const bool few = a.rows == kRows;
+    cudaError_t e = few ? run_rows<D, kBf16, true>(c, a, st) : launch_window_tc(c, a, st);
+    const long long nrb = ((long long)a.max_rows + a.rows - 1) / a.rows;
+    if (e == cudaSuccess) e = run_join<D, kBf16, true>(a, !few, a.max_rows, nrb, st);
+    return e;
+}
+
+// Segments' sums, their maxima and sums of exponentials, and whose they are.
+size_t part_floats(const AttnCache &c, int rows) {
+    return (size_t)attn_grid_max(rows) * 2 * rows * (c.D + 2);
+}
+
+}  // namespace
+}  // namespace attn
+
+size_t attn_window_ws_bytes(const AttnCache &c, int Hq, int max_new) {
+    const int rows = attn::rows_an_item(max_new * (Hq / c.Hkv));
+    const size_t n = attn::part_floats(c, rows) * 4 + (size_t)attn::attn_grid_max(rows) * 2 * sizeof(attn::PartInfo);
+    return (n + 255) / 256 * 256;
+}
+
+cudaError_t launch_attn_window(const AttnCache &c, const WindowCall &t, cudaStream_t st) {
+    using namespace attn;
+    TreeArgs a;
+    memset(&a, 0, sizeof(a));
+    int lpage = 0;
+    while ((1 << lpage) < c.page) ++lpage;
+    a.s = Seqs{t.s.table, t.s.ctx, t.s.cu, t.s.B, t.s.N, t.s.max_draft, t.s.max_pages, c.page, lpage, 0};
+    a.q = static_cast<const uint16_t *>(t.q);
+    a.q_stride = t.q_stride;
+    a.Hq = t.Hq; a.Hkv = c.Hkv; a.G = t.Hq / c.Hkv; a.pages = c.pages;
+    a.ginv = (uint32_t)(((1ull << 32) + a.G - 1) / a.G);
+    a.sl2 = t.scale == 0.f ? 1.f : fabsf(t.scale) * kLog2e;
+    a.qxor = t.scale < 0.f ? 0x80008000u : 0u;
+    a.qand = t.scale == 0.f ? 0u : 0xFFFFFFFFu;
+    a.o = t.o; a.o_f32 = t.o_f32; a.lse = t.lse;
+    a.vpool = static_cast<const uint16_t *>(c.v);
+    a.status = t.status;
+    a.window = t.window; a.sinks = t.sinks;
+    a.max_rows = t.s.max_draft * a.G;
+    a.rows = rows_an_item(a.max_rows);
+    a.unit = a.rows == kRows ? kWarps * 16 * (128 / c.D) : 128;  // keys a unit
+    while ((1 << a.lunit) < a.unit) ++a.lunit;
+    // units at most: the blocks of rows of N tokens (or of B sequences at their
+    // bound), each over a whole table row
+    const long long nrb = ((long long)a.max_rows + a.rows - 1) / a.rows;
+    long long items = t.s.B * nrb;
+    const long long by_n = (long long)t.s.N * a.G / a.rows + t.s.B;
+    if (by_n < items) items = by_n;
+    const long long most = items * c.Hkv * (((((long long)t.s.max_pages << lpage) + a.unit - 1) >> a.lunit) + 1);
+    const int gmax = attn_grid_max(a.rows);
+    if (most / gmax >= 0x7FFFFFFFLL) return cudaErrorInvalidValue;  // a block's units fit 31 bits
+    a.grid = most < gmax ? (int)most : gmax;
+    a.part_o = static_cast<float *>(t.ws);
+    a.part_ml = a.part_o + (size_t)gmax * 2 * a.rows * c.D;
+    a.info = reinterpret_cast<PartInfo *>(a.part_o + part_floats(c, a.rows));
+    if (c.D == 64) return c.bf16 ? run_window<64, true>(c, a, st) : run_window<64, false>(c, a, st);
+    return c.bf16 ? run_window<128, true>(c, a, st) : run_window<128, false>(c, a, st);
+}
+
+}  // namespace qmv

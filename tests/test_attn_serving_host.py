@@ -32,7 +32,16 @@ def norm(L, d=None, **kw):
                                    a["ctx"], a["cu"], a["B"], a["N"], a["out"], a["acc"], a["st"], None)
 
 
-CACHE_CALLS = {"norm": norm}
+def window(L, d=None, **kw):
+    a = dict(q=P, qs=256, Hq=4, table=P, mp=4, ctx=P, cu=P, B=2, N=3, T=2, W=9, S=1, scale=0.1, o=P, ot=1,
+             lse=P, st=None, ws=P, wb=1 << 40)
+    a.update(kw)
+    return L.attn_window(ctypes.byref(d or desc()), a["q"], a["qs"], a["Hq"], a["table"], a["mp"], a["ctx"],
+                         a["cu"], a["B"], a["N"], a["T"], a["W"], a["S"], a["scale"], a["o"], a["ot"],
+                         a["lse"], a["st"], a["ws"], a["wb"], None)
+
+
+CACHE_CALLS = {"norm": norm, "window": window}
 
 
 @pytest.mark.parametrize("call", CACHE_CALLS.values(), ids=CACHE_CALLS.keys())
@@ -68,3 +77,28 @@ def test_norm(L):
     assert norm(L, qw=odd1, wt=1) == EALIGN and norm(L, kw=odd1, wt=1) == EALIGN
     for k in ("pos", "table", "ctx", "cu", "acc", "st"):
         assert norm(L, **{k: ODD}) == EALIGN, k
+
+
+def test_window(L):
+    for k in ("q", "table", "ctx", "cu", "o", "lse"):
+        assert window(L, **{k: None}) == EINVAL, k
+    assert window(L, N=-1) == EINVAL and window(L, N=0) == 0 and window(L, N=(1 << 22) + 1) == ESHAPE
+    assert window(L, Hq=3) == EINVAL and window(L, T=0) == EINVAL and window(L, T=(1 << 22) + 1) == ESHAPE
+    assert window(L, T=1 << 22, Hq=1024, qs=1 << 20) == ESHAPE       # 2^22 * 512 rows
+    assert window(L, W=0) == EINVAL and window(L, W=-5) == EINVAL and window(L, S=-1) == EINVAL
+    assert window(L, scale=float("nan")) == EINVAL and window(L, scale=float("inf")) == EINVAL
+    assert window(L, ot=2) == EINVAL and window(L, ot=9) == EINVAL
+    assert window(L, qs=255) == ESHAPE and window(L, qs=260) == EALIGN
+    for k in ("q", "o"):
+        assert window(L, **{k: ctypes.c_void_p(FAKE + 8)}) == EALIGN, k
+    for k in ("table", "ctx", "cu", "lse", "st"):
+        assert window(L, **{k: ODD}) == EALIGN, k
+    d = desc()
+    for T in (2, 100, 1 << 20):
+        need = L.attn_window_workspace_bytes(ctypes.byref(d), 4, 2, 3, T, 4)
+        assert need > 0 and need % 256 == 0
+        assert window(L, T=T, ws=None) == EWORKSPACE and window(L, T=T, wb=need - 1) == EWORKSPACE
+        assert window(L, T=T, ws=ctypes.c_void_p(FAKE + 128)) == EWORKSPACE
+    assert L.attn_window_workspace_bytes(ctypes.byref(desc(D=96)), 4, 2, 3, 2, 4) == 0
+    assert L.attn_window_workspace_bytes(ctypes.byref(d), 3, 2, 3, 2, 4) == 0
+    assert L.attn_window_workspace_bytes(ctypes.byref(d), 4, 2, 3, 0, 4) == 0
