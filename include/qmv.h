@@ -560,6 +560,87 @@ int attn_evict(const qmv_attn_cache *src, const float *acc, const int32_t *table
                int dst_max_pages, int32_t *keep, int32_t *new_lens, int32_t *status,
                qmv_stream_t stream);
 
+/* ---------------------------------------------------------------- pages
+ *
+ * The upkeep of a cache's pages, for page tables as the attention calls take
+ * them. refs [pages] int32 counts the table entries that hold a page (0: it is
+ * free); a program starts with zeros and tables of -1 and lets the calls below
+ * keep both. One pool of pages serves the caches of all layers that use the same
+ * table. Everything is on the device and stream-ordered, so a captured step can
+ * take and give back pages.
+ *   table  [n][max_pages] int32, page of each `page` tokens; below 0: none
+ *   page   16, 32, 64, 128 or 256; pages <= 2^30; n <= 65535;
+ *          max_pages * page <= 2^30; n * max_pages < 2^31
+ *   status [1] int32 or NULL, OR-ed with
+ *            1  an id past the pool in an entry, or a page given back that nobody
+ *               held: that entry is left out;
+ *            2  lengths (or a parent) that are negative or do not fit: that row is
+ *               left as it is (attn_pages_fork: the child is empty);
+ *            8  no free page was left for some entry.
+ *   ws     at least the bytes that the call's workspace function says, 256-byte
+ *          aligned, not shared with a concurrent call. */
+
+size_t attn_pages_update_workspace_bytes(int pages, int B, int max_pages);
+
+/* Makes each row of a table hold the pages that its sequence needs, and no others.
+ * Sequence b has lens[b] tokens in the cache and is to take more[b] (0 and 0: it is
+ * over). With the window and sinks of attn_window, page i is needed when
+ *     i * page < lens + more   and
+ *     (i * page < sinks  or  (i + 1) * page > lens - window + 1)
+ * that is, when it has or will have tokens that a token to come (at slot lens or
+ * later) sees. Entries that are not needed give their pages back and become -1;
+ * then the needed ones that are below 0 take the lowest free pages, in the order
+ * of the sequences and of their entries (a page given back in this call can be
+ * taken in it). When the free ones run out the rest stay below 0 (status 8).
+ * Tokens are to be appended only to pages that their sequence holds alone:
+ * attn_pages_fork leaves it so; a sequence that is cut back into a page it shares
+ * is forked (from itself) first.
+ *   refs, table  updated in place; window >= 1 (INT32_MAX: none), sinks >= 0 */
+int attn_pages_update(int32_t *refs, int pages, int page, int32_t *table, int max_pages,
+                      const int32_t *lens, const int32_t *more, int B, int window, int sinks,
+                      int32_t *status, void *ws, size_t ws_bytes, qmv_stream_t stream);
+
+size_t attn_pages_fork_workspace_bytes(int pages, int F);
+
+/* F children of sequences: child f begins as parent[f] (0 .. B - 1) is, lens tokens
+ * long. Whole pages are shared (their refs grow); a last page that is partly filled
+ * is replaced by the lowest free page, and moves[f] says what to copy to it:
+ * (page to copy from, page to copy to, tokens), or (-1, -1, 0). attn_pages_copy
+ * copies it, in each layer's cache. A child for which no page is left (status 8) is
+ * as long as its whole pages. Parents keep what they hold until attn_pages_update
+ * takes it back.
+ *   new_table [F][max_pages], new_lens [F], moves [F][3] int32 (written); not the
+ *   parents' own arrays */
+int attn_pages_fork(int32_t *refs, int pages, int page, const int32_t *table, int max_pages,
+                    const int32_t *lens, int B, const int32_t *parent, int F, int32_t *new_table,
+                    int32_t *new_lens, int32_t *moves, int32_t *status, void *ws, size_t ws_bytes,
+                    qmv_stream_t stream);
+
+/* Copies the first tokens of pages, keys and values of all heads: moves [n][3]
+ * int32, (page of src, page of dst, tokens); a move with a page below 0 or without
+ * tokens is none. dst may be src or another cache with the same heads, page and
+ * dtype (and any number of pages). No page is the source of one move and the
+ * destination of another, or the destination of two. Pages past a pool are left
+ * out (status 1), token counts outside 0 .. page too (status 2).
+ *   src_acc, dst_acc  running attention weights [pages][Hkv][page] or NULL: with
+ *     dst_acc alone the copies' weights are cleared */
+int attn_pages_copy(const qmv_attn_cache *src, const qmv_attn_cache *dst, const int32_t *moves, int n,
+                    const float *src_acc, float *dst_acc, int32_t *status, qmv_stream_t stream);
+
+/* Keeps some of each sequence's new tokens (the accepted ones of a tree of drafts):
+ * token keep[cu[b] + i], counted from the sequence's first new one, moves to slot
+ * ctx[b] + i, i < kept[b], in all heads, with its running weights where acc is
+ * given; new_ctx[b] = ctx[b] + kept[b]. The kept ones are in strictly ascending
+ * order (a path's drafts are). table, ctx, cu as in the attention calls; the pages
+ * of new tokens belong to one sequence. A sequence whose lengths do not fit, or
+ * whose kept tokens are not ascending or not its own, stays as it is
+ * (status 2); moves from or to pages past the pool are left out (status 1).
+ *   keep [N] int32, kept [B] int32; acc [pages][Hkv][page] or NULL (in place)
+ *   new_ctx [B] int32 (written), not ctx itself */
+int attn_compact(const qmv_attn_cache *c, const int32_t *table, int max_pages, const int32_t *ctx,
+                 const int32_t *cu, int B, int N, const int32_t *keep, const int32_t *kept, float *acc,
+                 int32_t *new_ctx, int32_t *status, qmv_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -11,7 +11,8 @@ forms ``qmv_int4_gs_bf16`` and ``qmv_int8_row_bf16``,
 ``moe_route_topk``, ``moe_group``, ``moe_gate_up_silu``, ``moe_down``,
 ``moe_combine``, ``moe_workspace_bytes``, ``moe_expert_ffn_int4`` and
 ``moe_expert_ffn_int4_prefill``; ``attn_rope_append``, ``attn_norm_rope_append``,
-``attn_tree``, ``attn_window`` and ``attn_evict`` over a paged cache (``AttnCache``).
+``attn_tree``, ``attn_window``, ``attn_evict`` and ``attn_compact`` over a paged cache (``AttnCache``), and ``attn_pages_update``, ``attn_pages_fork`` and
+``attn_pages_copy`` for its pages.
 """
 from __future__ import annotations
 
@@ -108,6 +109,13 @@ def lib():
                              vp, vp, vp, sz, vp], i32),
             "attn_evict": ([C, vp, vp, i32, vp, i32, i32, i32, i32, C, vp, vp, i32, vp, vp, vp, vp],
                            i32),
+            "attn_pages_update_workspace_bytes": ([i32, i32, i32], sz),
+            "attn_pages_update": ([vp, i32, i32, vp, i32, vp, vp, i32, i32, i32, vp, vp, sz, vp], i32),
+            "attn_pages_fork_workspace_bytes": ([i32, i32], sz),
+            "attn_pages_fork": ([vp, i32, i32, vp, i32, vp, i32, vp, i32, vp, vp, vp, vp, vp, sz, vp],
+                                i32),
+            "attn_pages_copy": ([C, C, vp, i32, vp, vp, vp, vp], i32),
+            "attn_compact": ([C, vp, i32, vp, vp, i32, i32, vp, vp, vp, vp, vp, vp], i32),
         }
         for name, (args, res) in sig.items():
             if hasattr(L, name):
@@ -520,7 +528,9 @@ def _torch_binding():
         L = lib()
         mod.init(QmvError, *(ctypes.cast(getattr(L, f), ctypes.c_void_p).value for f in (
             "attn_rope_append", "attn_norm_rope_append", "attn_tree", "attn_tree_workspace_bytes", "attn_window",
-            "attn_window_workspace_bytes", "attn_evict")))
+            "attn_window_workspace_bytes", "attn_evict", "attn_pages_update",
+            "attn_pages_update_workspace_bytes", "attn_pages_fork", "attn_pages_fork_workspace_bytes",
+            "attn_pages_copy", "attn_compact")))
         _torch_mod = mod
     return _torch_mod
 
@@ -696,3 +706,81 @@ def attn_evict(src: AttnCache, acc, table, lens, budget: int, dst: AttnCache, ds
     return (_torch_mod or _torch_binding()).evict(
         src.address, src.device_index, acc, table, lens, budget, dst.address, dst_acc, dst_table,
         sink, recent, keep, new_lens, status, handle)
+
+
+# ------------------------------------------------------------------ pages
+
+def attn_pages_update_workspace_bytes(pages: int, B: int, max_pages: int) -> int:
+    return int(lib().attn_pages_update_workspace_bytes(pages, B, max_pages))
+
+
+def attn_pages_update(refs, table, lens, more, page: int, window=None, sinks: int = 0, ws=None,
+                      status=None, stream=None):
+    """Makes each row of the table hold the pages its sequence needs, and no others (in place).
+
+    refs int32 [pages] counts the entries that hold a page (0: free); table int32 [B][max_pages]
+    (below 0: none); lens and more int32 [B]: tokens in the cache, and tokens to come (0 and 0:
+    the sequence is over). Pages behind the window (None: no window) and past the first `sinks`
+    tokens are given back; missing ones are the lowest free pages, in the order of the entries."""
+    handle = None
+    if stream is not None:
+        import torch
+        handle = stream.cuda_stream
+        if ws is None:
+            ws = _on(stream, max(256, attn_pages_update_workspace_bytes(
+                refs.shape[0], table.shape[0], table.shape[1])), torch.uint8, refs.device)
+    (_torch_mod or _torch_binding()).pages_update(
+        refs, table, lens, more, page, _ALL if window is None else window, sinks, ws, status, handle)
+
+
+def attn_pages_fork_workspace_bytes(pages: int, F: int) -> int:
+    return int(lib().attn_pages_fork_workspace_bytes(pages, F))
+
+
+def attn_pages_fork(refs, table, lens, parent, page: int, new_table=None, new_lens=None, moves=None,
+                    ws=None, status=None, stream=None):
+    """Children of sequences (parent int32 [F], rows of the table): whole pages are shared, a partly
+    filled last page is replaced by a fresh one.
+
+    Returns (new_table [F][max_pages], new_lens [F], moves [F][3]); attn_pages_copy makes the moves,
+    in each layer's cache."""
+    handle = None
+    if stream is not None:
+        import torch
+        handle = stream.cuda_stream
+        F = parent.shape[0]
+        if new_table is None:
+            new_table = _on(stream, (F, table.shape[1]), torch.int32, refs.device)
+        if new_lens is None:
+            new_lens = _on(stream, (F,), torch.int32, refs.device)
+        if moves is None:
+            moves = _on(stream, (F, 3), torch.int32, refs.device)
+        if ws is None:
+            ws = _on(stream, max(256, attn_pages_fork_workspace_bytes(refs.shape[0], F)), torch.uint8,
+                     refs.device)
+    return (_torch_mod or _torch_binding()).pages_fork(
+        refs, table, lens, parent, page, new_table, new_lens, moves, ws, status, handle)
+
+
+def attn_pages_copy(src: AttnCache, dst: AttnCache, moves, src_acc=None, dst_acc=None, status=None,
+                    stream=None):
+    """Copies the first tokens of pages: moves int32 [n][3], (page of src, page of dst, tokens)."""
+    if dst.device_index != src.device_index:
+        raise ValueError("src and dst must be on one device")
+    (_torch_mod or _torch_binding()).pages_copy(
+        src.address, dst.address, src.device_index, moves, src_acc, dst_acc, status,
+        None if stream is None else stream.cuda_stream)
+
+
+def attn_compact(cache: AttnCache, table, ctx, cu, keep, kept, acc=None, new_ctx=None, status=None,
+                 stream=None):
+    """Keeps some of each sequence's new tokens: token keep[cu[b] + i], counted from its first new
+    one, moves to slot ctx[b] + i for i < kept[b] (ascending); returns the new lengths int32 [B]."""
+    handle = None
+    if stream is not None:
+        import torch
+        handle = stream.cuda_stream
+        if new_ctx is None:
+            new_ctx = _on(stream, ctx.shape, torch.int32, cache.device)
+    return (_torch_mod or _torch_binding()).compact(
+        cache.address, cache.device_index, table, ctx, cu, keep, kept, acc, new_ctx, status, handle)

@@ -81,4 +81,20 @@ cudaError_t launch_attn_evict(const AttnCache &src, const float *acc, const int3
                               const int32_t *dst_table, int dst_max_pages, int32_t *keep,
                               int32_t *new_lens, int32_t *status, cudaStream_t st);
 
+// Pages: page = tokens a page. (qmv_pages.cu)
+size_t pages_update_ws_bytes(int pages, int B, int max_pages);
+cudaError_t launch_pages_update(int32_t *refs, int pages, int page, int32_t *table, int max_pages,
+                                const int32_t *lens, const int32_t *more, int B, int window, int sinks,
+                                int32_t *status, void *ws, cudaStream_t st);
+size_t pages_fork_ws_bytes(int pages, int F);
+cudaError_t launch_pages_fork(int32_t *refs, int pages, int page, const int32_t *table, int max_pages,
+                              const int32_t *lens, int B, const int32_t *parent, int F,
+                              int32_t *new_table, int32_t *new_lens, int32_t *moves, int32_t *status,
+                              void *ws, cudaStream_t st);
+cudaError_t launch_pages_copy(const AttnCache &src, const AttnCache &dst, const int32_t *moves, int n,
+                              const float *src_acc, float *dst_acc, int32_t *status, cudaStream_t st);
+cudaError_t launch_attn_compact(const AttnCache &c, const AttnSeqs &s, const int32_t *keep,
+                                const int32_t *kept, float *acc, int32_t *new_ctx, int32_t *status,
+                                cudaStream_t st);
+
 }  // namespace qmv

@@ -16,11 +16,13 @@ inline bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintp
 inline cudaStream_t cs(qmv_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 inline int from_cuda(cudaError_t e) { return e == cudaSuccess ? QMV_OK : QMV_ECUDA; }
 
+bool page_ok(int page) { return page >= 16 && page <= 256 && !(page & (page - 1)); }
+
 int check_cache(const qmv_attn_cache *c) {
     if (!c || !c->k || !c->v || c->pages < 1 || c->Hkv < 1 || c->Hkv > kMaxHeads) return QMV_EINVAL;
     if (c->dtype != QMV_BF16 && c->dtype != QMV_F16) return QMV_EINVAL;
     if (c->D != 64 && c->D != 128) return QMV_ESHAPE;
-    if (c->page < 16 || c->page > 256 || (c->page & (c->page - 1))) return QMV_ESHAPE;
+    if (!page_ok(c->page)) return QMV_ESHAPE;
     if ((int64_t)c->pages * c->Hkv * c->page >= (int64_t)1 << 31) return QMV_ESHAPE;
     if (!aligned(c->k, 16) || !aligned(c->v, 16)) return QMV_EALIGN;
     return QMV_OK;
@@ -45,6 +47,15 @@ bool heads_ok(const qmv_attn_cache *c, int Hq) {
 // A bound of a sequence's new tokens: its rows a key/value head are counted in 31 bits.
 bool new_ok(const qmv_attn_cache *c, int Hq, int max_new) {
     return max_new >= 1 && max_new <= 1 << 22 && (int64_t)max_new * (Hq / c->Hkv) <= (int64_t)1 << 30;
+}
+
+// A pool of pages and a table of n rows.
+int check_pages(int pages, int page, int n, int max_pages) {
+    if (pages < 1 || n < 0 || max_pages < 1) return QMV_EINVAL;
+    if (!page_ok(page) || pages > 1 << 30 || n > 65535 || (int64_t)max_pages * page > (int64_t)1 << 30 ||
+        (int64_t)n * max_pages > INT32_MAX)
+        return QMV_ESHAPE;
+    return QMV_OK;
 }
 
 // Both rotary appends; norm null: without norms.
@@ -210,6 +221,83 @@ int attn_evict(const qmv_attn_cache *src, const float *acc, const int32_t *table
     return from_cuda(qmv::launch_attn_evict(cache(src), acc, table, max_pages, lens, B, budget,
                                             sink, recent, cache(dst), dst_acc, dst_table,
                                             dst_max_pages, keep, new_lens, status, cs(stream)));
+}
+
+size_t attn_pages_update_workspace_bytes(int pages, int B, int max_pages) {
+    return check_pages(pages, 16, B, max_pages) ? 0 : qmv::pages_update_ws_bytes(pages, B, max_pages);
+}
+
+int attn_pages_update(int32_t *refs, int pages, int page, int32_t *table, int max_pages,
+                      const int32_t *lens, const int32_t *more, int B, int window, int sinks,
+                      int32_t *status, void *ws, size_t ws_bytes, qmv_stream_t stream) {
+    const int r = check_pages(pages, page, B, max_pages);
+    if (r) return r;
+    if (window < 1 || sinks < 0) return QMV_EINVAL;
+    if (B == 0) return QMV_OK;
+    if (!refs || !table || !lens || !more) return QMV_EINVAL;
+    if (!aligned(refs, 4) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(more, 4) ||
+        !aligned(status, 4))
+        return QMV_EALIGN;
+    if (!ws || !aligned(ws, 256) || ws_bytes < qmv::pages_update_ws_bytes(pages, B, max_pages))
+        return QMV_EWORKSPACE;
+    return from_cuda(qmv::launch_pages_update(refs, pages, page, table, max_pages, lens, more, B,
+                                              window, sinks, status, ws, cs(stream)));
+}
+
+size_t attn_pages_fork_workspace_bytes(int pages, int F) {
+    return check_pages(pages, 16, F, 1) ? 0 : qmv::pages_fork_ws_bytes(pages, F);
+}
+
+int attn_pages_fork(int32_t *refs, int pages, int page, const int32_t *table, int max_pages,
+                    const int32_t *lens, int B, const int32_t *parent, int F, int32_t *new_table,
+                    int32_t *new_lens, int32_t *moves, int32_t *status, void *ws, size_t ws_bytes,
+                    qmv_stream_t stream) {
+    int r = check_pages(pages, page, B, max_pages);
+    if (r || (r = check_pages(pages, page, F, max_pages))) return r;
+    if (F == 0) return QMV_OK;
+    if (!refs || !table || !lens || !parent || !new_table || !new_lens || !moves) return QMV_EINVAL;
+    if (new_table == table || new_lens == lens) return QMV_EINVAL;  // children read their parents' rows
+    if (!aligned(refs, 4) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(parent, 4) ||
+        !aligned(new_table, 4) || !aligned(new_lens, 4) || !aligned(moves, 4) || !aligned(status, 4))
+        return QMV_EALIGN;
+    if (!ws || !aligned(ws, 256) || ws_bytes < qmv::pages_fork_ws_bytes(pages, F))
+        return QMV_EWORKSPACE;
+    return from_cuda(qmv::launch_pages_fork(refs, pages, page, table, max_pages, lens, B, parent, F,
+                                            new_table, new_lens, moves, status, ws, cs(stream)));
+}
+
+int attn_pages_copy(const qmv_attn_cache *src, const qmv_attn_cache *dst, const int32_t *moves, int n,
+                    const float *src_acc, float *dst_acc, int32_t *status, qmv_stream_t stream) {
+    int r = check_cache(src);
+    if (r) return r;
+    if ((r = check_cache(dst))) return r;
+    if (src->Hkv != dst->Hkv || src->D != dst->D || src->dtype != dst->dtype || src->page != dst->page)
+        return QMV_ESHAPE;
+    if (n < 0 || (src_acc && !dst_acc)) return QMV_EINVAL;
+    if ((int64_t)n * src->Hkv > INT32_MAX) return QMV_ESHAPE;
+    if (n == 0) return QMV_OK;
+    if (!moves) return QMV_EINVAL;
+    if (!aligned(moves, 4) || !aligned(src_acc, 4) || !aligned(dst_acc, 4) || !aligned(status, 4))
+        return QMV_EALIGN;
+    return from_cuda(qmv::launch_pages_copy(cache(src), cache(dst), moves, n, src_acc, dst_acc, status,
+                                            cs(stream)));
+}
+
+int attn_compact(const qmv_attn_cache *c, const int32_t *table, int max_pages, const int32_t *ctx,
+                 const int32_t *cu, int B, int N, const int32_t *keep, const int32_t *kept, float *acc,
+                 int32_t *new_ctx, int32_t *status, qmv_stream_t stream) {
+    int r = check_cache(c);
+    if (r) return r;
+    if ((r = check_batch(c, B, max_pages))) return r;
+    if (N < 0) return QMV_EINVAL;
+    if (B == 0) return QMV_OK;
+    if (!table || !ctx || !cu || (!keep && N) || !kept || !new_ctx) return QMV_EINVAL;
+    if (new_ctx == ctx) return QMV_EINVAL;  // other blocks still read ctx
+    if (!aligned(table, 4) || !aligned(ctx, 4) || !aligned(cu, 4) || !aligned(keep, 4) ||
+        !aligned(kept, 4) || !aligned(acc, 4) || !aligned(new_ctx, 4) || !aligned(status, 4))
+        return QMV_EALIGN;
+    return from_cuda(qmv::launch_attn_compact(cache(c), qmv::AttnSeqs{table, ctx, cu, B, N, 0, max_pages},
+                                              keep, kept, acc, new_ctx, status, cs(stream)));
 }
 
 }  // extern "C"

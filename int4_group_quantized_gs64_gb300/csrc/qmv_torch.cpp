@@ -25,6 +25,12 @@ decltype(&attn_tree_workspace_bytes) g_tree_ws;
 decltype(&attn_window) g_window;
 decltype(&attn_window_workspace_bytes) g_window_ws;
 decltype(&attn_evict) g_evict;
+decltype(&attn_pages_update) g_update;
+decltype(&attn_pages_update_workspace_bytes) g_update_ws;
+decltype(&attn_pages_fork) g_fork;
+decltype(&attn_pages_fork_workspace_bytes) g_fork_ws;
+decltype(&attn_pages_copy) g_copy;
+decltype(&attn_compact) g_compact;
 PyObject *g_error;  // QmvError(name, status)
 
 struct Bad : std::exception {};  // a Python error is set
@@ -53,7 +59,7 @@ const at::Tensor &tensor(PyObject *o, at::ScalarType t, int device, const char *
     if (!THPVariable_Check(o)) type_error(name, name_of(t));
     const at::Tensor &x = THPVariable_Unpack(o);
     if (!x.is_cuda() || x.scalar_type() != t) type_error(name, name_of(t));
-    if (device >= 0 && x.get_device() != device) value_error(name, "on the cache's device");
+    if (device >= 0 && x.get_device() != device) value_error(name, "on the device of the call's cache or pages");
     return x;
 }
 
@@ -431,9 +437,135 @@ PyObject *evict(PyObject *, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
+// The counts of a pool's pages: their number, and the device that they are on.
+struct Refs {
+    int32_t *p;
+    int pages, device;
+};
+Refs refs(PyObject *o) {
+    const at::Tensor &x = tensor(o, at::kInt, -1, "refs");
+    if (x.dim() != 1 || !x.is_contiguous()) value_error("refs", "[pages] and contiguous");
+    if (x.size(0) > INT32_MAX) value_error("refs", "smaller");
+    return Refs{x.data_ptr<int32_t>(), (int)x.size(0), (int)x.get_device()};
+}
+// A given workspace, or one made for the call.
+struct Workspace {
+    at::Tensor made;
+    void *p;
+    size_t bytes;
+    Workspace(PyObject *o, size_t want, int device) {
+        if (o == Py_None) {
+            bytes = want < 256 ? 256 : want;
+            made = make({(int64_t)bytes}, at::kByte, device);
+            p = made.data_ptr();
+        } else {
+            p = addr(o, at::kByte, -1, device, "ws");
+            bytes = (size_t)THPVariable_Unpack(o).numel();
+        }
+    }
+};
+// A given int32 output of this many elements, or one made with this shape.
+struct Out {
+    at::Tensor made;
+    int32_t *p;
+    Out(PyObject *o, at::IntArrayRef shape, int device, const char *name) {
+        int64_t n = 1;
+        for (const int64_t d : shape) n *= d;
+        if (o == Py_None) {
+            made = make(shape, at::kInt, device);
+            p = made.data_ptr<int32_t>();
+        } else {
+            p = static_cast<int32_t *>(addr(o, at::kInt, n, device, name));
+        }
+    }
+};
+
+// (refs, table, lens, more, page, window, sinks, ws, status, stream)
+PyObject *pages_update(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded<10>(n, [&]() -> PyObject * {
+        const Refs r = refs(a[0]);
+        const Device dev(r.device);
+        const Table t = table(a[1], dev, "table");
+        const auto *lens = static_cast<const int32_t *>(addr(a[2], at::kInt, t.B, dev, "lens"));
+        const auto *more = static_cast<const int32_t *>(addr(a[3], at::kInt, t.B, dev, "more"));
+        const int page = as_int(a[4]), win = as_int(a[5]), sinks = as_int(a[6]);
+        const Workspace ws(a[7], g_update_ws(r.pages, t.B, t.width), dev);
+        void *status = opt(a[8], at::kInt, 1, dev, "status");
+        check("attn_pages_update",
+              g_update(r.p, r.pages, page, const_cast<int32_t *>(t.p), t.width, lens, more, t.B, win,
+                       sinks, static_cast<int32_t *>(status), ws.p, ws.bytes, as_stream(a[9], dev)));
+        Py_RETURN_NONE;
+    });
+}
+
+// (refs, table, lens, parent, page, new_table, new_lens, moves, ws, status, stream)
+PyObject *pages_fork(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded<11>(n, [&]() -> PyObject * {
+        const Refs r = refs(a[0]);
+        const Device dev(r.device);
+        const Table t = table(a[1], dev, "table");
+        const auto *lens = static_cast<const int32_t *>(addr(a[2], at::kInt, t.B, dev, "lens"));
+        const auto *parent = static_cast<const int32_t *>(addr(a[3], at::kInt, -1, dev, "parent"));
+        const int64_t F = THPVariable_Unpack(a[3]).numel();
+        if (F > INT32_MAX) value_error("parent", "smaller");
+        const int page = as_int(a[4]);
+        const Out table2(a[5], {F, t.width}, dev, "new_table"), lens2(a[6], {F}, dev, "new_lens"),
+            moves(a[7], {F, 3}, dev, "moves");
+        const Workspace ws(a[8], g_fork_ws(r.pages, (int)F), dev);
+        void *status = opt(a[9], at::kInt, 1, dev, "status");
+        check("attn_pages_fork",
+              g_fork(r.p, r.pages, page, t.p, t.width, lens, t.B, parent, (int)F, table2.p, lens2.p,
+                     moves.p, static_cast<int32_t *>(status), ws.p, ws.bytes, as_stream(a[10], dev)));
+        PyObject *x = wrap(a[5], table2.made), *y = wrap(a[6], lens2.made), *z = wrap(a[7], moves.made);
+        PyObject *res = x && y && z ? PyTuple_Pack(3, x, y, z) : nullptr;
+        Py_XDECREF(x);
+        Py_XDECREF(y);
+        Py_XDECREF(z);
+        return res;
+    });
+}
+
+// (src, dst, device, moves, src_acc, dst_acc, status, stream)
+PyObject *pages_copy(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded<8>(n, [&]() -> PyObject * {
+        const qmv_attn_cache *s = as_cache(a[0]), *d = as_cache(a[1]);
+        const Device dev(as_int(a[2]));
+        const at::Tensor &m = tensor(a[3], at::kInt, dev, "moves");
+        if (m.dim() != 2 || m.size(1) != 3 || !m.is_contiguous()) value_error("moves", "[n][3] and contiguous");
+        if (m.size(0) > INT32_MAX) value_error("moves", "smaller");
+        const auto *sacc = static_cast<const float *>(opt(a[4], at::kFloat, slots(s), dev, "src_acc"));
+        auto *dacc = static_cast<float *>(opt(a[5], at::kFloat, slots(d), dev, "dst_acc"));
+        void *status = opt(a[6], at::kInt, 1, dev, "status");
+        check("attn_pages_copy", g_copy(s, d, m.data_ptr<int32_t>(), (int)m.size(0), sacc, dacc,
+                                        static_cast<int32_t *>(status), as_stream(a[7], dev)));
+        Py_RETURN_NONE;
+    });
+}
+
+// (cache, device, table, ctx, cu, keep, kept, acc, new_ctx, status, stream)
+PyObject *compact(PyObject *, PyObject *const *a, Py_ssize_t n) {
+    return guarded<11>(n, [&]() -> PyObject * {
+        const qmv_attn_cache *c = as_cache(a[0]);
+        const Device dev(as_int(a[1]));
+        const Table t = table(a[2], dev, "table");
+        const auto *ctx = static_cast<const int32_t *>(addr(a[3], at::kInt, t.B, dev, "ctx"));
+        const auto *cu = static_cast<const int32_t *>(addr(a[4], at::kInt, t.B + 1, dev, "cu"));
+        const auto *keep = static_cast<const int32_t *>(addr(a[5], at::kInt, -1, dev, "keep"));
+        const int64_t N = THPVariable_Unpack(a[5]).numel();
+        if (N > INT32_MAX) value_error("keep", "smaller");
+        const auto *kept = static_cast<const int32_t *>(addr(a[6], at::kInt, t.B, dev, "kept"));
+        auto *acc = static_cast<float *>(opt(a[7], at::kFloat, slots(c), dev, "acc"));
+        const Out now(a[8], {t.B}, dev, "new_ctx");
+        void *status = opt(a[9], at::kInt, 1, dev, "status");
+        check("attn_compact", g_compact(c, t.p, t.width, ctx, cu, t.B, (int)N, keep, kept, acc, now.p,
+                                        static_cast<int32_t *>(status), as_stream(a[10], dev)));
+        return wrap(a[8], now.made);
+    });
+}
+
 // (QmvError, address of each entry point)
 PyObject *init(PyObject *, PyObject *const *a, Py_ssize_t n) {
-    return guarded<8>(n, [&]() -> PyObject * {
+    return guarded<14>(n, [&]() -> PyObject * {
         Py_XDECREF(g_error);
         Py_INCREF(a[0]);
         g_error = a[0];
@@ -446,6 +578,12 @@ PyObject *init(PyObject *, PyObject *const *a, Py_ssize_t n) {
         take(g_window);
         take(g_window_ws);
         take(g_evict);
+        take(g_update);
+        take(g_update_ws);
+        take(g_fork);
+        take(g_fork_ws);
+        take(g_copy);
+        take(g_compact);
         if (PyErr_Occurred()) throw Bad();
         Py_RETURN_NONE;
     });
@@ -461,6 +599,10 @@ PyMethodDef methods[] = {{"init", fast(init), METH_FASTCALL, nullptr},
                          {"tree", fast(tree), METH_FASTCALL, nullptr},
                          {"window", fast(window), METH_FASTCALL, nullptr},
                          {"evict", fast(evict), METH_FASTCALL, nullptr},
+                         {"pages_update", fast(pages_update), METH_FASTCALL, nullptr},
+                         {"pages_fork", fast(pages_fork), METH_FASTCALL, nullptr},
+                         {"pages_copy", fast(pages_copy), METH_FASTCALL, nullptr},
+                         {"compact", fast(compact), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_qmv_torch", nullptr, -1, methods};
 

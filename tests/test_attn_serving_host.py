@@ -41,7 +41,15 @@ def window(L, d=None, **kw):
                          a["lse"], a["st"], a["ws"], a["wb"], None)
 
 
-CACHE_CALLS = {"norm": norm, "window": window}
+def compact(L, d=None, **kw):
+    a = dict(table=P, mp=4, ctx=P, cu=P, B=2, N=3, keep=P, kept=P, acc=None, out=ctypes.c_void_p(FAKE + 64),
+             st=None)
+    a.update(kw)
+    return L.attn_compact(ctypes.byref(d or desc()), a["table"], a["mp"], a["ctx"], a["cu"], a["B"], a["N"],
+                          a["keep"], a["kept"], a["acc"], a["out"], a["st"], None)
+
+
+CACHE_CALLS = {"norm": norm, "window": window, "compact": compact}
 
 
 @pytest.mark.parametrize("call", CACHE_CALLS.values(), ids=CACHE_CALLS.keys())
@@ -102,3 +110,81 @@ def test_window(L):
     assert L.attn_window_workspace_bytes(ctypes.byref(desc(D=96)), 4, 2, 3, 2, 4) == 0
     assert L.attn_window_workspace_bytes(ctypes.byref(d), 3, 2, 3, 2, 4) == 0
     assert L.attn_window_workspace_bytes(ctypes.byref(d), 4, 2, 3, 0, 4) == 0
+
+
+def test_compact(L):
+    for k in ("table", "ctx", "cu", "keep", "kept", "out"):
+        assert compact(L, **{k: None}) == EINVAL, k
+    assert compact(L, N=-1) == EINVAL
+    assert compact(L, out=P) == EINVAL             # onto ctx
+    for k in ("table", "ctx", "cu", "keep", "kept", "acc", "out", "st"):
+        assert compact(L, **{k: ODD}) == EALIGN, k
+
+
+def update(L, **kw):
+    a = dict(refs=P, pages=8, page=16, table=P, mp=4, lens=P, more=P, B=2, W=9, S=0, st=None, ws=P, wb=1 << 40)
+    a.update(kw)
+    return L.attn_pages_update(a["refs"], a["pages"], a["page"], a["table"], a["mp"], a["lens"], a["more"],
+                               a["B"], a["W"], a["S"], a["st"], a["ws"], a["wb"], None)
+
+
+def fork(L, **kw):
+    a = dict(refs=P, pages=8, page=16, table=P, mp=4, lens=P, B=2, parent=P, F=3, nt=ctypes.c_void_p(FAKE + 64),
+             nl=ctypes.c_void_p(FAKE + 64), moves=P, st=None, ws=P, wb=1 << 40)
+    a.update(kw)
+    return L.attn_pages_fork(a["refs"], a["pages"], a["page"], a["table"], a["mp"], a["lens"], a["B"],
+                             a["parent"], a["F"], a["nt"], a["nl"], a["moves"], a["st"], a["ws"], a["wb"], None)
+
+
+def copy(L, d=None, e=None, **kw):
+    a = dict(moves=P, n=2, sa=None, da=None, st=None)
+    a.update(kw)
+    return L.attn_pages_copy(ctypes.byref(d or desc()), ctypes.byref(e or desc()), a["moves"], a["n"], a["sa"],
+                             a["da"], a["st"], None)
+
+
+@pytest.mark.parametrize("call,rows", [(update, "B"), (fork, "F"), (fork, "B")])
+def test_pages_limits(L, call, rows):
+    assert call(L, pages=0) == EINVAL and call(L, pages=(1 << 30) + 1) == ESHAPE
+    assert call(L, mp=0) == EINVAL and call(L, mp=(1 << 26) + 1) == ESHAPE
+    for page in (0, 8, 24, 512, -16):
+        assert call(L, page=page) == ESHAPE
+    assert call(L, **{rows: -1}) == EINVAL and call(L, **{rows: 65536}) == ESHAPE
+    assert call(L, **{rows: 65535}, mp=32769) == ESHAPE             # 2^31 entries
+    for k in ("refs", "table", "lens"):
+        assert call(L, **{k: None}) == EINVAL, k
+    for k in ("refs", "table", "lens", "st"):
+        assert call(L, **{k: ODD}) == EALIGN, k
+
+
+def test_pages_update(L):
+    assert update(L, B=0) == 0 and update(L, more=None) == EINVAL and update(L, more=ODD) == EALIGN
+    assert update(L, W=0) == EINVAL and update(L, S=-1) == EINVAL
+    need = L.attn_pages_update_workspace_bytes(8, 2, 4)
+    assert need > 0 and need % 256 == 0
+    assert update(L, wb=need - 1) == EWORKSPACE and update(L, ws=None) == EWORKSPACE
+    assert update(L, ws=ctypes.c_void_p(FAKE + 4)) == EWORKSPACE
+    assert L.attn_pages_update_workspace_bytes(0, 2, 4) == 0
+
+
+def test_pages_fork(L):
+    assert fork(L, F=0) == 0
+    for k in ("parent", "nt", "nl", "moves"):
+        assert fork(L, **{k: None}) == EINVAL, k
+        assert fork(L, **{k: ODD}) == EALIGN, k
+    assert fork(L, nt=P) == EINVAL and fork(L, nl=P) == EINVAL      # onto the parents'
+    need = L.attn_pages_fork_workspace_bytes(8, 3)
+    assert need > 0 and need % 256 == 0
+    assert fork(L, wb=need - 1) == EWORKSPACE and fork(L, ws=None) == EWORKSPACE
+
+
+def test_pages_copy(L):
+    assert copy(L, n=0) == 0 and copy(L, n=-1) == EINVAL and copy(L, moves=None) == EINVAL
+    assert copy(L, n=1 << 30) == ESHAPE
+    assert copy(L, sa=P) == EINVAL                                  # weights to nowhere
+    for bad in (dict(Hkv=1), dict(D=128), dict(dtype=2), dict(page=32)):
+        assert copy(L, None, desc(**bad)) == ESHAPE
+    assert copy(L, desc(D=96)) == ESHAPE and copy(L, None, desc(k=None)) == EINVAL
+    for k in ("moves", "da", "st"):
+        assert copy(L, **{k: ODD}) == EALIGN, k
+    assert copy(L, sa=ODD, da=P) == EALIGN
