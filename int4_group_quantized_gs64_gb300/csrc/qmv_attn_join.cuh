@@ -64,11 +64,20 @@ __global__ void __launch_bounds__(128 * kSplit) k_attn_join(const TreeArgs a, bo
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
         if (c0 == c1) return;  // nothing here, or one segment, written by its block
     }
-    const int rows = min(a.rows, q.T * a.G - rb * a.rows);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int w = blockIdx.z * 4 + (warp & 3), split = warp >> 2;
     const int r = (w / kParts) * 8 + (lane & 7), col0 = (w % kParts) * (kCols * 16) + (lane >> 3) * 4;
-    const bool have_row = r < rows;
+    // the row's token and query head
+    int t, g;
+    bool have_row;
+    if constexpr (kWin) {
+        have_row = tile_row(a, q, rb * a.tpi + (r >> 7), r & 127, t, g);
+    } else {
+        const int rr = rb * a.rows + r;
+        t = div_g(a, rr);
+        g = rr - t * a.G;
+        have_row = r < min(a.rows, q.T * a.G - rb * a.rows);
+    }
     // this warp's stretch of the segments
     const int per = (c1 - c0 + kSplit) / kSplit;
     const int x_begin = c0 + split * per, x_end = min(c1 + 1, x_begin + per);
@@ -138,9 +147,7 @@ __global__ void __launch_bounds__(128 * kSplit) k_attn_join(const TreeArgs a, bo
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
     const float inv = L == 0.f ? 0.f : 1.f / L;
-    // (the block's first row is row r0 of token t0's G)
-    const int t0 = kWin ? rb * a.rows / a.G : 0, rr = rb * a.rows - t0 * a.G + r, t = div_g(a, rr);
-    const long long row = (long long)(q.first + t0 + t) * a.Hq + h * a.G + rr - t * a.G;
+    const long long row = (long long)(q.first + t) * a.Hq + h * a.G + g;
 #pragma unroll
     for (int i = 0; i < kCols; ++i) {
         const float x0 = acc[i][0] * inv, x1 = acc[i][1] * inv, x2 = acc[i][2] * inv, x3 = acc[i][3] * inv;

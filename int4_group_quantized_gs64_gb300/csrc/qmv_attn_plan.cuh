@@ -50,8 +50,14 @@ struct TreeArgs {
     int32_t *status;
     // kWin: a row at slot p sees j <= p with j > p - window or j < sinks
     int window, sinks;
-    int lunit;       // kWin: unit = 1 << lunit
-    PartInfo *info;  // kWin: which items the segments in part_o belong to, [grid][2]
+    int lunit;       // unit = 1 << lunit
+    // Rows come in tiles of whole tokens: tile x of a sequence holds the tokens from
+    // x / hs * tb on, tb of them, and of their G query heads those from x % hs * hb
+    // on, hb of them (all, unless G is above 128). An item is tpi tiles.
+    int tb, hb, hs, tpi;
+    uint32_t hinv;   // ceil(2^32 / hb)
+    float flip;      // what scores are multiplied by before sl2: 1, or -1 or 0 for such a scale
+    PartInfo *info;  // which items the segments in part_o belong to, [grid][2]
 };
 
 // r / G for a row r < 2^18 and G <= 1024: the rounding of ginv adds less than
@@ -67,18 +73,30 @@ __device__ __forceinline__ int key_units(const Seq &q, int unit) {
     return (q.ctx + q.T + unit - 1) / unit;
 }
 
-// kWin: the keys that some row of a block of rows sees: slots [lo, p1] and those
-// below a.sinks. They are looked at in units of a.unit slots on a grid from slot
-// 0; `us` units hold first keys only, the rest begin at `shift` units more.
+// kWin: a sequence's tiles of rows, and its items a head.
+__device__ __forceinline__ int row_tiles(const TreeArgs &a, const Seq &q) {
+    return (q.T + a.tb - 1) / a.tb * a.hs;
+}
+__device__ __forceinline__ int window_items(const TreeArgs &a, const Seq &q) {
+    return (row_tiles(a, q) + a.tpi - 1) / a.tpi;
+}
+// Token and head (among the G) of row i < 128 of a tile; false: there is none.
+__device__ __forceinline__ bool tile_row(const TreeArgs &a, const Seq &q, int tile, int i, int &t, int &g) {
+    const int x = a.hb == 1 ? i : (int)__umulhi((uint32_t)i, a.hinv), k = tile / a.hs;
+    t = k * a.tb + x;
+    g = (tile - k * a.hs) * a.hb + i - x * a.hb;
+    return x < a.tb && t < q.T && g < a.G;
+}
+
+// kWin: the keys that some row of an item sees: slots [lo, p1] and those below
+// a.sinks. They are looked at in units of a.unit slots on a grid from slot 0; `us`
+// units hold first keys only, the rest begin at `shift` units more.
 struct Reach {
     int p0, p1, lo, us, shift, nu;
-    int t0, r0;  // the block's first row is row r0 of token t0's G
-    __device__ __forceinline__ void set(const TreeArgs &a, const Seq &q, int rb) {
-        const int first = rb * a.rows, n = min(a.rows, q.T * a.G - first);
-        t0 = first / a.G;
-        r0 = first - t0 * a.G;
-        p0 = q.ctx + t0;
-        p1 = p0 + div_g(a, r0 + n - 1);
+    __device__ __forceinline__ void set(const TreeArgs &a, const Seq &q, int item) {
+        const int x = item * a.tpi, y = min(x + a.tpi, row_tiles(a, q)) - 1;
+        p0 = q.ctx + x / a.hs * a.tb;
+        p1 = q.ctx + min(y / a.hs * a.tb + a.tb, q.T) - 1;
         lo = max(0, p0 - a.window + 1);
         const int w0 = lo >> a.lunit;
         us = min((min(a.sinks, lo) + a.unit - 1) >> a.lunit, w0);
@@ -103,11 +121,11 @@ __device__ __forceinline__ uint32_t window_word(const TreeArgs &a, int p, int sl
     return bits_below(p + 1 - slot) & (~bits_below(lo - slot) | bits_below(a.sinks - slot));
 }
 
-// kWin: the units of one head of a sequence. A thread adds up the blocks of
-// rows `from`, `from` + step, ...
+// kWin: the units of one head of a sequence. A thread adds up the items `from`,
+// `from` + step, ...
 __device__ __forceinline__ long long window_units(const TreeArgs &a, const Seq &q, int from, int step) {
     long long n = 0;
-    const int nrb = row_blocks(q, a.G, a.rows);
+    const int nrb = window_items(a, q);
 #pragma unroll 1
     for (int rb = from; rb < nrb; rb += step) {
         Reach r;
@@ -116,7 +134,7 @@ __device__ __forceinline__ long long window_units(const TreeArgs &a, const Seq &
     }
     return n;
 }
-constexpr int kAlone = 4;  // blocks of rows that a thread adds up by itself
+constexpr int kAlone = 4;  // items that a thread adds up by itself
 
 // All units of a sequence, by one thread.
 template <bool kWin>
@@ -129,7 +147,7 @@ __device__ __forceinline__ long long seq_units(const TreeArgs &a, const Seq &q) 
 template <bool kWin>
 __device__ __forceinline__ long long lane_units(const TreeArgs &a, const Seq &q) {
     if (!kWin) return seq_units<false>(a, q);
-    const bool big = q.T > 0 && row_blocks(q, a.G, a.rows) > kAlone;
+    const bool big = q.T > 0 && window_items(a, q) > kAlone;
     long long n = big ? 0 : seq_units<true>(a, q);
     for (uint32_t who = __ballot_sync(0xFFFFFFFFu, big); who; who &= who - 1) {
         const int from = __ffs(who) - 1, lane = threadIdx.x & 31;
@@ -286,7 +304,7 @@ __device__ __forceinline__ Share find_share(const TreeArgs &a, ShareScratch<kThr
     return s;
 }
 
-// The place of a unit: sequence, head, row block, unit of the item's keys.
+// The place of a unit: sequence, head, row block (item), unit of the item's keys.
 template <bool kWin>
 struct CursorOf {
     int b, h, rb, u;
@@ -296,7 +314,7 @@ struct CursorOf {
     __device__ __forceinline__ void load(const TreeArgs &a) {
         bool ok;
         q = get_seq(a.s, b, ok);
-        nrb = row_blocks(q, a.G, a.rows);
+        nrb = kWin ? window_items(a, q) : row_blocks(q, a.G, a.rows);
         if (!kWin) nu = key_units(q, a.unit);
     }
     __device__ __forceinline__ void reach(const TreeArgs &a) {
@@ -307,13 +325,6 @@ struct CursorOf {
     }
     // The place of unit x of the item on the grid of units.
     __device__ __forceinline__ int at(int x) const { return kWin && x >= r.us ? x + r.shift : x; }
-    // Rows of this block, and of row i its token and its head among the G.
-    __device__ __forceinline__ int rows_left(const TreeArgs &a) const { return q.T * a.G - rb * a.rows; }
-    __device__ __forceinline__ int token(const TreeArgs &a, int i, int &g) const {
-        const int x = kWin ? r.r0 + i : rb * a.rows + i, t = div_g(a, x);
-        g = x - t * a.G;
-        return kWin ? r.t0 + t : t;
-    }
     // Whether some row of the item may see a slot of [s0, s1).
     __device__ __forceinline__ bool some(const TreeArgs &a, int s0, int s1) const {
         return kWin ? r.some(a, s0, s1) : s0 < q.ctx + q.T;
@@ -391,6 +402,11 @@ __device__ __forceinline__ float *part_at(const TreeArgs &a, int block, int last
 // A pool as a tensor map (128 bytes, row, 128-byte chunk of a row), boxes of
 // box_rows rows of one chunk, or of all (chunks), 128-byte swizzle.
 bool encode_pool(CUtensorMap *map, const void *pool, const AttnCache &c, int box_rows, bool all_chunks);
+
+// Queries as a tensor map (128 bytes, head, token, 128-byte chunk of a head), boxes
+// of some heads of some tokens, one chunk, 128-byte swizzle.
+bool encode_heads(CUtensorMap *map, const void *q, int N, int Hq, int D, long long q_stride, int heads,
+                  int tokens);
 
 // The scores of 16 keys from `slot` (a multiple of 16): [max_rows][16].
 __device__ __forceinline__ float *stash_at(const TreeArgs &a, int b, int h, int slot) {

@@ -73,6 +73,19 @@ bool encode_pool(CUtensorMap *map, const void *pool, const AttnCache &c, int box
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_heads(CUtensorMap *map, const void *q, int N, int Hq, int D, long long q_stride, int heads,
+                  int tokens) {
+    auto enc = encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[4] = {128, (cuuint64_t)Hq, (cuuint64_t)N, (cuuint64_t)D / 64};
+    cuuint64_t strides[3] = {(cuuint64_t)D * 2, (cuuint64_t)q_stride * 2, 128};
+    cuuint32_t box[4] = {128, (cuuint32_t)heads, (cuuint32_t)tokens, 1};
+    cuuint32_t es[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(q), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 namespace {
 
 // Where the weights come from with up to 16 rows: scores that the attention

@@ -3,17 +3,16 @@
 //
 // The token at slot p sees the slots j <= p with j > p - window or j < sinks;
 //     x_j = scale * q . k_j,   o = sum_j exp(x_j - M) v_j / sum_j exp(x_j - M)
-// as in qmv_attn_tree.cu, whose kernels these are in their second form (kWin):
-// the rows of a key/value head are its tokens times G query heads, a block of
-// rows is an item, and its keys are the union of what its rows see, in two
-// stretches of units (Reach): those with first tokens, and those from the first
-// row's window to the last row's slot. Units that every row sees whole need no
-// mask; the others (the edges: at most 255 slots a side) are masked row by row.
+// as in qmv_attn_tree.cu. The rows of a key/value head are its tokens times G
+// query heads; some of them are an item, and its keys are the union of what its
+// rows see, in two stretches of units (Reach): those with first tokens, and those
+// from the first row's window to the last row's slot. Units that every row sees
+// whole need no mask; the others (the edges) are masked row by row.
 // Units are shared out evenly over the blocks, so a prompt's early rows (short
 // reach) and late ones, and sequences of any length, fill the GPU alike.
 //
 // Up to 16 rows a sequence: k_attn_rows (warp MMA, bound by the copy of keys
-// and values); more: k_attn_tc (tcgen05).
+// and values); more: k_window_tc (tcgen05).
 #include <math.h>
 #include <string.h>
 
@@ -27,17 +26,40 @@
 namespace qmv {
 namespace attn {
 
-// Launches the tcgen05 kernel (qmv_attn_tc.cuh) for a.rows = 128 or 256.
+// Launches the tcgen05 kernel (qmv_window_tc.cu).
 cudaError_t launch_window_tc(const AttnCache &c, const TreeArgs &a, cudaStream_t st);
 
 namespace {
+
+// Items of a head of a sequence of T new tokens.
+long long items_a_head(const TreeArgs &a, long long T) {
+    return ((T + a.tb - 1) / a.tb * a.hs + a.tpi - 1) / a.tpi;
+}
+
+// The rows of an item: few, or one tile of 128 or two (rows_an_item says which
+// kernel they measured best on).
+void set_rows(TreeArgs &a, int max_new) {
+    a.max_rows = max_new * a.G;
+    if (a.max_rows <= kRows) {  // all of a sequence's
+        a.rows = kRows;
+        a.tb = 1 << 30;
+        a.hb = a.G;
+        a.hs = a.tpi = 1;
+    } else {
+        a.hb = a.G < 128 ? a.G : 128;
+        a.tb = 128 / a.hb;
+        a.hs = (a.G + 127) / 128;
+        a.tpi = max_new <= a.tb && a.hs == 1 ? 1 : 2;
+        a.rows = 128 * a.tpi;
+    }
+    a.hinv = (uint32_t)(((1ull << 32) + a.hb - 1) / a.hb);
+}
 
 template <int D, bool kBf16>
 cudaError_t run_window(const AttnCache &c, const TreeArgs &a, cudaStream_t st) {
     const bool few = a.rows == kRows;
     cudaError_t e = few ? run_rows<D, kBf16, true>(c, a, st) : launch_window_tc(c, a, st);
-    const long long nrb = ((long long)a.max_rows + a.rows - 1) / a.rows;
-    if (e == cudaSuccess) e = run_join<D, kBf16, true>(a, !few, a.max_rows, nrb, st);
+    if (e == cudaSuccess) e = run_join<D, kBf16, true>(a, !few, few ? a.max_rows : a.rows, items_a_head(a, a.s.max_draft), st);
     return e;
 }
 
@@ -50,7 +72,10 @@ size_t part_floats(const AttnCache &c, int rows) {
 }  // namespace attn
 
 size_t attn_window_ws_bytes(const AttnCache &c, int Hq, int max_new) {
-    const int rows = attn::rows_an_item(max_new * (Hq / c.Hkv));
+    attn::TreeArgs a;
+    a.G = Hq / c.Hkv;
+    attn::set_rows(a, max_new);
+    const int rows = a.rows;
     const size_t n = attn::part_floats(c, rows) * 4 + (size_t)attn::attn_grid_max(rows) * 2 * sizeof(attn::PartInfo);
     return (n + 255) / 256 * 256;
 }
@@ -66,22 +91,22 @@ cudaError_t launch_attn_window(const AttnCache &c, const WindowCall &t, cudaStre
     a.q_stride = t.q_stride;
     a.Hq = t.Hq; a.Hkv = c.Hkv; a.G = t.Hq / c.Hkv; a.pages = c.pages;
     a.ginv = (uint32_t)(((1ull << 32) + a.G - 1) / a.G);
+    // (k_attn_rows turns or clears the queries, k_window_tc the scores)
     a.sl2 = t.scale == 0.f ? 1.f : fabsf(t.scale) * kLog2e;
     a.qxor = t.scale < 0.f ? 0x80008000u : 0u;
     a.qand = t.scale == 0.f ? 0u : 0xFFFFFFFFu;
+    a.flip = t.scale < 0.f ? -1.f : t.scale == 0.f ? 0.f : 1.f;
     a.o = t.o; a.o_f32 = t.o_f32; a.lse = t.lse;
     a.vpool = static_cast<const uint16_t *>(c.v);
     a.status = t.status;
     a.window = t.window; a.sinks = t.sinks;
-    a.max_rows = t.s.max_draft * a.G;
-    a.rows = rows_an_item(a.max_rows);
+    set_rows(a, t.s.max_draft);
     a.unit = a.rows == kRows ? kWarps * 16 * (128 / c.D) : 128;  // keys a unit
     while ((1 << a.lunit) < a.unit) ++a.lunit;
-    // units at most: the blocks of rows of N tokens (or of B sequences at their
-    // bound), each over a whole table row
-    const long long nrb = ((long long)a.max_rows + a.rows - 1) / a.rows;
-    long long items = t.s.B * nrb;
-    const long long by_n = (long long)t.s.N * a.G / a.rows + t.s.B;
+    // units at most: the items of B sequences at their bound, or of N tokens (a
+    // sequence's last item may be short), each over a whole table row
+    long long items = t.s.B * items_a_head(a, t.s.max_draft);
+    const long long by_n = items_a_head(a, t.s.N) + t.s.B;
     if (by_n < items) items = by_n;
     const long long most = items * c.Hkv * (((((long long)t.s.max_pages << lpage) + a.unit - 1) >> a.lunit) + 1);
     const int gmax = attn_grid_max(a.rows);

@@ -1,12 +1,973 @@
-// qmv_window_tc.cu - windowed attention of many rows on the tcgen05 tensor cores:
-// the kernel k_attn_tc of qmv_attn_tc.cuh.
-#include "qmv_attn_tc.cuh"
+// qmv_window_tc.cu - windowed attention of many rows on the tcgen05 tensor cores.
+//
+// S = Q K^T from shared memory, O += P V with P in tensor memory, 128 rows a tile
+// (whole tokens with their query heads: qmv_attn_plan.cuh), 128 keys a step. A
+// block keeps two streams in flight, each with its own scores S and output O:
+//   prompts (kTwo): two tiles of rows against the same keys, which are copied once;
+//   up to 128 rows a head: one tile; the streams take alternate steps of the keys
+//   and are added up at the end of the block's part of an item.
+//
+// Warps: 0-3 and 4-7 the streams' softmax, a thread a row; 8 copies keys, 11 values
+// and queries, 9 and 10 issue the streams' products (9 all of them where the streams
+// take alternate steps). Every warp comes to a barrier's phases one by one.
+//
+// A stream's chain of a step is 1,024 cycles of products and its softmax; the two
+// streams together need 2,048 of products, so a softmax below 1,024 would hide
+// altogether. Its exponentials alone take 512 (four cycles a warp instruction). The
+// weights are handed over in two halves, so that the output's first products run
+// under the second half's exponentials, and maxima are taken three at a time.
+//
+// The end of an item costs a stream one look at O: queries of the next item come by
+// tensor-map copies while the last softmax runs, and its scores are formed while O
+// is written out. The streams do not wait for one another there (with the queries
+// through registers and both streams in step, 14 items a block cost 170 us of 670:
+// 12,279 prompt tokens, windows of 2048).
+//
+// Masks: a step that all rows of the item see whole is not looked at. In the others
+// (at the window's edge, the diagonal, the first tokens' end, with a missing page)
+// scores that a row does not see become -inf, and values that some row does not see
+// and that are not finite are replaced by zeros, since 0 x inf is not 0; the rows
+// that do see them get them added at the end (Misc::odd).
+//
+// The running maximum moves when it grows by more than 2^8; weights and sums for
+// 16-bit and fp32 outputs are those of qmv_attn_tc.cu: rounded once to 16 bits, or
+// two fp16 / three bf16 numbers and sums of each step added up in registers.
+#include <cudaTypedefs.h>
+#include <string.h>
+
+#include "qmv_attn.cuh"
+#include "qmv_attn.h"
+#include "qmv_attn_plan.cuh"
+#include "qmv_attn_tc05.cuh"
+#include "qmv_launch.cuh"
 
 namespace qmv {
 namespace attn {
+namespace {
+
+constexpr int kThreads = 384, kKeys = 128, kMaxSlots = 6;  // slots a ring
+constexpr int kMisc = 2880;               // barriers and small tables
+constexpr int kSmemMax = 227 * 1024;
+constexpr float kLazy = 8.f;              // log2 units the maximum may lag
+
+struct Misc {
+    ShareScratch<kThreads / 32> share;
+    uint64_t kfull[kMaxSlots], kempty[kMaxSlots], vfull[kMaxSlots], vempty[kMaxSlots];
+    uint64_t q_full[2], q_empty[2], s_full[2], s_free[2], p_half[2], p_full[2], pv_done[2], o_full[2];
+    uint64_t scrub[kMaxSlots], turn[2], fin[2];
+    uint32_t tmem, dead;
+    uint32_t odd;          // some value that not all rows saw was not finite
+    float2 ml[2][128];     // !kTwo: the streams' maxima and sums
+};
+static_assert(sizeof(Misc) <= kMisc, "");
+
+// Waits for a barrier's phase; gives up after a bounded time, or at once when
+// another warp has given up.
+__device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, Misc *m, int32_t *status) {
+    volatile uint32_t *dead = &m->dead;
+#pragma unroll 1
+    for (uint32_t i = 0; i < kPoll; ++i) {
+        if (try_wait(bar, parity)) return true;
+        if ((i & 255) == 255 && *dead) return false;
+    }
+    *dead = 1;
+    set_status(status, kStTimeout);
+    return false;
+}
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, Misc *m, int32_t *status) {
+    const uint32_t b = tc05::smem_addr(bar);
+    return try_wait(b, parity) || wait_slow(b, parity, m, status);
+}
+
+// One lane of a converged warp, always the same.
+__device__ __forceinline__ bool elected() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+__device__ __forceinline__ void tma_load4(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2,
+                                          int c3, uint64_t *mbar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3),
+        "r"(tc05::smem_addr(mbar))
+        : "memory");
+}
+
+// The upper halves of two floats, which are bf16 numbers, and what they leave.
+__device__ __forceinline__ uint32_t cut_bf16x2(float &x, float &y) {
+    const uint32_t u = __float_as_uint(x), v = __float_as_uint(y);
+    x -= __uint_as_float(u & 0xFFFF0000u);
+    y -= __uint_as_float(v & 0xFFFF0000u);
+    return __byte_perm(u, v, 0x7632);
+}
+
+// A block's part of an item: steps [j0, j0 + n) of the item's keys.
+struct Segment {
+    int j0, n;
+    bool whole;
+    __device__ __forceinline__ Segment(const CursorOf<true> &c, int left) {
+        j0 = c.u;
+        n = min(c.nu - c.u, left);
+        whole = j0 == 0 && n == c.nu;
+    }
+};
+
+// All steps of a block, one after the other.
+struct Walk {
+    CursorOf<true> c;
+    int left, n, i;  // steps from this segment's start on, its steps, the place among them
+    __device__ __forceinline__ Walk(const CursorOf<true> &start, int units) : c(start), left(units), i(0) {
+        n = min(c.nu - c.u, left);
+    }
+    __device__ __forceinline__ bool first() const { return i == 0; }
+    __device__ __forceinline__ bool last() const { return i == n - 1; }
+    __device__ __forceinline__ void advance(const TreeArgs &a) {
+        if (++i < n) return;
+        left -= n;
+        i = 0;
+        if (left > 0) {
+            c.next_item(a);
+            n = min(c.nu, left);
+        }
+    }
+};
+
+template <int D, bool kBf16, bool kTwo, bool kSplit>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_window_tc(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                const __grid_constant__ CUtensorMap qmap, const TreeArgs a, int stages) {
+    constexpr int kTile = kKeys * D * 2, kHalves = D / 64, kQ = kTwo ? 2 : 1;
+    constexpr uint32_t kIdescS = tc05::idesc_f16kind_f32(kBf16, 128, kKeys, false);
+    extern __shared__ __align__(1024) uint8_t smem[];
+    // Tensor memory columns. Where they suffice (64 elements, one 16-bit number a
+    // weight) P lies apart from S, and a stream's next S is formed while its
+    // exponentials run. Otherwise P overwrites S.
+    constexpr bool kApart = D == 64 && !kSplit;
+    // The third number of a bf16 weight lies in columns that O leaves: with 128
+    // elements O comes in two halves, one after the other.
+    constexpr bool kThird = kSplit && kBf16, kParted = kThird && D == 128;
+    constexpr int kOcols = kParted ? 64 : D;  // columns a product gives
+    constexpr uint32_t kIdescO = tc05::idesc_f16kind_f32(kBf16, 128, kOcols, true);
+    // The two streams' products are issued in turn where they are what bounds a step:
+    // side by side both streams' scores would come at once, and the pipe would wait
+    // for both softmaxes.
+    constexpr bool kTurns = kTwo && !kSplit && !kApart;
+    constexpr int kPcol = kApart ? 256 : 0, kPstep = kApart ? 64 : 128;   // P of stream s at kPcol + s * kPstep
+    constexpr int kOcol = kApart ? 384 : 256, kOstep = kApart ? 64 : 128;
+    const int kslots = stages / 2, vslots = stages - kslots;
+    uint8_t *qs = smem, *kring = smem + kQ * kTile, *vring = kring + kslots * kTile;
+    Misc *m = reinterpret_cast<Misc *>(vring + vslots * kTile);
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kMaxSlots; ++i) {
+            tc05::mbar_init(m->kfull + i, 1);
+            tc05::mbar_init(m->kempty + i, kQ);
+            tc05::mbar_init(m->vfull + i, 1);
+            tc05::mbar_init(m->vempty + i, kQ);
+            tc05::mbar_init(m->scrub + i, 4);
+        }
+        for (int s = 0; s < 2; ++s) {
+            tc05::mbar_init(m->q_full + s, 1);
+            tc05::mbar_init(m->q_empty + s, 1);
+            tc05::mbar_init(m->s_full + s, 1);
+            tc05::mbar_init(m->s_free + s, 4);
+            tc05::mbar_init(m->p_half + s, 4);
+            tc05::mbar_init(m->p_full + s, 4);
+            tc05::mbar_init(m->pv_done + s, 1);
+            tc05::mbar_init(m->o_full + s, 1);
+            tc05::mbar_init(m->turn + s, 1);
+            tc05::mbar_init(m->fin + s, 1);
+        }
+        m->dead = 0;
+        m->odd = 0;
+        tc05::fence_mbar_init();
+        prefetch_tmap(&kmap);
+        prefetch_tmap(&vmap);
+        prefetch_tmap(&qmap);
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (blockIdx.x == 0 && a.status) {
+        for (int b = threadIdx.x; b < a.s.B; b += kThreads) {
+            bool ok;
+            get_seq(a.s, b, ok);
+            if (!ok) set_status(a.status, kStLength);
+        }
+    }
+    const Share sh = find_share<kThreads, true>(a, &m->share);
+    if (threadIdx.x == 0) a.info[blockIdx.x * 2].n = a.info[blockIdx.x * 2 + 1].n = 0;
+    if (sh.u0 >= sh.u1) return;
+    if (warp == 9) tc05::tmem_alloc(&m->tmem, 512);
+    tc05::fence_before_sync();
+    __syncthreads();
+    tc05::fence_after_sync();
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, m->tmem, 0);
+    const int units = (int)(sh.u1 - sh.u0);  // (the launcher keeps this below 2^31)
+
+    // 168 x 384 registers at launch = 216 x 256 + 72 x 128
+    if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 8 || warp == 11) {
+        // ------------------------------------------------------------ copies
+        const bool keys = warp == 8;
+        const CUtensorMap *map = keys ? &kmap : &vmap;
+        // read once: first to leave L2 (not by several items)
+        const bool once = a.max_rows <= a.tb * a.hb * kQ;
+        const uint64_t policy = evict_first_policy();
+        const int prow = a.s.page < kKeys ? a.s.page : kKeys;  // rows a copy
+        CursorOf<true> c;
+        c.start(a, sh);
+        uint64_t *full = keys ? m->kfull : m->vfull, *empty = keys ? m->kempty : m->vempty;
+        const uint32_t ring = tc05::smem_addr(keys ? kring : vring);
+        const int slots = keys ? kslots : vslots;
+        int stage = 0;
+        uint32_t phase = 1, qphase = 1;  // a fresh barrier counts as passed for parity 1
+        // this lane's piece of the item's step u at c: its page
+        auto page_of = [&](int u, bool &lv) {
+            const int slot = c.at(u) * kKeys + lane * prow;
+            lv = lane * prow < kKeys && c.some(a, slot, slot + prow);
+            return lv ? __ldg(a.s.table + (long long)c.b * a.s.max_pages + (slot >> a.s.lpage)) : 0;
+        };
+        bool live;
+        int pid = page_of(c.u, live);
+        bool ok = true;
+        uint32_t pending = 0, pending_ph = 0;  // slots this warp copied to, and the phase that ends it
+        bool q_pending = false;
+        for (int left = units; left > 0;) {
+            const Segment sg(c, left);
+            if (!keys) {  // the item's queries, once the last item's scores are done
+#pragma unroll
+                for (int s = 0; s < kQ; ++s) {
+                    ok = ok && wait(m->q_empty + s, qphase, m, a.status);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (ok && lane == 0) {
+                        const int x = c.rb * a.tpi + s, k = x / a.hs;
+                        const int head = c.h * a.G + (x - k * a.hs) * a.hb;
+                        mbar_expect_tx(m->q_full + s, kHalves * 128 * a.hb * a.tb);
+#pragma unroll
+                        for (int hf = 0; hf < kHalves; ++hf)
+                            tma_load4(tc05::smem_addr(qs) + s * kTile + hf * (128 * 128), &qmap, 0, head,
+                                      c.q.first + k * a.tb, hf, m->q_full + s);
+                    }
+                    q_pending = q_pending || ok;
+                }
+                if (ok) qphase ^= 1u;
+            }
+#pragma unroll 1
+            for (int t = 0; t < sg.n; ++t) {
+                const bool good = live && (unsigned)pid < (unsigned)a.pages;
+                const int row =
+                    (pid * a.Hkv + c.h) * a.s.page + ((c.at(sg.j0 + t) * kKeys + lane * prow) & (a.s.page - 1));
+                if (live && !good && keys) set_status(a.status, kStPage);
+                if (t + 1 < sg.n) pid = page_of(sg.j0 + t + 1, live);
+                const uint32_t n = __popc(__ballot_sync(0xFFFFFFFFu, good));
+                ok = ok && wait(empty + stage, phase, m, a.status);
+                ok = __all_sync(0xFFFFFFFFu, ok);
+                if (!ok) continue;
+                if (lane == 0) {
+                    if (n)
+                        mbar_expect_tx(full + stage, n * prow * D * 2);
+                    else
+                        mbar_arrive(full + stage);
+                }
+                __syncwarp();
+                if (good) {
+                    const uint32_t dst = ring + stage * kTile + lane * prow * 128;
+#pragma unroll
+                    for (int hf = 0; hf < kHalves; ++hf)
+                        if (once)
+                            tma_load3_once(dst + hf * (kKeys * 128), map, 0, row, hf, full + stage, policy);
+                        else
+                            tma_load3(dst + hf * (kKeys * 128), map, 0, row, hf, full + stage);
+                }
+                pending |= 1u << stage;
+                pending_ph = (pending_ph & ~(1u << stage)) | ((phase ^ 1u) & 1u) << stage;
+                if (++stage == slots) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            left -= sg.n;
+            if (left > 0) {
+                c.next_item(a);
+                pid = page_of(c.u, live);
+            }
+        }
+        if (!ok) {  // gave up: wait (bounded) for this warp's copies in flight
+            for (int i = 0; i < slots; ++i)
+                if ((pending >> i) & 1u) tc05::mbar_wait(full + i, (pending_ph >> i) & 1u, kPoll / 64);
+            if (q_pending)  // (the last ones' phase)
+                for (int s = 0; s < kQ; ++s) tc05::mbar_wait(m->q_full + s, qphase, kPoll / 64);
+        }
+    } else if (kTwo || warp == 9) {
+        // ------------------------------------------------------------ products
+        // kTwo: a warp a stream. The warp walks its steps as a whole and one elected lane
+        // issues: operands that the compiler sees to be uniform go to a product in some 10
+        // cycles, where a lone thread's took 48 of the 64 that the product runs for.
+        CursorOf<true> start;
+        start.start(a, sh);
+        {
+            const int me = warp - 9;  // kTwo: the stream
+            const uint64_t kdesc = tc05::sdesc_sw128(tc05::smem_addr(kring));
+            const uint64_t vdesc = tc05::sdesc_sw128_mn(tc05::smem_addr(vring), kKeys * 128);
+            const uint64_t qdesc = tc05::sdesc_sw128(tc05::smem_addr(qs)) + (uint32_t)(me * (kTile >> 4));
+            Walk qw(start, units);  // of the scores
+            // the outputs' steps lag at most two behind: bits 2 x and 2 x + 1 say of the
+            // x-th whether its stream's O begins anew and whether the segment ends
+            uint32_t ahead_bits = 0;
+            int ahead_n = 0, kslot = 0, vslot = 0;
+            uint32_t kph = 0, vph = 0, qph = 0, tph = 0;
+            uint32_t hph = 0, fph = 0, frph = 0;  // bit s: p_half, p_full, s_free of stream s
+            bool live = true;
+            auto await = [&](uint64_t *bar, uint32_t parity) {
+                live = __all_sync(0xFFFFFFFFu, live && wait(bar, parity, m, a.status));
+            };
+            // The scores of a step: what they wait for, the products, and what they tell.
+            auto scores_wait = [&](int s, bool again) {  // again: not the stream's first
+                if (qw.first()) {
+                    await(m->q_full + me, qph);
+                    qph ^= 1u;
+                }
+                await(m->kfull + kslot, kph);
+                if (kApart && again) {
+                    await(m->s_free + s, (frph >> s) & 1u);
+                    frph ^= 1u << s;
+                }
+            };
+            auto scores_issue = [&](int s) {  // S = Q K^T
+                const uint64_t kd = kdesc + (uint32_t)(kslot * (kTile >> 4));
+                if (elected()) {
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const int of = ((k >> 2) * (kKeys * 128) + (k & 3) * 32) >> 4;
+                        tc05::mma_ss(tmem + s * 128, qdesc + of, kd + of, kIdescS, k > 0);
+                    }
+                    tc05::mma_commit(m->s_full + s);
+                }
+                __syncwarp();
+            };
+            auto scores_done = [&]() {
+                if (elected()) {
+                    tc05::mma_commit(m->kempty + kslot);
+                    if (qw.last()) tc05::mma_commit(m->q_empty + me);
+                }
+                __syncwarp();
+                ahead_bits |= ((qw.i < (kTwo ? 1 : 2) ? 1u : 0u) | (qw.last() ? 2u : 0u)) << (2 * ahead_n++);
+                if (++kslot == kslots) {
+                    kslot = 0;
+                    kph ^= 1u;
+                }
+                qw.advance(a);
+            };
+            auto scores = [&](int s, bool again) {
+                scores_wait(s, again);
+                if (!live) return;
+                tc05::fence_after_sync();
+                scores_issue(s);
+                scores_done();
+            };
+            // The output of the oldest step: O (+)= P V.
+            auto output_issue = [&](int s, int hf) {  // of half the keys; kSplit: of half the columns
+                const uint32_t tp = tmem + kPcol + s * kPstep, to = tmem + kOcol + s * kOstep;
+                const uint64_t v = vdesc + (uint32_t)(vslot * (kTile >> 4));
+                if (elected()) {
+                    if constexpr (kSplit) {  // the rests, then the weights: a sum of this step alone
+#pragma unroll
+                        for (int part = kThird ? 2 : 1; part >= 0; --part)
+#pragma unroll
+                            for (int k = 0; k < kKeys / 16; ++k)
+                                tc05::mma_ts(to, part == 2 ? to + 64 + k * 8 : tp + k * 16 + part * 8,
+                                             v + (hf * (kKeys * 128) + k * 2048 >> 4), kIdescO,
+                                             part < (kThird ? 2 : 1) || k > 0);
+                        tc05::mma_commit(m->pv_done + s);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            tc05::mma_ts(to, tp + hf * 32 + k * 8, v + (hf * 4 + k) * (2048 >> 4), kIdescO,
+                                         hf || k ? 1u : ~ahead_bits & 1u);
+                        if (kApart && hf) tc05::mma_commit(m->pv_done + s);
+                    }
+                }
+                __syncwarp();
+            };
+            auto half_wait = [&](int s) {  // the first weights of a step
+                await(m->vfull + vslot, vph);
+                if (kSplit) {
+                    await(m->p_full + s, (fph >> s) & 1u);
+                    fph ^= 1u << s;
+                } else {
+                    await(m->p_half + s, (hph >> s) & 1u);
+                    hph ^= 1u << s;
+                }
+            };
+            auto output_rest = [&](int s) {
+                if (kSplit && !kParted) return;
+                await(m->p_full + s, (fph >> s) & 1u);
+                fph ^= 1u << s;
+                if (!live) return;
+                tc05::fence_after_sync();
+                output_issue(s, 1);
+            };
+            auto output_done = [&](int s) {
+                if (elected()) {
+                    tc05::mma_commit(m->vempty + vslot);
+                    if (ahead_bits & 2u) {
+                        tc05::mma_commit(m->o_full + s);
+                        if (!kTwo) tc05::mma_commit(m->o_full + (s ^ 1));
+                    }
+                }
+                __syncwarp();
+                if (++vslot == vslots) {
+                    vslot = 0;
+                    vph ^= 1u;
+                }
+                ahead_bits >>= 2;
+                --ahead_n;
+            };
+            auto output = [&](int s) {
+                half_wait(s);
+                if (!live) return;
+                tc05::fence_after_sync();
+                output_issue(s, 0);
+                output_rest(s);
+                if (live) output_done(s);
+            };
+            auto pass = [&]() {
+                if (elected()) mbar_arrive(m->turn + (me ^ 1));
+                __syncwarp();
+            };
+            if constexpr (kTurns) {
+                // Stream 0's step n, stream 1's, stream 0's next: each the output of the
+                // step and the scores of the one after, with the waits before the turn and
+                // what can be told later after it (600 cycles of it in the turn, and the
+                // two threads' turns added up to 4,600 cycles a step).
+                scores(me, false);
+#pragma unroll 1
+                for (int n = 0; n < units && live; ++n) {
+                    // (the next item's queries may be on their way: then the turn passes first)
+                    const bool more = n + 1 < units, held = more && qw.first(), now = more && !held;
+                    if (now) scores_wait(me, true);
+                    half_wait(me);
+                    if (me || n) {
+                        await(m->turn + me, tph);
+                        tph ^= 1u;
+                    }
+                    if (!live) break;
+                    tc05::fence_after_sync();
+                    output_issue(me, 0);
+                    output_rest(me);
+                    if (!live) break;
+                    if (now) scores_issue(me);
+                    pass();
+                    output_done(me);
+                    if (now) scores_done();
+                    if (held) scores(me, true);
+                }
+            } else if constexpr (kTwo) {
+                scores(me, false);
+#pragma unroll 1
+                for (int n = 0; n < units && live; ++n) {
+                    const bool more = n + 1 < units;
+                    if (kApart && more) scores(me, true);
+                    output(me);
+                    if (!kApart && more) scores(me, true);
+                }
+            } else {
+                // step n is stream n % 2's; at most two steps' scores ahead
+                int qn = 0;
+                auto ahead = [&](int upto) {
+                    while (qn < units && qn < upto && live) {
+                        scores(qn & 1, qn >= 2);
+                        ++qn;
+                    }
+                };
+                ahead(1);
+                if (units > 1 && !qw.first()) ahead(2);
+#pragma unroll 1
+                for (int n = 0; n < units && live; ++n) {
+                    // S of step n + 2, and before it those that an item's start held
+                    // back: they wait for its queries, so the outputs before go first
+                    if (kApart && qn == n + 2 && qn < units && !qw.first()) ahead(n + 3);
+                    ahead(n + 1);
+                    output(n & 1);
+                    ahead(n + 2);
+                    if (qn < units && !qw.first()) ahead(n + 3);
+                }
+            }
+            // nothing of this warp's is in flight when the block ends
+            if (elected()) tc05::mma_commit(m->fin + me);
+            __syncwarp();
+            tc05::mbar_wait(m->fin + me, 0, kPoll);
+        }
+        __syncwarp();
+    }
+    } else {
+        // ------------------------------------------------------------ softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        const int s = warp >> 2, tid = threadIdx.x & 127, wq = warp & 3;
+        const uint32_t lanes = (uint32_t)(wq * 32) << 16;
+        const uint32_t ts = tmem + lanes + s * 128, to = tmem + lanes + kOcol;
+        const uint32_t tw = tmem + lanes + kPcol + s * kPstep;  // weights
+        uint32_t sp = 0, op = 0, vp = 0;  // phases of s_full, o_full, pv_done
+        uint32_t scrub_ph = 0;            // bit x: phase of scrub[x]
+        bool again = false;               // a step of this stream came before
+        CursorOf<true> c;
+        c.start(a, sh);
+        const float boost = kBf16 ? 0.f : 7.f;
+        const int piece = min(a.s.page, kKeys);
+        for (int left = units; left > 0;) {
+            const Segment sg(c, left);
+            const Seq q = c.q;
+            const int32_t *trow = a.s.table + (long long)c.b * a.s.max_pages;
+            // whether the page of some needed slot among n from `slot` on is missing
+            auto missing = [&](int slot, int n) {
+                return c.some(a, slot, slot + n) && (unsigned)trow[slot >> a.s.lpage] >= (unsigned)a.pages;
+            };
+            // this stream's steps: i0, i0 + kStep, ...
+            constexpr int kStep = kTwo ? 1 : 2;
+            const int i0 = kTwo ? 0 : (s ^ (units - left)) & 1;
+            // the page of this lane's piece of a step (a step ahead)
+            auto page_of = [&](int i) {
+                const int slot = c.at(sg.j0 + i) * kKeys + lane * piece;
+                const bool need = lane * piece < kKeys && i < sg.n && c.some(a, slot, slot + piece);
+                return need ? __ldg(trow + (slot >> a.s.lpage)) : 0;
+            };
+            int pid = page_of(i0);
+            int t, g;
+            const bool row_live = tile_row(a, q, c.rb * a.tpi + (kTwo ? s : 0), tid, t, g);
+            const bool warp_live = __any_sync(0xFFFFFFFFu, row_live);
+            const int pos = q.ctx + t;  // the row's slot
+            float mx = -INFINITY, l = 0.f;  // mx: the maximum in use (log2 units)
+            uint64_t acc[kSplit ? D / 2 : 1];  // for an fp32 output: O, two columns each
+            if (kSplit)
+#pragma unroll
+                for (int e = 0; e < D / 2; ++e) acc[e] = 0;
+            // P is free again, and O complete so far. Warps without rows wait
+            // too: nothing else keeps their next arrival with weights behind
+            // the others' last, and it would stand for a slow warp's.
+            auto products_done = [&]() {
+                wait(m->pv_done + s, vp, m, a.status);
+                __syncwarp();
+                tc05::fence_after_sync();
+                vp ^= 1u;
+            };
+            auto give = [&](uint64_t *bar) {  // weights are in tensor memory
+                tc05::tmem_wait_st();
+                tc05::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar + s);
+            };
+#pragma unroll 1
+            for (int i = i0; i < sg.n; i += kStep) {
+                const int j = c.at(sg.j0 + i);
+                const uint32_t gone = __ballot_sync(0xFFFFFFFFu, (unsigned)pid >= (unsigned)a.pages);
+                pid = page_of(i + kStep);
+                const bool special = gone || !c.r.all(a, j * kKeys, (j + 1) * kKeys);
+                uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};  // this step's keys that the row sees
+                if (special && warp_live) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        see[k] = row_live ? window_word(a, pos, j * kKeys + k * 32) : 0u;
+                    if (gone) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if ((gone >> (k * 16 / piece)) & 1u)
+                                see[k >> 1] &= k & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+                    }
+                }
+                wait(m->s_full + s, sp, m, a.status);
+                __syncwarp();
+                sp ^= 1;
+                tc05::fence_after_sync();
+                if (special) {
+                    const int at = units - left + i, vslot = at % vslots;  // the step's place in the ring
+                    // Values that some row must not see are kept out of the product
+                    // where zero times them is not zero, by the first stream for both:
+                    // a thread a key, zeros where no row sees it or there is no page,
+                    // and where some rows see it its infinities and NaNs replaced.
+                    if (!kTwo || s == 0) {
+                        if (wait(m->vfull + vslot, (uint32_t)(at / vslots) & 1u, m, a.status)) {
+                            const int key = j * kKeys + tid;
+                            uint8_t *row = vring + vslot * kTile + tid * 128;
+                            const bool none = !c.some(a, key, key + 1) || (gone && missing(key, 1));
+                            auto at_chunk = [&](int ch) {
+                                return reinterpret_cast<uint4 *>(
+                                    row + (ch >> 3) * (kKeys * 128) + (((ch & 7) ^ (tid & 7)) << 4));
+                            };
+                            if (none) {
+#pragma unroll
+                                for (int ch = 0; ch < D / 8; ++ch) *at_chunk(ch) = make_uint4(0u, 0u, 0u, 0u);
+                            } else if (!c.r.all(a, key, key + 1)) {
+                                uint32_t top = 0;  // the largest magnitudes of even and odd elements
+#pragma unroll
+                                for (int ch = 0; ch < D / 8; ++ch) {
+                                    const uint4 v = *at_chunk(ch);
+                                    top = __vimax3_u16x2(top, v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu);
+                                    top = __vimax3_u16x2(top, v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu);
+                                }
+                                if (nonfinite2<kBf16>(top)) {
+                                    atomicOr(&m->odd, 1u);
+#pragma unroll 1
+                                    for (int ch = 0; ch < D / 8; ++ch) {
+                                        uint4 v = *at_chunk(ch);
+                                        uint32_t *x = reinterpret_cast<uint32_t *>(&v);
+#pragma unroll
+                                        for (int e = 0; e < 4; ++e) {
+                                            if (nonfinite2<kBf16>(x[e] & 0xFFFFu)) x[e] &= 0xFFFF0000u;
+                                            if (nonfinite2<kBf16>(x[e] & 0xFFFF0000u)) x[e] &= 0xFFFFu;
+                                        }
+                                        *at_chunk(ch) = v;
+                                    }
+                                }
+                            }
+                        }
+                        tc05::fence_proxy_async();
+                        __syncwarp();
+                        if (kTwo && lane == 0) mbar_arrive(m->scrub + vslot);
+                    } else {
+                        // (a barrier a slot: the first stream may be steps ahead, but not
+                        // in this slot again)
+                        wait(m->scrub + vslot, (scrub_ph >> vslot) & 1u, m, a.status);
+                        __syncwarp();
+                    }
+                    scrub_ph ^= 1u << vslot;
+                }
+                if (warp_live) {
+                    // two elements an instruction: weight = 2^(s * sl2 - base)
+                    const uint64_t sl2 = pack_f32x2(a.sl2, a.sl2);
+                    uint64_t sum[2] = {0, 0};
+                    if constexpr (kSplit) {
+                        // Scores that a row must not see become -inf, and those of a
+                        // negative scale turn, in tensor memory.
+                        if (special || a.flip != 1.f) {
+#pragma unroll 1
+                            for (int k = 0; k < 4; ++k) {
+                                const uint32_t w = k < 2 ? (k ? see[1] : see[0]) : (k == 2 ? see[2] : see[3]);
+                                uint32_t x[32];
+                                tc05::tmem_ld32(ts + k * 32, x);
+                                tc05::tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    x[e] = (w >> e) & 1u ? __float_as_uint(__uint_as_float(x[e]) * a.flip) : 0xFF800000u;
+                                tc05::tmem_st32(ts + k * 32, x);
+                            }
+                            tc05::tmem_wait_st();
+                        }
+                        // The scores twice from tensor memory, 32 at a time: O has the registers.
+                        float tm = -INFINITY;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t x[32];
+                            tc05::tmem_ld32(ts + k * 32, x);
+                            tc05::tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; e += 2)
+                                tm = max3(tm, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                        }
+                        tm *= a.sl2;
+                        const bool move = tm > mx + kLazy || (mx == -INFINITY && tm > mx);
+                        if (__any_sync(0xFFFFFFFFu, move)) {
+                            const float al = move ? ex2(mx - tm) : 1.f;
+                            if (move) mx = tm;
+                            l *= al;
+                            const uint64_t al2 = pack_f32x2(al, al);
+#pragma unroll
+                            for (int e = 0; e < D / 2; ++e) acc[e] = fma_f32x2(acc[e], al2, 0);
+                        }
+                        const float base = mx == -INFINITY ? 0.f : mx - boost;
+                        const uint64_t nb = pack_f32x2(-base, -base);
+#pragma unroll 2
+                        for (int h = 0; h < 8; ++h) {  // 16 at a time: one step of the product
+                            uint32_t x[16], hi[8], lo[8], third[8];
+                            tc05::tmem_ld16(ts + h * 16, x);
+                            tc05::tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                float p0, p1;
+                                unpack_f32x2(fma_f32x2(pack_u32x2(x[2 * e], x[2 * e + 1]), sl2, nb), p0, p1);
+                                p0 = ex2(p0);
+                                p1 = ex2(p1);
+                                sum[e & 1] = add_f32x2(sum[e & 1], pack_f32x2(p0, p1));
+                                if (kThird) {  // cut, not rounded: 3 x 8 bits hold all 24
+                                    hi[e] = cut_bf16x2(p0, p1);
+                                    lo[e] = cut_bf16x2(p0, p1);
+                                    third[e] = cut_bf16x2(p0, p1);
+                                } else {
+                                    hi[e] = pack2<kBf16>(p0, p1);
+                                    const float2 f = unpack2<kBf16>(hi[e]);
+                                    lo[e] = pack2<kBf16>(p0 - f.x, p1 - f.y);
+                                }
+                            }
+                            tc05::tmem_st8(tw + h * 16, hi);
+                            tc05::tmem_st8(tw + h * 16 + 8, lo);
+                            if (kThird) tc05::tmem_st8(to + s * kOstep + 64 + h * 8, third);
+                        }
+                    } else {
+                        uint32_t x[4][32];
+                        float v[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) tc05::tmem_ld32(ts + k * 32, x[k]);
+                        tc05::tmem_wait_ld();
+                        if (kApart) {
+                            tc05::fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(m->s_free + s);
+                        }
+                        // scores that a row must not see become -inf, those of a negative scale turn
+                        if (special || a.flip != 1.f)
+#pragma unroll
+                            for (int e = 0; e < 128; ++e)
+                                x[e >> 5][e & 31] = (see[e >> 5] >> (e & 31)) & 1u
+                                                        ? __float_as_uint(__uint_as_float(x[e >> 5][e & 31]) * a.flip)
+                                                        : 0xFF800000u;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            v[k] = fmaxf(__uint_as_float(x[k][0]), __uint_as_float(x[k][1]));
+#pragma unroll
+                            for (int e = 2; e < 32; e += 2)
+                                v[k] = max3(v[k], __uint_as_float(x[k][e]), __uint_as_float(x[k][e + 1]));
+                        }
+                        const float tm = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])) * a.sl2;
+                        if (kApart && again) products_done();
+                        const bool move = tm > mx + kLazy || (mx == -INFINITY && tm > mx);
+                        if (__any_sync(0xFFFFFFFFu, move)) {
+                            const float al = move ? ex2(mx - tm) : 1.f;
+                            if (move) mx = tm;
+                            l *= al;
+                            if (i > i0) {
+                                // all earlier products of this stream are done: they
+                                // were issued before this step's scores
+#pragma unroll 1
+                                for (int k = 0; k < D / 16; ++k) {
+                                    uint32_t o[16];
+                                    tc05::tmem_ld16(to + s * kOstep + k * 16, o);
+                                    tc05::tmem_wait_ld();
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e)
+                                        o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+                                    tc05::tmem_st16(to + s * kOstep + k * 16, o);
+                                }
+                            }
+                        }
+                        const float base = mx == -INFINITY ? 0.f : mx - boost;
+                        const uint64_t nb = pack_f32x2(-base, -base);
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            uint32_t hi[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                float p0, p1;
+                                unpack_f32x2(fma_f32x2(pack_u32x2(x[h][2 * e], x[h][2 * e + 1]), sl2, nb), p0, p1);
+                                p0 = ex2(p0);
+                                p1 = ex2(p1);
+                                sum[e & 1] = add_f32x2(sum[e & 1], pack_f32x2(p0, p1));
+                                hi[e] = pack2<kBf16>(p0, p1);
+                            }
+                            tc05::tmem_st16(tw + h * 16, hi);
+                            if (h == 1) give(m->p_half);
+                        }
+                        give(m->p_full);
+                    }
+                    float s0, s1, s2, s3;
+                    unpack_f32x2(sum[0], s0, s1);
+                    unpack_f32x2(sum[1], s2, s3);
+                    l += (s0 + s1) + (s2 + s3);
+                } else if (!kSplit) {  // a warp without rows: the arrivals alone
+                    if (kApart) {
+                        tc05::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(m->s_free + s);
+                        if (again) products_done();
+                    }
+                    give(m->p_half);
+                    give(m->p_full);
+                }
+                if constexpr (kSplit) {  // this step's share of O
+#pragma unroll
+                    for (int hf = 0; hf < D / kOcols; ++hf) {
+                        give(m->p_full);
+                        products_done();
+                        if (warp_live)
+#pragma unroll
+                            for (int k = 0; k < kOcols / 32; ++k) {
+                                uint32_t o[32];
+                                tc05::tmem_ld32(to + s * kOstep + k * 32, o);
+                                tc05::tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) {
+                                    uint64_t &x = acc[hf * 32 + k * 16 + e];
+                                    x = add_f32x2(x, pack_u32x2(o[2 * e], o[2 * e + 1]));
+                                }
+                            }
+                    }
+                }
+                again = true;
+            }
+            // ---- the segment's end
+            const bool mine = i0 < sg.n;  // this stream had steps
+            if (kSplit && mine) {  // O to where the segment's end takes it from
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k) {
+                    float o[32];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) unpack_f32x2(acc[k * 16 + e], o[2 * e], o[2 * e + 1]);
+                    tc05::tmem_st32(to + s * kOstep + k * 32, *reinterpret_cast<uint32_t(*)[32]>(o));
+                }
+                tc05::tmem_wait_st();
+            }
+            wait(m->o_full + s, op, m, a.status);
+            op ^= 1;
+            __syncwarp();
+            tc05::fence_after_sync();
+            if (mx != -INFINITY) mx -= boost;
+            float M = mx, L = l, f0 = 1.f, f1 = 0.f;
+            bool has0 = true, has1 = false;
+            // the two warps that have the same rows
+            auto pair_sync = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(1 + wq) : "memory"); };
+            if (!kTwo) {
+                m->ml[s][tid] = make_float2(mx, l);
+                tc05::fence_before_sync();
+                pair_sync();
+                tc05::fence_after_sync();
+                const float2 v0 = m->ml[0][tid], v1 = m->ml[1][tid];
+                M = fmaxf(v0.x, v1.x);
+                f0 = v0.x == -INFINITY ? 1.f : ex2(v0.x - M);
+                f1 = v1.x == -INFINITY ? 1.f : ex2(v1.x - M);
+                L = v0.y * f0 + v1.y * f1;
+                const int e0 = (units - left) & 1;  // the stream of the segment's first step
+                has0 = sg.n > 1 || e0 == 0;
+                has1 = sg.n > 1 || e0 == 1;
+            }
+            if (!sg.whole && threadIdx.x == 0)
+                a.info[blockIdx.x * 2 + (left == units ? 0 : 1)] =
+                    PartInfo{c.b, c.h, c.rb, sg.j0, sg.n, c.nu, (int)sh.quota, 0};
+            if (warp_live) {
+                const float inv = sg.whole ? 1.f / L : 1.f;
+                const bool none = sg.whole && L == 0.f;  // no weight: zero, also where a value is infinite
+                const long long row = (long long)(q.first + t) * a.Hq + c.h * a.G + g;
+                const int seg_last = left == units ? 0 : 1, prow = (kTwo ? s * 128 : 0) + tid;
+                const bool odd = *(volatile uint32_t *)&m->odd != 0;  // values to add by hand
+                const int k0 = kTwo ? 0 : s * (D / 64), k1 = kTwo ? D / 32 : k0 + D / 64;
+                auto columns = [&](int k, float (&o)[32]) {  // columns 32 k .. 32 k + 31 of O, out
+                    if (odd && row_live) {
+#pragma unroll 1
+                        for (int d = 0; d < 512; ++d) {  // (Reach: at most 255 keys an edge)
+                            const int key = d < 256 ? c.r.p0 + d : c.r.lo + d - 256;
+                            const int tile = key / kKeys, u = tile < c.r.us ? tile : tile - c.r.shift;
+                            if (key > c.r.p1 || u < sg.j0 || u >= sg.j0 + sg.n || c.r.all(a, key, key + 1) ||
+                                (d >= 256 && key > c.r.p0) || !(window_word(a, pos, key) & 1u))
+                                continue;
+                            const int pg = trow[key >> a.s.lpage];
+                            if ((unsigned)pg >= (unsigned)a.pages) continue;
+                            const uint16_t *v =
+                                a.vpool + (((long long)pg * a.Hkv + c.h) * a.s.page +
+                                           (key & (a.s.page - 1))) * D + k * 32;
+                            for (int e = 0; e < 32; ++e) {
+                                const float y = to_f32<kBf16>(v[e]);
+                                if (!isfinite(y)) o[e] += y;
+                            }
+                        }
+                    }
+                    if (!row_live) return;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = none ? 0.f : o[e] * inv;
+                    if (!sg.whole) {
+                        float *p = part_at<D>(a, blockIdx.x, seg_last, prow, k * 32);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            *reinterpret_cast<float4 *>(p + e * (a.rows * 4LL)) =
+                                make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    } else if (kSplit) {  // (an fp32 output)
+                        float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(a.o) + row * D + k * 32);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            p[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    } else {
+                        uint4 *p = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.o) + row * D + k * 32);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            p[e] = make_uint4(pack2<kBf16>(o[8 * e], o[8 * e + 1]),
+                                              pack2<kBf16>(o[8 * e + 2], o[8 * e + 3]),
+                                              pack2<kBf16>(o[8 * e + 4], o[8 * e + 5]),
+                                              pack2<kBf16>(o[8 * e + 6], o[8 * e + 7]));
+                    }
+                };
+#pragma unroll 1
+                    for (int k = k0; k < k1; ++k) {
+                        float o[32];
+                        __syncwarp();
+                        if (kTwo) {
+                            tc05::tmem_ld32(to + s * kOstep + k * 32, *reinterpret_cast<uint32_t(*)[32]>(o));
+                            tc05::tmem_wait_ld();
+                        } else {
+                            float o1[32];
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = o1[e] = 0.f;
+                            if (has0) tc05::tmem_ld32(to + k * 32, *reinterpret_cast<uint32_t(*)[32]>(o));
+                            if (has1) tc05::tmem_ld32(to + kOstep + k * 32, *reinterpret_cast<uint32_t(*)[32]>(o1));
+                            tc05::tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = o[e] * f0 + o1[e] * f1;
+                        }
+                        columns(k, o);
+                    }
+                if (row_live && (kTwo || s == 0)) {
+                    if (sg.whole)
+                        a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+                    else
+                        *reinterpret_cast<float2 *>(a.part_ml + (((long long)blockIdx.x * 2 + seg_last) * a.rows + prow) * 2) =
+                            make_float2(M, L);
+                }
+            }
+            tc05::fence_before_sync();
+            __syncwarp();
+            if (!kTwo) pair_sync();  // O and the maxima may be overwritten
+            left -= sg.n;
+            if (left > 0) c.next_item(a);
+        }
+    }
+    tc05::fence_before_sync();
+    __syncthreads();
+    tc05::fence_after_sync();
+    if (warp == 9) tc05::tmem_dealloc(tmem, 512);
+}
+
+template <int D, bool kBf16>
+cudaError_t run_tc(const CUtensorMap &km, const CUtensorMap &vm, const CUtensorMap &qm, const TreeArgs &a,
+                   cudaStream_t st) {
+    constexpr int kTile = kKeys * D * 2;
+    const bool two = a.tpi == 2;
+    int stages = (kSmemMax - kMisc - (two ? 2 : 1) * kTile) / kTile;
+    if (stages > 2 * kMaxSlots) stages = 2 * kMaxSlots;
+    auto *k = two ? (a.o_f32 ? k_window_tc<D, kBf16, true, true> : k_window_tc<D, kBf16, true, false>)
+                  : (a.o_f32 ? k_window_tc<D, kBf16, false, true> : k_window_tc<D, kBf16, false, false>);
+    cudaError_t e = set_smem(k, kSmemMax);
+    if (e == cudaSuccess)
+        e = launch(k, dim3(a.grid), dim3(kThreads), kSmemMax, st, true, km, vm, qm, a, stages);
+    return e;
+}
+
+}  // namespace
 
 cudaError_t launch_window_tc(const AttnCache &c, const TreeArgs &a, cudaStream_t st) {
-    return run_tc<true>(c, a, st);
+    CUtensorMap km, vm, qm;
+    const int box = c.page < kKeys ? c.page : kKeys;
+    if (!encode_pool(&km, c.k, c, box, false) || !encode_pool(&vm, c.v, c, box, false) ||
+        !encode_heads(&qm, a.q, a.s.N, a.Hq, c.D, a.q_stride, a.hb, a.tb))
+        return cudaErrorNotSupported;
+    if (c.D == 64)
+        return c.bf16 ? run_tc<64, true>(km, vm, qm, a, st) : run_tc<64, false>(km, vm, qm, a, st);
+    return c.bf16 ? run_tc<128, true>(km, vm, qm, a, st) : run_tc<128, false>(km, vm, qm, a, st);
 }
 
 }  // namespace attn
