@@ -53,7 +53,7 @@ constexpr float kLazy = 8.f;              // log2 units the maximum may lag
 struct Misc {
     ShareScratch<kThreads / 32> share;
     uint64_t kfull[kMaxSlots], kempty[kMaxSlots], vfull[kMaxSlots], vempty[kMaxSlots];
-    uint64_t q_full[2], q_empty[2], s_full[2], s_free[2], p_half[2], p_full[2], pv_done[2], o_full[2];
+    uint64_t q_full[2], q_empty[2], s_full[2], s_free[2], p_full[2], pv_done[2], o_full[2];
     uint64_t scrub[kMaxSlots], turn[2], fin[2];
     uint32_t tmem, dead;
     uint32_t odd;          // some value that not all rows saw was not finite
@@ -181,7 +181,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc05::mbar_init(m->q_empty + s, 1);
             tc05::mbar_init(m->s_full + s, 1);
             tc05::mbar_init(m->s_free + s, 4);
-            tc05::mbar_init(m->p_half + s, 4);
             tc05::mbar_init(m->p_full + s, 4);
             tc05::mbar_init(m->pv_done + s, 1);
             tc05::mbar_init(m->o_full + s, 1);
@@ -327,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t ahead_bits = 0;
             int ahead_n = 0, kslot = 0, vslot = 0;
             uint32_t kph = 0, vph = 0, qph = 0, tph = 0;
-            uint32_t hph = 0, fph = 0, frph = 0;  // bit s: p_half, p_full, s_free of stream s
+            uint32_t fph = 0, frph = 0;  // bit s: p_full, s_free of stream s
             bool live = true;
             auto await = [&](uint64_t *bar, uint32_t parity) {
                 live = __all_sync(0xFFFFFFFFu, live && wait(bar, parity, m, a.status));
@@ -377,7 +376,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 scores_done();
             };
             // The output of the oldest step: O (+)= P V.
-            auto output_issue = [&](int s, int hf) {  // of half the keys; kSplit: of half the columns
+            auto output_wait = [&](int s) {
+                await(m->vfull + vslot, vph);
+                await(m->p_full + s, (fph >> s) & 1u);
+                fph ^= 1u << s;
+            };
+            auto output_issue = [&](int s, int hf) {  // hf: kParted, which half of the columns
                 const uint32_t tp = tmem + kPcol + s * kPstep, to = tmem + kOcol + s * kOstep;
                 const uint64_t v = vdesc + (uint32_t)(vslot * (kTile >> 4));
                 if (elected()) {
@@ -389,30 +393,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 tc05::mma_ts(to, part == 2 ? to + 64 + k * 8 : tp + k * 16 + part * 8,
                                              v + (hf * (kKeys * 128) + k * 2048 >> 4), kIdescO,
                                              part < (kThird ? 2 : 1) || k > 0);
-                        tc05::mma_commit(m->pv_done + s);
                     } else {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            tc05::mma_ts(to, tp + hf * 32 + k * 8, v + (hf * 4 + k) * (2048 >> 4), kIdescO,
-                                         hf || k ? 1u : ~ahead_bits & 1u);
-                        if (kApart && hf) tc05::mma_commit(m->pv_done + s);
+                        for (int k = 0; k < kKeys / 16; ++k)
+                            tc05::mma_ts(to, tp + k * 8, v + k * (2048 >> 4), kIdescO, k ? 1u : ~ahead_bits & 1u);
                     }
+                    if (kSplit || kApart) tc05::mma_commit(m->pv_done + s);
                 }
                 __syncwarp();
             };
-            auto half_wait = [&](int s) {  // the first weights of a step
-                await(m->vfull + vslot, vph);
-                if (kSplit) {
-                    await(m->p_full + s, (fph >> s) & 1u);
-                    fph ^= 1u << s;
-                } else {
-                    await(m->p_half + s, (hph >> s) & 1u);
-                    hph ^= 1u << s;
-                }
-            };
             auto output_rest = [&](int s) {
-                if (kSplit && !kParted) return;
-                await(m->p_full + s, (fph >> s) & 1u);
+                if (!kParted) return;
+                await(m->p_full + s, (fph >> s) & 1u);  // (the first half has been taken)
                 fph ^= 1u << s;
                 if (!live) return;
                 tc05::fence_after_sync();
@@ -435,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 --ahead_n;
             };
             auto output = [&](int s) {
-                half_wait(s);
+                output_wait(s);
                 if (!live) return;
                 tc05::fence_after_sync();
                 output_issue(s, 0);
@@ -457,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // (the next item's queries may be on their way: then the turn passes first)
                     const bool more = n + 1 < units, held = more && qw.first(), now = more && !held;
                     if (now) scores_wait(me, true);
-                    half_wait(me);
+                    output_wait(me);
                     if (me || n) {
                         await(m->turn + me, tph);
                         tph ^= 1u;
@@ -465,8 +457,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!live) break;
                     tc05::fence_after_sync();
                     output_issue(me, 0);
-                    output_rest(me);
-                    if (!live) break;
                     if (now) scores_issue(me);
                     pass();
                     output_done(me);
@@ -521,10 +511,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t sp = 0, op = 0, vp = 0;  // phases of s_full, o_full, pv_done
         uint32_t scrub_ph = 0;            // bit x: phase of scrub[x]
         bool again = false;               // a step of this stream came before
-        CursorOf<true> c;
+        CursorOf<true> c, next;
         c.start(a, sh);
         const float boost = kBf16 ? 0.f : 7.f;
+        constexpr float kMost = kBf16 ? 1048576.f : 32768.f;
         const int piece = min(a.s.page, kKeys);
+        // The page of this lane's piece of step i of a segment (it is loaded a step ahead, and
+        // over the end of a segment).
+        auto page_of = [&](const CursorOf<true> &x, const Segment &g, int i) {
+            const int slot = x.at(g.j0 + i) * kKeys + lane * piece;
+            const bool need = lane * piece < kKeys && i < g.n && x.some(a, slot, slot + piece);
+            return need ? __ldg(a.s.table + (long long)x.b * a.s.max_pages + (slot >> a.s.lpage)) : 0;
+        };
+        int pid = page_of(c, Segment(c, units), kTwo ? 0 : s);
         for (int left = units; left > 0;) {
             const Segment sg(c, left);
             const Seq q = c.q;
@@ -536,13 +535,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             // this stream's steps: i0, i0 + kStep, ...
             constexpr int kStep = kTwo ? 1 : 2;
             const int i0 = kTwo ? 0 : (s ^ (units - left)) & 1;
-            // the page of this lane's piece of a step (a step ahead)
-            auto page_of = [&](int i) {
-                const int slot = c.at(sg.j0 + i) * kKeys + lane * piece;
-                const bool need = lane * piece < kKeys && i < sg.n && c.some(a, slot, slot + piece);
-                return need ? __ldg(trow + (slot >> a.s.lpage)) : 0;
-            };
-            int pid = page_of(i0);
             int t, g;
             const bool row_live = tile_row(a, q, c.rb * a.tpi + (kTwo ? s : 0), tid, t, g);
             const bool warp_live = __any_sync(0xFFFFFFFFu, row_live);
@@ -561,6 +553,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc05::fence_after_sync();
                 vp ^= 1u;
             };
+            auto scores_free = [&]() {  // S may be overwritten
+                tc05::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(m->s_free + s);
+            };
             auto give = [&](uint64_t *bar) {  // weights are in tensor memory
                 tc05::tmem_wait_st();
                 tc05::fence_before_sync();
@@ -571,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = i0; i < sg.n; i += kStep) {
                 const int j = c.at(sg.j0 + i);
                 const uint32_t gone = __ballot_sync(0xFFFFFFFFu, (unsigned)pid >= (unsigned)a.pages);
-                pid = page_of(i + kStep);
+                pid = page_of(c, sg, i + kStep);
                 const bool special = gone || !c.r.all(a, j * kKeys, (j + 1) * kKeys);
                 uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};  // this step's keys that the row sees
                 if (special && warp_live) {
@@ -646,23 +643,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // two elements an instruction: weight = 2^(s * sl2 - base)
                     const uint64_t sl2 = pack_f32x2(a.sl2, a.sl2);
                     uint64_t sum[2] = {0, 0};
-                    if constexpr (kSplit) {
-                        // Scores that a row must not see become -inf, and those of a
-                        // negative scale turn, in tensor memory.
-                        if (special || a.flip != 1.f) {
+                    if (special || a.flip != 1.f) {
+                        // Scores that a row must not see become -inf, and those of a negative
+                        // scale turn, in tensor memory, 32 at a time: nothing to do where all
+                        // rows of the warp see all, no look at them where none sees any.
+                        // (As selects among the registers' 128 scores the code that every step
+                        // jumps over cost all steps.)
 #pragma unroll 1
-                            for (int k = 0; k < 4; ++k) {
-                                const uint32_t w = k < 2 ? (k ? see[1] : see[0]) : (k == 2 ? see[2] : see[3]);
-                                uint32_t x[32];
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t w = k < 2 ? (k ? see[1] : see[0]) : (k == 2 ? see[2] : see[3]);
+                            uint32_t x[32];
+                            if (__any_sync(0xFFFFFFFFu, w != 0u)) {
+                                if (__all_sync(0xFFFFFFFFu, w == ~0u) && a.flip == 1.f) continue;
                                 tc05::tmem_ld32(ts + k * 32, x);
                                 tc05::tmem_wait_ld();
 #pragma unroll
                                 for (int e = 0; e < 32; ++e)
                                     x[e] = (w >> e) & 1u ? __float_as_uint(__uint_as_float(x[e]) * a.flip) : 0xFF800000u;
-                                tc05::tmem_st32(ts + k * 32, x);
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) x[e] = 0xFF800000u;
                             }
-                            tc05::tmem_wait_st();
+                            tc05::tmem_st32(ts + k * 32, x);
                         }
+                        tc05::tmem_wait_st();
+                    }
+                    if constexpr (kSplit) {
                         // The scores twice from tensor memory, 32 at a time: O has the registers.
                         float tm = -INFINITY;
 #pragma unroll
@@ -713,69 +719,78 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (kThird) tc05::tmem_st8(to + s * kOstep + 64 + h * 8, third);
                         }
                     } else {
-                        uint32_t x[4][32];
-                        float v[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) tc05::tmem_ld32(ts + k * 32, x[k]);
-                        tc05::tmem_wait_ld();
-                        if (kApart) {
-                            tc05::fence_before_sync();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(m->s_free + s);
-                        }
-                        // scores that a row must not see become -inf, those of a negative scale turn
-                        if (special || a.flip != 1.f)
-#pragma unroll
-                            for (int e = 0; e < 128; ++e)
-                                x[e >> 5][e & 31] = (see[e >> 5] >> (e & 31)) & 1u
-                                                        ? __float_as_uint(__uint_as_float(x[e >> 5][e & 31]) * a.flip)
-                                                        : 0xFF800000u;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            v[k] = fmaxf(__uint_as_float(x[k][0]), __uint_as_float(x[k][1]));
-#pragma unroll
-                            for (int e = 2; e < 32; e += 2)
-                                v[k] = max3(v[k], __uint_as_float(x[k][e]), __uint_as_float(x[k][e + 1]));
-                        }
-                        const float tm = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])) * a.sl2;
-                        if (kApart && again) products_done();
-                        const bool move = tm > mx + kLazy || (mx == -INFINITY && tm > mx);
-                        if (__any_sync(0xFFFFFFFFu, move)) {
-                            const float al = move ? ex2(mx - tm) : 1.f;
-                            if (move) mx = tm;
-                            l *= al;
-                            if (i > i0) {
-                                // all earlier products of this stream are done: they
-                                // were issued before this step's scores
+                        // P over S: weights from the maximum that the row has, which need not
+                        // be this step's. Only if they get too large for fp16, or for sums of
+                        // them (kMost), is the maximum looked for and the step begun again;
+                        // nothing has left the registers by then. (Maxima of every step: 553
+                        // us where this takes 4XX.) P apart: the maximum first, since S is
+                        // wanted free soon.
+                        uint32_t hi[4][16];
+                        bool look = kApart || __any_sync(0xFFFFFFFFu, row_live && mx == -INFINITY);
 #pragma unroll 1
-                                for (int k = 0; k < D / 16; ++k) {
-                                    uint32_t o[16];
-                                    tc05::tmem_ld16(to + s * kOstep + k * 16, o);
-                                    tc05::tmem_wait_ld();
+                        for (;;) {
+                            uint32_t x[4][32];
 #pragma unroll
-                                    for (int e = 0; e < 16; ++e)
-                                        o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
-                                    tc05::tmem_st16(to + s * kOstep + k * 16, o);
+                            for (int k = 0; k < 4; ++k) tc05::tmem_ld32(ts + k * 32, x[k]);
+                            tc05::tmem_wait_ld();
+                            if (kApart) scores_free();
+                            if (look) {
+                                float v[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(x[0][e]);
+#pragma unroll
+                                for (int e = 4; e < 128; ++e)
+                                    v[e & 3] = fmaxf(v[e & 3], __uint_as_float(x[e >> 5][e & 31]));
+                                const float tm = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])) * a.sl2;
+                                if (kApart && again) products_done();
+                                const bool move = tm > mx + kLazy || (mx == -INFINITY && tm > mx);
+                                if (__any_sync(0xFFFFFFFFu, move)) {
+                                    const float al = move ? ex2(mx - tm) : 1.f;
+                                    if (move) mx = tm;
+                                    l *= al;
+                                    if (i > i0) {
+                                        // all earlier products of this stream are done: they
+                                        // were issued before this step's scores
+#pragma unroll 1
+                                        for (int k = 0; k < D / 32; ++k) {
+                                            uint32_t o[32];
+                                            tc05::tmem_ld32(to + s * kOstep + k * 32, o);
+                                            tc05::tmem_wait_ld();
+#pragma unroll
+                                            for (int e = 0; e < 32; ++e)
+                                                o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+                                            tc05::tmem_st32(to + s * kOstep + k * 32, o);
+                                        }
+                                    }
                                 }
                             }
-                        }
-                        const float base = mx == -INFINITY ? 0.f : mx - boost;
-                        const uint64_t nb = pack_f32x2(-base, -base);
+                            const float base = mx == -INFINITY ? 0.f : mx - boost;
+                            const uint64_t nb = pack_f32x2(-base, -base);
+                            sum[0] = sum[1] = 0;
 #pragma unroll
-                        for (int h = 0; h < 4; ++h) {
-                            uint32_t hi[16];
+                            for (int h = 0; h < 4; ++h) {
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) {
-                                float p0, p1;
-                                unpack_f32x2(fma_f32x2(pack_u32x2(x[h][2 * e], x[h][2 * e + 1]), sl2, nb), p0, p1);
-                                p0 = ex2(p0);
-                                p1 = ex2(p1);
-                                sum[e & 1] = add_f32x2(sum[e & 1], pack_f32x2(p0, p1));
-                                hi[e] = pack2<kBf16>(p0, p1);
+                                for (int e = 0; e < 16; ++e) {
+                                    float p0, p1;
+                                    unpack_f32x2(fma_f32x2(pack_u32x2(x[h][2 * e], x[h][2 * e + 1]), sl2, nb), p0, p1);
+                                    p0 = ex2(p0);
+                                    p1 = ex2(p1);
+                                    sum[e & 1] = add_f32x2(sum[e & 1], pack_f32x2(p0, p1));
+                                    hi[h][e] = pack2<kBf16>(p0, p1);
+                                }
+                                if (kApart) tc05::tmem_st16(tw + h * 16, hi[h]);
                             }
-                            tc05::tmem_st16(tw + h * 16, hi);
-                            if (h == 1) give(m->p_half);
+                            if (kApart) break;
+                            float s0, s1, s2, s3;
+                            unpack_f32x2(sum[0], s0, s1);
+                            unpack_f32x2(sum[1], s2, s3);
+                            const bool large = row_live && !((s0 + s1) + (s2 + s3) <= kMost);
+                            if (look || !__any_sync(0xFFFFFFFFu, large)) break;
+                            look = true;
                         }
+                        if (!kApart)
+#pragma unroll
+                            for (int h = 0; h < 4; ++h) tc05::tmem_st16(tw + h * 16, hi[h]);
                         give(m->p_full);
                     }
                     float s0, s1, s2, s3;
@@ -784,12 +799,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     l += (s0 + s1) + (s2 + s3);
                 } else if (!kSplit) {  // a warp without rows: the arrivals alone
                     if (kApart) {
-                        tc05::fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(m->s_free + s);
+                        scores_free();
                         if (again) products_done();
                     }
-                    give(m->p_half);
                     give(m->p_full);
                 }
                 if constexpr (kSplit) {  // this step's share of O
@@ -824,6 +836,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc05::tmem_st32(to + s * kOstep + k * 32, *reinterpret_cast<uint32_t(*)[32]>(o));
                 }
                 tc05::tmem_wait_st();
+            }
+            next = c;
+            if (left > sg.n) {
+                next.next_item(a);
+                pid = page_of(next, Segment(next, left - sg.n), kTwo ? 0 : (s ^ (units - left + sg.n)) & 1);
             }
             wait(m->o_full + s, op, m, a.status);
             op ^= 1;
@@ -933,7 +950,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (!kTwo) pair_sync();  // O and the maxima may be overwritten
             left -= sg.n;
-            if (left > 0) c.next_item(a);
+            c = next;
         }
     }
     tc05::fence_before_sync();

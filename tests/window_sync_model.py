@@ -22,8 +22,8 @@ def window_tc(seed, segments, stages, two, apart=False, split=False, parted=Fals
     kring, vring = Ring(sim, "keys'", stages[0], nq), Ring(sim, "values'", stages[1], nq)
     turns = two and not split and not apart
     B = lambda name, count: [Barrier(f"{name}[{s}]", count) for s in range(2)]  # noqa: E731
-    q_full, q_empty, s_full, s_free, p_half, p_full, pv_done, o_full, scrub, turn = (
-        B("q_full", 1), B("q_empty", 1), B("s_full", 1), B("s_free", 4), B("p_half", 4), B("p_full", 4),
+    q_full, q_empty, s_full, s_free, p_full, pv_done, o_full, scrub, turn = (
+        B("q_full", 1), B("q_empty", 1), B("s_full", 1), B("s_free", 4), B("p_full", 4),
         B("pv_done", 1), B("o_full", 1),
         [Barrier(f"scrub[{i}]", 4) for i in range(stages[1] if own_scrub else 2)], B("turn", 1))
     steps = [(k, i, i == len(seg) - 1, sp) for k, seg in enumerate(segments) for i, sp in enumerate(seg)]
@@ -55,7 +55,7 @@ def window_tc(seed, segments, stages, two, apart=False, split=False, parted=Fals
             yield sim.jitter(60)
 
     def products(me):
-        at = {"q": 0, "o": 0, "fr": [0, 0], "h": [0, 0], "f": [0, 0], "t": 0}
+        at = {"q": 0, "o": 0, "fr": [0, 0], "f": [0, 0], "t": 0}
 
         def scores_wait(s, again):
             n = at["q"]
@@ -92,11 +92,10 @@ def window_tc(seed, segments, stages, two, apart=False, split=False, parted=Fals
             scores_issue(s)
             scores_done()
 
-        def half_wait(s):
+        def output_wait(s):
             yield vring.landed_wait(at["o"])
-            bar, c = (p_full, "f") if split else (p_half, "h")
-            yield bar[s], at[c][s]
-            at[c][s] += 1
+            yield p_full[s], at["f"][s]
+            at["f"][s] += 1
 
         def output_issue(s, part):
             n = at["o"]
@@ -107,19 +106,17 @@ def window_tc(seed, segments, stages, two, apart=False, split=False, parted=Fals
                     raise Broken(f"values of step {n} before they were looked at")
                 if i < (1 if two else 2) and k and o_taken[s].get(k - 1, 0) != (4 if two else 8):
                     raise Broken(f"O of segment {k} over that of {k - 1}")
-            if p_written[s].get(n, 0) != 4 and (part or split):
-                raise Broken(f"product of step {n} before its weights")
-            unit.product(256 if split or parted else 128)
-            if split:
+                if p_written[s].get(n, 0) != 4:
+                    raise Broken(f"product of step {n} before its weights")
+            unit.product(256)
+            if split or apart:
                 unit.commit(pv_done[s])
 
         def output_rest(s):
-            if not split or parted:
+            if parted:
                 yield p_full[s], at["f"][s]
                 at["f"][s] += 1
                 output_issue(s, 1)
-                if apart:
-                    unit.commit(pv_done[s])
             o_end[s][at["o"]] = unit.free
 
         def output_done(s):
@@ -132,7 +129,7 @@ def window_tc(seed, segments, stages, two, apart=False, split=False, parted=Fals
             at["o"] += 1
 
         def output(s):
-            yield from half_wait(s)
+            yield from output_wait(s)
             output_issue(s, 0)
             yield from output_rest(s)
             output_done(s)
@@ -146,7 +143,7 @@ def window_tc(seed, segments, stages, two, apart=False, split=False, parted=Fals
                 now = more and not held
                 if now:
                     yield from scores_wait(me, True)
-                yield from half_wait(me)
+                yield from output_wait(me)
                 if me or n:
                     yield turn[me], at["t"]
                     at["t"] += 1
@@ -222,10 +219,7 @@ def window_tc(seed, segments, stages, two, apart=False, split=False, parted=Fals
                         vp += 1
                 if last is not None and sim.now < o_end[s].get(last, float("inf")):
                     raise Broken(f"step {x} moves O or writes weights before the products of {last} end")
-                yield sim.jitter(300)
-                if not split:
-                    sim.arrive(p_half[s])
-                    yield sim.jitter(300)
+                yield sim.jitter(600)
                 p_written[s][x] = p_written[s].get(x, 0) + 1
                 if not split:
                     sim.arrive(p_full[s])
