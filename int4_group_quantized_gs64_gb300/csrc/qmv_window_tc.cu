@@ -54,7 +54,9 @@ struct Misc {
     ShareScratch<kThreads / 32> share;
     uint64_t kfull[kMaxSlots], kempty[kMaxSlots], vfull[kMaxSlots], vempty[kMaxSlots];
     uint64_t q_full[2], q_empty[2], s_full[2], s_free[2], p_full[2], pv_done[2], o_full[2];
-    uint64_t scrub[kMaxSlots], turn[2], fin[2];
+    uint64_t vready[kMaxSlots];  // values have been looked at
+    uint64_t turn[2], fin[2];
+    uint32_t kflag[kMaxSlots];  // of the step whose keys lie there: 1 first of its segment, 2 last
     uint32_t tmem, dead;
     uint32_t odd;          // some value that not all rows saw was not finite
     float2 ml[2][128];     // !kTwo: the streams' maxima and sums
@@ -121,26 +123,6 @@ struct Segment {
     }
 };
 
-// All steps of a block, one after the other.
-struct Walk {
-    CursorOf<true> c;
-    int left, n, i;  // steps from this segment's start on, its steps, the place among them
-    __device__ __forceinline__ Walk(const CursorOf<true> &start, int units) : c(start), left(units), i(0) {
-        n = min(c.nu - c.u, left);
-    }
-    __device__ __forceinline__ bool first() const { return i == 0; }
-    __device__ __forceinline__ bool last() const { return i == n - 1; }
-    __device__ __forceinline__ void advance(const TreeArgs &a) {
-        if (++i < n) return;
-        left -= n;
-        i = 0;
-        if (left > 0) {
-            c.next_item(a);
-            n = min(c.nu, left);
-        }
-    }
-};
-
 template <int D, bool kBf16, bool kTwo, bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     k_window_tc(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -174,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc05::mbar_init(m->kempty + i, kQ);
             tc05::mbar_init(m->vfull + i, 1);
             tc05::mbar_init(m->vempty + i, kQ);
-            tc05::mbar_init(m->scrub + i, 4);
+            tc05::mbar_init(m->vready + i, 1);
         }
         for (int s = 0; s < 2; ++s) {
             tc05::mbar_init(m->q_full + s, 1);
@@ -237,6 +219,65 @@ __global__ void __launch_bounds__(kThreads, 1)
             lv = lane * prow < kKeys && c.some(a, slot, slot + prow);
             return lv ? __ldg(a.s.table + (long long)c.b * a.s.max_pages + (slot >> a.s.lpage)) : 0;
         };
+        // Values that some row must not see are kept out of the product where zero times
+        // them is not zero: a step behind its copies the values' warp looks at them, in the
+        // steps that not all rows see whole; keys that no row of the item sees, or without
+        // a page, get zeros, and of those that some rows see infinities and NaNs are
+        // replaced (the rows that see them get them added when O is written).
+        struct {
+            int j, p0, p1, lo, stage;
+            uint32_t gone, phase;  // pieces without a page
+        } was;
+        was.stage = -1;
+        auto look = [&]() {
+            if (was.stage < 0) return;
+            Reach r;
+            r.p0 = was.p0;
+            r.p1 = was.p1;
+            r.lo = was.lo;
+            if (wait(m->vfull + was.stage, was.phase, m, a.status) &&
+                (was.gone || !r.all(a, was.j * kKeys, (was.j + 1) * kKeys))) {
+                __syncwarp();
+#pragma unroll 1
+                for (int x = lane; x < kKeys; x += 32) {
+                    const int key = was.j * kKeys + x;
+                    uint8_t *row = vring + was.stage * kTile + x * 128;
+                    auto at_chunk = [&](int ch) {
+                        return reinterpret_cast<uint4 *>(row + (ch >> 3) * (kKeys * 128) +
+                                                         (((ch & 7) ^ (x & 7)) << 4));
+                    };
+                    if (!r.some(a, key, key + 1) || ((was.gone >> (x / prow)) & 1u)) {
+#pragma unroll
+                        for (int ch = 0; ch < D / 8; ++ch) *at_chunk(ch) = make_uint4(0u, 0u, 0u, 0u);
+                    } else if (!r.all(a, key, key + 1)) {
+                        uint32_t top = 0;  // the largest magnitudes of even and odd elements
+#pragma unroll
+                        for (int ch = 0; ch < D / 8; ++ch) {
+                            const uint4 v = *at_chunk(ch);
+                            top = __vimax3_u16x2(top, v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu);
+                            top = __vimax3_u16x2(top, v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu);
+                        }
+                        if (nonfinite2<kBf16>(top)) {
+                            atomicOr(&m->odd, 1u);
+#pragma unroll 1
+                            for (int ch = 0; ch < D / 8; ++ch) {
+                                uint4 v = *at_chunk(ch);
+                                uint32_t *y = reinterpret_cast<uint32_t *>(&v);
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    if (nonfinite2<kBf16>(y[e] & 0xFFFFu)) y[e] &= 0xFFFF0000u;
+                                    if (nonfinite2<kBf16>(y[e] & 0xFFFF0000u)) y[e] &= 0xFFFFu;
+                                }
+                                *at_chunk(ch) = v;
+                            }
+                        }
+                    }
+                }
+                tc05::fence_proxy_async();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(m->vready + was.stage);
+        };
         bool live;
         int pid = page_of(c.u, live);
         bool ok = true;
@@ -268,12 +309,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int row =
                     (pid * a.Hkv + c.h) * a.s.page + ((c.at(sg.j0 + t) * kKeys + lane * prow) & (a.s.page - 1));
                 if (live && !good && keys) set_status(a.status, kStPage);
-                if (t + 1 < sg.n) pid = page_of(sg.j0 + t + 1, live);
                 const uint32_t n = __popc(__ballot_sync(0xFFFFFFFFu, good));
+                const uint32_t gone = __ballot_sync(0xFFFFFFFFu, live && !good);
+                if (t + 1 < sg.n) pid = page_of(sg.j0 + t + 1, live);
                 ok = ok && wait(empty + stage, phase, m, a.status);
                 ok = __all_sync(0xFFFFFFFFu, ok);
                 if (!ok) continue;
                 if (lane == 0) {
+                    if (keys) m->kflag[stage] = (t == 0 ? 1u : 0u) | (t == sg.n - 1 ? 2u : 0u);
                     if (n)
                         mbar_expect_tx(full + stage, n * prow * D * 2);
                     else
@@ -289,6 +332,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         else
                             tma_load3(dst + hf * (kKeys * 128), map, 0, row, hf, full + stage);
                 }
+                if (!keys) {
+                    look();
+                    was.j = c.at(sg.j0 + t);
+                    was.p0 = c.r.p0;
+                    was.p1 = c.r.p1;
+                    was.lo = c.r.lo;
+                    was.stage = stage;
+                    was.gone = gone;
+                    was.phase = phase ^ 1u;
+                }
                 pending |= 1u << stage;
                 pending_ph = (pending_ph & ~(1u << stage)) | ((phase ^ 1u) & 1u) << stage;
                 if (++stage == slots) {
@@ -302,6 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 pid = page_of(c.u, live);
             }
         }
+        if (!keys) look();
         if (!ok) {  // gave up: wait (bounded) for this warp's copies in flight
             for (int i = 0; i < slots; ++i)
                 if ((pending >> i) & 1u) tc05::mbar_wait(full + i, (pending_ph >> i) & 1u, kPoll / 64);
@@ -313,14 +367,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         // kTwo: a warp a stream. The warp walks its steps as a whole and one elected lane
         // issues: operands that the compiler sees to be uniform go to a product in some 10
         // cycles, where a lone thread's took 48 of the 64 that the product runs for.
-        CursorOf<true> start;
-        start.start(a, sh);
         {
             const int me = warp - 9;  // kTwo: the stream
             const uint64_t kdesc = tc05::sdesc_sw128(tc05::smem_addr(kring));
             const uint64_t vdesc = tc05::sdesc_sw128_mn(tc05::smem_addr(vring), kKeys * 128);
             const uint64_t qdesc = tc05::sdesc_sw128(tc05::smem_addr(qs)) + (uint32_t)(me * (kTile >> 4));
-            Walk qw(start, units);  // of the scores
+            // the next scores' step: whether its keys have been waited for, its flags, and
+            // its place in its segment
+            bool seen = false;
+            uint32_t flag = 0;
+            int place = 0;
             // the outputs' steps lag at most two behind: bits 2 x and 2 x + 1 say of the
             // x-th whether its stream's O begins anew and whether the segment ends
             uint32_t ahead_bits = 0;
@@ -332,12 +388,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 live = __all_sync(0xFFFFFFFFu, live && wait(bar, parity, m, a.status));
             };
             // The scores of a step: what they wait for, the products, and what they tell.
+            auto peek = [&]() {
+                if (seen) return;
+                await(m->kfull + kslot, kph);
+                flag = *(volatile uint32_t *)(m->kflag + kslot);
+                seen = true;
+                place = flag & 1u ? 0 : place + 1;
+            };
             auto scores_wait = [&](int s, bool again) {  // again: not the stream's first
-                if (qw.first()) {
+                peek();
+                if (flag & 1u) {
                     await(m->q_full + me, qph);
                     qph ^= 1u;
                 }
-                await(m->kfull + kslot, kph);
                 if (kApart && again) {
                     await(m->s_free + s, (frph >> s) & 1u);
                     frph ^= 1u << s;
@@ -358,15 +421,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto scores_done = [&]() {
                 if (elected()) {
                     tc05::mma_commit(m->kempty + kslot);
-                    if (qw.last()) tc05::mma_commit(m->q_empty + me);
+                    if (flag & 2u) tc05::mma_commit(m->q_empty + me);
                 }
                 __syncwarp();
-                ahead_bits |= ((qw.i < (kTwo ? 1 : 2) ? 1u : 0u) | (qw.last() ? 2u : 0u)) << (2 * ahead_n++);
+                ahead_bits |= ((place < (kTwo ? 1 : 2) ? 1u : 0u) | (flag & 2u)) << (2 * ahead_n++);
+                seen = false;
                 if (++kslot == kslots) {
                     kslot = 0;
                     kph ^= 1u;
                 }
-                qw.advance(a);
             };
             auto scores = [&](int s, bool again) {
                 scores_wait(s, again);
@@ -377,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             // The output of the oldest step: O (+)= P V.
             auto output_wait = [&](int s) {
-                await(m->vfull + vslot, vph);
+                await(m->vready + vslot, vph);
                 await(m->p_full + s, (fph >> s) & 1u);
                 fph ^= 1u << s;
             };
@@ -447,7 +510,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (int n = 0; n < units && live; ++n) {
                     // (the next item's queries may be on their way: then the turn passes first)
-                    const bool more = n + 1 < units, held = more && qw.first(), now = more && !held;
+                    const bool more = n + 1 < units;
+                    if (more) peek();
+                    const bool held = more && (flag & 1u), now = more && !held;
                     if (now) scores_wait(me, true);
                     output_wait(me);
                     if (me || n) {
@@ -481,17 +546,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ++qn;
                     }
                 };
+                auto starts = [&]() {  // whether the next step begins a segment
+                    peek();
+                    return (flag & 1u) != 0;
+                };
                 ahead(1);
-                if (units > 1 && !qw.first()) ahead(2);
+                if (units > 1 && !starts()) ahead(2);
 #pragma unroll 1
                 for (int n = 0; n < units && live; ++n) {
                     // S of step n + 2, and before it those that an item's start held
                     // back: they wait for its queries, so the outputs before go first
-                    if (kApart && qn == n + 2 && qn < units && !qw.first()) ahead(n + 3);
+                    if (kApart && qn == n + 2 && qn < units && !starts()) ahead(n + 3);
                     ahead(n + 1);
                     output(n & 1);
                     ahead(n + 2);
-                    if (qn < units && !qw.first()) ahead(n + 3);
+                    if (qn < units && !starts()) ahead(n + 3);
                 }
             }
             // nothing of this warp's is in flight when the block ends
@@ -509,7 +578,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t ts = tmem + lanes + s * 128, to = tmem + lanes + kOcol;
         const uint32_t tw = tmem + lanes + kPcol + s * kPstep;  // weights
         uint32_t sp = 0, op = 0, vp = 0;  // phases of s_full, o_full, pv_done
-        uint32_t scrub_ph = 0;            // bit x: phase of scrub[x]
         bool again = false;               // a step of this stream came before
         CursorOf<true> c, next;
         c.start(a, sh);
@@ -528,10 +596,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Segment sg(c, left);
             const Seq q = c.q;
             const int32_t *trow = a.s.table + (long long)c.b * a.s.max_pages;
-            // whether the page of some needed slot among n from `slot` on is missing
-            auto missing = [&](int slot, int n) {
-                return c.some(a, slot, slot + n) && (unsigned)trow[slot >> a.s.lpage] >= (unsigned)a.pages;
-            };
             // this stream's steps: i0, i0 + kStep, ...
             constexpr int kStep = kTwo ? 1 : 2;
             const int i0 = kTwo ? 0 : (s ^ (units - left)) & 1;
@@ -586,59 +650,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 sp ^= 1;
                 tc05::fence_after_sync();
-                if (special) {
-                    const int at = units - left + i, vslot = at % vslots;  // the step's place in the ring
-                    // Values that some row must not see are kept out of the product
-                    // where zero times them is not zero, by the first stream for both:
-                    // a thread a key, zeros where no row sees it or there is no page,
-                    // and where some rows see it its infinities and NaNs replaced.
-                    if (!kTwo || s == 0) {
-                        if (wait(m->vfull + vslot, (uint32_t)(at / vslots) & 1u, m, a.status)) {
-                            const int key = j * kKeys + tid;
-                            uint8_t *row = vring + vslot * kTile + tid * 128;
-                            const bool none = !c.some(a, key, key + 1) || (gone && missing(key, 1));
-                            auto at_chunk = [&](int ch) {
-                                return reinterpret_cast<uint4 *>(
-                                    row + (ch >> 3) * (kKeys * 128) + (((ch & 7) ^ (tid & 7)) << 4));
-                            };
-                            if (none) {
-#pragma unroll
-                                for (int ch = 0; ch < D / 8; ++ch) *at_chunk(ch) = make_uint4(0u, 0u, 0u, 0u);
-                            } else if (!c.r.all(a, key, key + 1)) {
-                                uint32_t top = 0;  // the largest magnitudes of even and odd elements
-#pragma unroll
-                                for (int ch = 0; ch < D / 8; ++ch) {
-                                    const uint4 v = *at_chunk(ch);
-                                    top = __vimax3_u16x2(top, v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu);
-                                    top = __vimax3_u16x2(top, v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu);
-                                }
-                                if (nonfinite2<kBf16>(top)) {
-                                    atomicOr(&m->odd, 1u);
-#pragma unroll 1
-                                    for (int ch = 0; ch < D / 8; ++ch) {
-                                        uint4 v = *at_chunk(ch);
-                                        uint32_t *x = reinterpret_cast<uint32_t *>(&v);
-#pragma unroll
-                                        for (int e = 0; e < 4; ++e) {
-                                            if (nonfinite2<kBf16>(x[e] & 0xFFFFu)) x[e] &= 0xFFFF0000u;
-                                            if (nonfinite2<kBf16>(x[e] & 0xFFFF0000u)) x[e] &= 0xFFFFu;
-                                        }
-                                        *at_chunk(ch) = v;
-                                    }
-                                }
-                            }
-                        }
-                        tc05::fence_proxy_async();
-                        __syncwarp();
-                        if (kTwo && lane == 0) mbar_arrive(m->scrub + vslot);
-                    } else {
-                        // (a barrier a slot: the first stream may be steps ahead, but not
-                        // in this slot again)
-                        wait(m->scrub + vslot, (scrub_ph >> vslot) & 1u, m, a.status);
-                        __syncwarp();
-                    }
-                    scrub_ph ^= 1u << vslot;
-                }
                 if (warp_live) {
                     // two elements an instruction: weight = 2^(s * sl2 - base)
                     const uint64_t sl2 = pack_f32x2(a.sl2, a.sl2);
@@ -657,9 +668,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 if (__all_sync(0xFFFFFFFFu, w == ~0u) && a.flip == 1.f) continue;
                                 tc05::tmem_ld32(ts + k * 32, x);
                                 tc05::tmem_wait_ld();
+                                if (a.flip != 1.f)
 #pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    x[e] = (w >> e) & 1u ? __float_as_uint(__uint_as_float(x[e]) * a.flip) : 0xFF800000u;
+                                    for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * a.flip);
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) x[e] = w & (1u << e) ? x[e] : 0xFF800000u;
                             } else {
 #pragma unroll
                                 for (int e = 0; e < 32; ++e) x[e] = 0xFF800000u;

@@ -35,10 +35,9 @@ def test_attention(form):
             model.window_tc(seed, segments(seed), **FORMS[form], **times)
 
 
-def test_two_barriers_for_the_values_looked_at_are_noticed():
-    """The first stream can be steps ahead: the second waits for a phase that has passed."""
-    assert noticed(lambda seed: model.window_tc(seed, segments(seed), **FORMS["two_d64"], copy=300, slow=100,
-                                                own_scrub=False))
+def test_products_that_do_not_wait_for_the_look_at_values_are_noticed():
+    assert noticed(lambda seed: model.window_tc(seed, segments(seed), **FORMS["two_d128"], copy=300, slow=100,
+                                                wait_ready=False))
 
 
 def test_new_weights_before_the_last_products_are_noticed():

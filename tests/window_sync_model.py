@@ -10,22 +10,23 @@ from attn_sync_model import Barrier, Broken, Issuer, Ring, Sim
 
 
 def window_tc(seed, segments, stages, two, apart=False, split=False, parted=False, copy=2000.0, slow=20.0,
-              own_scrub=True, wait_done=True):
+              wait_ready=True, wait_done=True):
     """One block over segments, lists of steps that are true where values have to be looked at.
 
-    stages: slots for keys and for values. own_scrub False: two barriers, not one a slot, for
-    the values that the first stream has looked at. wait_done False: with weights beside the
-    scores, warps do not wait for the last products before they hand over new weights."""
+    stages: slots for keys and for values. wait_ready False: products wait for values that
+    have come, not for those that have been looked at. wait_done False: with weights beside the
+    scores, warps do not wait for the last products before they hand over new ones."""
     rng = random.Random(seed)
     sim = Sim(rng, slow)
     nq = 2 if two else 1
     kring, vring = Ring(sim, "keys'", stages[0], nq), Ring(sim, "values'", stages[1], nq)
     turns = two and not split and not apart
     B = lambda name, count: [Barrier(f"{name}[{s}]", count) for s in range(2)]  # noqa: E731
-    q_full, q_empty, s_full, s_free, p_full, pv_done, o_full, scrub, turn = (
+    q_full, q_empty, s_full, s_free, p_full, pv_done, o_full, turn = (
         B("q_full", 1), B("q_empty", 1), B("s_full", 1), B("s_free", 4), B("p_full", 4),
         B("pv_done", 1), B("o_full", 1),
-        [Barrier(f"scrub[{i}]", 4) for i in range(stages[1] if own_scrub else 2)], B("turn", 1))
+        B("turn", 1))
+    vready = [Barrier(f"vready[{i}]", 1) for i in range(stages[1])]
     steps = [(k, i, i == len(seg) - 1, sp) for k, seg in enumerate(segments) for i, sp in enumerate(seg)]
     total = len(steps)
     streams = (lambda n: (0, 1)) if two else (lambda n: (n & 1,))
@@ -35,6 +36,14 @@ def window_tc(seed, segments, stages, two, apart=False, split=False, parted=Fals
     o_taken, o_end = [{}, {}], [{}, {}]             # warps that have taken a segment's O; when products end
     p_written = [{}, {}]                            # warps' parts of a step's weights
     scrubbed = {}
+
+    def look(n):
+        if n >= 0:
+            yield vring.landed_wait(n)
+            vring.read(n)
+            yield sim.jitter(400 if steps[n][3] else 30)
+            scrubbed[n] = 1
+            sim.arrive(vready[n % stages[1]])
 
     def copier(ring):
         k = -1
@@ -53,15 +62,26 @@ def window_tc(seed, segments, stages, two, apart=False, split=False, parted=Fals
             yield ring.may_copy(n)
             ring.copy(n, copy)
             yield sim.jitter(60)
+            if ring is vring:
+                yield from look(n - 1)
+        if ring is vring:
+            yield from look(total - 1)
 
     def products(me):
-        at = {"q": 0, "o": 0, "fr": [0, 0], "f": [0, 0], "t": 0}
+        at = {"q": 0, "seen": -1, "o": 0, "fr": [0, 0], "f": [0, 0], "t": 0}
+
+        def peek():  # the keys of the next scores' step have come, and with them its flags
+            n = at["q"]
+            if at["seen"] != n:
+                yield kring.landed_wait(n)
+                kring.read(n)
+                at["seen"] = n
 
         def scores_wait(s, again):
             n = at["q"]
+            yield from peek()
             if steps[n][1] == 0:
                 yield q_full[me], steps[n][0]
-            yield kring.landed_wait(n)
             if apart and again:
                 yield s_free[s], at["fr"][s]
                 at["fr"][s] += 1
@@ -93,7 +113,8 @@ def window_tc(seed, segments, stages, two, apart=False, split=False, parted=Fals
             scores_done()
 
         def output_wait(s):
-            yield vring.landed_wait(at["o"])
+            n = at["o"]
+            yield (vready[n % stages[1]], n // stages[1]) if wait_ready else vring.landed_wait(n)
             yield p_full[s], at["f"][s]
             at["f"][s] += 1
 
@@ -102,7 +123,7 @@ def window_tc(seed, segments, stages, two, apart=False, split=False, parted=Fals
             k, i, _, special = steps[n]
             if part == 0:
                 vring.read(n)
-                if special and scrubbed.get(n, 0) != 4:
+                if special and n not in scrubbed:
                     raise Broken(f"values of step {n} before they were looked at")
                 if i < (1 if two else 2) and k and o_taken[s].get(k - 1, 0) != (4 if two else 8):
                     raise Broken(f"O of segment {k} over that of {k - 1}")
@@ -139,6 +160,8 @@ def window_tc(seed, segments, stages, two, apart=False, split=False, parted=Fals
             yield from scores(me, False)
             for n in range(total):
                 more = n + 1 < total
+                if more:
+                    yield from peek()
                 held = more and starts()
                 now = more and not held
                 if now:
@@ -172,21 +195,26 @@ def window_tc(seed, segments, stages, two, apart=False, split=False, parted=Fals
                 while at["q"] < total and at["q"] < upto:
                     yield from scores(at["q"] & 1, at["q"] >= 2)
             yield from ahead(1)
-            if total > 1 and not starts():
-                yield from ahead(2)
+            if total > 1:
+                yield from peek()
+                if not starts():
+                    yield from ahead(2)
             for n in range(total):
-                if apart and at["q"] == n + 2 and at["q"] < total and not starts():
-                    yield from ahead(n + 3)
+                if apart and at["q"] == n + 2 and at["q"] < total:
+                    yield from peek()
+                    if not starts():
+                        yield from ahead(n + 3)
                 yield from ahead(n + 1)
                 yield from output(n & 1)
                 yield from ahead(n + 2)
-                if at["q"] < total and not starts():
-                    yield from ahead(n + 3)
+                if at["q"] < total:
+                    yield from peek()
+                    if not starts():
+                        yield from ahead(n + 3)
                 yield sim.jitter(20)
 
     def softmax(s, w):
         sp = op = vp = 0
-        looked = [0] * len(scrub)
         again, n, last = False, 0, None
         for k, seg in enumerate(segments):
             mine = []
@@ -199,17 +227,6 @@ def window_tc(seed, segments, stages, two, apart=False, split=False, parted=Fals
                 sp += 1
                 if s_holds[s] != x:
                     raise Broken(f"softmax of step {x} reads scores of {s_holds[s]}")
-                if special:
-                    if not two or s == 0:
-                        yield vring.landed_wait(x)
-                        vring.read(x)
-                        yield sim.jitter(200)
-                        scrubbed[x] = scrubbed.get(x, 0) + 1
-                        if two:
-                            sim.arrive(scrub[x % len(scrub)])
-                    else:
-                        yield scrub[x % len(scrub)], looked[x % len(scrub)]
-                        looked[x % len(scrub)] += 1
                 yield sim.jitter(150)
                 s_read[s][x] = s_read[s].get(x, 0) + 1
                 if apart:
