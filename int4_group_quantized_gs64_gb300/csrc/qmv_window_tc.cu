@@ -104,6 +104,19 @@ __device__ __forceinline__ void tma_load4(uint32_t dst, const CUtensorMap *map, 
         : "memory");
 }
 
+// 32 bytes (a whole sector) where `wide`, which wants p on a 32-byte boundary; else 16 twice.
+__device__ __forceinline__ void store32(void *p, bool wide, const uint32_t (&x)[8]) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]),
+                     "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                     : "memory");
+    } else {
+        uint4 *q = static_cast<uint4 *>(p);
+        q[0] = make_uint4(x[0], x[1], x[2], x[3]);
+        q[1] = make_uint4(x[4], x[5], x[6], x[7]);
+    }
+}
+
 // The upper halves of two floats, which are bf16 numbers, and what they leave.
 __device__ __forceinline__ uint32_t cut_bf16x2(float &x, float &y) {
     const uint32_t u = __float_as_uint(x), v = __float_as_uint(y);
@@ -886,6 +899,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool none = sg.whole && L == 0.f;  // no weight: zero, also where a value is infinite
                 const long long row = (long long)(q.first + t) * a.Hq + c.h * a.G + g;
                 const int seg_last = left == units ? 0 : 1, prow = (kTwo ? s * 128 : 0) + tid;
+                const bool wide = reinterpret_cast<uintptr_t>(a.o) % 32 == 0;
                 const bool odd = *(volatile uint32_t *)&m->odd != 0;  // values to add by hand
                 const int k0 = kTwo ? 0 : s * (D / 64), k1 = kTwo ? D / 32 : k0 + D / 64;
                 auto columns = [&](int k, float (&o)[32]) {  // columns 32 k .. 32 k + 31 of O, out
@@ -918,18 +932,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                             *reinterpret_cast<float4 *>(p + e * (a.rows * 4LL)) =
                                 make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                     } else if (kSplit) {  // (an fp32 output)
-                        float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(a.o) + row * D + k * 32);
+                        float *p = static_cast<float *>(a.o) + row * D + k * 32;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            p[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t x[8];
+#pragma unroll
+                            for (int z = 0; z < 8; ++z) x[z] = __float_as_uint(o[8 * e + z]);
+                            store32(p + 8 * e, wide, x);
+                        }
                     } else {
-                        uint4 *p = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.o) + row * D + k * 32);
+                        uint16_t *p = static_cast<uint16_t *>(a.o) + row * D + k * 32;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            p[e] = make_uint4(pack2<kBf16>(o[8 * e], o[8 * e + 1]),
-                                              pack2<kBf16>(o[8 * e + 2], o[8 * e + 3]),
-                                              pack2<kBf16>(o[8 * e + 4], o[8 * e + 5]),
-                                              pack2<kBf16>(o[8 * e + 6], o[8 * e + 7]));
+                        for (int e = 0; e < 2; ++e) {
+                            uint32_t x[8];
+#pragma unroll
+                            for (int z = 0; z < 8; ++z) x[z] = pack2<kBf16>(o[16 * e + 2 * z], o[16 * e + 2 * z + 1]);
+                            store32(p + 16 * e, wide, x);
+                        }
                     }
                 };
 #pragma unroll 1
