@@ -51,6 +51,7 @@ struct TreeArgs {
     // kWin: a row at slot p sees j <= p with j > p - window or j < sinks
     int window, sinks;
     int lunit;       // unit = 1 << lunit
+    int align;       // slots in a row that are copied together, a power of two
     // Rows come in tiles of whole tokens: tile x of a sequence holds the tokens from
     // x / hs * tb on, tb of them, and of their G query heads those from x % hs * hb
     // on, hb of them (all, unless G is above 128). An item is tpi tiles.
@@ -88,30 +89,6 @@ __device__ __forceinline__ bool tile_row(const TreeArgs &a, const Seq &q, int ti
     return x < a.tb && t < q.T && g < a.G;
 }
 
-// kWin: the keys that some row of an item sees: slots [lo, p1] and those below
-// a.sinks. They are looked at in units of a.unit slots on a grid from slot 0; `us`
-// units hold first keys only, the rest begin at `shift` units more.
-struct Reach {
-    int p0, p1, lo, us, shift, nu;
-    __device__ __forceinline__ void set(const TreeArgs &a, const Seq &q, int item) {
-        const int x = item * a.tpi, y = min(x + a.tpi, row_tiles(a, q)) - 1;
-        p0 = q.ctx + x / a.hs * a.tb;
-        p1 = q.ctx + min(y / a.hs * a.tb + a.tb, q.T) - 1;
-        lo = max(0, p0 - a.window + 1);
-        const int w0 = lo >> a.lunit;
-        us = min((min(a.sinks, lo) + a.unit - 1) >> a.lunit, w0);
-        shift = w0 - us;
-        nu = (p1 >> a.lunit) - shift + 1;
-    }
-    // Whether some row sees a slot of [s0, s1), and whether all rows see all of them.
-    __device__ __forceinline__ bool some(const TreeArgs &a, int s0, int s1) const {
-        return s0 <= p1 && (s1 > lo || s0 < a.sinks);
-    }
-    __device__ __forceinline__ bool all(const TreeArgs &a, int s0, int s1) const {
-        return s1 - 1 <= p0 && (s0 > p1 - a.window || s1 <= a.sinks);
-    }
-};
-
 __device__ __forceinline__ uint32_t bits_below(int n) {
     return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u;
 }
@@ -120,6 +97,41 @@ __device__ __forceinline__ uint32_t window_word(const TreeArgs &a, int p, int sl
     const int lo = max(0, p - a.window + 1);
     return bits_below(p + 1 - slot) & (~bits_below(lo - slot) | bits_below(a.sinks - slot));
 }
+
+// kWin: the keys of an item, those that some row of it sees: slots below a.sinks and
+// slots [lo, p1]. Both stretches, to whole pieces of a.align slots, are put side by
+// side (sp slots from 0 on, then those from sw on); units count along that row of
+// places, so that a few first tokens cost a piece and not a unit.
+struct Reach {
+    int p0, p1, lo, sp, sw, nu;
+    __device__ __forceinline__ void set(const TreeArgs &a, const Seq &q, int item) {
+        const int x = item * a.tpi, y = min(x + a.tpi, row_tiles(a, q)) - 1;
+        p0 = q.ctx + x / a.hs * a.tb;
+        p1 = q.ctx + min(y / a.hs * a.tb + a.tb, q.T) - 1;
+        lo = max(0, p0 - a.window + 1);
+        sw = lo & -a.align;
+        sp = (min(a.sinks, lo) + a.align - 1) & -a.align;
+        if (sp >= sw) sp = sw = 0;  // one stretch
+        nu = ((sp + p1 - sw) >> a.lunit) + 1;
+    }
+    __device__ __forceinline__ int slot(int place) const { return place < sp ? place : place - sp + sw; }
+    __device__ __forceinline__ int place(int slot) const { return slot < sp ? slot : slot - sw + sp; }
+    // Whether some row sees a slot of [s0, s1), and whether all rows see all of them.
+    __device__ __forceinline__ bool some(const TreeArgs &a, int s0, int s1) const {
+        return s0 <= p1 && (s1 > lo || s0 < a.sinks);
+    }
+    __device__ __forceinline__ bool all(const TreeArgs &a, int s0, int s1) const {
+        return s1 - 1 <= p0 && (s0 > p1 - a.window || s1 <= a.sinks);
+    }
+    // Whether all rows see n places from `at` on (both stretches: no, to be looked at).
+    __device__ __forceinline__ bool all_at(const TreeArgs &a, int at, int n) const {
+        return (at >= sp || at + n <= sp) && all(a, slot(at), slot(at) + n);
+    }
+    // Which of 32 places from `at` on (a multiple of 16) a row at slot p sees.
+    __device__ __forceinline__ uint32_t word(const TreeArgs &a, int p, int at) const {
+        return (window_word(a, p, slot(at)) & 0xFFFFu) | window_word(a, p, slot(at + 16)) << 16;
+    }
+};
 
 // kWin: the units of one head of a sequence. A thread adds up the items `from`,
 // `from` + step, ...
@@ -220,6 +232,7 @@ __device__ __forceinline__ long long count_units(const TreeArgs &a, int upto, lo
 // This block's share [u0, u1) of all units, and where it starts.
 struct Share {
     long long u0, u1, rest, quota;  // rest: u0's place among its sequence's units
+    int padded;  // > 0: an item's units, filled up to whole quotas
     int b;
 };
 template <int kWarps>
@@ -240,6 +253,48 @@ __device__ __forceinline__ Share find_share(const TreeArgs &a, ShareScratch<kThr
         Seq q;
         q.ctx = q.first = q.T = 0;
         if (lane < a.s.B) q = get_seq(a.s, lane, ok);
+        if (kWin && a.tpi == 1 && a.hs == 1 && a.tb >= a.s.N) {
+            // One item a head and sequence. A block whose share ends one item and
+            // begins another has two segments to finish, which costs it more than
+            // another unit: if whole blocks an item take at most one unit more than
+            // even shares, each item gets whole blocks (one token over 4100 keys, 8
+            // items of 65 units for 304 blocks: 18.3 us with shares of 2 units across
+            // items, 14.9 without).
+            uint32_t nu = 0;
+            if (q.T > 0) {
+                Reach r;
+                r.set(a, q, 0);
+                nu = r.nu;
+            }
+            const uint32_t items = __reduce_add_sync(0xFFFFFFFFu, q.T > 0 ? 1u : 0u) * a.Hkv;
+            const long long all = (long long)__reduce_add_sync(0xFFFFFFFFu, nu) * a.Hkv;
+            const uint32_t grid = a.grid;
+            if (items > 0 && items < grid && all < 1 << 30) {
+                const uint32_t even = ((uint32_t)all + grid - 1) / grid;
+                const uint32_t whole = ((uint32_t)all + grid - items - 1) / (grid - items);
+                if (whole <= even + 1) {
+                    const uint32_t blocks = (nu + whole - 1) / whole;  // an item
+                    uint32_t inc = blocks * a.Hkv;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+                        if (lane >= o) inc += v;
+                    }
+                    const uint32_t who = __ballot_sync(0xFFFFFFFFu, inc > blockIdx.x);
+                    Share s;
+                    s.quota = whole;
+                    s.b = who ? __ffs(who) - 1 : 0;
+                    const uint32_t per = __shfl_sync(0xFFFFFFFFu, blocks, s.b);
+                    const uint32_t units = __shfl_sync(0xFFFFFFFFu, nu, s.b);
+                    // among the sequence's blocks
+                    const uint32_t at = blockIdx.x - (__shfl_sync(0xFFFFFFFFu, inc, s.b) - per * a.Hkv);
+                    s.padded = (int)(per * whole);
+                    s.rest = s.u0 = at * whole;
+                    s.u1 = who ? s.u0 + min(whole, units - at % per * whole) : s.u0;
+                    return s;
+                }
+            }
+        }
         const long long n = lane_units<kWin>(a, q);
         long long inc = n;
 #pragma unroll
@@ -249,6 +304,7 @@ __device__ __forceinline__ Share find_share(const TreeArgs &a, ShareScratch<kThr
         }
         const long long total = __shfl_sync(0xFFFFFFFFu, inc, 31), quota = (total + a.grid - 1) / a.grid;
         Share s;
+        s.padded = 0;
         s.quota = quota;
         s.u0 = quota * blockIdx.x;
         s.u1 = min(s.u0 + quota, total);
@@ -282,6 +338,7 @@ __device__ __forceinline__ Share find_share(const TreeArgs &a, ShareScratch<kThr
         total += sh->sums[w];
     }
     Share s;
+    s.padded = 0;
     const long long quota = (total + a.grid - 1) / a.grid;
     s.quota = quota;
     s.u0 = quota * blockIdx.x;
@@ -323,8 +380,8 @@ struct CursorOf {
             nu = r.nu;
         }
     }
-    // The place of unit x of the item on the grid of units.
-    __device__ __forceinline__ int at(int x) const { return kWin && x >= r.us ? x + r.shift : x; }
+    // The slot at a place among the item's keys.
+    __device__ __forceinline__ int slot(int place) const { return kWin ? r.slot(place) : place; }
     // Whether some row of the item may see a slot of [s0, s1).
     __device__ __forceinline__ bool some(const TreeArgs &a, int s0, int s1) const {
         return kWin ? r.some(a, s0, s1) : s0 < q.ctx + q.T;
@@ -345,20 +402,21 @@ struct CursorOf {
     __device__ __forceinline__ void start(const TreeArgs &a, const Share &s) {
         b = s.b;
         load(a);
-        if (kWin) return start_window(a, s.rest);
+        if (kWin) return start_window(a, s.rest, s.padded);
         const int item = (int)(s.rest / nu);
         u = (int)(s.rest - (long long)item * nu);
         h = item / nrb;
         rb = item - h * nrb;
     }
     // kWin, whole warp: the head from the units of one, then its block of rows, 32 at a time.
-    __device__ __forceinline__ void start_window(const TreeArgs &a, long long rest) {
+    __device__ __forceinline__ void start_window(const TreeArgs &a, long long rest, int padded) {
         const int lane = threadIdx.x & 31;
         if (nrb == 1) {
             rb = 0;
             reach(a);
-            h = (int)(rest / nu);
-            u = (int)(rest - (long long)h * nu);
+            const int n = padded ? padded : nu;
+            h = (int)(rest / n);
+            u = (int)(rest - (long long)h * n);
             return;
         }
         long long n = window_units(a, q, lane, 32);

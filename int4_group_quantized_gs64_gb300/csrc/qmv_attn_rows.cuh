@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
     const uint32_t ring = tc05::smem_addr(smem) + warp * (kStages * 2 * S::kSlice);
     // this lane's 16-key part of the slice (lanes 0 .. kSub - 1 copy one each)
     const int part = kSub > 1 ? min(lane, kSub - 1) : 0;
-    auto part_slot = [&](int u) { return (pc.at(u) * kWarps + warp) * (kSub * 16) + part * 16; };
+    auto part_slot = [&](int u) { return pc.slot((u * kWarps + warp) * (kSub * 16) + part * 16); };
 
     auto fetch_page = [&]() {
         const int s0 = part_slot(pc.u);
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
                 }
             }
             dead = __any_sync(0xFFFFFFFFu, dead);
-            const int s0 = (cc.at(cc.u) * kWarps + warp) * (kSub * 16);
+            const int s0 = (cc.u * kWarps + warp) * (kSub * 16);  // (kWin: a place)
             const int copied = dead ? 0 : flag[stage];
             if (copied) {
                 const uint32_t ks = ring + stage * (2 * S::kSlice), vs = ks + S::kSlice;
@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
                     }
                 // drafts, the end of the sequence (keys that some row does not see) or a
                 // missing page in this slice
-                const bool special = (kWin ? !seg_r.all(a, s0, s0 + kSub * 16) : s0 + kSub * 16 > sq.ctx) ||
+                const bool special = (kWin ? !seg_r.all_at(a, s0, kSub * 16) : s0 + kSub * 16 > sq.ctx) ||
                                      copied != (1 << kSub) - 1;
                 auto there = [&]() {  // its keys that were copied
                     uint32_t w = 0;
@@ -235,7 +235,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
                 };
                 auto sees = [&](int e) {  // and those that this lane's row sees
                     return rt[e] < 0 ? 0u
-                           : kWin    ? window_word(a, sq.ctx + rt[e], s0) & there()
+                           : kWin    ? seg_r.word(a, sq.ctx + rt[e], s0) & there()
                                      : seen_word(a, sq, rt[e], s0) & there();
                 };
                 if (special) {
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
                     const int len = sq.ctx + sq.T;
                     const uint32_t all = there(), see[2] = {sees(0), sees(1)};
                     for (int j = 0; j < kSub * 16; ++j) {
-                        const int key = s0 + j;
+                        const int key = kWin ? seg_r.slot(s0 + j) : s0 + j;
                         const bool none =
                             (kWin ? !seg_r.some(a, key, key + 1) : key >= len) || !((all >> j) & 1u);
                         if (!none && (kWin ? seg_r.all(a, key, key + 1) : key < sq.ctx)) continue;

@@ -5,9 +5,9 @@
 //     x_j = scale * q . k_j,   o = sum_j exp(x_j - M) v_j / sum_j exp(x_j - M)
 // as in qmv_attn_tree.cu. The rows of a key/value head are its tokens times G
 // query heads; some of them are an item, and its keys are the union of what its
-// rows see, in two stretches of units (Reach): those with first tokens, and those
-// from the first row's window to the last row's slot. Units that every row sees
-// whole need no mask; the others (the edges) are masked row by row.
+// rows see, in two stretches that are put side by side (Reach): first tokens, and
+// those from the first row's window to the last row's slot. Units that every row
+// sees whole need no mask; the others (the edges) are masked row by row.
 // Units are shared out evenly over the blocks, so a prompt's early rows (short
 // reach) and late ones, and sequences of any length, fill the GPU alike.
 //
@@ -103,12 +103,13 @@ cudaError_t launch_attn_window(const AttnCache &c, const WindowCall &t, cudaStre
     set_rows(a, t.s.max_draft);
     a.unit = a.rows == kRows ? kWarps * 16 * (128 / c.D) : 128;  // keys a unit
     while ((1 << a.lunit) < a.unit) ++a.lunit;
+    a.align = a.rows == kRows ? 16 : c.page < 128 ? c.page : 128;
     // units at most: the items of B sequences at their bound, or of N tokens (a
     // sequence's last item may be short), each over a whole table row
     long long items = t.s.B * items_a_head(a, t.s.max_draft);
     const long long by_n = items_a_head(a, t.s.N) + t.s.B;
     if (by_n < items) items = by_n;
-    const long long most = items * c.Hkv * (((((long long)t.s.max_pages << lpage) + a.unit - 1) >> a.lunit) + 1);
+    const long long most = items * c.Hkv * (((((long long)t.s.max_pages << lpage) + a.unit - 1) >> a.lunit) + 2);
     const int gmax = attn_grid_max(a.rows);
     if (most / gmax >= 0x7FFFFFFFLL) return cudaErrorInvalidValue;  // a block's units fit 31 bits
     a.grid = most < gmax ? (int)most : gmax;

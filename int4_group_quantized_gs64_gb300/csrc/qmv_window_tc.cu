@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t phase = 1, qphase = 1;  // a fresh barrier counts as passed for parity 1
         // this lane's piece of the item's step u at c: its page
         auto page_of = [&](int u, bool &lv) {
-            const int slot = c.at(u) * kKeys + lane * prow;
+            const int slot = c.slot(u * kKeys + lane * prow);
             lv = lane * prow < kKeys && c.some(a, slot, slot + prow);
             return lv ? __ldg(a.s.table + (long long)c.b * a.s.max_pages + (slot >> a.s.lpage)) : 0;
         };
@@ -238,22 +238,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         // a page, get zeros, and of those that some rows see infinities and NaNs are
         // replaced (the rows that see them get them added when O is written).
         struct {
-            int j, p0, p1, lo, stage;
+            int at, stage;         // its first place; the slot of the ring
             uint32_t gone, phase;  // pieces without a page
+            Reach r;
         } was;
         was.stage = -1;
         auto look = [&]() {
             if (was.stage < 0) return;
-            Reach r;
-            r.p0 = was.p0;
-            r.p1 = was.p1;
-            r.lo = was.lo;
+            const Reach &r = was.r;
             if (wait(m->vfull + was.stage, was.phase, m, a.status) &&
-                (was.gone || !r.all(a, was.j * kKeys, (was.j + 1) * kKeys))) {
+                (was.gone || !r.all_at(a, was.at, kKeys))) {
                 __syncwarp();
 #pragma unroll 1
                 for (int x = lane; x < kKeys; x += 32) {
-                    const int key = was.j * kKeys + x;
+                    const int key = r.slot(was.at + x);
                     uint8_t *row = vring + was.stage * kTile + x * 128;
                     auto at_chunk = [&](int ch) {
                         return reinterpret_cast<uint4 *>(row + (ch >> 3) * (kKeys * 128) +
@@ -320,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int t = 0; t < sg.n; ++t) {
                 const bool good = live && (unsigned)pid < (unsigned)a.pages;
                 const int row =
-                    (pid * a.Hkv + c.h) * a.s.page + ((c.at(sg.j0 + t) * kKeys + lane * prow) & (a.s.page - 1));
+                    (pid * a.Hkv + c.h) * a.s.page + (c.slot((sg.j0 + t) * kKeys + lane * prow) & (a.s.page - 1));
                 if (live && !good && keys) set_status(a.status, kStPage);
                 const uint32_t n = __popc(__ballot_sync(0xFFFFFFFFu, good));
                 const uint32_t gone = __ballot_sync(0xFFFFFFFFu, live && !good);
@@ -347,10 +345,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (!keys) {
                     look();
-                    was.j = c.at(sg.j0 + t);
-                    was.p0 = c.r.p0;
-                    was.p1 = c.r.p1;
-                    was.lo = c.r.lo;
+                    was.at = (sg.j0 + t) * kKeys;
+                    was.r = c.r;
                     was.stage = stage;
                     was.gone = gone;
                     was.phase = phase ^ 1u;
@@ -600,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The page of this lane's piece of step i of a segment (it is loaded a step ahead, and
         // over the end of a segment).
         auto page_of = [&](const CursorOf<true> &x, const Segment &g, int i) {
-            const int slot = x.at(g.j0 + i) * kKeys + lane * piece;
+            const int slot = x.slot((g.j0 + i) * kKeys + lane * piece);
             const bool need = lane * piece < kKeys && i < g.n && x.some(a, slot, slot + piece);
             return need ? __ldg(a.s.table + (long long)x.b * a.s.max_pages + (slot >> a.s.lpage)) : 0;
         };
@@ -643,15 +639,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
 #pragma unroll 1
             for (int i = i0; i < sg.n; i += kStep) {
-                const int j = c.at(sg.j0 + i);
+                const int at = (sg.j0 + i) * kKeys;
                 const uint32_t gone = __ballot_sync(0xFFFFFFFFu, (unsigned)pid >= (unsigned)a.pages);
                 pid = page_of(c, sg, i + kStep);
-                const bool special = gone || !c.r.all(a, j * kKeys, (j + 1) * kKeys);
+                const bool special = gone || !c.r.all_at(a, at, kKeys);
                 uint32_t see[4] = {~0u, ~0u, ~0u, ~0u};  // this step's keys that the row sees
                 if (special && warp_live) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        see[k] = row_live ? window_word(a, pos, j * kKeys + k * 32) : 0u;
+                        see[k] = row_live ? c.r.word(a, pos, at + k * 32) : 0u;
                     if (gone) {
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
@@ -907,7 +903,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                         for (int d = 0; d < 512; ++d) {  // (Reach: at most 255 keys an edge)
                             const int key = d < 256 ? c.r.p0 + d : c.r.lo + d - 256;
-                            const int tile = key / kKeys, u = tile < c.r.us ? tile : tile - c.r.shift;
+                            const int u = c.r.place(key) / kKeys;
                             if (key > c.r.p1 || u < sg.j0 || u >= sg.j0 + sg.n || c.r.all(a, key, key + 1) ||
                                 (d >= 256 && key > c.r.p0) || !(window_word(a, pos, key) & 1u))
                                 continue;
