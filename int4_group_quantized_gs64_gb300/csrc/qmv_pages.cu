@@ -127,22 +127,33 @@ __device__ __forceinline__ int scan_misses(const PagesArgs &a, int n, int *sh) {
 }
 
 // The `want` lowest free pages, or as many as there are, to the list, each held
-// once from here on; returns how many. A warp looks at 128 pages a pass.
+// once from here on; returns how many. A warp looks at 256 pages a pass, and loads
+// the next pass's meanwhile: what bounds it is the latency of a pass (an update
+// that takes 36,000 pages out of 670,000, with its two copies: 42 us in passes of
+// 128 pages a warp without that, 30 so).
 __device__ __forceinline__ int take_free(const PagesArgs &a, int want, int *sh) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    constexpr int kPer = 4;
-    int got = 0;
-    for (int p0 = 0; p0 < a.pages && got < want; p0 += kOne * kPer) {
-        const int p = p0 + warp * (32 * kPer) + lane;
-        uint32_t free[kPer];
-        int r[kPer], n = 0;
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) r[k] = p + k * 32 < a.pages ? a.refs[p + k * 32] : 1;
+    constexpr int kPer = 8, kPass = kOne * kPer;
+    const int p0 = warp * (32 * kPer) + lane;
+    int next[kPer];
+    auto load = [&](int pass) {
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
-            free[k] = __ballot_sync(0xFFFFFFFFu, r[k] == 0);
+            const int p = pass + p0 + k * 32;
+            next[k] = p < a.pages ? a.refs[p] : 1;
+        }
+    };
+    if (want > 0) load(0);
+    int got = 0;
+    for (int pass = 0; pass < a.pages && got < want; pass += kPass) {
+        uint32_t free[kPer];
+        int n = 0;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            free[k] = __ballot_sync(0xFFFFFFFFu, next[k] == 0);
             n += __popc(free[k]);
         }
+        load(pass + kPass);
         int total;
         int at = got + block_scan(lane == 31 ? n : 0, sh, total);
         at = __shfl_sync(0xFFFFFFFFu, at, 31) - n;  // free pages before this warp's
@@ -150,8 +161,8 @@ __device__ __forceinline__ int take_free(const PagesArgs &a, int want, int *sh) 
         for (int k = 0; k < kPer; ++k) {
             const int rank = at + __popc(free[k] & ((1u << lane) - 1u));
             if (((free[k] >> lane) & 1u) && rank < want) {
-                a.list[rank] = p + k * 32;
-                a.refs[p + k * 32] = 1;
+                a.list[rank] = pass + p0 + k * 32;
+                a.refs[pass + p0 + k * 32] = 1;
             }
             at += __popc(free[k]);
         }
@@ -327,18 +338,18 @@ struct CompactArgs {
     int32_t *new_ctx, *status;
 };
 
-// A block a sequence, head and pool. Rows go to lower slots in ascending order: a
-// pass reads its rows, and when all are read writes them; what it overwrites are
-// rows of this pass or of passes before, since keep[i] >= i.
+// A block a sequence and head. Rows go to lower slots in ascending order: a pass
+// reads its rows, and when all are read writes them; what it overwrites are rows of
+// this pass or of passes before, since keep[i] >= i. What bounds it is the chain of
+// loads: lengths, kept tokens, page, row.
 __global__ void __launch_bounds__(128) k_compact(const CompactArgs a) {
-    constexpr int kAhead = 8;
+    constexpr int kAhead = 4;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int b = blockIdx.x / a.Hkv, h = blockIdx.x - b * a.Hkv;
-    const bool first = h == 0 && blockIdx.y == 0;
     bool ok;
-    const Seq q = get_seq(a.s, b, ok);
     const int n = a.kept[b];
+    const Seq q = get_seq(a.s, b, ok);
     ok = ok && n >= 0 && n <= q.T;
     const int32_t *keep = a.keep + q.first;
     bool bad = false;
@@ -348,14 +359,13 @@ __global__ void __launch_bounds__(128) k_compact(const CompactArgs a) {
             bad |= x < i || x >= q.T || (i > 0 && x <= keep[i - 1]);
         }
     ok = !__syncthreads_or(bad || !ok);
-    if (first && threadIdx.x == 0) {
+    if (h == 0 && threadIdx.x == 0) {
         a.new_ctx[b] = ok ? q.ctx + n : a.s.ctx[b];
         if (!ok) set_status(a.status, kStLength);
     }
     if (!ok || n == 0 || keep[n - 1] == n - 1) return;  // (all in their places)
     const int32_t *row = a.s.table + (long long)b * a.s.max_pages;
-    uint16_t *pool = blockIdx.y ? a.v : a.k;
-    // element offset of slot x's row in a pool of one element a token, -1: no page
+    // offset of slot x's row in a pool of one element a token, -1: no page
     auto place = [&](int x) -> long long {
         const int slot = q.ctx + x, pid = row[slot >> a.s.lpage];
         if ((unsigned)pid >= (unsigned)a.pages) {
@@ -367,7 +377,7 @@ __global__ void __launch_bounds__(128) k_compact(const CompactArgs a) {
     const int lanes = a.D / 8, per = 128 / lanes;  // threads a row, rows at a time
     const int l = threadIdx.x % lanes, r = threadIdx.x / lanes;
     for (int i0 = 0; i0 < n; i0 += per * kAhead) {
-        uint4 x[kAhead];
+        uint4 x[kAhead], y[kAhead];
         float w[kAhead];
         long long to[kAhead];
 #pragma unroll
@@ -379,15 +389,17 @@ __global__ void __launch_bounds__(128) k_compact(const CompactArgs a) {
             to[j] = place(i);
             if (from < 0) to[j] = -1;
             if (to[j] < 0) continue;
-            x[j] = *reinterpret_cast<const uint4 *>(pool + from * a.D + l * 8);
-            if (a.acc && l == 0 && blockIdx.y == 0) w[j] = a.acc[from];
+            x[j] = *reinterpret_cast<const uint4 *>(a.k + from * a.D + l * 8);
+            y[j] = *reinterpret_cast<const uint4 *>(a.v + from * a.D + l * 8);
+            if (a.acc && l == 0) w[j] = a.acc[from];
         }
         __syncthreads();
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
             if (to[j] < 0) continue;
-            *reinterpret_cast<uint4 *>(pool + to[j] * a.D + l * 8) = x[j];
-            if (a.acc && l == 0 && blockIdx.y == 0) a.acc[to[j]] = w[j];
+            *reinterpret_cast<uint4 *>(a.k + to[j] * a.D + l * 8) = x[j];
+            *reinterpret_cast<uint4 *>(a.v + to[j] * a.D + l * 8) = y[j];
+            if (a.acc && l == 0) a.acc[to[j]] = w[j];
         }
         __syncthreads();
     }
@@ -477,7 +489,7 @@ cudaError_t launch_attn_compact(const AttnCache &c, const AttnSeqs &s, const int
     a.v = static_cast<uint16_t *>(c.v);
     a.pages = c.pages; a.Hkv = c.Hkv; a.D = c.D;
     a.keep = keep; a.kept = kept; a.acc = acc; a.new_ctx = new_ctx; a.status = status;
-    return launch(k_compact, dim3((unsigned)(s.B * c.Hkv), 2), dim3(128), 0, st, true, a);
+    return launch(k_compact, dim3((unsigned)(s.B * c.Hkv)), dim3(128), 0, st, true, a);
 }
 
 }  // namespace qmv
