@@ -11,17 +11,23 @@
 // and queries, 9 and 10 issue the streams' products (9 all of them where the streams
 // take alternate steps). Every warp comes to a barrier's phases one by one.
 //
-// A stream's chain of a step is 1,024 cycles of products and its softmax; the two
-// streams together need 2,048 of products, so a softmax below 1,024 would hide
-// altogether. Its exponentials alone take 512 (four cycles a warp instruction). The
-// weights are handed over in two halves, so that the output's first products run
-// under the second half's exponentials, and maxima are taken three at a time.
+// A stream's chain of a step is 1,024 cycles of products (at 128 elements) and its
+// softmax; the two streams together need 2,048 of products and, side by side, some
+// 1,400 of softmax (exponentials 512 a stream, and as much again for scaling, sums,
+// packing and the maximum). What shortens the chain: the next scores are issued right
+// behind the output's products, in turns that hold nothing but the issue; a step's
+// weights come from the maximum that its rows have, so that no exponential waits for
+// the step's own (below); what is looked at or written for the edges is kept out of
+// the loop that every step runs through.
 //
 // The end of an item costs a stream one look at O: queries of the next item come by
 // tensor-map copies while the last softmax runs, and its scores are formed while O
-// is written out. The streams do not wait for one another there (with the queries
-// through registers and both streams in step, 14 items a block cost 170 us of 670:
-// 12,279 prompt tokens, windows of 2048).
+// is written out. The streams do not wait for one another there.
+//
+// Measured: 12,279 prompt tokens of 48 heads (8 key/value heads of 128), windows of
+// 2048, 16-bit outputs: 466 us, 1,141 TFLOP/s (the kernel of qmv_attn_tc.cu, with
+// windows: 678). Of that the steps at the edges cost some 27 us, the look at values
+// 24, writing O 28.
 //
 // Masks: a step that all rows of the item see whole is not looked at. In the others
 // (at the window's edge, the diagonal, the first tokens' end, with a missing page)
@@ -29,9 +35,10 @@
 // and that are not finite are replaced by zeros, since 0 x inf is not 0; the rows
 // that do see them get them added at the end (Misc::odd).
 //
-// The running maximum moves when it grows by more than 2^8; weights and sums for
-// 16-bit and fp32 outputs are those of qmv_attn_tc.cu: rounded once to 16 bits, or
-// two fp16 / three bf16 numbers and sums of each step added up in registers.
+// The maximum in use moves when it is found to have grown by more than 2^8; weights
+// and sums for 16-bit and fp32 outputs are those of qmv_attn_tc.cu: rounded once to
+// 16 bits, or two fp16 / three bf16 numbers and sums of each step added up in
+// registers.
 #include <cudaTypedefs.h>
 #include <string.h>
 
@@ -293,10 +300,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         int pid = page_of(c.u, live);
         bool ok = true;
         uint32_t pending = 0, pending_ph = 0;  // slots this warp copied to, and the phase that ends it
-        bool q_pending = false;
+        uint32_t q_pending = 0, q_phase = 0;  // streams whose queries were copied last, and the phase that ends it
         for (int left = units; left > 0;) {
             const Segment sg(c, left);
             if (!keys) {  // the item's queries, once the last item's scores are done
+                if (ok) {
+                    q_pending = 0;
+                    q_phase = qphase ^ 1u;
+                }
 #pragma unroll
                 for (int s = 0; s < kQ; ++s) {
                     ok = ok && wait(m->q_empty + s, qphase, m, a.status);
@@ -310,9 +321,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             tma_load4(tc05::smem_addr(qs) + s * kTile + hf * (128 * 128), &qmap, 0, head,
                                       c.q.first + k * a.tb, hf, m->q_full + s);
                     }
-                    q_pending = q_pending || ok;
+                    if (ok) q_pending |= 1u << s;
                 }
-                if (ok) qphase ^= 1u;
+                qphase ^= 1u;
             }
 #pragma unroll 1
             for (int t = 0; t < sg.n; ++t) {
@@ -368,8 +379,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) {  // gave up: wait (bounded) for this warp's copies in flight
             for (int i = 0; i < slots; ++i)
                 if ((pending >> i) & 1u) tc05::mbar_wait(full + i, (pending_ph >> i) & 1u, kPoll / 64);
-            if (q_pending)  // (the last ones' phase)
-                for (int s = 0; s < kQ; ++s) tc05::mbar_wait(m->q_full + s, qphase, kPoll / 64);
+            for (int s = 0; s < kQ; ++s)
+                if ((q_pending >> s) & 1u) tc05::mbar_wait(m->q_full + s, q_phase, kPoll / 64);
         }
     } else if (kTwo || warp == 9) {
         // ------------------------------------------------------------ products
@@ -745,7 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // be this step's. Only if they get too large for fp16, or for sums of
                         // them (kMost), is the maximum looked for and the step begun again;
                         // nothing has left the registers by then. (Maxima of every step: 553
-                        // us where this takes 4XX.) P apart: the maximum first, since S is
+                        // us where this took 521.) P apart: the maximum first, since S is
                         // wanted free soon.
                         uint32_t hi[4][16];
                         bool look = kApart || __any_sync(0xFFFFFFFFu, row_live && mx == -INFINITY);
