@@ -14,8 +14,10 @@
 // A stream's chain of a step is 1,024 cycles of products (at 128 elements) and its
 // softmax; the two streams together need 2,048 of products and, side by side, some
 // 1,400 of softmax (exponentials 512 a stream, and as much again for scaling, sums,
-// packing and the maximum). What shortens the chain: the next scores are issued right
-// behind the output's products, in turns that hold nothing but the issue; a step's
+// packing and the maximum). For fp32 outputs the softmax is what bounds a step: some
+// 3,500 cycles with two or three numbers a weight. What shortens the chain: the next scores are issued right
+// behind the output's products, in turns that hold nothing but the issue; products of
+// two or three numbers a weight begin when half of the keys have theirs; a step's
 // weights come from the maximum that its rows have, so that no exponential waits for
 // the step's own (below); what is looked at or written for the edges is kept out of
 // the loop that every step runs through.
@@ -53,7 +55,7 @@ namespace attn {
 namespace {
 
 constexpr int kThreads = 384, kKeys = 128, kMaxSlots = 6;  // slots a ring
-constexpr int kMisc = 2880;               // barriers and small tables
+constexpr int kMisc = 2896;               // barriers and small tables
 constexpr int kSmemMax = 227 * 1024;
 constexpr float kLazy = 8.f;              // log2 units the maximum may lag
 
@@ -61,6 +63,7 @@ struct Misc {
     ShareScratch<kThreads / 32> share;
     uint64_t kfull[kMaxSlots], kempty[kMaxSlots], vfull[kMaxSlots], vempty[kMaxSlots];
     uint64_t q_full[2], q_empty[2], s_full[2], s_free[2], p_full[2], pv_done[2], o_full[2];
+    uint64_t p_half[2];  // kSplit: the weights of the step's first 64 keys are there
     uint64_t vready[kMaxSlots];  // values have been looked at
     uint64_t turn[2], fin[2];
     uint32_t kflag[kMaxSlots];  // of the step whose keys lie there: 1 first of its segment, 2 last
@@ -184,6 +187,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc05::mbar_init(m->s_full + s, 1);
             tc05::mbar_init(m->s_free + s, 4);
             tc05::mbar_init(m->p_full + s, 4);
+            tc05::mbar_init(m->p_half + s, 4);
             tc05::mbar_init(m->pv_done + s, 1);
             tc05::mbar_init(m->o_full + s, 1);
             tc05::mbar_init(m->turn + s, 1);
@@ -402,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t ahead_bits = 0;
             int ahead_n = 0, kslot = 0, vslot = 0;
             uint32_t kph = 0, vph = 0, qph = 0, tph = 0;
-            uint32_t fph = 0, frph = 0;  // bit s: p_full, s_free of stream s
+            uint32_t fph = 0, hph = 0, frph = 0;  // bit s: p_full, p_half, s_free of stream s
             bool live = true;
             auto await = [&](uint64_t *bar, uint32_t parity) {
                 live = __all_sync(0xFFFFFFFFu, live && wait(bar, parity, m, a.status));
@@ -459,12 +463,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                 scores_done();
             };
             // The output of the oldest step: O (+)= P V.
-            auto output_wait = [&](int s) {
-                await(m->vready + vslot, vph);
+            auto weights_wait = [&](int s) {
                 await(m->p_full + s, (fph >> s) & 1u);
                 fph ^= 1u << s;
             };
-            auto output_issue = [&](int s, int hf) {  // hf: kParted, which half of the columns
+            auto output_wait = [&](int s) {
+                await(m->vready + vslot, vph);
+                if (kSplit) {
+                    await(m->p_half + s, (hph >> s) & 1u);
+                    hph ^= 1u << s;
+                } else {
+                    weights_wait(s);
+                }
+            };
+            // kSplit: k0 .. k1 - 1 of the eight sixteenths of the keys; hf: kParted, which
+            // half of the columns.
+            auto output_issue = [&](int s, int hf, int k0, int k1) {
                 const uint32_t tp = tmem + kPcol + s * kPstep, to = tmem + kOcol + s * kOstep;
                 const uint64_t v = vdesc + (uint32_t)(vslot * (kTile >> 4));
                 if (elected()) {
@@ -472,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int part = kThird ? 2 : 1; part >= 0; --part)
 #pragma unroll
-                            for (int k = 0; k < kKeys / 16; ++k)
+                            for (int k = k0; k < k1; ++k)
                                 tc05::mma_ts(to, part == 2 ? to + 64 + k * 8 : tp + k * 16 + part * 8,
                                              v + (hf * (kKeys * 128) + k * 2048 >> 4), kIdescO,
                                              part < (kThird ? 2 : 1) || k > 0);
@@ -481,17 +495,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int k = 0; k < kKeys / 16; ++k)
                             tc05::mma_ts(to, tp + k * 8, v + k * (2048 >> 4), kIdescO, k ? 1u : ~ahead_bits & 1u);
                     }
-                    if (kSplit || kApart) tc05::mma_commit(m->pv_done + s);
+                    if (kSplit ? k1 == kKeys / 16 : kApart) tc05::mma_commit(m->pv_done + s);
                 }
                 __syncwarp();
             };
             auto output_rest = [&](int s) {
                 if (!kParted) return;
-                await(m->p_full + s, (fph >> s) & 1u);  // (the first half has been taken)
-                fph ^= 1u << s;
+                weights_wait(s);  // (the first half has been taken)
                 if (!live) return;
                 tc05::fence_after_sync();
-                output_issue(s, 1);
+                output_issue(s, 1, 0, kKeys / 16);
             };
             auto output_done = [&](int s) {
                 if (elected()) {
@@ -513,7 +526,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 output_wait(s);
                 if (!live) return;
                 tc05::fence_after_sync();
-                output_issue(s, 0);
+                if (kSplit) {  // as the weights come
+                    output_issue(s, 0, 0, kKeys / 32);
+                    weights_wait(s);
+                    if (!live) return;
+                    tc05::fence_after_sync();
+                    output_issue(s, 0, kKeys / 32, kKeys / 16);
+                } else {
+                    output_issue(s, 0, 0, kKeys / 16);
+                }
                 output_rest(s);
                 if (live) output_done(s);
             };
@@ -541,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (!live) break;
                     tc05::fence_after_sync();
-                    output_issue(me, 0);
+                    output_issue(me, 0, 0, kKeys / 16);
                     if (now) scores_issue(me);
                     pass();
                     output_done(me);
@@ -727,6 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint64_t nb = pack_f32x2(-base, -base);
 #pragma unroll 2
                         for (int h = 0; h < 8; ++h) {  // 16 at a time: one step of the product
+                            if (h == 4) give(m->p_half);
                             uint32_t x[16], hi[8], lo[8], third[8];
                             tc05::tmem_ld16(ts + h * 16, x);
                             tc05::tmem_wait_ld();
@@ -837,6 +859,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     give(m->p_full);
                 }
+                if (kSplit && !warp_live) give(m->p_half);
                 if constexpr (kSplit) {  // this step's share of O
 #pragma unroll
                     for (int hf = 0; hf < D / kOcols; ++hf) {

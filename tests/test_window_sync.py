@@ -43,3 +43,8 @@ def test_products_that_do_not_wait_for_the_look_at_values_are_noticed():
 def test_new_weights_before_the_last_products_are_noticed():
     assert noticed(lambda seed: model.window_tc(seed, segments(seed), **FORMS["two_d64"], copy=300, slow=100,
                                                 wait_done=False))
+
+
+def test_both_halves_of_the_weights_at_one_barrier_are_noticed():
+    assert noticed(lambda seed: model.window_tc(seed, segments(seed), **FORMS["two_d64_fp32"], copy=300, slow=100,
+                                                one_barrier=True))

@@ -10,22 +10,25 @@ from attn_sync_model import Barrier, Broken, Issuer, Ring, Sim
 
 
 def window_tc(seed, segments, stages, two, apart=False, split=False, parted=False, copy=2000.0, slow=20.0,
-              wait_ready=True, wait_done=True):
+              wait_ready=True, wait_done=True, one_barrier=False):
     """One block over segments, lists of steps that are true where values have to be looked at.
 
     stages: slots for keys and for values. wait_ready False: products wait for values that
     have come, not for those that have been looked at. wait_done False: with weights beside the
-    scores, warps do not wait for the last products before they hand over new ones."""
+    scores, warps do not wait for the last products before they hand over new ones. one_barrier: both
+    halves of a step's weights (split) arrive at the same barrier."""
     rng = random.Random(seed)
     sim = Sim(rng, slow)
     nq = 2 if two else 1
     kring, vring = Ring(sim, "keys'", stages[0], nq), Ring(sim, "values'", stages[1], nq)
     turns = two and not split and not apart
     B = lambda name, count: [Barrier(f"{name}[{s}]", count) for s in range(2)]  # noqa: E731
-    q_full, q_empty, s_full, s_free, p_full, pv_done, o_full, turn = (
-        B("q_full", 1), B("q_empty", 1), B("s_full", 1), B("s_free", 4), B("p_full", 4),
+    q_full, q_empty, s_full, s_free, p_full, p_half, pv_done, o_full, turn = (
+        B("q_full", 1), B("q_empty", 1), B("s_full", 1), B("s_free", 4), B("p_full", 4), B("p_half", 4),
         B("pv_done", 1), B("o_full", 1),
         B("turn", 1))
+    if one_barrier:
+        p_half = p_full
     vready = [Barrier(f"vready[{i}]", 1) for i in range(stages[1])]
     steps = [(k, i, i == len(seg) - 1, sp) for k, seg in enumerate(segments) for i, sp in enumerate(seg)]
     total = len(steps)
@@ -34,7 +37,7 @@ def window_tc(seed, segments, stages, two, apart=False, split=False, parted=Fals
     q_there, q_used = [None, None], [None, None]    # segment whose queries lie there, whose scores have ended
     s_holds, s_read = [None, None], [{}, {}]        # step of the scores, warps that have taken them
     o_taken, o_end = [{}, {}], [{}, {}]             # warps that have taken a segment's O; when products end
-    p_written = [{}, {}]                            # warps' parts of a step's weights
+    p_written, h_written = [{}, {}], [{}, {}]       # warps' parts of a step's weights, of their first half
     scrubbed = {}
 
     def look(n):
@@ -68,7 +71,7 @@ def window_tc(seed, segments, stages, two, apart=False, split=False, parted=Fals
             yield from look(total - 1)
 
     def products(me):
-        at = {"q": 0, "seen": -1, "o": 0, "fr": [0, 0], "f": [0, 0], "t": 0}
+        at = {"q": 0, "seen": -1, "o": 0, "fr": [0, 0], "f": [0, 0], "h": [0, 0], "t": 0}
 
         def peek():  # the keys of the next scores' step have come, and with them its flags
             n = at["q"]
@@ -115,8 +118,18 @@ def window_tc(seed, segments, stages, two, apart=False, split=False, parted=Fals
         def output_wait(s):
             n = at["o"]
             yield (vready[n % stages[1]], n // stages[1]) if wait_ready else vring.landed_wait(n)
+            if split:
+                yield p_half[s], at["h"][s]
+                at["h"][s] += 1
+                if one_barrier:
+                    at["f"][s] += 1
+                if h_written[s].get(n, 0) != 4:
+                    raise Broken(f"product of step {n} before the first half of its weights")
+                unit.product(128)
             yield p_full[s], at["f"][s]
             at["f"][s] += 1
+            if one_barrier:
+                at["h"][s] += 1
 
         def output_issue(s, part):
             n = at["o"]
@@ -236,7 +249,11 @@ def window_tc(seed, segments, stages, two, apart=False, split=False, parted=Fals
                         vp += 1
                 if last is not None and sim.now < o_end[s].get(last, float("inf")):
                     raise Broken(f"step {x} moves O or writes weights before the products of {last} end")
-                yield sim.jitter(600)
+                if split:
+                    yield sim.jitter(300)
+                    h_written[s][x] = h_written[s].get(x, 0) + 1
+                    sim.arrive(p_half[s])
+                yield sim.jitter(300 if split else 600)
                 p_written[s][x] = p_written[s].get(x, 0) + 1
                 if not split:
                     sim.arrive(p_full[s])
