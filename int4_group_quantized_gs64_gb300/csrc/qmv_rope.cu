@@ -206,11 +206,16 @@ __device__ __forceinline__ void clear_sums(const RopeArgs &a, int lane, int pid,
     for (int h = lane; h < a.Hkv; h += 32) a.acc[((long long)pid * a.Hkv + h) * a.s.page + row] = 0.f;
 }
 
-// Rows and strides on 16-byte boundaries, rot a multiple of 16.
-template <int D, bool kBf16, bool kF32, bool kInter, bool kNorm>
-__global__ void __launch_bounds__(32 * kWarps, kNorm ? 4 : 0) k_rope_append(const RopeArgs a) {
+// Rows and strides on 16-byte boundaries, rot a multiple of 16. kFew (with norms): for
+// tokens whose heads are few passes of a warp, where a token's slot and angles are what
+// it costs: more warps an SM, and no weights kept in registers (7 heads of 128, 54,000
+// tokens: 137 -> 111 us; 4 + 4 heads, 11,600 tokens: 41 -> 30; 64 heads, 14 passes,
+// 92 -> 97, so those go the other way).
+constexpr int kFewPasses = 4;
+template <int D, bool kBf16, bool kF32, bool kInter, bool kNorm, bool kFew>
+__global__ void __launch_bounds__(32 * kWarps, kNorm ? (kFew ? 7 : 4) : 0) k_rope_append(const RopeArgs a) {
     constexpr int kPerHead = D / 16, kHeads = 32 / kPerHead;  // lanes a head, heads a pass
-    constexpr int kAngles = 8 / kHeads, kAhead = kNorm ? (kF32 ? 1 : 2) : kF32 ? 2 : 4;
+    constexpr int kAngles = 8 / kHeads, kAhead = kNorm ? (kF32 || kFew ? 1 : 2) : kF32 ? 2 : 4;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31;
@@ -257,7 +262,7 @@ __global__ void __launch_bounds__(32 * kWarps, kNorm ? 4 : 0) k_rope_append(cons
         }
     }
     float w0[8], w1[8];  // queries' weights (the few key heads load theirs when they come)
-    if (kNorm) {
+    if (kNorm && !kFew) {
         weights8<kBf16>(a, a.qw, lo, w0);
         weights8<kBf16>(a, a.qw, hi, w1);
     }
@@ -296,16 +301,17 @@ __global__ void __launch_bounds__(32 * kWarps, kNorm ? 4 : 0) k_rope_append(cons
                 for (int o = kPerHead / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
                 if (hd >= he) continue;
                 const float f = norm_of(sum, D, a.eps);
-                if (hd < a.Hq) {
+                if (!kFew && hd < a.Hq) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         x0[e] *= f * w0[e];
                         x1[e] *= f * w1[e];
                     }
                 } else if (hd < a.Hq + a.Hkv) {
+                    const void *hw = kFew && hd < a.Hq ? a.qw : a.kw;
                     float k0[8], k1[8];
-                    weights8<kBf16>(a, a.kw, lo, k0);
-                    weights8<kBf16>(a, a.kw, hi, k1);
+                    weights8<kBf16>(a, hw, lo, k0);
+                    weights8<kBf16>(a, hw, hi, k1);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         x0[e] *= f * k0[e];
@@ -392,9 +398,12 @@ __global__ void __launch_bounds__(32 * kWarps) k_rope_any(const RopeArgs a) {
 template <bool kBf16, bool kF32, bool kInter, bool kNorm>
 cudaError_t run(const RopeArgs &a, bool vec, cudaStream_t st) {
     const dim3 grid((unsigned)(((long long)a.s.N * a.parts + kWarps - 1) / kWarps)), block(32 * kWarps);
-    return launch(!vec        ? k_rope_any<kBf16, kF32, kInter, kNorm>
-                  : a.D == 64 ? k_rope_append<64, kBf16, kF32, kInter, kNorm>
-                              : k_rope_append<128, kBf16, kF32, kInter, kNorm>,
+    const bool few = kNorm && (a.Hq + 2 * a.Hkv) * (a.D / 16) <= 32 * kFewPasses;
+    return launch(!vec ? k_rope_any<kBf16, kF32, kInter, kNorm>
+                  : a.D == 64 ? (few ? k_rope_append<64, kBf16, kF32, kInter, kNorm, kNorm>
+                                     : k_rope_append<64, kBf16, kF32, kInter, kNorm, false>)
+                              : (few ? k_rope_append<128, kBf16, kF32, kInter, kNorm, kNorm>
+                                     : k_rope_append<128, kBf16, kF32, kInter, kNorm, false>),
                   grid, block, 0, st, true, a);
 }
 

@@ -185,3 +185,16 @@ def test_refusals():
         call(c, qkv, (w[0].cuda(), w[1].cuda().repeat(2)[::2]), pos, inv)      # not contiguous
     torch.cuda.synchronize()
     assert torch.equal(c.cache.k.cpu(), c.k)
+
+
+@pytest.mark.parametrize("Hkv,G,D,src", [(2, 6, 128, BF), (2, 7, 128, BF), (8, 5, 128, F32), (2, 14, 64, F32),
+                                         (2, 15, 64, BF), (8, 8, 64, BF), (1, 1, 128, F32)])
+def test_few_and_many_heads(Hkv, G, D, src):
+    """Up to four passes of a warp over a token's heads, and more; the last pass full or not."""
+    c = Case([33, 0, 700], [5, 1, 130], Hkv, G, D, 32, BF, seed=G).dev()
+    qkv, w, pos, inv = inputs(c, src, F32, D // 2)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = call(c, qkv, w, pos, inv, eps=1e-5, status=st)
+    torch.cuda.synchronize()
+    assert int(st) == 0
+    check(c, out, qkv, w, pos, inv, D // 2, False, 1.0, 1e-5)
