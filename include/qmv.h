@@ -572,8 +572,9 @@ int attn_evict(const qmv_attn_cache *src, const float *acc, const int32_t *table
  *   page   16, 32, 64, 128 or 256; pages <= 2^30; n <= 65535;
  *          max_pages * page <= 2^30; n * max_pages < 2^31
  *   status [1] int32 or NULL, OR-ed with
- *            1  an id past the pool in an entry, or a page given back that nobody
- *               held: that entry is left out;
+ *            1  an id past the pool in an entry, a page given back that nobody held,
+ *               or a parent's last, partly filled page that is not there: that entry
+ *               is left out;
  *            2  lengths (or a parent) that are negative or do not fit: that row is
  *               left as it is (attn_pages_fork: the child is empty);
  *            8  no free page was left for some entry.
@@ -609,8 +610,8 @@ size_t attn_pages_fork_workspace_bytes(int pages, int F);
  * copies it, in each layer's cache. A child for which no page is left (status 8) is
  * as long as its whole pages. Parents keep what they hold until attn_pages_update
  * takes it back.
- *   new_table [F][max_pages], new_lens [F], moves [F][3] int32 (written); not the
- *   parents' own arrays */
+ *   new_table [F][max_pages], new_lens [F], moves [F][3] int32 (written); not
+ *   arrays that the call reads */
 int attn_pages_fork(int32_t *refs, int pages, int page, const int32_t *table, int max_pages,
                     const int32_t *lens, int B, const int32_t *parent, int F, int32_t *new_table,
                     int32_t *new_lens, int32_t *moves, int32_t *status, void *ws, size_t ws_bytes,
@@ -636,7 +637,7 @@ int attn_pages_copy(const qmv_attn_cache *src, const qmv_attn_cache *dst, const 
  * whose kept tokens are not ascending or not its own, stays as it is
  * (status 2); moves from or to pages past the pool are left out (status 1).
  *   keep [N] int32, kept [B] int32; acc [pages][Hkv][page] or NULL (in place)
- *   new_ctx [B] int32 (written), not ctx itself */
+ *   new_ctx [B] int32 (written), not ctx, keep or kept */
 int attn_compact(const qmv_attn_cache *c, const int32_t *table, int max_pages, const int32_t *ctx,
                  const int32_t *cu, int B, int N, const int32_t *keep, const int32_t *kept, float *acc,
                  int32_t *new_ctx, int32_t *status, qmv_stream_t stream);

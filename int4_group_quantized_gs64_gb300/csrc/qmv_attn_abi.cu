@@ -256,7 +256,8 @@ int attn_pages_fork(int32_t *refs, int pages, int page, const int32_t *table, in
     if (r || (r = check_pages(pages, page, F, max_pages))) return r;
     if (F == 0) return QMV_OK;
     if (!refs || !table || !lens || !parent || !new_table || !new_lens || !moves) return QMV_EINVAL;
-    if (new_table == table || new_lens == lens) return QMV_EINVAL;  // children read their parents' rows
+    // (children read their parents' rows while others are written)
+    if (new_table == table || new_lens == lens || new_lens == parent) return QMV_EINVAL;
     if (!aligned(refs, 4) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(parent, 4) ||
         !aligned(new_table, 4) || !aligned(new_lens, 4) || !aligned(moves, 4) || !aligned(status, 4))
         return QMV_EALIGN;
@@ -292,7 +293,7 @@ int attn_compact(const qmv_attn_cache *c, const int32_t *table, int max_pages, c
     if (N < 0) return QMV_EINVAL;
     if (B == 0) return QMV_OK;
     if (!table || !ctx || !cu || (!keep && N) || !kept || !new_ctx) return QMV_EINVAL;
-    if (new_ctx == ctx) return QMV_EINVAL;  // other blocks still read ctx
+    if (new_ctx == ctx || new_ctx == kept || new_ctx == keep) return QMV_EINVAL;  // other blocks still read them
     if (!aligned(table, 4) || !aligned(ctx, 4) || !aligned(cu, 4) || !aligned(keep, 4) ||
         !aligned(kept, 4) || !aligned(acc, 4) || !aligned(new_ctx, 4) || !aligned(status, 4))
         return QMV_EALIGN;

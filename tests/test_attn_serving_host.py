@@ -188,3 +188,10 @@ def test_pages_copy(L):
     for k in ("moves", "da", "st"):
         assert copy(L, **{k: ODD}) == EALIGN, k
     assert copy(L, sa=ODD, da=P) == EALIGN
+
+
+def test_outputs_onto_what_other_blocks_read(L):
+    other = ctypes.c_void_p(FAKE + 128)
+    assert fork(L, parent=other, nl=other) == EINVAL
+    for k in ("ctx", "keep", "kept"):
+        assert compact(L, **{k: other, "out": other}) == EINVAL, k

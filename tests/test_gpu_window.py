@@ -279,3 +279,44 @@ def test_nothing_to_do_and_refusals():
         q.attn_window(c.cache, c.q.cuda().float(), *args[1:], 4)
     with pytest.raises(q.QmvError):
         q.attn_window(c.cache, *args, 4, ws=torch.empty(256, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("T,G,D,dt", [(3, 2, 128, BF), (40, 4, 128, BF), (150, 2, 128, FP), (70, 4, 64, FP),
+                                      (150, 2, 64, BF)])
+@pytest.mark.parametrize("out", ["same", "fp32"])
+@pytest.mark.parametrize("how", ["grow", "leap", "fall"])
+def test_scores_that_grow_and_fall_along_the_keys(T, G, D, dt, out, how):
+    """Maxima that move at every step, once and late, and never again."""
+    c = Win([900], [T], ALL, 0, 2, G, D, 64, dt, seed=T)
+    for j in range(900 + T):
+        f = {"grow": 2.0 ** (j // 100 - 4), "leap": 24.0 if j == 500 else 0.25, "fall": 2.0 ** (3 - j // 100)}[how]
+        c.k[c.table_l[0][j // 64], :, j % 64] *= f
+    o, lse = run(c, o_dtype=F32 if out == "fp32" else dt)
+    s = D ** -0.5
+    check_tree(c, o, lse, c.reference(s), p_rounding(c, s, o.dtype))
+
+
+@pytest.mark.parametrize("T,D,odt", [(3, 128, BF), (70, 128, BF), (70, 64, F32)])
+def test_outputs_on_a_16_byte_boundary_that_is_no_32_byte_one(T, D, odt):
+    c = Win([200], [T], 100, 4, 2, 4, D, 16, BF, seed=D)
+    o, lse = run(c, o_dtype=odt)
+    n = o.numel()
+    flat = torch.full((n + 64,), 7.0, dtype=odt, device="cuda")
+    at = 16 // flat.element_size()
+    odd = flat[at:at + n].view(o.shape)
+    assert odd.data_ptr() % 32 == 16
+    run(c, o=odd)
+    assert torch.equal(odd, o) and torch.all(flat[:at] == 7) and torch.all(flat[at + n:] == 7)
+
+
+@pytest.mark.parametrize("T,G,D", [(3, 2, 128), (60, 4, 128), (150, 2, 64)])
+def test_keys_that_are_not_finite(T, G, D):
+    """A NaN key spoils the rows that see it and no others."""
+    c = Win([300], [T], 64, 2, 1, G, D, 16, BF, seed=D)
+    o, lse = run(c)
+    j = 300 + T // 2
+    c.k[c.table_l[0][j // 16], :, j % 16, 5] = math.nan
+    p, y = run(c)
+    see = c.seen(0)[:, j].cuda()
+    assert torch.equal(p[~see], o[~see]) and torch.equal(y[~see], lse[~see])
+    assert torch.isnan(p[see]).all() and torch.isnan(y[see]).all()
