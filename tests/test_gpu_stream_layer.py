@@ -114,3 +114,58 @@ def test_example_runs():
     out = subprocess.run([sys.executable, PATH, "--steps", "60"], capture_output=True, text=True, timeout=600)
     assert out.returncode == 0, out.stderr[-2000:]
     assert "pages held" in out.stdout
+
+
+@pytest.mark.parametrize("T", [1, 9])
+def test_a_captured_step_takes_and_gives_back_pages(T):
+    """Pages, append, attention and lengths of a step in one graph: replays follow the eager steps
+    bit for bit while windows leave pages, others take them, and a page ends inside a step."""
+    q.build()
+    B, Hq, Hkv, D, page, W, S, pool = 5, 8, 2, 64, 16, 50, 3, 40
+    N = B * T
+    g = torch.Generator(device="cuda").manual_seed(T)
+    inv = 10000.0 ** (-torch.arange(0, D, 2, dtype=torch.float64, device="cuda") / D)
+    w = 1 + 0.1 * torch.randn(D, device="cuda", generator=g)
+    cu = torch.arange(0, N + 1, T, dtype=torch.int32, device="cuda")
+    more = torch.full((B,), T, dtype=torch.int32, device="cuda")
+
+    class Side:
+        def __init__(self):
+            self.cache = q.AttnCache.empty(pool, Hkv, page, D, torch.bfloat16, "cuda")
+            self.refs = torch.zeros(pool, dtype=torch.int32, device="cuda")
+            self.table = torch.full((B, 64), -1, dtype=torch.int32, device="cuda")
+            self.lens = torch.tensor([0, 3, 14, 15, 16], dtype=torch.int32, device="cuda")
+            self.x = torch.zeros(N, Hq + 2 * Hkv, D, device="cuda")
+            self.st = torch.zeros(1, dtype=torch.int32, device="cuda")
+            self.cache.k.zero_()
+            self.cache.v.zero_()
+
+        def step(self):
+            q.attn_pages_update(self.refs, self.table, self.lens, more, page, window=W, sinks=S, status=self.st)
+            a, k, v = self.x.split([Hq, Hkv, Hkv], 1)
+            pos = (self.lens[:, None] + torch.arange(T, dtype=torch.int32, device="cuda")).view(-1)
+            a = q.attn_norm_rope_append(self.cache, a, k, v, w, w, pos, inv, self.table, self.lens, cu, status=self.st)
+            self.o, self.lse = q.attn_window(self.cache, a, self.table, self.lens, cu, T, window=W, sinks=S,
+                                             status=self.st)
+            self.lens += T
+
+    one, two = Side(), Side()
+    start = [t.clone() for t in (two.refs, two.table, two.lens)]
+    two.step()          # (warm-up)
+    for t, v in zip((two.refs, two.table, two.lens), start):
+        t.copy_(v)
+    two.cache.k.zero_(), two.cache.v.zero_(), two.st.zero_()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        two.step()
+    for i in range(40):
+        x = torch.randn(N, Hq + 2 * Hkv, D, device="cuda", generator=g)
+        one.x.copy_(x), two.x.copy_(x)
+        one.step()
+        graph.replay()
+        assert torch.equal(one.o, two.o) and torch.equal(one.lse, two.lse), i
+        assert torch.equal(one.table, two.table) and torch.equal(one.refs, two.refs), i
+        assert int(one.st) == int(two.st) == 0
+    most = -(-(W + S + T) // page) + 3
+    assert 0 < int(one.refs.sum()) <= B * most and int(one.refs.max()) == 1
