@@ -105,9 +105,15 @@ __device__ __forceinline__ uint32_t window_word(const TreeArgs &a, int p, int sl
 struct Reach {
     int p0, p1, lo, sp, sw, nu;
     __device__ __forceinline__ void set(const TreeArgs &a, const Seq &q, int item) {
-        const int x = item * a.tpi, y = min(x + a.tpi, row_tiles(a, q)) - 1;
-        p0 = q.ctx + x / a.hs * a.tb;
-        p1 = q.ctx + min(y / a.hs * a.tb + a.tb, q.T) - 1;
+        const int x = item * a.tpi;
+        if (a.hs == 1) {  // (no divisions: planning goes through all items)
+            p0 = q.ctx + x * a.tb;
+            p1 = q.ctx + min((x + a.tpi) * a.tb, q.T) - 1;
+        } else {
+            const int y = min(x + a.tpi, row_tiles(a, q)) - 1;
+            p0 = q.ctx + x / a.hs * a.tb;
+            p1 = q.ctx + min(y / a.hs * a.tb + a.tb, q.T) - 1;
+        }
         lo = max(0, p0 - a.window + 1);
         sw = lo & -a.align;
         sp = (min(a.sinks, lo) + a.align - 1) & -a.align;
@@ -146,7 +152,9 @@ __device__ __forceinline__ long long window_units(const TreeArgs &a, const Seq &
     }
     return n;
 }
-constexpr int kAlone = 4;  // items that a thread adds up by itself
+// Items that a thread adds up by itself for every sequence that a warp would else add up
+// together: some 40 cycles each, against 600 a sequence.
+constexpr int kAlone = 16;
 
 // All units of a sequence, by one thread.
 template <bool kWin>
@@ -155,11 +163,13 @@ __device__ __forceinline__ long long seq_units(const TreeArgs &a, const Seq &q) 
     if (kWin) return window_units(a, q, 0, 1) * a.Hkv;
     return (long long)key_units(q, a.unit) * row_blocks(q, a.G, a.rows) * a.Hkv;
 }
-// A lane's sequence each; the whole warp helps with long ones.
+// A lane's sequence each; the whole warp helps with long ones where they are few.
 template <bool kWin>
 __device__ __forceinline__ long long lane_units(const TreeArgs &a, const Seq &q) {
     if (!kWin) return seq_units<false>(a, q);
-    const bool big = q.T > 0 && window_items(a, q) > kAlone;
+    const int items = q.T > 0 ? window_items(a, q) : 0;
+    const int several = __popc(__ballot_sync(0xFFFFFFFFu, items > kAlone / 4));
+    const bool big = items > kAlone * max(several, 1);
     long long n = big ? 0 : seq_units<true>(a, q);
     for (uint32_t who = __ballot_sync(0xFFFFFFFFu, big); who; who &= who - 1) {
         const int from = __ffs(who) - 1, lane = threadIdx.x & 31;
