@@ -219,9 +219,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, m->tmem, 0);
     const int units = (int)(sh.u1 - sh.u0);  // (the launcher keeps this below 2^31)
 
-    // 168 x 384 registers at launch = 216 x 256 + 72 x 128
+    // 168 x 384 registers at launch = 216 x 256 + 72 x 128 = 208 x 256 + 88 x 128. With 64
+    // elements the softmax has some to spare, and the warps that copy and issue keep
+    // theirs out of memory (16 chunks to fp32 105 -> 101 us; with 128 elements long
+    // contexts to fp32 go from 2,190 to 2,270, prompts differ by less than a percent).
+    constexpr int kSoftRegs = D == 64 ? 208 : 216, kIssueRegs = D == 64 ? 88 : 72;
     if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
     if (warp == 8 || warp == 11) {
         // ------------------------------------------------------------ copies
         const bool keys = warp == 8;
@@ -613,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     } else {
         // ------------------------------------------------------------ softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         const int s = warp >> 2, tid = threadIdx.x & 127, wq = warp & 3;
         const uint32_t lanes = (uint32_t)(wq * 32) << 16;
         const uint32_t ts = tmem + lanes + s * 128, to = tmem + lanes + kOcol;
@@ -724,6 +728,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if constexpr (kSplit) {
                         // The scores twice from tensor memory, 32 at a time: O has the registers.
+                        constexpr int kUnroll = D == 64 ? 1 : 2;
                         float tm = -INFINITY;
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
@@ -746,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         const float base = mx == -INFINITY ? 0.f : mx - boost;
                         const uint64_t nb = pack_f32x2(-base, -base);
-#pragma unroll 2
+#pragma unroll kUnroll
                         for (int h = 0; h < 8; ++h) {  // 16 at a time: one step of the product
                             if (h == 4) give(m->p_half);
                             uint32_t x[16], hi[8], lo[8], third[8];
