@@ -446,8 +446,9 @@ int attn_rope_append(const qmv_attn_cache *c, const void *q, int64_t q_stride, c
  *     x_i * w_i / sqrt(mean(x^2) + eps)
  * (the mean over its D elements, all of them, also where rot < D), then is turned
  * and goes to q_out or the cache as above; values pass unchanged. In fp32 from the
- * inputs to the one rounding at the end. A head of zeros stays zeros, also with
- * eps = 0; one whose squares add up to more than fp32 holds becomes zeros.
+ * inputs to the one rounding at the end, heads of any finite magnitude (where their
+ * squares leave fp32's range they are scaled by a power of two first). A head of
+ * zeros stays zeros, also with eps = 0.
  *   q_weight, k_weight [D] in w_dtype (QMV_F32 or the cache's), aligned to it, or
  *     NULL: ones; 16-byte aligned ones keep the vector path
  *   eps finite, >= 0; everything else as attn_rope_append. */
