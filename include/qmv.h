@@ -575,7 +575,7 @@ int attn_evict(const qmv_attn_cache *src, const float *acc, const int32_t *table
  *   status [1] int32 or NULL, OR-ed with
  *            1  an id past the pool in an entry, a page given back that nobody held,
  *               or a parent's last, partly filled page that is not there: that entry
- *               is left out;
+ *               is left out (attn_pages_fork: the child ends before it);
  *            2  lengths (or a parent) that are negative or do not fit: that row is
  *               left as it is (attn_pages_fork: the child is empty);
  *            8  no free page was left for some entry.
@@ -608,9 +608,9 @@ size_t attn_pages_fork_workspace_bytes(int pages, int F);
  * long. Whole pages are shared (their refs grow); a last page that is partly filled
  * is replaced by the lowest free page, and moves[f] says what to copy to it:
  * (page to copy from, page to copy to, tokens), or (-1, -1, 0). attn_pages_copy
- * copies it, in each layer's cache. A child for which no page is left (status 8) is
- * as long as its whole pages. Parents keep what they hold until attn_pages_update
- * takes it back.
+ * copies it, in each layer's cache. A child for which no page is left (status 8), or
+ * whose parent's partly filled page is not there (status 1), is as long as its whole
+ * pages. Parents keep what they hold until attn_pages_update takes it back.
  *   new_table [F][max_pages], new_lens [F], moves [F][3] int32 (written); not
  *   arrays that the call reads */
 int attn_pages_fork(int32_t *refs, int pages, int page, const int32_t *table, int max_pages,

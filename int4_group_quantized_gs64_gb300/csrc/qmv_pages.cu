@@ -251,11 +251,13 @@ __global__ void __launch_bounds__(kSmall) k_pages_share(const PagesArgs a) {
                 set_status(a.status, kStPage);
             }
         }
+        // (without it the child ends with its whole pages: a hole there would be filled
+        // by the next update, with a page that its tokens were never written to)
         a.miss[f] = id >= 0;
         a.moves[f * 3LL] = id;
         a.moves[f * 3LL + 1] = -1;
         a.moves[f * 3LL + 2] = id >= 0 ? rows : 0;
-        a.new_lens[f] = ok ? len : 0;
+        a.new_lens[f] = ok ? (id >= 0 ? len : whole << a.lpage) : 0;
         if (!ok) set_status(a.status, kStLength);
     }
 }
