@@ -597,7 +597,8 @@ size_t attn_pages_update_workspace_bytes(int pages, int B, int max_pages);
  * Tokens are to be appended only to pages that their sequence holds alone:
  * attn_pages_fork leaves it so; a sequence that is cut back into a page it shares
  * is forked (from itself) first.
- *   refs, table  updated in place; window >= 1 (INT32_MAX: none), sinks >= 0 */
+ *   refs, table  updated in place, and share no bytes with lens, more or one another
+ *   window >= 1 (INT32_MAX: none), sinks >= 0 */
 int attn_pages_update(int32_t *refs, int pages, int page, int32_t *table, int max_pages,
                       const int32_t *lens, const int32_t *more, int B, int window, int sinks,
                       int32_t *status, void *ws, size_t ws_bytes, qmv_stream_t stream);
@@ -611,8 +612,8 @@ size_t attn_pages_fork_workspace_bytes(int pages, int F);
  * copies it, in each layer's cache. A child for which no page is left (status 8), or
  * whose parent's partly filled page is not there (status 1), is as long as its whole
  * pages. Parents keep what they hold until attn_pages_update takes it back.
- *   new_table [F][max_pages], new_lens [F], moves [F][3] int32 (written); not
- *   arrays that the call reads */
+ *   new_table [F][max_pages], new_lens [F], moves [F][3] int32 (written); they
+ *   share no bytes with one another or with what the call reads */
 int attn_pages_fork(int32_t *refs, int pages, int page, const int32_t *table, int max_pages,
                     const int32_t *lens, int B, const int32_t *parent, int F, int32_t *new_table,
                     int32_t *new_lens, int32_t *moves, int32_t *status, void *ws, size_t ws_bytes,
@@ -638,7 +639,7 @@ int attn_pages_copy(const qmv_attn_cache *src, const qmv_attn_cache *dst, const 
  * whose kept tokens are not ascending or not its own, stays as it is
  * (status 2); moves from or to pages past the pool are left out (status 1).
  *   keep [N] int32, kept [B] int32; acc [pages][Hkv][page] or NULL (in place)
- *   new_ctx [B] int32 (written), not ctx, keep or kept */
+ *   new_ctx [B] int32 (written); it shares no bytes with what the call reads */
 int attn_compact(const qmv_attn_cache *c, const int32_t *table, int max_pages, const int32_t *ctx,
                  const int32_t *cu, int B, int N, const int32_t *keep, const int32_t *kept, float *acc,
                  int32_t *new_ctx, int32_t *status, qmv_stream_t stream);

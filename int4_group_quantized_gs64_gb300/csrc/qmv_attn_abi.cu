@@ -4,6 +4,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "../../include/qmv.h"
 #include "qmv_attn.h"
 
@@ -56,6 +58,21 @@ int check_pages(int pages, int page, int n, int max_pages) {
         (int64_t)n * max_pages > INT32_MAX)
         return QMV_ESHAPE;
     return QMV_OK;
+}
+
+// An int32 array of a call.
+struct Ints {
+    const int32_t *p;
+    int64_t n;
+};
+// Blocks write `out` while others still read or write the `rest`: no shared bytes.
+bool apart(const Ints &out, std::initializer_list<Ints> rest) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(out.p), e = a + 4 * (uintptr_t)out.n;
+    for (const Ints &r : rest) {
+        const uintptr_t b = reinterpret_cast<uintptr_t>(r.p);
+        if (a < b + 4 * (uintptr_t)r.n && b < e) return false;
+    }
+    return true;
 }
 
 // Both rotary appends; norm null: without norms.
@@ -240,6 +257,8 @@ int attn_pages_update(int32_t *refs, int pages, int page, int32_t *table, int ma
         return QMV_EALIGN;
     if (!ws || !aligned(ws, 256) || ws_bytes < qmv::pages_update_ws_bytes(pages, B, max_pages))
         return QMV_EWORKSPACE;
+    const Ints ta{table, (int64_t)B * max_pages}, le{lens, B}, mo{more, B};
+    if (!apart(ta, {le, mo}) || !apart(Ints{refs, pages}, {ta, le, mo})) return QMV_EINVAL;
     return from_cuda(qmv::launch_pages_update(refs, pages, page, table, max_pages, lens, more, B,
                                               window, sinks, status, ws, cs(stream)));
 }
@@ -256,13 +275,16 @@ int attn_pages_fork(int32_t *refs, int pages, int page, const int32_t *table, in
     if (r || (r = check_pages(pages, page, F, max_pages))) return r;
     if (F == 0) return QMV_OK;
     if (!refs || !table || !lens || !parent || !new_table || !new_lens || !moves) return QMV_EINVAL;
-    // (children read their parents' rows while others are written)
-    if (new_table == table || new_lens == lens || new_lens == parent) return QMV_EINVAL;
     if (!aligned(refs, 4) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(parent, 4) ||
         !aligned(new_table, 4) || !aligned(new_lens, 4) || !aligned(moves, 4) || !aligned(status, 4))
         return QMV_EALIGN;
     if (!ws || !aligned(ws, 256) || ws_bytes < qmv::pages_fork_ws_bytes(pages, F))
         return QMV_EWORKSPACE;
+    // (children read their parents' rows while others are written)
+    const Ints re{refs, pages}, ta{table, (int64_t)B * max_pages}, le{lens, B}, pa{parent, F};
+    const Ints nt{new_table, (int64_t)F * max_pages}, nl{new_lens, F}, mv{moves, (int64_t)F * 3};
+    if (!apart(nt, {re, ta, le, pa, nl, mv}) || !apart(nl, {re, ta, le, pa, mv}) || !apart(mv, {re, ta, le, pa}))
+        return QMV_EINVAL;
     return from_cuda(qmv::launch_pages_fork(refs, pages, page, table, max_pages, lens, B, parent, F,
                                             new_table, new_lens, moves, status, ws, cs(stream)));
 }
@@ -293,10 +315,12 @@ int attn_compact(const qmv_attn_cache *c, const int32_t *table, int max_pages, c
     if (N < 0) return QMV_EINVAL;
     if (B == 0) return QMV_OK;
     if (!table || !ctx || !cu || (!keep && N) || !kept || !new_ctx) return QMV_EINVAL;
-    if (new_ctx == ctx || new_ctx == kept || new_ctx == keep) return QMV_EINVAL;  // other blocks still read them
     if (!aligned(table, 4) || !aligned(ctx, 4) || !aligned(cu, 4) || !aligned(keep, 4) ||
         !aligned(kept, 4) || !aligned(acc, 4) || !aligned(new_ctx, 4) || !aligned(status, 4))
         return QMV_EALIGN;
+    // (other blocks still read them)
+    if (!apart(Ints{new_ctx, B}, {Ints{table, (int64_t)B * max_pages}, Ints{ctx, B}, Ints{cu, B + 1}, Ints{keep, N}, Ints{kept, B}}))
+        return QMV_EINVAL;
     return from_cuda(qmv::launch_attn_compact(cache(c), qmv::AttnSeqs{table, ctx, cu, B, N, 0, max_pages},
                                               keep, kept, acc, new_ctx, status, cs(stream)));
 }
