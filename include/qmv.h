@@ -531,7 +531,10 @@ size_t attn_window_workspace_bytes(const qmv_attn_cache *c, int Hq, int B, int N
  *     elements apart (a multiple of 8); N <= 2^22
  *   max_new  an upper bound of a sequence's new tokens, >= 1, at most 2^22 and
  *     2^30 / (Hq / Hkv); calls of up to 16 / (Hq / Hkv) take a kernel made for few rows
- *   window >= 1 (INT32_MAX: all tokens before), sinks >= 0
+ *   window >= 1 (INT32_MAX: all tokens before), sinks >= 0. The work is counted in
+ *     steps of 64 to 128 keys (of min(window + sinks, max_pages * page), plus a few
+ *     pieces) by up to 16 rows (the kernel for few) or 128 / (Hq / Hkv) or twice as
+ *     many tokens; 2^31 steps a thread block, hours of work, are refused (QMV_ESHAPE)
  *   o     [N][Hq][D] in o_dtype (QMV_F32 or the cache's), 16-byte aligned
  *   lse   [N][Hq] fp32
  *   ws  at least attn_window_workspace_bytes(...) bytes, 256-byte aligned, not

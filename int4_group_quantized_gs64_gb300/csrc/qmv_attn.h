@@ -73,6 +73,8 @@ struct WindowCall {
     void *ws;
 };
 size_t attn_window_ws_bytes(const AttnCache &c, int Hq, int max_new);
+// Whether a block's share of the call's units can be counted in 31 bits.
+bool attn_window_fits(const AttnCache &c, const AttnSeqs &s, int Hq, int window, int sinks);
 cudaError_t launch_attn_window(const AttnCache &c, const WindowCall &t, cudaStream_t st);
 
 cudaError_t launch_attn_evict(const AttnCache &src, const float *acc, const int32_t *table,

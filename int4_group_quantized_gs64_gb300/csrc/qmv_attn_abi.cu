@@ -210,6 +210,7 @@ int attn_window(const qmv_attn_cache *c, const void *q, int64_t q_stride, int Hq
         return QMV_EWORKSPACE;
     qmv::WindowCall t;
     t.s = qmv::AttnSeqs{table, ctx, cu, B, N, max_new, max_pages};
+    if (!qmv::attn_window_fits(cache(c), t.s, Hq, window, sinks)) return QMV_ESHAPE;
     t.q = q; t.q_stride = q_stride; t.Hq = Hq;
     t.window = window; t.sinks = sinks; t.scale = scale;
     t.o = o; t.o_f32 = o_dtype == QMV_F32; t.lse = lse;

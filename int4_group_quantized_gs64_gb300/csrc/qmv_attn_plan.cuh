@@ -371,6 +371,14 @@ __device__ __forceinline__ Share find_share(const TreeArgs &a, ShareScratch<kThr
     return s;
 }
 
+// kWin: shares that 31 bits do not count. The launcher refuses them; only sequences that
+// overlap (cu not ascending) add up to more than it knows of. Whole grid.
+__device__ __forceinline__ bool too_long(const TreeArgs &a, const Share &s) {
+    if (s.quota <= 0x7FFFFFFFLL) return false;
+    if (threadIdx.x == 0) set_status(a.status, kStLength);
+    return true;
+}
+
 // The place of a unit: sequence, head, row block (item), unit of the item's keys.
 template <bool kWin>
 struct CursorOf {

@@ -91,6 +91,7 @@ __global__ void __launch_bounds__(32 * kWarps, 2)
     }
     const Share sh = find_share<32 * kWarps, kWin>(a, share);
     if (kWin && threadIdx.x == 0) a.info[blockIdx.x * 2].n = a.info[blockIdx.x * 2 + 1].n = 0;
+    if (kWin && too_long(a, sh)) return;
     if (sh.u0 >= sh.u1) return;
     const int units = (int)(sh.u1 - sh.u0);  // (the launcher keeps this below 2^31)
 

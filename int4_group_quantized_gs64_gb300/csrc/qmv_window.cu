@@ -16,6 +16,8 @@
 #include <math.h>
 #include <string.h>
 
+#include <algorithm>
+
 #include "qmv_attn.cuh"
 #include "qmv_attn.h"
 #include "qmv_attn_join.cuh"
@@ -55,6 +57,27 @@ void set_rows(TreeArgs &a, int max_new) {
     a.hinv = (uint32_t)(((1ull << 32) + a.hb - 1) / a.hb);
 }
 
+// Rows and keys of a unit; a.s, a.G, a.window and a.sinks are set.
+void set_units(TreeArgs &a, const AttnCache &c) {
+    set_rows(a, a.s.max_draft);
+    a.unit = a.rows == kRows ? kWarps * 16 * (128 / c.D) : 128;  // keys a unit
+    a.lunit = 0;
+    while ((1 << a.lunit) < a.unit) ++a.lunit;
+    a.align = a.rows == kRows ? 16 : c.page < 128 ? c.page : 128;
+}
+
+// Units of a call, at most: the items of B sequences at their bound, or of N tokens (a
+// sequence's last item may be short), each over what its tokens may see (Reach: first
+// slots and those from the first token's window to the last token, each stretch to
+// whole pieces of a.align slots), or over the table's row where that is less.
+long long units_at_most(const TreeArgs &a, int Hkv) {
+    const long long items = std::min(a.s.B * items_a_head(a, a.s.max_draft), items_a_head(a, a.s.N) + a.s.B);
+    const long long tokens = std::min<long long>(a.s.max_draft, (long long)a.tpi * a.tb);
+    const long long seen = (long long)a.window + a.sinks + tokens + 2 * a.align;
+    const long long slots = std::min((long long)a.s.max_pages << a.s.lpage, seen);
+    return items * Hkv * (((slots + a.unit - 1) >> a.lunit) + 2);
+}
+
 template <int D, bool kBf16>
 cudaError_t run_window(const AttnCache &c, const TreeArgs &a, cudaStream_t st) {
     const bool few = a.rows == kRows;
@@ -80,16 +103,31 @@ size_t attn_window_ws_bytes(const AttnCache &c, int Hq, int max_new) {
     return (n + 255) / 256 * 256;
 }
 
+// What the plan goes by.
+static void plan_window(attn::TreeArgs &a, const AttnCache &c, const AttnSeqs &s, int Hq, int window, int sinks) {
+    int lpage = 0;
+    while ((1 << lpage) < c.page) ++lpage;
+    a.s = attn::Seqs{s.table, s.ctx, s.cu, s.B, s.N, s.max_draft, s.max_pages, c.page, lpage, 0};
+    a.G = Hq / c.Hkv;
+    a.window = window;
+    a.sinks = sinks;
+    attn::set_units(a, c);
+}
+
+bool attn_window_fits(const AttnCache &c, const AttnSeqs &s, int Hq, int window, int sinks) {
+    attn::TreeArgs a;
+    plan_window(a, c, s, Hq, window, sinks);
+    return attn::units_at_most(a, c.Hkv) / attn::attn_grid_max(a.rows) < 0x7FFFFFFFLL;
+}
+
 cudaError_t launch_attn_window(const AttnCache &c, const WindowCall &t, cudaStream_t st) {
     using namespace attn;
     TreeArgs a;
     memset(&a, 0, sizeof(a));
-    int lpage = 0;
-    while ((1 << lpage) < c.page) ++lpage;
-    a.s = Seqs{t.s.table, t.s.ctx, t.s.cu, t.s.B, t.s.N, t.s.max_draft, t.s.max_pages, c.page, lpage, 0};
+    plan_window(a, c, t.s, t.Hq, t.window, t.sinks);
     a.q = static_cast<const uint16_t *>(t.q);
     a.q_stride = t.q_stride;
-    a.Hq = t.Hq; a.Hkv = c.Hkv; a.G = t.Hq / c.Hkv; a.pages = c.pages;
+    a.Hq = t.Hq; a.Hkv = c.Hkv; a.pages = c.pages;
     a.ginv = (uint32_t)(((1ull << 32) + a.G - 1) / a.G);
     // (k_attn_rows turns or clears the queries, k_window_tc the scores)
     a.sl2 = t.scale == 0.f ? 1.f : fabsf(t.scale) * kLog2e;
@@ -99,20 +137,8 @@ cudaError_t launch_attn_window(const AttnCache &c, const WindowCall &t, cudaStre
     a.o = t.o; a.o_f32 = t.o_f32; a.lse = t.lse;
     a.vpool = static_cast<const uint16_t *>(c.v);
     a.status = t.status;
-    a.window = t.window; a.sinks = t.sinks;
-    set_rows(a, t.s.max_draft);
-    a.unit = a.rows == kRows ? kWarps * 16 * (128 / c.D) : 128;  // keys a unit
-    while ((1 << a.lunit) < a.unit) ++a.lunit;
-    a.align = a.rows == kRows ? 16 : c.page < 128 ? c.page : 128;
-    // units at most: the items of B sequences at their bound, or of N tokens (a
-    // sequence's last item may be short), each over a whole table row
-    long long items = t.s.B * items_a_head(a, t.s.max_draft);
-    const long long by_n = items_a_head(a, t.s.N) + t.s.B;
-    if (by_n < items) items = by_n;
-    const long long most = items * c.Hkv * (((((long long)t.s.max_pages << lpage) + a.unit - 1) >> a.lunit) + 2);
     const int gmax = attn_grid_max(a.rows);
-    if (most / gmax >= 0x7FFFFFFFLL) return cudaErrorInvalidValue;  // a block's units fit 31 bits
-    a.grid = most < gmax ? (int)most : gmax;
+    a.grid = (int)std::min<long long>(units_at_most(a, c.Hkv), gmax);
     a.part_o = static_cast<float *>(t.ws);
     a.part_ml = a.part_o + (size_t)gmax * 2 * a.rows * c.D;
     a.info = reinterpret_cast<PartInfo *>(a.part_o + part_floats(c, a.rows));

@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const Share sh = find_share<kThreads, true>(a, &m->share);
     if (threadIdx.x == 0) a.info[blockIdx.x * 2].n = a.info[blockIdx.x * 2 + 1].n = 0;
-    if (sh.u0 >= sh.u1) return;
+    if (too_long(a, sh) || sh.u0 >= sh.u1) return;
     if (warp == 9) tc05::tmem_alloc(&m->tmem, 512);
     tc05::fence_before_sync();
     __syncthreads();
