@@ -527,6 +527,12 @@ size_t attn_window_workspace_bytes(const qmv_attn_cache *c, int Hq, int B, int N
  * one of the sequence's new tokens sees are not looked at: their table entries
  * may be anything, and they may belong to others by now. Sequences may share
  * pages. Results do not depend on the order in which thread blocks finish.
+ * Scores, maxima, sums and outputs are fp32. Where max_new * Hq / Hkv is above 16
+ * and o has 16 bits, every exp(x_j - M) is rounded once to the cache's type before it
+ * meets its value (half a step of the weight; in all 1.4 times the error of the
+ * output's own rounding); otherwise it is carried as two or three 16-bit numbers, and
+ * o is off by its own rounding. So the precision of 16-bit outputs, not of fp32 ones,
+ * depends on max_new.
  *   q [N] rows of Hq * D in the cache's type, 16-byte aligned, q_stride
  *     elements apart (a multiple of 8); N <= 2^22
  *   max_new  an upper bound of a sequence's new tokens, >= 1, at most 2^22 and
@@ -536,7 +542,7 @@ size_t attn_window_workspace_bytes(const qmv_attn_cache *c, int Hq, int B, int N
  *     pieces) by up to 16 rows (the kernel for few) or 128 / (Hq / Hkv) or twice as
  *     many tokens; 2^31 steps a thread block, hours of work, are refused (QMV_ESHAPE)
  *   o     [N][Hq][D] in o_dtype (QMV_F32 or the cache's), 16-byte aligned
- *   lse   [N][Hq] fp32
+ *   lse   [N][Hq] fp32; o and lse are not arrays that the call reads
  *   ws  at least attn_window_workspace_bytes(...) bytes, 256-byte aligned, not
  *     shared with a concurrent call. */
 int attn_window(const qmv_attn_cache *c, const void *q, int64_t q_stride, int Hq,

@@ -11,8 +11,9 @@ forms ``qmv_int4_gs_bf16`` and ``qmv_int8_row_bf16``,
 ``moe_route_topk``, ``moe_group``, ``moe_gate_up_silu``, ``moe_down``,
 ``moe_combine``, ``moe_workspace_bytes``, ``moe_expert_ffn_int4`` and
 ``moe_expert_ffn_int4_prefill``; ``attn_rope_append``, ``attn_norm_rope_append``,
-``attn_tree``, ``attn_window``, ``attn_evict`` and ``attn_compact`` over a paged cache (``AttnCache``), and ``attn_pages_update``, ``attn_pages_fork`` and
-``attn_pages_copy`` for its pages.
+``attn_tree``, ``attn_window``, ``attn_evict`` and ``attn_compact`` over a paged cache
+(``AttnCache``), and ``attn_pages_update``, ``attn_pages_fork`` and ``attn_pages_copy``
+for its pages.
 """
 from __future__ import annotations
 
@@ -666,7 +667,9 @@ def attn_window(cache: AttnCache, q, table, ctx, cu, max_new: int, window=None, 
     q [N][Hq][D] in the cache's type; max_new an upper bound of a sequence's new tokens (any
     number). The token at slot p sees the slots j <= p with j > p - window (None: all) or
     j < sinks; pages that no new token of a sequence sees may be missing from its table. scale
-    defaults to D ** -0.5; o_dtype the cache's (default) or float32."""
+    defaults to D ** -0.5; o_dtype the cache's (default) or float32. Towards 16-bit outputs the
+    weights of more than 16 rows a key/value head (max_new * Hq / Hkv) are rounded once to 16 bits;
+    of fewer, and towards float32, they are not."""
     import torch
     if o_dtype is None:
         o_dtype = cache.dtype if o is None else o.dtype

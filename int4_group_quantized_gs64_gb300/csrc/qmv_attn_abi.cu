@@ -320,7 +320,8 @@ int attn_compact(const qmv_attn_cache *c, const int32_t *table, int max_pages, c
         !aligned(kept, 4) || !aligned(acc, 4) || !aligned(new_ctx, 4) || !aligned(status, 4))
         return QMV_EALIGN;
     // (other blocks still read them)
-    if (!apart(Ints{new_ctx, B}, {Ints{table, (int64_t)B * max_pages}, Ints{ctx, B}, Ints{cu, B + 1}, Ints{keep, N}, Ints{kept, B}}))
+    if (!apart(Ints{new_ctx, B}, {Ints{table, (int64_t)B * max_pages}, Ints{ctx, B}, Ints{cu, B + 1},
+                                  Ints{keep, N}, Ints{kept, B}}))
         return QMV_EINVAL;
     return from_cuda(qmv::launch_attn_compact(cache(c), qmv::AttnSeqs{table, ctx, cu, B, N, 0, max_pages},
                                               keep, kept, acc, new_ctx, status, cs(stream)));

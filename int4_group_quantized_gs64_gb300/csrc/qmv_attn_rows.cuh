@@ -1,6 +1,5 @@
 // qmv_attn_rows.cuh - attention of few rows on the warp MMA: trees of drafts
 // (qmv_attn_tree.cu) and causal rows with a sliding window (qmv_window.cu).
-//
 #pragma once
 
 #include "qmv_attn.cuh"
@@ -494,7 +493,7 @@ cudaError_t run_rows(const AttnCache &c, const TreeArgs &a, cudaStream_t st) {
     return e;
 }
 
-// Rows an item: up to 16 on the warp MMA, more on tcgen05 (qmv_attn_tc.cuh).
+// Rows an item: up to 16 on the warp MMA, more on tcgen05 (qmv_attn_tc.cu, qmv_window_tc.cu).
 // With 16 rows the two measured 250 and 240 us (64 sequences of 8191 keys), 124
 // and 156 with 64 elements a head, and 12.3 and 15.4 us (one of 777 keys); with 32
 // rows 452 and 244. Above 128 rows two tiles share the keys: 192 rows over 16 x

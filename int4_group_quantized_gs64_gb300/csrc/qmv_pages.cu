@@ -128,9 +128,11 @@ __device__ __forceinline__ int scan_misses(const PagesArgs &a, int n, int *sh) {
 
 // The `want` lowest free pages, or as many as there are, to the list, each held
 // once from here on; returns how many. A warp looks at 256 pages a pass, and loads
-// the next pass's meanwhile: what bounds it is the latency of a pass (an update
-// that takes 36,000 pages out of 670,000, with its two copies: 42 us in passes of
-// 128 pages a warp without that, 30 so).
+// the next pass's meanwhile: what bounds it is the latency of a pass. (An update of
+// 1,024 sequences that takes 34,345 pages, the last of them number 94,590 of 650,492,
+// looks at 12 passes: GPU time with the two copies around it 42 us in passes of 128
+// pages a warp without loading ahead, 30 so. By themselves and from cold the three
+// kernels take 7, 20 and 7 us.)
 __device__ __forceinline__ int take_free(const PagesArgs &a, int want, int *sh) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     constexpr int kPer = 8, kPass = kOne * kPer;

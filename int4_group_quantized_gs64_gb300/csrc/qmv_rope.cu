@@ -17,13 +17,13 @@
 // so the norm costs no traffic. Where the sum of squares leaves fp32's range (elements
 // near 1e19 or, with an eps as small, near 1e-16 and below) the head is scaled by a
 // power of two first and its squares are added up again: a vote a pass, and code that
-// ordinary heads do not run (16,372 tokens of 64 heads 92.6 -> 93.7 us).
+// ordinary heads do not run (14,839 tokens of 64 heads 92.6 -> 93.7 us).
 //
 // A warp takes one token (or a share of its heads, so that few tokens fill the
 // GPU too). D / 16 lanes share a head, 16 elements each: a lane has the same
 // place in every head that it meets, and so the same eight angles, which stay
 // in registers: no shared memory, no barrier. The lanes that share a place
-// divide its eight angles and exchange them. What bounds it is the copy: 16,372
+// divide its eight angles and exchange them. What bounds it is the copy: 14,839
 // tokens of 64 heads take 82 us, 5.9 TB/s of the 486 MB they read and write; one
 // token takes a launch (4.5 us).
 #include "qmv_attn.cuh"
@@ -227,8 +227,8 @@ __device__ __forceinline__ void clear_sums(const RopeArgs &a, int lane, int pid,
 
 // Rows and strides on 16-byte boundaries, rot a multiple of 16. kFew (with norms): for
 // tokens whose heads are few passes of a warp, where a token's slot and angles are what
-// it costs: more warps an SM, and no weights kept in registers (7 heads of 128, 54,000
-// tokens: 137 -> 111 us; 4 + 4 heads, 11,600 tokens: 41 -> 30; 64 heads, 14 passes,
+// it costs: more warps an SM, and no weights kept in registers (7 heads of 128, 70,803
+// tokens: 137 -> 111 us; 4 + 4 heads, 20,361 tokens: 41 -> 30; 64 heads, 14 passes,
 // 92 -> 97, so those go the other way).
 constexpr int kFewPasses = 4;
 template <int D, bool kBf16, bool kF32, bool kInter, bool kNorm, bool kFew>
@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(32 * kWarps, kNorm ? (kFew ? 7 : 4) : 0) k_rop
         }
     };
     // (norms take longer than the turns alone: the next heads are on their way meanwhile,
-    // the first ones while slot and angles are found; 103 -> 92 us for 16,372 tokens)
+    // the first ones while slot and angles are found; 103 -> 92 us for 14,839 tokens)
     if (kNorm) load(next, hb);
     int pid, row;
     const bool good = find_slot(a, n, lane, pid, row);

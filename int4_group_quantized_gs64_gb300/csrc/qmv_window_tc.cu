@@ -14,8 +14,10 @@
 // A stream's chain of a step is 1,024 cycles of products (at 128 elements) and its
 // softmax; the two streams together need 2,048 of products and, side by side, some
 // 1,400 of softmax (exponentials 512 a stream, and as much again for scaling, sums,
-// packing and the maximum). For fp32 outputs the softmax is what bounds a step: some
-// 3,500 cycles with two or three numbers a weight. What shortens the chain: the next
+// packing and the maximum). For fp32 outputs the softmax is what bounds a step, some
+// 3,500 cycles with two or three numbers a weight, and of these more are waits than
+// issue (41% of the issue slots taken, loads from tensor memory the top stall: two
+// softmax warps a scheduler do not cover each other's). What shortens the chain: the next
 // scores are issued right behind the output's products, in turns that hold nothing but
 // the issue; products of two or three numbers a weight begin when half of the keys have
 // theirs; a step's weights come from the maximum that its rows have, so that no
@@ -26,11 +28,12 @@
 // tensor-map copies while the last softmax runs, and its scores are formed while O
 // is written out. The streams do not wait for one another there.
 //
-// Measured: 12,279 prompt tokens of 48 heads (8 key/value heads of 128), windows of
-// 2048, 16-bit outputs: 466 us, 1,141 TFLOP/s (the kernel of qmv_attn_tc.cu, with
+// Measured (GPU time, from captured graphs; 479 and 101 us through the Python calls):
+// 10,746 prompt tokens of 48 heads (8 key/value heads of 128), windows of
+// 2048, 16-bit outputs: 467 us, 1,139 TFLOP/s (the kernel of qmv_attn_tc.cu, with
 // windows: 678). Of that the steps at the edges cost some 27 us, the look at values
 // 24, writing O 28. 16 chunks of up to 301 tokens of 40 heads (8 of 64 elements),
-// windows of 513 and 17 first tokens, fp16 to fp32: 98 us, 235 TFLOP/s (with the
+// windows of 513 and 17 first tokens, fp16 to fp32: 99 us, 234 TFLOP/s (with the
 // kernel of qmv_attn_tc.cu 178 us).
 //
 // Masks: a step that all rows of the item see whole is not looked at. In the others
@@ -40,9 +43,12 @@
 // that do see them get them added at the end (Misc::odd).
 //
 // The maximum in use moves when it is found to have grown by more than 2^8; weights
-// and sums for 16-bit and fp32 outputs are those of qmv_attn_tc.cu: rounded once to
-// 16 bits, or two fp16 / three bf16 numbers and sums of each step added up in
-// registers.
+// and sums for 16-bit and fp32 outputs are those of qmv_attn_tc.cu. For 16-bit outputs a
+// weight is rounded once, to half a step of itself, as the operand of its product: a
+// second number would be half as many products again (1,024 cycles more a step of 2,840),
+// and the output is rounded to the same type anyway (prompts against 64 bits: 2.3e-3 of
+// the norm, the output's rounding alone 1.7e-3). For fp32 outputs two fp16 or three bf16
+// numbers, and sums of each step added up in registers: 5e-7.
 #include <cudaTypedefs.h>
 #include <string.h>
 
