@@ -28,7 +28,7 @@
 // tensor-map copies while the last softmax runs, and its scores are formed while O
 // is written out. The streams do not wait for one another there.
 //
-// Measured (GPU time, from captured graphs; 479 and 101 us through the Python calls):
+// Measured (GPU time, from captured graphs; 482 and 101 us through the Python calls):
 // 10,746 prompt tokens of 48 heads (8 key/value heads of 128), windows of
 // 2048, 16-bit outputs: 467 us, 1,139 TFLOP/s (the kernel of qmv_attn_tc.cu, with
 // windows: 678). Of that the steps at the edges cost some 27 us, the look at values
